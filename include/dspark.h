@@ -438,6 +438,111 @@ int dspark_accept_label(dspark_ctx* ctx, const float* P, const float* U, const u
 int dspark_schedule(dspark_ctx* ctx, const float* a, int R, int K, const float* sps, int sps_len,
                     int32_t* ell, float* theta, dspark_stream_t stream);
 
+/* --------------------------------------------------------------------- */
+/* Verification from given probabilities and random numbers                 */
+/* --------------------------------------------------------------------- */
+
+/* The accept-or-correct rule of dspark_verify for a draft of any kind: against the
+ * target's probabilities (filtered ones, say) instead of its logits, with the draft's
+ * own probabilities instead of a head to recompute them from, and with the caller's
+ * random numbers.  Source: as dspark_verify.
+ *   P [B, K+1, V] fp32 target probabilities (row K: after a fully accepted block)
+ *   the draft's probabilities, in one of two forms:
+ *     Q [B, K, V] fp32 (m = 0; cand and cand_q NULL), or
+ *     cand [B, K, m] int32, cand_q [B, K, m] fp32: m candidates a position (the
+ *     selector walk's drafts), every other token having none; negative ids are empty
+ *     slots, of equal ids the first counts (Q NULL, 1 <= m <= 256)
+ *   tokens [B, K] drafted tokens; u_accept [B, K], u_draw [B] fp32 uniforms in [0, 1)
+ *   ell [B] verified positions in [0, K] (NULL: K; values outside are clamped)
+ * Position k < ell[b] survives while u q_k(x_k) < p_k(x_k), compared exactly.  At the
+ * first rejection j the weights are r_v = max(0, p_j(v) - q_j(v)), or p_j where that is
+ * zero everywhere; after a full window r = p_ell.  next_token is the first v (by id)
+ * with sum_{w <= v} r_w > u_draw sum_w r_w, the sums kept to about 2^-48 of the whole;
+ * -1 where no token has mass.  Entries that are negative or not finite have no mass.
+ * Outputs as dspark_verify: n_acc [B], next_token [B], accept_prob [B, K] (NULL: not
+ * written) min(1, p/q) (q = 0: 1 if p > 0 else 0) for k < ell[b], -1 beyond.
+ * K <= 64, V <= 2^18, any V; 4-byte aligned pointers.  Drafted tokens out of [0, V) are
+ * reported as DSPARK_ERR_DEVICE_OOB.  One kernel. */
+int dspark_verify_probs(dspark_ctx* ctx, const float* P, const float* Q, const int32_t* cand,
+                        const float* cand_q, int m, const int32_t* tokens, const float* u_accept,
+                        const float* u_draw, const int32_t* ell, int B, int K, int V,
+                        int32_t* n_acc, int32_t* next_token, float* accept_prob,
+                        dspark_stream_t stream);
+
+/* --------------------------------------------------------------------- */
+/* Training: distillation from a teacher's top logits                      */
+/* --------------------------------------------------------------------- */
+
+/* Element types of the training calls' large tensors. */
+typedef enum dspark_dtype { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
+
+/* Loss of each row of student logits against the teacher's k likeliest tokens, and
+ * its gradient.  Source: DSpark explainer, "How DSpark is trained" (cross entropy and
+ * total variation against the target, weights 0.1 and 0.9, position weights
+ * exp(-(k - 1) / gamma)); the teacher given by its top logits is this library's form.
+ * The events of a row are the teacher's tokens and the rest of the vocabulary:
+ *   p_i = (1 - rho) softmax(teacher_logits / T)_i, p_rest = rho = teacher_rest[n]
+ *   q = softmax(logits / T), q_rest its sum outside the teacher's tokens
+ *   KL = sum_i p_i ln(p_i / q_i) + rho ln(rho / q_rest)
+ *   TV = (sum_i |p_i - q_i| + |rho - q_rest|) / 2
+ *   loss = row_weight (alpha_kl KL + alpha_tv TV);  grad = d loss / d logits
+ * (sgn(0) = 0 at TV's kinks; KL's teacher entropy is included, so equality gives 0).
+ *   logits [N, V] of type dtype, rows ld elements apart (ld >= V)
+ *   teacher_ids [N, k] int32, teacher_logits [N, k] fp32; 1 <= k <= 256.  Negative ids
+ *     are empty slots, of equal ids the first counts; ids >= V are reported as
+ *     DSPARK_ERR_DEVICE_OOB and skipped
+ *   teacher_rest [N] fp32 in [0, 1] (clamped; NULL: 0), row_weight [N] fp32 (NULL: 1)
+ *   T = temperature > 0; alpha_kl, alpha_tv finite
+ * Outputs loss [N] fp32, tv [N] fp32 (NULL: not written; 1 - tv is the acceptance
+ * label of the row), grad [N, V] of type dtype, rows ld_grad apart (NULL: loss only;
+ * may be logits itself, with the same ld).  A row of weight 0 is not read, and it, a row
+ * without a teacher token of finite logit and a row whose student logits are all -inf
+ * get loss 0, tv 0 and a zero gradient.  V <= 2^18, any V; pointers aligned to their
+ * element size.  One kernel; no scratch, no atomics: equal inputs give equal bits. */
+int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
+                   const int32_t* teacher_ids, const float* teacher_logits, int k,
+                   const float* teacher_rest, const float* row_weight, int64_t N, int V,
+                   float temperature, float alpha_kl, float alpha_tv, float* loss, float* tv,
+                   void* grad, int64_t ld_grad, dspark_stream_t stream);
+
+/* --------------------------------------------------------------------- */
+/* Training: the RNN head's recurrence over given sequences                */
+/* --------------------------------------------------------------------- */
+
+/* The states of the RNN head's recurrence, channel by channel:
+ *   s_t = a_t s_{t-1} + g_t e_t,  a = sigmoid(za), g = sigmoid(zg) (1 if zg is NULL).
+ * Source and reading as dspark_rnn_draft (za = h . Wa, zg = h . Wg, e = W1[x_{t-1}]);
+ * the state is held in fp32 and rounded only where it is written (the draft call rounds
+ * the state it carries at every position).
+ *   za, zg, e [N, L, D] of type dtype: channels contiguous, consecutive rows (n L + t)
+ *     ld_za, ld_zg, ld_e elements apart (two halves of one projection's output, say)
+ *   s0 [N, D] fp32 state before t = 0 (NULL: 0)
+ *   reset [N, L] uint8 (NULL: none): non-zero makes a_t zero, so a sequence starts there;
+ *     a decay of exactly zero drops the earlier state whatever it holds
+ * Outputs s [N, L, D] of type dtype, contiguous; s_last [N, D] fp32 the state after
+ * t = L - 1 (NULL: not written).  L = 1 with s0 and s_last is the step of one token; s0
+ * and s_last may be the same buffer.  Any N, L, D >= 1 (N L < 2^31, N D < 2^31); pointers
+ * aligned to their element size.  Equal inputs give equal bits. */
+int dspark_rnn_scan(dspark_ctx* ctx, const void* za, const void* zg, const void* e, int dtype,
+                    int64_t ld_za, int64_t ld_zg, int64_t ld_e, const float* s0,
+                    const uint8_t* reset, int64_t N, int64_t L, int D, void* s, float* s_last,
+                    dspark_stream_t stream);
+
+/* Gradients of dspark_rnn_scan: with ds [N, L, D] (type dtype, contiguous) and ds_last
+ * [N, D] fp32 (NULL: 0) the gradients of s and s_last,
+ *   delta_t = ds_t + a_{t+1} delta_{t+1},  delta_{L-1} = ds_{L-1} + ds_last
+ *   dza = delta_t s_{t-1} a (1 - a), dzg = delta_t e g (1 - g), de = delta_t g,
+ *   ds0 = a_0 delta_0.
+ * Inputs as given to dspark_rnn_scan, s its output.  Outputs dza, dzg of type dtype,
+ * rows ld_dza, ld_dzg elements apart (dzg NULL where zg is), de [N, L, D] of type dtype,
+ * contiguous, ds0 [N, D] fp32 (NULL: not written). */
+int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const void* e,
+                         const void* s, const void* ds, int dtype, int64_t ld_za, int64_t ld_zg,
+                         int64_t ld_e, const float* s0, const uint8_t* reset,
+                         const float* ds_last, int64_t N, int64_t L, int D, void* dza, void* dzg,
+                         int64_t ld_dza, int64_t ld_dzg, void* de, float* ds0,
+                         dspark_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,7 +36,8 @@ EXPORTS = (
     "dspark_markov_draft", "dspark_gated_draft", "dspark_gate", "dspark_selector_scores",
     "dspark_selector_walk", "dspark_confidence", "dspark_markov_logits",
     "dspark_markov_draft_noalloc", "dspark_verify", "dspark_schedule", "dspark_accept_label",
-    "dspark_sts_fit", "dspark_rnn_draft", "dspark_rnn_logits",
+    "dspark_sts_fit", "dspark_rnn_draft", "dspark_rnn_logits", "dspark_verify_probs",
+    "dspark_distill", "dspark_rnn_scan", "dspark_rnn_scan_grad",
 )
 
 
@@ -67,6 +68,7 @@ def load(path: str = LIB_PATH):
                            "(python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(path)
     P, I, F, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64
+    I64 = ctypes.c_int64
     sig = {
         "dspark_ctx_create": [ctypes.POINTER(P), I, I, I, I],
         "dspark_ctx_destroy": [P],
@@ -92,6 +94,11 @@ def load(path: str = LIB_PATH):
         "dspark_sts_fit": [P, P, P, I, I, F, F, P, P, P],
         "dspark_rnn_draft": [P, P, P, P, P, P, P, P, I, I, I, I, I, F, U64, P, P, P, P],
         "dspark_rnn_logits": [P, P, P, P, P, P, P, P, I, I, I, I, I, F, P, P, P],
+        "dspark_verify_probs": [P, P, P, P, P, I, P, P, P, P, I, I, I, P, P, P, P],
+        "dspark_distill": [P, P, I, I64, P, P, I, P, P, I64, I, F, F, F, P, P, P, I64, P],
+        "dspark_rnn_scan": [P, P, P, P, I, I64, I64, I64, P, P, I64, I64, I, P, P, P],
+        "dspark_rnn_scan_grad": [P, P, P, P, P, P, I, I64, I64, I64, P, P, P, I64, I64, I, P, P,
+                                 I64, I64, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -124,6 +131,47 @@ def _ptr(t: Optional[torch.Tensor], dtypes=None, name: str = "tensor"):
     if t.device.type != "cuda":
         raise ValueError(f"{name}: must live in CUDA device memory")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t: Optional[torch.Tensor], dtype, name: str):
+    """Pointer and row distance (elements) of a [..., D] tensor whose last dimension is
+    contiguous and whose rows are evenly spaced (a slice of a wider contiguous tensor)."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must live in CUDA device memory")
+    ld = step = None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != step:
+            raise ValueError(f"{name}: rows must be evenly spaced")
+        step = stride * size
+    if t.dim() == 0 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.shape[-1] if ld is None else ld
+
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1}  # dspark_dtype
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(_DTYPE)}")
+    return _DTYPE[t.dtype]
+
+
+def _shape(t: Optional[torch.Tensor], shape, name: str):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
 
 
 def _stream(stream, device):
@@ -373,6 +421,63 @@ def dspark_schedule(ctx: Context, a, R, K, sps, ell, theta, stream=None):
     _check(code, "dspark_schedule")
 
 
+def dspark_verify_probs(ctx: Context, P, Q, cand, cand_q, m, tokens, u_accept, u_draw, ell, B, K,
+                        V, n_acc, next_token, accept_prob, stream=None):
+    f32, i32 = (torch.float32,), (torch.int32,)
+    code = ctx.lib.dspark_verify_probs(
+        ctx.handle, _ptr(P, f32, "P"), _ptr(Q, f32, "Q"), _ptr(cand, i32, "cand"),
+        _ptr(cand_q, f32, "cand_q"), m, _ptr(tokens, i32, "tokens"),
+        _ptr(u_accept, f32, "u_accept"), _ptr(u_draw, f32, "u_draw"), _ptr(ell, i32, "ell"), B, K,
+        V, _ptr(n_acc, i32, "n_acc"), _ptr(next_token, i32, "next_token"),
+        _ptr(accept_prob, f32, "accept_prob"), _stream(stream, ctx.device))
+    _check(code, "dspark_verify_probs")
+
+
+def dspark_distill(ctx: Context, logits, teacher_ids, teacher_logits, k, teacher_rest, row_weight,
+                   N, V, temperature, alpha_kl, alpha_tv, loss, tv, grad, stream=None):
+    f32 = (torch.float32,)
+    dtype = _dtype(logits, "logits")
+    p, ld = _rows(logits, logits.dtype, "logits")
+    pg, ld_grad = _rows(grad, logits.dtype, "grad")
+    code = ctx.lib.dspark_distill(
+        ctx.handle, p, dtype, ld, _ptr(teacher_ids, (torch.int32,), "teacher_ids"),
+        _ptr(teacher_logits, f32, "teacher_logits"), k, _ptr(teacher_rest, f32, "teacher_rest"),
+        _ptr(row_weight, f32, "row_weight"), N, V, float(temperature), float(alpha_kl),
+        float(alpha_tv), _ptr(loss, f32, "loss"), _ptr(tv, f32, "tv"), pg, ld_grad,
+        _stream(stream, ctx.device))
+    _check(code, "dspark_distill")
+
+
+def dspark_rnn_scan(ctx: Context, za, zg, e, s0, reset, N, L, D, s, s_last, stream=None):
+    f32 = (torch.float32,)
+    dtype = _dtype(e, "e")
+    pa, ld_za = _rows(za, e.dtype, "za")
+    pg, ld_zg = _rows(zg, e.dtype, "zg")
+    pe, ld_e = _rows(e, e.dtype, "e")
+    code = ctx.lib.dspark_rnn_scan(
+        ctx.handle, pa, pg, pe, dtype, ld_za, ld_zg, ld_e, _ptr(s0, f32, "s0"),
+        _ptr(reset, (torch.uint8, torch.bool), "reset"), N, L, D, _ptr(s, (e.dtype,), "s"),
+        _ptr(s_last, f32, "s_last"), _stream(stream, ctx.device))
+    _check(code, "dspark_rnn_scan")
+
+
+def dspark_rnn_scan_grad(ctx: Context, za, zg, e, s, ds, s0, reset, ds_last, N, L, D, dza, dzg, de,
+                         ds0, stream=None):
+    f32 = (torch.float32,)
+    dtype = _dtype(e, "e")
+    pa, ld_za = _rows(za, e.dtype, "za")
+    pg, ld_zg = _rows(zg, e.dtype, "zg")
+    pe, ld_e = _rows(e, e.dtype, "e")
+    pda, ld_dza = _rows(dza, e.dtype, "dza")
+    pdg, ld_dzg = _rows(dzg, e.dtype, "dzg")
+    code = ctx.lib.dspark_rnn_scan_grad(
+        ctx.handle, pa, pg, pe, _ptr(s, (e.dtype,), "s"), _ptr(ds, (e.dtype,), "ds"), dtype, ld_za,
+        ld_zg, ld_e, _ptr(s0, f32, "s0"), _ptr(reset, (torch.uint8, torch.bool), "reset"),
+        _ptr(ds_last, f32, "ds_last"), N, L, D, pda, pdg, ld_dza, ld_dzg,
+        _ptr(de, (e.dtype,), "de"), _ptr(ds0, f32, "ds0"), _stream(stream, ctx.device))
+    _check(code, "dspark_rnn_scan_grad")
+
+
 def dspark_markov_draft_noalloc(U, W1, W2, anchors, B, K, V, r, temperature, seed, tokens,
                                 logprobs, device_status=None, stream=None):
     """Context-free draft that allocates no device memory (scratch compiled into the library).
@@ -553,3 +658,92 @@ def markov_logits(ctx: Context, U, W1, W2, prev_tokens, *, temperature=1.0, h=No
     dspark_markov_logits(ctx, U, W1, W2, prev_tokens, h, Wg, d, B, K, V, r, temperature, logits,
                          lse, stream)
     return dict(logits=logits, lse=lse)
+
+
+def verify_probs(ctx: Context, P, tokens, u_accept, u_draw, *, Q=None, cand=None, cand_q=None,
+                 ell=None, stream=None) -> dict:
+    """Accept-or-correct of drafted tokens [B, K] against target probabilities P [B, K+1, V] from
+    uniforms u_accept [B, K] and u_draw [B]; the draft's probabilities are Q [B, K, V], or cand_q
+    on the candidates cand [B, K, m]."""
+    B, K = tokens.shape
+    V = P.shape[-1]
+    m = 0 if cand is None else int(cand.shape[-1])
+    _shape(P, (B, K + 1, V), "P")
+    _shape(Q, (B, K, V), "Q")
+    _shape(cand, (B, K, m), "cand")
+    _shape(cand_q, (B, K, m), "cand_q")
+    _shape(u_accept, (B, K), "u_accept")
+    _shape(u_draw, (B,), "u_draw")
+    _shape(ell, (B,), "ell")
+    n_acc = torch.empty(B, dtype=torch.int32, device=P.device)
+    next_token = torch.empty(B, dtype=torch.int32, device=P.device)
+    accept_prob = torch.empty(B, K, dtype=torch.float32, device=P.device)
+    dspark_verify_probs(ctx, P, Q, cand, cand_q, m, tokens, u_accept, u_draw, ell, B, K, V, n_acc,
+                        next_token, accept_prob, stream)
+    return dict(n_acc=n_acc, next_token=next_token, accept_prob=accept_prob)
+
+
+def distill(ctx: Context, logits, teacher_ids, teacher_logits, *, teacher_rest=None,
+            row_weight=None, temperature=1.0, alpha_kl=0.1, alpha_tv=0.9, grad=True,
+            stream=None) -> dict:
+    """Loss of student logits [..., V] (fp32 or bf16, rows evenly spaced) against a teacher's top
+    logits [..., k], and its gradient: grad True allocates it, a tensor (logits itself, say)
+    receives it, False leaves it out.  Returns loss and tv [...], and grad [..., V]."""
+    lead, V = logits.shape[:-1], int(logits.shape[-1])
+    k = int(teacher_ids.shape[-1])
+    _shape(teacher_ids, (*lead, k), "teacher_ids")
+    _shape(teacher_logits, (*lead, k), "teacher_logits")
+    _shape(teacher_rest, lead, "teacher_rest")
+    _shape(row_weight, lead, "row_weight")
+    N = lead.numel()
+    loss = torch.empty(lead, dtype=torch.float32, device=logits.device)
+    tv = torch.empty(lead, dtype=torch.float32, device=logits.device)
+    if grad is True:
+        grad = torch.empty(*lead, V, dtype=logits.dtype, device=logits.device)
+    elif grad is False:
+        grad = None
+    _shape(grad, (*lead, V), "grad")
+    dspark_distill(ctx, logits, teacher_ids, teacher_logits, k, teacher_rest, row_weight, N, V,
+                   temperature, alpha_kl, alpha_tv, loss, tv, grad, stream)
+    out = dict(loss=loss, tv=tv)
+    if grad is not None:
+        out["grad"] = grad
+    return out
+
+
+def rnn_scan(ctx: Context, za, zg, e, *, s0=None, reset=None, stream=None) -> dict:
+    """States of the RNN head over given sequences: s_t = sigmoid(za_t) s_{t-1} + sigmoid(zg_t) e_t
+    (zg None: 1), tensors [N, L, D] in fp32 or bf16; returns s [N, L, D] and s_last [N, D] fp32."""
+    N, L, D = e.shape
+    _shape(za, e.shape, "za")
+    _shape(zg, e.shape, "zg")
+    _shape(s0, (N, D), "s0")
+    _shape(reset, (N, L), "reset")
+    s = torch.empty(N, L, D, dtype=e.dtype, device=e.device)
+    s_last = torch.empty(N, D, dtype=torch.float32, device=e.device)
+    dspark_rnn_scan(ctx, za, zg, e, s0, reset, N, L, D, s, s_last, stream)
+    return dict(s=s, s_last=s_last)
+
+
+def rnn_scan_grad(ctx: Context, za, zg, e, s, ds, *, s0=None, ds_last=None, reset=None,
+                  stream=None) -> dict:
+    """Gradients of rnn_scan from ds [N, L, D] (of s) and ds_last [N, D] (of s_last).  Returns
+    dza and dzg (the two halves of one [N, L, 2 D] tensor; dzg only with zg), de, and ds0 [N, D]."""
+    N, L, D = e.shape
+    _shape(za, e.shape, "za")
+    _shape(zg, e.shape, "zg")
+    _shape(s, e.shape, "s")
+    _shape(ds, e.shape, "ds")
+    _shape(s0, (N, D), "s0")
+    _shape(ds_last, (N, D), "ds_last")
+    _shape(reset, (N, L), "reset")
+    dz = torch.empty(N, L, D if zg is None else 2 * D, dtype=e.dtype, device=e.device)
+    dza, dzg = dz[..., :D], None if zg is None else dz[..., D:]
+    de = torch.empty(N, L, D, dtype=e.dtype, device=e.device)
+    ds0 = torch.empty(N, D, dtype=torch.float32, device=e.device)
+    dspark_rnn_scan_grad(ctx, za, zg, e, s, ds, s0, reset, ds_last, N, L, D, dza, dzg, de, ds0,
+                         stream)
+    out = dict(dza=dza, de=de, ds0=ds0)
+    if zg is not None:
+        out["dzg"] = dzg
+    return out

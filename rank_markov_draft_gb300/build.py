@@ -26,7 +26,7 @@ CHECKED = "draft.cu"  # the unit that holds the checks
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "draft.cu", "gate.cu", "selector.cu", "confidence.cu", "noalloc.cu", "verify.cu",
-           "schedule.cu", "label.cu", "calibrate.cu"]
+           "schedule.cu", "label.cu", "calibrate.cu", "verify_probs.cu", "distill.cu", "rnn_scan.cu"]
 
 
 def nvcc() -> str:

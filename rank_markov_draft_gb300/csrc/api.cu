@@ -128,6 +128,29 @@ bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Element size of a dspark_dtype (0: not one).
+size_t dtype_size(int dtype) {
+  return dtype == DSPARK_F32 ? 4 : (dtype == DSPARK_BF16 ? 2 : 0);
+}
+
+// The arguments that both directions of the RNN head's recurrence share.
+int check_scan_args(const void* za, const void* zg, const void* e, int dtype, int64_t ld_za,
+                    int64_t ld_zg, int64_t ld_e, const float* s0, int64_t N, int64_t L, int D) {
+  const size_t size = dtype_size(dtype);
+  if (za == nullptr || e == nullptr || size == 0) return DSPARK_ERR_INVALID_ARG;
+  if (N <= 0 || L <= 0 || D <= 0) return DSPARK_ERR_INVALID_ARG;
+  if (ld_za < D || (zg != nullptr && ld_zg < D) || ld_e < D) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(za, size) || !aligned_to(zg, size) || !aligned_to(e, size) ||
+      !aligned_to(s0, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  const int64_t most = (1ll << 31) - 1;
+  if (N > most || L > most || N * L > most || N * D > most) return DSPARK_ERR_UNSUPPORTED;
+  if (ld_za > most || ld_zg > most || ld_e > most) return DSPARK_ERR_UNSUPPORTED;
+  return DSPARK_OK;
+}
+
 int check_rank(int r) {
   if (r < 0) return DSPARK_ERR_INVALID_ARG;
   if (r > dspark::kMaxRank || (r % 16) != 0) return DSPARK_ERR_UNSUPPORTED;
@@ -926,6 +949,179 @@ int dspark_schedule(dspark_ctx* ctx, const float* a, int R, int K, const float* 
                                           reinterpret_cast<cudaStream_t>(stream));
   ctx->last_launches = 1;
   return cuda_status(e);
+}
+
+int dspark_verify_probs(dspark_ctx* ctx, const float* P, const float* Q, const int32_t* cand,
+                        const float* cand_q, int m, const int32_t* tokens, const float* u_accept,
+                        const float* u_draw, const int32_t* ell, int B, int K, int V,
+                        int32_t* n_acc, int32_t* next_token, float* accept_prob,
+                        dspark_stream_t stream) {
+  if (P == nullptr || tokens == nullptr || u_accept == nullptr || u_draw == nullptr ||
+      n_acc == nullptr || next_token == nullptr)
+    return DSPARK_ERR_INVALID_ARG;
+  if (m < 0 || (m == 0) != (Q != nullptr) || (m > 0) != (cand != nullptr) ||
+      (m > 0) != (cand_q != nullptr))
+    return DSPARK_ERR_INVALID_ARG;
+  if (B <= 0 || K <= 0 || V <= 0) return DSPARK_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(P), static_cast<const void*>(Q),
+                        static_cast<const void*>(cand), static_cast<const void*>(cand_q),
+                        static_cast<const void*>(tokens), static_cast<const void*>(u_accept),
+                        static_cast<const void*>(u_draw), static_cast<const void*>(ell),
+                        static_cast<const void*>(n_acc), static_cast<const void*>(next_token),
+                        static_cast<const void*>(accept_prob)})
+    if (!aligned_to(p, 4)) return DSPARK_ERR_INVALID_ARG;
+  if (K > dspark::kMaxK || V > (1 << 18) || m > dspark::kMaxTeacher)
+    return DSPARK_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::VerifyProbsArgs a{};
+  a.P = P;
+  a.Q = Q;
+  a.cand = cand;
+  a.cand_q = cand_q;
+  a.tokens = tokens;
+  a.u_accept = u_accept;
+  a.u_draw = u_draw;
+  a.ell = ell;
+  a.m = m;
+  a.B = B;
+  a.K = K;
+  a.V = V;
+  a.n_acc = n_acc;
+  a.next_token = next_token;
+  a.accept_prob = accept_prob;
+  a.status = ctx->d_status;
+  st = cuda_status(dspark::launch_verify_probs(a, reinterpret_cast<cudaStream_t>(stream)));
+  if (st == DSPARK_OK) ctx->last_launches = 1;
+  return st;
+}
+
+int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
+                   const int32_t* teacher_ids, const float* teacher_logits, int k,
+                   const float* teacher_rest, const float* row_weight, int64_t N, int V,
+                   float temperature, float alpha_kl, float alpha_tv, float* loss, float* tv,
+                   void* grad, int64_t ld_grad, dspark_stream_t stream) {
+  const size_t size = dtype_size(dtype);
+  if (logits == nullptr || teacher_ids == nullptr || teacher_logits == nullptr ||
+      loss == nullptr || size == 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (N <= 0 || V <= 0 || k <= 0 || ld < V || (grad != nullptr && ld_grad < V))
+    return DSPARK_ERR_INVALID_ARG;
+  if (grad == logits && ld_grad != ld) return DSPARK_ERR_INVALID_ARG;
+  if (!(temperature > 0.f) || temperature > 3.0e38f || !(alpha_kl - alpha_kl == 0.f) ||
+      !(alpha_tv - alpha_tv == 0.f))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(logits, size) || !aligned_to(grad, size)) return DSPARK_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(teacher_ids),
+                        static_cast<const void*>(teacher_logits),
+                        static_cast<const void*>(teacher_rest),
+                        static_cast<const void*>(row_weight), static_cast<const void*>(loss),
+                        static_cast<const void*>(tv)})
+    if (!aligned_to(p, 4)) return DSPARK_ERR_INVALID_ARG;
+  if (V > (1 << 18) || k > dspark::kMaxTeacher || N >= (1ll << 31)) return DSPARK_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::DistillArgs a{};
+  a.logits = logits;
+  a.teacher_ids = teacher_ids;
+  a.teacher_logits = teacher_logits;
+  a.teacher_rest = teacher_rest;
+  a.row_weight = row_weight;
+  a.N = N;
+  a.ld = ld;
+  a.ld_grad = ld_grad;
+  a.V = V;
+  a.k = k;
+  a.dtype = dtype;
+  a.temperature = temperature;
+  a.alpha_kl = alpha_kl;
+  a.alpha_tv = alpha_tv;
+  a.loss = loss;
+  a.tv = tv;
+  a.grad = grad;
+  a.status = ctx->d_status;
+  st = cuda_status(dspark::launch_distill(a, reinterpret_cast<cudaStream_t>(stream)));
+  if (st == DSPARK_OK) ctx->last_launches = 1;
+  return st;
+}
+
+int dspark_rnn_scan(dspark_ctx* ctx, const void* za, const void* zg, const void* e, int dtype,
+                    int64_t ld_za, int64_t ld_zg, int64_t ld_e, const float* s0,
+                    const uint8_t* reset, int64_t N, int64_t L, int D, void* s, float* s_last,
+                    dspark_stream_t stream) {
+  int st = check_scan_args(za, zg, e, dtype, ld_za, ld_zg, ld_e, s0, N, L, D);
+  if (st != DSPARK_OK) return st;
+  if (s == nullptr || !aligned_to(s, dtype_size(dtype)) || !aligned_to(s_last, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::RnnScanArgs a{};
+  a.za = za;
+  a.zg = zg;
+  a.e = e;
+  a.ld_za = ld_za;
+  a.ld_zg = ld_zg;
+  a.ld_e = ld_e;
+  a.s0 = s0;
+  a.reset = reset;
+  a.N = N;
+  a.L = L;
+  a.D = D;
+  a.dtype = dtype;
+  a.s = s;
+  a.s_last = s_last;
+  st = cuda_status(dspark::launch_rnn_scan(a, reinterpret_cast<cudaStream_t>(stream)));
+  if (st == DSPARK_OK) ctx->last_launches = 1;
+  return st;
+}
+
+int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const void* e,
+                         const void* s, const void* ds, int dtype, int64_t ld_za, int64_t ld_zg,
+                         int64_t ld_e, const float* s0, const uint8_t* reset,
+                         const float* ds_last, int64_t N, int64_t L, int D, void* dza, void* dzg,
+                         int64_t ld_dza, int64_t ld_dzg, void* de, float* ds0,
+                         dspark_stream_t stream) {
+  int st = check_scan_args(za, zg, e, dtype, ld_za, ld_zg, ld_e, s0, N, L, D);
+  if (st != DSPARK_OK) return st;
+  const size_t size = dtype_size(dtype);
+  if (s == nullptr || ds == nullptr || dza == nullptr || de == nullptr ||
+      (zg == nullptr) != (dzg == nullptr))
+    return DSPARK_ERR_INVALID_ARG;
+  if (ld_dza < D || (dzg != nullptr && ld_dzg < D)) return DSPARK_ERR_INVALID_ARG;
+  for (const void* p : {s, ds, static_cast<const void*>(dza), static_cast<const void*>(dzg),
+                        static_cast<const void*>(de)})
+    if (!aligned_to(p, size)) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(ds_last, 4) || !aligned_to(ds0, 4)) return DSPARK_ERR_INVALID_ARG;
+  if (ld_dza >= (1ll << 31) || ld_dzg >= (1ll << 31)) return DSPARK_ERR_UNSUPPORTED;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::RnnScanGradArgs a{};
+  a.za = za;
+  a.zg = zg;
+  a.e = e;
+  a.s = s;
+  a.ds = ds;
+  a.ld_za = ld_za;
+  a.ld_zg = ld_zg;
+  a.ld_e = ld_e;
+  a.ld_dza = ld_dza;
+  a.ld_dzg = ld_dzg;
+  a.s0 = s0;
+  a.reset = reset;
+  a.ds_last = ds_last;
+  a.N = N;
+  a.L = L;
+  a.D = D;
+  a.dtype = dtype;
+  a.dza = dza;
+  a.dzg = dzg;
+  a.de = de;
+  a.ds0 = ds0;
+  st = cuda_status(dspark::launch_rnn_scan_grad(a, reinterpret_cast<cudaStream_t>(stream)));
+  if (st == DSPARK_OK) ctx->last_launches = 1;
+  return st;
 }
 
 }  // extern "C"

@@ -228,4 +228,65 @@ cudaError_t launch_confidence(const uint16_t* h, const uint16_t* W1, const int32
 cudaError_t launch_sts_fit(const float* conf, const float* label, int N, int K, float tau_lo,
                            float tau_hi, float* tau, float* loss, cudaStream_t stream);
 
+// ---- verification from given probabilities and random numbers (verify_probs.cu)
+struct VerifyProbsArgs {
+  const float* P;           // [B, K+1, V]
+  const float* Q;           // [B, K, V] (m = 0)
+  const int32_t* cand;      // [B, K, m] (m > 0)
+  const float* cand_q;      // [B, K, m]
+  const int32_t* tokens;    // [B, K]
+  const float* u_accept;    // [B, K]
+  const float* u_draw;      // [B]
+  const int32_t* ell;       // [B] or null: K
+  int m, B, K, V;
+  int32_t* n_acc;           // [B]
+  int32_t* next_token;      // [B]
+  float* accept_prob;       // [B, K] or null
+  int* status;
+};
+cudaError_t launch_verify_probs(const VerifyProbsArgs& a, cudaStream_t stream);
+
+// ---- distillation from a teacher's top logits (distill.cu)
+constexpr int kMaxTeacher = 256;  // teacher tokens (and draft candidates) a row
+struct DistillArgs {
+  const void* logits;           // [N, V] of dtype, rows ld apart
+  const int32_t* teacher_ids;   // [N, k]
+  const float* teacher_logits;  // [N, k]
+  const float* teacher_rest;    // [N] or null: 0
+  const float* row_weight;      // [N] or null: 1
+  int64_t N, ld, ld_grad;
+  int V, k, dtype;
+  float temperature, alpha_kl, alpha_tv;
+  float* loss;                  // [N]
+  float* tv;                    // [N] or null
+  void* grad;                   // [N, V] of dtype, rows ld_grad apart, or null
+  int* status;
+};
+cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream);
+
+// ---- the RNN head's recurrence over given sequences (rnn_scan.cu)
+struct RnnScanArgs {
+  const void *za, *zg, *e;   // [N, L, D] of dtype, rows ld_* apart; zg may be null
+  int64_t ld_za, ld_zg, ld_e;
+  const float* s0;           // [N, D] or null
+  const uint8_t* reset;      // [N, L] or null
+  int64_t N, L;
+  int D, dtype;
+  void* s;                   // [N, L, D]
+  float* s_last;             // [N, D] or null
+};
+struct RnnScanGradArgs {
+  const void *za, *zg, *e, *s, *ds;
+  int64_t ld_za, ld_zg, ld_e, ld_dza, ld_dzg;
+  const float* s0;
+  const uint8_t* reset;
+  const float* ds_last;      // [N, D] or null
+  int64_t N, L;
+  int D, dtype;
+  void *dza, *dzg, *de;
+  float* ds0;                // [N, D] or null
+};
+cudaError_t launch_rnn_scan(const RnnScanArgs& a, cudaStream_t stream);
+cudaError_t launch_rnn_scan_grad(const RnnScanGradArgs& a, cudaStream_t stream);
+
 }  // namespace dspark

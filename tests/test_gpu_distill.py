@@ -1,0 +1,270 @@
+"""GPU parity of the distillation loss and its gradient (dspark_distill) against the 64-bit
+statement.
+
+Tolerances: a gradient element is off by the 32-bit evaluation's bound (oracle.training, built
+from the exponents' sizes and the sum's depth) and half a step of its type; a loss by the same
+relative error of every p, q and logarithm."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import training as tr
+from rank_markov_draft_gb300 import binding
+from tests.gpu_util import dev, host
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float32: torch.finfo(torch.float32).eps / 2, torch.bfloat16: torch.finfo(torch.bfloat16).eps / 2}
+DTYPES = [torch.float32, torch.bfloat16]
+KW = dict(temperature=1.3, alpha_kl=0.4, alpha_tv=0.9)
+
+
+def make(seed, N, V, k, dtype, spread=2.0):
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.normal(0, spread, (N, V)).astype(np.float32)).to(dtype)
+    ids = np.stack([rng.permutation(V)[:k] if k <= V else np.arange(k) - (k - V) for _ in range(N)]).astype(np.int32)
+    return dict(x=x, ids=ids, t=rng.normal(0, spread, (N, k)).astype(np.float32),
+                rho=rng.uniform(0, 0.3, N).astype(np.float32), w=rng.uniform(0.1, 2, N).astype(np.float32))
+
+
+def call(ctx, a, logits=None, grad=True, **kw):
+    o = {n: None if a[n] is None else dev(a[n]) for n in ("ids", "t", "rho", "w")}
+    return binding.distill(ctx, a["x"].cuda() if logits is None else logits, o["ids"], o["t"], teacher_rest=o["rho"],
+                           row_weight=o["w"], grad=grad, **(KW | kw))
+
+
+def compare(a, out, rows=None, **kw):
+    kw = KW | kw
+    x = a["x"].double().numpy()
+    loss, tv = host(out["loss"]), host(out["tv"])
+    grad = None if "grad" not in out else out["grad"].double().cpu().numpy()
+    half = HALF[a["x"].dtype]
+    for n in range(x.shape[0]) if rows is None else rows:
+        w = 1.0 if a["w"] is None else float(a["w"][n])
+        L, d, g, b, E = tr.distill_row(x[n], a["ids"][n], a["t"][n], 0.0 if a["rho"] is None else a["rho"][n], w,
+                                       kw["temperature"], kw["alpha_kl"], kw["alpha_tv"])
+        # KL: each of p, q and ln(p / q) is off by E relative (the logarithm's argument) once
+        span = abs(L / w) / max(abs(kw["alpha_kl"]), 1e-9) if w and np.isfinite(L) else 0.0
+        tol = abs(w) * (abs(kw["alpha_kl"]) * (2 + 2 * span) + 2 * abs(kw["alpha_tv"])) * E
+        if np.isfinite(L):
+            assert abs(loss[n] - L) <= tol + 1e-45, (n, loss[n], L, tol)
+        else:
+            assert loss[n] == L, (n, loss[n], L)
+        assert abs(tv[n] - d) <= 2 * E, (n, tv[n], d)
+        if grad is not None:
+            # (2^-126: below it float32 itself is coarser)
+            bad = ~(np.abs(grad[n] - g) <= b + half * np.abs(g) * (1 + 1e-6) + 2.0 ** -126)
+            assert not bad.any(), (n, np.flatnonzero(bad)[:5], grad[n][bad][:5], g[bad][:5], b[bad][:5])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 8, 9, 31, 255, 256, 257, 2047, 2048, 4099, 32003])
+def test_vocabularies(dsp, V, dtype):
+    a = make(V, 6, V, min(V, 9), dtype)
+    out = call(dsp, a)
+    torch.cuda.synchronize()
+    assert dsp.status() == 0
+    compare(a, out)
+    alone = call(dsp, a, grad=False)
+    assert "grad" not in alone and torch.equal(alone["loss"], out["loss"]) and torch.equal(alone["tv"], out["tv"])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [65536, 100001, 151936, 1 << 18])
+def test_large_vocabularies(dsp, V, dtype):
+    a = make(V, 3, V, 64, dtype, spread=3.0)
+    compare(a, call(dsp, a))
+
+
+@pytest.mark.parametrize("k", [1, 2, 31, 32, 33, 64, 128, 129, 255, 256])
+def test_teacher_lists(dsp, k):
+    a = make(k, 8, 1500, k, torch.float32)
+    a["ids"][1, k // 2:] = -1
+    a["ids"][2] = -1                   # no teacher: nothing
+    a["ids"][3, :] = a["ids"][3, 0]    # one token, repeated
+    a["t"][4, : k // 2] = -np.inf
+    a["t"][5] = -np.inf                # no mass: nothing
+    out = call(dsp, a)
+    compare(a, out)
+    assert host(out["loss"])[2] == 0 and host(out["loss"])[5] == 0 and not out["grad"][[2, 5]].any()
+
+
+@pytest.mark.parametrize("V,k", [(4, 4), (5, 8), (3, 256)])
+def test_every_token_is_the_teachers(dsp, V, k):
+    a = make(V + k, 5, V, k, torch.float32)
+    a["rho"] = None
+    compare(a, call(dsp, a))
+    a["rho"] = np.full(5, 0.2, np.float32)  # mass where the student cannot have any
+    out = call(dsp, a)
+    assert np.all(np.isposinf(host(out["loss"]))) and torch.isfinite(out["grad"]).all()
+    out = call(dsp, a, alpha_kl=0.0)
+    compare(a, out, alpha_kl=0.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_masked_student_logits(dsp, dtype):
+    a = make(31, 8, 3001, 12, dtype)
+    lowest = torch.finfo(dtype).min
+    a["x"][0, ::2] = -torch.inf
+    a["x"][1, 5:] = -torch.inf
+    a["x"][2] = -torch.inf                 # nothing at all: zero
+    a["x"][3] = lowest                     # uniform at the lowest value
+    a["x"][4, ::3] = lowest
+    a["x"][5] = -torch.inf
+    a["x"][5, int(a["ids"][5, 3])] = 1.0   # only a teacher's token is left
+    a["x"][6, torch.from_numpy(a["ids"][6].astype(np.int64))] = -torch.inf
+    a["x"][7, 17] = torch.finfo(dtype).max
+    out = call(dsp, a)
+    assert not out["grad"][2].any() and float(out["loss"][2]) == 0 and float(out["tv"][2]) == 0
+    assert torch.isfinite(out["grad"]).all()
+    compare(a, out, rows=[0, 1, 2, 3, 4, 5, 6])
+    # row 7: the whole mass on one token
+    g = out["grad"][7].double().cpu().numpy()
+    want = tr.distill_row(a["x"][7].double().numpy(), a["ids"][7], a["t"][7], a["rho"][7], a["w"][7], 1.3, 0.4, 0.9)
+    assert np.abs(g - want[2]).max() <= 8 * HALF[dtype] * np.abs(want[2]).max()
+
+
+def test_nan_stays_in_its_row(dsp):
+    a = make(32, 5, 901, 6, torch.float32)
+    a["x"][1, 700] = torch.nan
+    a["x"][3] = torch.nan
+    out = call(dsp, a)
+    assert torch.isnan(out["loss"]).tolist() == [False, True, False, True, False]
+    assert torch.isnan(out["grad"]).any(1).tolist() == [False, True, False, True, False]
+    compare(a, out, rows=[0, 2, 4])
+
+
+def test_rows_of_no_weight_are_not_read(dsp):
+    a = make(33, 6, 777, 5, torch.bfloat16)
+    a["w"][[0, 4]] = 0.0
+    a["x"][0] = torch.nan
+    a["t"][4] = np.nan
+    a["ids"][4] = 10 ** 6
+    out = call(dsp, a)
+    torch.cuda.synchronize()
+    assert dsp.status() == 0
+    compare(a, out)
+    assert not out["grad"][[0, 4]].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad", [1, 3, 8])
+def test_padded_rows_and_the_gradient_in_place(dsp, dtype, pad):
+    """Rows of a wider buffer: the padding is neither read into the loss nor written."""
+    a = make(34 + pad, 7, 1003, 9, dtype)
+    buf = torch.full((7, 1003 + pad), torch.nan, dtype=dtype, device="cuda")
+    buf[:, :1003] = a["x"].cuda()
+    want = call(dsp, a)
+    compare(a, want)
+    gbuf = torch.full((7, 1003 + 2 * pad + 1), 7.0, dtype=dtype, device="cuda")
+    got = call(dsp, a, logits=buf[:, :1003], grad=gbuf[:, :1003])
+    assert torch.equal(got["grad"], want["grad"]) and torch.equal(got["loss"], want["loss"])
+    assert torch.all(gbuf[:, 1003:] == 7.0)
+    got = call(dsp, a, logits=buf[:, :1003], grad=buf[:, :1003])
+    assert torch.equal(buf[:, :1003], want["grad"]) and torch.equal(got["loss"], want["loss"])
+    assert torch.isnan(buf[:, 1003:]).all()
+
+
+def test_block_shapes_and_defaults(dsp):
+    a = make(35, 12, 640, 4, torch.float32)
+    flat = call(dsp, a | dict(rho=None, w=None))
+    compare(a | dict(rho=None, w=None), flat)
+    out = binding.distill(dsp, a["x"].cuda().view(3, 4, 640), dev(a["ids"]).view(3, 4, 4), dev(a["t"]).view(3, 4, 4), **KW)
+    assert out["loss"].shape == (3, 4) and out["grad"].shape == (3, 4, 640)
+    assert torch.equal(out["loss"].flatten(), flat["loss"]) and torch.equal(out["grad"].view(12, 640), flat["grad"])
+
+
+@pytest.mark.parametrize("T", [0.05, 1.0, 20.0])
+@pytest.mark.parametrize("kl,tv", [(1.0, 0.0), (0.0, 1.0), (0.1, 0.9), (-0.5, 0.25)])
+def test_temperatures_and_weights(dsp, T, kl, tv):
+    a = make(36, 5, 1200, 10, torch.float32)
+    a["rho"][:3] = (0.0, 1.0, 1e-6)
+    kw = dict(temperature=T, alpha_kl=kl, alpha_tv=tv)
+    compare(a, call(dsp, a, **kw), **kw)
+
+
+def test_equal_student_and_teacher(dsp):
+    """p = q: the loss is zero up to rounding, and so is KL's gradient."""
+    a = make(37, 4, 500, 20, torch.float32)
+    x = a["x"].double().numpy()
+    q = np.exp(x) / np.exp(x).sum(1, keepdims=True)
+    a["t"] = np.take_along_axis(x, a["ids"].astype(np.int64), 1).astype(np.float32)
+    a["rho"] = (1 - np.take_along_axis(q, a["ids"].astype(np.int64), 1).sum(1)).astype(np.float32)
+    out = call(dsp, a, temperature=1.0, alpha_kl=1.0, alpha_tv=0.0)
+    E = tr.distill_row(x[0], a["ids"][0], a["t"][0], a["rho"][0], 1.0, 1.0, 1.0, 0.0)[4]
+    assert out["loss"].abs().max() <= 2 * 2 * E
+    assert out["grad"].abs().max() <= 2 * 2 * E
+
+
+def test_gradient_equals_differences(dsp):
+    """The call's own loss, differenced by its own logits (32 bits: steps of 2^-6)."""
+    a = make(38, 1, 12, 4, torch.float32)
+    g = host(call(dsp, a)["grad"])[0]
+    h = 2.0 ** -6
+    for v in range(12):
+        L = []
+        for s in (h, -h):
+            b = dict(a, x=a["x"].clone())
+            b["x"][0, v] += s
+            L.append(float(call(dsp, b, grad=False)["loss"][0]))
+        # second-order remainder h^2 / 6 of a third derivative below w (|a_kl| + a_tv), and the
+        # losses' own rounding over 2 h
+        assert abs((L[0] - L[1]) / (2 * h) - g[v]) <= float(a["w"][0]) * 1.3 * (h * h + 2e-6 / h)
+
+
+def test_offsets_past_32_bits(dsp):
+    N, V, ld = 10, 1003, 1 << 28
+    a = make(39, N, V, 6, torch.bfloat16)
+    buf = torch.empty(N * ld - (ld - V), dtype=torch.bfloat16, device="cuda").as_strided((N, V), (ld, 1))
+    buf.copy_(a["x"].cuda())
+    out = call(dsp, a, logits=buf, grad=buf)
+    compare(a, dict(out, grad=buf.contiguous()))
+
+
+def test_teacher_token_out_of_range_is_reported():
+    a = make(40, 3, 50, 4, torch.float32)
+    b = {k: v.copy() if k == "ids" else v for k, v in a.items()}
+    b["ids"][1, 2] = 50
+    with binding.Context(0, B_max=1, V_max=8, K_max=1) as ctx:
+        out = call(ctx, b)
+        torch.cuda.synchronize()
+        assert ctx.status() == binding.DEVICE_OOB
+        b["ids"][1, 2] = -1  # skipped like an empty slot
+        compare(b, out)
+
+
+def test_side_stream_graph_and_repeat(dsp):
+    a = make(41, 9, 5000, 8, torch.bfloat16)
+    want = call(dsp, a)
+    x = a["x"].cuda()
+    ids, t, rho, w = (dev(a[n]) for n in ("ids", "t", "rho", "w"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = binding.distill(dsp, x, ids, t, teacher_rest=rho, row_weight=w, **KW)
+    side.synchronize()
+    assert torch.equal(out["grad"], want["grad"]) and torch.equal(out["loss"], want["loss"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = binding.distill(dsp, x, ids, t, teacher_rest=rho, row_weight=w, **KW)
+    for s in (0.5, 1.0):
+        x.copy_(a["x"].cuda() * s)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out["grad"], want["grad"]) and torch.equal(out["loss"], want["loss"])
+
+
+def test_refusals(dsp):
+    a = make(42, 3, 64, 4, torch.float32)
+    with pytest.raises(binding.DSparkError) as err:
+        call(dsp, a, temperature=0.0)
+    assert err.value.code == binding.INVALID_ARG
+    with pytest.raises(TypeError, match="float16"):
+        call(dsp, a, logits=a["x"].cuda().half())
+    with pytest.raises(ValueError, match="last dimension"):
+        call(dsp, a, logits=a["x"].cuda().t().contiguous().t())
+    with pytest.raises(TypeError):
+        call(dsp, a, grad=torch.empty(3, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="grad: shape"):
+        call(dsp, a, grad=torch.empty(3, 65, device="cuda"))
