@@ -120,6 +120,7 @@ _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 
 
 def _ptr(t: Optional[torch.Tensor], dtypes=None, name: str = "tensor"):
+    """Address of a contiguous CUDA tensor (None passes through)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
@@ -128,13 +129,13 @@ def _ptr(t: Optional[torch.Tensor], dtypes=None, name: str = "tensor"):
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: must live in CUDA device memory")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows(t: Optional[torch.Tensor], dtype, name: str):
-    """Pointer and row distance (elements) of a [..., D] tensor whose last dimension is
+    """Address and row distance (elements) of a [..., D] tensor whose last dimension is
     contiguous and whose rows are evenly spaced (a slice of a wider contiguous tensor)."""
     if t is None:
         return None, 0
@@ -142,20 +143,23 @@ def _rows(t: Optional[torch.Tensor], dtype, name: str):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: must live in CUDA device memory")
+    if t.is_contiguous() and t.dim() > 0:
+        return t.data_ptr(), t.shape[-1]
+    shape, strides = t.shape, t.stride()
+    if t.dim() == 0 or (shape[-1] > 1 and strides[-1] != 1):
+        raise ValueError(f"{name}: the last dimension must be contiguous")
     ld = step = None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if size == 1:
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] == 1:
             continue
         if ld is None:
-            ld = stride
-        elif stride != step:
+            ld = strides[i]
+        elif strides[i] != step:
             raise ValueError(f"{name}: rows must be evenly spaced")
-        step = stride * size
-    if t.dim() == 0 or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.shape[-1] if ld is None else ld
+        step = strides[i] * shape[i]
+    return t.data_ptr(), shape[-1] if ld is None else ld
 
 
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}  # dspark_dtype
@@ -176,10 +180,14 @@ def _shape(t: Optional[torch.Tensor], shape, name: str):
 
 def _stream(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        index = device if isinstance(device, int) else device.index
+        if index is None:
+            index = torch.cuda.current_device()
+        # the handle that torch.cuda.current_stream(device).cuda_stream gives, without the object
+        return torch._C._cuda_getCurrentRawStream(index)
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _check(code: int, where: str):

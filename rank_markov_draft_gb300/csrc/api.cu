@@ -1042,7 +1042,8 @@ int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
   a.tv = tv;
   a.grad = grad;
   a.status = ctx->d_status;
-  st = cuda_status(dspark::launch_distill(a, reinterpret_cast<cudaStream_t>(stream)));
+  a.timeout_ns = ctx->timeout_ns;
+  st = cuda_status(dspark::launch_distill(a, ctx->num_sms, reinterpret_cast<cudaStream_t>(stream)));
   if (st == DSPARK_OK) ctx->last_launches = 1;
   return st;
 }

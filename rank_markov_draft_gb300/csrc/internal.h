@@ -261,8 +261,9 @@ struct DistillArgs {
   float* tv;                    // [N] or null
   void* grad;                   // [N, V] of dtype, rows ld_grad apart, or null
   int* status;
+  uint64_t timeout_ns;
 };
-cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream);
+cudaError_t launch_distill(const DistillArgs& a, int num_sms, cudaStream_t stream);
 
 // ---- the RNN head's recurrence over given sequences (rnn_scan.cu)
 struct RnnScanArgs {
