@@ -46,6 +46,8 @@ struct dspark_ctx {
   int32_t* d_l_prev = nullptr;           // [B_max * K_max] predecessors of the drafted tokens
   float* d_l_offq2 = nullptr;            // [B_max * K_max] log2 q offsets
   float* d_topk_part_v = nullptr;
+  // recurrence over long sequences: tile records, zero between calls
+  uint8_t* d_chain = nullptr;
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
   uint32_t epoch = 0;                    // last key epoch used
   int poisoned = 0;
@@ -133,6 +135,10 @@ bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p
 // Element size of a dspark_dtype (0: not one).
 size_t dtype_size(int dtype) {
   return dtype == DSPARK_F32 ? 4 : (dtype == DSPARK_BF16 ? 2 : 0);
+}
+
+dspark::ScanLaunch scan_launch(dspark_ctx* ctx) {
+  return {ctx->d_chain, ctx->num_sms, ctx->d_status, ctx->timeout_ns, &ctx->last_launches, 0, 0};
 }
 
 // The arguments that both directions of the RNN head's recurrence share.
@@ -482,13 +488,15 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
             cudaMalloc(&ctx->d_v_fail, sizeof(unsigned long long) * B_max) == cudaSuccess &&
             cudaMalloc(&ctx->d_v_count, sizeof(int) * B_max) == cudaSuccess &&
             cudaMalloc(&ctx->d_l_prev, sizeof(int32_t) * rows) == cudaSuccess &&
-            cudaMalloc(&ctx->d_l_offq2, sizeof(float) * rows) == cudaSuccess;
+            cudaMalloc(&ctx->d_l_offq2, sizeof(float) * rows) == cudaSuccess &&
+            cudaMalloc(&ctx->d_chain, dspark::kChainBytes) == cudaSuccess;
   ok = ok && cudaMemset(ctx->d_status, 0, sizeof(int)) == cudaSuccess &&
        cudaMemset(ctx->d_bar, 0, sizeof(uint32_t)) == cudaSuccess &&
        cudaMemset(ctx->d_keys, 0, sizeof(unsigned long long) * K_max * dspark::kBatchChunk) ==
            cudaSuccess &&
        cudaMemset(ctx->d_v_fail, 0, sizeof(unsigned long long) * B_max) == cudaSuccess &&
        cudaMemset(ctx->d_v_count, 0, sizeof(int) * B_max) == cudaSuccess &&
+       cudaMemset(ctx->d_chain, 0, dspark::kChainBytes) == cudaSuccess &&
        cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
     dspark_ctx_destroy(ctx);
@@ -520,6 +528,7 @@ int dspark_ctx_destroy(dspark_ctx* ctx) {
   cudaFree(ctx->d_l_prev);
   cudaFree(ctx->d_l_offq2);
   cudaFree(ctx->d_topk_part_v);
+  cudaFree(ctx->d_chain);
   delete ctx;
   return DSPARK_OK;
 }
@@ -535,7 +544,8 @@ int dspark_ctx_reset(dspark_ctx* ctx, dspark_stream_t stream) {
                             s) == cudaSuccess &&
             cudaMemsetAsync(ctx->d_v_fail, 0, sizeof(unsigned long long) * ctx->B_max, s) ==
                 cudaSuccess &&
-            cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess;
+            cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess &&
+            cudaMemsetAsync(ctx->d_chain, 0, dspark::kChainBytes, s) == cudaSuccess;
   if (!ok) return DSPARK_ERR_CUDA;
   ctx->bar_counter = 0;
   ctx->epoch = 0;
@@ -1073,9 +1083,8 @@ int dspark_rnn_scan(dspark_ctx* ctx, const void* za, const void* zg, const void*
   a.dtype = dtype;
   a.s = s;
   a.s_last = s_last;
-  st = cuda_status(dspark::launch_rnn_scan(a, reinterpret_cast<cudaStream_t>(stream)));
-  if (st == DSPARK_OK) ctx->last_launches = 1;
-  return st;
+  return cuda_status(
+      dspark::launch_rnn_scan(a, scan_launch(ctx), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const void* e,
@@ -1120,9 +1129,8 @@ int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const 
   a.dzg = dzg;
   a.de = de;
   a.ds0 = ds0;
-  st = cuda_status(dspark::launch_rnn_scan_grad(a, reinterpret_cast<cudaStream_t>(stream)));
-  if (st == DSPARK_OK) ctx->last_launches = 1;
-  return st;
+  return cuda_status(
+      dspark::launch_rnn_scan_grad(a, scan_launch(ctx), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

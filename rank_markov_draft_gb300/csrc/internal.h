@@ -287,7 +287,23 @@ struct RnnScanGradArgs {
   void *dza, *dzg, *de;
   float* ds0;                // [N, D] or null
 };
-cudaError_t launch_rnn_scan(const RnnScanArgs& a, cudaStream_t stream);
-cudaError_t launch_rnn_scan_grad(const RnnScanGradArgs& a, cudaStream_t stream);
+// Scratch of sequences split over CTAs: kChainSlots records of a tile's span (8 bytes) and end
+// value (4 bytes) for kChainLanes channels, the values that pass from launch to launch, and a
+// flag a record and two counters, zero between launches.
+constexpr int kChainSlots = 8192, kChainLanes = 64, kChainBlocks = 512;
+constexpr size_t kChainBytes = static_cast<size_t>(kChainSlots) * (kChainLanes * 12 + 4) +
+                               kChainBlocks * kChainLanes * 4 + 8;
+struct ScanLaunch {
+  void* chain;
+  int num_sms;
+  int* status;
+  uint64_t timeout_ns;
+  int* launches;       // host: kernels launched (added to)
+  int64_t first_tile;  // set by the launch
+  int launch_tiles;
+};
+cudaError_t launch_rnn_scan(const RnnScanArgs& a, const ScanLaunch& c, cudaStream_t stream);
+cudaError_t launch_rnn_scan_grad(const RnnScanGradArgs& a, const ScanLaunch& c,
+                                 cudaStream_t stream);
 
 }  // namespace dspark

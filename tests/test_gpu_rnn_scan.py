@@ -99,6 +99,28 @@ def test_long_memory(dsp, dtype):
     check_backward(dsp, a, check_forward(dsp, a)["s"])
 
 
+@pytest.mark.parametrize("dtype,D", [(torch.float32, 64), (torch.bfloat16, 128)])
+def test_more_tiles_than_one_launch_has_records_for(dsp, dtype, D):
+    """300 blocks of lanes over 30 tiles of 128 steps: the sequence passes from launch to launch."""
+    N, L = 150, 3801
+    a = make(13, N, L, D, dtype, reset=0.0005)
+    out = forward(dsp, a)
+    grad = binding.rnn_scan_grad(dsp, cuda(a["za"]), cuda(a["zg"]), cuda(a["e"]), out["s"], cuda(a["ds"]), s0=dev(a["s0"]),
+                                 ds_last=dev(a["ds_last"]), reset=dev(a["reset"]))
+    torch.cuda.synchronize()
+    assert dsp.last_launches == 2 and dsp.status() == 0
+    at = [0, 77, 149]
+    b = {k: None if v is None else v[at] for k, v in a.items()}
+    s, err = tr.rnn_scan(f64(b["za"]), f64(b["zg"]), f64(b["e"]), b["s0"], b["reset"])
+    near(out["s"][at], s, err, HALF[dtype], "s")
+    near(out["s_last"][at], s[:, -1], err[:, -1], HALF[torch.float32], "s_last")
+    want, bound = tr.rnn_scan_grad(f64(b["za"]), f64(b["zg"]), f64(b["e"]), f64(out["s"][at]), f64(b["ds"]), b["s0"],
+                                   b["ds_last"], b["reset"])
+    for i, name in enumerate(("dza", "dzg", "de")):
+        near(grad[name][at], want[i], bound[i], HALF[dtype], name)
+    near(grad["ds0"][at], want[3], bound[3], HALF[torch.float32], "ds0")
+
+
 def test_saturated_gates(dsp):
     """Gates of exactly 0 and 1, and beyond: infinities, the type's lowest and largest values."""
     a = make(6, 2, 700, 24, torch.float32)
