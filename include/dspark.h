@@ -518,8 +518,8 @@ int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
  *   za, zg, e [N, L, D] of type dtype: channels contiguous, consecutive rows (n L + t)
  *     ld_za, ld_zg, ld_e elements apart (two halves of one projection's output, say)
  *   s0 [N, D] fp32 state before t = 0 (NULL: 0)
- *   reset [N, L] uint8 (NULL: none): non-zero makes a_t zero, so a sequence starts there;
- *     a decay of exactly zero drops the earlier state whatever it holds
+ *   reset [N, L] uint8 (NULL: none): non-zero makes a_t zero and drops the earlier state
+ *     whatever it holds, so a sequence starts there
  * Outputs s [N, L, D] of type dtype, contiguous; s_last [N, D] fp32 the state after
  * t = L - 1 (NULL: not written).  L = 1 with s0 and s_last is the step of one token; s0
  * and s_last may be the same buffer.  Any N, L, D >= 1 (N L < 2^31, N D < 2^31); pointers

@@ -138,7 +138,8 @@ size_t dtype_size(int dtype) {
 }
 
 dspark::ScanLaunch scan_launch(dspark_ctx* ctx) {
-  return {ctx->d_chain, ctx->num_sms, ctx->d_status, ctx->timeout_ns, &ctx->last_launches, 0, 0};
+  return {ctx->d_chain, ctx->num_sms, ctx->d_status, ctx->timeout_ns, &ctx->last_launches, 0, 0,
+          false};
 }
 
 // The arguments that both directions of the RNN head's recurrence share.

@@ -289,7 +289,7 @@ struct RnnScanGradArgs {
 };
 // Scratch of sequences split over CTAs: kChainSlots records of a tile's span (8 bytes) and end
 // value (4 bytes) for kChainLanes channels, the values that pass from launch to launch, and a
-// flag a record and two counters, zero between launches.
+// flag a record and a counter, zero between launches.
 constexpr int kChainSlots = 8192, kChainLanes = 64, kChainBlocks = 512;
 constexpr size_t kChainBytes = static_cast<size_t>(kChainSlots) * (kChainLanes * 12 + 4) +
                                kChainBlocks * kChainLanes * 4 + 8;
@@ -301,6 +301,7 @@ struct ScanLaunch {
   int* launches;       // host: kernels launched (added to)
   int64_t first_tile;  // set by the launch
   int launch_tiles;
+  bool wide;
 };
 cudaError_t launch_rnn_scan(const RnnScanArgs& a, const ScanLaunch& c, cudaStream_t stream);
 cudaError_t launch_rnn_scan_grad(const RnnScanGradArgs& a, const ScanLaunch& c,

@@ -8,27 +8,29 @@
 //   delta_t = ds_t + y_{t+1},  y_t = a_t delta_t,  y_L = ds_last,  ds0 = y_0
 //   dza_t = delta_t s_{t-1} a_t (1 - a_t),  dzg_t = delta_t e_t g_t (1 - g_t),
 //   de_t = delta_t g_t.
-// A reset at t makes a_t zero.  A decay of exactly zero drops the earlier state, whatever it
-// holds (an infinity or NaN before a reset stays before it).
+// A reset at t makes a_t zero and drops the earlier state, whatever it holds (an infinity or NaN
+// before a reset stays before it).
 //
 // Both directions are a recurrence x_t = a_t x_{t-1} + b_t, so a span of steps acts on the
 // value before it as x -> A x + S (A the product of its decays, S its end from zero).  A warp
-// holds 16 steps of 32 lanes in registers (a lane is 4 bytes of channels: two bf16 or one fp32;
-// lanes run over sequences and channels alike, so no channel count leaves lanes empty): it
-// loads them once, reduces them to (A, S), learns the value before them from the warps before
-// it, and runs them again from there.  Three ways to learn it:
+// works on 16 steps of 32 lanes at a time (a lane is 4 bytes of channels: two bf16 or one fp32;
+// lanes run over sequences and channels alike, so no channel count leaves lanes empty).  The
+// steps arrive in shared memory by asynchronous copies, the next unit's while this one is
+// worked on, so loads are in flight all the time; a warp reduces its steps to (A, S), learns
+// the value before them from the warps before it, and runs them from there.  Three ways:
 //   L <= 16:         there is nothing before them but s0.
-//   many lanes:      the CTA's W warps hold consecutive spans, exchange (A, S) through shared
+//   many lanes:      a CTA's warps hold consecutive spans, exchange (A, S) through shared
 //                    memory and walk over the sequence; the value after a tile stays with them.
-//   few lanes, long: the walk alone would leave most SMs empty, so tiles of one sequence go to
-//                    different CTAs in the order of a ticket.  A tile publishes its (A, S) as
-//                    soon as it has them and its end value once that is known; a tile folds
-//                    the (A, S) after the nearest known end value, strictly in order, so the
-//                    result does not depend on which one that was.
+//   few lanes, long: the walk alone would leave most SMs empty, so the tiles of a sequence go
+//                    around the CTAs of a cooperative launch (all of them run).  A tile publishes
+//                    its (A, S) as soon as it has them and its end value once that is known; a
+//                    tile folds the (A, S) after the nearest known end value, strictly in order,
+//                    so the result does not depend on which one that was.
 // Every input is read once and every output written once in all three.
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -38,42 +40,24 @@ namespace dspark {
 namespace {
 
 constexpr int kSteps = 16;      // of a warp
-constexpr int kScanWarps = 8;   // of a CTA
+constexpr int kStages = 2;      // units in shared memory: this one and the next
 constexpr float kRsLog2e = 1.4426950408889634f;
 
-// ---- lanes: kVec channels of 4 bytes (2 for single bf16 channels), kept raw in one register
+// ---- lanes: kVec channels in one 32-bit word
 template <typename T, int kVec>
-struct Lane;
-template <>
-struct Lane<float, 1> {
-  static __device__ __forceinline__ uint32_t load(const float* p) {
-    return __ldcs(reinterpret_cast<const uint32_t*>(p));
-  }
-  static __device__ __forceinline__ float get(uint32_t r, int) { return __uint_as_float(r); }
-  static __device__ __forceinline__ void store(float* p, const float* x) { __stcs(p, x[0]); }
-};
-template <>
-struct Lane<uint16_t, 1> {
-  static __device__ __forceinline__ uint32_t load(const uint16_t* p) { return __ldcs(p); }
-  static __device__ __forceinline__ float get(uint32_t r, int) { return __uint_as_float(r << 16); }
-  static __device__ __forceinline__ void store(uint16_t* p, const float* x) {
-    __stcs(p, __bfloat16_as_ushort(__float2bfloat16_rn(x[0])));
-  }
-};
-template <>
-struct Lane<uint16_t, 2> {
-  static __device__ __forceinline__ uint32_t load(const uint16_t* p) {
-    return __ldcs(reinterpret_cast<const uint32_t*>(p));
-  }
-  static __device__ __forceinline__ float get(uint32_t r, int i) {
-    return __uint_as_float(i == 0 ? r << 16 : r & 0xFFFF0000u);
-  }
-  static __device__ __forceinline__ void store(uint16_t* p, const float* x) {
-    uint32_t r;  // one rounding to bf16, to nearest even, where a value leaves the recurrence
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x[1]), "f"(x[0]));
-    __stcs(reinterpret_cast<uint32_t*>(p), r);
-  }
-};
+__device__ __forceinline__ float channel(uint32_t w, int i) {
+  if (sizeof(T) == 4) return __uint_as_float(w);
+  return __uint_as_float(kVec == 2 && i == 1 ? w & 0xFFFF0000u : w << 16);
+}
+__device__ __forceinline__ void put_lane(float* p, const float (&x)[1]) { __stcs(p, x[0]); }
+__device__ __forceinline__ void put_lane(uint16_t* p, const float (&x)[1]) {
+  __stcs(p, __bfloat16_as_ushort(__float2bfloat16_rn(x[0])));
+}
+__device__ __forceinline__ void put_lane(uint16_t* p, const float (&x)[2]) {
+  uint32_t r;  // one rounding to bf16, to nearest even, where a value leaves the recurrence
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x[1]), "f"(x[0]));
+  __stcs(reinterpret_cast<uint32_t*>(p), r);
+}
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
@@ -85,14 +69,27 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ float gate(float z) {
   return rcp_approx(1.f + ex2_approx(-z * kRsLog2e));
 }
-// and 1 - sigmoid(z) to full relative precision, down to the denormals that a product with a
-// large gradient brings back into range (so not the exponential that flushes them)
-__device__ __forceinline__ float gate(float z, float& rest) {
-  const float t = exp2f(-z * kRsLog2e);
-  float a;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(a) : "f"(1.f + t));
-  rest = t <= 1.f ? t * a : 1.f - a;
-  return a;
+// and its derivative to full relative precision: with t = e^-|z| and r = 1 / (1 + t) the two
+// sides of the gate are r and t r, the derivative t r^2.  t is the square of e^(-|z| / 2), which
+// keeps it down to the denormals that a product with a large gradient brings back into range.
+// (Explicit roundings here and below: what the compiler fuses differs between instances.)
+__device__ __forceinline__ float gate(float z, float& slope) {
+  const float h = ex2_approx(-0.5f * kRsLog2e * fabsf(z));
+  const float t = __fmul_rn(h, h), r = rcp_approx(__fadd_rn(1.f, t)), low = __fmul_rn(t, r);
+  slope = __fmul_rn(low, r);
+  return z >= 0.f ? r : low;
+}
+
+// Asynchronous copy of 16 or 4 bytes, zeros where `on` is false.
+__device__ __forceinline__ void copy_16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_4(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(on ? 4 : 0)
+               : "memory");
 }
 
 // A span's effect x -> A x + S.  kDrops in A: a decay of exactly zero inside, so x is dropped
@@ -108,13 +105,13 @@ __device__ __forceinline__ Span then(Span f, Span g) {  // f first
   return {f.A == kDrops || g.A == kDrops ? kDrops : f.A * g.A, apply(g, f.S)};
 }
 
-// ---- the ticketed tiles' records (context scratch; flags and tickets zero between launches)
+// ---- the chained tiles' records (context scratch; flags and counter zero between launches)
 struct ChainView {
   Span* span;       // [slots][kChainLanes]
   float* end;       // [slots][kChainLanes]
   float* carry;     // [kChainBlocks][kChainLanes] the value after the launch before
   uint32_t* flag;   // [slots] 1: span known, 2: end known
-  uint32_t* ticket; // [0] next ticket, [1] CTAs done
+  uint32_t* done;   // CTAs
 };
 __device__ __forceinline__ ChainView chain_view(void* scratch) {
   ChainView v;
@@ -122,7 +119,7 @@ __device__ __forceinline__ ChainView chain_view(void* scratch) {
   v.end = reinterpret_cast<float*>(v.span + kChainSlots * kChainLanes);
   v.carry = v.end + kChainSlots * kChainLanes;
   v.flag = reinterpret_cast<uint32_t*>(v.carry + kChainBlocks * kChainLanes);
-  v.ticket = v.flag + kChainSlots;
+  v.done = v.flag + kChainSlots;
   return v;
 }
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
@@ -196,76 +193,99 @@ __device__ __forceinline__ void chain_step(const ChainView& v, int tile, int fir
   }
 }
 
-// The last CTA of the launch to finish leaves flags and tickets as it found them.
-__device__ __forceinline__ void chain_leave(const ChainView& v, uint32_t* s_last) {
+// The last CTA of the launch to finish leaves flags and counter as it found them.
+__device__ __forceinline__ void chain_leave(const ChainView& v, int tiles) {
+  __shared__ uint32_t s_last;
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    *s_last = atomicAdd(v.ticket + 1, 1u) == gridDim.x - 1 ? 1u : 0u;
+    s_last = atomicAdd(v.done, 1u) == gridDim.x - 1 ? 1u : 0u;
   }
   __syncthreads();
-  if (*s_last == 0u) return;
-  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += blockDim.x) v.flag[i] = 0u;
-  if (threadIdx.x < 2) v.ticket[threadIdx.x] = 0u;
+  if (s_last == 0u) return;
+  for (int i = threadIdx.x; i < tiles; i += blockDim.x) v.flag[i] = 0u;
+  if (threadIdx.x == 0) *v.done = 0u;
 }
 
-// What a direction does with its 16 steps: load them, give their span, run them from a value.
+// ---- the two directions: their streams, their step's (a, b), and what a step writes
+struct Stream {
+  const void* p;
+  int64_t ld;  // elements between rows
+  int shift;   // rows back (the state before a step)
+};
+
 template <typename T, int kVec>
 struct Forward {
   using Args = RnnScanArgs;
-  using Ln = Lane<T, kVec>;
   static constexpr bool kReverse = false;
-  float a[kSteps][kVec], b[kSteps][kVec];
+  static constexpr int kStreams = 3, kWarps = 8;
+  static __device__ __forceinline__ Stream stream(const Args& p, int i) {
+    return i == 0 ? Stream{p.za, p.ld_za, 0} : i == 1 ? Stream{p.zg, p.ld_zg, 0}
+                                                      : Stream{p.e, p.ld_e, 0};
+  }
+  static __device__ __forceinline__ const float* first(const Args& p) { return p.s0; }
 
-  __device__ __forceinline__ void load(const Args& p, int64_t n, int d, int64_t t0, int steps) {
-    const int64_t r = n * p.L + t0;
-    const T* za = static_cast<const T*>(p.za) + r * p.ld_za + d;
-    const T* zg = static_cast<const T*>(p.zg) + r * p.ld_zg + d;
-    const T* e = static_cast<const T*>(p.e) + r * p.ld_e + d;
-    uint32_t ra[kSteps], rg[kSteps], re[kSteps], keep = 0xFFFFFFFFu;
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      ra[j] = rg[j] = re[j] = 0u;
-      if (j < steps) {
-        ra[j] = Ln::load(za + j * p.ld_za);
-        if (p.zg != nullptr) rg[j] = Ln::load(zg + j * p.ld_zg);
-        re[j] = Ln::load(e + j * p.ld_e);
-        if (p.reset != nullptr && __ldg(p.reset + r + j) != 0) keep &= ~(1u << j);
-      }
-    }
+  // words: [stream][step][lane] of this warp, at this lane.  a < 0: a reset.
+  float a[kSteps][kVec], b[kSteps][kVec];
+  template <bool kReset>
+  __device__ __forceinline__ void read(const Args& p, const uint32_t* words, uint32_t resets,
+                                       int steps) {
 #pragma unroll
     for (int j = 0; j < kSteps; ++j)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const float g = p.zg != nullptr ? gate(Ln::get(rg[j], i)) : 1.f;
-        a[j][i] = j >= steps ? 1.f : (keep >> j & 1u ? gate(Ln::get(ra[j], i)) : 0.f);
-        b[j][i] = j < steps ? g * Ln::get(re[j], i) : 0.f;
+        a[j][i] = gate(channel<T, kVec>(words[j * 32], i));
+        b[j][i] = channel<T, kVec>(words[(2 * kSteps + j) * 32], i);
       }
-  }
-  __device__ __forceinline__ void span(int, Span (&f)[kVec]) const {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      f[i] = {1.f, 0.f};
+    if (p.zg != nullptr) {
 #pragma unroll
       for (int j = 0; j < kSteps; ++j)
-        f[i] = then(f[i], Span{a[j][i] == 0.f ? kDrops : a[j][i], b[j][i]});
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          b[j][i] *= gate(channel<T, kVec>(words[(kSteps + j) * 32], i));
+    }
+    if (kReset && resets != 0u) {
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          if (resets >> j & 1u) a[j][i] = kDrops;
+    }
+    if (steps < kSteps) {  // a step past the end changes nothing
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          if (j >= steps) a[j][i] = 1.f, b[j][i] = 0.f;
     }
   }
-  __device__ __forceinline__ void first_value(const Args& p, int64_t q, float (&x)[kVec]) const {
+  template <bool kReset>
+  __device__ __forceinline__ Span span(int i) const {
+    Span f{1.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = p.s0 != nullptr ? p.s0[q + i] : 0.f;
+    for (int j = 0; j < kSteps; ++j) {
+      if (kReset) {
+        f = then(f, Span{a[j][i], b[j][i]});
+      } else {
+        f.A *= a[j][i];
+        f.S = fmaf(a[j][i], f.S, b[j][i]);
+      }
+    }
+    return f;
   }
-  __device__ __forceinline__ void run(const Args& p, int64_t n, int d, int64_t t0, int steps,
-                                      float (&x)[kVec]) const {
+  template <bool kReset, bool kFull>
+  __device__ __forceinline__ void run(const Args& p, const uint32_t*, uint32_t, int64_t n, int d,
+                                      int64_t t0, int steps, float (&x)[kVec]) const {
     T* s = static_cast<T*>(p.s) + (n * p.L + t0) * p.D + d;
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-      if (j >= steps) break;
+      if (!kFull && j >= steps) break;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = a[j][i] == 0.f ? b[j][i] : fmaf(a[j][i], x[i], b[j][i]);
-      Ln::store(s + static_cast<int64_t>(j) * p.D, x);
+      for (int i = 0; i < kVec; ++i)
+        x[i] = kReset && a[j][i] < 0.f ? b[j][i] : fmaf(a[j][i], x[i], b[j][i]);
+      put_lane(s + static_cast<int64_t>(j) * p.D, x);
     }
-    if (p.s_last != nullptr && steps > 0 && t0 + steps == p.L)
+    if (p.s_last != nullptr && t0 + steps == p.L && (kFull || steps > 0))
 #pragma unroll
       for (int i = 0; i < kVec; ++i) p.s_last[n * p.D + d + i] = x[i];
   }
@@ -274,150 +294,283 @@ struct Forward {
 template <typename T, int kVec>
 struct Backward {
   using Args = RnnScanGradArgs;
-  using Ln = Lane<T, kVec>;
   static constexpr bool kReverse = true;
-  uint32_t za[kSteps], zg[kSteps], e[kSteps], ds[kSteps], s[kSteps], keep;
+  static constexpr int kStreams = 5, kWarps = 4;
+  static __device__ __forceinline__ Stream stream(const Args& p, int i) {
+    return i == 0   ? Stream{p.za, p.ld_za, 0}
+           : i == 1 ? Stream{p.zg, p.ld_zg, 0}
+           : i == 2 ? Stream{p.e, p.ld_e, 0}
+           : i == 3 ? Stream{p.ds, p.D, 0}
+                    : Stream{p.s, p.D, 1};
+  }
+  static __device__ __forceinline__ const float* first(const Args& p) { return p.ds_last; }
 
-  __device__ __forceinline__ void load(const Args& p, int64_t n, int d, int64_t t0, int steps) {
-    const int64_t r = n * p.L + t0;
-    const T* pa = static_cast<const T*>(p.za) + r * p.ld_za + d;
-    const T* pg = static_cast<const T*>(p.zg) + r * p.ld_zg + d;
-    const T* pe = static_cast<const T*>(p.e) + r * p.ld_e + d;
-    const T* pd = static_cast<const T*>(p.ds) + r * p.D + d;
-    const T* ps = static_cast<const T*>(p.s) + (r - 1) * p.D + d;  // the state before
-    keep = 0xFFFFFFFFu;
+  const uint32_t* w;
+  uint32_t drop;
+  int count;
+  template <bool kReset>
+  __device__ __forceinline__ void read(const Args&, const uint32_t* words, uint32_t resets,
+                                       int steps) {
+    w = words;
+    drop = kReset ? resets : 0u;
+    count = steps;
+  }
+  template <bool kReset>
+  __device__ __forceinline__ Span span(int i) const {
+    Span f{1.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      za[j] = zg[j] = e[j] = ds[j] = s[j] = 0u;
-      if (j < steps) {
-        za[j] = Ln::load(pa + j * p.ld_za);
-        ds[j] = Ln::load(pd + static_cast<int64_t>(j) * p.D);
-        if (p.reset != nullptr && __ldg(p.reset + r + j) != 0) keep &= ~(1u << j);
+    for (int j = kSteps - 1; j >= 0; --j) {
+      const float a = gate(channel<T, kVec>(w[j * 32], i));
+      const float ds = channel<T, kVec>(w[(3 * kSteps + j) * 32], i);
+      if (j >= count) continue;
+      if (kReset && (drop >> j & 1u)) {
+        f = Span{kDrops, 0.f};
+      } else {
+        f.S = __fmul_rn(a, __fadd_rn(f.S, ds));
+        f.A = f.A == kDrops ? kDrops : f.A * a;
       }
     }
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j)
-      if (j < steps) {
-        if (p.zg != nullptr) zg[j] = Ln::load(pg + j * p.ld_zg);
-        e[j] = Ln::load(pe + j * p.ld_e);
-        if (t0 + j > 0) s[j] = Ln::load(ps + static_cast<int64_t>(j) * p.D);
-      }
+    return f;
   }
-  __device__ __forceinline__ void span(int steps, Span (&f)[kVec]) const {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      f[i] = {1.f, 0.f};
-#pragma unroll
-      for (int j = kSteps - 1; j >= 0; --j) {
-        if (j >= steps) continue;
-        const float a = keep >> j & 1u ? gate(Ln::get(za[j], i)) : 0.f;
-        f[i] = then(f[i], Span{a == 0.f ? kDrops : a, a == 0.f ? 0.f : a * Ln::get(ds[j], i)});
-      }
-    }
-  }
-  __device__ __forceinline__ void first_value(const Args& p, int64_t q, float (&x)[kVec]) const {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = p.ds_last != nullptr ? p.ds_last[q + i] : 0.f;
-  }
-  __device__ __forceinline__ void run(const Args& p, int64_t n, int d, int64_t t0, int steps,
+  template <bool kReset, bool kFull>
+  __device__ __forceinline__ void run(const Args& p, const uint32_t* words, uint32_t resets,
+                                      int64_t n, int d, int64_t t0, int steps,
                                       float (&x)[kVec]) const {
     const int64_t r = n * p.L + t0;
     T* pa = static_cast<T*>(p.dza) + r * p.ld_dza + d;
     T* pg = static_cast<T*>(p.dzg) + r * p.ld_dzg + d;
     T* pe = static_cast<T*>(p.de) + r * p.D + d;
+    const bool gated = p.dzg != nullptr;
+    const int ld_a = static_cast<int>(p.ld_dza), ld_g = static_cast<int>(p.ld_dzg);
 #pragma unroll
     for (int j = kSteps - 1; j >= 0; --j) {
-      if (j >= steps) continue;
+      if (!kFull && j >= steps) continue;
+      const bool reset = kReset && (resets >> j & 1u);
       float oa[kVec], og[kVec], oe[kVec];
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        float na, ng = 0.f, g = 1.f;
-        float a = gate(Ln::get(za[j], i), na);
-        if (!(keep >> j & 1u)) a = 0.f;
-        if (p.zg != nullptr) g = gate(Ln::get(zg[j], i), ng);
-        float before = Ln::get(s[j], i);
-        if (t0 + j == 0) before = p.s0 != nullptr ? p.s0[n * p.D + d + i] : 0.f;
-        const float delta = Ln::get(ds[j], i) + x[i];
-        oa[i] = a == 0.f ? 0.f : delta * before * a * na;
-        og[i] = delta * Ln::get(e[j], i) * g * ng;
-        oe[i] = delta * g;
-        x[i] = a == 0.f ? 0.f : a * delta;
+        const auto get = [&](int k) { return channel<T, kVec>(words[(k * kSteps + j) * 32], i); };
+        float slope;
+        const float a = gate(get(0), slope);
+        float before = get(4);
+        if (j == 0 && t0 == 0) before = p.s0 != nullptr ? p.s0[n * p.D + d + i] : 0.f;
+        const float delta = __fadd_rn(get(3), x[i]);
+        oa[i] = reset ? 0.f : delta * before * slope;
+        x[i] = reset ? 0.f : __fmul_rn(a, delta);
+        oe[i] = delta;
       }
-      Ln::store(pa + j * p.ld_dza, oa);
-      if (p.dzg != nullptr) Ln::store(pg + j * p.ld_dzg, og);
-      Ln::store(pe + static_cast<int64_t>(j) * p.D, oe);
+      put_lane(pa + static_cast<int64_t>(j) * ld_a, oa);
+      if (gated) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          float slope;
+          const float g = gate(channel<T, kVec>(words[(kSteps + j) * 32], i), slope);
+          og[i] = oe[i] * channel<T, kVec>(words[(2 * kSteps + j) * 32], i) * slope;
+          oe[i] *= g;
+        }
+        put_lane(pg + static_cast<int64_t>(j) * ld_g, og);
+      }
+      put_lane(pe + static_cast<int64_t>(j) * p.D, oe);
     }
-    if (p.ds0 != nullptr && t0 == 0 && steps > 0)
+    if (p.ds0 != nullptr && t0 == 0 && (kFull || steps > 0))
 #pragma unroll
       for (int i = 0; i < kVec; ++i) p.ds0[n * p.D + d + i] = x[i];
   }
 };
 
-// Walks: a CTA of kScanWarps warps is kScanWarps / W lane blocks of W consecutive spans (W = 1:
-// no exchange).  Tickets: one lane block, tile c.first_tile + ticket / blocks of `tiles`.
-template <template <typename, int> class Dir, typename T, int kVec, bool kTicket>
-__global__ void __launch_bounds__(kScanWarps * 32, 2)
+// A unit of work of a CTA: spans of W warps, of one lane block a group of W warps.
+struct Unit {
+  int64_t block, tile;  // of the CTA's first group; block < 0: none
+};
+
+// Walks: units (block, 0), (block, 1), ... of every gridDim.x-th CTA's worth of blocks, so a CTA
+// carries the value from unit to unit.  Chains: unit i is tile i / blocks of block i % blocks and
+// goes to CTA i % gridDim.x; CTAs take their units in order, so the first unfinished tile is
+// always being worked on.
+template <template <typename, int> class Dir, typename T, int kVec, bool kChain, bool kReset>
+__global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     scan_kernel(const typename Dir<T, kVec>::Args p, const int W, const int blocks,
                 const ScanLaunch c) {
   using D = Dir<T, kVec>;
-  __shared__ Span s_span[2][kScanWarps][32 * kVec];
+  constexpr int kWarps = D::kWarps, kWords = D::kStreams * kSteps * 32;
+  extern __shared__ uint4 s_raw[];  // [kStages][kWarps] x (kWords words, 32 kVec floats)
+  __shared__ Span s_span[2][kWarps][32 * kVec];
   __shared__ float s_x[32 * kVec];
-  __shared__ uint32_t s_ticket;
+  constexpr int kWarpWords = kWords + 32 * kVec;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t tiles = (p.L + W * kSteps - 1) / (W * kSteps);
+  const int groups = kWarps / W, group = warp / W;
   // `order`: this warp's place in the recurrence's order, `w` in the order of time
-  const int group = warp / W, order = warp % W, w = D::kReverse ? W - 1 - order : order;
-  int64_t block = static_cast<int64_t>(blockIdx.x) * (kScanWarps / W) + group;
-  int64_t tile = 0, tile_end = tiles;
-  ChainView chain{};
-  if (kTicket) {
-    chain = chain_view(c.chain);
-    if (threadIdx.x == 0) s_ticket = atomicAdd(chain.ticket, 1u);
-    __syncthreads();
-    block = s_ticket % blocks;
-    tile = c.first_tile + s_ticket / blocks;
-    tile_end = tile + 1;
+  const int order = warp % W, w = D::kReverse ? W - 1 - order : order;
+  const uint32_t lanes = static_cast<uint32_t>(p.N * p.D);  // channels of all sequences
+  const auto words = [&](int stage) {
+    return reinterpret_cast<uint32_t*>(s_raw) + (stage * kWarps + warp) * kWarpWords;
+  };
+  const ChainView chain = kChain ? chain_view(c.chain) : ChainView{};
+  const int chained = kChain ? blocks * c.launch_tiles : 0;  // units
+  const auto chain_unit = [&](int i) {
+    return i < chained ? Unit{i % blocks, c.first_tile + i / blocks} : Unit{-1, 0};
+  };
+  const auto after = [&](Unit u) {  // (walks)
+    if (++u.tile == tiles) {
+      u.tile = 0;
+      u.block += static_cast<int64_t>(gridDim.x) * groups;
+      if (u.block >= blocks) u.block = -1;
+    }
+    return u;
+  };
+  // first step of this warp's span in a unit
+  const auto start = [&](const Unit& u) {
+    return ((D::kReverse ? tiles - 1 - u.tile : u.tile) * W + w) * kSteps;
+  };
+  const auto sequence = [&](uint32_t q, int64_t& n, int& d) {
+    const uint32_t s = q / static_cast<uint32_t>(p.D);
+    n = s;
+    d = static_cast<int>(q - s * static_cast<uint32_t>(p.D));
+  };
+  // whether the 32 lanes of a block lie in one sequence (then one load brings all its flags)
+  const bool one = kReset && p.D % (32 * kVec) == 0;
+
+  // Start copying a unit's steps (and its flags, into a register).
+  const auto fetch = [&](const Unit& u, int stage, uint32_t& flags) {
+    if (u.block < 0) {
+      cp_async_commit();
+      return;
+    }
+    uint32_t* dst = words(stage);
+    const int64_t t0 = start(u);
+    const uint32_t q0 = static_cast<uint32_t>(u.block + group) * 32u * kVec;
+    if (c.wide) {  // 16-byte pieces: this lane's are 4 steps apart, in one sequence
+      constexpr int kPiece = 16 / sizeof(T);
+      const uint32_t q = q0 + (lane & 7) * kPiece;
+      int64_t n = 0;
+      int d = 0;
+      const bool in = q < lanes;
+      if (in) sequence(q, n, d);
+#pragma unroll
+      for (int i = 0; i < D::kStreams; ++i) {
+        const Stream st = D::stream(p, i);
+        if (st.p == nullptr) continue;
+        const int64_t row = n * p.L + t0 - st.shift + (lane >> 3);
+        const T* src = static_cast<const T*>(st.p) + row * st.ld + d;
+#pragma unroll
+        for (int j = 0; j < kSteps; j += 4) {
+          const int64_t t = t0 + j + (lane >> 3);
+          const bool on = in && t < p.L && (st.shift == 0 || t > 0);
+          copy_16(dst + (i * kSteps + j + (lane >> 3)) * 32 + (lane & 7) * 4,
+                  on ? src + j * st.ld : static_cast<const T*>(st.p), on);
+        }
+      }
+    }
+    const uint32_t q = q0 + lane * kVec;
+    int64_t n = 0;
+    int d = 0;
+    const bool in = q < lanes;
+    if (in) sequence(q, n, d);
+    if (!c.wide) {
+#pragma unroll
+      for (int i = 0; i < D::kStreams; ++i) {
+        const Stream st = D::stream(p, i);
+        if (st.p == nullptr) continue;
+        const T* src = static_cast<const T*>(st.p) + (n * p.L + t0 - st.shift) * st.ld + d;
+        if (sizeof(T) * kVec == 4) {
+#pragma unroll 4
+          for (int j = 0; j < kSteps; ++j) {
+            const bool on = in && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
+            copy_4(dst + (i * kSteps + j) * 32 + lane,
+                   on ? src + j * st.ld : static_cast<const T*>(st.p), on);
+          }
+        } else {  // single bf16 channels: no asynchronous copy is that small
+          uint32_t v[kSteps];
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) {
+            const bool on = in && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
+            v[j] = on ? static_cast<uint32_t>(__ldcs(src + j * st.ld)) : 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) dst[(i * kSteps + j) * 32 + lane] = v[j];
+        }
+      }
+    }
+    if (u.tile == 0 && D::first(p) != nullptr)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        copy_4(dst + kWords + lane * kVec + i, D::first(p) + (in ? q + i : 0), in);
+    cp_async_commit();
+    if (kReset) {
+      const uint8_t* src = p.reset + n * p.L + t0;
+      flags = 0u;
+      if (one) {
+        if (in && lane < kSteps && t0 + lane < p.L) flags = __ldg(src + lane);
+      } else if (in) {
+        for (int j = 0; j < kSteps && t0 + j < p.L; ++j)
+          flags |= static_cast<uint32_t>(__ldg(src + j) != 0) << j;
+      }
+    }
+  };
+
+  Unit cur, nxt;
+  if (kChain) {
+    cur = chain_unit(blockIdx.x);
+    nxt = chain_unit(blockIdx.x + gridDim.x);
+  } else {
+    cur = Unit{static_cast<int64_t>(blockIdx.x) * groups, 0};
+    if (cur.block >= blocks) cur.block = -1;
+    nxt = cur.block < 0 ? cur : after(cur);
   }
-  const int64_t q = (block * 32 + lane) * kVec;
-  const bool valid = q < p.N * p.D;
-  const int64_t n = valid ? q / p.D : 0;
-  const int d = valid ? static_cast<int>(q - n * p.D) : 0;
-  D steps;
+  uint32_t flags = 0u, next_flags = 0u;
+  fetch(cur, 0, flags);
   float x[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) x[i] = 0.f;
-  if (valid && tile == 0) steps.first_value(p, q, x);
-  if (kTicket && tile > 0 && tile == c.first_tile) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = chain.carry[block * kChainLanes + lane * kVec + i];
-  }
-  for (; tile < tile_end; ++tile) {
-    const int64_t t0 = ((D::kReverse ? tiles - 1 - tile : tile) * W + w) * kSteps;
-    const int64_t left = p.L - t0;
+  for (int turn = 0; cur.block >= 0; ++turn) {
+    const int stage = turn & 1;
+    fetch(nxt, stage ^ 1, next_flags);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    const uint32_t* in = words(stage) + lane;
+    const int64_t t0 = start(cur), left = p.L - t0;
+    const int64_t block = cur.block + group;
+    const uint32_t q = static_cast<uint32_t>(block) * 32u * kVec + lane * kVec;
+    const bool valid = block < blocks && q < lanes;
+    int64_t n = 0;
+    int d = 0;
+    if (valid) sequence(q, n, d);
     const int count = !valid || left <= 0 ? 0 : (left < kSteps ? static_cast<int>(left) : kSteps);
-    steps.load(p, n, d, t0, count);
-    if (W > 1) {
-      const int buf = static_cast<int>(tile & 1);
-      Span f[kVec];
-      steps.span(count, f);
+    uint32_t resets = 0u;
+    if (kReset) resets = one ? __ballot_sync(0xFFFFFFFFu, flags != 0u) : flags;
+    if (cur.tile == 0) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) s_span[buf][warp][lane * kVec + i] = f[i];
+      for (int i = 0; i < kVec; ++i)
+        x[i] = D::first(p) != nullptr
+                   ? __uint_as_float(words(stage)[kWords + lane * kVec + i])
+                   : 0.f;
+    } else if (kChain && cur.tile == c.first_tile) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = chain.carry[block * kChainLanes + lane * kVec + i];
+    }
+    D dir;
+    dir.template read<kReset>(p, in, resets, count);
+    if (W > 1) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        s_span[stage][warp][lane * kVec + i] = dir.template span<kReset>(i);
       __syncthreads();
-      if (kTicket) {
+      if (kChain) {
         if (warp == 0) {
           Span all[kVec];
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
             all[i] = {1.f, 0.f};
-            for (int k = 0; k < W; ++k) all[i] = then(all[i], s_span[buf][k][lane * kVec + i]);
+            for (int k = 0; k < W; ++k) all[i] = then(all[i], s_span[stage][k][lane * kVec + i]);
           }
-          chain_step<kVec>(chain, static_cast<int>(tile - c.first_tile),
+          chain_step<kVec>(chain, static_cast<int>(cur.tile - c.first_tile),
                            static_cast<int>(block) * c.launch_tiles, lane, all, x, c.status,
                            c.timeout_ns);
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
             s_x[lane * kVec + i] = x[i];
-            if (tile + 1 == c.first_tile + c.launch_tiles)
+            if (cur.tile + 1 == c.first_tile + c.launch_tiles)
               chain.carry[block * kChainLanes + lane * kVec + i] = apply(all[i], x[i]);
           }
         }
@@ -431,71 +584,129 @@ __global__ void __launch_bounds__(kScanWarps * 32, 2)
         mine[i] = x[i];
         for (int k = 0; k < W; ++k) {
           if (k == order) mine[i] = x[i];
-          x[i] = apply(s_span[buf][group * W + k][lane * kVec + i], x[i]);
+          x[i] = apply(s_span[stage][group * W + k][lane * kVec + i], x[i]);
         }
       }
-      steps.run(p, n, d, t0, count, mine);
+      if (count == kSteps)
+        dir.template run<kReset, true>(p, in, resets, n, d, t0, count, mine);
+      else
+        dir.template run<kReset, false>(p, in, resets, n, d, t0, count, mine);
+    } else if (count == kSteps) {
+      dir.template run<kReset, true>(p, in, resets, n, d, t0, count, x);
     } else {
-      steps.run(p, n, d, t0, count, x);
+      dir.template run<kReset, false>(p, in, resets, n, d, t0, count, x);
     }
+    __syncwarp();  // this warp's steps are read before the next copies land on them
+    cur = nxt;
+    if (kChain)
+      nxt = chain_unit(blockIdx.x + (turn + 2) * gridDim.x);
+    else if (nxt.block >= 0)
+      nxt = after(nxt);
+    flags = next_flags;
   }
-  if (kTicket) chain_leave(chain, &s_ticket);
+  if (kChain) chain_leave(chain, chained);
 }
 
-template <template <typename, int> class Dir, typename T, int kVec>
+template <template <typename, int> class Dir, typename T, int kVec, bool kChain, bool kReset>
+cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& c, int W,
+                        int64_t blocks, int64_t units, cudaStream_t stream) {
+  using D = Dir<T, kVec>;
+  const auto fn = scan_kernel<Dir, T, kVec, kChain, kReset>;
+  constexpr int kSmem = kStages * D::kWarps * (D::kStreams * kSteps * 32 + 32 * kVec) * 4;
+  static const cudaError_t once =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (once != cudaSuccess) return once;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, 2 * c.num_sms));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(D::kWarps * 32);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kChain ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, W, static_cast<int>(blocks), c);
+  if (e == cudaSuccess) *c.launches += 1;
+  return e;
+}
+
+template <template <typename, int> class Dir, typename T, int kVec, bool kReset>
 cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStream_t stream) {
+  constexpr int kWarps = Dir<T, kVec>::kWarps;
   const int64_t lanes = (a.N * a.D + kVec - 1) / kVec, blocks = (lanes + 31) / 32;
   int W = 1;
-  while (W < kScanWarps && W * kSteps < a.L) W *= 2;
+  while (W < kWarps && W * kSteps < a.L) W *= 2;
   const int64_t tiles = (a.L + W * kSteps - 1) / (W * kSteps);
   // Two CTAs fit an SM.  Where walking would leave SMs without and there are tiles to give
-  // away, they go by tickets, as many to a launch as there are records (no record is used
-  // twice in a launch, so a slow reader finds what it was told of).
+  // away, they are chained, as many to a launch as there are records (no record is used twice
+  // in a launch, so a slow reader finds what it was told of).
   const int64_t most = kChainSlots / std::max<int64_t>(blocks, 1);
-  if (W == kScanWarps && blocks < std::min(2 * c.num_sms, kChainBlocks) && tiles > 1) {
+  if (W == kWarps && blocks < std::min(2 * c.num_sms, kChainBlocks) && tiles > 1) {
     for (int64_t t = 0; t < tiles; t += most) {
       c.first_tile = t;
       c.launch_tiles = static_cast<int>(std::min(most, tiles - t));
-      scan_kernel<Dir, T, kVec, true>
-          <<<static_cast<unsigned>(c.launch_tiles * blocks), kScanWarps * 32, 0, stream>>>(
-              a, W, static_cast<int>(blocks), c);
-      *c.launches += 1;
-      const cudaError_t e = cudaGetLastError();
+      const cudaError_t e = scan_launch<Dir, T, kVec, true, kReset>(
+          a, c, W, blocks, c.launch_tiles * blocks, stream);
       if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
   }
-  const int64_t groups = kScanWarps / W;
-  scan_kernel<Dir, T, kVec, false>
-      <<<static_cast<unsigned>((blocks + groups - 1) / groups), kScanWarps * 32, 0, stream>>>(
-          a, W, static_cast<int>(blocks), c);
-  *c.launches += 1;
-  return cudaGetLastError();
+  const int64_t groups = kWarps / W;
+  return scan_launch<Dir, T, kVec, false, kReset>(a, c, W, blocks, (blocks + groups - 1) / groups,
+                                                  stream);
 }
 
-bool even(int64_t x) { return (x & 1) == 0; }
-bool word_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+template <template <typename, int> class Dir, typename T, int kVec>
+cudaError_t scan_any(const typename Dir<T, kVec>::Args& a, const ScanLaunch& c,
+                     cudaStream_t stream) {
+  return a.reset != nullptr ? scan_as<Dir, T, kVec, true>(a, c, stream)
+                            : scan_as<Dir, T, kVec, false>(a, c, stream);
+}
+
+// Whether every row of these tensors starts on a multiple of `bytes`.
+struct Rows {
+  const void* p;
+  int64_t ld;
+};
+bool aligned(std::initializer_list<Rows> all, int D, size_t size, size_t bytes) {
+  if (D * size % bytes != 0) return false;
+  for (const Rows& r : all)
+    if (r.p != nullptr && (reinterpret_cast<uintptr_t>(r.p) % bytes != 0 ||
+                           static_cast<size_t>(r.ld) * size % bytes != 0))
+      return false;
+  return true;
+}
 
 }  // namespace
 
-cudaError_t launch_rnn_scan(const RnnScanArgs& a, const ScanLaunch& c, cudaStream_t stream) {
-  if (a.dtype == DSPARK_F32) return scan_as<Forward, float, 1>(a, c, stream);
+cudaError_t launch_rnn_scan(const RnnScanArgs& a, const ScanLaunch& launch, cudaStream_t stream) {
+  const size_t size = a.dtype == DSPARK_F32 ? 4 : 2;
+  const std::initializer_list<Rows> in = {{a.za, a.ld_za}, {a.zg, a.ld_zg}, {a.e, a.ld_e}};
+  ScanLaunch c = launch;
+  c.wide = aligned(in, a.D, size, 16);  // 16-byte copies, else 4-byte ones
+  if (a.dtype == DSPARK_F32) return scan_any<Forward, float, 1>(a, c, stream);
   // pairs of bf16 channels where every row starts on a 4-byte boundary
-  if (even(a.D) && even(a.ld_za) && even(a.ld_zg) && even(a.ld_e) && word_aligned(a.za) &&
-      word_aligned(a.zg) && word_aligned(a.e) && word_aligned(a.s))
-    return scan_as<Forward, uint16_t, 2>(a, c, stream);
-  return scan_as<Forward, uint16_t, 1>(a, c, stream);
+  if (aligned(in, a.D, size, 4) && aligned({{a.s, a.D}}, a.D, size, 4))
+    return scan_any<Forward, uint16_t, 2>(a, c, stream);
+  c.wide = false;
+  return scan_any<Forward, uint16_t, 1>(a, c, stream);
 }
 
-cudaError_t launch_rnn_scan_grad(const RnnScanGradArgs& a, const ScanLaunch& c,
+cudaError_t launch_rnn_scan_grad(const RnnScanGradArgs& a, const ScanLaunch& launch,
                                  cudaStream_t stream) {
-  if (a.dtype == DSPARK_F32) return scan_as<Backward, float, 1>(a, c, stream);
-  if (even(a.D) && even(a.ld_za) && even(a.ld_zg) && even(a.ld_e) && even(a.ld_dza) &&
-      even(a.ld_dzg) && word_aligned(a.za) && word_aligned(a.zg) && word_aligned(a.e) &&
-      word_aligned(a.s) && word_aligned(a.ds) && word_aligned(a.dza) && word_aligned(a.dzg) &&
-      word_aligned(a.de))
-    return scan_as<Backward, uint16_t, 2>(a, c, stream);
-  return scan_as<Backward, uint16_t, 1>(a, c, stream);
+  const size_t size = a.dtype == DSPARK_F32 ? 4 : 2;
+  const std::initializer_list<Rows> in = {
+      {a.za, a.ld_za}, {a.zg, a.ld_zg}, {a.e, a.ld_e}, {a.ds, a.D}, {a.s, a.D}};
+  ScanLaunch c = launch;
+  c.wide = aligned(in, a.D, size, 16);
+  if (a.dtype == DSPARK_F32) return scan_any<Backward, float, 1>(a, c, stream);
+  if (aligned(in, a.D, size, 4) &&
+      aligned({{a.dza, a.ld_dza}, {a.dzg, a.ld_dzg}, {a.de, a.D}}, a.D, size, 4))
+    return scan_any<Backward, uint16_t, 2>(a, c, stream);
+  c.wide = false;
+  return scan_any<Backward, uint16_t, 1>(a, c, stream);
 }
 
 }  // namespace dspark

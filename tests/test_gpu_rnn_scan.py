@@ -108,7 +108,7 @@ def test_more_tiles_than_one_launch_has_records_for(dsp, dtype, D):
     grad = binding.rnn_scan_grad(dsp, cuda(a["za"]), cuda(a["zg"]), cuda(a["e"]), out["s"], cuda(a["ds"]), s0=dev(a["s0"]),
                                  ds_last=dev(a["ds_last"]), reset=dev(a["reset"]))
     torch.cuda.synchronize()
-    assert dsp.last_launches == 2 and dsp.status() == 0
+    assert dsp.last_launches >= 2 and dsp.status() == 0
     at = [0, 77, 149]
     b = {k: None if v is None else v[at] for k, v in a.items()}
     s, err = tr.rnn_scan(f64(b["za"]), f64(b["zg"]), f64(b["e"]), b["s0"], b["reset"])
