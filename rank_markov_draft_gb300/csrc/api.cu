@@ -46,8 +46,7 @@ struct dspark_ctx {
   int32_t* d_l_prev = nullptr;           // [B_max * K_max] predecessors of the drafted tokens
   float* d_l_offq2 = nullptr;            // [B_max * K_max] log2 q offsets
   float* d_topk_part_v = nullptr;
-  // recurrence over long sequences: tile records, zero between calls
-  uint8_t* d_chain = nullptr;
+  dspark::ScanSpan* d_spans = nullptr;   // [kScanSpanCount] segments of long recurrences
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
   uint32_t epoch = 0;                    // last key epoch used
   int poisoned = 0;
@@ -138,8 +137,7 @@ size_t dtype_size(int dtype) {
 }
 
 dspark::ScanLaunch scan_launch(dspark_ctx* ctx) {
-  return {ctx->d_chain, ctx->num_sms, ctx->d_status, ctx->timeout_ns, &ctx->last_launches, 0, 0,
-          false};
+  return {ctx->d_spans, ctx->num_sms, &ctx->last_launches, 0, 0, 0, 0, false};
 }
 
 // The arguments that both directions of the RNN head's recurrence share.
@@ -490,14 +488,14 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
             cudaMalloc(&ctx->d_v_count, sizeof(int) * B_max) == cudaSuccess &&
             cudaMalloc(&ctx->d_l_prev, sizeof(int32_t) * rows) == cudaSuccess &&
             cudaMalloc(&ctx->d_l_offq2, sizeof(float) * rows) == cudaSuccess &&
-            cudaMalloc(&ctx->d_chain, dspark::kChainBytes) == cudaSuccess;
+            cudaMalloc(&ctx->d_spans, sizeof(dspark::ScanSpan) * dspark::kScanSpanCount) ==
+                cudaSuccess;
   ok = ok && cudaMemset(ctx->d_status, 0, sizeof(int)) == cudaSuccess &&
        cudaMemset(ctx->d_bar, 0, sizeof(uint32_t)) == cudaSuccess &&
        cudaMemset(ctx->d_keys, 0, sizeof(unsigned long long) * K_max * dspark::kBatchChunk) ==
            cudaSuccess &&
        cudaMemset(ctx->d_v_fail, 0, sizeof(unsigned long long) * B_max) == cudaSuccess &&
        cudaMemset(ctx->d_v_count, 0, sizeof(int) * B_max) == cudaSuccess &&
-       cudaMemset(ctx->d_chain, 0, dspark::kChainBytes) == cudaSuccess &&
        cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
     dspark_ctx_destroy(ctx);
@@ -529,7 +527,7 @@ int dspark_ctx_destroy(dspark_ctx* ctx) {
   cudaFree(ctx->d_l_prev);
   cudaFree(ctx->d_l_offq2);
   cudaFree(ctx->d_topk_part_v);
-  cudaFree(ctx->d_chain);
+  cudaFree(ctx->d_spans);
   delete ctx;
   return DSPARK_OK;
 }
@@ -545,8 +543,7 @@ int dspark_ctx_reset(dspark_ctx* ctx, dspark_stream_t stream) {
                             s) == cudaSuccess &&
             cudaMemsetAsync(ctx->d_v_fail, 0, sizeof(unsigned long long) * ctx->B_max, s) ==
                 cudaSuccess &&
-            cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess &&
-            cudaMemsetAsync(ctx->d_chain, 0, dspark::kChainBytes, s) == cudaSuccess;
+            cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess;
   if (!ok) return DSPARK_ERR_CUDA;
   ctx->bar_counter = 0;
   ctx->epoch = 0;

@@ -287,21 +287,23 @@ struct RnnScanGradArgs {
   void *dza, *dzg, *de;
   float* ds0;                // [N, D] or null
 };
-// Scratch of sequences split over CTAs: kChainSlots records of a tile's span (8 bytes) and end
-// value (4 bytes) for kChainLanes channels, the values that pass from launch to launch, and a
-// flag a record and a counter, zero between launches.
-constexpr int kChainSlots = 8192, kChainLanes = 64, kChainBlocks = 512;
-constexpr size_t kChainBytes = static_cast<size_t>(kChainSlots) * (kChainLanes * 12 + 4) +
-                               kChainBlocks * kChainLanes * 4 + 8;
+// A span of steps acts on the value before it as x -> A x + S.
+struct ScanSpan {
+  float A, S;
+};
+// Scratch of sequences cut into segments: for each CTA (of at most kScanCtas) its span and the
+// spans before each of its (at most 8) warps, of 64 channels each.
+constexpr int kScanCtas = 1024;
+constexpr size_t kScanSpanCount = static_cast<size_t>(kScanCtas) * 9 * 64;
 struct ScanLaunch {
-  void* chain;
+  ScanSpan* spans;
   int num_sms;
-  int* status;
-  uint64_t timeout_ns;
-  int* launches;       // host: kernels launched (added to)
-  int64_t first_tile;  // set by the launch
-  int launch_tiles;
-  bool wide;
+  int* launches;  // host: kernels launched (added to)
+  // set by the launch
+  int64_t blocks;  // of 32 lanes
+  int W;           // warps that walk a block together
+  int segs, seg;   // segments a block, and their length in units of 16 steps
+  bool wide;       // rows start on 16-byte boundaries
 };
 cudaError_t launch_rnn_scan(const RnnScanArgs& a, const ScanLaunch& c, cudaStream_t stream);
 cudaError_t launch_rnn_scan_grad(const RnnScanGradArgs& a, const ScanLaunch& c,

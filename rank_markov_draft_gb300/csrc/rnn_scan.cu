@@ -16,17 +16,17 @@
 // works on 16 steps of 32 lanes at a time (a lane is 4 bytes of channels: two bf16 or one fp32;
 // lanes run over sequences and channels alike, so no channel count leaves lanes empty).  The
 // steps arrive in shared memory by asynchronous copies, the next unit's while this one is
-// worked on, so loads are in flight all the time; a warp reduces its steps to (A, S), learns
-// the value before them from the warps before it, and runs them from there.  Three ways:
+// worked on, so loads are in flight all the time; a warp that does not start a sequence learns
+// the value before its steps from the spans before them.  Three ways:
 //   L <= 16:         there is nothing before them but s0.
 //   many lanes:      a CTA's warps hold consecutive spans, exchange (A, S) through shared
 //                    memory and walk over the sequence; the value after a tile stays with them.
-//   few lanes, long: the walk alone would leave most SMs empty, so the tiles of a sequence go
-//                    around the CTAs of a cooperative launch (all of them run).  A tile publishes
-//                    its (A, S) as soon as it has them and its end value once that is known; a
-//                    tile folds the (A, S) after the nearest known end value, strictly in order,
-//                    so the result does not depend on which one that was.
-// Every input is read once and every output written once in all three.
+//   few lanes, long: the walk alone would leave most SMs empty, so every sequence is cut into
+//                    segments, one a warp.  One launch finds the segments' spans (forward from
+//                    three, backward from two streams), walking each from its end, so that the
+//                    steps the second launch starts with are the ones still in L2; the second
+//                    folds the spans before its segment and walks it.
+// The first two read every input once.
 
 #include <algorithm>
 #include <cstdint>
@@ -92,119 +92,15 @@ __device__ __forceinline__ void copy_4(void* dst, const void* src, bool on) {
                : "memory");
 }
 
-// A span's effect x -> A x + S.  kDrops in A: a decay of exactly zero inside, so x is dropped
-// (a product that has merely underflowed keeps an infinity or NaN).
+// Spans.  kDrops in A: a reset inside, so the value before is dropped (a product that has merely
+// underflowed keeps an infinity or NaN).
 constexpr float kDrops = -1.f;
-struct Span {
-  float A, S;
-};
+using Span = ScanSpan;
 __device__ __forceinline__ float apply(Span f, float x) {
   return f.A == kDrops ? f.S : fmaf(f.A, x, f.S);
 }
 __device__ __forceinline__ Span then(Span f, Span g) {  // f first
   return {f.A == kDrops || g.A == kDrops ? kDrops : f.A * g.A, apply(g, f.S)};
-}
-
-// ---- the chained tiles' records (context scratch; flags and counter zero between launches)
-struct ChainView {
-  Span* span;       // [slots][kChainLanes]
-  float* end;       // [slots][kChainLanes]
-  float* carry;     // [kChainBlocks][kChainLanes] the value after the launch before
-  uint32_t* flag;   // [slots] 1: span known, 2: end known
-  uint32_t* done;   // CTAs
-};
-__device__ __forceinline__ ChainView chain_view(void* scratch) {
-  ChainView v;
-  v.span = static_cast<Span*>(scratch);
-  v.end = reinterpret_cast<float*>(v.span + kChainSlots * kChainLanes);
-  v.carry = v.end + kChainSlots * kChainLanes;
-  v.flag = reinterpret_cast<uint32_t*>(v.carry + kChainBlocks * kChainLanes);
-  v.done = v.flag + kChainSlots;
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-  uint32_t r;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
-  return r;
-}
-__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// One warp, tile `tile` of its chain, whose records start at slot `first`: publish the span,
-// find the value before the tile, publish the value after it.  x: the value before tile 0 on
-// entry, before this tile on return.
-template <int kVec>
-__device__ __forceinline__ void chain_step(const ChainView& v, int tile, int first, int lane,
-                                           const Span (&span)[kVec], float (&x)[kVec], int* status,
-                                           uint64_t timeout_ns) {
-  const auto at = [&](int t, int i) {
-    return static_cast<size_t>(first + t) * kChainLanes + lane * kVec + i;
-  };
-  uint32_t* flag = v.flag + first;
-  if (tile > 0) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) v.span[at(tile, i)] = span[i];
-    __syncwarp();
-    if (lane == 0) {
-      __threadfence();
-      st_release(flag + tile, 1u);
-    }
-    // the nearest earlier tile whose end is known, the spans of all after it being known too
-    int from = -1;
-    uint64_t deadline = 0;
-    for (uint32_t spins = 0; from < 0; ++spins) {
-      const int t = tile - 1 - lane;
-      const uint32_t state = t >= 0 ? ld_acquire(flag + t) : 0u;
-      const uint32_t ends = __ballot_sync(0xFFFFFFFFu, state == 2u);
-      const uint32_t unknown = __ballot_sync(0xFFFFFFFFu, state == 0u);
-      if (ends != 0u && (unknown & ((ends & (0u - ends)) - 1u)) == 0u) {
-        from = tile - __ffs(ends);
-      } else if (spins > 16u) {
-        const uint64_t now = globaltimer_ns();
-        if (deadline == 0) {
-          deadline = now + timeout_ns;
-        } else if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(now > deadline), 0)) {
-          if (lane == 0) record_error(status, kStatusTimeout);
-          break;
-        }
-      }
-    }
-    __syncwarp();
-    __threadfence();
-    if (from >= 0) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = __ldcg(v.end + at(from, i));
-#pragma unroll 8
-      for (int t = from + 1; t < tile; ++t)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(v.span + at(t, i)));
-          x[i] = apply(Span{f.x, f.y}, x[i]);
-        }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) v.end[at(tile, i)] = apply(span[i], x[i]);
-  __syncwarp();
-  if (lane == 0) {
-    __threadfence();
-    st_release(flag + tile, 2u);
-  }
-}
-
-// The last CTA of the launch to finish leaves flags and counter as it found them.
-__device__ __forceinline__ void chain_leave(const ChainView& v, int tiles) {
-  __shared__ uint32_t s_last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = atomicAdd(v.done, 1u) == gridDim.x - 1 ? 1u : 0u;
-  }
-  __syncthreads();
-  if (s_last == 0u) return;
-  for (int i = threadIdx.x; i < tiles; i += blockDim.x) v.flag[i] = 0u;
-  if (threadIdx.x == 0) *v.done = 0u;
 }
 
 // ---- the two directions: their streams, their step's (a, b), and what a step writes
@@ -223,6 +119,7 @@ struct Forward {
     return i == 0 ? Stream{p.za, p.ld_za, 0} : i == 1 ? Stream{p.zg, p.ld_zg, 0}
                                                       : Stream{p.e, p.ld_e, 0};
   }
+  static constexpr __device__ bool in_span(int) { return true; }  // a stream that spans need
   static __device__ __forceinline__ const float* first(const Args& p) { return p.s0; }
 
   // words: [stream][step][lane] of this warp, at this lane.  a < 0: a reset.
@@ -303,6 +200,7 @@ struct Backward {
            : i == 3 ? Stream{p.ds, p.D, 0}
                     : Stream{p.s, p.D, 1};
   }
+  static constexpr __device__ bool in_span(int i) { return i == 0 || i == 3; }
   static __device__ __forceinline__ const float* first(const Args& p) { return p.ds_last; }
 
   const uint32_t* w;
@@ -378,50 +276,64 @@ struct Backward {
   }
 };
 
-// A unit of work of a CTA: spans of W warps, of one lane block a group of W warps.
-struct Unit {
-  int64_t block, tile;  // of the CTA's first group; block < 0: none
-};
+// What a launch does with the sequences (see above).
+enum class Mode { kWalk, kSpans, kSegments };
 
-// Walks: units (block, 0), (block, 1), ... of every gridDim.x-th CTA's worth of blocks, so a CTA
-// carries the value from unit to unit.  Chains: unit i is tile i / blocks of block i % blocks and
-// goes to CTA i % gridDim.x; CTAs take their units in order, so the first unfinished tile is
-// always being worked on.
-template <template <typename, int> class Dir, typename T, int kVec, bool kChain, bool kReset>
+// A unit of work of a warp: 16 steps at place `pos` (in units of 16, in the recurrence's order)
+// of a lane block; block < 0: none.  Walks: a CTA's kWarps / W groups of W warps take every
+// gridDim.x-th kWarps / W blocks, W places at a time.  Segments: the CTA's warps are consecutive
+// segments of c.seg places of one block.
+template <template <typename, int> class Dir, typename T, int kVec, Mode kMode, bool kReset>
 __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
-    scan_kernel(const typename Dir<T, kVec>::Args p, const int W, const int blocks,
-                const ScanLaunch c) {
+    scan_kernel(const typename Dir<T, kVec>::Args p, const ScanLaunch c) {
   using D = Dir<T, kVec>;
   constexpr int kWarps = D::kWarps, kWords = D::kStreams * kSteps * 32;
-  extern __shared__ uint4 s_raw[];  // [kStages][kWarps] x (kWords words, 32 kVec floats)
-  __shared__ Span s_span[2][kWarps][32 * kVec];
-  __shared__ float s_x[32 * kVec];
   constexpr int kWarpWords = kWords + 32 * kVec;
+  constexpr bool kWalk = kMode == Mode::kWalk;
+  extern __shared__ uint4 s_raw[];  // [kStages][kWarps] x (kWords words, 32 kVec floats)
+  __shared__ Span s_span[kStages][kWarps][32 * kVec];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tiles = (p.L + W * kSteps - 1) / (W * kSteps);
-  const int groups = kWarps / W, group = warp / W;
-  // `order`: this warp's place in the recurrence's order, `w` in the order of time
-  const int order = warp % W, w = D::kReverse ? W - 1 - order : order;
+  const int W = kWalk ? c.W : 1, groups = kWarps / W, group = warp / W, order = warp % W;
+  const int64_t places = (p.L + kSteps - 1) / kSteps;
   const uint32_t lanes = static_cast<uint32_t>(p.N * p.D);  // channels of all sequences
   const auto words = [&](int stage) {
     return reinterpret_cast<uint32_t*>(s_raw) + (stage * kWarps + warp) * kWarpWords;
   };
-  const ChainView chain = kChain ? chain_view(c.chain) : ChainView{};
-  const int chained = kChain ? blocks * c.launch_tiles : 0;  // units
-  const auto chain_unit = [&](int i) {
-    return i < chained ? Unit{i % blocks, c.first_tile + i / blocks} : Unit{-1, 0};
+  // units: (block, pos), pos in steps of W (walk), up or (spans) down to `pos_end`
+  struct Unit {
+    int64_t block, pos;
   };
-  const auto after = [&](Unit u) {  // (walks)
-    if (++u.tile == tiles) {
-      u.tile = 0;
-      u.block += static_cast<int64_t>(gridDim.x) * groups;
-      if (u.block >= blocks) u.block = -1;
+  int64_t pos_begin = order, pos_end = 0;
+  Unit cur;
+  if (kWalk) {
+    cur = Unit{static_cast<int64_t>(blockIdx.x) * groups + group, pos_begin};
+    pos_end = (places + W - 1) / W * W + order;  // every warp of a group does every turn
+    if (cur.block - group >= c.blocks) cur.block = -1;
+  } else {
+    const int per = c.segs / kWarps;  // CTAs a block
+    const int64_t seg = static_cast<int64_t>(blockIdx.x % per) * kWarps + warp;
+    pos_begin = seg * c.seg;
+    pos_end = pos_begin + c.seg < places ? pos_begin + c.seg : places;
+    cur = Unit{blockIdx.x / per, kMode == Mode::kSpans ? pos_end - 1 : pos_begin};
+    if (pos_begin >= places) cur.block = -1;
+  }
+  const auto after = [&](Unit u) {
+    if (u.block < 0) return u;
+    if (kWalk) {
+      u.pos += W;
+      if (u.pos >= pos_end) {
+        u.pos = pos_begin;
+        u.block += static_cast<int64_t>(gridDim.x) * groups;
+        if (u.block - group >= c.blocks) u.block = -1;
+      }
+    } else {
+      u.pos += kMode == Mode::kSpans ? -1 : 1;
+      if (u.pos < pos_begin || u.pos >= pos_end) u.block = -1;
     }
     return u;
   };
-  // first step of this warp's span in a unit
-  const auto start = [&](const Unit& u) {
-    return ((D::kReverse ? tiles - 1 - u.tile : u.tile) * W + w) * kSteps;
+  const auto start = [&](const Unit& u) {  // first step
+    return (D::kReverse ? places - 1 - u.pos : u.pos) * kSteps;
   };
   const auto sequence = [&](uint32_t q, int64_t& n, int& d) {
     const uint32_t s = q / static_cast<uint32_t>(p.D);
@@ -433,13 +345,13 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
 
   // Start copying a unit's steps (and its flags, into a register).
   const auto fetch = [&](const Unit& u, int stage, uint32_t& flags) {
+    const int64_t t0 = start(u);
     if (u.block < 0) {
       cp_async_commit();
       return;
     }
     uint32_t* dst = words(stage);
-    const int64_t t0 = start(u);
-    const uint32_t q0 = static_cast<uint32_t>(u.block + group) * 32u * kVec;
+    const uint32_t q0 = static_cast<uint32_t>(u.block) * 32u * kVec;
     if (c.wide) {  // 16-byte pieces: this lane's are 4 steps apart, in one sequence
       constexpr int kPiece = 16 / sizeof(T);
       const uint32_t q = q0 + (lane & 7) * kPiece;
@@ -450,13 +362,13 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
 #pragma unroll
       for (int i = 0; i < D::kStreams; ++i) {
         const Stream st = D::stream(p, i);
-        if (st.p == nullptr) continue;
+        if (st.p == nullptr || (kMode == Mode::kSpans && !D::in_span(i))) continue;
         const int64_t row = n * p.L + t0 - st.shift + (lane >> 3);
         const T* src = static_cast<const T*>(st.p) + row * st.ld + d;
 #pragma unroll
         for (int j = 0; j < kSteps; j += 4) {
           const int64_t t = t0 + j + (lane >> 3);
-          const bool on = in && t < p.L && (st.shift == 0 || t > 0);
+          const bool on = in && t0 >= 0 && t < p.L && (st.shift == 0 || t > 0);
           copy_16(dst + (i * kSteps + j + (lane >> 3)) * 32 + (lane & 7) * 4,
                   on ? src + j * st.ld : static_cast<const T*>(st.p), on);
         }
@@ -471,12 +383,12 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
 #pragma unroll
       for (int i = 0; i < D::kStreams; ++i) {
         const Stream st = D::stream(p, i);
-        if (st.p == nullptr) continue;
+        if (st.p == nullptr || (kMode == Mode::kSpans && !D::in_span(i))) continue;
         const T* src = static_cast<const T*>(st.p) + (n * p.L + t0 - st.shift) * st.ld + d;
         if (sizeof(T) * kVec == 4) {
 #pragma unroll 4
           for (int j = 0; j < kSteps; ++j) {
-            const bool on = in && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
+            const bool on = in && t0 >= 0 && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
             copy_4(dst + (i * kSteps + j) * 32 + lane,
                    on ? src + j * st.ld : static_cast<const T*>(st.p), on);
           }
@@ -484,7 +396,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
           uint32_t v[kSteps];
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) {
-            const bool on = in && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
+            const bool on = in && t0 >= 0 && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
             v[j] = on ? static_cast<uint32_t>(__ldcs(src + j * st.ld)) : 0u;
           }
 #pragma unroll
@@ -492,7 +404,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
         }
       }
     }
-    if (u.tile == 0 && D::first(p) != nullptr)
+    if (kWalk && u.pos == pos_begin && D::first(p) != nullptr)
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
         copy_4(dst + kWords + lane * kVec + i, D::first(p) + (in ? q + i : 0), in);
@@ -501,28 +413,54 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
       const uint8_t* src = p.reset + n * p.L + t0;
       flags = 0u;
       if (one) {
-        if (in && lane < kSteps && t0 + lane < p.L) flags = __ldg(src + lane);
-      } else if (in) {
+        if (in && lane < kSteps && t0 >= 0 && t0 + lane < p.L) flags = __ldg(src + lane);
+      } else if (in && t0 >= 0) {
         for (int j = 0; j < kSteps && t0 + j < p.L; ++j)
           flags |= static_cast<uint32_t>(__ldg(src + j) != 0) << j;
       }
     }
   };
 
-  Unit cur, nxt;
-  if (kChain) {
-    cur = chain_unit(blockIdx.x);
-    nxt = chain_unit(blockIdx.x + gridDim.x);
-  } else {
-    cur = Unit{static_cast<int64_t>(blockIdx.x) * groups, 0};
-    if (cur.block >= blocks) cur.block = -1;
-    nxt = cur.block < 0 ? cur : after(cur);
-  }
   uint32_t flags = 0u, next_flags = 0u;
   fetch(cur, 0, flags);
   float x[kVec];
+  Span acc[kVec];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) x[i] = 0.f;
+  for (int i = 0; i < kVec; ++i) {
+    x[i] = 0.f;
+    acc[i] = {1.f, 0.f};
+  }
+  const size_t channel0 = static_cast<size_t>(lane) * kVec;
+  if (kMode == Mode::kSegments) {
+    // the value before the segment: through the spans of the CTAs before this one and of the
+    // warps before this one (the first of them drops what is before it for the sequence's first
+    // value, which another CTA may by now have overwritten with the last)
+    const int per = c.segs / kWarps, mine = blockIdx.x % per;
+    const Span* sums = c.spans + (static_cast<size_t>(blockIdx.x) - mine) * (kWarps + 1) * 64;
+    constexpr int kBatch = 16 / kVec;  // spans in flight
+    for (int k0 = 0; k0 < mine; k0 += kBatch) {
+      float2 f[kBatch][kVec];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          if (k0 + k < mine)
+            f[k][i] = __ldcg(reinterpret_cast<const float2*>(
+                sums + static_cast<size_t>(k0 + k) * (kWarps + 1) * 64 + channel0 + i));
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          if (k0 + k < mine) x[i] = apply(Span{f[k][i].x, f[k][i].y}, x[i]);
+    }
+    const Span* own = c.spans + (static_cast<size_t>(blockIdx.x) * (kWarps + 1) + 1 + warp) * 64;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float2 f = __ldcg(reinterpret_cast<const float2*>(own + channel0 + i));
+      x[i] = apply(Span{f.x, f.y}, x[i]);
+    }
+  }
+  Unit nxt = after(cur);
   for (int turn = 0; cur.block >= 0; ++turn) {
     const int stage = turn & 1;
     fetch(nxt, stage ^ 1, next_flags);
@@ -530,132 +468,111 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     __syncwarp();
     const uint32_t* in = words(stage) + lane;
     const int64_t t0 = start(cur), left = p.L - t0;
-    const int64_t block = cur.block + group;
-    const uint32_t q = static_cast<uint32_t>(block) * 32u * kVec + lane * kVec;
-    const bool valid = block < blocks && q < lanes;
+    const uint32_t q = static_cast<uint32_t>(cur.block) * 32u * kVec + lane * kVec;
+    const bool valid = q < lanes && t0 >= 0;
     int64_t n = 0;
     int d = 0;
     if (valid) sequence(q, n, d);
     const int count = !valid || left <= 0 ? 0 : (left < kSteps ? static_cast<int>(left) : kSteps);
     uint32_t resets = 0u;
     if (kReset) resets = one ? __ballot_sync(0xFFFFFFFFu, flags != 0u) : flags;
-    if (cur.tile == 0) {
+    if (kWalk && cur.pos == pos_begin) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
         x[i] = D::first(p) != nullptr
                    ? __uint_as_float(words(stage)[kWords + lane * kVec + i])
                    : 0.f;
-    } else if (kChain && cur.tile == c.first_tile) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = chain.carry[block * kChainLanes + lane * kVec + i];
     }
     D dir;
     dir.template read<kReset>(p, in, resets, count);
-    if (W > 1) {
+    if (kMode == Mode::kSpans) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        s_span[stage][warp][lane * kVec + i] = dir.template span<kReset>(i);
-      __syncthreads();
-      if (kChain) {
-        if (warp == 0) {
-          Span all[kVec];
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            all[i] = {1.f, 0.f};
-            for (int k = 0; k < W; ++k) all[i] = then(all[i], s_span[stage][k][lane * kVec + i]);
-          }
-          chain_step<kVec>(chain, static_cast<int>(cur.tile - c.first_tile),
-                           static_cast<int>(block) * c.launch_tiles, lane, all, x, c.status,
-                           c.timeout_ns);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            s_x[lane * kVec + i] = x[i];
-            if (cur.tile + 1 == c.first_tile + c.launch_tiles)
-              chain.carry[block * kChainLanes + lane * kVec + i] = apply(all[i], x[i]);
-          }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) x[i] = s_x[lane * kVec + i];
-      }
+      for (int i = 0; i < kVec; ++i) acc[i] = then(dir.template span<kReset>(i), acc[i]);
+    } else {
       float mine[kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        mine[i] = x[i];
-        for (int k = 0; k < W; ++k) {
-          if (k == order) mine[i] = x[i];
-          x[i] = apply(s_span[stage][group * W + k][lane * kVec + i], x[i]);
-        }
+      for (int i = 0; i < kVec; ++i) mine[i] = x[i];
+      if (W > 1) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          s_span[stage][warp][lane * kVec + i] = dir.template span<kReset>(i);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          for (int k = 0; k < W; ++k) {
+            if (k == order) mine[i] = x[i];
+            x[i] = apply(s_span[stage][group * W + k][lane * kVec + i], x[i]);
+          }
       }
       if (count == kSteps)
         dir.template run<kReset, true>(p, in, resets, n, d, t0, count, mine);
       else
         dir.template run<kReset, false>(p, in, resets, n, d, t0, count, mine);
-    } else if (count == kSteps) {
-      dir.template run<kReset, true>(p, in, resets, n, d, t0, count, x);
-    } else {
-      dir.template run<kReset, false>(p, in, resets, n, d, t0, count, x);
+      if (W == 1)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[i] = mine[i];
     }
     __syncwarp();  // this warp's steps are read before the next copies land on them
     cur = nxt;
-    if (kChain)
-      nxt = chain_unit(blockIdx.x + (turn + 2) * gridDim.x);
-    else if (nxt.block >= 0)
-      nxt = after(nxt);
+    nxt = after(nxt);
     flags = next_flags;
   }
-  if (kChain) chain_leave(chain, chained);
+  if (kMode == Mode::kSpans) {
+    // this CTA's span, and before each warp's segment the span of the warps before it
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) s_span[0][warp][channel0 + i] = acc[i];
+    __syncthreads();
+    Span* out = c.spans + static_cast<size_t>(blockIdx.x) * (kWarps + 1) * 64;
+    const int per = c.segs / kWarps;
+    const uint32_t q = (blockIdx.x / per * 32u + lane) * kVec;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      Span f{1.f, 0.f};
+      if (blockIdx.x % per == 0)
+        f = {kDrops, q < lanes && D::first(p) != nullptr ? D::first(p)[q + i] : 0.f};
+      for (int k = 0; k < warp; ++k) f = then(f, s_span[0][k][channel0 + i]);
+      out[(1 + warp) * 64 + channel0 + i] = f;
+      if (warp == kWarps - 1) out[channel0 + i] = then(f, acc[i]);
+    }
+  }
 }
 
-template <template <typename, int> class Dir, typename T, int kVec, bool kChain, bool kReset>
-cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& c, int W,
-                        int64_t blocks, int64_t units, cudaStream_t stream) {
+template <template <typename, int> class Dir, typename T, int kVec, Mode kMode, bool kReset>
+cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& c, int64_t grid,
+                        cudaStream_t stream) {
   using D = Dir<T, kVec>;
-  const auto fn = scan_kernel<Dir, T, kVec, kChain, kReset>;
+  const auto fn = scan_kernel<Dir, T, kVec, kMode, kReset>;
   constexpr int kSmem = kStages * D::kWarps * (D::kStreams * kSteps * 32 + 32 * kVec) * 4;
   static const cudaError_t once =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (once != cudaSuccess) return once;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, 2 * c.num_sms));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(D::kWarps * 32);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kChain ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, W, static_cast<int>(blocks), c);
-  if (e == cudaSuccess) *c.launches += 1;
-  return e;
+  fn<<<static_cast<unsigned>(grid), D::kWarps * 32, kSmem, stream>>>(a, c);
+  *c.launches += 1;
+  return cudaGetLastError();
 }
 
 template <template <typename, int> class Dir, typename T, int kVec, bool kReset>
 cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStream_t stream) {
   constexpr int kWarps = Dir<T, kVec>::kWarps;
-  const int64_t lanes = (a.N * a.D + kVec - 1) / kVec, blocks = (lanes + 31) / 32;
-  int W = 1;
-  while (W < kWarps && W * kSteps < a.L) W *= 2;
-  const int64_t tiles = (a.L + W * kSteps - 1) / (W * kSteps);
-  // Two CTAs fit an SM.  Where walking would leave SMs without and there are tiles to give
-  // away, they are chained, as many to a launch as there are records (no record is used twice
-  // in a launch, so a slow reader finds what it was told of).
-  const int64_t most = kChainSlots / std::max<int64_t>(blocks, 1);
-  if (W == kWarps && blocks < std::min(2 * c.num_sms, kChainBlocks) && tiles > 1) {
-    for (int64_t t = 0; t < tiles; t += most) {
-      c.first_tile = t;
-      c.launch_tiles = static_cast<int>(std::min(most, tiles - t));
-      const cudaError_t e = scan_launch<Dir, T, kVec, true, kReset>(
-          a, c, W, blocks, c.launch_tiles * blocks, stream);
-      if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+  const int64_t lanes = (a.N * a.D + kVec - 1) / kVec, places = (a.L + kSteps - 1) / kSteps;
+  const int64_t room = 2 * c.num_sms;  // two CTAs fit an SM
+  c.blocks = (lanes + 31) / 32;
+  c.W = 1;
+  while (c.W < kWarps && c.W < places) c.W *= 2;
+  // Segments where walking would leave SMs without a CTA and sequences are long enough to cut.
+  if (2 * c.blocks <= room && places >= 4 * kWarps) {
+    int64_t per = std::min<int64_t>(room / c.blocks, kScanCtas / c.blocks);  // CTAs a block
+    per = std::min(per, places / (2 * kWarps));
+    c.segs = static_cast<int>(per * kWarps);
+    c.seg = static_cast<int>((places + c.segs - 1) / c.segs);
+    const cudaError_t e =
+        scan_launch<Dir, T, kVec, Mode::kSpans, kReset>(a, c, c.blocks * per, stream);
+    if (e != cudaSuccess) return e;
+    return scan_launch<Dir, T, kVec, Mode::kSegments, kReset>(a, c, c.blocks * per, stream);
   }
-  const int64_t groups = kWarps / W;
-  return scan_launch<Dir, T, kVec, false, kReset>(a, c, W, blocks, (blocks + groups - 1) / groups,
-                                                  stream);
+  const int64_t groups = kWarps / c.W;
+  return scan_launch<Dir, T, kVec, Mode::kWalk, kReset>(
+      a, c, std::min((c.blocks + groups - 1) / groups, room), stream);
 }
 
 template <template <typename, int> class Dir, typename T, int kVec>

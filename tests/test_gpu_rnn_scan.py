@@ -99,26 +99,28 @@ def test_long_memory(dsp, dtype):
     check_backward(dsp, a, check_forward(dsp, a)["s"])
 
 
-@pytest.mark.parametrize("dtype,D", [(torch.float32, 64), (torch.bfloat16, 128)])
-def test_more_tiles_than_one_launch_has_records_for(dsp, dtype, D):
-    """300 blocks of lanes over 30 tiles of 128 steps: the sequence passes from launch to launch."""
-    N, L = 150, 3801
-    a = make(13, N, L, D, dtype, reset=0.0005)
-    out = forward(dsp, a)
-    grad = binding.rnn_scan_grad(dsp, cuda(a["za"]), cuda(a["zg"]), cuda(a["e"]), out["s"], cuda(a["ds"]), s0=dev(a["s0"]),
-                                 ds_last=dev(a["ds_last"]), reset=dev(a["reset"]))
-    torch.cuda.synchronize()
-    assert dsp.last_launches >= 2 and dsp.status() == 0
-    at = [0, 77, 149]
-    b = {k: None if v is None else v[at] for k, v in a.items()}
-    s, err = tr.rnn_scan(f64(b["za"]), f64(b["zg"]), f64(b["e"]), b["s0"], b["reset"])
-    near(out["s"][at], s, err, HALF[dtype], "s")
-    near(out["s_last"][at], s[:, -1], err[:, -1], HALF[torch.float32], "s_last")
-    want, bound = tr.rnn_scan_grad(f64(b["za"]), f64(b["zg"]), f64(b["e"]), f64(out["s"][at]), f64(b["ds"]), b["s0"],
-                                   b["ds_last"], b["reset"])
-    for i, name in enumerate(("dza", "dzg", "de")):
-        near(grad[name][at], want[i], bound[i], HALF[dtype], name)
-    near(grad["ds0"][at], want[3], bound[3], HALF[torch.float32], "ds0")
+def test_state_handed_on_in_one_buffer(dsp):
+    """A long sequence whose last state lands on its first, and the gradients likewise."""
+    a = make(13, 2, 20000, 48, torch.float32)
+    want = forward(dsp, a)
+    state, s = dev(a["s0"]), torch.empty_like(want["s"])
+    binding.dspark_rnn_scan(dsp, cuda(a["za"]), cuda(a["zg"]), cuda(a["e"]), state, None, 2, 20000, 48, s, state)
+    assert torch.equal(s, want["s"]) and torch.equal(state, want["s_last"])
+    args = [cuda(a[n]) for n in ("za", "zg", "e")] + [s, cuda(a["ds"])]
+    g = binding.rnn_scan_grad(dsp, *args, s0=dev(a["s0"]), ds_last=dev(a["ds_last"]))
+    dza, dzg, de, d = torch.empty_like(s), torch.empty_like(s), torch.empty_like(s), dev(a["ds_last"])
+    binding.dspark_rnn_scan_grad(dsp, *args, dev(a["s0"]), None, d, 2, 20000, 48, dza, dzg, de, d)
+    assert torch.equal(dza, g["dza"]) and torch.equal(dzg, g["dzg"]) and torch.equal(de, g["de"]) and torch.equal(d, g["ds0"])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1, 511, 32), (1, 512, 32), (1, 513, 64), (1, 1024, 2), (9, 1040, 512), (19, 515, 256),
+                                   (1, 40000, 3), (150, 600, 64)])
+def test_around_the_cut_into_segments(dsp, shape, dtype):
+    a = make(sum(shape), *shape, dtype, reset=0.002)
+    check_backward(dsp, a, check_forward(dsp, a)["s"])
+    a["s0"] = a["ds_last"] = a["reset"] = None
+    check_backward(dsp, a, check_forward(dsp, a)["s"])
 
 
 def test_saturated_gates(dsp):
