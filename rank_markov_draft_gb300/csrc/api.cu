@@ -137,7 +137,11 @@ size_t dtype_size(int dtype) {
 }
 
 dspark::ScanLaunch scan_launch(dspark_ctx* ctx) {
-  return {ctx->d_spans, ctx->num_sms, &ctx->last_launches, 0, 0, 0, 0, false};
+  dspark::ScanLaunch c{};
+  c.spans = ctx->d_spans;
+  c.num_sms = ctx->num_sms;
+  c.launches = &ctx->last_launches;
+  return c;
 }
 
 // The arguments that both directions of the RNN head's recurrence share.

@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include "cluster.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "rowscan.cuh"
 #include "sm103.cuh"
@@ -62,28 +63,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 // 2^((m - top) c), 0 where m is -inf (an empty part, whatever top is)
 __device__ __forceinline__ float part_scale(float m, float top, float c) {
   return m == -INFINITY ? 0.f : ex2_approx((m - top) * c);
-}
-
-// Two floats as the register pair of Blackwell's packed fp32 instructions (half the issue slots).
-struct F2 {
-  uint64_t v;
-  __device__ __forceinline__ F2() {}
-  __device__ __forceinline__ F2(float a, float b) {
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  }
-  __device__ __forceinline__ void get(float& a, float& b) const {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-  }
-};
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
 }
 
 // 16 bytes of a row: 4 fp32 or 8 bf16 logits.

@@ -302,7 +302,9 @@ struct ScanLaunch {
   // set by the launch
   int64_t blocks;  // of 32 lanes
   int W;           // warps that walk a block together
-  int segs, seg;   // segments a block, and their length in units of 16 steps
+  int segs, seg;   // segments a block, and their length in places
+  uint32_t div_mul;  // q / D
+  int div_shift;
   bool wide;       // rows start on 16-byte boundaries
 };
 cudaError_t launch_rnn_scan(const RnnScanArgs& a, const ScanLaunch& c, cudaStream_t stream);

@@ -13,12 +13,12 @@
 //
 // Both directions are a recurrence x_t = a_t x_{t-1} + b_t, so a span of steps acts on the
 // value before it as x -> A x + S (A the product of its decays, S its end from zero).  A warp
-// works on 16 steps of 32 lanes at a time (a lane is 4 bytes of channels: two bf16 or one fp32;
+// works on 8 or 16 steps of 32 lanes at a time (a lane is 4 bytes of channels: two bf16 or one fp32;
 // lanes run over sequences and channels alike, so no channel count leaves lanes empty).  The
 // steps arrive in shared memory by asynchronous copies, the next unit's while this one is
 // worked on, so loads are in flight all the time; a warp that does not start a sequence learns
 // the value before its steps from the spans before them.  Three ways:
-//   L <= 16:         there is nothing before them but s0.
+//   very many lanes: one warp walks a block of lanes alone, from s0 on.
 //   many lanes:      a CTA's warps hold consecutive spans, exchange (A, S) through shared
 //                    memory and walk over the sequence; the value after a tile stays with them.
 //   few lanes, long: the walk alone would leave most SMs empty, so every sequence is cut into
@@ -33,13 +33,13 @@
 #include <initializer_list>
 #include <cuda_bf16.h>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "sm103.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kSteps = 16;      // of a warp
 constexpr int kStages = 2;      // units in shared memory: this one and the next
 constexpr float kRsLog2e = 1.4426950408889634f;
 
@@ -65,19 +65,30 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// sigmoid(z): exact zero and one at the far ends
-__device__ __forceinline__ float gate(float z) {
-  return rcp_approx(1.f + ex2_approx(-z * kRsLog2e));
+// Two gates: sigmoid(z), exact zero and one at the far ends.
+__device__ __forceinline__ void gates(float z0, float z1, float& a0, float& a1) {
+  float y0, y1;
+  (F2(z0, z1) * F2(-kRsLog2e, -kRsLog2e)).get(y0, y1);
+  (F2(1.f, 1.f) + F2(ex2_approx(y0), ex2_approx(y1))).get(y0, y1);
+  a0 = rcp_approx(y0);
+  a1 = rcp_approx(y1);
 }
-// and its derivative to full relative precision: with t = e^-|z| and r = 1 / (1 + t) the two
-// sides of the gate are r and t r, the derivative t r^2.  t is the square of e^(-|z| / 2), which
+// and their derivatives to full relative precision: with t = e^-|z| and r = 1 / (1 + t) the two
+// sides of a gate are r and t r, the derivative t r^2.  t is the square of e^(-|z| / 2), which
 // keeps it down to the denormals that a product with a large gradient brings back into range.
-// (Explicit roundings here and below: what the compiler fuses differs between instances.)
-__device__ __forceinline__ float gate(float z, float& slope) {
-  const float h = ex2_approx(-0.5f * kRsLog2e * fabsf(z));
-  const float t = __fmul_rn(h, h), r = rcp_approx(__fadd_rn(1.f, t)), low = __fmul_rn(t, r);
-  slope = __fmul_rn(low, r);
-  return z >= 0.f ? r : low;
+__device__ __forceinline__ void gates(float z0, float z1, float& a0, float& a1, float& slope0,
+                                      float& slope1) {
+  float y0, y1, l0, l1;
+  (F2(fabsf(z0), fabsf(z1)) * F2(-0.5f * kRsLog2e, -0.5f * kRsLog2e)).get(y0, y1);
+  const F2 h(ex2_approx(y0), ex2_approx(y1)), t = h * h;
+  fma2(h, h, F2(1.f, 1.f)).get(y0, y1);
+  y0 = rcp_approx(y0);
+  y1 = rcp_approx(y1);
+  const F2 r(y0, y1), low = t * r;
+  (low * r).get(slope0, slope1);
+  low.get(l0, l1);
+  a0 = z0 >= 0.f ? y0 : l0;
+  a1 = z1 >= 0.f ? y1 : l1;
 }
 
 // Asynchronous copy of 16 or 4 bytes, zeros where `on` is false.
@@ -110,11 +121,50 @@ struct Stream {
   int shift;   // rows back (the state before a step)
 };
 
+// Values of kSteps steps of a lane's channels, [step][channel], are worked on two at a time: the
+// two channels of a step, or one channel of two steps.
+template <typename T, int kVec, int kSteps>
+struct Values {
+  float v[kSteps * kVec];
+  __device__ __forceinline__ void read(const uint32_t* words) {
+#pragma unroll
+    for (int k = 0; k < kSteps * kVec; ++k) v[k] = channel<T, kVec>(words[k / kVec * 32], k % kVec);
+  }
+  __device__ __forceinline__ void to_gates() {
+#pragma unroll
+    for (int k = 0; k < kSteps * kVec; k += 2) gates(v[k], v[k + 1], v[k], v[k + 1]);
+  }
+  __device__ __forceinline__ void to_gates(Values& slope) {
+#pragma unroll
+    for (int k = 0; k < kSteps * kVec; k += 2)
+      gates(v[k], v[k + 1], v[k], v[k + 1], slope.v[k], slope.v[k + 1]);
+  }
+  __device__ __forceinline__ void times(const Values& o) {
+#pragma unroll
+    for (int k = 0; k < kSteps * kVec; k += 2)
+      (F2(v[k], v[k + 1]) * F2(o.v[k], o.v[k + 1])).get(v[k], v[k + 1]);
+  }
+};
+// x <- a x + b and products over a step's channels (explicit fused steps: what the compiler would
+// fuse by itself differs between instances)
+__device__ __forceinline__ void step(const float* a, const float* b, float (&x)[1]) {
+  x[0] = fmaf(a[0], x[0], b[0]);
+}
+__device__ __forceinline__ void step(const float* a, const float* b, float (&x)[2]) {
+  fma2(F2(a[0], a[1]), F2(x[0], x[1]), F2(b[0], b[1])).get(x[0], x[1]);
+}
+__device__ __forceinline__ void mul(const float (&x)[1], const float* y, float (&r)[1]) {
+  r[0] = __fmul_rn(x[0], y[0]);
+}
+__device__ __forceinline__ void mul(const float (&x)[2], const float* y, float (&r)[2]) {
+  (F2(x[0], x[1]) * F2(y[0], y[1])).get(r[0], r[1]);
+}
+
 template <typename T, int kVec>
 struct Forward {
   using Args = RnnScanArgs;
   static constexpr bool kReverse = false;
-  static constexpr int kStreams = 3, kWarps = 8;
+  static constexpr int kStreams = 3, kWarps = 8, kSteps = 16;
   static __device__ __forceinline__ Stream stream(const Args& p, int i) {
     return i == 0 ? Stream{p.za, p.ld_za, 0} : i == 1 ? Stream{p.zg, p.ld_zg, 0}
                                                       : Stream{p.e, p.ld_e, 0};
@@ -123,52 +173,53 @@ struct Forward {
   static __device__ __forceinline__ const float* first(const Args& p) { return p.s0; }
 
   // words: [stream][step][lane] of this warp, at this lane.  a < 0: a reset.
-  float a[kSteps][kVec], b[kSteps][kVec];
+  Values<T, kVec, kSteps> a, b;
   template <bool kReset>
   __device__ __forceinline__ void read(const Args& p, const uint32_t* words, uint32_t resets,
                                        int steps) {
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        a[j][i] = gate(channel<T, kVec>(words[j * 32], i));
-        b[j][i] = channel<T, kVec>(words[(2 * kSteps + j) * 32], i);
-      }
+    b.read(words + 2 * kSteps * 32);
     if (p.zg != nullptr) {
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          b[j][i] *= gate(channel<T, kVec>(words[(kSteps + j) * 32], i));
+      a.read(words + kSteps * 32);
+      a.to_gates();
+      b.times(a);
     }
+    a.read(words);
+    a.to_gates();
     if (kReset && resets != 0u) {
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          if (resets >> j & 1u) a[j][i] = kDrops;
+      for (int k = 0; k < kSteps * kVec; ++k)
+        if (resets >> (k / kVec) & 1u) a.v[k] = kDrops;
     }
     if (steps < kSteps) {  // a step past the end changes nothing
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          if (j >= steps) a[j][i] = 1.f, b[j][i] = 0.f;
+      for (int k = 0; k < kSteps * kVec; ++k)
+        if (k / kVec >= steps) a.v[k] = 1.f, b.v[k] = 0.f;
     }
   }
   template <bool kReset>
-  __device__ __forceinline__ Span span(int i) const {
-    Span f{1.f, 0.f};
+  __device__ __forceinline__ void span(Span (&f)[kVec]) const {
+    float A[kVec], S[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      A[i] = 1.f;
+      S[i] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
       if (kReset) {
-        f = then(f, Span{a[j][i], b[j][i]});
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const Span g = then(Span{A[i], S[i]}, Span{a.v[j * kVec + i], b.v[j * kVec + i]});
+          A[i] = g.A;
+          S[i] = g.S;
+        }
       } else {
-        f.A *= a[j][i];
-        f.S = fmaf(a[j][i], f.S, b[j][i]);
+        mul(A, a.v + j * kVec, A);
+        step(a.v + j * kVec, b.v + j * kVec, S);
       }
     }
-    return f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = {A[i], S[i]};
   }
   template <bool kReset, bool kFull>
   __device__ __forceinline__ void run(const Args& p, const uint32_t*, uint32_t, int64_t n, int d,
@@ -177,9 +228,12 @@ struct Forward {
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
       if (!kFull && j >= steps) break;
+      if (kReset) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        x[i] = kReset && a[j][i] < 0.f ? b[j][i] : fmaf(a[j][i], x[i], b[j][i]);
+        for (int i = 0; i < kVec; ++i) x[i] = apply(Span{a.v[j * kVec + i], b.v[j * kVec + i]}, x[i]);
+      } else {
+        step(a.v + j * kVec, b.v + j * kVec, x);
+      }
       put_lane(s + static_cast<int64_t>(j) * p.D, x);
     }
     if (p.s_last != nullptr && t0 + steps == p.L && (kFull || steps > 0))
@@ -192,7 +246,7 @@ template <typename T, int kVec>
 struct Backward {
   using Args = RnnScanGradArgs;
   static constexpr bool kReverse = true;
-  static constexpr int kStreams = 5, kWarps = 4;
+  static constexpr int kStreams = 5, kWarps = 8, kSteps = 8;
   static __device__ __forceinline__ Stream stream(const Args& p, int i) {
     return i == 0   ? Stream{p.za, p.ld_za, 0}
            : i == 1 ? Stream{p.zg, p.ld_zg, 0}
@@ -203,73 +257,107 @@ struct Backward {
   static constexpr __device__ bool in_span(int i) { return i == 0 || i == 3; }
   static __device__ __forceinline__ const float* first(const Args& p) { return p.ds_last; }
 
-  const uint32_t* w;
+  Values<T, kVec, kSteps> a, slope, ds;
   uint32_t drop;
   int count;
   template <bool kReset>
   __device__ __forceinline__ void read(const Args&, const uint32_t* words, uint32_t resets,
                                        int steps) {
-    w = words;
+    a.read(words);
+    a.to_gates(slope);
+    ds.read(words + 3 * kSteps * 32);
     drop = kReset ? resets : 0u;
     count = steps;
   }
   template <bool kReset>
-  __device__ __forceinline__ Span span(int i) const {
-    Span f{1.f, 0.f};
+  __device__ __forceinline__ void span(Span (&f)[kVec]) const {
+    // y = a delta is kept as its two factors, so a step is one fused operation
+    float A[kVec], an[kVec], delta[kVec], y[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      A[i] = an[i] = 1.f;
+      delta[i] = 0.f;
+    }
 #pragma unroll
     for (int j = kSteps - 1; j >= 0; --j) {
-      const float a = gate(channel<T, kVec>(w[j * 32], i));
-      const float ds = channel<T, kVec>(w[(3 * kSteps + j) * 32], i);
       if (j >= count) continue;
-      if (kReset && (drop >> j & 1u)) {
-        f = Span{kDrops, 0.f};
-      } else {
-        f.S = __fmul_rn(a, __fadd_rn(f.S, ds));
-        f.A = f.A == kDrops ? kDrops : f.A * a;
+      step(an, ds.v + j * kVec, delta);
+      const bool reset = kReset && (drop >> j & 1u);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        an[i] = reset ? 0.f : a.v[j * kVec + i];
+        if (reset) delta[i] = 0.f;
+        if (kReset) A[i] = reset || A[i] == kDrops ? kDrops : A[i] * an[i];
       }
+      if (!kReset) mul(A, an, A);
     }
-    return f;
+    mul(delta, an, y);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = {A[i], y[i]};
   }
   template <bool kReset, bool kFull>
   __device__ __forceinline__ void run(const Args& p, const uint32_t* words, uint32_t resets,
-                                      int64_t n, int d, int64_t t0, int steps,
-                                      float (&x)[kVec]) const {
+                                      int64_t n, int d, int64_t t0, int steps, float (&x)[kVec]) {
     const int64_t r = n * p.L + t0;
     T* pa = static_cast<T*>(p.dza) + r * p.ld_dza + d;
     T* pg = static_cast<T*>(p.dzg) + r * p.ld_dzg + d;
     T* pe = static_cast<T*>(p.de) + r * p.D + d;
-    const bool gated = p.dzg != nullptr;
     const int ld_a = static_cast<int>(p.ld_dza), ld_g = static_cast<int>(p.ld_dzg);
+    // the state before each step, then delta
+    Values<T, kVec, kSteps> o;
+    o.read(words + 4 * kSteps * 32);
+    if (t0 == 0)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) o.v[i] = p.s0 != nullptr ? p.s0[n * p.D + d + i] : 0.f;
+    float an[kVec], delta[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      an[i] = 1.f;
+      delta[i] = x[i];
+    }
 #pragma unroll
     for (int j = kSteps - 1; j >= 0; --j) {
       if (!kFull && j >= steps) continue;
+      const int k = j * kVec;
       const bool reset = kReset && (resets >> j & 1u);
-      float oa[kVec], og[kVec], oe[kVec];
+      float y[kVec];
+      step(an, ds.v + k, delta);
+      mul(delta, o.v + k, y);
+      mul(y, slope.v + k, y);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const auto get = [&](int k) { return channel<T, kVec>(words[(k * kSteps + j) * 32], i); };
-        float slope;
-        const float a = gate(get(0), slope);
-        float before = get(4);
-        if (j == 0 && t0 == 0) before = p.s0 != nullptr ? p.s0[n * p.D + d + i] : 0.f;
-        const float delta = __fadd_rn(get(3), x[i]);
-        oa[i] = reset ? 0.f : delta * before * slope;
-        x[i] = reset ? 0.f : __fmul_rn(a, delta);
-        oe[i] = delta;
+        o.v[k + i] = delta[i];
+        an[i] = reset ? 0.f : a.v[k + i];
+        if (reset) y[i] = delta[i] = 0.f;
       }
-      put_lane(pa + static_cast<int64_t>(j) * ld_a, oa);
-      if (gated) {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          float slope;
-          const float g = gate(channel<T, kVec>(words[(kSteps + j) * 32], i), slope);
-          og[i] = oe[i] * channel<T, kVec>(words[(2 * kSteps + j) * 32], i) * slope;
-          oe[i] *= g;
-        }
-        put_lane(pg + static_cast<int64_t>(j) * ld_g, og);
-      }
-      put_lane(pe + static_cast<int64_t>(j) * p.D, oe);
+      put_lane(pa + static_cast<int64_t>(j) * ld_a, y);
     }
+    mul(delta, an, x);
+    if (p.dzg != nullptr) {
+      Values<T, kVec, kSteps> e;
+      a.read(words + kSteps * 32);
+      a.to_gates(slope);
+      e.read(words + 2 * kSteps * 32);
+      e.times(o);
+      e.times(slope);
+      o.times(a);
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+        if (kFull || j < steps) {
+          float y[kVec];
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) y[i] = e.v[j * kVec + i];
+          put_lane(pg + static_cast<int64_t>(j) * ld_g, y);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j)
+      if (kFull || j < steps) {
+        float y[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) y[i] = o.v[j * kVec + i];
+        put_lane(pe + static_cast<int64_t>(j) * p.D, y);
+      }
     if (p.ds0 != nullptr && t0 == 0 && (kFull || steps > 0))
 #pragma unroll
       for (int i = 0; i < kVec; ++i) p.ds0[n * p.D + d + i] = x[i];
@@ -279,7 +367,8 @@ struct Backward {
 // What a launch does with the sequences (see above).
 enum class Mode { kWalk, kSpans, kSegments };
 
-// A unit of work of a warp: 16 steps at place `pos` (in units of 16, in the recurrence's order)
+// A unit of work of a warp: kSteps steps at place `pos` (counted in such, in the recurrence's
+// order)
 // of a lane block; block < 0: none.  Walks: a CTA's kWarps / W groups of W warps take every
 // gridDim.x-th kWarps / W blocks, W places at a time.  Segments: the CTA's warps are consecutive
 // segments of c.seg places of one block.
@@ -287,7 +376,7 @@ template <template <typename, int> class Dir, typename T, int kVec, Mode kMode, 
 __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     scan_kernel(const typename Dir<T, kVec>::Args p, const ScanLaunch c) {
   using D = Dir<T, kVec>;
-  constexpr int kWarps = D::kWarps, kWords = D::kStreams * kSteps * 32;
+  constexpr int kWarps = D::kWarps, kSteps = D::kSteps, kWords = D::kStreams * kSteps * 32;
   constexpr int kWarpWords = kWords + 32 * kVec;
   constexpr bool kWalk = kMode == Mode::kWalk;
   extern __shared__ uint4 s_raw[];  // [kStages][kWarps] x (kWords words, 32 kVec floats)
@@ -335,10 +424,9 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
   const auto start = [&](const Unit& u) {  // first step
     return (D::kReverse ? places - 1 - u.pos : u.pos) * kSteps;
   };
-  const auto sequence = [&](uint32_t q, int64_t& n, int& d) {
-    const uint32_t s = q / static_cast<uint32_t>(p.D);
-    n = s;
-    d = static_cast<int>(q - s * static_cast<uint32_t>(p.D));
+  const auto sequence = [&](uint32_t q, int& n, int& d) {  // q / D by the launch's multiplier
+    n = static_cast<int>((static_cast<uint64_t>(q) * c.div_mul) >> c.div_shift);
+    d = static_cast<int>(q - static_cast<uint32_t>(n) * static_cast<uint32_t>(p.D));
   };
   // whether the 32 lanes of a block lie in one sequence (then one load brings all its flags)
   const bool one = kReset && p.D % (32 * kVec) == 0;
@@ -351,54 +439,61 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
       return;
     }
     uint32_t* dst = words(stage);
-    const uint32_t q0 = static_cast<uint32_t>(u.block) * 32u * kVec;
+    const uint32_t q0 = static_cast<uint32_t>(u.block) * 32u * kVec, q = q0 + lane * kVec;
+    const bool in = q < lanes;
+    int n = 0, d = 0;
+    if (in) sequence(q, n, d);
+    const bool full = q0 + 32u * kVec <= lanes && t0 > 0 && t0 + kSteps <= p.L;
     if (c.wide) {  // 16-byte pieces: this lane's are 4 steps apart, in one sequence
       constexpr int kPiece = 16 / sizeof(T);
-      const uint32_t q = q0 + (lane & 7) * kPiece;
-      int64_t n = 0;
-      int d = 0;
-      const bool in = q < lanes;
-      if (in) sequence(q, n, d);
+      const int sub = lane >> 3;
+      const uint32_t qp = q0 + (lane & 7) * kPiece;
+      const bool inp = qp < lanes;
+      int np = 0, dp = 0;
+      if (inp) sequence(qp, np, dp);
+      const int row = np * static_cast<int>(p.L) + static_cast<int>(t0) + sub;
+      uint32_t* to = dst + sub * 32 + (lane & 7) * 4;
 #pragma unroll
       for (int i = 0; i < D::kStreams; ++i) {
         const Stream st = D::stream(p, i);
         if (st.p == nullptr || (kMode == Mode::kSpans && !D::in_span(i))) continue;
-        const int64_t row = n * p.L + t0 - st.shift + (lane >> 3);
-        const T* src = static_cast<const T*>(st.p) + row * st.ld + d;
+        const int ld = static_cast<int>(st.ld);
+        const T* src = static_cast<const T*>(st.p) + static_cast<int64_t>(row - st.shift) * ld + dp;
+        if (full) {
 #pragma unroll
-        for (int j = 0; j < kSteps; j += 4) {
-          const int64_t t = t0 + j + (lane >> 3);
-          const bool on = in && t0 >= 0 && t < p.L && (st.shift == 0 || t > 0);
-          copy_16(dst + (i * kSteps + j + (lane >> 3)) * 32 + (lane & 7) * 4,
-                  on ? src + j * st.ld : static_cast<const T*>(st.p), on);
+          for (int j = 0; j < kSteps; j += 4)
+            copy_16(to + (i * kSteps + j) * 32, src + static_cast<int64_t>(j) * ld, true);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kSteps; j += 4) {
+            const int64_t t = t0 + j + sub;
+            const bool on = inp && t0 >= 0 && t < p.L && (st.shift == 0 || t > 0);
+            copy_16(to + (i * kSteps + j) * 32,
+                    on ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p), on);
+          }
         }
       }
-    }
-    const uint32_t q = q0 + lane * kVec;
-    int64_t n = 0;
-    int d = 0;
-    const bool in = q < lanes;
-    if (in) sequence(q, n, d);
-    if (!c.wide) {
+    } else {
+      const int row = n * static_cast<int>(p.L) + static_cast<int>(t0);
 #pragma unroll
       for (int i = 0; i < D::kStreams; ++i) {
         const Stream st = D::stream(p, i);
         if (st.p == nullptr || (kMode == Mode::kSpans && !D::in_span(i))) continue;
-        const T* src = static_cast<const T*>(st.p) + (n * p.L + t0 - st.shift) * st.ld + d;
+        const int ld = static_cast<int>(st.ld);
+        const T* src = static_cast<const T*>(st.p) + static_cast<int64_t>(row - st.shift) * ld + d;
+        const auto on = [&](int j) {
+          return in && t0 >= 0 && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
+        };
         if (sizeof(T) * kVec == 4) {
 #pragma unroll 4
-          for (int j = 0; j < kSteps; ++j) {
-            const bool on = in && t0 >= 0 && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
+          for (int j = 0; j < kSteps; ++j)
             copy_4(dst + (i * kSteps + j) * 32 + lane,
-                   on ? src + j * st.ld : static_cast<const T*>(st.p), on);
-          }
+                   on(j) ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p), on(j));
         } else {  // single bf16 channels: no asynchronous copy is that small
           uint32_t v[kSteps];
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) {
-            const bool on = in && t0 >= 0 && t0 + j < p.L && (st.shift == 0 || t0 + j > 0);
-            v[j] = on ? static_cast<uint32_t>(__ldcs(src + j * st.ld)) : 0u;
-          }
+          for (int j = 0; j < kSteps; ++j)
+            v[j] = on(j) ? static_cast<uint32_t>(__ldcs(src + static_cast<int64_t>(j) * ld)) : 0u;
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) dst[(i * kSteps + j) * 32 + lane] = v[j];
         }
@@ -410,7 +505,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
         copy_4(dst + kWords + lane * kVec + i, D::first(p) + (in ? q + i : 0), in);
     cp_async_commit();
     if (kReset) {
-      const uint8_t* src = p.reset + n * p.L + t0;
+      const uint8_t* src = p.reset + static_cast<int64_t>(n) * p.L + t0;
       flags = 0u;
       if (one) {
         if (in && lane < kSteps && t0 >= 0 && t0 + lane < p.L) flags = __ldg(src + lane);
@@ -470,8 +565,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     const int64_t t0 = start(cur), left = p.L - t0;
     const uint32_t q = static_cast<uint32_t>(cur.block) * 32u * kVec + lane * kVec;
     const bool valid = q < lanes && t0 >= 0;
-    int64_t n = 0;
-    int d = 0;
+    int n = 0, d = 0;
     if (valid) sequence(q, n, d);
     const int count = !valid || left <= 0 ? 0 : (left < kSteps ? static_cast<int>(left) : kSteps);
     uint32_t resets = 0u;
@@ -486,16 +580,19 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     D dir;
     dir.template read<kReset>(p, in, resets, count);
     if (kMode == Mode::kSpans) {
+      Span f[kVec];
+      dir.template span<kReset>(f);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = then(dir.template span<kReset>(i), acc[i]);
+      for (int i = 0; i < kVec; ++i) acc[i] = then(f[i], acc[i]);
     } else {
       float mine[kVec];
 #pragma unroll
       for (int i = 0; i < kVec; ++i) mine[i] = x[i];
       if (W > 1) {
+        Span f[kVec];
+        dir.template span<kReset>(f);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          s_span[stage][warp][lane * kVec + i] = dir.template span<kReset>(i);
+        for (int i = 0; i < kVec; ++i) s_span[stage][warp][lane * kVec + i] = f[i];
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
@@ -542,7 +639,7 @@ cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& 
                         cudaStream_t stream) {
   using D = Dir<T, kVec>;
   const auto fn = scan_kernel<Dir, T, kVec, kMode, kReset>;
-  constexpr int kSmem = kStages * D::kWarps * (D::kStreams * kSteps * 32 + 32 * kVec) * 4;
+  constexpr int kSmem = kStages * D::kWarps * (D::kStreams * D::kSteps * 32 + 32 * kVec) * 4;
   static const cudaError_t once =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (once != cudaSuccess) return once;
@@ -553,12 +650,15 @@ cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& 
 
 template <template <typename, int> class Dir, typename T, int kVec, bool kReset>
 cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStream_t stream) {
-  constexpr int kWarps = Dir<T, kVec>::kWarps;
+  constexpr int kWarps = Dir<T, kVec>::kWarps, kSteps = Dir<T, kVec>::kSteps;
   const int64_t lanes = (a.N * a.D + kVec - 1) / kVec, places = (a.L + kSteps - 1) / kSteps;
   const int64_t room = 2 * c.num_sms;  // two CTAs fit an SM
   c.blocks = (lanes + 31) / 32;
-  c.W = 1;
-  while (c.W < kWarps && c.W < places) c.W *= 2;
+  // q / D = q * div_mul >> div_shift for q < 2^31
+  int bits = 0;
+  while ((1ll << bits) < a.D) ++bits;
+  c.div_shift = 31 + bits;
+  c.div_mul = static_cast<uint32_t>(((1ull << c.div_shift) + a.D - 1) / a.D);
   // Segments where walking would leave SMs without a CTA and sequences are long enough to cut.
   if (2 * c.blocks <= room && places >= 4 * kWarps) {
     int64_t per = std::min<int64_t>(room / c.blocks, kScanCtas / c.blocks);  // CTAs a block
@@ -570,6 +670,9 @@ cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStre
     if (e != cudaSuccess) return e;
     return scan_launch<Dir, T, kVec, Mode::kSegments, kReset>(a, c, c.blocks * per, stream);
   }
+  // as few warps to a block as fill the SMs: more of them exchange spans at every turn
+  c.W = 1;
+  while (c.W < kWarps && c.W < places && c.blocks * c.W < room * kWarps) c.W *= 2;
   const int64_t groups = kWarps / c.W;
   return scan_launch<Dir, T, kVec, Mode::kWalk, kReset>(
       a, c, std::min((c.blocks + groups - 1) / groups, room), stream);
