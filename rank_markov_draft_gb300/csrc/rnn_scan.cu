@@ -15,7 +15,7 @@
 // value before it as x -> A x + S (A the product of its decays, S its end from zero).  A warp
 // works on 8 or 16 steps of 32 lanes at a time (a lane is 4 bytes of channels: two bf16 or one fp32;
 // lanes run over sequences and channels alike, so no channel count leaves lanes empty).  The
-// steps arrive in shared memory by asynchronous copies, the next unit's while this one is
+// steps arrive in shared memory by asynchronous copies, the next units' while this one is
 // worked on, so loads are in flight all the time; a warp that does not start a sequence learns
 // the value before its steps from the spans before them.  Three ways:
 //   very many lanes: one warp walks a block of lanes alone, from s0 on.
@@ -40,7 +40,6 @@
 namespace dspark {
 namespace {
 
-constexpr int kStages = 2;      // units in shared memory: this one and the next
 constexpr float kRsLog2e = 1.4426950408889634f;
 
 // ---- lanes: kVec channels in one 32-bit word
@@ -114,6 +113,9 @@ __device__ __forceinline__ Span then(Span f, Span g) {  // f first
   return {f.A == kDrops || g.A == kDrops ? kDrops : f.A * g.A, apply(g, f.S)};
 }
 
+// What a launch does with the sequences (see above).
+enum class Mode { kWalk, kSpans, kSegments };
+
 // ---- the two directions: their streams, their step's (a, b), and what a step writes
 struct Stream {
   const void* p;
@@ -164,17 +166,21 @@ template <typename T, int kVec>
 struct Forward {
   using Args = RnnScanArgs;
   static constexpr bool kReverse = false;
-  static constexpr int kStreams = 3, kWarps = 8, kSteps = 16;
+  static constexpr int kStreams = 3, kWarps = 8, kSteps = 8;
+  // units in shared memory of a warp: the one worked on and the ones on their way
+  static constexpr __host__ __device__ int stages(Mode) { return 4; }
   static __device__ __forceinline__ Stream stream(const Args& p, int i) {
     return i == 0 ? Stream{p.za, p.ld_za, 0} : i == 1 ? Stream{p.zg, p.ld_zg, 0}
                                                       : Stream{p.e, p.ld_e, 0};
   }
-  static constexpr __device__ bool in_span(int) { return true; }  // a stream that spans need
+  // the place of a stream among those copied (spans may need fewer), -1: none
+  static constexpr __host__ __device__ int streams(Mode) { return 3; }
+  static constexpr __device__ int place(Mode, int i) { return i; }
   static __device__ __forceinline__ const float* first(const Args& p) { return p.s0; }
 
   // words: [stream][step][lane] of this warp, at this lane.  a < 0: a reset.
   Values<T, kVec, kSteps> a, b;
-  template <bool kReset>
+  template <Mode kMode, bool kReset>
   __device__ __forceinline__ void read(const Args& p, const uint32_t* words, uint32_t resets,
                                        int steps) {
     b.read(words + 2 * kSteps * 32);
@@ -247,6 +253,7 @@ struct Backward {
   using Args = RnnScanGradArgs;
   static constexpr bool kReverse = true;
   static constexpr int kStreams = 5, kWarps = 8, kSteps = 8;
+  static constexpr __host__ __device__ int stages(Mode m) { return m == Mode::kSpans ? 5 : 2; }
   static __device__ __forceinline__ Stream stream(const Args& p, int i) {
     return i == 0   ? Stream{p.za, p.ld_za, 0}
            : i == 1 ? Stream{p.zg, p.ld_zg, 0}
@@ -254,18 +261,21 @@ struct Backward {
            : i == 3 ? Stream{p.ds, p.D, 0}
                     : Stream{p.s, p.D, 1};
   }
-  static constexpr __device__ bool in_span(int i) { return i == 0 || i == 3; }
+  static constexpr __host__ __device__ int streams(Mode m) { return m == Mode::kSpans ? 2 : 5; }
+  static constexpr __device__ int place(Mode m, int i) {
+    return m != Mode::kSpans ? i : i == 0 ? 0 : i == 3 ? 1 : -1;
+  }
   static __device__ __forceinline__ const float* first(const Args& p) { return p.ds_last; }
 
   Values<T, kVec, kSteps> a, slope, ds;
   uint32_t drop;
   int count;
-  template <bool kReset>
+  template <Mode kMode, bool kReset>
   __device__ __forceinline__ void read(const Args&, const uint32_t* words, uint32_t resets,
                                        int steps) {
     a.read(words);
     a.to_gates(slope);
-    ds.read(words + 3 * kSteps * 32);
+    ds.read(words + place(kMode, 3) * kSteps * 32);
     drop = kReset ? resets : 0u;
     count = steps;
   }
@@ -364,9 +374,6 @@ struct Backward {
   }
 };
 
-// What a launch does with the sequences (see above).
-enum class Mode { kWalk, kSpans, kSegments };
-
 // A unit of work of a warp: kSteps steps at place `pos` (counted in such, in the recurrence's
 // order)
 // of a lane block; block < 0: none.  Walks: a CTA's kWarps / W groups of W warps take every
@@ -376,11 +383,12 @@ template <template <typename, int> class Dir, typename T, int kVec, Mode kMode, 
 __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     scan_kernel(const typename Dir<T, kVec>::Args p, const ScanLaunch c) {
   using D = Dir<T, kVec>;
-  constexpr int kWarps = D::kWarps, kSteps = D::kSteps, kWords = D::kStreams * kSteps * 32;
+  constexpr int kWarps = D::kWarps, kSteps = D::kSteps, kStages = D::stages(kMode);
+  constexpr int kWords = D::streams(kMode) * kSteps * 32;
   constexpr int kWarpWords = kWords + 32 * kVec;
   constexpr bool kWalk = kMode == Mode::kWalk;
-  extern __shared__ uint4 s_raw[];  // [kStages][kWarps] x (kWords words, 32 kVec floats)
-  __shared__ Span s_span[kStages][kWarps][32 * kVec];
+  extern __shared__ uint4 s_raw[];  // [stage][warp] x (kWords words, 32 kVec floats)
+  __shared__ Span s_span[2][kWarps][32 * kVec];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = kWalk ? c.W : 1, groups = kWarps / W, group = warp / W, order = warp % W;
   const int64_t places = (p.L + kSteps - 1) / kSteps;
@@ -456,19 +464,20 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
 #pragma unroll
       for (int i = 0; i < D::kStreams; ++i) {
         const Stream st = D::stream(p, i);
-        if (st.p == nullptr || (kMode == Mode::kSpans && !D::in_span(i))) continue;
+        const int at = D::place(kMode, i) * kSteps;
+        if (st.p == nullptr || at < 0) continue;
         const int ld = static_cast<int>(st.ld);
         const T* src = static_cast<const T*>(st.p) + static_cast<int64_t>(row - st.shift) * ld + dp;
         if (full) {
 #pragma unroll
           for (int j = 0; j < kSteps; j += 4)
-            copy_16(to + (i * kSteps + j) * 32, src + static_cast<int64_t>(j) * ld, true);
+            copy_16(to + (at + j) * 32, src + static_cast<int64_t>(j) * ld, true);
         } else {
 #pragma unroll
           for (int j = 0; j < kSteps; j += 4) {
             const int64_t t = t0 + j + sub;
             const bool on = inp && t0 >= 0 && t < p.L && (st.shift == 0 || t > 0);
-            copy_16(to + (i * kSteps + j) * 32,
+            copy_16(to + (at + j) * 32,
                     on ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p), on);
           }
         }
@@ -478,7 +487,8 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
 #pragma unroll
       for (int i = 0; i < D::kStreams; ++i) {
         const Stream st = D::stream(p, i);
-        if (st.p == nullptr || (kMode == Mode::kSpans && !D::in_span(i))) continue;
+        const int at = D::place(kMode, i) * kSteps;
+        if (st.p == nullptr || at < 0) continue;
         const int ld = static_cast<int>(st.ld);
         const T* src = static_cast<const T*>(st.p) + static_cast<int64_t>(row - st.shift) * ld + d;
         const auto on = [&](int j) {
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
         if (sizeof(T) * kVec == 4) {
 #pragma unroll 4
           for (int j = 0; j < kSteps; ++j)
-            copy_4(dst + (i * kSteps + j) * 32 + lane,
+            copy_4(dst + (at + j) * 32 + lane,
                    on(j) ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p), on(j));
         } else {  // single bf16 channels: no asynchronous copy is that small
           uint32_t v[kSteps];
@@ -495,7 +505,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
           for (int j = 0; j < kSteps; ++j)
             v[j] = on(j) ? static_cast<uint32_t>(__ldcs(src + static_cast<int64_t>(j) * ld)) : 0u;
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) dst[(i * kSteps + j) * 32 + lane] = v[j];
+          for (int j = 0; j < kSteps; ++j) dst[(at + j) * 32 + lane] = v[j];
         }
       }
     }
@@ -516,8 +526,14 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     }
   };
 
-  uint32_t flags = 0u, next_flags = 0u;
-  fetch(cur, 0, flags);
+  // the first kStages - 1 units on their way
+  uint32_t flags[kStages];  // of the units in turn
+  Unit far = cur;
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) {
+    fetch(far, k, flags[k]);
+    far = after(far);
+  }
   float x[kVec];
   Span acc[kVec];
 #pragma unroll
@@ -526,7 +542,9 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     acc[i] = {1.f, 0.f};
   }
   const size_t channel0 = static_cast<size_t>(lane) * kVec;
+  if (kMode == Mode::kSpans) griddep_launch_dependents();
   if (kMode == Mode::kSegments) {
+    griddep_wait();
     // the value before the segment: through the spans of the CTAs before this one and of the
     // warps before this one (the first of them drops what is before it for the sequence's first
     // value, which another CTA may by now have overwritten with the last)
@@ -555,11 +573,11 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
       x[i] = apply(Span{f.x, f.y}, x[i]);
     }
   }
-  Unit nxt = after(cur);
+  int stage = 0;
   for (int turn = 0; cur.block >= 0; ++turn) {
-    const int stage = turn & 1;
-    fetch(nxt, stage ^ 1, next_flags);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    fetch(far, stage == 0 ? kStages - 1 : stage - 1, flags[kStages - 1]);
+    far = after(far);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
     const uint32_t* in = words(stage) + lane;
     const int64_t t0 = start(cur), left = p.L - t0;
@@ -569,7 +587,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     if (valid) sequence(q, n, d);
     const int count = !valid || left <= 0 ? 0 : (left < kSteps ? static_cast<int>(left) : kSteps);
     uint32_t resets = 0u;
-    if (kReset) resets = one ? __ballot_sync(0xFFFFFFFFu, flags != 0u) : flags;
+    if (kReset) resets = one ? __ballot_sync(0xFFFFFFFFu, flags[0] != 0u) : flags[0];
     if (kWalk && cur.pos == pos_begin) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
@@ -578,7 +596,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
                    : 0.f;
     }
     D dir;
-    dir.template read<kReset>(p, in, resets, count);
+    dir.template read<kMode, kReset>(p, in, resets, count);
     if (kMode == Mode::kSpans) {
       Span f[kVec];
       dir.template span<kReset>(f);
@@ -592,13 +610,13 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
         Span f[kVec];
         dir.template span<kReset>(f);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) s_span[stage][warp][lane * kVec + i] = f[i];
+        for (int i = 0; i < kVec; ++i) s_span[turn & 1][warp][lane * kVec + i] = f[i];
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
           for (int k = 0; k < W; ++k) {
             if (k == order) mine[i] = x[i];
-            x[i] = apply(s_span[stage][group * W + k][lane * kVec + i], x[i]);
+            x[i] = apply(s_span[turn & 1][group * W + k][lane * kVec + i], x[i]);
           }
       }
       if (count == kSteps)
@@ -610,9 +628,10 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
         for (int i = 0; i < kVec; ++i) x[i] = mine[i];
     }
     __syncwarp();  // this warp's steps are read before the next copies land on them
-    cur = nxt;
-    nxt = after(nxt);
-    flags = next_flags;
+    cur = after(cur);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) flags[k] = flags[k + 1];
   }
   if (kMode == Mode::kSpans) {
     // this CTA's span, and before each warp's segment the span of the warps before it
@@ -639,13 +658,26 @@ cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& 
                         cudaStream_t stream) {
   using D = Dir<T, kVec>;
   const auto fn = scan_kernel<Dir, T, kVec, kMode, kReset>;
-  constexpr int kSmem = kStages * D::kWarps * (D::kStreams * D::kSteps * 32 + 32 * kVec) * 4;
+  constexpr int kSmem =
+      D::stages(kMode) * D::kWarps * (D::streams(kMode) * D::kSteps * 32 + 32 * kVec) * 4;
   static const cudaError_t once =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (once != cudaSuccess) return once;
-  fn<<<static_cast<unsigned>(grid), D::kWarps * 32, kSmem, stream>>>(a, c);
-  *c.launches += 1;
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(D::kWarps * 32);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  // the walk of the segments starts while their spans are finished: its first copies read only
+  // what the launch for the spans had to wait for as well
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kMode == Mode::kSegments ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, c);
+  if (e == cudaSuccess) *c.launches += 1;
+  return e;
 }
 
 template <template <typename, int> class Dir, typename T, int kVec, bool kReset>
@@ -670,9 +702,10 @@ cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStre
     if (e != cudaSuccess) return e;
     return scan_launch<Dir, T, kVec, Mode::kSegments, kReset>(a, c, c.blocks * per, stream);
   }
-  // as few warps to a block as fill the SMs: more of them exchange spans at every turn
+  // As few warps to a block as fill the SMs, since they exchange spans at every turn, and none
+  // that would have a single turn (so 16 steps give what 16 calls of one step give).
   c.W = 1;
-  while (c.W < kWarps && c.W < places && c.blocks * c.W < room * kWarps) c.W *= 2;
+  while (c.W < kWarps && 2 * c.W < places && c.blocks * c.W < room * kWarps) c.W *= 2;
   const int64_t groups = kWarps / c.W;
   return scan_launch<Dir, T, kVec, Mode::kWalk, kReset>(
       a, c, std::min((c.blocks + groups - 1) / groups, room), stream);
