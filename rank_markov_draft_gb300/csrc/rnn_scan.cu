@@ -595,11 +595,21 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
                    ? __uint_as_float(words(stage)[kWords + lane * kVec + i])
                    : 0.f;
     }
+    // (a unit without a reset, as most are, takes the shorter code)
+    const bool any = kReset && __any_sync(0xFFFFFFFFu, resets != 0u);
     D dir;
-    dir.template read<kMode, kReset>(p, in, resets, count);
+    if (kReset && any)
+      dir.template read<kMode, true>(p, in, resets, count);
+    else
+      dir.template read<kMode, false>(p, in, 0u, count);
+    Span f[kVec];
+    if (kMode == Mode::kSpans || W > 1) {
+      if (kReset && any)
+        dir.template span<true>(f);
+      else
+        dir.template span<false>(f);
+    }
     if (kMode == Mode::kSpans) {
-      Span f[kVec];
-      dir.template span<kReset>(f);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) acc[i] = then(f[i], acc[i]);
     } else {
@@ -607,8 +617,6 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) mine[i] = x[i];
       if (W > 1) {
-        Span f[kVec];
-        dir.template span<kReset>(f);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) s_span[turn & 1][warp][lane * kVec + i] = f[i];
         __syncthreads();
@@ -619,8 +627,8 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
             x[i] = apply(s_span[turn & 1][group * W + k][lane * kVec + i], x[i]);
           }
       }
-      if (count == kSteps)
-        dir.template run<kReset, true>(p, in, resets, n, d, t0, count, mine);
+      if (count == kSteps && !any)
+        dir.template run<false, true>(p, in, 0u, n, d, t0, count, mine);
       else
         dir.template run<kReset, false>(p, in, resets, n, d, t0, count, mine);
       if (W == 1)
