@@ -1005,7 +1005,7 @@ int dspark_verify_probs(dspark_ctx* ctx, const float* P, const float* Q, const i
   a.accept_prob = accept_prob;
   a.status = ctx->d_status;
   st = cuda_status(dspark::launch_verify_probs(a, reinterpret_cast<cudaStream_t>(stream)));
-  if (st == DSPARK_OK) ctx->last_launches = 1;
+  if (st == DSPARK_OK) ctx->last_launches = 2;
   return st;
 }
 

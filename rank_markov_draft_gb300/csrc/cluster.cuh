@@ -27,8 +27,14 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Store two floats at `p` (an address of this CTA's shared memory) in CTA `rank` of the cluster
-// and count their 8 bytes on that CTA's copy of the mbarrier `bar`.
+// Store two floats at `p` (an address of this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ void st_cluster_f32x2(void* p, uint32_t rank, float a, float b) {
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(there), "f"(a), "f"(b) : "memory");
+}
+
+// The same by an asynchronous store, and count their 8 bytes on that CTA's copy of the mbarrier `bar`.
 __device__ __forceinline__ void st_async_f32x2(void* p, uint64_t* bar, uint32_t rank, float a,
                                                float b) {
   uint32_t there, bar_there;
