@@ -46,6 +46,9 @@ struct dspark_ctx {
   int32_t* d_l_prev = nullptr;           // [B_max * K_max] predecessors of the drafted tokens
   float* d_l_offq2 = nullptr;            // [B_max * K_max] log2 q offsets
   float* d_topk_part_v = nullptr;
+  // draws from given probabilities: segment sums, CTAs done (zero between calls)
+  float* d_vp_sums = nullptr;
+  int* d_vp_count = nullptr;             // [kVpMaxRequests]
   dspark::ScanSpan* d_spans = nullptr;   // [kScanSpanCount] segments of long recurrences
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
   uint32_t epoch = 0;                    // last key epoch used
@@ -492,6 +495,9 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
             cudaMalloc(&ctx->d_v_count, sizeof(int) * B_max) == cudaSuccess &&
             cudaMalloc(&ctx->d_l_prev, sizeof(int32_t) * rows) == cudaSuccess &&
             cudaMalloc(&ctx->d_l_offq2, sizeof(float) * rows) == cudaSuccess &&
+            cudaMalloc(&ctx->d_vp_sums, sizeof(float) * 2 * 8 * dspark::kVpMaxCtas *
+                                            dspark::kVpMaxRequests) == cudaSuccess &&
+            cudaMalloc(&ctx->d_vp_count, sizeof(int) * dspark::kVpMaxRequests) == cudaSuccess &&
             cudaMalloc(&ctx->d_spans, sizeof(dspark::ScanSpan) * dspark::kScanSpanCount) ==
                 cudaSuccess;
   ok = ok && cudaMemset(ctx->d_status, 0, sizeof(int)) == cudaSuccess &&
@@ -500,6 +506,7 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
            cudaSuccess &&
        cudaMemset(ctx->d_v_fail, 0, sizeof(unsigned long long) * B_max) == cudaSuccess &&
        cudaMemset(ctx->d_v_count, 0, sizeof(int) * B_max) == cudaSuccess &&
+       cudaMemset(ctx->d_vp_count, 0, sizeof(int) * dspark::kVpMaxRequests) == cudaSuccess &&
        cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
     dspark_ctx_destroy(ctx);
@@ -531,6 +538,8 @@ int dspark_ctx_destroy(dspark_ctx* ctx) {
   cudaFree(ctx->d_l_prev);
   cudaFree(ctx->d_l_offq2);
   cudaFree(ctx->d_topk_part_v);
+  cudaFree(ctx->d_vp_sums);
+  cudaFree(ctx->d_vp_count);
   cudaFree(ctx->d_spans);
   delete ctx;
   return DSPARK_OK;
@@ -547,7 +556,9 @@ int dspark_ctx_reset(dspark_ctx* ctx, dspark_stream_t stream) {
                             s) == cudaSuccess &&
             cudaMemsetAsync(ctx->d_v_fail, 0, sizeof(unsigned long long) * ctx->B_max, s) ==
                 cudaSuccess &&
-            cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess;
+            cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess &&
+            cudaMemsetAsync(ctx->d_vp_count, 0, sizeof(int) * dspark::kVpMaxRequests, s) ==
+                cudaSuccess;
   if (!ok) return DSPARK_ERR_CUDA;
   ctx->bar_counter = 0;
   ctx->epoch = 0;
@@ -1004,9 +1015,10 @@ int dspark_verify_probs(dspark_ctx* ctx, const float* P, const float* Q, const i
   a.next_token = next_token;
   a.accept_prob = accept_prob;
   a.status = ctx->d_status;
-  st = cuda_status(dspark::launch_verify_probs(a, reinterpret_cast<cudaStream_t>(stream)));
-  if (st == DSPARK_OK) ctx->last_launches = 2;
-  return st;
+  a.sums = ctx->d_vp_sums;
+  a.count = ctx->d_vp_count;
+  return cuda_status(dspark::launch_verify_probs(a, &ctx->last_launches,
+                                                 reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,

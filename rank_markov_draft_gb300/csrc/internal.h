@@ -243,8 +243,12 @@ struct VerifyProbsArgs {
   int32_t* next_token;      // [B]
   float* accept_prob;       // [B, K] or null
   int* status;
+  float* sums;              // context scratch: [kVpMaxRequests][128 segments] x (hi, lo)
+  int* count;               // [kVpMaxRequests] CTAs done, zero between calls
 };
-cudaError_t launch_verify_probs(const VerifyProbsArgs& a, cudaStream_t stream);
+constexpr int kVpMaxRequests = 1024;  // of one launch
+constexpr int kVpMaxCtas = 16;        // of a request
+cudaError_t launch_verify_probs(const VerifyProbsArgs& a, int* launches, cudaStream_t stream);
 
 // ---- distillation from a teacher's top logits (distill.cu)
 constexpr int kMaxTeacher = 256;  // teacher tokens (and draft candidates) a row

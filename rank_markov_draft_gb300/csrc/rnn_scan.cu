@@ -90,18 +90,6 @@ __device__ __forceinline__ void gates(float z0, float z1, float& a0, float& a1, 
   a1 = z1 >= 0.f ? y1 : l1;
 }
 
-// Asynchronous copy of 16 or 4 bytes, zeros where `on` is false.
-__device__ __forceinline__ void copy_16(void* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(on ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy_4(void* dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(on ? 4 : 0)
-               : "memory");
-}
-
 // Spans.  kDrops in A: a reset inside, so the value before is dropped (a product that has merely
 // underflowed keeps an infinity or NaN).
 constexpr float kDrops = -1.f;
@@ -471,14 +459,15 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
         if (full) {
 #pragma unroll
           for (int j = 0; j < kSteps; j += 4)
-            copy_16(to + (at + j) * 32, src + static_cast<int64_t>(j) * ld, true);
+            cp_async_16_zfill(to + (at + j) * 32, src + static_cast<int64_t>(j) * ld, 16);
         } else {
 #pragma unroll
           for (int j = 0; j < kSteps; j += 4) {
             const int64_t t = t0 + j + sub;
             const bool on = inp && t0 >= 0 && t < p.L && (st.shift == 0 || t > 0);
-            copy_16(to + (at + j) * 32,
-                    on ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p), on);
+            cp_async_16_zfill(to + (at + j) * 32,
+                              on ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p),
+                              on ? 16 : 0);
           }
         }
       }
@@ -497,8 +486,9 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
         if (sizeof(T) * kVec == 4) {
 #pragma unroll 4
           for (int j = 0; j < kSteps; ++j)
-            copy_4(dst + (at + j) * 32 + lane,
-                   on(j) ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p), on(j));
+            cp_async_4_zfill(dst + (at + j) * 32 + lane,
+                             on(j) ? src + static_cast<int64_t>(j) * ld : static_cast<const T*>(st.p),
+                             on(j) ? 4 : 0);
         } else {  // single bf16 channels: no asynchronous copy is that small
           uint32_t v[kSteps];
 #pragma unroll
@@ -512,7 +502,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
     if (kWalk && u.pos == pos_begin && D::first(p) != nullptr)
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
-        copy_4(dst + kWords + lane * kVec + i, D::first(p) + (in ? q + i : 0), in);
+        cp_async_4_zfill(dst + kWords + lane * kVec + i, D::first(p) + (in ? q + i : 0), in ? 4 : 0);
     cp_async_commit();
     if (kReset) {
       const uint8_t* src = p.reset + static_cast<int64_t>(n) * p.L + t0;
@@ -577,7 +567,7 @@ __global__ void __launch_bounds__((Dir<T, kVec>::kWarps * 32), 2)
   for (int turn = 0; cur.block >= 0; ++turn) {
     fetch(far, stage == 0 ? kStages - 1 : stage - 1, flags[kStages - 1]);
     far = after(far);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    cp_async_wait_group<kStages - 1>();
     __syncwarp();
     const uint32_t* in = words(stage) + lane;
     const int64_t t0 = start(cur), left = p.L - t0;

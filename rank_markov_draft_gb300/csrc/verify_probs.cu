@@ -15,15 +15,18 @@
 // sums of a warp's end in it took more of the kernel than its reads.)
 //
 // One small launch makes the tests of every position.  The draw's reads one row (two with a
-// dense draft) of the vocabulary once and starts while the tests are made.  A request is a
-// cluster of CTAs whose warps take consecutive segments of the row, each read as it comes; the
-// segments' sums go to every CTA of the cluster, the CTA that holds the segment where the sum
-// passes u R reads that one segment (16 KB at most, still in L2) again, in order.
+// dense draft) of the vocabulary once and starts while the tests are made.  A request's row is
+// cut into segments, one a warp of its CTAs; a thread's next reads are always on their way to
+// shared memory while it adds up the ones that have come.  The CTA of a request that ends last
+// joins the segments' sums, in order, and reads the one segment where the sum passes u R again.
+// (Clusters, which could exchange the sums through shared memory, left SMs empty: with four CTAs
+// a request the draw took 41 us where 128 x 152k dense rows take 32 now.)
 
+#include <algorithm>
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
-#include "cluster.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
 #include "sm103.cuh"
@@ -33,9 +36,12 @@ namespace {
 
 constexpr int kVpThreads = 256;
 constexpr int kVpWarps = kVpThreads / 32;
-constexpr int kVpGroup = 128;              // tokens a warp reads at a time
-constexpr int kVpSegment = 32 * kVpGroup;  // of a warp at most
-constexpr int kVpMaxCtas = 8;
+constexpr int kVpSegments = kVpWarps * kVpMaxCtas;  // of a request at most
+constexpr int kVpGroup = 128;                       // tokens a warp adds up at a time
+constexpr int kVpMaxGroups = 16;                    // of a segment (V <= 2^18)
+constexpr int kVpSlot = 2 * kVpGroup;               // tokens of a ring's slot
+constexpr int kVpRing = 3;                          // slots in shared memory, one worked on
+static_assert(kVpSegments * kVpMaxGroups * kVpGroup >= 1 << 18 && kVpSegments == 128, "");
 
 // s + e = a + b exactly (Knuth's two-sum), two at a time
 __device__ __forceinline__ void two_sum(F2 a, F2 b, F2& s, F2& e) {
@@ -81,27 +87,52 @@ __device__ __forceinline__ Pair warp_running(Pair x, int lane) {
   return x;
 }
 
+__device__ __forceinline__ Pair warp_sum(Pair x, int lane) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const Pair y = shfl_xor(x, off);
+    x = lane & off ? y + x : x + y;  // (the same on both sides)
+  }
+  return x;
+}
+// The first lane with mass whose running sum passes `want`; where rounding leaves none, the last
+// with mass (-1: none has).
+__device__ __forceinline__ int first_past(Pair x, Pair run, Pair want) {
+  const unsigned mass = __ballot_sync(0xFFFFFFFFu, x.hi > 0.f);
+  const unsigned past = __ballot_sync(0xFFFFFFFFu, run > want) & mass;
+  return past != 0u ? __ffs(past) - 1 : 31 - __clz(mass);
+}
+
 // Running sums of weights, two at a time.
 struct Sum {
   F2 hi = F2(0.f, 0.f), lo = F2(0.f, 0.f);
-  __device__ __forceinline__ void add(F2 x, F2 err) {
-    F2 s, e;
-    two_sum(hi, x, s, e);
+  // max(0, p - q) as max(p, q) - q, with its rounding error (p - (p - q)) - q (exact where
+  // p >= q >= 0).  An entry that is not finite ends in a sum that is not; kCareful gives such
+  // entries no mass instead.
+  template <bool kCareful>
+  __device__ __forceinline__ void add_residual(float p0, float p1, float q0, float q1) {
+    const F2 p(fmaxf(p0, q0), fmaxf(p1, q1)), q(q0, q1), neg(-1.f, -1.f);
+    F2 d = fma2(q, neg, p), err = fma2(q, neg, fma2(d, neg, p)), s, e;
+    if (kCareful) {
+      float d0, d1, e0, e1;
+      d.get(d0, d1);
+      err.get(e0, e1);
+      const bool m0 = has_mass(d0), m1 = has_mass(d1);
+      d = F2(m0 ? d0 : 0.f, m1 ? d1 : 0.f);
+      err = F2(m0 ? e0 : 0.f, m1 ? e1 : 0.f);
+    }
+    two_sum(hi, d, s, e);
     hi = s;
     lo = lo + (e + err);
   }
-  // max(0, p - q) with its rounding error; entries that are not finite have no mass
-  __device__ __forceinline__ void add_residual(float p0, float p1, float q0, float q1) {
-    F2 d, e;
-    two_sum(F2(p0, p1), F2(-q0, -q1), d, e);
-    float d0, d1, e0, e1;
-    d.get(d0, d1);
-    e.get(e0, e1);
-    const bool m0 = has_mass(d0), m1 = has_mass(d1);
-    add(F2(m0 ? d0 : 0.f, m1 ? d1 : 0.f), F2(m0 ? e0 : 0.f, m1 ? e1 : 0.f));
-  }
+  template <bool kCareful>
   __device__ __forceinline__ void add_mass(float p0, float p1) {
-    add(F2(has_mass(p0) ? p0 : 0.f, has_mass(p1) ? p1 : 0.f), F2(0.f, 0.f));
+    p0 = kCareful ? (has_mass(p0) ? p0 : 0.f) : fmaxf(p0, 0.f);
+    p1 = kCareful ? (has_mass(p1) ? p1 : 0.f) : fmaxf(p1, 0.f);
+    F2 s, e;
+    two_sum(hi, F2(p0, p1), s, e);
+    hi = s;
+    lo = lo + e;
   }
   __device__ __forceinline__ Pair value() const {
     float a, b, c, d;
@@ -113,8 +144,8 @@ struct Sum {
 
 // One weight.
 __device__ __forceinline__ Pair weight_of(float p, float q) {
-  const float d = p - q, bb = d - p;
-  return has_mass(d) ? Pair{d, (p - (d - bb)) - (q + bb)} : Pair{0.f, 0.f};
+  const float d = p - q;
+  return has_mass(d) ? Pair{d, (p - d) - q} : Pair{0.f, 0.f};
 }
 
 // u q < p of the exact product (its low part is lost where the product is near the denormals)
@@ -173,41 +204,36 @@ __global__ void __launch_bounds__(128) verify_tests_kernel(const VerifyProbsArgs
 
 // kWide: rows start on 16-byte boundaries (V and the addresses a multiple of 4 tokens).
 template <bool kWide>
-__global__ void __launch_bounds__(kVpThreads, 5) verify_draw_kernel(const VerifyProbsArgs a) {
-  const uint32_t rank = cluster_cta_rank(), ctas = cluster_cta_count();
-  const int b = blockIdx.x / ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(kVpThreads, 4)
+    verify_draw_kernel(const VerifyProbsArgs a, const int ctas, const int seg) {
+  const int b = blockIdx.x / ctas, cta = blockIdx.x - b * ctas;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int V = a.V, K = a.K, m = a.m;
+  extern __shared__ float4 s_ring4[];  // [warp][kVpRing][p, q][kVpSlot]
+  float* s_ring = reinterpret_cast<float*>(s_ring4);
   __shared__ int s_id[kMaxTeacher];
   __shared__ float s_q[kMaxTeacher];
-  __shared__ alignas(8) Pair s_sum[2][kVpMaxCtas * kVpWarps];  // of the cluster's segments
-  __shared__ Pair s_warp[kVpWarps];
-  __shared__ int s_last[kVpWarps], s_hit[kVpWarps];
+  __shared__ Pair s_sum[kVpSegments];    // the last CTA's: of every segment
+  __shared__ Pair s_group[kVpMaxGroups];  // and of the groups of the one it looks into
+  __shared__ int s_done;
 
   const int len = a.ell == nullptr ? K : min(max(__ldg(a.ell + b), 0), K);
   griddep_wait();
   const int j = __ldcg(a.n_acc + b);
 
-  // ---- the row of the draw, and this warp's segment of it
+  // ---- the row of the draw, and its segments
   const size_t o = static_cast<size_t>(b) * K + j;
   const float* prow = a.P + (static_cast<size_t>(b) * (K + 1) + j) * V;
   const float* qrow = m == 0 && j < len ? a.Q + o * V : nullptr;
   const bool sparse = m > 0 && j < len;
-  const int segments = static_cast<int>(ctas) * kVpWarps;
-  const int seg = ((V + segments - 1) / segments + 3) & ~3;
+  const int segments = ctas * kVpWarps;
   const auto begin = [&](int s) { return min(V, s * seg); };
-  const int v0 = begin(rank * kVpWarps + warp), v1 = begin(rank * kVpWarps + warp + 1);
-  uint32_t listed = 0u;  // groups of this warp's segment that hold a candidate
   if (sparse) {
     for (int i = tid; i < m; i += kVpThreads) {
       s_id[i] = __ldg(a.cand + o * m + i);
       s_q[i] = __ldg(a.cand_q + o * m + i);
     }
     __syncthreads();
-    for (int i = lane; i < m; i += 32) {
-      const int id = s_id[i];
-      if (id >= v0 && id < v1) listed |= 1u << ((id - v0) / kVpGroup);
-    }
-    listed = __reduce_or_sync(0xFFFFFFFFu, listed);
   }
   // q of the tokens v, v + step, ... among the candidates (from the last, so that the first of
   // equal ids stays)
@@ -224,192 +250,263 @@ __global__ void __launch_bounds__(kVpThreads, 5) verify_draw_kernel(const Verify
     }
   };
 
-  bool left = j < len;  // weights are what the draft left over, else the target's row
-  int owner = -1, pass = 0;
-  Pair want{0.f, 0.f};
-  for (;; ++pass) {
+  // One pass over segment `s` by this warp; its sum.  Two rows or the target's alone.
+  float* const ring = s_ring + warp * kVpRing * 2 * kVpSlot + (kWide ? 4 * lane : lane);
+  const auto stream = [&](auto two, auto careful, bool lists, int s) {
+    constexpr bool kTwo = decltype(two)::value, kCareful = decltype(careful)::value;
+    const int v0 = begin(s), v1 = begin(s + 1);
+    uint32_t listed = 0u;  // groups of the segment that hold a candidate
+    if (!kTwo && lists) {
+      for (int i = lane; i < m; i += 32) {
+        const int id = s_id[i];
+        if (id >= v0 && id < v1) listed |= 1u << ((id - v0) / kVpGroup);
+      }
+      listed = __reduce_or_sync(0xFFFFFFFFu, listed);
+    }
+    const int slots = (v1 - v0 + kVpSlot - 1) / kVpSlot;
+    const float* pp = prow + v0 + (kWide ? 4 * lane : lane);  // this lane's next copies
+    const float* qq = kTwo ? qrow + v0 + (kWide ? 4 * lane : lane) : nullptr;
+    int rest = v1 - v0 - (kWide ? 4 * lane : lane), to = 0, from = 0;
+    // a lane copies the tokens it will read (zeros past the segment's end)
+    const auto fetch = [&](int k) {
+      if (k < slots) {
+        float* dst = ring + to * 2 * kVpSlot;
+        constexpr int kPieces = kWide ? 2 : 8, kStep = kWide ? kVpGroup : 32;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int n = rest - i * kStep;  // tokens left from this piece on
+          if (kWide) {
+            const int bytes = n >= 4 ? 16 : (n > 0 ? 4 * n : 0);
+            cp_async_16_zfill(dst + i * kStep, n > 0 ? pp + i * kStep : prow, bytes);
+            if (kTwo) cp_async_16_zfill(dst + kVpSlot + i * kStep, n > 0 ? qq + i * kStep : qrow, bytes);
+          } else {
+            cp_async_4_zfill(dst + i * kStep, n > 0 ? pp + i * kStep : prow, n > 0 ? 4 : 0);
+            if (kTwo)
+              cp_async_4_zfill(dst + kVpSlot + i * kStep, n > 0 ? qq + i * kStep : qrow, n > 0 ? 4 : 0);
+          }
+        }
+        pp += kVpSlot;
+        if (kTwo) qq += kVpSlot;
+        rest -= kVpSlot;
+        to = to == kVpRing - 1 ? 0 : to + 1;
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kVpRing - 1; ++k) fetch(k);
     Sum sum;
-    const auto group = [&](int v, int g, const float (&p)[4], float (&q)[4]) {
-      if (left && qrow == nullptr && (listed >> g & 1u)) candidates(v, kWide ? 1 : 32, q);
-      if (left && (qrow != nullptr || (listed >> g & 1u))) {
-        sum.add_residual(p[0], p[1], q[0], q[1]);
-        sum.add_residual(p[2], p[3], q[2], q[3]);
-      } else {
-        sum.add_mass(p[0], p[1]);
-        sum.add_mass(p[2], p[3]);
-      }
-    };
-    const auto load = [&](const float* row, int v, float (&x)[4]) {
-      if (kWide) {
-        const float4 f = __ldcs(reinterpret_cast<const float4*>(row + v));
-        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-      } else {
+    for (int k = 0; k < slots; ++k) {
+      fetch(k + kVpRing - 1);
+      cp_async_wait_group<kVpRing - 1>();
+      const float* src = ring + from * 2 * kVpSlot;
+      from = from == kVpRing - 1 ? 0 : from + 1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __ldcs(row + v + 32 * i);
-      }
-    };
-    const int lane0 = kWide ? 4 * lane : lane;
-    const bool two = left && qrow != nullptr;
-    int v = v0, g = 0;
-    // two groups at a time (four loads of a lane in flight); the row's last group by itself
-    for (; v + 2 * kVpGroup <= v1; v += 2 * kVpGroup, g += 2) {
-      float p0[4], p1[4], q0[4], q1[4];
-      load(prow, v + lane0, p0);
-      load(prow, v + kVpGroup + lane0, p1);
-      if (two) {
-        load(qrow, v + lane0, q0);
-        load(qrow, v + kVpGroup + lane0, q1);
-      }
-      group(v + lane0, g, p0, q0);
-      group(v + kVpGroup + lane0, g + 1, p1, q1);
-    }
-    for (; v < v1; v += kVpGroup, ++g) {
-      float p[4], q[4];
+      for (int h = 0; h < 2; ++h) {
+        float p[4], q[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = v + lane0 + (kWide ? i : 32 * i);
-        p[i] = t < v1 ? __ldcs(prow + t) : 0.f;
-        q[i] = t < v1 && two ? __ldcs(qrow + t) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const int at = h * kVpGroup + (kWide ? i : 32 * i);
+          p[i] = src[at];
+          if (kTwo) q[i] = src[kVpSlot + at];
+        }
+        const int g = 2 * k + h;
+        if (kTwo) {
+          sum.add_residual<kCareful>(p[0], p[1], q[0], q[1]);
+          sum.add_residual<kCareful>(p[2], p[3], q[2], q[3]);
+        } else if (listed >> g & 1u) {
+          candidates(v0 + g * kVpGroup + (kWide ? 4 * lane : lane), kWide ? 1 : 32, q);
+          sum.add_residual<true>(p[0], p[1], q[0], q[1]);
+          sum.add_residual<true>(p[2], p[3], q[2], q[3]);
+        } else {
+          sum.add_mass<kCareful>(p[0], p[1]);
+          sum.add_mass<kCareful>(p[2], p[3]);
+        }
       }
-      group(v + lane0, g, p, q);
     }
-    // every CTA of the cluster gets every segment's sum
-    Pair mine = sum.value();
+    return warp_sum(sum.value(), lane);
+  };
+  using No = std::false_type;
+  using Yes = std::true_type;
+
+  bool left = j < len;  // weights are what the draft left over, else the target's row
+  {
+    const int s = cta * kVpWarps + warp;
+    const Pair mine = left && qrow != nullptr ? stream(Yes{}, No{}, false, s)
+                                              : stream(No{}, No{}, left, s);
+    if (lane == 0) reinterpret_cast<float2*>(a.sums)[b * kVpSegments + s] = make_float2(mine.hi, mine.lo);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    s_done = atomicAdd(a.count + b, 1);
+  }
+  __syncthreads();
+  if (s_done != ctas - 1) return;
+
+  // ---- the request's last CTA: the total, the segment where the running sum passes u total
+  __threadfence();
+  if (tid == 0) a.count[b] = 0;  // as it was found
+  if (tid < segments) {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(a.sums) + b * kVpSegments + tid);
+    s_sum[tid] = Pair{x.x, x.y};
+  }
+  const Pair none{0.f, 0.f};
+  Pair want = none;
+  int owner = -1;
+  for (bool careful = false;;) {
+    __syncthreads();
+    // (each warp for itself: lane's four segments, then the lanes)
+    Pair x[4], of_lane = none;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const Pair other = shfl_xor(mine, off);
-      mine = lane & off ? other + mine : mine + other;  // (the same on both sides)
+    for (int i = 0; i < 4; ++i) {
+      x[i] = 4 * lane + i < segments ? s_sum[4 * lane + i] : none;
+      of_lane = of_lane + x[i];
     }
-    if (lane < static_cast<int>(ctas))
-      st_cluster_f32x2(&s_sum[pass][rank * kVpWarps + warp], lane, mine.hi, mine.lo);
-    if (ctas > 1)
-      cluster_barrier();
-    else
-      __syncthreads();
-    // total, and the segment where the running sum passes u total (each warp for itself)
-    const Pair none{0.f, 0.f};
-    const Pair lo = lane < segments ? s_sum[pass][lane] : none;
-    const Pair run_lo = warp_running(lo, lane);
-    Pair total = shfl(run_lo, 31), hi = none, run_hi = none;
-    if (segments > 32) {
-      hi = lane + 32 < segments ? s_sum[pass][lane + 32] : none;
-      run_hi = total + warp_running(hi, lane);
-      total = shfl(run_hi, 31);
-    }
-    if (total.hi > 0.f) {
+    const Pair run = warp_running(of_lane, lane), total = shfl(run, 31);
+    if (total.hi > 0.f && total.hi <= FLT_MAX) {
       want = __ldg(a.u_draw + b) * total;
-      const unsigned m_lo = __ballot_sync(0xFFFFFFFFu, lo.hi > 0.f);
-      const unsigned m_hi = __ballot_sync(0xFFFFFFFFu, hi.hi > 0.f);
-      const unsigned p_lo = __ballot_sync(0xFFFFFFFFu, run_lo > want) & m_lo;
-      const unsigned p_hi = __ballot_sync(0xFFFFFFFFu, run_hi > want) & m_hi;
-      // (rounding may leave no segment past it: then the last with mass)
-      owner = p_lo != 0u ? __ffs(p_lo) - 1
-              : p_hi != 0u ? 31 + __ffs(p_hi)
-              : m_hi != 0u ? 63 - __clz(m_hi) : 31 - __clz(m_lo);
-      if (owner > 0) {  // what the owner's own sum has to pass: less the sum before it
-        const Pair before = owner <= 32 ? shfl(run_lo, owner - 1) : shfl(run_hi, owner - 33);
-        want = want - before;
+      const int at = first_past(of_lane, run, want);
+      if (at > 0) want = want - shfl(run, at - 1);
+      Pair acc = none;
+      int found = -1, last = -1;
+      for (int i = 0; i < 4; ++i) {
+        const Pair y = shfl(x[i], at);
+        if (y.hi > 0.f) {
+          last = i;
+          if (found < 0 && acc + y > want) found = i;
+          if (found < 0) acc = acc + y;
+        }
       }
+      if (found < 0) {  // (rounding) the last with mass: what is before it goes off again
+        found = last;
+        acc = none;
+        for (int i = 0; i < found; ++i) acc = acc + shfl(x[i], at);
+      }
+      want = want - acc;
+      owner = 4 * at + found;
       break;
     }
-    if (!left) break;
-    left = false;  // nothing left over: the target's own row
+    // rare: an infinity or NaN among the probabilities (they get no mass), or nothing left over
+    // (then the target's own row); this CTA reads the row once more by itself
+    if (total.hi == 0.f) {
+      if (!left) break;
+      left = false;
+    } else if (careful) {
+      break;
+    }
+    careful = true;
+    __syncthreads();
+    for (int s = warp; s < segments; s += kVpWarps) {
+      const Pair sum = left && qrow != nullptr ? stream(Yes{}, Yes{}, false, s)
+                                               : stream(No{}, Yes{}, left, s);
+      if (lane == 0) s_sum[s] = sum;
+    }
   }
   if (owner < 0) {
-    if (rank == 0 && tid == 0) a.next_token[b] = -1;
+    if (tid == 0) a.next_token[b] = -1;
     return;
   }
-  if (owner / kVpWarps != static_cast<int>(rank)) return;
 
-  // ---- the owner's segment in order: 16 tokens a thread, then the thread that passes `want`
-  constexpr int kPer = kVpSegment / kVpThreads;
-  const int t0 = begin(owner) + tid * kPer, t1 = min(t0 + kPer, begin(owner + 1));
-  uint32_t of_list = 0u;  // which of them are candidates
-  if (left && sparse)
-    for (int i = 0; i < m; ++i) {
-      const int e = s_id[i] - t0;
-      if (e >= 0 && e < kPer) of_list |= 1u << e;
+  // ---- that segment: the sums of its groups (two a warp), the group's token
+  const int w0 = begin(owner), w1 = begin(owner + 1);
+  const bool two = left && qrow != nullptr;
+  constexpr int kEach = kVpMaxGroups / kVpWarps;
+  Pair x[kEach][4], each[kEach];  // this lane's four tokens of a group, in order
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int t = w0 + (warp + k * kVpWarps) * kVpGroup + 4 * lane;
+    float p[4], q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = t + i < w1 ? __ldg(prow + t + i) : 0.f;
+      q[i] = two && t + i < w1 ? __ldg(qrow + t + i) : 0.f;
     }
-  const auto weight = [&](int e) {
-    if (t0 + e >= t1) return Pair{0.f, 0.f};
-    float q = 0.f;
-    if (left && qrow != nullptr) q = __ldg(qrow + t0 + e);
-    if (of_list >> e & 1u)
-      for (int i = m - 1; i >= 0; --i)
-        if (s_id[i] == t0 + e) q = s_q[i];
-    return weight_of(__ldg(prow + t0 + e), q);
-  };
-  Pair sum{0.f, 0.f};
-  int last = -1;
-#pragma unroll 8
-  for (int e = 0; e < kPer; ++e) {
-    const Pair x = weight(e);
-    if (x.hi > 0.f) last = t0 + e;
-    sum = sum + x;
+    if (left && sparse && t < w1) candidates(t, 1, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[k][i] = weight_of(p[i], q[i]);
   }
-  const Pair run = warp_running(sum, lane);
-  last = __reduce_max_sync(0xFFFFFFFFu, last);
-  if (lane == 31) s_warp[warp] = run;
-  if (lane == 0) s_last[warp] = last;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    each[k] = (x[k][0] + x[k][1]) + (x[k][2] + x[k][3]);
+    const Pair y = warp_sum(each[k], lane);
+    if (lane == 0) s_group[warp + k * kVpWarps] = y;
+  }
   __syncthreads();
-  Pair base{0.f, 0.f};
-  int end = -1;
-  for (int k = 0; k < kVpWarps; ++k) {
-    if (k < warp) base = base + s_warp[k];
-    end = max(end, s_last[k]);
-  }
-  const unsigned hits = __ballot_sync(0xFFFFFFFFu, sum.hi > 0.f && base + run > want);
-  if (lane == 0) s_hit[warp] = hits != 0u ? 1 : 0;
-  __syncthreads();
-  int first = -1;
-  for (int k = kVpWarps - 1; k >= 0; --k)
-    if (s_hit[k] != 0) first = k;
-  if (first < 0) {  // rounding: the segment's last token with mass
-    if (tid == 0) a.next_token[b] = end;
-    return;
-  }
-  if (warp != first) return;
-  const int chosen = __ffs(hits) - 1;
-  const Pair before = base + shfl(run, max(chosen - 1, 0));
-  if (lane != chosen) return;
-  Pair acc = chosen > 0 ? before : base;
-  int found = -1;
-  for (int e = 0; e < kPer && found < 0; ++e) {
-    const Pair x = weight(e);
-    if (!(x.hi > 0.f)) continue;
-    acc = acc + x;
-    last = t0 + e;  // (of this thread's: the one if rounding leaves none past it)
-    if (acc > want) found = t0 + e;
-  }
-  a.next_token[b] = found >= 0 ? found : last;
+  const Pair of_group = lane < kVpMaxGroups ? s_group[lane] : none;
+  Pair run = warp_running(of_group, lane);
+  const int g = first_past(of_group, run, want);
+  if (g % kVpWarps != warp) return;
+  if (g > 0) want = want - shfl(run, g - 1);
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (g / kVpWarps == k) {
+      run = warp_running(each[k], lane);
+      const int chosen = first_past(each[k], run, want);
+      Pair acc = shfl(run, max(chosen - 1, 0));
+      if (lane != chosen) return;
+      if (chosen == 0) acc = none;
+      int found = -1, last = -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc = acc + x[k][i];
+        if (!(x[k][i].hi > 0.f)) continue;
+        last = i;
+        if (found < 0 && acc > want) found = i;
+      }
+      a.next_token[b] = w0 + g * kVpGroup + 4 * lane + (found >= 0 ? found : last);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_verify_probs(const VerifyProbsArgs& a, cudaStream_t stream) {
-  // One CTA per 32768 tokens at least (a warp's segment fits its 32 group bits); more CTAs than
-  // that while rows are long, so that a request's reads are spread: a CTA per 16384 tokens.
-  int ctas = 1;
-  while (ctas < kVpMaxCtas && a.V > ctas * 16384) ctas *= 2;
-  const bool wide = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.P) % 16 == 0 &&
-                    reinterpret_cast<uintptr_t>(a.Q) % 16 == 0;
-  verify_tests_kernel<<<(a.B + 3) / 4, 128, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ctas);
-  cfg.blockDim = dim3(kVpThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, wide ? verify_draw_kernel<true> : verify_draw_kernel<false>, a);
+cudaError_t launch_verify_probs(const VerifyProbsArgs& all, int* launches, cudaStream_t stream) {
+  // A CTA per 9728 tokens (a warp's segment at the full vocabulary, 1216, is a ring and a half),
+  // 16 at most; every segment a multiple of 4 tokens.
+  const int ctas = std::min(kVpMaxCtas, (all.V + 9727) / 9728), segments = ctas * kVpWarps;
+  const int seg = ((all.V + segments - 1) / segments + 3) & ~3;
+  const bool wide = all.V % 4 == 0 && reinterpret_cast<uintptr_t>(all.P) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(all.Q) % 16 == 0;
+  const auto fn = wide ? verify_draw_kernel<true> : verify_draw_kernel<false>;
+  constexpr int kSmem = kVpWarps * kVpRing * 2 * kVpSlot * 4;
+  static const cudaError_t once[2] = {
+      cudaFuncSetAttribute(verify_draw_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmem),
+      cudaFuncSetAttribute(verify_draw_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmem)};
+  if (once[wide ? 1 : 0] != cudaSuccess) return once[wide ? 1 : 0];
+  for (int b0 = 0; b0 < all.B; b0 += kVpMaxRequests) {  // as many as there is scratch for
+    VerifyProbsArgs a = all;
+    const size_t rows = static_cast<size_t>(b0) * a.K;
+    a.B = std::min(kVpMaxRequests, all.B - b0);
+    a.P += (rows + b0) * a.V;
+    if (a.m == 0) a.Q += rows * a.V;
+    if (a.m > 0) a.cand += rows * a.m;
+    if (a.m > 0) a.cand_q += rows * a.m;
+    a.tokens += rows;
+    a.u_accept += rows;
+    a.u_draw += b0;
+    if (a.ell != nullptr) a.ell += b0;
+    a.n_acc += b0;
+    a.next_token += b0;
+    if (a.accept_prob != nullptr) a.accept_prob += rows;
+    verify_tests_kernel<<<(a.B + 3) / 4, 128, 0, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ctas);
+    cfg.blockDim = dim3(kVpThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fn, a, ctas, seg);
+    if (e != cudaSuccess) return e;
+    *launches += 2;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace dspark
