@@ -46,6 +46,7 @@ struct dspark_ctx {
   int32_t* d_l_prev = nullptr;           // [B_max * K_max] predecessors of the drafted tokens
   float* d_l_offq2 = nullptr;            // [B_max * K_max] log2 q offsets
   float* d_topk_part_v = nullptr;
+  uint8_t* d_distill = nullptr;          // [kLongScratchBytes] distillation of long rows, zero at first
   // draws from given probabilities: segment sums, CTAs done (zero between calls)
   float* d_vp_sums = nullptr;
   int* d_vp_count = nullptr;             // [kVpMaxRequests]
@@ -495,6 +496,7 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
             cudaMalloc(&ctx->d_v_count, sizeof(int) * B_max) == cudaSuccess &&
             cudaMalloc(&ctx->d_l_prev, sizeof(int32_t) * rows) == cudaSuccess &&
             cudaMalloc(&ctx->d_l_offq2, sizeof(float) * rows) == cudaSuccess &&
+            cudaMalloc(&ctx->d_distill, dspark::kLongScratchBytes) == cudaSuccess &&
             cudaMalloc(&ctx->d_vp_sums, sizeof(float) * 2 * 8 * dspark::kVpMaxCtas *
                                             dspark::kVpMaxRequests) == cudaSuccess &&
             cudaMalloc(&ctx->d_vp_count, sizeof(int) * dspark::kVpMaxRequests) == cudaSuccess &&
@@ -506,6 +508,7 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
            cudaSuccess &&
        cudaMemset(ctx->d_v_fail, 0, sizeof(unsigned long long) * B_max) == cudaSuccess &&
        cudaMemset(ctx->d_v_count, 0, sizeof(int) * B_max) == cudaSuccess &&
+       cudaMemset(ctx->d_distill, 0, dspark::kLongScratchBytes) == cudaSuccess &&
        cudaMemset(ctx->d_vp_count, 0, sizeof(int) * dspark::kVpMaxRequests) == cudaSuccess &&
        cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
@@ -538,6 +541,7 @@ int dspark_ctx_destroy(dspark_ctx* ctx) {
   cudaFree(ctx->d_l_prev);
   cudaFree(ctx->d_l_offq2);
   cudaFree(ctx->d_topk_part_v);
+  cudaFree(ctx->d_distill);
   cudaFree(ctx->d_vp_sums);
   cudaFree(ctx->d_vp_count);
   cudaFree(ctx->d_spans);
@@ -557,6 +561,7 @@ int dspark_ctx_reset(dspark_ctx* ctx, dspark_stream_t stream) {
             cudaMemsetAsync(ctx->d_v_fail, 0, sizeof(unsigned long long) * ctx->B_max, s) ==
                 cudaSuccess &&
             cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess &&
+            cudaMemsetAsync(ctx->d_distill, 0, dspark::kLongScratchBytes, s) == cudaSuccess &&
             cudaMemsetAsync(ctx->d_vp_count, 0, sizeof(int) * dspark::kVpMaxRequests, s) ==
                 cudaSuccess;
   if (!ok) return DSPARK_ERR_CUDA;
@@ -1067,9 +1072,17 @@ int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
   a.grad = grad;
   a.status = ctx->d_status;
   a.timeout_ns = ctx->timeout_ns;
-  st = cuda_status(dspark::launch_distill(a, ctx->num_sms, reinterpret_cast<cudaStream_t>(stream)));
-  if (st == DSPARK_OK) ctx->last_launches = 1;
-  return st;
+  uint8_t* p = ctx->d_distill;
+  a.scratch.part = reinterpret_cast<unsigned long long*>(p);
+  p += static_cast<size_t>(dspark::kLongMaxRows) * dspark::kLongMaxSegments * 16;
+  a.scratch.coef = reinterpret_cast<unsigned long long*>(p);
+  p += static_cast<size_t>(dspark::kLongMaxRows) * 3 * 8;
+  a.scratch.list = reinterpret_cast<int2*>(p);
+  p += static_cast<size_t>(dspark::kLongMaxRows) * dspark::kMaxTeacher * 8;
+  a.scratch.epoch = reinterpret_cast<uint32_t*>(p);
+  a.scratch.done = a.scratch.epoch + 1;
+  return cuda_status(dspark::launch_distill(a, ctx->num_sms, &ctx->last_launches,
+                                            reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dspark_rnn_scan(dspark_ctx* ctx, const void* za, const void* zg, const void* e, int dtype,

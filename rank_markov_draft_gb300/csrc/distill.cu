@@ -13,24 +13,25 @@
 // with o the softmax over the other tokens alone.  The outside sum is taken without the
 // teacher's tokens rather than as 1 - sum_i q_i, which cancels when the student agrees.
 //
-// The gradient needs the row's sum, so a kernel that streams reads every logit twice.  Here a
-// row is spread over the registers of a cluster of CTAs (about 40 KB a CTA): one read of the
-// logits, all loads of a thread in flight at once, one exchange of (maximum, sum) through the
-// cluster's shared memory, one write.  Clusters walk over the rows.  In each CTA one warp holds
-// no part of the row: it prepares the next row's teacher slots (which count, the student's
-// logits there, a bit map of their tokens) while the others stream the current one, so the
-// dependent loads of the slots hide behind the row's.  The map tells the streaming warps which
-// registers to overwrite with -inf, so neither pass tests for the teacher's tokens; their own
-// gradients are written last, over the zeros.
+// The gradient needs the row's sum, so every logit is wanted twice, and is to come from memory
+// once.  Two kernels:
+//   Short rows (40 KB at most) lie in the registers of one CTA between the passes.  CTAs walk
+//   over the rows; one warp of each holds no part of the row and prepares the next row's teacher
+//   slots (which count, the student's logits there, a bit map of their tokens) while the others
+//   stream the current one, so the dependent loads of the slots hide behind the row's.
+//   Long rows are cut into segments of about 10 KB, one a warp.  A warp sums its segment of one
+//   round, then writes the gradient of its segment of the round before, which it reads again: the
+//   two readings are one round (23 MB over the chip) apart, so the second comes from L2.  Each
+//   segment's (maximum, sum) goes through memory to the row's service warp (one in each CTA),
+//   which joins them, finishes the row and publishes the coefficients; a round of work lies
+//   between, so nobody waits for long.  The launch is cooperative: all of its CTAs run.
+// In both the teacher's tokens are left out of the outside sum by overwriting them with -inf on
+// chip, and their own gradients are written last, over what the stream wrote there.
 
 #include <algorithm>
 #include <cstdint>
-#include <map>
-#include <mutex>
-#include <tuple>
 #include <cuda_bf16.h>
 
-#include "cluster.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
 #include "rowscan.cuh"
@@ -186,10 +187,10 @@ struct SlotSmem {  // double-buffered by the row's turn
   int out_id[2][kMaxTeacher];                  // the last row's slots, for their gradients
   float out_g[2][kMaxTeacher];
   float2 part[2][32];                          // (maximum, sum) of each streaming warp
-  alignas(8) float2 cta[2][8];                 // of each CTA of the cluster
-  alignas(8) uint64_t bar[2];                  // counts the bytes of cta[]
   float coef[3];                               // outside coefficient, any of it at all, maximum
 };
+
+constexpr int kShortVectors = 288 * 9;  // of the longest row that lies in one CTA's registers
 
 // Where a row lies: `off` elements past a 16-byte boundary, so `head` elements before the first
 // aligned vector, `body` vectors, `tail` elements after the last.
@@ -205,6 +206,73 @@ struct RowSpan {
   }
 };
 
+// The sides of a row's teacher slots: maxima and sums of the logits that count.
+struct SlotStats {
+  float t_top, s_top, sum_t, sum_s;
+};
+
+// A row's events (one warp).  t, s, g: the slots' teacher and student logits, their gradients on
+// return (t and s are overwritten with p and q).
+struct RowEvents {
+  float rho, top, total, q_rest, sgn_r, S, kl, tv;
+  float m_out, sum_out, wt;
+  bool any;  // both sides have a distribution
+
+  __device__ __forceinline__ RowEvents(const DistillArgs& a, float c, int64_t n, float w,
+                                       const SlotStats& r, float m, float sum, float* t, float* s,
+                                       float* g, int lane)
+      : m_out(m), sum_out(sum) {
+    rho = a.teacher_rest != nullptr ? fminf(fmaxf(__ldg(a.teacher_rest + n), 0.f), 1.f) : 0.f;
+    top = max_nan(m_out, r.s_top);
+    any = !(r.t_top == -INFINITY || top == -INFINITY);
+    const float out_part = sum_out * part_scale(m_out, top, c);
+    total = r.sum_s * part_scale(r.s_top, top, c) + out_part;
+    const float inv = 1.f / total, p_scale = (1.f - rho) / r.sum_t;
+    const float ratio = log2f(total) - log2f(r.sum_t) + log2f(1.f - rho);
+    q_rest = out_part * inv;
+    sgn_r = sign_of(q_rest, rho);
+    S = kl = tv = 0.f;
+    for (int j = lane; j < a.k; j += 32) {
+      const float tj = t[j], sj = s[j];
+      // an empty slot has neither side (a teacher's logit of -inf keeps its student's)
+      const float xj = (tj - r.t_top) * c, yj = (sj - top) * c;
+      const float p = tj == -INFINITY ? 0.f : exp2f(xj) * p_scale;
+      const float q = sj == -INFINITY ? 0.f : exp2f(yj) * inv;
+      float sg = sign_of(q, p);
+      if (fabsf(q - p) < 1e-5f * p)
+        sg = sign64(sj, top, total, tj, r.t_top, r.sum_t, rho, a.temperature);
+      S += sg * q;
+      tv += fabsf(p - q);
+      if (p > 0.f) kl += p * (xj - yj + ratio);
+      t[j] = p;
+      s[j] = q;
+      g[j] = sg;
+    }
+    S = warp_sum(S) + sgn_r * q_rest;
+    wt = w / a.temperature;
+  }
+  // of any other token v: coefficient * 2^((x_v - m_out) c), where there is one
+  __device__ __forceinline__ float coefficient(const DistillArgs& a) const {
+    return wt * (a.alpha_kl * (q_rest - rho) + 0.5f * a.alpha_tv * (sgn_r - S) * q_rest) / sum_out;
+  }
+  __device__ __forceinline__ bool outside() const { return any && sum_out != 0.f; }
+  __device__ __forceinline__ float slot(const DistillArgs& a, float p, float q, float sg) const {
+    return any ? wt * (a.alpha_kl * (q - p) + 0.5f * a.alpha_tv * (sg - S) * q) : 0.f;
+  }
+  __device__ __forceinline__ void write_loss(const DistillArgs& a, float c, int64_t n, float w,
+                                             int lane) {
+    kl = warp_sum(kl);
+    tv = 0.5f * (warp_sum(tv) + fabsf(rho - q_rest));
+    if (rho > 0.f)
+      kl += rho * (log2f(rho) - log2f(sum_out) - (m_out - top) * c + log2f(total));
+    if (lane == 0) {
+      a.loss[n] = any ? w * ((a.alpha_kl != 0.f ? a.alpha_kl * kl * kLn2 : 0.f) + a.alpha_tv * tv)
+                      : 0.f;
+      if (a.tv != nullptr) a.tv[n] = any ? tv : 0.f;
+    }
+  }
+};
+
 template <typename T>
 struct SlotWarp {
   const DistillArgs& a;
@@ -212,12 +280,10 @@ struct SlotWarp {
   SlotSmem& sm;
   uint32_t* map[2];
   int lane;
-  bool first;  // rank 0 of the cluster
 
-  struct Row {
+  struct Row : SlotStats {
     int64_t n;
     float w;
-    float t_top, s_top, sum_t, sum_s;
   };
 
   __device__ __forceinline__ float weight(int64_t n) const {
@@ -253,7 +319,7 @@ struct SlotWarp {
     for (int j = lane; j < a.k; j += 32) {
       int id = sm.next_id[j];
       if (id >= a.V) {
-        if (first) record_error(a.status, kStatusDeviceOob);
+        record_error(a.status, kStatusDeviceOob);
         id = -1;
       }
       const int pos = id < 0 ? -1 : id + off;
@@ -295,90 +361,42 @@ struct SlotWarp {
     r.sum_s = warp_sum(r.sum_s);
     __syncwarp();
   }
-  // Loss and coefficients from the outside's (maximum, sum).
+  // Coefficients and loss from the outside's (maximum, sum).
   __device__ __forceinline__ void finish(const Row& r, int b, float m_out, float sum_out,
                                          int threads) {
-    const bool grads = a.grad != nullptr;
-    const float rho = a.teacher_rest != nullptr
-                          ? fminf(fmaxf(__ldg(a.teacher_rest + r.n), 0.f), 1.f)
-                          : 0.f;
-    const float top = max_nan(m_out, r.s_top);
-    const bool any = !(r.t_top == -INFINITY || top == -INFINITY);
-    const float out_part = sum_out * part_scale(m_out, top, c);
-    const float total = r.sum_s * part_scale(r.s_top, top, c) + out_part;
-    const float inv = 1.f / total, p_scale = (1.f - rho) / r.sum_t;
-    const float ratio = log2f(total) - log2f(r.sum_t) + log2f(1.f - rho);
-    const float q_rest = out_part * inv, sgn_r = sign_of(q_rest, rho);
-    float S = 0.f, kl = 0.f, tv = 0.f;
-    for (int j = lane; j < a.k; j += 32) {
-      const float tj = sm.t[b][j], sj = sm.s[b][j];
-      // an empty slot has neither side (a teacher's logit of -inf keeps its student's)
-      const float xj = (tj - r.t_top) * c, yj = (sj - top) * c;
-      const float p = tj == -INFINITY ? 0.f : exp2f(xj) * p_scale;
-      const float q = sj == -INFINITY ? 0.f : exp2f(yj) * inv;
-      float sg = sign_of(q, p);
-      if (fabsf(q - p) < 1e-5f * p)
-        sg = sign64(sj, top, total, tj, r.t_top, r.sum_t, rho, a.temperature);
-      S += sg * q;
-      tv += fabsf(p - q);
-      if (p > 0.f) kl += p * (xj - yj + ratio);
-      sm.t[b][j] = p;
-      sm.s[b][j] = q;
-      sm.out_g[b][j] = sg;
-    }
-    if (grads) {
-      S = warp_sum(S) + sgn_r * q_rest;
-      const float wt = r.w / a.temperature;
+    RowEvents ev(a, c, r.n, r.w, r, m_out, sum_out, sm.t[b], sm.s[b], sm.out_g[b], lane);
+    if (a.grad != nullptr) {
       if (lane == 0) {
-        sm.coef[0] = wt *
-                     (a.alpha_kl * (q_rest - rho) + 0.5f * a.alpha_tv * (sgn_r - S) * q_rest) /
-                     sum_out;
-        sm.coef[1] = any && sum_out != 0.f ? 1.f : 0.f;
+        sm.coef[0] = ev.coefficient(a);
+        sm.coef[1] = ev.outside() ? 1.f : 0.f;
         sm.coef[2] = m_out;
       }
       __syncwarp();
       bar_arrive(kBarCoef, threads);
       for (int j = lane; j < a.k; j += 32) {
-        const float p = sm.t[b][j], q = sm.s[b][j], sg = sm.out_g[b][j];
-        sm.out_g[b][j] =
-            any ? wt * (a.alpha_kl * (q - p) + 0.5f * a.alpha_tv * (sg - S) * q) : 0.f;
+        sm.out_g[b][j] = ev.slot(a, sm.t[b][j], sm.s[b][j], sm.out_g[b][j]);
         sm.out_id[b][j] = sm.id[b][j];
       }
     }
-    if (!first) return;
-    kl = warp_sum(kl);
-    tv = 0.5f * (warp_sum(tv) + fabsf(rho - q_rest));
-    if (rho > 0.f)
-      kl += rho * (log2f(rho) - log2f(sum_out) - (m_out - top) * c + log2f(total));
-    if (lane == 0) {
-      a.loss[r.n] =
-          any ? r.w * ((a.alpha_kl != 0.f ? a.alpha_kl * kl * kLn2 : 0.f) + a.alpha_tv * tv) : 0.f;
-      if (a.tv != nullptr) a.tv[r.n] = any ? tv : 0.f;
-    }
+    ev.write_loss(a, c, r.n, r.w, lane);
   }
-  // The gradients of a finished row's slots whose tokens this CTA holds, over the zeros that
-  // its streaming warps wrote there before they arrived at a barrier this warp has passed.
-  __device__ __forceinline__ void patch(int64_t n, int b, int v0, int cnt, bool edges,
-                                        const RowSpan<T>& sp) const {
+  // The gradients of a finished row's slots, over what the streaming warps wrote there before
+  // they arrived at a barrier that this warp has passed.
+  __device__ __forceinline__ void patch(int64_t n, int b) const {
     T* grad = static_cast<T*>(a.grad) + n * a.ld_grad;
     for (int j = lane; j < a.k; j += 32) {
       const int id = sm.out_id[b][j];
-      if (id < 0) continue;
-      const int e = id - sp.head;
-      const bool inner = e >= 0 && e < sp.body * Row16<T>::kVec;
-      const int v = e / Row16<T>::kVec - v0;
-      if (inner ? v >= 0 && v < cnt : edges) Row16<T>::put(grad + id, sm.out_g[b][j]);
+      if (id >= 0) Row16<T>::put(grad + id, sm.out_g[b][j]);
     }
   }
 };
 
-// A cluster walks over rows g, g + clusters, ...; CTA `rank` holds body vectors [v0, v0 + cnt)
-// of a row, vector i of a streaming thread at tid + i * (threads - 32); all but the last i are
-// full (the host picks the threads so).  The up to 14 elements outside the body are single elements of warp
-// 0's lanes in rank 0.
+// Short rows.  A CTA walks over rows; vector i of a streaming thread is the row's body vector
+// tid + i * (threads - 32); all but the last i are full (the host picks the threads so).  The up
+// to 14 elements outside the body are single elements of warp 0's lanes.
 template <typename T, int NV, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
-    distill_kernel(const DistillArgs a, const float c, const int map_words, const uint2 sel) {
+    distill_short_kernel(const DistillArgs a, const float c, const int map_words, const uint2 sel) {
   using R = Row16<T>;
   constexpr int kVec = R::kVec;
   const int nt = blockDim.x, row_threads = nt - 32, row_warps = row_threads / 32;
@@ -386,24 +404,14 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
   extern __shared__ uint32_t maps[];  // 2 x map_words
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_cta_rank(), ctas = cluster_cta_count();
-  const int64_t step = gridDim.x / ctas, n0 = blockIdx.x / ctas;
+  const int64_t step = gridDim.x, n0 = blockIdx.x;
   const bool grads = a.grad != nullptr;
-  const auto v_begin = [&](int body, int r) {
-    return static_cast<int>(static_cast<int64_t>(body) * r / static_cast<int>(ctas));
-  };
   for (int i = tid; i < 2 * map_words; i += nt) maps[i] = 0u;
   for (int i = tid; i < 2 * kMaxTeacher; i += nt) (&sm.pos[0][0])[i] = -1;
-  if (tid == 0) {
-    mbar_init(&sm.bar[0], 1);
-    mbar_init(&sm.bar[1], 1);
-    fence_mbar_init();
-  }
   __syncthreads();
-  if (ctas > 1) cluster_barrier();  // every CTA's mbarriers exist
 
   if (warp == row_warps) {  // ---------------------------------------------- the slot warp
-    SlotWarp<T> sw{a, c, sm, {maps, maps + map_words}, lane, rank == 0};
+    SlotWarp<T> sw{a, c, sm, {maps, maps + map_words}, lane};
     using Row = typename SlotWarp<T>::Row;
     Row cur = sw.next_live(n0, step), last;
     last.n = a.N;
@@ -431,34 +439,17 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
       }
       float m = warp_max(o.x);
       float sum = warp_sum(o.y * part_scale(o.x, m, c));
-      if (ctas > 1) {
-        if (lane == 0) mbar_arrive_expect_tx(&sm.bar[b], 8u * ctas);
-        if (lane < static_cast<int>(ctas)) st_async_f32x2(&sm.cta[b][rank], &sm.bar[b], lane, m, sum);
-        if (!mbar_wait_cluster(&sm.bar[b], (turn >> 1) & 1, a.timeout_ns) && lane == 0)
-          record_error(a.status, kStatusTimeout);
-        __syncwarp();
-        const float2 p = lane < static_cast<int>(ctas) ? sm.cta[b][lane] : make_float2(-INFINITY, 0.f);
-        m = warp_max(p.x);
-        sum = warp_sum(p.y * part_scale(p.x, m, c));
-      }
-      if (grads || rank == 0) sw.finish(cur, b, m, sum, nt);
-      if (grads && last.n < a.N) {  // (the streaming warps were done with it at kBarSums)
-        const RowSpan<T> sp(static_cast<const T*>(a.logits) + last.n * a.ld, a.V);
-        const int v0 = v_begin(sp.body, rank);
-        sw.patch(last.n, b ^ 1, v0, v_begin(sp.body, rank + 1) - v0, rank == 0, sp);
-      }
+      sw.finish(cur, b, m, sum, nt);
+      if (grads && last.n < a.N)  // (the streaming warps were done with it at kBarSums)
+        sw.patch(last.n, b ^ 1);
       last = cur;
       cur = nxt;
       nxt = after;
       if (grads && cur.n >= a.N) {
         bar_sync(kBarSums, nt);  // the streaming warps have written the last row
-        const RowSpan<T> sp(static_cast<const T*>(a.logits) + last.n * a.ld, a.V);
-        const int v0 = v_begin(sp.body, rank);
-        __syncwarp();
-        sw.patch(last.n, b, v0, v_begin(sp.body, rank + 1) - v0, rank == 0, sp);
+        sw.patch(last.n, b);
       }
     }
-    if (ctas > 1) cluster_barrier();  // no CTA leaves while another may still store into it
     return;
   }
 
@@ -472,13 +463,13 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     const T* row = static_cast<const T*>(a.logits) + n * a.ld;
     T* grad = grads ? static_cast<T*>(a.grad) + n * a.ld_grad : nullptr;
     const RowSpan<T> sp(row, a.V);
-    const int v0 = v_begin(sp.body, rank), cnt = v_begin(sp.body, rank + 1) - v0;
-    const uint4* src = reinterpret_cast<const uint4*>(row + sp.head) + v0 + tid;
-    T* dst = grad + sp.head + static_cast<int64_t>(v0 + tid) * kVec;
+    const int cnt = sp.body;
+    const uint4* src = reinterpret_cast<const uint4*>(row + sp.head) + tid;
+    T* dst = grad + sp.head + static_cast<int64_t>(tid) * kVec;
     const bool aligned = (reinterpret_cast<uintptr_t>(grad + sp.head) & 15u) == 0;
     // this thread's single element, if it has one
     int edge = -1;
-    if (rank == 0 && tid < 16) {
+    if (tid < 16) {
       if (tid < sp.head) edge = tid;
       if (tid >= 8 && tid - 8 < sp.tail) edge = a.V - sp.tail + tid - 8;
     }
@@ -492,7 +483,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
       }
     };
     if (w == 0.f) {  // neither read nor looked at
-      if (rank == 0 && tid == 0) {
+      if (tid == 0) {
         a.loss[n] = 0.f;
         if (a.tv != nullptr) a.tv[n] = 0.f;
       }
@@ -519,7 +510,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     bar_sync(kBarSlots + b, nt);
     // the teacher's tokens out
     {
-      const int p0 = v0 + tid + (sp.off > 0 ? 1 : 0);
+      const int p0 = tid + (sp.off > 0 ? 1 : 0);
       const uint8_t* bytes = reinterpret_cast<const uint8_t*>(map);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -591,96 +582,492 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     __syncwarp();
     bar_arrive(kBarSums, nt);
   }
-  if (ctas > 1) cluster_barrier();
 }
 
-// Clusters of this launch that the device holds at once (an SM takes kPerSm CTAs, but a cluster
-// has to fit one GPC); asked once for each shape a kernel is launched with.
-int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int ctas) {
-  static std::mutex lock;
-  static std::map<std::tuple<const void*, int, unsigned, size_t>, int> known;
-  const auto key = std::make_tuple(fn, ctas, cfg.blockDim.x, cfg.dynamicSmemBytes);
-  std::lock_guard<std::mutex> hold(lock);
-  const auto it = known.find(key);
-  if (it != known.end()) return it->second;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    n = 1;
+// ---- long rows
+constexpr int kLongWarps = 8;               // that stream, and one more for the service
+constexpr int kLongThreads = kLongWarps * 32 + 32;
+constexpr int kLongSlot = 64;               // vectors of a ring's slot
+constexpr int kLongRing = 6;                // slots in shared memory, one worked on
+constexpr int kLongSegment = 608;           // vectors of a segment, about
+constexpr int kHash = 2 * kMaxTeacher;
+
+// Values that pass between CTAs carry the launch's tag beside them in one 8-byte word, so a reader
+// that sees the tag sees the value.
+__device__ __forceinline__ void publish(unsigned long long* p, uint32_t tag, float x) {
+  *reinterpret_cast<volatile unsigned long long*>(p) =
+      static_cast<unsigned long long>(tag) << 32 | __float_as_uint(x);
+}
+// Wait for a word of this launch; false after `timeout_ns` or once *abort is set.
+__device__ __forceinline__ bool await(const unsigned long long* p, uint32_t tag, float& x,
+                                      uint64_t timeout_ns, volatile int* abort) {
+  uint64_t deadline = 0;
+  for (uint32_t spins = 1;; ++spins) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    if (static_cast<uint32_t>(v >> 32) == tag) {
+      x = __uint_as_float(static_cast<uint32_t>(v));
+      return true;
+    }
+    if ((spins & 31u) != 0u) continue;
+    if (*abort != 0) return false;
+    const uint64_t now = globaltimer_ns();
+    if (deadline == 0) {
+      deadline = now + timeout_ns;
+    } else if (now > deadline) {
+      *abort = 1;
+      return false;
+    }
   }
-  if (known.size() < 4096) known[key] = n;
-  return n;
+}
+
+struct LongSmem {
+  uint4 ring[kLongWarps][kLongRing][kLongSlot];
+  int2 list[kLongWarps][kMaxTeacher];  // a warp's segment's teacher tokens, and their gradients
+  // the service warp's row
+  int id[kMaxTeacher];
+  float t[kMaxTeacher], s[kMaxTeacher], g[kMaxTeacher];
+  int key[kHash], slot[kHash];  // tokens seen, and their first slots
+  int abort;
+};
+
+// One of the row's segments: body vectors [v0, v0 + cnt) in `slots` slots; the first segment's
+// warp has the elements outside the body as well.
+template <typename T>
+struct Segment {
+  int64_t n;
+  int index, v0, cnt, slots;
+  const T* row;
+  RowSpan<T> sp;
+  __device__ __forceinline__ Segment(const DistillArgs& a, int unit, int S)
+      : n(unit / S),
+        index(unit - static_cast<int>(n) * S),
+        row(static_cast<const T*>(a.logits) + n * a.ld),
+        sp(row, a.V) {
+    v0 = sp.body * index / S;
+    cnt = sp.body * (index + 1) / S - v0;
+    slots = (cnt + kLongSlot - 1) / kLongSlot;
+  }
+  // this lane's single element, -1: none
+  __device__ __forceinline__ int edge(int V, int lane) const {
+    if (index != 0) return -1;
+    if (lane < sp.head) return lane;
+    return lane >= 8 && lane - 8 < sp.tail ? V - sp.tail + lane - 8 : -1;
+  }
+  // whether token `id` lies in this segment, edges among them
+  __device__ __forceinline__ bool holds(int id) const {
+    const int e = id - sp.head - v0 * Row16<T>::kVec;
+    const bool body = id >= sp.head && id < sp.head + sp.body * Row16<T>::kVec;
+    return body ? e >= 0 && e < cnt * Row16<T>::kVec : index == 0;
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads, 2)
+    distill_long_kernel(const DistillArgs a, const float c, const int S, const uint2 sel) {
+  using R = Row16<T>;
+  constexpr int kVec = R::kVec;
+  extern __shared__ uint4 s_raw[];
+  LongSmem& sm = *reinterpret_cast<LongSmem*>(s_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = a.k, V = a.V;
+  const bool grads = a.grad != nullptr;
+  const LongScratch& x = a.scratch;
+  const uint32_t tag = __ldcg(x.epoch) + 1u;
+  const auto weight = [&](int64_t n) { return a.row_weight != nullptr ? __ldg(a.row_weight + n) : 1.f; };
+  if (threadIdx.x == 0) sm.abort = 0;
+  __syncthreads();
+
+  if (warp == kLongWarps) {  // ------------------------------------------- the service warp
+    for (int i = lane; i < kHash; i += 32) {
+      sm.key[i] = -1;
+      sm.slot[i] = kMaxTeacher;
+    }
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+      const float w = weight(n);
+      if (w == 0.f) {
+        if (lane == 0) {
+          a.loss[n] = 0.f;
+          if (a.tv != nullptr) a.tv[n] = 0.f;
+        }
+        continue;
+      }
+      const T* row = static_cast<const T*>(a.logits) + n * a.ld;
+      // the slots that count: of equal tokens the first
+      __syncwarp();
+#pragma unroll 2
+      for (int j = lane; j < k; j += 32) {
+        int id = __ldg(a.teacher_ids + n * k + j);
+        const float t = __ldg(a.teacher_logits + n * k + j);
+        if (id >= V) {
+          record_error(a.status, kStatusDeviceOob);
+          id = -1;
+        }
+        sm.t[j] = t;
+        sm.id[j] = id;
+        sm.g[j] = id >= 0 ? R::one(row + id) : 0.f;
+        if (id >= 0) {
+          uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) >> 23;
+          for (;;) {
+            const int old = atomicCAS(&sm.key[h], -1, id);
+            if (old == -1 || old == id) break;
+            h = (h + 1u) & (kHash - 1);
+          }
+          atomicMin(&sm.slot[h], j);
+          sm.s[j] = __uint_as_float(h);
+        }
+      }
+      __syncwarp();
+      SlotStats st{-INFINITY, -INFINITY, 0.f, 0.f};
+      uint32_t counts = 0u;
+      for (int i = 0, j = lane; j < k; ++i, j += 32)
+        if (sm.id[j] >= 0 && sm.slot[__float_as_uint(sm.s[j])] == j) counts |= 1u << i;
+      __syncwarp();
+      for (int i = 0, j = lane; j < k; ++i, j += 32) {
+        if (sm.id[j] >= 0) {  // the table as it was
+          const uint32_t h = __float_as_uint(sm.s[j]);
+          sm.key[h] = -1;
+          sm.slot[h] = kMaxTeacher;
+        }
+        const bool in = counts >> i & 1u;
+        if (!in) sm.id[j] = -1;
+        sm.t[j] = in ? sm.t[j] : -INFINITY;
+        sm.s[j] = in ? sm.g[j] : -INFINITY;
+        st.t_top = max_nan(st.t_top, sm.t[j]);
+        st.s_top = max_nan(st.s_top, sm.s[j]);
+      }
+      st.t_top = warp_max(st.t_top);
+      st.s_top = warp_max(st.s_top);
+      for (int j = lane; j < k; j += 32) {
+        st.sum_t += part_scale(sm.t[j], st.t_top, c);
+        st.sum_s += part_scale(sm.s[j], st.s_top, c);
+      }
+      st.sum_t = warp_sum(st.sum_t);
+      st.sum_s = warp_sum(st.sum_s);
+      // the segments' sums
+      float m = -INFINITY, sum = 0.f;
+      bool ok = true;
+      for (int i = lane; i < S; i += 32) {
+        float pm = -INFINITY, ps = 0.f;
+        const unsigned long long* p = x.part + (n * kLongMaxSegments + i) * 2;
+        ok = ok && await(p, tag, pm, a.timeout_ns, &sm.abort) &&
+             await(p + 1, tag, ps, a.timeout_ns, &sm.abort);
+        const float top = max_nan(m, pm);
+        sum = sum * part_scale(m, top, c) + ps * part_scale(pm, top, c);
+        m = top;
+      }
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        if (lane == 0) record_error(a.status, kStatusTimeout);
+        break;
+      }
+      const float m_out = warp_max(m);
+      const float sum_out = warp_sum(sum * part_scale(m, m_out, c));
+      RowEvents ev(a, c, n, w, st, m_out, sum_out, sm.t, sm.s, sm.g, lane);
+      if (grads) {
+        for (int j = lane; j < k; j += 32)
+          x.list[n * kMaxTeacher + j] =
+              make_int2(sm.id[j], __float_as_int(ev.slot(a, sm.t[j], sm.s[j], sm.g[j])));
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence();
+          unsigned long long* p = x.coef + n * 3;
+          publish(p, tag, ev.coefficient(a));
+          publish(p + 1, tag, m_out);
+          publish(p + 2, tag, ev.outside() ? 1.f : 0.f);
+        }
+      }
+      ev.write_loss(a, c, n, w, lane);
+    }
+  } else {  // -------------------------------------------------------- the streaming warps
+    const int units = static_cast<int>(a.N) * S, step = gridDim.x * kLongWarps;
+    const int u0 = warp * gridDim.x + blockIdx.x;
+    const int own = u0 < units ? (units - u0 + step - 1) / step : 0;  // this warp's units
+    // Tasks in turn: the sums of unit 0; the sums of unit i + 1, the gradient of unit i; ...
+    const int tasks = grads ? 2 * own + 1 : own;
+    const auto unit_of = [&](int t) {  // -1: none
+      const int i = grads ? ((t & 1) != 0 ? (t + 1) / 2 : t / 2 - (t > 0 ? 1 : 0)) : t;
+      return i < own ? i : -1;
+    };
+    const auto is_sum = [&](int t) { return !grads || t == 0 || (t & 1) != 0; };
+    const auto live = [&](int i) { return weight((u0 + i * step) / S) != 0.f; };
+    uint4* ring = &sm.ring[warp][0][lane];
+    // the copies run ahead of the work by kLongRing - 1 slots, over the tasks' ends
+    int f_task = -1, f_left = 0, f_to = 0, f_vec = 0, f_cnt = 0;
+    const uint4* f_src = nullptr;
+    const auto fetch = [&]() {
+      while (f_left == 0 && f_task + 1 < tasks) {
+        ++f_task;
+        const int i = unit_of(f_task);
+        if (i < 0) continue;
+        if (!live(i)) continue;
+        const Segment<T> g(a, u0 + i * step, S);
+        f_left = g.slots;
+        f_cnt = g.cnt;
+        f_vec = lane;
+        f_src = reinterpret_cast<const uint4*>(g.row + g.sp.head) + g.v0;
+      }
+      if (f_left > 0) {
+        uint4* to = ring + f_to * kLongSlot;
+        if (f_vec < f_cnt) cp_async_16(to, f_src + f_vec);
+        if (f_vec + 32 < f_cnt) cp_async_16(to + 32, f_src + f_vec + 32);
+        f_vec += kLongSlot;
+        f_to = f_to == kLongRing - 1 ? 0 : f_to + 1;
+        --f_left;
+      }
+      cp_async_commit();
+    };
+    int from = 0;
+    const auto next_slot = [&](uint4& v0, uint4& v1) {
+      fetch();
+      cp_async_wait_group<kLongRing - 1>();
+      const uint4* at = ring + from * kLongSlot;
+      from = from == kLongRing - 1 ? 0 : from + 1;
+      v0 = at[0];
+      v1 = at[32];
+    };
+#pragma unroll 1
+    for (int i = 0; i < kLongRing - 1; ++i) fetch();
+
+    const F2 scale(c, c);
+    const uint4 nothing = make_uint4(R::kNegInf, R::kNegInf, R::kNegInf, R::kNegInf);
+    for (int task = 0; task < tasks; ++task) {
+      const int i = unit_of(task);
+      if (i < 0) continue;
+      const Segment<T> g(a, u0 + i * step, S);
+      const int edge = g.edge(V, lane);
+      if (is_sum(task)) {
+        if (!live(i)) continue;
+        // the teacher's tokens of this segment
+        float xe = edge >= 0 ? R::one(g.row + edge) : -INFINITY;
+        int listed_n = 0;
+        uint32_t listed = 0u;  // slots with any
+        for (int j0 = 0; j0 < k; j0 += 32) {
+          const int j = j0 + lane;
+          const int id = j < k ? __ldg(a.teacher_ids + g.n * k + j) : -1;
+          const bool in = id >= 0 && id < V && g.holds(id);
+          const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, in);
+          if (in) {
+            sm.list[warp][listed_n + __popc(lanes & ((1u << lane) - 1u))] = make_int2(id, 0);
+            const int e = id - g.sp.head - g.v0 * kVec;
+            if (e >= 0 && e < g.cnt * kVec) listed |= 1u << (e / (kLongSlot * kVec));
+          }
+          listed_n += __popc(lanes);
+        }
+        listed = __reduce_or_sync(0xFFFFFFFFu, listed);
+        __syncwarp();
+        if (g.index == 0 && g.sp.head + g.sp.tail > 0)
+          for (int j = 0; j < listed_n; ++j)
+            if (sm.list[warp][j].x == edge) xe = -INFINITY;
+        float m = xe, sum = xe == -INFINITY ? 0.f : 1.f;
+        if (!(xe == xe)) sum = xe;
+        for (int s = 0; s < g.slots; ++s) {
+          uint4 v[2];
+          next_slot(v[0], v[1]);
+          const int left = g.cnt - s * kLongSlot - lane;
+          if (left <= 0) v[0] = nothing;
+          if (left <= 32) v[1] = nothing;
+          if (listed >> s & 1u) {
+            uint32_t bits[2] = {0u, 0u};
+            for (int j = 0; j < listed_n; ++j) {
+              const int e = sm.list[warp][j].x - g.sp.head - (g.v0 + s * kLongSlot + lane) * kVec;
+              if (e >= 0 && e < kVec) bits[0] |= 1u << e;
+              if (e >= 32 * kVec && e < 33 * kVec) bits[1] |= 1u << (e - 32 * kVec);
+            }
+            if (bits[0] != 0u) R::mask(v[0], bits[0]);
+            if (bits[1] != 0u) R::mask(v[1], bits[1]);
+          }
+          const float top = max_nan(m, max_nan(R::max4(v[0]), R::max4(v[1])));
+          if (__any_sync(0xFFFFFFFFu, !(top == m))) {
+            sum *= part_scale(m, top, c);
+            m = top;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const F2 minus(-ref, -ref);
+          F2 acc(0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < R::kPairs; ++p) {
+              float y0, y1;
+              ((R::pair(v[h], p) + minus) * scale).get(y0, y1);
+              acc = acc + F2(ex2_approx(y0), ex2_approx(y1));
+            }
+          float y0, y1;
+          acc.get(y0, y1);
+          sum += y0 + y1;
+        }
+        const float top = warp_max(m);
+        sum = warp_sum(sum * part_scale(m, top, c));
+        if (lane == 0) {
+          unsigned long long* p = x.part + (g.n * kLongMaxSegments + g.index) * 2;
+          publish(p, tag, top);
+          publish(p + 1, tag, sum);
+        }
+        __syncwarp();  // (the list is read before the next task writes it)
+        continue;
+      }
+      // ---- the gradient of a segment
+      T* grad = static_cast<T*>(a.grad) + g.n * a.ld_grad;
+      T* dst = grad + g.sp.head + static_cast<int64_t>(g.v0 + lane) * kVec;
+      const bool aligned = (reinterpret_cast<uintptr_t>(grad + g.sp.head) & 15u) == 0;
+      const auto store = [&](int vec, const uint4& y) {
+        if (aligned) {
+          __stcs(reinterpret_cast<uint4*>(dst) + vec, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) dst[vec * kVec + e] = R::get(y, e);
+        }
+      };
+      float coef = 0.f, m_out = 0.f, any = 0.f;
+      if (live(i)) {
+        const unsigned long long* p = x.coef + g.n * 3;
+        const bool ok = await(p, tag, coef, a.timeout_ns, &sm.abort) &&
+                        await(p + 1, tag, m_out, a.timeout_ns, &sm.abort) &&
+                        await(p + 2, tag, any, a.timeout_ns, &sm.abort);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          if (lane == 0) record_error(a.status, kStatusTimeout);
+          break;
+        }
+      }
+      const uint4 zeros = make_uint4(0u, 0u, 0u, 0u);
+      if (!live(i)) {  // a row of no weight, neither read nor looked at
+        for (int v = 0; v + lane < g.cnt; v += 32) store(v, zeros);
+        if (edge >= 0) R::put(grad + edge, 0.f);
+        continue;
+      }
+      const float ref = m_out == -INFINITY ? 0.f : m_out;
+      const F2 minus(-ref, -ref), mul(coef, coef);
+      const float xe = edge >= 0 ? R::one(g.row + edge) : 0.f;
+      const auto write = [&](auto exp2_of) {
+        for (int s = 0; s < g.slots; ++s) {
+          uint4 v[2];
+          next_slot(v[0], v[1]);
+          const int left = g.cnt - s * kLongSlot - lane;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 y = zeros;
+            if (any != 0.f) {
+#pragma unroll
+              for (int p = 0; p < R::kPairs; ++p) {
+                float y0, y1;
+                ((R::pair_again(v[h], p, sel) + minus) * scale).get(y0, y1);
+                (F2(exp2_of(y0), exp2_of(y1)) * mul).get(y0, y1);
+                R::set_pair(y, p, y0, y1);
+              }
+            }
+            if (left > 32 * h) store(s * kLongSlot + 32 * h, y);
+          }
+        }
+        if (edge >= 0) R::put(grad + edge, any != 0.f ? exp2_of((xe - ref) * c) * coef : 0.f);
+      };
+      // (a coefficient above one brings results below 2^-126, which the fast exponential drops,
+      // back into range)
+      if (fabsf(coef) <= 1.f || any == 0.f)
+        write([](float y) { return ex2_approx(y); });
+      else
+        write([](float y) { return exp2f(y); });
+      // the teacher's tokens of this segment, over what is there now
+      __syncwarp();
+      for (int j = lane; j < k; j += 32) {
+        const int2 e = __ldcg(x.list + g.n * kMaxTeacher + j);
+        if (e.x >= 0 && g.holds(e.x)) R::put(grad + e.x, __int_as_float(e.y));
+      }
+    }
+    cp_async_wait_all();  // (copies are left under way only where a wait ran out)
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {  // the launch's last CTA moves the tag on
+    __threadfence();
+    if (atomicAdd(x.done, 1u) == gridDim.x - 1) {
+      *x.done = 0u;
+      *x.epoch = tag;
+    }
+  }
 }
 
 template <typename T, int NV, int kMaxThreads, int kPerSm>
-cudaError_t launch(const DistillArgs& a, int row_threads, int ctas, int num_sms,
-                   cudaStream_t stream) {
-  const auto fn = distill_kernel<T, NV, kMaxThreads, kPerSm>;
+cudaError_t launch_short(const DistillArgs& a, int row_threads, int num_sms, cudaStream_t stream) {
+  const auto fn = distill_short_kernel<T, NV, kMaxThreads, kPerSm>;
   const int map_words = (a.V + 2 * Row16<T>::kVec + 31) / 32;
-  // (the largest maps are above the default limit of dynamic shared memory)
-  static const cudaError_t once =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * 8200);
-  if (once != cudaSuccess) return once;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms / ctas * ctas));
-  cfg.blockDim = dim3(row_threads + 32);
-  cfg.dynamicSmemBytes = 2 * 4 * map_words;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const int64_t clusters =
-      std::min<int64_t>(a.N, resident_clusters(reinterpret_cast<const void*>(fn), cfg, ctas));
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * ctas));
   const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.temperature));
-  return cudaLaunchKernelEx(&cfg, fn, a, c, map_words, make_uint2(0x1044u, 0x3244u));
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>(a.N, static_cast<int64_t>(num_sms) * kPerSm));
+  fn<<<grid, row_threads + 32, 2 * 4 * map_words, stream>>>(a, c, map_words,
+                                                             make_uint2(0x1044u, 0x3244u));
+  return cudaGetLastError();
 }
 
-// Streaming threads that hold `most` vectors in NV each with all but the last NV full for a CTA
-// of `least` (0: none below `limit` do).
+// Streaming threads that hold `most` vectors in NV each with all but the last NV full where there
+// are `least` (0: none below `limit` do).
 int threads_for(int nv, int most, int least, int limit) {
   const int t = (((most + nv - 1) / nv + 31) / 32) * 32;
   return t <= limit && (nv - 1) * t <= least ? std::max(t, 32) : 0;
 }
 
 template <typename T>
-cudaError_t dispatch(const DistillArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStream_t stream) {
   constexpr int kVec = Row16<T>::kVec;
   // 16-byte vectors of a row: a row that starts off a boundary has one less
-  const int body = a.V / kVec, body_least = std::max(0, (a.V - kVec + 1) / kVec);
-  // The smallest cluster whose CTAs hold the row in 288 threads x 9 vectors (three CTAs an SM),
-  // up to 8 CTAs; more CTAs a row while the SMs would otherwise be empty.
-  int ctas = 1;
-  while (ctas < 8 && ((body + ctas - 1) / ctas > 288 * 9 ||
-                      (a.N * ctas * 2 <= num_sms && (body + ctas - 1) / ctas > 288)))
-    ctas *= 2;
-  const int most = std::max(1, (body + ctas - 1) / ctas), least = body_least / ctas;
+  const int body = all.V / kVec, body_least = std::max(0, (all.V - kVec + 1) / kVec);
+  const int most = std::max(1, body), least = body_least;
   int t;
-  if ((t = threads_for(1, most, least, 96))) return launch<T, 1, 128, 6>(a, t, ctas, num_sms, stream);
-  if ((t = threads_for(2, most, least, 96))) return launch<T, 2, 128, 6>(a, t, ctas, num_sms, stream);
-  if ((t = threads_for(3, most, least, 96))) return launch<T, 3, 128, 6>(a, t, ctas, num_sms, stream);
-  if ((t = threads_for(4, most, least, 288)))
-    return launch<T, 4, 320, 3>(a, t, ctas, num_sms, stream);
-  if ((t = threads_for(6, most, least, 288)))
-    return launch<T, 6, 320, 3>(a, t, ctas, num_sms, stream);
-  if ((t = threads_for(9, most, least, 288)))
-    return launch<T, 9, 320, 3>(a, t, ctas, num_sms, stream);
-  if ((t = threads_for(10, most, least, 480)))
-    return launch<T, 10, 512, 2>(a, t, ctas, num_sms, stream);
-  // (fp32 rows of more than 153600 logits)
-  t = threads_for(10, most, least, 992);
-  return launch<T, 10, 1024, 1>(a, t, ctas, num_sms, stream);
+  if (body <= kShortVectors) {
+    *launches += 1;
+    if ((t = threads_for(1, most, least, 96)))
+      return launch_short<T, 1, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(2, most, least, 96)))
+      return launch_short<T, 2, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(3, most, least, 96)))
+      return launch_short<T, 3, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(4, most, least, 288)))
+      return launch_short<T, 4, 320, 3>(all, t, num_sms, stream);
+    if ((t = threads_for(6, most, least, 288)))
+      return launch_short<T, 6, 320, 3>(all, t, num_sms, stream);
+    t = threads_for(9, most, least, 288);
+    return launch_short<T, 9, 320, 3>(all, t, num_sms, stream);
+  }
+  const auto fn = distill_long_kernel<T>;
+  static const cudaError_t once = cudaFuncSetAttribute(
+      fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(LongSmem)));
+  if (once != cudaSuccess) return once;
+  for (int64_t n0 = 0; n0 < all.N; n0 += kLongMaxRows) {  // as many rows as there is scratch for
+    DistillArgs a = all;
+    a.N = std::min<int64_t>(kLongMaxRows, all.N - n0);
+    a.logits = static_cast<const T*>(a.logits) + n0 * a.ld;
+    if (a.grad != nullptr) a.grad = static_cast<T*>(a.grad) + n0 * a.ld_grad;
+    a.teacher_ids += n0 * a.k;
+    a.teacher_logits += n0 * a.k;
+    if (a.teacher_rest != nullptr) a.teacher_rest += n0;
+    if (a.row_weight != nullptr) a.row_weight += n0;
+    a.loss += n0;
+    if (a.tv != nullptr) a.tv += n0;
+    // segments of about 10 KB, shorter ones (two slots at least) while there are warps without
+    int S = (body + kLongSegment - 1) / kLongSegment;
+    const int64_t warps = 2ll * num_sms * kLongWarps;
+    while (S < kLongMaxSegments && a.N * S < warps && body / (2 * S) >= 2 * kLongSlot) S *= 2;
+    S = std::min(S, kLongMaxSegments);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * num_sms);
+    cfg.blockDim = dim3(kLongThreads);
+    cfg.dynamicSmemBytes = sizeof(LongSmem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.temperature));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, c, S, make_uint2(0x1044u, 0x3244u));
+    if (e != cudaSuccess) return e;
+    *launches += 1;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_distill(const DistillArgs& a, int num_sms, cudaStream_t stream) {
-  return a.dtype == DSPARK_F32 ? dispatch<float>(a, num_sms, stream)
-                               : dispatch<uint16_t>(a, num_sms, stream);
+cudaError_t launch_distill(const DistillArgs& a, int num_sms, int* launches, cudaStream_t stream) {
+  return a.dtype == DSPARK_F32 ? dispatch<float>(a, num_sms, launches, stream)
+                               : dispatch<uint16_t>(a, num_sms, launches, stream);
 }
 
 }  // namespace dspark

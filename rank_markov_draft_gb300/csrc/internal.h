@@ -252,6 +252,16 @@ cudaError_t launch_verify_probs(const VerifyProbsArgs& a, int* launches, cudaStr
 
 // ---- distillation from a teacher's top logits (distill.cu)
 constexpr int kMaxTeacher = 256;  // teacher tokens (and draft candidates) a row
+constexpr int kLongMaxRows = 2048, kLongMaxSegments = 128;  // of one launch, of a row
+struct LongScratch {               // rows of several segments
+  unsigned long long* part;        // [kLongMaxRows][kLongMaxSegments][2] tagged maximum and sum
+  unsigned long long* coef;        // [kLongMaxRows][3] tagged coefficient, maximum, any outside
+  int2* list;                      // [kLongMaxRows][kMaxTeacher] tokens and their gradients
+  uint32_t* epoch;                 // tag of the last launch
+  uint32_t* done;                  // CTAs done, zero between launches
+};
+constexpr size_t kLongScratchBytes =
+    static_cast<size_t>(kLongMaxRows) * (kLongMaxSegments * 16 + 3 * 8 + kMaxTeacher * 8) + 8;
 struct DistillArgs {
   const void* logits;           // [N, V] of dtype, rows ld apart
   const int32_t* teacher_ids;   // [N, k]
@@ -266,8 +276,9 @@ struct DistillArgs {
   void* grad;                   // [N, V] of dtype, rows ld_grad apart, or null
   int* status;
   uint64_t timeout_ns;
+  LongScratch scratch;
 };
-cudaError_t launch_distill(const DistillArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_distill(const DistillArgs& a, int num_sms, int* launches, cudaStream_t stream);
 
 // ---- the RNN head's recurrence over given sequences (rnn_scan.cu)
 struct RnnScanArgs {
