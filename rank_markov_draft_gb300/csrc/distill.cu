@@ -19,9 +19,9 @@
 //   over the rows; one warp of each holds no part of the row and prepares the next row's teacher
 //   slots (which count, the student's logits there, a bit map of their tokens) while the others
 //   stream the current one, so the dependent loads of the slots hide behind the row's.
-//   Long rows are cut into segments of about 10 KB, one a warp.  A warp sums its segment of one
+//   Long rows are cut into segments of 10 to 16 KB, one a warp.  A warp sums its segment of one
 //   round, then writes the gradient of its segment of the round before, which it reads again: the
-//   two readings are one round (23 MB over the chip) apart, so the second comes from L2.  Each
+//   two readings are one round (23 to 38 MB over the chip) apart, so the second comes from L2.  Each
 //   segment's (maximum, sum) goes through memory to the row's service warp (one in each CTA),
 //   which joins them, finishes the row and publishes the coefficients; a round of work lies
 //   between, so nobody waits for long.  The launch is cooperative: all of its CTAs run.
@@ -80,6 +80,9 @@ struct Row16<float> {
     return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
                    max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
   }
+  static __device__ __forceinline__ float max8(const uint4& v, const uint4& w) {
+    return max_nan(max4(v), max4(w));
+  }
   static __device__ __forceinline__ F2 pair(const uint4& w, int i) {
     return i == 0 ? F2(__uint_as_float(w.x), __uint_as_float(w.y))
                   : F2(__uint_as_float(w.z), __uint_as_float(w.w));
@@ -119,6 +122,10 @@ struct Row16<uint16_t> {
   }
   static __device__ __forceinline__ float max4(const uint4& w) {
     const uint32_t m = max2(max2(w.x, w.y), max2(w.z, w.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ float max8(const uint4& v, const uint4& w) {
+    const uint32_t m = max2(max2(max2(v.x, v.y), max2(v.z, v.w)), max2(max2(w.x, w.y), max2(w.z, w.w)));
     return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
   static __device__ __forceinline__ uint32_t word(const uint4& w, int i) {
@@ -206,23 +213,25 @@ struct RowSpan {
   }
 };
 
-// The sides of a row's teacher slots: maxima and sums of the logits that count.
+// The sides of a row's teacher slots: maxima and sums of the logits that count, and the
+// teacher's rest.
 struct SlotStats {
-  float t_top, s_top, sum_t, sum_s;
+  float t_top, s_top, sum_t, sum_s, rho;
 };
+__device__ __forceinline__ float teacher_rest(const DistillArgs& a, int64_t n) {
+  return a.teacher_rest != nullptr ? fminf(fmaxf(__ldg(a.teacher_rest + n), 0.f), 1.f) : 0.f;
+}
 
 // A row's events (one warp).  t, s, g: the slots' teacher and student logits, their gradients on
 // return (t and s are overwritten with p and q).
 struct RowEvents {
-  float rho, top, total, q_rest, sgn_r, S, kl, tv;
-  float m_out, sum_out, wt;
+  float rho, m_out, sum_out, top, total, q_rest, sgn_r, S, kl, tv, wt;
   bool any;  // both sides have a distribution
 
-  __device__ __forceinline__ RowEvents(const DistillArgs& a, float c, int64_t n, float w,
+  __device__ __forceinline__ RowEvents(const DistillArgs& a, float c, float w,
                                        const SlotStats& r, float m, float sum, float* t, float* s,
                                        float* g, int lane)
-      : m_out(m), sum_out(sum) {
-    rho = a.teacher_rest != nullptr ? fminf(fmaxf(__ldg(a.teacher_rest + n), 0.f), 1.f) : 0.f;
+      : rho(r.rho), m_out(m), sum_out(sum) {
     top = max_nan(m_out, r.s_top);
     any = !(r.t_top == -INFINITY || top == -INFINITY);
     const float out_part = sum_out * part_scale(m_out, top, c);
@@ -339,6 +348,7 @@ struct SlotWarp {
       for (int i = 0; lane + 32 * i < a.k; ++i)
         if (drop >> i & 1u) sm.id[b][lane + 32 * i] = -1;
     }
+    r.rho = teacher_rest(a, r.n);
     r.t_top = r.s_top = -INFINITY;
 #pragma unroll 4
     for (int j = lane; j < a.k; j += 32) {
@@ -364,7 +374,7 @@ struct SlotWarp {
   // Coefficients and loss from the outside's (maximum, sum).
   __device__ __forceinline__ void finish(const Row& r, int b, float m_out, float sum_out,
                                          int threads) {
-    RowEvents ev(a, c, r.n, r.w, r, m_out, sum_out, sm.t[b], sm.s[b], sm.out_g[b], lane);
+    RowEvents ev(a, c, r.w, r, m_out, sum_out, sm.t[b], sm.s[b], sm.out_g[b], lane);
     if (a.grad != nullptr) {
       if (lane == 0) {
         sm.coef[0] = ev.coefficient(a);
@@ -587,9 +597,15 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
 // ---- long rows
 constexpr int kLongWarps = 8;               // that stream, and one more for the service
 constexpr int kLongThreads = kLongWarps * 32 + 32;
-constexpr int kLongSlot = 64;               // vectors of a ring's slot
-constexpr int kLongRing = 6;                // slots in shared memory, one worked on
-constexpr int kLongSegment = 608;           // vectors of a segment, about
+constexpr int kLongEach = 4;                // vectors of a lane in a ring's slot
+constexpr int kLongSlot = 32 * kLongEach;   // vectors of a slot
+constexpr int kLongRing = 4;                // slots in shared memory, one worked on
+// Vectors of a segment at most.  A segment costs a warp some 500 instructions beside its logits,
+// but what is summed in a round has to be in L2 when the gradient reads it: 2048 x 151936 rows
+// took, cut in 32 / 38 / 48 / 64 segments, fp32 522 / 515 / 527 / 468 us and, in 16 / 19 / 24 / 32,
+// bf16 283 / 272 / 286 / 290 us (loss alone 70 / 68 / - / 73 us).
+template <typename T>
+constexpr int kLongSegment = sizeof(T) == 4 ? 608 : 1024;
 constexpr int kHash = 2 * kMaxTeacher;
 
 // Values that pass between CTAs carry the launch's tag beside them in one 8-byte word, so a reader
@@ -598,17 +614,23 @@ __device__ __forceinline__ void publish(unsigned long long* p, uint32_t tag, flo
   *reinterpret_cast<volatile unsigned long long*>(p) =
       static_cast<unsigned long long>(tag) << 32 | __float_as_uint(x);
 }
-// Wait for a word of this launch; false after `timeout_ns` or once *abort is set.
-__device__ __forceinline__ bool await(const unsigned long long* p, uint32_t tag, float& x,
+// Wait for kN consecutive words of this launch, read together; false after `timeout_ns` or once
+// *abort is set.  Orders nothing that follows (see `acquire`).
+template <int kN>
+__device__ __forceinline__ bool await(const unsigned long long* p, uint32_t tag, float (&x)[kN],
                                       uint64_t timeout_ns, volatile int* abort) {
   uint64_t deadline = 0;
   for (uint32_t spins = 1;; ++spins) {
-    unsigned long long v;
-    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    if (static_cast<uint32_t>(v >> 32) == tag) {
-      x = __uint_as_float(static_cast<uint32_t>(v));
-      return true;
+    unsigned long long v[kN];
+    bool there = true;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = *const_cast<const volatile unsigned long long*>(p + i);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      there = there && static_cast<uint32_t>(v[i] >> 32) == tag;
+      x[i] = __uint_as_float(static_cast<uint32_t>(v[i]));
     }
+    if (there) return true;
     if ((spins & 31u) != 0u) continue;
     if (*abort != 0) return false;
     const uint64_t now = globaltimer_ns();
@@ -619,6 +641,10 @@ __device__ __forceinline__ bool await(const unsigned long long* p, uint32_t tag,
       return false;
     }
   }
+}
+// What the writer of a word seen by `await` wrote before it is visible after this.
+__device__ __forceinline__ void acquire(const unsigned long long* p) {
+  asm volatile("{\n\t.reg .b64 v;\n\tld.acquire.gpu.global.u64 v, [%0];\n\t}" ::"l"(p) : "memory");
 }
 
 struct LongSmem {
@@ -631,6 +657,13 @@ struct LongSmem {
   int abort;
 };
 
+// How rows are cut: S segments of `vecs` vectors (the last of a row has fewer); unit / S is the
+// high word of unit * magic (unit * S is far below 2^32).
+struct Split {
+  int S, vecs;
+  uint32_t magic;
+};
+
 // One of the row's segments: body vectors [v0, v0 + cnt) in `slots` slots; the first segment's
 // warp has the elements outside the body as well.
 template <typename T>
@@ -639,13 +672,13 @@ struct Segment {
   int index, v0, cnt, slots;
   const T* row;
   RowSpan<T> sp;
-  __device__ __forceinline__ Segment(const DistillArgs& a, int unit, int S)
-      : n(unit / S),
-        index(unit - static_cast<int>(n) * S),
+  __device__ __forceinline__ Segment(const DistillArgs& a, int unit, const Split& d)
+      : n(static_cast<int64_t>(static_cast<uint64_t>(unit) * d.magic >> 32)),
+        index(unit - static_cast<int>(n) * d.S),
+        v0(index * d.vecs),
         row(static_cast<const T*>(a.logits) + n * a.ld),
         sp(row, a.V) {
-    v0 = sp.body * index / S;
-    cnt = sp.body * (index + 1) / S - v0;
+    cnt = min(max(sp.body - v0, 0), d.vecs);
     slots = (cnt + kLongSlot - 1) / kLongSlot;
   }
   // this lane's single element, -1: none
@@ -664,7 +697,8 @@ struct Segment {
 
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads, 2)
-    distill_long_kernel(const DistillArgs a, const float c, const int S, const uint2 sel) {
+    distill_long_kernel(const DistillArgs a, const float c, const Split split) {
+  const int S = split.S;
   using R = Row16<T>;
   constexpr int kVec = R::kVec;
   extern __shared__ uint4 s_raw[];
@@ -717,7 +751,7 @@ __global__ void __launch_bounds__(kLongThreads, 2)
         }
       }
       __syncwarp();
-      SlotStats st{-INFINITY, -INFINITY, 0.f, 0.f};
+      SlotStats st{-INFINITY, -INFINITY, 0.f, 0.f, teacher_rest(a, n)};
       uint32_t counts = 0u;
       for (int i = 0, j = lane; j < k; ++i, j += 32)
         if (sm.id[j] >= 0 && sm.slot[__float_as_uint(sm.s[j])] == j) counts |= 1u << i;
@@ -747,12 +781,11 @@ __global__ void __launch_bounds__(kLongThreads, 2)
       float m = -INFINITY, sum = 0.f;
       bool ok = true;
       for (int i = lane; i < S; i += 32) {
-        float pm = -INFINITY, ps = 0.f;
+        float part[2] = {-INFINITY, 0.f};
         const unsigned long long* p = x.part + (n * kLongMaxSegments + i) * 2;
-        ok = ok && await(p, tag, pm, a.timeout_ns, &sm.abort) &&
-             await(p + 1, tag, ps, a.timeout_ns, &sm.abort);
-        const float top = max_nan(m, pm);
-        sum = sum * part_scale(m, top, c) + ps * part_scale(pm, top, c);
+        ok = ok && await(p, tag, part, a.timeout_ns, &sm.abort);
+        const float top = max_nan(m, part[0]);
+        sum = sum * part_scale(m, top, c) + part[1] * part_scale(part[0], top, c);
         m = top;
       }
       if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -761,7 +794,7 @@ __global__ void __launch_bounds__(kLongThreads, 2)
       }
       const float m_out = warp_max(m);
       const float sum_out = warp_sum(sum * part_scale(m, m_out, c));
-      RowEvents ev(a, c, n, w, st, m_out, sum_out, sm.t, sm.s, sm.g, lane);
+      RowEvents ev(a, c, w, st, m_out, sum_out, sm.t, sm.s, sm.g, lane);
       if (grads) {
         for (int j = lane; j < k; j += 32)
           x.list[n * kMaxTeacher + j] =
@@ -781,48 +814,62 @@ __global__ void __launch_bounds__(kLongThreads, 2)
     const int units = static_cast<int>(a.N) * S, step = gridDim.x * kLongWarps;
     const int u0 = warp * gridDim.x + blockIdx.x;
     const int own = u0 < units ? (units - u0 + step - 1) / step : 0;  // this warp's units
-    // Tasks in turn: the sums of unit 0; the sums of unit i + 1, the gradient of unit i; ...
-    const int tasks = grads ? 2 * own + 1 : own;
-    const auto unit_of = [&](int t) {  // -1: none
-      const int i = grads ? ((t & 1) != 0 ? (t + 1) / 2 : t / 2 - (t > 0 ? 1 : 0)) : t;
+    // Tasks in turn: sum(0), -, sum(1), gradient(0), sum(2), gradient(1), ...; -1: none.  (Units
+    // taken from a counter as warps get to them, which would even out rows of no weight, were no
+    // faster: the waits for the counter and the bookkeeping cost what they gave.)
+    const int tasks = grads ? 2 * (own + 1) : own;
+    const auto is_sum = [&](int t) { return !grads || (t & 1) == 0; };
+    const auto unit_of = [&](int t) {
+      const int i = grads ? (t >> 1) - (t & 1) : t;
       return i < own ? i : -1;
     };
-    const auto is_sum = [&](int t) { return !grads || t == 0 || (t & 1) != 0; };
-    const auto live = [&](int i) { return weight((u0 + i * step) / S) != 0.f; };
-    uint4* ring = &sm.ring[warp][0][lane];
+    const auto live = [&](int64_t n) { return weight(n) != 0.f; };
+    const uint32_t ring = smem_addr(&sm.ring[warp][0][lane]);
+    constexpr uint32_t kSlotBytes = kLongSlot * 16;
     // the copies run ahead of the work by kLongRing - 1 slots, over the tasks' ends
-    int f_task = -1, f_left = 0, f_to = 0, f_vec = 0, f_cnt = 0;
+    // the copies run ahead of the work by kLongRing - 1 slots, over the tasks' ends
+    int f_task = -1, f_left = 0, f_rest = 0;
+    uint32_t f_to = 0;
     const uint4* f_src = nullptr;
-    const auto fetch = [&]() {
+    const auto advance = [&]() {  // to the next task that has something to copy
       while (f_left == 0 && f_task + 1 < tasks) {
         ++f_task;
         const int i = unit_of(f_task);
         if (i < 0) continue;
-        if (!live(i)) continue;
-        const Segment<T> g(a, u0 + i * step, S);
+        const Segment<T> g(a, u0 + i * step, split);
+        if (!live(g.n)) continue;
         f_left = g.slots;
-        f_cnt = g.cnt;
-        f_vec = lane;
-        f_src = reinterpret_cast<const uint4*>(g.row + g.sp.head) + g.v0;
+        f_rest = g.cnt - lane;
+        f_src = reinterpret_cast<const uint4*>(g.row + g.sp.head) + g.v0 + lane;
       }
+    };
+    const auto fetch = [&]() {
+      if (f_left == 0) advance();
       if (f_left > 0) {
-        uint4* to = ring + f_to * kLongSlot;
-        if (f_vec < f_cnt) cp_async_16(to, f_src + f_vec);
-        if (f_vec + 32 < f_cnt) cp_async_16(to + 32, f_src + f_vec + 32);
-        f_vec += kLongSlot;
-        f_to = f_to == kLongRing - 1 ? 0 : f_to + 1;
+#pragma unroll
+        for (int e = 0; e < kLongEach; ++e)
+          if (f_rest > 32 * e)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + f_to + 512 * e),
+                         "l"(f_src + 32 * e)
+                         : "memory");
+        f_src += kLongSlot;
+        f_rest -= kLongSlot;
+        f_to = (f_to + kSlotBytes) & (kLongRing * kSlotBytes - 1);
         --f_left;
       }
       cp_async_commit();
     };
-    int from = 0;
-    const auto next_slot = [&](uint4& v0, uint4& v1) {
+    uint32_t from = 0;
+    const auto next_slot = [&](uint4 (&v)[kLongEach]) {
       fetch();
       cp_async_wait_group<kLongRing - 1>();
-      const uint4* at = ring + from * kLongSlot;
-      from = from == kLongRing - 1 ? 0 : from + 1;
-      v0 = at[0];
-      v1 = at[32];
+#pragma unroll
+      for (int e = 0; e < kLongEach; ++e)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[e].x), "=r"(v[e].y), "=r"(v[e].z), "=r"(v[e].w)
+                     : "r"(ring + from + 512 * e)
+                     : "memory");
+      from = (from + kSlotBytes) & (kLongRing * kSlotBytes - 1);
     };
 #pragma unroll 1
     for (int i = 0; i < kLongRing - 1; ++i) fetch();
@@ -832,10 +879,11 @@ __global__ void __launch_bounds__(kLongThreads, 2)
     for (int task = 0; task < tasks; ++task) {
       const int i = unit_of(task);
       if (i < 0) continue;
-      const Segment<T> g(a, u0 + i * step, S);
+      const Segment<T> g(a, u0 + i * step, split);
       const int edge = g.edge(V, lane);
-      if (is_sum(task)) {
-        if (!live(i)) continue;
+      const bool alive = live(g.n);
+      if (is_sum(task)) {  // ---- the sum of a segment
+        if (!alive) continue;
         // the teacher's tokens of this segment
         float xe = edge >= 0 ? R::one(g.row + edge) : -INFINITY;
         int listed_n = 0;
@@ -859,41 +907,55 @@ __global__ void __launch_bounds__(kLongThreads, 2)
             if (sm.list[warp][j].x == edge) xe = -INFINITY;
         float m = xe, sum = xe == -INFINITY ? 0.f : 1.f;
         if (!(xe == xe)) sum = xe;
-        for (int s = 0; s < g.slots; ++s) {
-          uint4 v[2];
-          next_slot(v[0], v[1]);
-          const int left = g.cnt - s * kLongSlot - lane;
-          if (left <= 0) v[0] = nothing;
-          if (left <= 32) v[1] = nothing;
+        const auto add = [&](uint4 (&v)[kLongEach], int s) {
           if (listed >> s & 1u) {
-            uint32_t bits[2] = {0u, 0u};
+            uint32_t bits[kLongEach] = {};
             for (int j = 0; j < listed_n; ++j) {
               const int e = sm.list[warp][j].x - g.sp.head - (g.v0 + s * kLongSlot + lane) * kVec;
-              if (e >= 0 && e < kVec) bits[0] |= 1u << e;
-              if (e >= 32 * kVec && e < 33 * kVec) bits[1] |= 1u << (e - 32 * kVec);
+#pragma unroll
+              for (int h = 0; h < kLongEach; ++h)
+                if (e >= 32 * h * kVec && e < (32 * h + 1) * kVec) bits[h] |= 1u << (e - 32 * h * kVec);
             }
-            if (bits[0] != 0u) R::mask(v[0], bits[0]);
-            if (bits[1] != 0u) R::mask(v[1], bits[1]);
+#pragma unroll
+            for (int h = 0; h < kLongEach; ++h)
+              if (bits[h] != 0u) R::mask(v[h], bits[h]);
           }
-          const float top = max_nan(m, max_nan(R::max4(v[0]), R::max4(v[1])));
+          float top = max_nan(m, R::max8(v[0], v[1]));
+#pragma unroll
+          for (int h = 2; h < kLongEach; h += 2) top = max_nan(top, R::max8(v[h], v[h + 1]));
           if (__any_sync(0xFFFFFFFFu, !(top == m))) {
             sum *= part_scale(m, top, c);
             m = top;
           }
           const float ref = m == -INFINITY ? 0.f : m;
           const F2 minus(-ref, -ref);
-          F2 acc(0.f, 0.f);
+          F2 acc[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < kLongEach; ++h)
 #pragma unroll
             for (int p = 0; p < R::kPairs; ++p) {
               float y0, y1;
               ((R::pair(v[h], p) + minus) * scale).get(y0, y1);
-              acc = acc + F2(ex2_approx(y0), ex2_approx(y1));
+              acc[h & 1] = acc[h & 1] + F2(ex2_approx(y0), ex2_approx(y1));
             }
           float y0, y1;
-          acc.get(y0, y1);
+          (acc[0] + acc[1]).get(y0, y1);
           sum += y0 + y1;
+        };
+        const int full = g.cnt / kLongSlot;
+        for (int s = 0; s < full; ++s) {
+          uint4 v[kLongEach];
+          next_slot(v);
+          add(v, s);
+        }
+        if (full < g.slots) {
+          uint4 v[kLongEach];
+          next_slot(v);
+          const int left = g.cnt - full * kLongSlot - lane;
+#pragma unroll
+          for (int h = 0; h < kLongEach; ++h)
+            if (left <= 32 * h) v[h] = nothing;
+          add(v, full);
         }
         const float top = warp_max(m);
         sum = warp_sum(sum * part_scale(m, top, c));
@@ -902,14 +964,22 @@ __global__ void __launch_bounds__(kLongThreads, 2)
           publish(p, tag, top);
           publish(p + 1, tag, sum);
         }
-        __syncwarp();  // (the list is read before the next task writes it)
+        __syncwarp();  // (the list is read before the next sum writes it)
         continue;
       }
       // ---- the gradient of a segment
+      float of_row[3] = {0.f, 0.f, 0.f};  // its row's coefficient, maximum, any outside
+      if (alive) {
+        const bool ok = await(x.coef + g.n * 3, tag, of_row, a.timeout_ns, &sm.abort);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          if (lane == 0) record_error(a.status, kStatusTimeout);
+          break;
+        }
+      }
       T* grad = static_cast<T*>(a.grad) + g.n * a.ld_grad;
       T* dst = grad + g.sp.head + static_cast<int64_t>(g.v0 + lane) * kVec;
       const bool aligned = (reinterpret_cast<uintptr_t>(grad + g.sp.head) & 15u) == 0;
-      const auto store = [&](int vec, const uint4& y) {
+      const auto store = [&](int vec, const uint4& y) {  // wherever the gradient's rows start
         if (aligned) {
           __stcs(reinterpret_cast<uint4*>(dst) + vec, y);
         } else {
@@ -917,55 +987,59 @@ __global__ void __launch_bounds__(kLongThreads, 2)
           for (int e = 0; e < kVec; ++e) dst[vec * kVec + e] = R::get(y, e);
         }
       };
-      float coef = 0.f, m_out = 0.f, any = 0.f;
-      if (live(i)) {
-        const unsigned long long* p = x.coef + g.n * 3;
-        const bool ok = await(p, tag, coef, a.timeout_ns, &sm.abort) &&
-                        await(p + 1, tag, m_out, a.timeout_ns, &sm.abort) &&
-                        await(p + 2, tag, any, a.timeout_ns, &sm.abort);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          if (lane == 0) record_error(a.status, kStatusTimeout);
-          break;
-        }
-      }
       const uint4 zeros = make_uint4(0u, 0u, 0u, 0u);
-      if (!live(i)) {  // a row of no weight, neither read nor looked at
+      if (!alive) {  // a row of no weight, neither read nor looked at
         for (int v = 0; v + lane < g.cnt; v += 32) store(v, zeros);
         if (edge >= 0) R::put(grad + edge, 0.f);
         continue;
       }
-      const float ref = m_out == -INFINITY ? 0.f : m_out;
+      const float coef = of_row[0], any = of_row[2];
+      const float ref = of_row[1] == -INFINITY ? 0.f : of_row[1];
       const F2 minus(-ref, -ref), mul(coef, coef);
       const float xe = edge >= 0 ? R::one(g.row + edge) : 0.f;
-      const auto write = [&](auto exp2_of) {
-        for (int s = 0; s < g.slots; ++s) {
-          uint4 v[2];
-          next_slot(v[0], v[1]);
-          const int left = g.cnt - s * kLongSlot - lane;
+      const auto gradient = [&](const uint4& v, auto exp2_of) {
+        uint4 y;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint4 y = zeros;
-            if (any != 0.f) {
+        for (int p = 0; p < R::kPairs; ++p) {
+          float y0, y1;
+          ((R::pair(v, p) + minus) * scale).get(y0, y1);
+          (F2(exp2_of(y0), exp2_of(y1)) * mul).get(y0, y1);
+          R::set_pair(y, p, y0, y1);
+        }
+        return y;
+      };
+      // The common case first.  Apart from it, in little code: a gradient that starts elsewhere
+      // in 16 bytes than the logits; a coefficient above one, which brings results below 2^-126,
+      // dropped by the fast exponential, back into range; no token outside with any probability.
+      const bool common = aligned && any != 0.f && fabsf(coef) <= 1.f;
+      int s = 0;
+      if (common)
+        for (int left = g.cnt - lane; s < g.slots; ++s, left -= kLongSlot) {
+          uint4 v[kLongEach];
+          next_slot(v);
 #pragma unroll
-              for (int p = 0; p < R::kPairs; ++p) {
-                float y0, y1;
-                ((R::pair_again(v[h], p, sel) + minus) * scale).get(y0, y1);
-                (F2(exp2_of(y0), exp2_of(y1)) * mul).get(y0, y1);
-                R::set_pair(y, p, y0, y1);
-              }
-            }
-            if (left > 32 * h) store(s * kLongSlot + 32 * h, y);
+          for (int h = 0; h < kLongEach; ++h) {
+            const uint4 y = gradient(v[h], [](float y) { return ex2_approx(y); });
+            if (left > 32 * h)
+              __stcs(reinterpret_cast<uint4*>(dst) + s * kLongSlot + 32 * h, y);
           }
         }
-        if (edge >= 0) R::put(grad + edge, any != 0.f ? exp2_of((xe - ref) * c) * coef : 0.f);
-      };
-      // (a coefficient above one brings results below 2^-126, which the fast exponential drops,
-      // back into range)
-      if (fabsf(coef) <= 1.f || any == 0.f)
-        write([](float y) { return ex2_approx(y); });
-      else
-        write([](float y) { return exp2f(y); });
+#pragma unroll 1
+      for (; s < g.slots; ++s) {
+        uint4 v[kLongEach];
+        next_slot(v);
+        const int left = g.cnt - s * kLongSlot - lane;
+#pragma unroll 1
+        for (int h = 0; h < kLongEach; ++h) {
+          const uint4 w = h == 0 ? v[0] : h == 1 ? v[1] : h == 2 ? v[2] : v[3];
+          uint4 y = zeros;
+          if (any != 0.f) y = gradient(w, [](float y) { return exp2f(y); });
+          if (left > 32 * h) store(s * kLongSlot + 32 * h, y);
+        }
+      }
+      if (edge >= 0) R::put(grad + edge, any != 0.f ? exp2f((xe - ref) * c) * coef : 0.f);
       // the teacher's tokens of this segment, over what is there now
+      acquire(x.coef + g.n * 3);
       __syncwarp();
       for (int j = lane; j < k; j += 32) {
         const int2 e = __ldcg(x.list + g.n * kMaxTeacher + j);
@@ -1040,11 +1114,21 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStr
     if (a.row_weight != nullptr) a.row_weight += n0;
     a.loss += n0;
     if (a.tv != nullptr) a.tv += n0;
-    // segments of about 10 KB, shorter ones (two slots at least) while there are warps without
-    int S = (body + kLongSegment - 1) / kLongSegment;
+    // shorter segments (a slot at least) while there are warps without any
+    int S = std::min(kLongMaxSegments, (body + kLongSegment<T> - 1) / kLongSegment<T>);
     const int64_t warps = 2ll * num_sms * kLongWarps;
-    while (S < kLongMaxSegments && a.N * S < warps && body / (2 * S) >= 2 * kLongSlot) S *= 2;
+    while (S < kLongMaxSegments && a.N * S < warps && body / (2 * S) >= kLongSlot) S *= 2;
     S = std::min(S, kLongMaxSegments);
+    // With more units than warps, a count that divides the warps: a round of units is then whole
+    // rows, and no sum waits a round for the rest of its row (2048 x 151936, 63 against 64
+    // segments fp32: 536 and 472 us; 28 against 32 bf16: 309 and 284).  The nearest one.
+    if (a.N * S > warps) {
+      int near = 1;
+      for (int d = 2; d <= kLongMaxSegments; ++d)
+        if (warps % d == 0 && std::max(d, S) * std::min(near, S) < std::max(near, S) * std::min(d, S))
+          near = d;
+      S = near;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * num_sms);
     cfg.blockDim = dim3(kLongThreads);
@@ -1056,7 +1140,8 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStr
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.temperature));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, c, S, make_uint2(0x1044u, 0x3244u));
+    const Split split{S, (body + S - 1) / S, static_cast<uint32_t>((1ull << 32) / S + 1)};
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, c, split);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }

@@ -253,6 +253,107 @@ def test_side_stream_graph_and_repeat(dsp):
     assert torch.equal(out["grad"], want["grad"]) and torch.equal(out["loss"], want["loss"])
 
 
+# Rows past 41,472 bytes (288 * 9 pieces of 16) take the other kernel: 10,368 fp32 logits, 20,736 bf16.
+@pytest.mark.parametrize("dtype,V", [(dt, base + d) for dt, base in ((torch.float32, 10368), (torch.bfloat16, 20736))
+                                     for d in (-9, -1, 0, 1, 7, 33, 130)])
+def test_around_the_longest_short_row(dsp, dtype, V):
+    a = make(V, 5, V, 33, dtype)
+    a["ids"][0, :3] = (V - 1, 0, V - 2)
+    a["ids"][1, :4] = (V // 2, -1, V // 2, V // 2 + 1)
+    compare(a, call(dsp, a))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad", [1, 3, 8])
+def test_long_rows_padded_and_in_place(dsp, dtype, pad):
+    """As above for rows in segments: logits and gradient at different offsets modulo 16 bytes."""
+    N, V = 7, 40003
+    a = make(50 + pad, N, V, 21, dtype)
+    buf = torch.full((N, V + pad), torch.nan, dtype=dtype, device="cuda")
+    buf[:, :V] = a["x"].cuda()
+    gbuf = torch.full((N, V + 2 * pad + 1), 7.0, dtype=dtype, device="cuda")
+    got = call(dsp, a, logits=buf[:, :V], grad=gbuf[:, :V])
+    compare(a, got)
+    assert torch.all(gbuf[:, V:] == 7.0)
+    same = call(dsp, a, logits=buf[:, :V], grad=buf[:, :V])
+    assert torch.equal(buf[:, :V], got["grad"]) and torch.equal(same["loss"], got["loss"])
+    assert torch.isnan(buf[:, V:]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_long_rows_masked_and_without_weight(dsp, dtype):
+    a = make(60, 10, 50021, 12, dtype)
+    lowest = torch.finfo(dtype).min
+    a["x"][0, ::2] = -torch.inf
+    a["x"][1, 5:] = -torch.inf             # whole segments of nothing
+    a["x"][2] = -torch.inf                 # nothing at all: zero
+    a["x"][3] = lowest                     # uniform at the lowest value
+    a["x"][4] = -torch.inf
+    a["x"][4, int(a["ids"][4, 3])] = 1.0   # only a teacher's token is left
+    a["x"][5, torch.from_numpy(a["ids"][5].astype(np.int64))] = -torch.inf
+    a["w"][[6, 8]] = 0.0
+    a["x"][6] = torch.nan                  # not looked at
+    a["ids"][8] = 10 ** 6
+    a["x"][7, 40000] = torch.nan
+    out = call(dsp, a)
+    torch.cuda.synchronize()
+    assert dsp.status() == 0
+    assert not out["grad"][[2, 6, 8]].any() and float(out["loss"][2]) == 0
+    assert torch.isnan(out["loss"]).tolist() == [n == 7 for n in range(10)]
+    assert torch.isnan(out["grad"]).any(1).tolist() == [n == 7 for n in range(10)]
+    compare(a, out, rows=[0, 1, 2, 3, 4, 5, 6, 8, 9])
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 12007), (torch.bfloat16, 24001)])
+@pytest.mark.parametrize("grad", [True, False])
+def test_many_long_rows(dsp, dtype, V, grad):
+    """More rows than one launch takes (2048), over many rounds, a run of them without weight."""
+    N, k = 2300, 7
+    rng = np.random.default_rng(V)
+    base = make(V, 8, V, k, dtype)
+    pick = rng.integers(0, 8, N)
+    a = {n: base[n][pick] for n in ("x", "ids", "t", "rho")} | dict(w=rng.uniform(0.1, 2, N).astype(np.float32))
+    a["w"][300:900] = 0.0
+    a["w"][2047:2050] = 0.0
+    out = call(dsp, a, grad=grad)
+    torch.cuda.synchronize()
+    assert dsp.status() == 0
+    rows = [0, 1, 299, 300, 901, 1500, 2046, 2048, 2050, 2051, N - 1]
+    compare(a, out, rows=rows)
+    # every other row against the one of the same logits: the loss is linear in its weight, with
+    # two roundings, and TV does not depend on it
+    alone = call(dsp, base | dict(w=np.ones(8, np.float32)), grad=False)
+    want = host(alone["loss"])[pick] * a["w"]
+    live = a["w"] != 0
+    assert np.abs(host(out["loss"]) - want).max() <= 1e-5 * np.abs(want).max()
+    assert (host(out["loss"])[~live] == 0).all()
+    assert np.abs(host(out["tv"])[live] - host(alone["tv"])[pick][live]).max() <= 1e-5
+
+
+def test_long_rows_on_a_side_stream_in_a_graph_and_repeated(dsp):
+    a = make(61, 9, 60000, 8, torch.bfloat16)
+    want = call(dsp, a)
+    x = a["x"].cuda()
+    ids, t, rho, w = (dev(a[n]) for n in ("ids", "t", "rho", "w"))
+    for _ in range(3):  # the context's scratch is used again
+        out = binding.distill(dsp, x, ids, t, teacher_rest=rho, row_weight=w, **KW)
+        assert torch.equal(out["grad"], want["grad"]) and torch.equal(out["loss"], want["loss"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = binding.distill(dsp, x, ids, t, teacher_rest=rho, row_weight=w, **KW)
+    side.synchronize()
+    assert torch.equal(out["grad"], want["grad"]) and torch.equal(out["loss"], want["loss"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = binding.distill(dsp, x, ids, t, teacher_rest=rho, row_weight=w, **KW)
+    for s in (0.5, 1.0):
+        x.copy_(a["x"].cuda() * s)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out["grad"], want["grad"]) and torch.equal(out["loss"], want["loss"])
+
+
 def test_refusals(dsp):
     a = make(42, 3, 64, 4, torch.float32)
     with pytest.raises(binding.DSparkError) as err:
