@@ -19,8 +19,11 @@
 // cut into segments, one a warp of its CTAs; a thread's next reads are always on their way to
 // shared memory while it adds up the ones that have come.  The CTA of a request that ends last
 // joins the segments' sums, in order, and reads the one segment where the sum passes u R again.
-// (Clusters, which could exchange the sums through shared memory, left SMs empty: with four CTAs
-// a request the draw took 41 us where 128 x 152k dense rows take 32 now.)
+// 128 dense rows of 152k tokens (156 MB) take 39 us, 4.0 TB/s: the tests' dependent loads, the
+// start and the join of the last request are some 12 us beside the reads.
+// Not kept: clusters, which could exchange the sums through shared memory, left SMs empty (the
+// draw alone 41 us); warps that run on from segment to segment with a third launch that joins took
+// 46 us, the bookkeeping and the third launch costing more than the starts that they saved.
 
 #include <algorithm>
 #include <cfloat>
@@ -228,13 +231,14 @@ __global__ void __launch_bounds__(kVpThreads, 4)
   const bool sparse = m > 0 && j < len;
   const int segments = ctas * kVpWarps;
   const auto begin = [&](int s) { return min(V, s * seg); };
-  if (sparse) {
+  const auto lists = [&]() {
+    if (!sparse) return;
     for (int i = tid; i < m; i += kVpThreads) {
       s_id[i] = __ldg(a.cand + o * m + i);
       s_q[i] = __ldg(a.cand_q + o * m + i);
     }
     __syncthreads();
-  }
+  };
   // q of the tokens v, v + step, ... among the candidates (from the last, so that the first of
   // equal ids stays)
   const auto candidates = [&](int v, int step, float (&q)[4]) {
@@ -252,18 +256,11 @@ __global__ void __launch_bounds__(kVpThreads, 4)
 
   // One pass over segment `s` by this warp; its sum.  Two rows or the target's alone.
   float* const ring = s_ring + warp * kVpRing * 2 * kVpSlot + (kWide ? 4 * lane : lane);
-  const auto stream = [&](auto two, auto careful, bool lists, int s) {
+  const auto stream = [&](auto two, auto careful, bool listing, int s, auto meanwhile) {
     constexpr bool kTwo = decltype(two)::value, kCareful = decltype(careful)::value;
     const int v0 = begin(s), v1 = begin(s + 1);
-    uint32_t listed = 0u;  // groups of the segment that hold a candidate
-    if (!kTwo && lists) {
-      for (int i = lane; i < m; i += 32) {
-        const int id = s_id[i];
-        if (id >= v0 && id < v1) listed |= 1u << ((id - v0) / kVpGroup);
-      }
-      listed = __reduce_or_sync(0xFFFFFFFFu, listed);
-    }
-    const int slots = (v1 - v0 + kVpSlot - 1) / kVpSlot;
+    constexpr int kSlot = kTwo ? kVpSlot : 2 * kVpSlot;  // one row has a slot to itself
+    const int slots = (v1 - v0 + kSlot - 1) / kSlot;
     const float* pp = prow + v0 + (kWide ? 4 * lane : lane);  // this lane's next copies
     const float* qq = kTwo ? qrow + v0 + (kWide ? 4 * lane : lane) : nullptr;
     int rest = v1 - v0 - (kWide ? 4 * lane : lane), to = 0, from = 0;
@@ -271,7 +268,7 @@ __global__ void __launch_bounds__(kVpThreads, 4)
     const auto fetch = [&](int k) {
       if (k < slots) {
         float* dst = ring + to * 2 * kVpSlot;
-        constexpr int kPieces = kWide ? 2 : 8, kStep = kWide ? kVpGroup : 32;
+        constexpr int kStep = kWide ? kVpGroup : 32, kPieces = kSlot / kStep;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const int n = rest - i * kStep;  // tokens left from this piece on
@@ -285,15 +282,24 @@ __global__ void __launch_bounds__(kVpThreads, 4)
               cp_async_4_zfill(dst + kVpSlot + i * kStep, n > 0 ? qq + i * kStep : qrow, n > 0 ? 4 : 0);
           }
         }
-        pp += kVpSlot;
-        if (kTwo) qq += kVpSlot;
-        rest -= kVpSlot;
+        pp += kSlot;
+        if (kTwo) qq += kSlot;
+        rest -= kSlot;
         to = to == kVpRing - 1 ? 0 : to + 1;
       }
       cp_async_commit();
     };
 #pragma unroll
     for (int k = 0; k < kVpRing - 1; ++k) fetch(k);
+    meanwhile();
+    uint32_t listed = 0u;  // groups of the segment that hold a candidate
+    if (!kTwo && listing) {
+      for (int i = lane; i < m; i += 32) {
+        const int id = s_id[i];
+        if (id >= v0 && id < v1) listed |= 1u << ((id - v0) / kVpGroup);
+      }
+      listed = __reduce_or_sync(0xFFFFFFFFu, listed);
+    }
     Sum sum;
     for (int k = 0; k < slots; ++k) {
       fetch(k + kVpRing - 1);
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kVpThreads, 4)
       const float* src = ring + from * 2 * kVpSlot;
       from = from == kVpRing - 1 ? 0 : from + 1;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kSlot / kVpGroup; ++h) {
         float p[4], q[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kVpThreads, 4)
           p[i] = src[at];
           if (kTwo) q[i] = src[kVpSlot + at];
         }
-        const int g = 2 * k + h;
+        const int g = kSlot / kVpGroup * k + h;
         if (kTwo) {
           sum.add_residual<kCareful>(p[0], p[1], q[0], q[1]);
           sum.add_residual<kCareful>(p[2], p[3], q[2], q[3]);
@@ -331,8 +337,8 @@ __global__ void __launch_bounds__(kVpThreads, 4)
   bool left = j < len;  // weights are what the draft left over, else the target's row
   {
     const int s = cta * kVpWarps + warp;
-    const Pair mine = left && qrow != nullptr ? stream(Yes{}, No{}, false, s)
-                                              : stream(No{}, No{}, left, s);
+    const Pair mine = left && qrow != nullptr ? stream(Yes{}, No{}, false, s, lists)
+                                              : stream(No{}, No{}, left, s, lists);
     if (lane == 0) reinterpret_cast<float2*>(a.sums)[b * kVpSegments + s] = make_float2(mine.hi, mine.lo);
   }
   __syncthreads();
@@ -397,8 +403,8 @@ __global__ void __launch_bounds__(kVpThreads, 4)
     careful = true;
     __syncthreads();
     for (int s = warp; s < segments; s += kVpWarps) {
-      const Pair sum = left && qrow != nullptr ? stream(Yes{}, Yes{}, false, s)
-                                               : stream(No{}, Yes{}, left, s);
+      const Pair sum = left && qrow != nullptr ? stream(Yes{}, Yes{}, false, s, [] {})
+                                               : stream(No{}, Yes{}, left, s, [] {});
       if (lane == 0) s_sum[s] = sum;
     }
   }
@@ -460,9 +466,10 @@ __global__ void __launch_bounds__(kVpThreads, 4)
 }  // namespace
 
 cudaError_t launch_verify_probs(const VerifyProbsArgs& all, int* launches, cudaStream_t stream) {
-  // A CTA per 9728 tokens (a warp's segment at the full vocabulary, 1216, is a ring and a half),
-  // 16 at most; every segment a multiple of 4 tokens.
-  const int ctas = std::min(kVpMaxCtas, (all.V + 9727) / 9728), segments = ctas * kVpWarps;
+  // A CTA per 15,360 tokens, 16 at most; every segment a multiple of 4 tokens.  (Of 152k tokens, in
+  // 5 / 6 / 8 / 10 / 16 CTAs: 128 dense rows 43.4 / 42.6 / 43.2 / 39.0 / 39.1 us, 256 rows with lists
+  // 54.0 / 51.4 / 52.6 / 49.2 / 55.5 us.)
+  const int ctas = std::min(kVpMaxCtas, (all.V + 15359) / 15360), segments = ctas * kVpWarps;
   const int seg = ((all.V + segments - 1) / segments + 3) & ~3;
   const bool wide = all.V % 4 == 0 && reinterpret_cast<uintptr_t>(all.P) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(all.Q) % 16 == 0;
