@@ -462,7 +462,7 @@ int dspark_schedule(dspark_ctx* ctx, const float* a, int R, int K, const float* 
  * Outputs as dspark_verify: n_acc [B], next_token [B], accept_prob [B, K] (NULL: not
  * written) min(1, p/q) (q = 0: 1 if p > 0 else 0) for k < ell[b], -1 beyond.
  * K <= 64, V <= 2^18, any V; 4-byte aligned pointers.  Drafted tokens out of [0, V) are
- * reported as DSPARK_ERR_DEVICE_OOB.  Two kernels (per 1024 requests). */
+ * reported as DSPARK_ERR_DEVICE_OOB.  Two kernels (one up to V = 15,360) per 1024 requests. */
 int dspark_verify_probs(dspark_ctx* ctx, const float* P, const float* Q, const int32_t* cand,
                         const float* cand_q, int m, const int32_t* tokens, const float* u_accept,
                         const float* u_draw, const int32_t* ell, int B, int K, int V,

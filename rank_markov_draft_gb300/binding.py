@@ -174,7 +174,7 @@ def _dtype(t: torch.Tensor, name: str) -> int:
 
 
 def _shape(t: Optional[torch.Tensor], shape, name: str):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:  # (a torch.Size is a tuple)
         raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
 
 

@@ -62,6 +62,20 @@ def test_vocabularies(dsp, V, m):
     check(dsp, make(V + m, B, K, V, min(m, V)))
 
 
+@pytest.mark.parametrize("V", [15359, 15360, 15361, 15364, 30720, 30721])
+@pytest.mark.parametrize("m", [0, 20])
+def test_around_the_tokens_of_one_cta(dsp, V, m):
+    """Up to 15,360 tokens one CTA makes a request's tests and its draw."""
+    a = make(V + m, 6, 3, V, m, noise=0.5)
+    a["ell"] = np.array([0, 1, 2, 3, 3, 3], np.int32)
+    check(dsp, a)
+
+
+@pytest.mark.parametrize("B,V", [(1101, 40), (1030, 15364)])
+def test_more_requests_than_a_launch_takes(dsp, B, V):
+    check(dsp, make(B, B, 1, V, noise=0.3))
+
+
 @pytest.mark.parametrize("B,K", [(1, 1), (1, 64), (3, 33), (200, 2)])
 def test_batches_and_blocks(dsp, B, K):
     n, _ = check(dsp, make(B + K, B, K, 517, noise=0.3))
