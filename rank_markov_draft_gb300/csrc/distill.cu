@@ -402,8 +402,9 @@ struct SlotWarp {
 };
 
 // Short rows.  A CTA walks over rows; vector i of a streaming thread is the row's body vector
-// tid + i * (threads - 32); all but the last i are full (the host picks the threads so).  The up
-// to 14 elements outside the body are single elements of warp 0's lanes.
+// tid + i * (threads - 32); all but the last partial_of(NV) are full (the host picks the threads
+// so).  The up to 14 elements outside the body are single elements of warp 0's lanes.
+__host__ __device__ constexpr int partial_of(int nv) { return nv >= 9 ? 2 : 1; }
 template <typename T, int NV, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     distill_short_kernel(const DistillArgs a, const float c, const int map_words, const uint2 sel) {
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
       if (tid < sp.head) edge = tid;
       if (tid >= 8 && tid - 8 < sp.tail) edge = a.V - sp.tail + tid - 8;
     }
-    const auto has = [&](int i) { return i < NV - 1 || tid + i * row_threads < cnt; };
+    const auto has = [&](int i) { return i < NV - partial_of(NV) || tid + i * row_threads < cnt; };
     const auto store = [&](int i, const uint4& g) {
       if (aligned) {
         __stcs(reinterpret_cast<uint4*>(dst) + i * row_threads, g);
@@ -1070,11 +1071,11 @@ cudaError_t launch_short(const DistillArgs& a, int row_threads, int num_sms, cud
   return cudaGetLastError();
 }
 
-// Streaming threads that hold `most` vectors in NV each with all but the last NV full where there
-// are `least` (0: none below `limit` do).
+// Streaming threads that hold `most` vectors in nv each with all but the last partial_of(nv) full
+// where there are `least` (0: none up to `limit` do).
 int threads_for(int nv, int most, int least, int limit) {
   const int t = (((most + nv - 1) / nv + 31) / 32) * 32;
-  return t <= limit && (nv - 1) * t <= least ? std::max(t, 32) : 0;
+  return t <= limit && (nv - partial_of(nv)) * t <= least ? std::max(t, 32) : 0;
 }
 
 template <typename T>

@@ -253,6 +253,20 @@ def test_side_stream_graph_and_repeat(dsp):
     assert torch.equal(out["grad"], want["grad"]) and torch.equal(out["loss"], want["loss"])
 
 
+# 16-byte pieces of a row at which the number that a thread holds, or the threads, change.
+STEPS = sorted({p + d for p in [96, 192, 288, 384, 512, 1024, 1152, 1344, 1536, 1728, 1792, 2016, 2304, 2592]
+                for d in (0, 1)} | {1760, 1791})
+
+
+@pytest.mark.parametrize("dtype,per", [(torch.float32, 4), (torch.bfloat16, 8)])
+@pytest.mark.parametrize("pieces", STEPS)
+def test_every_way_a_short_row_is_dealt_out(dsp, dtype, per, pieces):
+    for V in (pieces * per, pieces * per + 3):
+        a = make(V, 3, V, 12, dtype)
+        a["ids"][0, :3] = (V - 1, 0, V - 2)
+        compare(a, call(dsp, a))
+
+
 # Rows past 41,472 bytes (288 * 9 pieces of 16) take the other kernel: 10,368 fp32 logits, 20,736 bf16.
 @pytest.mark.parametrize("dtype,V", [(dt, base + d) for dt, base in ((torch.float32, 10368), (torch.bfloat16, 20736))
                                      for d in (-9, -1, 0, 1, 7, 33, 130)])
