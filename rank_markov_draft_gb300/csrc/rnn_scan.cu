@@ -689,8 +689,10 @@ cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStre
   while ((1ll << bits) < a.D) ++bits;
   c.div_shift = 31 + bits;
   c.div_mul = static_cast<uint32_t>(((1ull << c.div_shift) + a.D - 1) / a.D);
-  // Segments where walking would leave SMs without a CTA and sequences are long enough to cut.
-  if (2 * c.blocks <= room && places >= 4 * kWarps) {
+  // Segments where walking would leave most SMs without work and sequences are long enough to cut.
+  // 16.8 M steps of fp32 channels in 8 / 38 / 76 / 152 / 304 blocks, forward and backward: segments
+  // 82 and 95 us throughout, walking 1081 / 234 / 121 / 64 / 53 and 1504 / 325 / 166 / 86 / 70 us.
+  if (8 * c.blocks <= 3 * room && places >= 4 * kWarps) {
     int64_t per = std::min<int64_t>(room / c.blocks, kScanCtas / c.blocks);  // CTAs a block
     per = std::min(per, places / (2 * kWarps));
     c.segs = static_cast<int>(per * kWarps);
@@ -700,10 +702,12 @@ cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStre
     if (e != cudaSuccess) return e;
     return scan_launch<Dir, T, kVec, Mode::kSegments, kReset>(a, c, c.blocks * per, stream);
   }
-  // As few warps to a block as fill the SMs, since they exchange spans at every turn, and none
-  // that would have a single turn (so 16 steps give what 16 calls of one step give).
+  // More warps to a block while blocks are few, and none that would have a single turn (so 16 steps
+  // give what 16 calls of one step give).  10 M steps of fp32 channels walked by 1 / 2 / 4 / 8 warps a
+  // block, backward: 1216 blocks 47 / 45 / 45 / 43 us, 2432 and 4864 blocks 47 / 43 / 43 / 43 us, 9728
+  // blocks 45 / 43 / 43 / 78 us; 5 M in 304 blocks 84 / 52 / 31 / 25 us.
   c.W = 1;
-  while (c.W < kWarps && 2 * c.W < places && c.blocks * c.W < room * kWarps) c.W *= 2;
+  while (c.W < kWarps && 2 * c.W < places && c.blocks * c.W < 8 * room * kWarps) c.W *= 2;
   const int64_t groups = kWarps / c.W;
   return scan_launch<Dir, T, kVec, Mode::kWalk, kReset>(
       a, c, std::min((c.blocks + groups - 1) / groups, room), stream);
