@@ -15,7 +15,7 @@
 //
 // The gradient needs the row's sum, so every logit is wanted twice, and is to come from memory
 // once.  Two kernels:
-//   Short rows (40 KB at most) lie in the registers of one CTA between the passes.  CTAs walk
+//   Short rows (152 KB at most) lie in the registers of one CTA between the passes.  CTAs walk
 //   over the rows; one warp of each holds no part of the row and prepares the next row's teacher
 //   slots (which count, the student's logits there, a bit map of their tokens) while the others
 //   stream the current one, so the dependent loads of the slots hide behind the row's.
@@ -197,7 +197,11 @@ struct SlotSmem {  // double-buffered by the row's turn
   float coef[3];                               // outside coefficient, any of it at all, maximum
 };
 
-constexpr int kShortVectors = 288 * 9;  // of the longest row that lies in one CTA's registers
+// Up to 288 * 9 vectors three CTAs share an SM, up to 288 * 16 two, up to 608 * 16 there is one.
+// 4096 rows of 10000 / 16400 fp32 logits took 90 / 131 us, cut in segments as the longer ones 129 / 156;
+// of 20000 / 36800 bf16 88 / 135 against 137 / 174; 2048 of 30400 fp32 125 against 135, of 76800 bf16
+// 148 against 152; and 128 rows of 50257 bf16 16.4 against 30.7.
+constexpr int kShortVectors = 608 * 16;  // of the longest row that lies in one CTA's registers
 
 // Where a row lies: `off` elements past a 16-byte boundary, so `head` elements before the first
 // aligned vector, `body` vectors, `tail` elements after the last.
@@ -1097,8 +1101,14 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStr
       return launch_short<T, 4, 320, 3>(all, t, num_sms, stream);
     if ((t = threads_for(6, most, least, 288)))
       return launch_short<T, 6, 320, 3>(all, t, num_sms, stream);
-    t = threads_for(9, most, least, 288);
-    return launch_short<T, 9, 320, 3>(all, t, num_sms, stream);
+    if ((t = threads_for(9, most, least, 288)))
+      return launch_short<T, 9, 320, 3>(all, t, num_sms, stream);
+    if ((t = threads_for(12, most, least, 288)))
+      return launch_short<T, 12, 320, 2>(all, t, num_sms, stream);
+    if ((t = threads_for(16, most, least, 288)))
+      return launch_short<T, 16, 320, 2>(all, t, num_sms, stream);
+    t = threads_for(16, most, least, 608);
+    return launch_short<T, 16, 640, 1>(all, t, num_sms, stream);
   }
   const auto fn = distill_long_kernel<T>;
   static const cudaError_t once = cudaFuncSetAttribute(
