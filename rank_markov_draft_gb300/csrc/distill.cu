@@ -197,7 +197,7 @@ struct SlotSmem {  // double-buffered by the row's turn
   float coef[3];                               // outside coefficient, any of it at all, maximum
 };
 
-// Up to 288 * 9 vectors three CTAs share an SM, up to 288 * 16 two, up to 608 * 16 there is one.
+// (From 96 * 16 vectors on; up to 288 * 9 three CTAs share an SM, up to 288 * 16 two, then there is one.)
 // 4096 rows of 10000 / 16400 fp32 logits took 90 / 131 us, cut in segments as the longer ones 129 / 156;
 // of 20000 / 36800 bf16 88 / 135 against 137 / 174; 2048 of 30400 fp32 125 against 135, of 76800 bf16
 // 148 against 152; and 128 rows of 50257 bf16 16.4 against 30.7.
@@ -406,10 +406,9 @@ struct SlotWarp {
 };
 
 // Short rows.  A CTA walks over rows; vector i of a streaming thread is the row's body vector
-// tid + i * (threads - 32); all but the last partial_of(NV) are full (the host picks the threads
+// tid + i * (threads - 32); all but the last kPartial of them are full (the host picks the threads
 // so).  The up to 14 elements outside the body are single elements of warp 0's lanes.
-__host__ __device__ constexpr int partial_of(int nv) { return nv >= 9 ? 2 : 1; }
-template <typename T, int NV, int kMaxThreads, int kPerSm>
+template <typename T, int NV, int kPartial, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     distill_short_kernel(const DistillArgs a, const float c, const int map_words, const uint2 sel) {
   using R = Row16<T>;
@@ -488,7 +487,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
       if (tid < sp.head) edge = tid;
       if (tid >= 8 && tid - 8 < sp.tail) edge = a.V - sp.tail + tid - 8;
     }
-    const auto has = [&](int i) { return i < NV - partial_of(NV) || tid + i * row_threads < cnt; };
+    const auto has = [&](int i) { return i < NV - kPartial || tid + i * row_threads < cnt; };
     const auto store = [&](int i, const uint4& g) {
       if (aligned) {
         __stcs(reinterpret_cast<uint4*>(dst) + i * row_threads, g);
@@ -1063,9 +1062,9 @@ __global__ void __launch_bounds__(kLongThreads, 2)
   }
 }
 
-template <typename T, int NV, int kMaxThreads, int kPerSm>
+template <typename T, int NV, int kPartial, int kMaxThreads, int kPerSm>
 cudaError_t launch_short(const DistillArgs& a, int row_threads, int num_sms, cudaStream_t stream) {
-  const auto fn = distill_short_kernel<T, NV, kMaxThreads, kPerSm>;
+  const auto fn = distill_short_kernel<T, NV, kPartial, kMaxThreads, kPerSm>;
   const int map_words = (a.V + 2 * Row16<T>::kVec + 31) / 32;
   const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.temperature));
   const unsigned grid =
@@ -1075,11 +1074,11 @@ cudaError_t launch_short(const DistillArgs& a, int row_threads, int num_sms, cud
   return cudaGetLastError();
 }
 
-// Streaming threads that hold `most` vectors in nv each with all but the last partial_of(nv) full
+// Streaming threads that hold `most` vectors in nv each with all but the last `partial` full
 // where there are `least` (0: none up to `limit` do).
-int threads_for(int nv, int most, int least, int limit) {
+int threads_for(int nv, int partial, int most, int least, int limit) {
   const int t = (((most + nv - 1) / nv + 31) / 32) * 32;
-  return t <= limit && (nv - partial_of(nv)) * t <= least ? std::max(t, 32) : 0;
+  return t <= limit && (nv - partial) * t <= least ? std::max(t, 32) : 0;
 }
 
 template <typename T>
@@ -1091,24 +1090,32 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStr
   int t;
   if (body <= kShortVectors) {
     *launches += 1;
-    if ((t = threads_for(1, most, least, 96)))
-      return launch_short<T, 1, 128, 6>(all, t, num_sms, stream);
-    if ((t = threads_for(2, most, least, 96)))
-      return launch_short<T, 2, 128, 6>(all, t, num_sms, stream);
-    if ((t = threads_for(3, most, least, 96)))
-      return launch_short<T, 3, 128, 6>(all, t, num_sms, stream);
-    if ((t = threads_for(4, most, least, 288)))
-      return launch_short<T, 4, 320, 3>(all, t, num_sms, stream);
-    if ((t = threads_for(6, most, least, 288)))
-      return launch_short<T, 6, 320, 3>(all, t, num_sms, stream);
-    if ((t = threads_for(9, most, least, 288)))
-      return launch_short<T, 9, 320, 3>(all, t, num_sms, stream);
-    if ((t = threads_for(12, most, least, 288)))
-      return launch_short<T, 12, 320, 2>(all, t, num_sms, stream);
-    if ((t = threads_for(16, most, least, 288)))
-      return launch_short<T, 16, 320, 2>(all, t, num_sms, stream);
-    t = threads_for(16, most, least, 608);
-    return launch_short<T, 16, 640, 1>(all, t, num_sms, stream);
+    // Few threads with many vectors while they hold the row: a row is bound by its slot warp's
+    // chain, and small CTAs bring more of those to an SM.  4096 rows, 128 slots, in three warps
+    // against up to nine: 9120 bf16 logits 70 -> 61 us, 15400 78 -> 64, 24000 86 -> 76; 6000 fp32
+    // 88 -> 74 (loss alone 70 -> 53).
+    if ((t = threads_for(1, 1, most, least, 96)))
+      return launch_short<T, 1, 1, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(2, 1, most, least, 96)))
+      return launch_short<T, 2, 1, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(3, 1, most, least, 96)))
+      return launch_short<T, 3, 1, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(4, 1, most, least, 96)))
+      return launch_short<T, 4, 1, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(6, 2, most, least, 96)))
+      return launch_short<T, 6, 2, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(8, 2, most, least, 96)))
+      return launch_short<T, 8, 2, 128, 6>(all, t, num_sms, stream);
+    if ((t = threads_for(16, 6, most, least, 96)))
+      return launch_short<T, 16, 6, 128, 4>(all, t, num_sms, stream);
+    if ((t = threads_for(9, 2, most, least, 288)))
+      return launch_short<T, 9, 2, 320, 3>(all, t, num_sms, stream);
+    if ((t = threads_for(12, 2, most, least, 288)))
+      return launch_short<T, 12, 2, 320, 2>(all, t, num_sms, stream);
+    if ((t = threads_for(16, 2, most, least, 288)))
+      return launch_short<T, 16, 2, 320, 2>(all, t, num_sms, stream);
+    t = threads_for(16, 2, most, least, 608);
+    return launch_short<T, 16, 2, 640, 1>(all, t, num_sms, stream);
   }
   const auto fn = distill_long_kernel<T>;
   static const cudaError_t once = cudaFuncSetAttribute(

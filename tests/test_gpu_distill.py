@@ -254,7 +254,7 @@ def test_side_stream_graph_and_repeat(dsp):
 
 
 # 16-byte pieces of a row at which the number that a thread holds, or the threads, change.
-STEPS = sorted({p + d for p in [96, 192, 288, 384, 512, 1024, 1152, 1344, 1536, 1728, 1792, 2016, 2304, 2592,
+STEPS = sorted({p + d for p in [96, 192, 288, 384, 480, 512, 576, 640, 768, 864, 1024, 1152, 1344, 1536, 1728, 1792, 2016, 2304, 2592,
                                  2688, 3136, 3456, 3584, 4096, 4608, 5120, 7168, 9216, 9728]
                 for d in (0, 1)} | {1760, 1791})
 
