@@ -458,9 +458,11 @@ int dspark_schedule(dspark_ctx* ctx, const float* a, int R, int K, const float* 
  * first rejection j the weights are r_v = max(0, p_j(v) - q_j(v)), or p_j where that is
  * zero everywhere; after a full window r = p_ell.  next_token is the first v (by id)
  * with sum_{w <= v} r_w > u_draw sum_w r_w, the sums kept to about 2^-48 of the whole;
- * -1 where no token has mass.  Entries that are negative or not finite have no mass.
+ * -1 where no token has mass.  A p that is negative or not finite counts as 0, and so
+ * does a negative q; a token whose q is infinite or NaN is rejected and has no weight.
  * Outputs as dspark_verify: n_acc [B], next_token [B], accept_prob [B, K] (NULL: not
- * written) min(1, p/q) (q = 0: 1 if p > 0 else 0) for k < ell[b], -1 beyond.
+ * written) min(1, p/q) (q = 0: 1 if p > 0 else 0; q infinite or NaN: 0) for k < ell[b],
+ * -1 beyond.
  * K <= 64, V <= 2^18, any V; 4-byte aligned pointers.  Drafted tokens out of [0, V) are
  * reported as DSPARK_ERR_DEVICE_OOB.  Two kernels (one up to V = 15,360) per 1024 requests. */
 int dspark_verify_probs(dspark_ctx* ctx, const float* P, const float* Q, const int32_t* cand,

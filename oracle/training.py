@@ -14,13 +14,19 @@ EPS32 = 2.0 ** -24  # half a step of float32, relative
 
 def verify_probs(P, tokens, u_accept, u_draw, *, Q=None, cand=None, cand_q=None, ell=None):
     """n_acc [B], next_token [B], accept_prob [B, K] (min(1, p/q), -1 outside the window)."""
+    top = float(np.finfo(np.float32).max)
     P = np.asarray(P, np.float64)
+    P = np.where((P > 0) & (P <= top), P, 0.0)  # negative or not finite: nothing
     B, K = tokens.shape
     V = P.shape[2]
     n_acc, nxt = np.zeros(B, np.int64), np.zeros(B, np.int64)
     prob = np.full((B, K), -1.0)
 
     def draft_row(b, k):
+        row = plain_row(b, k)
+        return np.where(row < 0, 0.0, row)
+
+    def plain_row(b, k):
         if cand is None:
             return np.asarray(Q[b, k], np.float64)
         row = np.zeros(V)
@@ -36,16 +42,15 @@ def verify_probs(P, tokens, u_accept, u_draw, *, Q=None, cand=None, cand_q=None,
             for k in range(n):
                 x = tokens[b, k]
                 p, q = P[b, k, x], draft_row(b, k)[x]
-                prob[b, k] = min(1.0, p / q) if q > 0 else float(p > 0)
+                prob[b, k] = min(1.0, p / q) if q > 0 else float(p > 0 and q == 0)
                 if j == n and not float(u_accept[b, k]) * q < p:
                     j = k
             r = P[b, j]
             if j < n:
                 r = r - draft_row(b, j)
-            weigh = lambda w: np.where((w > 0) & (w <= np.finfo(np.float32).max), w, 0.0)  # noqa: E731
-            w = weigh(r)
+            w = np.where(r > 0, r, 0.0)
             if not w.sum() > 0:
-                w = weigh(P[b, j])
+                w = P[b, j]
             n_acc[b] = j
             cum = np.cumsum(w)
             nxt[b] = int(np.argmax(cum > float(u_draw[b]) * cum[-1])) if cum[-1] > 0 else -1

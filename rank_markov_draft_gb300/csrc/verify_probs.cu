@@ -8,7 +8,8 @@
 // Position k of the window survives while u_k q_k(x_k) < p_k(x_k), a product of two 24-bit
 // numbers compared exactly.  At the first rejection j the weights are
 // r_v = max(0, p_j(v) - q_j(v)), after a full window r = p_ell, and the token is the first v
-// whose running sum of r passes u R, R the whole sum.  A vocabulary's sum in 32 bits is off by
+// whose running sum of r passes u R, R the whole sum.  A negative p or q counts as zero, and so does
+// a p that is not finite; a q that is infinite or NaN is above every p.  A vocabulary's sum in 32 bits is off by
 // more than a rare token's probability, so a neighbour would be drawn; each difference is kept
 // with its rounding error and summed as a pair of floats (hi + lo, about 2^-48 of the sum).
 // (Pairs, not 64-bit arithmetic: this chip adds two doubles a clock and SM, and even the few
@@ -57,6 +58,12 @@ __device__ __forceinline__ void two_sum(F2 a, F2 b, F2& s, F2& e) {
 }
 
 __device__ __forceinline__ bool has_mass(float x) { return x > 0.f && x <= FLT_MAX; }
+// A draft's probability: a negative one is zero, a NaN stays.
+__device__ __forceinline__ float draft_mass(float q) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(q), "f"(0.f));
+  return r;
+}
 
 // A number as hi + lo, |lo| at most half a step of hi.
 struct Pair {
@@ -116,6 +123,8 @@ struct Sum {
   // entries no mass instead.
   template <bool kCareful>
   __device__ __forceinline__ void add_residual(float p0, float p1, float q0, float q1) {
+    q0 = draft_mass(q0);
+    q1 = draft_mass(q1);
     const F2 p(fmaxf(p0, q0), fmaxf(p1, q1)), q(q0, q1), neg(-1.f, -1.f);
     F2 d = fma2(q, neg, p), err = fma2(q, neg, fma2(d, neg, p)), s, e;
     if (kCareful) {
@@ -149,6 +158,7 @@ struct Sum {
 
 // One weight.
 __device__ __forceinline__ Pair weight_of(float p, float q) {
+  q = draft_mass(q);
   const float d = p - q;
   return has_mass(d) ? Pair{d, (p - d) - q} : Pair{0.f, 0.f};
 }
@@ -178,7 +188,8 @@ __device__ __forceinline__ int first_failure(const VerifyProbsArgs& a, int b, in
           record_error(a.status, kStatusDeviceOob);
           x = 0;
         }
-        const float p = __ldg(a.P + (static_cast<size_t>(b) * (a.K + 1) + k) * a.V + x);
+        const float target = __ldg(a.P + (static_cast<size_t>(b) * (a.K + 1) + k) * a.V + x);
+        const float p = has_mass(target) ? target : 0.f;
         float q = 0.f;
         if (a.m == 0) {
           q = __ldg(a.Q + o * a.V + x);
@@ -194,8 +205,9 @@ __device__ __forceinline__ int first_failure(const VerifyProbsArgs& a, int b, in
             }
           }
         }
+        q = draft_mass(q);
         fail = !survives(u, q, p);
-        prob = q > 0.f ? fminf(1.f, p / q) : (p > 0.f ? 1.f : 0.f);
+        prob = q > 0.f ? fminf(1.f, p / q) : (p > 0.f && q == 0.f ? 1.f : 0.f);
       }
       if (a.accept_prob != nullptr) a.accept_prob[o] = prob;
     }

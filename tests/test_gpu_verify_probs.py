@@ -142,6 +142,46 @@ def test_rows_without_mass(dsp):
     assert t[1] == -1
 
 
+@pytest.mark.parametrize("V", [263, 20004])  # one CTA; several, in 16-byte pieces
+@pytest.mark.parametrize("m", [0, 5])
+def test_entries_that_are_no_probabilities(dsp, V, m):
+    """A p that is negative or not finite is nothing, a negative q likewise; a token whose q is
+    infinite or NaN is rejected and left out: the acceptance probability, the test and the
+    draw agree on each, one such entry among good ones and whole rows of them."""
+    a = make(V + m, 64, 3, V, m, noise=0.5)
+    rng = np.random.default_rng(V)
+    q = a["cand_q"] if m else a["Q"]
+    values = [np.nan, np.inf, -np.inf, -0.25]
+    for b in range(64):
+        p_bad, q_bad = values[b % 4], values[b // 4 % 4]
+        x = a["tokens"][b]
+        if b & 16:  # the drafted token's p
+            a["P"][b, np.arange(3), x] = p_bad
+        if b & 32:  # and its q
+            if m:
+                q[b][a["cand"][b] == x[:, None]] = q_bad
+            else:
+                q[b, np.arange(3), x] = q_bad
+        if b & 48 == 0:  # many entries of both
+            a["P"][b][rng.random((4, V)) < 0.3] = p_bad
+            q[b][rng.random(q[b].shape) < 0.3] = q_bad
+    check(dsp, a)
+    a["u_accept"][:] = 0.0
+    check(dsp, a)
+
+
+def test_acceptance_probability_of_every_row_without_mass(dsp):
+    """The rows of test_rows_without_mass, all compared."""
+    a = make(10, 16, 3, 263)
+    a["tokens"][2:5] = 7
+    a["P"][2, :, 7], a["P"][3, :, 7], a["P"][4, :, 7] = 0.0, np.nan, -1.0
+    a["Q"][5], a["Q"][6] = 0.0, np.nan
+    a["Q"][7, :, ::2] = np.inf
+    a["P"][8, :, ::3], a["P"][9, :, ::3], a["P"][10, :, ::2] = np.inf, np.nan, -0.5
+    a["tokens"][7:11] = 6
+    check(dsp, a)
+
+
 def test_tiny_mass_decides(dsp):
     """A row of one large and many rare tokens: the draw lands among the rare ones, whose
     probabilities a 32-bit running sum would lose beside the large one."""

@@ -109,6 +109,29 @@ def test_verification_edge_rows():
     assert (acc[0], nxt[0], prob[0, 0]) == (0, 1, 0.5)
 
 
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf, -0.5])
+def test_verification_of_entries_that_are_no_probabilities(bad):
+    """A drafted token whose p is no probability is rejected (0); one whose q is negative counts
+    as undrafted, and one whose q is infinite or NaN is rejected and not drawn either."""
+    p = np.array([[[0.5, 0.5], [0.5, 0.5]]])
+    q = np.array([[[0.5, 0.5]]])
+    token, u, u_draw = np.array([[0]]), np.array([[0.25]]), np.array([0.0])
+    broken = p.copy()
+    broken[0, 0, 0] = bad
+    with_q = lambda x: np.array([[[x, 0.5]]])  # noqa: E731
+    acc, nxt, prob = tr.verify_probs(broken, token, u, u_draw, Q=q)
+    assert (acc[0], nxt[0], prob[0, 0]) == (0, 1, 0.0)
+    acc, nxt, prob = tr.verify_probs(p, token, u, u_draw, Q=with_q(bad))
+    assert (acc[0], prob[0, 0]) == ((1, 1.0) if bad < 0 else (0, 0.0))
+    # both: rejected, and the target's other token is drawn, its own mass being left
+    acc, nxt, prob = tr.verify_probs(broken, token, u, u_draw, Q=with_q(bad))
+    assert (acc[0], nxt[0], prob[0, 0]) == (0, 1, 0.0)
+    # a negative q adds nothing to what is left over
+    acc, nxt, _ = tr.verify_probs(np.array([[[0.0, 0.5, 0.5], [1.0, 0.0, 0.0]]]), token, u, np.array([0.6]),
+                                  Q=np.array([[[0.5, -8.0, 0.0]]]))
+    assert (acc[0], nxt[0]) == (0, 2)
+
+
 # ------------------------------------------------------------------ host-side refusals
 P = ctypes.c_void_p
 GOOD, ODD = P(0x1000), P(0x1002)
