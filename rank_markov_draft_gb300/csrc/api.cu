@@ -51,6 +51,7 @@ struct dspark_ctx {
   float* d_vp_sums = nullptr;
   int* d_vp_count = nullptr;             // [kVpMaxRequests]
   dspark::ScanSpan* d_spans = nullptr;   // [kScanSpanCount] segments of long recurrences
+  dspark::SmemOptIn opt_in;
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
   uint32_t epoch = 0;                    // last key epoch used
   int poisoned = 0;
@@ -145,6 +146,7 @@ dspark::ScanLaunch scan_launch(dspark_ctx* ctx) {
   c.spans = ctx->d_spans;
   c.num_sms = ctx->num_sms;
   c.launches = &ctx->last_launches;
+  c.opt_in = &ctx->opt_in;
   return c;
 }
 
@@ -1022,7 +1024,7 @@ int dspark_verify_probs(dspark_ctx* ctx, const float* P, const float* Q, const i
   a.status = ctx->d_status;
   a.sums = ctx->d_vp_sums;
   a.count = ctx->d_vp_count;
-  return cuda_status(dspark::launch_verify_probs(a, &ctx->last_launches,
+  return cuda_status(dspark::launch_verify_probs(a, ctx->opt_in, &ctx->last_launches,
                                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1081,7 +1083,7 @@ int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
   p += static_cast<size_t>(dspark::kLongMaxRows) * dspark::kMaxTeacher * 8;
   a.scratch.epoch = reinterpret_cast<uint32_t*>(p);
   a.scratch.done = a.scratch.epoch + 1;
-  return cuda_status(dspark::launch_distill(a, ctx->num_sms, &ctx->last_launches,
+  return cuda_status(dspark::launch_distill(a, ctx->num_sms, ctx->opt_in, &ctx->last_launches,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -1097,7 +1097,8 @@ int threads_for(int nv, int partial, int most, int least, int limit) {
 }
 
 template <typename T>
-cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStream_t stream) {
+cudaError_t dispatch(const DistillArgs& all, int num_sms, SmemOptIn& opt_in, int* launches,
+                     cudaStream_t stream) {
   constexpr int kVec = Row16<T>::kVec;
   // 16-byte vectors of a row: a row that starts off a boundary has one less
   const int body = all.V / kVec, body_least = std::max(0, (all.V - kVec + 1) / kVec);
@@ -1133,9 +1134,8 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStr
     return launch_short<T, 16, 2, 640, 1>(all, t, num_sms, stream);
   }
   const auto fn = distill_long_kernel<T>;
-  static const cudaError_t once = cudaFuncSetAttribute(
-      fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(LongSmem)));
-  if (once != cudaSuccess) return once;
+  cudaError_t e = opt_in(fn, static_cast<int>(sizeof(LongSmem)));
+  if (e != cudaSuccess) return e;
   for (int64_t n0 = 0; n0 < all.N; n0 += kLongMaxRows) {  // as many rows as there is scratch for
     DistillArgs a = all;
     a.N = std::min<int64_t>(kLongMaxRows, all.N - n0);
@@ -1175,7 +1175,7 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStr
     cfg.numAttrs = 1;
     const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.temperature));
     const Split split{S, (body + S - 1) / S, static_cast<uint32_t>((1ull << 32) / S + 1)};
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, c, split);
+    e = cudaLaunchKernelEx(&cfg, fn, a, c, split);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
@@ -1184,9 +1184,10 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, int* launches, cudaStr
 
 }  // namespace
 
-cudaError_t launch_distill(const DistillArgs& a, int num_sms, int* launches, cudaStream_t stream) {
-  return a.dtype == DSPARK_F32 ? dispatch<float>(a, num_sms, launches, stream)
-                               : dispatch<uint16_t>(a, num_sms, launches, stream);
+cudaError_t launch_distill(const DistillArgs& a, int num_sms, SmemOptIn& opt_in, int* launches,
+                           cudaStream_t stream) {
+  return a.dtype == DSPARK_F32 ? dispatch<float>(a, num_sms, opt_in, launches, stream)
+                               : dispatch<uint16_t>(a, num_sms, opt_in, launches, stream);
 }
 
 }  // namespace dspark

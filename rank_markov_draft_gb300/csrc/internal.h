@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "dspark.h"
+#include "smem_optin.h"
 
 namespace dspark {
 
@@ -248,7 +249,8 @@ struct VerifyProbsArgs {
 };
 constexpr int kVpMaxRequests = 1024;  // of one launch
 constexpr int kVpMaxCtas = 16;        // of a request
-cudaError_t launch_verify_probs(const VerifyProbsArgs& a, int* launches, cudaStream_t stream);
+cudaError_t launch_verify_probs(const VerifyProbsArgs& a, SmemOptIn& opt_in, int* launches,
+                                cudaStream_t stream);
 
 // ---- distillation from a teacher's top logits (distill.cu)
 constexpr int kMaxTeacher = 256;  // teacher tokens (and draft candidates) a row
@@ -278,7 +280,8 @@ struct DistillArgs {
   uint64_t timeout_ns;
   LongScratch scratch;
 };
-cudaError_t launch_distill(const DistillArgs& a, int num_sms, int* launches, cudaStream_t stream);
+cudaError_t launch_distill(const DistillArgs& a, int num_sms, SmemOptIn& opt_in, int* launches,
+                           cudaStream_t stream);
 
 // ---- the RNN head's recurrence over given sequences (rnn_scan.cu)
 struct RnnScanArgs {
@@ -313,7 +316,8 @@ constexpr size_t kScanSpanCount = static_cast<size_t>(kScanCtas) * 9 * 64;
 struct ScanLaunch {
   ScanSpan* spans;
   int num_sms;
-  int* launches;  // host: kernels launched (added to)
+  int* launches;      // host: kernels launched (added to)
+  SmemOptIn* opt_in;  // host: the context's
   // set by the launch
   int64_t blocks;  // of 32 lanes
   int W;           // warps that walk a block together

@@ -660,9 +660,8 @@ cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& 
   const auto fn = scan_kernel<Dir, T, kVec, kMode, kReset>;
   constexpr int kSmem =
       D::stages(kMode) * D::kWarps * (D::streams(kMode) * D::kSteps * 32 + 32 * kVec) * 4;
-  static const cudaError_t once =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (once != cudaSuccess) return once;
+  cudaError_t e = (*c.opt_in)(fn, kSmem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(D::kWarps * 32);
@@ -675,7 +674,7 @@ cudaError_t scan_launch(const typename Dir<T, kVec>::Args& a, const ScanLaunch& 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kMode == Mode::kSegments ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, c);
+  e = cudaLaunchKernelEx(&cfg, fn, a, c);
   if (e == cudaSuccess) *c.launches += 1;
   return e;
 }

@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(kVpThreads, 4)
 
 }  // namespace
 
-cudaError_t launch_verify_probs(const VerifyProbsArgs& all, int* launches, cudaStream_t stream) {
+cudaError_t launch_verify_probs(const VerifyProbsArgs& all, SmemOptIn& opt_in, int* launches,
+                                cudaStream_t stream) {
   // A CTA per 15,360 tokens, 16 at most; every segment a multiple of 4 tokens.  (Of 152k tokens, in
   // 5 / 6 / 8 / 10 / 16 CTAs: 128 dense rows 43.4 / 42.6 / 43.2 / 39.0 / 39.1 us, 256 rows with lists
   // 54.0 / 51.4 / 52.6 / 49.2 / 55.5 us.)
@@ -502,12 +503,8 @@ cudaError_t launch_verify_probs(const VerifyProbsArgs& all, int* launches, cudaS
                     reinterpret_cast<uintptr_t>(all.Q) % 16 == 0;
   const auto fn = wide ? verify_draw_kernel<true> : verify_draw_kernel<false>;
   constexpr int kSmem = kVpWarps * kVpRing * 2 * kVpSlot * 4;
-  static const cudaError_t once[2] = {
-      cudaFuncSetAttribute(verify_draw_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmem),
-      cudaFuncSetAttribute(verify_draw_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmem)};
-  if (once[wide ? 1 : 0] != cudaSuccess) return once[wide ? 1 : 0];
+  cudaError_t e = opt_in(fn, kSmem);
+  if (e != cudaSuccess) return e;
   for (int b0 = 0; b0 < all.B; b0 += kVpMaxRequests) {  // as many as there is scratch for
     VerifyProbsArgs a = all;
     const size_t rows = static_cast<size_t>(b0) * a.K;
@@ -523,7 +520,6 @@ cudaError_t launch_verify_probs(const VerifyProbsArgs& all, int* launches, cudaS
     a.n_acc += b0;
     a.next_token += b0;
     if (a.accept_prob != nullptr) a.accept_prob += rows;
-    cudaError_t e = cudaSuccess;
     if (ctas > 1) {
       verify_tests_kernel<<<(a.B + 3) / 4, 128, 0, stream>>>(a);
       e = cudaGetLastError();
