@@ -488,7 +488,9 @@ typedef enum dspark_dtype { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
  *   KL = sum_i p_i ln(p_i / q_i) + rho ln(rho / q_rest)
  *   TV = (sum_i |p_i - q_i| + |rho - q_rest|) / 2
  *   loss = row_weight (alpha_kl KL + alpha_tv TV);  grad = d loss / d logits
- * (sgn(0) = 0 at TV's kinks; KL's teacher entropy is included, so equality gives 0).
+ * (KL's teacher entropy is included, so equality gives 0; sgn(0) = 0 at TV's kinks, where p
+ * and q are told apart down to some 1e-6 of themselves: the sums are of 32 bits, and a
+ * nearer tie may fall either way).
  *   logits [N, V] of type dtype, rows ld elements apart (ld >= V)
  *   teacher_ids [N, k] int32, teacher_logits [N, k] fp32; 1 <= k <= 256.  Negative ids
  *     are empty slots, of equal ids the first counts; ids >= V are reported as

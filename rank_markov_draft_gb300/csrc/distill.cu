@@ -164,8 +164,11 @@ struct Row16<uint16_t> {
   }
 };
 
-// The sign of q - p where 32 bits cannot tell: TV's derivative jumps there, so the two sides
-// are compared in 64 bits (rare: one slot in 1e5).
+// The sign of q - p, where TV's derivative jumps.  Where the slot's own exponentials and products in
+// 32 bits could hide it (rare: one slot in 1e5) they are taken in 64; the row's sums stay those of 32
+// bits, a few 1e-7 off, so a nearer tie falls either way, all slots of a row alike.  (So it does by
+// the roundings of the logits and of the teacher's rest themselves.  Sums in 64 bits as well cost
+// short rows of 128 slots 4 to 10%.)
 __device__ __noinline__ float sign64(float s, float top, float total, float t, float t_top,
                                      float sum_t, float rho, float T) {
   const double q = exp((static_cast<double>(s) - top) / T) / total;
@@ -246,7 +249,7 @@ struct RowEvents {
     const float inv = 1.f / total, p_scale = (1.f - rho) / r.sum_t;
     const float ratio = log2f(total) - log2f(r.sum_t) + log2f(1.f - rho);
     q_rest = out_part * inv;
-    sgn_r = sign_of(q_rest, rho);
+    sgn_r = sign_of(q_rest, rho);  // (all it is made of are the sums)
     S = kl = tv = 0.f;
     for (int j = lane; j < a.k; j += 32) {
       const float tj = t[j], sj = s[j];

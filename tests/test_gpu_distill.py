@@ -195,6 +195,39 @@ def test_equal_student_and_teacher(dsp):
     assert out["grad"].abs().max() <= 2 * 2 * E
 
 
+# 39001 logits are a long row.
+@pytest.mark.parametrize("V", [500, 39001])
+def test_signs_next_to_tvs_kinks(dsp, V):
+    """p and q of every event nearly equal: slots 4e-6 apart, the rest 2e-5.  What decides are sums
+    of 32 bits.  A slots' sum: exponentials off by 2^-22, of exponents up to 2 log2 e with three
+    roundings, and at most 13 additions, so 2^-22 + (3 * 2 + 13) 2^-24 = 1.4e-6, two of them
+    2.8e-6.  The outside's: exponents up to 14 (3 * 14 * ln 2 * 2^-24 = 1.7e-6), at most 90 additions
+    a lane and ten on the way together, 7.9e-6 in all, of which a slot's q feels the outside's
+    share of the whole, below a tenth."""
+    N, k = 40, 64
+    a = make(43, N, V, k, torch.float32, spread=1.0)
+    rng = np.random.default_rng(44)
+    at = a["ids"].astype(np.int64)
+    a["x"].scatter_(1, torch.from_numpy(at), torch.from_numpy(rng.uniform(9, 11, (N, k)).astype(np.float32)))
+    x = a["x"].double().numpy()
+    q = np.exp(x) / np.exp(x).sum(1, keepdims=True)
+    side = rng.choice([-1.0, 1.0], (N, k))
+    side[:, ::2] = -side[:, 1::2]  # as many above as below, of all weights
+    s = np.take_along_axis(x, at, 1)
+    a["t"] = (s + 8e-6 * side).astype(np.float32)
+    qs = np.take_along_axis(q, at, 1)
+    a["rho"] = ((1 - qs.sum(1)) * (1 + 2.5e-5 * rng.choice([-1.0, 1.0], N))).astype(np.float32)
+    t = a["t"].astype(np.float64)
+    p = np.exp(t) / np.exp(t).sum(1, keepdims=True) * (1 - a["rho"].astype(np.float64))[:, None]
+    # (the rest's step moves every slot by a part of its own)
+    far = np.abs(p / qs - 1) >= 4e-6
+    rows = np.flatnonzero(far.all(1))
+    assert rows.size >= N // 4 and (1 - qs.sum(1)).max() < 0.1 and (np.abs(a["rho"] / (1 - qs.sum(1)) - 1) >= 2e-5).all()
+    assert (p < qs)[rows].any() and (p > qs)[rows].any()
+    out = call(dsp, a, temperature=1.0)
+    compare(a, out, rows=rows, temperature=1.0)
+
+
 def test_gradient_equals_differences(dsp):
     """The call's own loss, differenced by its own logits (32 bits: steps of 2^-6)."""
     a = make(38, 1, 12, 4, torch.float32)
