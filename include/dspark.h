@@ -495,7 +495,8 @@ typedef enum dspark_dtype { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
  *   teacher_ids [N, k] int32, teacher_logits [N, k] fp32; 1 <= k <= 256.  Negative ids
  *     are empty slots, of equal ids the first counts; ids >= V are reported as
  *     DSPARK_ERR_DEVICE_OOB and skipped
- *   teacher_rest [N] fp32 in [0, 1] (clamped; NULL: 0), row_weight [N] fp32 (NULL: 1)
+ *   teacher_rest [N] fp32 in [0, 1] (clamped; a NaN makes its row NaN; NULL: 0),
+ *     row_weight [N] fp32 (NULL: 1)
  *   T = temperature > 0; alpha_kl, alpha_tv finite
  * Outputs loss [N] fp32, tv [N] fp32 (NULL: not written; 1 - tv is the acceptance
  * label of the row), grad [N, V] of type dtype, rows ld_grad apart (NULL: loss only;

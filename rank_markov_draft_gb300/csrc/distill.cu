@@ -229,7 +229,8 @@ struct SlotStats {
   float t_top, s_top, sum_t, sum_s, rho;
 };
 __device__ __forceinline__ float teacher_rest(const DistillArgs& a, int64_t n) {
-  return a.teacher_rest != nullptr ? fminf(fmaxf(__ldg(a.teacher_rest + n), 0.f), 1.f) : 0.f;
+  const float rho = a.teacher_rest != nullptr ? __ldg(a.teacher_rest + n) : 0.f;
+  return rho < 0.f ? 0.f : (rho > 1.f ? 1.f : rho);  // (a NaN stays, and makes its row NaN)
 }
 
 // A row's events (one warp).  t, s, g: the slots' teacher and student logits, their gradients on

@@ -135,6 +135,18 @@ def test_nan_stays_in_its_row(dsp):
     compare(a, out, rows=[0, 2, 4])
 
 
+@pytest.mark.parametrize("V", [901, 39001])
+def test_teachers_rest_that_is_no_probability(dsp, V):
+    """NaN goes through to its row's loss and gradient; the rest is clamped to [0, 1]."""
+    a = make(45, 5, V, 6, torch.float32)
+    a["rho"][:] = (0.1, np.nan, -0.5, 1.5, -np.inf)
+    out = call(dsp, a)
+    assert torch.isnan(out["loss"]).tolist() == torch.isnan(out["tv"]).tolist() == [False, True, False, False, False]
+    assert torch.isnan(out["grad"]).all(1).tolist() == [False, True, False, False, False]
+    compare(a, out, rows=[0, 2, 3, 4])
+    assert torch.isnan(call(dsp, a, grad=False)["loss"]).tolist() == [False, True, False, False, False]
+
+
 def test_rows_of_no_weight_are_not_read(dsp):
     a = make(33, 6, 777, 5, torch.bfloat16)
     a["w"][[0, 4]] = 0.0
