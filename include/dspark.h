@@ -117,7 +117,8 @@ int dspark_get_status(dspark_ctx* ctx, int* device_status);
  * the knob off and timeout_ms <= 0 restores the default limit (2000 ms). */
 int dspark_debug_set(dspark_ctx* ctx, int cta, int timeout_ms);
 
-/* Testing knob: the next draft-kernel launch through this context asks the
+/* Testing knob: the next draft-kernel launch (or the launches of the next
+ * dspark_distill, where its rows are long) through this context asks the
  * CUDA runtime for 1 KB more dynamic shared memory than the kernel allows, so
  * the runtime refuses it on the host: the call returns DSPARK_ERR_CUDA, that
  * launch enqueues nothing, the refusal's error is cleared from the CUDA

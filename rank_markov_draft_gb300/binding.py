@@ -241,7 +241,8 @@ class Context:
         _check(self.lib.dspark_debug_set(self.handle, cta, timeout_ms), "dspark_debug_set")
 
     def refuse_next_launch(self):
-        """The next draft-kernel launch is refused by the CUDA runtime (a test aid)."""
+        """The next draft or long-row distillation launch is refused by the CUDA runtime (a test
+        aid)."""
         _check(self.lib.dspark_debug_refuse_next_launch(self.handle),
                "dspark_debug_refuse_next_launch")
 

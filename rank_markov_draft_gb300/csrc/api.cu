@@ -56,7 +56,7 @@ struct dspark_ctx {
   uint32_t epoch = 0;                    // last key epoch used
   int poisoned = 0;
   int debug_skip_cta = -1;
-  bool debug_refuse_launch = false;  // the next draft launch asks for too much shared memory
+  bool debug_refuse_launch = false;  // the next draft or distillation asks for too much shared memory
   uint64_t timeout_ns = dspark::kDefaultTimeoutNs;
   int last_launches = 0;
   unsigned long long* trace = nullptr;  // caller's device buffer for the next draft's phase trace
@@ -193,7 +193,13 @@ int check_ctx(dspark_ctx* ctx) {
   return DSPARK_OK;
 }
 
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA; }
+// A refused launch leaves its (non-sticky) error as the thread's last one: cleared, so that the next
+// call's check does not see it again.
+int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return DSPARK_OK;
+  (void)cudaGetLastError();
+  return DSPARK_ERR_CUDA;
+}
 
 // Next key epoch; keys of older epochs always lose an atomicMax against it.
 int next_epoch(dspark_ctx* ctx, cudaStream_t stream, uint32_t* epoch) {
@@ -1083,7 +1089,10 @@ int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
   p += static_cast<size_t>(dspark::kLongMaxRows) * dspark::kMaxTeacher * 8;
   a.scratch.epoch = reinterpret_cast<uint32_t*>(p);
   a.scratch.done = a.scratch.epoch + 1;
-  return cuda_status(dspark::launch_distill(a, ctx->num_sms, ctx->opt_in, &ctx->last_launches,
+  const uint32_t extra = ctx->debug_refuse_launch ? 1024u : 0u;
+  ctx->debug_refuse_launch = false;
+  return cuda_status(dspark::launch_distill(a, ctx->num_sms, extra, ctx->opt_in,
+                                            &ctx->last_launches,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 

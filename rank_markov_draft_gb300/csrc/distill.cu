@@ -1101,8 +1101,8 @@ int threads_for(int nv, int partial, int most, int least, int limit) {
 }
 
 template <typename T>
-cudaError_t dispatch(const DistillArgs& all, int num_sms, SmemOptIn& opt_in, int* launches,
-                     cudaStream_t stream) {
+cudaError_t dispatch(const DistillArgs& all, int num_sms, uint32_t extra_smem, SmemOptIn& opt_in,
+                     int* launches, cudaStream_t stream) {
   constexpr int kVec = Row16<T>::kVec;
   // 16-byte vectors of a row: a row that starts off a boundary has one less
   const int body = all.V / kVec, body_least = std::max(0, (all.V - kVec + 1) / kVec);
@@ -1170,7 +1170,7 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, SmemOptIn& opt_in, int
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * num_sms);
     cfg.blockDim = dim3(kLongThreads);
-    cfg.dynamicSmemBytes = sizeof(LongSmem);
+    cfg.dynamicSmemBytes = sizeof(LongSmem) + extra_smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -1188,10 +1188,11 @@ cudaError_t dispatch(const DistillArgs& all, int num_sms, SmemOptIn& opt_in, int
 
 }  // namespace
 
-cudaError_t launch_distill(const DistillArgs& a, int num_sms, SmemOptIn& opt_in, int* launches,
-                           cudaStream_t stream) {
-  return a.dtype == DSPARK_F32 ? dispatch<float>(a, num_sms, opt_in, launches, stream)
-                               : dispatch<uint16_t>(a, num_sms, opt_in, launches, stream);
+cudaError_t launch_distill(const DistillArgs& a, int num_sms, uint32_t extra_smem,
+                           SmemOptIn& opt_in, int* launches, cudaStream_t stream) {
+  return a.dtype == DSPARK_F32
+             ? dispatch<float>(a, num_sms, extra_smem, opt_in, launches, stream)
+             : dispatch<uint16_t>(a, num_sms, extra_smem, opt_in, launches, stream);
 }
 
 }  // namespace dspark

@@ -280,8 +280,9 @@ struct DistillArgs {
   uint64_t timeout_ns;
   LongScratch scratch;
 };
-cudaError_t launch_distill(const DistillArgs& a, int num_sms, SmemOptIn& opt_in, int* launches,
-                           cudaStream_t stream);
+// extra_smem: testing, beyond what a long row's launch may have
+cudaError_t launch_distill(const DistillArgs& a, int num_sms, uint32_t extra_smem,
+                           SmemOptIn& opt_in, int* launches, cudaStream_t stream);
 
 // ---- the RNN head's recurrence over given sequences (rnn_scan.cu)
 struct RnnScanArgs {

@@ -111,6 +111,32 @@ def test_refused_launch_returns_cuda_error_and_enqueues_nothing():
         assert torch.equal(again["logprobs"], clean["logprobs"])
 
 
+def _rows(N, V, k=8):
+    gen = torch.Generator("cuda").manual_seed(V)
+    return (torch.randn(N, V, generator=gen, device="cuda"),
+            torch.randint(0, V, (N, k), generator=gen, device="cuda", dtype=torch.int32),
+            torch.randn(N, k, generator=gen, device="cuda"))
+
+
+def test_refused_distillation_leaves_no_error_behind():
+    """A refused launch of long rows is reported by its own call alone: the calls after it, which
+    ask the runtime for its last error, run, and the refused call's outputs are untouched."""
+    long, short = _rows(3, 40000), _rows(3, 1000)
+    with binding.Context(0, B_max=1, V_max=8, K_max=1) as ctx:
+        clean = [binding.distill(ctx, *a) for a in (long, short)]
+        loss, grad = torch.full((3,), -7.0, device="cuda"), torch.full_like(long[0], -7.0)
+        ctx.refuse_next_launch()
+        with pytest.raises(binding.DSparkError) as err:
+            binding.dspark_distill(ctx, *long, 8, None, None, 3, 40000, 1.0, 0.1, 0.9, loss, None, grad)
+        assert err.value.code == binding.CUDA and ctx.last_launches == 0
+        again = [binding.distill(ctx, *a) for a in (short, long)][::-1]
+        torch.cuda.synchronize()
+        assert ctx.status() == 0
+        assert bool((loss == -7).all()) and bool((grad == -7).all())
+        for a, c in zip(again, clean):
+            assert all(torch.equal(a[n], c[n]) for n in c)
+
+
 def _target(rng, U):
     B, K, V = U.shape
     P = np.empty((B, K + 1, V), np.float32)
