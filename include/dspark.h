@@ -113,8 +113,10 @@ int dspark_get_status(dspark_ctx* ctx, int* device_status);
 
 /* Testing knob: make CTA `cta` skip its grid-barrier arrival at step 0 in the
  * next draft launch (so every CTA's bounded wait runs out and the kernel exits
- * with DSPARK_ERR_TIMEOUT), with waits limited to timeout_ms.  cta = -1 turns
- * the knob off and timeout_ms <= 0 restores the default limit (2000 ms). */
+ * with DSPARK_ERR_TIMEOUT), or the sums of its first segments in the next
+ * dspark_distill of long rows (so the waits for these rows run out), with
+ * waits limited to timeout_ms.  Covers one call.  cta = -1 turns the knob off and
+ * timeout_ms <= 0 restores the default limit (2000 ms). */
 int dspark_debug_set(dspark_ctx* ctx, int cta, int timeout_ms);
 
 /* Testing knob: the next draft-kernel launch (or the launches of the next

@@ -1080,6 +1080,8 @@ int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
   a.grad = grad;
   a.status = ctx->d_status;
   a.timeout_ns = ctx->timeout_ns;
+  a.debug_skip_cta = ctx->debug_skip_cta;
+  ctx->debug_skip_cta = -1;  // covers one call
   uint8_t* p = ctx->d_distill;
   a.scratch.part = reinterpret_cast<unsigned long long*>(p);
   p += static_cast<size_t>(dspark::kLongMaxRows) * dspark::kLongMaxSegments * 16;

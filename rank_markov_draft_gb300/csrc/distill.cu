@@ -982,7 +982,8 @@ __global__ void __launch_bounds__(kLongThreads, 2)
         }
         const float top = warp_max(m);
         sum = warp_sum(sum * part_scale(m, top, c));
-        if (lane == 0) {
+        const bool skip = task == 0 && static_cast<int>(blockIdx.x) == a.debug_skip_cta;
+        if (lane == 0 && !skip) {
           unsigned long long* p = x.part + (g.n * kLongMaxSegments + g.index) * 2;
           publish(p, tag, top);
           publish(p + 1, tag, sum);

@@ -278,6 +278,7 @@ struct DistillArgs {
   void* grad;                   // [N, V] of dtype, rows ld_grad apart, or null
   int* status;
   uint64_t timeout_ns;
+  int debug_skip_cta;           // long rows: the CTA that publishes no first sums (-1: none)
   LongScratch scratch;
 };
 // extra_smem: testing, beyond what a long row's launch may have

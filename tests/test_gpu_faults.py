@@ -137,6 +137,39 @@ def test_refused_distillation_leaves_no_error_behind():
             assert all(torch.equal(a[n], c[n]) for n in c)
 
 
+@pytest.mark.parametrize("N", [2, 300])  # fewer segments than warps; several rounds of them
+@pytest.mark.parametrize("grad", [True, False])
+def test_distillation_timeout_is_reported_and_recoverable(N, grad):
+    """The fault knob on the distillation of long rows: one CTA's first segments are summed but
+    not published, so the waits for their rows' sums, and for the coefficients of those rows,
+    run out after 200 ms; the kernel exits on its own, and after a reset the same call gives
+    the clean bits.  The knob covers that one call."""
+    a = _rows(N, 40000)
+    with binding.Context(0, B_max=1, V_max=8, K_max=1) as ctx:
+        clean = binding.distill(ctx, *a, grad=grad)
+        torch.cuda.synchronize()
+        assert ctx.status() == 0
+        ctx.debug_set(cta=0, timeout_ms=200)
+        binding.distill(ctx, *a, grad=grad)
+        torch.cuda.synchronize()          # returns: the kernel exited on its own
+        assert ctx.status() == binding.TIMEOUT
+        with pytest.raises(binding.DSparkError) as err:
+            binding.distill(ctx, *a, grad=grad)
+        assert err.value.code == binding.POISONED
+        ctx.reset()
+        for _ in range(2):
+            again = binding.distill(ctx, *a, grad=grad)
+            torch.cuda.synchronize()
+            assert ctx.status() == 0
+            assert all(torch.equal(again[n], clean[n]) for n in clean)
+        # a call of short rows, which wait for nothing, clears the knob as well
+        ctx.debug_set(cta=0, timeout_ms=200)
+        binding.distill(ctx, *_rows(2, 100))
+        again = binding.distill(ctx, *a, grad=grad)
+        torch.cuda.synchronize()
+        assert ctx.status() == 0 and torch.equal(again["loss"], clean["loss"])
+
+
 def _target(rng, U):
     B, K, V = U.shape
     P = np.empty((B, K + 1, V), np.float32)
