@@ -50,7 +50,7 @@ struct dspark_ctx {
   // draws from given probabilities: segment sums, CTAs done (zero between calls)
   float* d_vp_sums = nullptr;
   int* d_vp_count = nullptr;             // [kVpMaxRequests]
-  dspark::ScanSpan* d_spans = nullptr;   // [kScanSpanCount] segments of long recurrences
+  dspark::ScanSpan* d_spans = nullptr;   // [scan_span_count] segments of long recurrences
   dspark::SmemOptIn opt_in;
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
   uint32_t epoch = 0;                    // last key epoch used
@@ -508,7 +508,7 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
             cudaMalloc(&ctx->d_vp_sums, sizeof(float) * 2 * 8 * dspark::kVpMaxCtas *
                                             dspark::kVpMaxRequests) == cudaSuccess &&
             cudaMalloc(&ctx->d_vp_count, sizeof(int) * dspark::kVpMaxRequests) == cudaSuccess &&
-            cudaMalloc(&ctx->d_spans, sizeof(dspark::ScanSpan) * dspark::kScanSpanCount) ==
+            cudaMalloc(&ctx->d_spans, sizeof(dspark::ScanSpan) * dspark::scan_span_count(ctx->num_sms)) ==
                 cudaSuccess;
   ok = ok && cudaMemset(ctx->d_status, 0, sizeof(int)) == cudaSuccess &&
        cudaMemset(ctx->d_bar, 0, sizeof(uint32_t)) == cudaSuccess &&
@@ -569,7 +569,9 @@ int dspark_ctx_reset(dspark_ctx* ctx, dspark_stream_t stream) {
             cudaMemsetAsync(ctx->d_v_fail, 0, sizeof(unsigned long long) * ctx->B_max, s) ==
                 cudaSuccess &&
             cudaMemsetAsync(ctx->d_v_count, 0, sizeof(int) * ctx->B_max, s) == cudaSuccess &&
-            cudaMemsetAsync(ctx->d_distill, 0, dspark::kLongScratchBytes, s) == cudaSuccess &&
+            // (the tag of the last launch goes on, so words of earlier ones stay old)
+            cudaMemsetAsync(ctx->d_distill + dspark::kLongScratchBytes - sizeof(uint32_t), 0,
+                            sizeof(uint32_t), s) == cudaSuccess &&
             cudaMemsetAsync(ctx->d_vp_count, 0, sizeof(int) * dspark::kVpMaxRequests, s) ==
                 cudaSuccess;
   if (!ok) return DSPARK_ERR_CUDA;

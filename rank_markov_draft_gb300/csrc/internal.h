@@ -260,7 +260,7 @@ struct LongScratch {               // rows of several segments
   unsigned long long* coef;        // [kLongMaxRows][3] tagged coefficient, maximum, any outside
   int2* list;                      // [kLongMaxRows][kMaxTeacher] tokens and their gradients
   uint32_t* epoch;                 // tag of the last launch
-  uint32_t* done;                  // CTAs done, zero between launches
+  uint32_t* done;                  // CTAs done, zero between launches (the last word)
 };
 constexpr size_t kLongScratchBytes =
     static_cast<size_t>(kLongMaxRows) * (kLongMaxSegments * 16 + 3 * 8 + kMaxTeacher * 8) + 8;
@@ -311,10 +311,9 @@ struct RnnScanGradArgs {
 struct ScanSpan {
   float A, S;
 };
-// Scratch of sequences cut into segments: for each CTA (of at most kScanCtas) its span and the
-// spans before each of its (at most 8) warps, of 64 channels each.
-constexpr int kScanCtas = 1024;
-constexpr size_t kScanSpanCount = static_cast<size_t>(kScanCtas) * 9 * 64;
+// Scratch of sequences cut into segments: for each CTA (two an SM) its span and the spans before
+// each of its (at most 8) warps, of 64 channels each.
+constexpr size_t scan_span_count(int num_sms) { return static_cast<size_t>(2 * num_sms) * 9 * 64; }
 struct ScanLaunch {
   ScanSpan* spans;
   int num_sms;

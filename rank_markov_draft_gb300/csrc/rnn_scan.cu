@@ -694,8 +694,7 @@ cudaError_t scan_as(const typename Dir<T, kVec>::Args& a, ScanLaunch c, cudaStre
   // 16.8 M steps of fp32 channels in 8 / 38 / 76 / 152 / 304 blocks, forward and backward: segments
   // 82 and 95 us throughout, walking 1081 / 234 / 121 / 64 / 53 and 1504 / 325 / 166 / 86 / 70 us.
   if (8 * c.blocks <= 3 * room && places >= 4 * kWarps) {
-    int64_t per = std::min<int64_t>(room / c.blocks, kScanCtas / c.blocks);  // CTAs a block
-    per = std::min(per, places / (2 * kWarps));
+    int64_t per = std::min(room / c.blocks, places / (2 * kWarps));  // CTAs a block
     c.segs = static_cast<int>(per * kWarps);
     c.seg = static_cast<int>((places + c.segs - 1) / c.segs);
     const cudaError_t e =

@@ -170,6 +170,26 @@ def test_distillation_timeout_is_reported_and_recoverable(N, grad):
         assert ctx.status() == 0 and torch.equal(again["loss"], clean["loss"])
 
 
+def test_a_reset_between_distillations_and_replays():
+    """The words that a launch of long rows hands between its CTAs carry its tag, which a reset
+    leaves where it is: calls and replays before and after give the same bits."""
+    a = _rows(5, 40000)
+    with binding.Context(0, B_max=1, V_max=8, K_max=1) as ctx:
+        clean = binding.distill(ctx, *a)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = binding.distill(ctx, *a)
+        for _ in range(3):
+            ctx.reset()
+            again = binding.distill(ctx, *a)
+            for t in out.values():
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert ctx.status() == 0
+            assert all(torch.equal(again[n], clean[n]) and torch.equal(out[n], clean[n]) for n in clean)
+
+
 def _target(rng, U):
     B, K, V = U.shape
     P = np.empty((B, K + 1, V), np.float32)
