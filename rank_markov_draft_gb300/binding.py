@@ -178,13 +178,18 @@ def _shape(t: Optional[torch.Tensor], shape, name: str):
         raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
 
 
+# The handle that torch.cuda.current_stream(device).cuda_stream gives, without making the object
+# (some 1 us a call); a torch without this call makes it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream, device):
     if stream is None:
         index = device if isinstance(device, int) else device.index
         if index is None:
             index = torch.cuda.current_device()
-        # the handle that torch.cuda.current_stream(device).cuda_stream gives, without the object
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _raw_stream(index)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
