@@ -501,12 +501,13 @@ typedef enum dspark_dtype { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
  *   teacher_rest [N] fp32 in [0, 1] (clamped; a NaN makes its row NaN; NULL: 0),
  *     row_weight [N] fp32 (NULL: 1)
  *   T = temperature > 0; alpha_kl, alpha_tv finite
- * Outputs loss [N] fp32, tv [N] fp32 (NULL: not written; 1 - tv is the acceptance
- * label of the row), grad [N, V] of type dtype, rows ld_grad apart (NULL: loss only;
- * may be logits itself, with the same ld).  A row of weight 0 is not read, and it, a row
- * without a teacher token of finite logit and a row whose student logits are all -inf
- * get loss 0, tv 0 and a zero gradient.  V <= 2^18, any V; pointers aligned to their
- * element size.  Equal inputs at equal addresses modulo 16 give equal bits.  Rows of up
+ * Outputs loss [N] fp32, tv [N] fp32 (NULL: not written; the rest being one event, it is
+ * at most the TV over the vocabulary, so 1 - tv is at least the acceptance label that
+ * dspark_accept_label gives, and no label to train a confidence head on), grad [N, V] of
+ * type dtype, rows ld_grad apart (NULL: loss only; may be logits itself, with the same ld).
+ * A row of weight 0 is not read, and it, a row without a teacher token of finite logit and a
+ * row whose student logits are all -inf get loss 0, tv 0 and a zero gradient.  V <= 2^18,
+ * any V; pointers aligned to their element size.  Equal inputs at equal addresses modulo 16 give equal bits.  Rows of up
  * to 155,648 bytes: one kernel, no scratch.  Longer ones: a cooperative kernel per 2048
  * rows, whose blocks hand sums to one another through the context's scratch; a wait for
  * one that passes the context's time limit is reported as DSPARK_ERR_TIMEOUT. */

@@ -41,6 +41,19 @@ def test_distill_of_equal_distributions_is_zero():
     assert abs(loss) < 1e-14 and tv < 1e-14 and np.abs(g).max() < 1e-15
 
 
+def test_distill_tv_is_at_most_the_vocabularys():
+    """One event for the rest hides what moves inside it: 1 - tv is at least the acceptance
+    probability sum min(p, q), and equals it where the teacher's list is the vocabulary."""
+    rng = np.random.default_rng(4)
+    for k in (1, 3, 11):
+        x, t = rng.normal(0, 2, 11), rng.normal(0, 2, 11)
+        q, p = np.exp(x) / np.exp(x).sum(), np.exp(t) / np.exp(t).sum()
+        ids = np.argsort(-t)[:k]
+        accept = np.minimum(p, q).sum()
+        tv = tr.distill_row(x, ids, t[ids], 1 - p[ids].sum(), 1.0, 1.0, 1.0, 1.0)[1]
+        assert 1 - tv >= accept - 1e-15 and (k == 11) == (abs(1 - tv - accept) < 1e-12)
+
+
 def test_distill_rows_without_anything_are_zero():
     x, ids, t, rho = _row(5)
     for case in (dict(w=0.0), dict(ids=np.full_like(ids, -1)), dict(t=np.full_like(t, -np.inf)),
