@@ -507,10 +507,11 @@ typedef enum dspark_dtype { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
  * type dtype, rows ld_grad apart (NULL: loss only; may be logits itself, with the same ld).
  * A row of weight 0 is not read, and it, a row without a teacher token of finite logit and a
  * row whose student logits are all -inf get loss 0, tv 0 and a zero gradient.  V <= 2^18,
- * any V; pointers aligned to their element size.  Equal inputs at equal addresses modulo 16 give equal bits.  Rows of up
- * to 155,648 bytes: one kernel, no scratch.  Longer ones: a cooperative kernel per 2048
- * rows, whose blocks hand sums to one another through the context's scratch; a wait for
- * one that passes the context's time limit is reported as DSPARK_ERR_TIMEOUT. */
+ * any V; pointers aligned to their element size.  Equal inputs at equal addresses modulo 16
+ * give equal bits.  Rows of up to 155,648 bytes: one kernel, no scratch.  Longer ones: a
+ * cooperative kernel per 2048 rows, whose blocks hand sums to one another through the
+ * context's scratch; a wait for one that passes the context's time limit is reported as
+ * DSPARK_ERR_TIMEOUT. */
 int dspark_distill(dspark_ctx* ctx, const void* logits, int dtype, int64_t ld,
                    const int32_t* teacher_ids, const float* teacher_logits, int k,
                    const float* teacher_rest, const float* row_weight, int64_t N, int V,

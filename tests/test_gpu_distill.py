@@ -394,6 +394,42 @@ def test_many_long_rows(dsp, dtype, V, grad):
     assert np.abs(host(out["tv"])[live] - host(alone["tv"])[pick][live]).max() <= 1e-5
 
 
+@pytest.mark.parametrize("dtype,V,N", [(torch.float32, 131075, 500), (torch.float32, 131072, 77), (torch.bfloat16, 151936, 600),
+                                       (torch.bfloat16, 78001, 2100)])
+@pytest.mark.parametrize("T", [1.3, 0.25])
+def test_every_gradient_of_many_long_rows(dsp, dtype, V, N, T):
+    """Many rounds of segments, up to 64 of a row: every element of every row, which has the
+    logits of one of eight and a weight of its own, against the 64-bit gradient times the weight;
+    weights of 1e6 bring coefficients above one, rows of none are zeros."""
+    rng = np.random.default_rng(V + N)
+    base = make(V, 8, V, 40, dtype)
+    pick = rng.integers(0, 8, N)
+    w = rng.uniform(0.1, 2, N).astype(np.float32)
+    w[::7] *= 1e6
+    w[rng.random(N) < 0.2] = 0.0
+    w[N // 3:N // 2] = 0.0
+    at = torch.from_numpy(pick).cuda()
+    x = base["x"].cuda()[at]
+    ids, t, rho = (dev(base[n][pick]) for n in ("ids", "t", "rho"))
+    out = binding.distill(dsp, x, ids, t, teacher_rest=rho, row_weight=dev(w), **KW | dict(temperature=T))
+    torch.cuda.synchronize()
+    assert dsp.status() == 0
+    del x
+    row = [tr.distill_row(base["x"][n].double().numpy(), base["ids"][n], base["t"][n], base["rho"][n], 1.0, T,
+                          KW["alpha_kl"], KW["alpha_tv"]) for n in range(8)]
+    want, bound = (torch.from_numpy(np.stack([r[i] for r in row])).cuda() for i in (2, 3))
+    for n in range(N):
+        if w[n] == 0:
+            assert not out["grad"][n].any() and float(out["loss"][n]) == 0, n
+            continue
+        g = want[pick[n]] * float(w[n])
+        bad = ~((out["grad"][n].double() - g).abs() <= bound[pick[n]] * float(w[n]) + HALF[dtype] * g.abs() * (1 + 1e-6) + 2.0 ** -126)
+        assert not bad.any(), (n, w[n], bad.nonzero()[:3].flatten().tolist())
+    loss, E = np.array([r[0] for r in row])[pick] * w, max(r[4] for r in row)
+    tol = w * (KW["alpha_kl"] * (2 + 2 * np.abs(loss / np.maximum(w, 1e-30)) / KW["alpha_kl"]) + 2 * KW["alpha_tv"]) * E
+    assert (np.abs(host(out["loss"]) - loss) <= tol).all()
+
+
 @pytest.mark.parametrize("V", [60000, 120000])
 def test_long_rows_on_a_side_stream_in_a_graph_and_repeated(dsp, V):
     a = make(61, 9, V, 8, torch.bfloat16)
