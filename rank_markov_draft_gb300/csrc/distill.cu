@@ -19,15 +19,19 @@
 //   over the rows; one warp of each holds no part of the row and prepares the next row's teacher
 //   slots (which count, the student's logits there, a bit map of their tokens) while the others
 //   stream the current one, so the dependent loads of the slots hide behind the row's.
-//   Long rows are cut into segments of 10 to 16 KB, one a warp.  A warp sums its segment of one
-//   round, then writes the gradient of its segment of the round before, which it reads again: the
-//   two readings are one round (23 to 38 MB over the chip) apart, so the second comes from L2.  Each
+//   Long rows are cut into segments of 7 to 22 KB (fewer rows into shorter ones, from 2 KB), one a
+//   warp.  A warp sums its segment of one round, then writes the gradient of its segment of the
+//   round before, which it reads again: the two readings are one round (18 to 55 MB over the chip)
+//   apart, so that the second may come from L2.  In fp32 it does, but for 7%, since the copies say
+//   what is read for the last time; in bf16 83% of it comes from DRAM.  Each
 //   segment's (maximum, sum) goes through memory to the row's service warp (one in each CTA),
 //   which joins them, finishes the row and publishes the coefficients; a round of work lies
 //   between, so nobody waits for long.  The launch is cooperative: all of its CTAs run.
-//   2048 x 151936 with gradient: fp32 447 us (5.6 TB/s, 83% of a copy's rate; 10% of the rows have
-//   no weight), bf16 271 us (4.6 TB/s), 1024 bf16 rows without 67 us (4.6 TB/s).  Instructions bound
-//   it: two exponentials and two conversions a logit at 16 warps an SM.
+//   2048 x 151936 with gradient: fp32 450 us (5.5 TB/s, 83% of a copy's rate, the 10% of the rows
+//   that have no weight counted as read), bf16 272 us (4.6 TB/s; what it moves, the second reading
+//   with it, is 84% of a copy's rate and bounds it: 47% of the issue slots are used), 1024 bf16 rows
+//   without 68 us (4.6 TB/s): neither DRAM nor the issue slots (59%) bound that one, but its eight
+//   units a warp, dealt out with the rows of no weight among them, and a short launch's start and end.
 // In both the teacher's tokens are left out of the outside sum by overwriting them with -inf on
 // chip, and their own gradients are written last, over what the stream wrote there.
 
@@ -611,7 +615,9 @@ constexpr int kLongThreads = kLongWarps * 32 + 32;
 constexpr int kLongEach = 4;                // vectors of a lane in a ring's slot
 constexpr int kLongSlot = 32 * kLongEach;   // vectors of a slot
 constexpr int kLongRing = 4;                // slots in shared memory, one worked on
-// Vectors of a segment at most.  A segment costs a warp some 500 instructions beside its logits,
+// Vectors of a segment that the rows' cut starts from; the count that divides the warps may then leave
+// up to 784 fp32 and 1408 bf16, and few rows are cut down to a slot's 128 (see the dispatch).  A
+// segment costs a warp some 500 instructions beside its logits,
 // but what is summed in a round has to be in L2 when the gradient reads it: 2048 x 151936 rows
 // took, cut in 32 / 38 / 64 segments, fp32 517 / 460 / 446 us and, in 16 / 19 / 24 / 32, bf16
 // 283 / 272 / 286 / 290 us (loss alone 70 / 68 / - / 73 us).
@@ -838,8 +844,8 @@ __global__ void __launch_bounds__(kLongThreads, 2)
     const uint32_t ring = smem_addr(&sm.ring[warp][0][lane]);
     constexpr uint32_t kSlotBytes = kLongSlot * 16;
     // the copies run ahead of the work by kLongRing - 1 slots, over the tasks' ends
-    // What is read for the last time leaves L2 first: 2048 x 151936 fp32 466 -> 446 us.  bf16, bound
-    // by its instructions, does without (271 against 291 us).
+    // What is read for the last time leaves L2 first: 2048 x 151936 fp32 466 -> 446 us, 34 -> 7% of
+    // the second reading from DRAM.  bf16 is faster without (271 against 291 us).
     constexpr bool kHint = sizeof(T) == 4;
     const uint64_t policy_again = l2_policy_evict_normal(), policy_last = l2_policy_evict_first();
     uint64_t f_policy = policy_last;

@@ -13,7 +13,7 @@
 //
 // Both directions are a recurrence x_t = a_t x_{t-1} + b_t, so a span of steps acts on the
 // value before it as x -> A x + S (A the product of its decays, S its end from zero).  A warp
-// works on 8 or 16 steps of 32 lanes at a time (a lane is 4 bytes of channels: two bf16 or one fp32;
+// works on 8 steps of 32 lanes at a time (a lane is 4 bytes of channels: two bf16 or one fp32;
 // lanes run over sequences and channels alike, so no channel count leaves lanes empty).  The
 // steps arrive in shared memory by asynchronous copies, the next units' while this one is
 // worked on, so loads are in flight all the time; a warp that does not start a sequence learns

@@ -22,8 +22,10 @@
 // cut into segments, one a warp of its CTAs; a thread's next reads are always on their way to
 // shared memory while it adds up the ones that have come.  The CTA of a request that ends last
 // joins the segments' sums, in order, and reads the one segment where the sum passes u R again.
-// 128 dense rows of 152k tokens (156 MB) take 39 us, 4.0 TB/s: the tests' dependent loads, the
-// start and the join of the last request are some 12 us beside the reads.
+// 128 dense rows of 152k tokens (156 MB) take 39 us, 4.0 TB/s, 256 with lists (as many bytes) 50:
+// the tests' dependent loads and the last request's join are a part of what is beside the reads; the
+// larger is that 1280 and 2560 CTAs run in 2.1 and 4.2 waves, each with its row's position, its
+// first reads, a fence and an atomic for eight slots of work a warp.
 // Not kept: clusters, which could exchange the sums through shared memory, left SMs empty (the
 // draw alone 41 us); warps that run on from segment to segment with a third launch that joins took
 // 46 us, the bookkeeping and the third launch costing more than the starts that they saved.
@@ -496,7 +498,8 @@ cudaError_t launch_verify_probs(const VerifyProbsArgs& all, SmemOptIn& opt_in, i
                                 cudaStream_t stream) {
   // A CTA per 15,360 tokens, 16 at most; every segment a multiple of 4 tokens.  (Of 152k tokens, in
   // 5 / 6 / 8 / 10 / 16 CTAs: 128 dense rows 43.4 / 42.6 / 43.2 / 39.0 / 39.1 us, 256 rows with lists
-  // 54.0 / 51.4 / 52.6 / 49.2 / 55.5 us.)
+  // 54.0 / 51.4 / 52.6 / 49.2 / 55.5 us.  Measured at these two batches alone: the rule does not look
+  // at B, and one request of 152k tokens has 10 CTAs.)
   const int ctas = std::min(kVpMaxCtas, (all.V + 15359) / 15360), segments = ctas * kVpWarps;
   const int seg = ((all.V + segments - 1) / segments + 3) & ~3;
   const bool wide = all.V % 4 == 0 && reinterpret_cast<uintptr_t>(all.P) % 16 == 0 &&
