@@ -23,9 +23,9 @@
 // shared memory while it adds up the ones that have come.  The CTA of a request that ends last
 // joins the segments' sums, in order, and reads the one segment where the sum passes u R again.
 // 128 dense rows of 152k tokens (156 MB) take 39 us, 4.0 TB/s, 256 with lists (as many bytes) 50:
-// the tests' dependent loads and the last request's join are a part of what is beside the reads; the
-// larger is that 1280 and 2560 CTAs run in 2.1 and 4.2 waves, each with its row's position, its
-// first reads, a fence and an atomic for eight slots of work a warp.
+// beside the reads stand the tests' dependent loads, the last request's join, and the starts and ends
+// of 1280 and 2560 CTAs in 2.1 and 4.2 waves, each with its row's position, its first reads, a fence
+// and an atomic for eight and four slots of work a warp.
 // Not kept: clusters, which could exchange the sums through shared memory, left SMs empty (the
 // draw alone 41 us); warps that run on from segment to segment with a third launch that joins took
 // 46 us, the bookkeeping and the third launch costing more than the starts that they saved.
