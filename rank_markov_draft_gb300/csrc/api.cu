@@ -14,6 +14,7 @@
 #include "dspark.h"
 #include "internal.h"
 #include "philox.cuh"
+#include "training.h"
 
 using dspark::DraftArgs;
 using dspark::DraftParams;

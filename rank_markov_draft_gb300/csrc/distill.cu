@@ -39,10 +39,12 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 
+#include "async_copy.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
 #include "rowscan.cuh"
 #include "sm103.cuh"
+#include "training.h"
 
 namespace dspark {
 namespace {

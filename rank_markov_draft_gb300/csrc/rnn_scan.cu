@@ -35,9 +35,11 @@
 #include <initializer_list>
 #include <cuda_bf16.h>
 
+#include "async_copy.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
 #include "sm103.cuh"
+#include "training.h"
 
 namespace dspark {
 namespace {

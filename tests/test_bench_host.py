@@ -110,3 +110,10 @@ def test_profiles_name_existing_sources_and_carry_their_figures():
         text = open(os.path.join(bench.ROOT, "profiles", summary)).read()
         assert re.search(r"kernel source hash:\s*`[0-9a-f]{16}`", text), summary
         assert re.search(r"dram bytes per launch:\s*`[0-9]+`", text), summary
+
+
+def test_the_bench_reports_the_traffic_of_every_profiled_workload():
+    """The profiled kernels' sources are those of the captures: what other operators need lives in
+    headers of its own, so that adding to them does not retire a profile."""
+    for workload in bench.PROFILES:
+        assert bench.ncu_traffic(workload), workload
