@@ -556,6 +556,105 @@ int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const 
                          int64_t ld_dza, int64_t ld_dzg, void* de, float* ds0,
                          dspark_stream_t stream);
 
+/* --------------------------------------------------------------------- */
+/* Training: embedding rows and their gradient                             */
+/* --------------------------------------------------------------------- */
+
+/* out[n] = scale * table[ids[n]]: the rows W1[x_{k-1}] that the heads read, for given
+ * tokens.  Source: DSpark explainer, "The Markov head" (B(x_{k-1}, .) = W1[x_{k-1}] W2);
+ * scale and types are this library's form.
+ *   table [V, D] of type table_dtype, rows ld_table elements apart
+ *   ids [N] int32: negative ids are padding (a row of zeros); ids >= V are reported as
+ *     DSPARK_ERR_DEVICE_OOB and give zeros
+ *   out [N, D] of type out_dtype, rows ld_out elements apart
+ * The product is formed in fp32 and rounded once.  Any N >= 0 (< 2^31), D >= 1; V <= 2^18;
+ * pointers aligned to their element size. */
+int dspark_embed(dspark_ctx* ctx, const void* table, int table_dtype, int64_t ld_table,
+                 const int32_t* ids, int64_t N, int V, int D, float scale, void* out,
+                 int out_dtype, int64_t ld_out, dspark_stream_t stream);
+
+/* The gradient of dspark_embed by its table: grad[v] = scale * sum_{n: ids[n] = v} de[n], added
+ * to grad[v] with accumulate (rows that no token names are then left alone) and stored without
+ * (such rows become zero).  Sums are of fp32, in an order that the ids alone fix: equal inputs
+ * give equal bits.
+ *   ids [N] as given to dspark_embed (negative: skipped; >= V: reported and skipped)
+ *   de [N, D] of type de_dtype, rows ld_de elements apart
+ *   grad [V, D] of type grad_dtype, rows ld_grad elements apart
+ * 0 <= N <= 2^20 (more rows: several calls with accumulate); otherwise as dspark_embed. */
+int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int de_dtype,
+                      int64_t ld_de, int64_t N, int V, int D, float scale, int accumulate,
+                      void* grad, int grad_dtype, int64_t ld_grad, dspark_stream_t stream);
+
+/* --------------------------------------------------------------------- */
+/* Training: the norm of all gradients and their clipping                  */
+/* --------------------------------------------------------------------- */
+
+/* norm = sqrt(sum over all tensors of g^2); out = g min(1, max_norm / (norm + 1e-6)).
+ * Source: none on the pages (the step that commonly precedes an optimiser's).
+ *   grads, numel, dtypes: HOST arrays of `count` device addresses, element counts and
+ *     dspark_dtypes (contiguous tensors; a count of 0 elements may have a NULL address)
+ *   out: HOST array of `count` addresses that receive the scaled tensors, in their types:
+ *     a tensor's own address scales it in place (where the factor is 1 it is not touched);
+ *     otherwise tensors must not overlap.  NULL: only the norm is computed, max_norm unread
+ *   norm: device fp32 scalar
+ * The host arrays are read during the call.  Squares are of fp32 (a gradient beyond 1e19 makes
+ * the norm infinite), their sums of 64 bits beyond a thread's own.  An infinite norm gives the
+ * factor 0 and a NaN one NaN, as the formula does.  max_norm >= 0; equal inputs give equal bits. */
+int dspark_clip_grads(dspark_ctx* ctx, const void* const* grads, const int64_t* numel,
+                      const int32_t* dtypes, int count, float max_norm, void* const* out,
+                      float* norm, dspark_stream_t stream);
+
+/* --------------------------------------------------------------------- */
+/* Training: linear layers with their epilogue, and their gradients        */
+/* --------------------------------------------------------------------- */
+
+typedef enum dspark_act {
+  DSPARK_ACT_NONE = 0,
+  DSPARK_ACT_SIGMOID = 1,
+  DSPARK_ACT_TANH = 2,
+  DSPARK_ACT_RELU = 3,
+  DSPARK_ACT_SILU = 4, /* z sigmoid(z) */
+  DSPARK_ACT_GELU = 5  /* z Phi(z), by the error function */
+} dspark_act;
+
+/* y = act(x W + bias) + residual: the heads' gates (sigmoid(h Wg), h Wa) for any sizes, and
+ * their calibrated logits U + s W2 for given states or embeddings.  Source: equivalence page,
+ * "What the two methods do" (gate of the hidden state; logits_k = U_k + W1[a]^T W2).
+ *   x [M, K], W [K, N] bf16, rows ld_x, ld_w elements apart; products summed in fp32
+ *   bias [N] fp32 (NULL: 0)
+ *   residual [M, N] of type residual_dtype, rows ld_residual apart (NULL: 0; may be y itself,
+ *     of the same type and distance)
+ *   y [M, N] of type y_dtype, rows ld_y apart
+ *   pre [M, N] of type y_dtype, rows ld_pre apart: x W + bias, for the gradient (NULL: not
+ *     written)
+ * Any M >= 0 (< 2^31), K, N >= 1; pointers aligned to their element size.  Equal inputs at equal
+ * addresses modulo 16 give equal bits.
+ * workspace: device memory of the caller, 256-byte aligned, of *workspace_bytes bytes (it must
+ * stay untouched until the call's work has run).  Where that is too little, *workspace_bytes is
+ * set to what the same call needs, nothing is enqueued and DSPARK_ERR_CAPACITY is returned; 0
+ * suffices (with NULL) where x and W have 16-byte aligned rows. */
+int dspark_linear(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16_t* W,
+                  int64_t ld_w, const float* bias, int act, const void* residual,
+                  int residual_dtype, int64_t ld_residual, int64_t M, int K, int N, void* y,
+                  int y_dtype, int64_t ld_y, void* pre, int64_t ld_pre, void* workspace,
+                  int64_t* workspace_bytes, dspark_stream_t stream);
+
+/* Gradients of dspark_linear: dz = dy act'(pre), dx = dz W^T, dW = x^T dz, dbias = sum_m dz
+ * (the residual's is dy).  dz is formed in fp32 and enters the products as bf16, or, where it is
+ * no bf16 number (dy of fp32, or an activation), as the sum of two (2^-17 of itself).
+ *   dy [M, N] of type dy_dtype, rows ld_dy apart; pre [M, N] of type pre_dtype, rows ld_pre
+ *     apart, as dspark_linear wrote it (read only with an activation; else it may be NULL)
+ *   dx [M, K] of dx_dtype, dW [K, N] of dw_dtype, dbias [N] fp32: each may be NULL (W is read
+ *     only for dx, x only for dW)
+ * Sizes, workspace and determinism as dspark_linear; *workspace_bytes of 0 suffices where x, W
+ * and dy have 16-byte aligned rows and dy is bf16 without an activation. */
+int dspark_linear_grad(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16_t* W,
+                       int64_t ld_w, const void* dy, int dy_dtype, int64_t ld_dy, int act,
+                       const void* pre, int pre_dtype, int64_t ld_pre, int64_t M, int K, int N,
+                       void* dx, int dx_dtype, int64_t ld_dx, void* dW, int dw_dtype,
+                       int64_t ld_dw, float* dbias, void* workspace, int64_t* workspace_bytes,
+                       dspark_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,10 +7,12 @@ The compute lives in ``csrc/`` (hand-written CUDA kernels behind the C ABI of
 
 from . import build  # noqa: F401
 from .binding import (  # noqa: F401
-    Confidence, Context, DSparkError, confidence, distill, gate, markov_draft, markov_logits,
-    rnn_scan, rnn_scan_grad, selector_scores, selector_walk, verify_probs,
+    Confidence, Context, DSparkError, clip_grads, confidence, distill, embed, embed_grad, gate,
+    grad_norm, linear, linear_grad, markov_draft, markov_logits, rnn_scan, rnn_scan_grad,
+    selector_scores, selector_walk, verify_probs,
 )
 
-__all__ = ["Confidence", "Context", "DSparkError", "confidence", "distill", "gate", "markov_draft",
+__all__ = ["Confidence", "Context", "DSparkError", "clip_grads", "confidence", "distill", "embed",
+           "embed_grad", "gate", "grad_norm", "linear", "linear_grad", "markov_draft",
            "markov_logits", "rnn_scan", "rnn_scan_grad", "selector_scores", "selector_walk",
            "verify_probs", "build"]

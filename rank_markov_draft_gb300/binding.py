@@ -37,7 +37,8 @@ EXPORTS = (
     "dspark_selector_walk", "dspark_confidence", "dspark_markov_logits",
     "dspark_markov_draft_noalloc", "dspark_verify", "dspark_schedule", "dspark_accept_label",
     "dspark_sts_fit", "dspark_rnn_draft", "dspark_rnn_logits", "dspark_verify_probs",
-    "dspark_distill", "dspark_rnn_scan", "dspark_rnn_scan_grad",
+    "dspark_distill", "dspark_rnn_scan", "dspark_rnn_scan_grad", "dspark_embed",
+    "dspark_embed_grad", "dspark_clip_grads", "dspark_linear", "dspark_linear_grad",
 )
 
 
@@ -99,6 +100,13 @@ def load(path: str = LIB_PATH):
         "dspark_rnn_scan": [P, P, P, P, I, I64, I64, I64, P, P, I64, I64, I, P, P, P],
         "dspark_rnn_scan_grad": [P, P, P, P, P, P, I, I64, I64, I64, P, P, P, I64, I64, I, P, P,
                                  I64, I64, P, P, P],
+        "dspark_embed": [P, P, I, I64, P, I64, I, I, F, P, I, I64, P],
+        "dspark_embed_grad": [P, P, P, I, I64, I64, I, I, F, I, P, I, I64, P],
+        "dspark_clip_grads": [P, P, P, P, I, F, P, P, P],
+        "dspark_linear": [P, P, I64, P, I64, P, I, P, I, I64, I64, I, I, P, I, I64, P, I64, P,
+                          ctypes.POINTER(I64), P],
+        "dspark_linear_grad": [P, P, I64, P, I64, P, I, I64, I, P, I, I64, I64, I, I, P, I, I64, P,
+                               I, I64, P, P, ctypes.POINTER(I64), P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -171,6 +179,15 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(_DTYPE)}")
     return _DTYPE[t.dtype]
+
+
+_ACT = {None: 0, "sigmoid": 1, "tanh": 2, "relu": 3, "silu": 4, "gelu": 5}  # dspark_act
+
+
+def _act(name) -> int:
+    if name not in _ACT:
+        raise ValueError(f"act: {name!r} not in {tuple(_ACT)}")
+    return _ACT[name]
 
 
 def _shape(t: Optional[torch.Tensor], shape, name: str):
@@ -492,6 +509,103 @@ def dspark_rnn_scan_grad(ctx: Context, za, zg, e, s, ds, s0, reset, ds_last, N, 
     _check(code, "dspark_rnn_scan_grad")
 
 
+def dspark_embed(ctx: Context, table, ids, N, V, D, scale, out, stream=None):
+    p, ld = _rows(table, table.dtype, "table")
+    po, ldo = _rows(out, out.dtype, "out")
+    code = ctx.lib.dspark_embed(
+        ctx.handle, p, _dtype(table, "table"), ld, _ptr(ids, (torch.int32,), "ids"), N, V, D,
+        float(scale), po, _dtype(out, "out"), ldo, _stream(stream, ctx.device))
+    _check(code, "dspark_embed")
+
+
+def dspark_embed_grad(ctx: Context, ids, de, N, V, D, scale, accumulate, grad, stream=None):
+    p, ld = _rows(de, de.dtype, "de")
+    pg, ldg = _rows(grad, grad.dtype, "grad")
+    code = ctx.lib.dspark_embed_grad(
+        ctx.handle, _ptr(ids, (torch.int32,), "ids"), p, _dtype(de, "de"), ld, N, V, D,
+        float(scale), int(bool(accumulate)), pg, _dtype(grad, "grad"), ldg,
+        _stream(stream, ctx.device))
+    _check(code, "dspark_embed_grad")
+
+
+def dspark_clip_grads(ctx: Context, grads, max_norm, out, norm, stream=None):
+    """grads and out: lists of contiguous tensors (out None: only the norm)."""
+    n = len(grads)
+    src = (ctypes.c_void_p * n)(*[_ptr(g, None, "grads") for g in grads])
+    numel = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    dtypes = (ctypes.c_int32 * n)(*[_dtype(g, "grads") for g in grads])
+    dst = None
+    if out is grads:
+        dst = src
+    elif out is not None:
+        if len(out) != n:
+            raise ValueError(f"out: {len(out)} tensors for {n} gradients")
+        for o, g in zip(out, grads):
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError(f"out: {tuple(o.shape)} {o.dtype} is not {tuple(g.shape)} {g.dtype}")
+        dst = (ctypes.c_void_p * n)(*[_ptr(o, None, "out") for o in out])
+    code = ctx.lib.dspark_clip_grads(ctx.handle, src, numel, dtypes, n, float(max_norm), dst,
+                                     _ptr(norm, (torch.float32,), "norm"),
+                                     _stream(stream, ctx.device))
+    _check(code, "dspark_clip_grads")
+
+
+def _with_workspace(call, workspace, device, stream, where: str):
+    """call(address, bytes) -> status; a call that asks for more workspace gets it from torch's
+    allocator (given back when the stream's work so far is done)."""
+    size = ctypes.c_int64(0 if workspace is None else workspace.numel() * workspace.element_size())
+    code = call(_ptr(workspace, None, "workspace"), ctypes.byref(size))
+    if code == CAPACITY and workspace is None:
+        workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                    torch.cuda.ExternalStream(int(stream), device=device))
+        code = call(workspace.data_ptr(), ctypes.byref(size))
+    _check(code, where)
+
+
+def dspark_linear(ctx: Context, x, W, bias, act, residual, M, K, N, y, pre, workspace=None,
+                  stream=None):
+    """workspace None: allocated where the call needs one."""
+    px, ld_x = _rows(x, torch.bfloat16, "x")
+    pw, ld_w = _rows(W, torch.bfloat16, "W")
+    dtype = _dtype(y, "y")
+    py, ld_y = _rows(y, y.dtype, "y")
+    pp, ld_pre = _rows(pre, y.dtype, "pre")
+    pr, ld_r, rdt = None, 0, 0
+    if residual is not None:
+        rdt = _dtype(residual, "residual")
+        pr, ld_r = _rows(residual, residual.dtype, "residual")
+    pb, a, s = _ptr(bias, (torch.float32,), "bias"), _act(act), _stream(stream, ctx.device)
+    _with_workspace(
+        lambda p, size: ctx.lib.dspark_linear(ctx.handle, px, ld_x, pw, ld_w, pb, a, pr, rdt, ld_r,
+                                              M, K, N, py, dtype, ld_y, pp, ld_pre, p, size, s),
+        workspace, x.device, stream, "dspark_linear")
+
+
+def dspark_linear_grad(ctx: Context, x, W, dy, act, pre, M, K, N, dx, dW, dbias, workspace=None,
+                       stream=None):
+    """workspace None: allocated where the call needs one."""
+    px, ld_x = _rows(x, torch.bfloat16, "x")
+    pw, ld_w = _rows(W, torch.bfloat16, "W")
+    ydt = _dtype(dy, "dy")
+    py, ld_dy = _rows(dy, dy.dtype, "dy")
+    rows = []
+    for t, name in ((pre, "pre"), (dx, "dx"), (dW, "dW")):
+        if t is None:
+            rows.append((None, 0, 0))
+        else:
+            dt = _dtype(t, name)
+            rows.append((*_rows(t, t.dtype, name), dt))
+    (pp, ld_p, pdt), (pdx, ld_dx, xdt), (pdw, ld_dw, wdt) = rows
+    pb, a, s = _ptr(dbias, (torch.float32,), "dbias"), _act(act), _stream(stream, ctx.device)
+    _with_workspace(
+        lambda p, size: ctx.lib.dspark_linear_grad(
+            ctx.handle, px, ld_x, pw, ld_w, py, ydt, ld_dy, a, pp, pdt, ld_p, M, K, N, pdx, xdt,
+            ld_dx, pdw, wdt, ld_dw, pb, p, size, s),
+        workspace, dy.device, stream, "dspark_linear_grad")
+
+
 def dspark_markov_draft_noalloc(U, W1, W2, anchors, B, K, V, r, temperature, seed, tokens,
                                 logprobs, device_status=None, stream=None):
     """Context-free draft that allocates no device memory (scratch compiled into the library).
@@ -760,4 +874,92 @@ def rnn_scan_grad(ctx: Context, za, zg, e, s, ds, *, s0=None, ds_last=None, rese
     out = dict(dza=dza, de=de, ds0=ds0)
     if zg is not None:
         out["dzg"] = dzg
+    return out
+
+
+def embed(ctx: Context, table, ids, *, scale=1.0, dtype=None, out=None, stream=None) -> torch.Tensor:
+    """scale * table[ids] [..., D] for ids [...] (negative: zeros), of the table's type or `dtype`
+    (fp32, bf16); out receives it."""
+    V, D = table.shape
+    if out is None:
+        out = torch.empty(*ids.shape, D, dtype=dtype or table.dtype, device=table.device)
+    _shape(out, (*ids.shape, D), "out")
+    dspark_embed(ctx, table, ids, ids.numel(), V, D, scale, out, stream)
+    return out
+
+
+def embed_grad(ctx: Context, ids, de, V=None, *, scale=1.0, dtype=torch.float32, grad=None,
+               accumulate=False, stream=None) -> torch.Tensor:
+    """Gradient [V, D] of embed's table from de [..., D]: per token, scale times the sum of its
+    rows.  grad receives it (with accumulate: is added to)."""
+    D = de.shape[-1]
+    _shape(de, (*ids.shape, D), "de")
+    if grad is None:
+        if accumulate or V is None:
+            raise ValueError("embed_grad: accumulate needs grad, and a new gradient V")
+        grad = torch.empty(V, D, dtype=dtype, device=de.device)
+    _shape(grad, (grad.shape[0] if V is None else V, D), "grad")
+    dspark_embed_grad(ctx, ids, de, ids.numel(), grad.shape[0], D, scale, accumulate, grad, stream)
+    return grad
+
+
+def grad_norm(ctx: Context, grads, stream=None) -> torch.Tensor:
+    """The norm of all tensors of a list together (fp32 scalar on the device)."""
+    norm = torch.empty((), dtype=torch.float32, device=torch.device("cuda", ctx.device))
+    dspark_clip_grads(ctx, grads, 0.0, None, norm, stream)
+    return norm
+
+
+def clip_grads(ctx: Context, grads, max_norm, *, out=None, stream=None) -> torch.Tensor:
+    """Scale a list of gradients (fp32, bf16) to a common norm of at most max_norm, in place or
+    into the tensors of out; returns their norm before (fp32 scalar on the device)."""
+    norm = torch.empty((), dtype=torch.float32, device=torch.device("cuda", ctx.device))
+    dspark_clip_grads(ctx, grads, max_norm, grads if out is None else out, norm, stream)
+    return norm
+
+
+def linear(ctx: Context, x, W, *, bias=None, act=None, residual=None, dtype=None, out=None,
+           pre=False, workspace=None, stream=None) -> dict:
+    """act(x W + bias) + residual for x [..., K] and W [K, N] in bf16 (rows evenly spaced), act None,
+    "sigmoid", "tanh", "relu", "silu" or "gelu".  Returns y [..., N] (of `dtype`, x's by default;
+    out receives it and may be the residual) and, with pre, x W + bias in y's type."""
+    K, N = W.shape
+    lead = x.shape[:-1]
+    _shape(x, (*lead, K), "x")
+    _shape(bias, (N,), "bias")
+    _shape(residual, (*lead, N), "residual")
+    y = torch.empty(*lead, N, dtype=dtype or x.dtype, device=x.device) if out is None else out
+    _shape(y, (*lead, N), "out")
+    if pre is True:
+        pre = torch.empty(*lead, N, dtype=y.dtype, device=x.device)
+    elif pre is False:
+        pre = None
+    _shape(pre, (*lead, N), "pre")
+    dspark_linear(ctx, x, W, bias, act, residual, lead.numel(), K, N, y, pre, workspace, stream)
+    out = dict(y=y)
+    if pre is not None:
+        out["pre"] = pre
+    return out
+
+
+def linear_grad(ctx: Context, x, W, dy, *, act=None, pre=None, dx=True, dW=True, dbias=False,
+                workspace=None, stream=None) -> dict:
+    """Gradients of linear from dy [..., N] (fp32 or bf16; pre as linear returned it, where there
+    is an activation).  dx [..., K] in x's type, dW [K, N] and dbias [N] in fp32: True allocates, a
+    tensor receives (dx, dW of either type), False leaves out."""
+    K, N = W.shape
+    lead = dy.shape[:-1]
+    _shape(x, (*lead, K), "x")
+    _shape(dy, (*lead, N), "dy")
+    _shape(pre, (*lead, N), "pre")
+    given = dict(dx=(dx, (*lead, K), x.dtype), dW=(dW, (K, N), torch.float32), dbias=(dbias, (N,), torch.float32))
+    out = {}
+    for name, (want, shape, dtype) in given.items():
+        if want is True:
+            out[name] = torch.empty(shape, dtype=dtype, device=dy.device)
+        elif want is not False:
+            _shape(want, shape, name)
+            out[name] = want
+    dspark_linear_grad(ctx, x, W, dy, act, pre, lead.numel(), K, N, out.get("dx"), out.get("dW"),
+                       out.get("dbias"), workspace, stream)
     return out

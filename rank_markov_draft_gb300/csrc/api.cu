@@ -14,6 +14,7 @@
 #include "dspark.h"
 #include "internal.h"
 #include "philox.cuh"
+#include "step.h"
 #include "training.h"
 
 using dspark::DraftArgs;
@@ -52,6 +53,7 @@ struct dspark_ctx {
   float* d_vp_sums = nullptr;
   int* d_vp_count = nullptr;             // [kVpMaxRequests]
   dspark::ScanSpan* d_spans = nullptr;   // [scan_span_count] segments of long recurrences
+  double* d_clip = nullptr;              // [clip_partials] sums of squares
   dspark::SmemOptIn opt_in;
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
   uint32_t epoch = 0;                    // last key epoch used
@@ -68,6 +70,7 @@ namespace {
 
 constexpr int kGateSplitsMax = 8;
 constexpr uint32_t kEpochMax = 16383;
+constexpr int64_t kMost = (1ll << 31) - 1;  // rows and row distances of the training step's tensors
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -510,6 +513,8 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
                                             dspark::kVpMaxRequests) == cudaSuccess &&
             cudaMalloc(&ctx->d_vp_count, sizeof(int) * dspark::kVpMaxRequests) == cudaSuccess &&
             cudaMalloc(&ctx->d_spans, sizeof(dspark::ScanSpan) * dspark::scan_span_count(ctx->num_sms)) ==
+                cudaSuccess &&
+            cudaMalloc(&ctx->d_clip, sizeof(double) * dspark::clip_partials(ctx->num_sms)) ==
                 cudaSuccess;
   ok = ok && cudaMemset(ctx->d_status, 0, sizeof(int)) == cudaSuccess &&
        cudaMemset(ctx->d_bar, 0, sizeof(uint32_t)) == cudaSuccess &&
@@ -554,6 +559,7 @@ int dspark_ctx_destroy(dspark_ctx* ctx) {
   cudaFree(ctx->d_vp_sums);
   cudaFree(ctx->d_vp_count);
   cudaFree(ctx->d_spans);
+  cudaFree(ctx->d_clip);
   delete ctx;
   return DSPARK_OK;
 }
@@ -1174,6 +1180,209 @@ int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const 
   a.ds0 = ds0;
   return cuda_status(
       dspark::launch_rnn_scan_grad(a, scan_launch(ctx), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_embed(dspark_ctx* ctx, const void* table, int table_dtype, int64_t ld_table,
+                 const int32_t* ids, int64_t N, int V, int D, float scale, void* out,
+                 int out_dtype, int64_t ld_out, dspark_stream_t stream) {
+  const size_t ts = dtype_size(table_dtype), os = dtype_size(out_dtype);
+  if (table == nullptr || ts == 0 || os == 0 || N < 0 || V <= 0 || D <= 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (N > 0 && (ids == nullptr || out == nullptr)) return DSPARK_ERR_INVALID_ARG;
+  if (ld_table < D || ld_out < D) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(table, ts) || !aligned_to(ids, 4) || !aligned_to(out, os))
+    return DSPARK_ERR_INVALID_ARG;
+  if (V > (1 << 18) || N > kMost || ld_table > kMost || ld_out > kMost)
+    return DSPARK_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::EmbedArgs a{};
+  a.table = table;
+  a.ids = ids;
+  a.N = N;
+  a.ld_table = ld_table;
+  a.ld_out = ld_out;
+  a.V = V;
+  a.D = D;
+  a.table_dtype = table_dtype;
+  a.out_dtype = out_dtype;
+  a.scale = scale;
+  a.out = out;
+  a.status = ctx->d_status;
+  return cuda_status(dspark::launch_embed(a, &ctx->last_launches,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int de_dtype,
+                      int64_t ld_de, int64_t N, int V, int D, float scale, int accumulate,
+                      void* grad, int grad_dtype, int64_t ld_grad, dspark_stream_t stream) {
+  const size_t ds = dtype_size(de_dtype), gs = dtype_size(grad_dtype);
+  if (grad == nullptr || ds == 0 || gs == 0 || N < 0 || V <= 0 || D <= 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (N > 0 && (ids == nullptr || de == nullptr)) return DSPARK_ERR_INVALID_ARG;
+  if (ld_de < D || ld_grad < D) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(ids, 4) || !aligned_to(de, ds) || !aligned_to(grad, gs))
+    return DSPARK_ERR_INVALID_ARG;
+  if (V > (1 << 18) || N > dspark::kEmbedGradMaxRows || ld_de > kMost || ld_grad > kMost)
+    return DSPARK_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::EmbedGradArgs a{};
+  a.ids = ids;
+  a.de = de;
+  a.N = N;
+  a.ld_de = ld_de;
+  a.ld_grad = ld_grad;
+  a.V = V;
+  a.D = D;
+  a.de_dtype = de_dtype;
+  a.grad_dtype = grad_dtype;
+  a.scale = scale;
+  a.accumulate = accumulate != 0;
+  a.grad = grad;
+  a.status = ctx->d_status;
+  return cuda_status(dspark::launch_embed_grad(a, &ctx->last_launches,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_clip_grads(dspark_ctx* ctx, const void* const* grads, const int64_t* numel,
+                      const int32_t* dtypes, int count, float max_norm, void* const* out,
+                      float* norm, dspark_stream_t stream) {
+  if (count < 0 || norm == nullptr || !aligned_to(norm, 4)) return DSPARK_ERR_INVALID_ARG;
+  if (count > 0 && (grads == nullptr || numel == nullptr || dtypes == nullptr))
+    return DSPARK_ERR_INVALID_ARG;
+  if (out != nullptr && !(max_norm >= 0.f)) return DSPARK_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const size_t size = dtype_size(dtypes[i]);
+    if (size == 0 || numel[i] < 0) return DSPARK_ERR_INVALID_ARG;
+    if (numel[i] > (1ll << 40)) return DSPARK_ERR_UNSUPPORTED;
+    if (numel[i] == 0) continue;
+    if (grads[i] == nullptr || !aligned_to(grads[i], size)) return DSPARK_ERR_INVALID_ARG;
+    if (out != nullptr && (out[i] == nullptr || !aligned_to(out[i], size)))
+      return DSPARK_ERR_INVALID_ARG;
+  }
+  int st;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::ClipArgs a{};
+  a.in = grads;
+  a.out = out;
+  a.numel = numel;
+  a.dtypes = dtypes;
+  a.count = count;
+  a.max_norm = max_norm;
+  a.norm = norm;
+  a.partial = ctx->d_clip;
+  a.num_sms = ctx->num_sms;
+  return cuda_status(dspark::launch_clip(a, &ctx->last_launches,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_linear(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16_t* W,
+                  int64_t ld_w, const float* bias, int act, const void* residual,
+                  int residual_dtype, int64_t ld_residual, int64_t M, int K, int N, void* y,
+                  int y_dtype, int64_t ld_y, void* pre, int64_t ld_pre, void* workspace,
+                  int64_t* workspace_bytes, dspark_stream_t stream) {
+  const size_t ys = dtype_size(y_dtype), rs = dtype_size(residual_dtype);
+  if (W == nullptr || workspace_bytes == nullptr || ys == 0 || M < 0 || K <= 0 || N <= 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (M > 0 && (x == nullptr || y == nullptr)) return DSPARK_ERR_INVALID_ARG;
+  if (act < DSPARK_ACT_NONE || act > DSPARK_ACT_GELU) return DSPARK_ERR_INVALID_ARG;
+  if (ld_x < K || ld_w < N || ld_y < N || (pre != nullptr && ld_pre < N))
+    return DSPARK_ERR_INVALID_ARG;
+  if (residual != nullptr && (rs == 0 || ld_residual < N || !aligned_to(residual, rs)))
+    return DSPARK_ERR_INVALID_ARG;
+  if (M > 0 && (pre == y || (residual == y && (residual_dtype != y_dtype || ld_residual != ld_y))))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(x, 2) || !aligned_to(W, 2) || !aligned_to(bias, 4) || !aligned_to(y, ys) ||
+      !aligned_to(pre, ys) || !aligned_to(workspace, 256) || *workspace_bytes < 0)
+    return DSPARK_ERR_INVALID_ARG;
+  for (int64_t ld : {M, ld_x, ld_w, ld_y, ld_residual, ld_pre})
+    if (ld > kMost) return DSPARK_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::LinearArgs a{};
+  a.x = x;
+  a.W = W;
+  a.bias = bias;
+  a.residual = residual;
+  a.M = M;
+  a.ld_x = ld_x;
+  a.ld_w = ld_w;
+  a.ld_res = ld_residual;
+  a.ld_y = ld_y;
+  a.ld_pre = ld_pre;
+  a.K = K;
+  a.N = N;
+  a.act = act;
+  a.res_dtype = residual_dtype;
+  a.y_dtype = y_dtype;
+  a.y = y;
+  a.pre = pre;
+  return cuda_status(dspark::launch_linear(a, &ctx->last_launches,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_linear_grad(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16_t* W,
+                       int64_t ld_w, const void* dy, int dy_dtype, int64_t ld_dy, int act,
+                       const void* pre, int pre_dtype, int64_t ld_pre, int64_t M, int K, int N,
+                       void* dx, int dx_dtype, int64_t ld_dx, void* dW, int dw_dtype,
+                       int64_t ld_dw, float* dbias, void* workspace, int64_t* workspace_bytes,
+                       dspark_stream_t stream) {
+  const size_t ys = dtype_size(dy_dtype);
+  if (workspace_bytes == nullptr || ys == 0 || M < 0 || K <= 0 || N <= 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (act < DSPARK_ACT_NONE || act > DSPARK_ACT_GELU) return DSPARK_ERR_INVALID_ARG;
+  if (act == DSPARK_ACT_NONE) pre = nullptr;
+  // (without rows dx is empty, and its address may be null)
+  if (dx == nullptr && dW == nullptr && dbias == nullptr && M > 0) return DSPARK_ERR_INVALID_ARG;
+  if (M > 0 && (dy == nullptr || (dx != nullptr && W == nullptr) || (dW != nullptr && x == nullptr) ||
+                (act != DSPARK_ACT_NONE && pre == nullptr)))
+    return DSPARK_ERR_INVALID_ARG;
+  if (ld_dy < N || (pre != nullptr && (dtype_size(pre_dtype) == 0 || ld_pre < N)))
+    return DSPARK_ERR_INVALID_ARG;
+  if (dx != nullptr && (dtype_size(dx_dtype) == 0 || ld_dx < K || ld_w < N ||
+                        !aligned_to(dx, dtype_size(dx_dtype))))
+    return DSPARK_ERR_INVALID_ARG;
+  if (dW != nullptr && (dtype_size(dw_dtype) == 0 || ld_dw < N || ld_x < K ||
+                        !aligned_to(dW, dtype_size(dw_dtype))))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(x, 2) || !aligned_to(W, 2) || !aligned_to(dy, ys) ||
+      (pre != nullptr && !aligned_to(pre, dtype_size(pre_dtype))) || !aligned_to(dbias, 4) ||
+      !aligned_to(workspace, 256) || *workspace_bytes < 0)
+    return DSPARK_ERR_INVALID_ARG;
+  for (int64_t ld : {M, ld_x, ld_w, ld_dy, ld_pre, ld_dx, ld_dw})
+    if (ld > kMost) return DSPARK_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
+  ctx->last_launches = 0;
+  dspark::LinearGradArgs a{};
+  a.x = x;
+  a.W = W;
+  a.dy = dy;
+  a.pre = pre;
+  a.M = M;
+  a.ld_x = ld_x;
+  a.ld_w = ld_w;
+  a.ld_dy = ld_dy;
+  a.ld_pre = ld_pre;
+  a.ld_dx = ld_dx;
+  a.ld_dw = ld_dw;
+  a.K = K;
+  a.N = N;
+  a.act = act;
+  a.dy_dtype = dy_dtype;
+  a.pre_dtype = pre_dtype;
+  a.dx_dtype = dx_dtype;
+  a.dw_dtype = dw_dtype;
+  a.dx = dx;
+  a.dW = dW;
+  a.dbias = dbias;
+  return cuda_status(dspark::launch_linear_grad(a, &ctx->last_launches,
+                                                reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,149 @@
+// embed.cu -- rows of an embedding table by token, scaled and converted, and the table's gradient.
+//
+// The Markov head reads W1[x_{k-1}] (DSpark explainer, "The Markov head"); in training the same
+// rows are gathered for given predecessors and their gradients summed token by token.
+
+#include <algorithm>
+
+#include "dspark.h"
+#include "sm103.cuh"
+#include "step.h"
+#include "typed.cuh"
+
+namespace dspark {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // units under way a thread
+
+// A unit is eight elements of a row (one, where rows do not lie on 16-byte boundaries or D is no
+// multiple of eight: VEC false).  A block takes `rows` rows, each thread kUnroll units at a time.
+template <typename Tin, typename Tout, bool VEC>
+__global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, int rows) {
+  const int per_row = VEC ? a.D / 8 : a.D;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
+  const int nrows = static_cast<int>(min(static_cast<int64_t>(rows), a.N - row0));
+  const int units = nrows * per_row;
+  for (int u0 = threadIdx.x; u0 < units; u0 += kThreads * kUnroll) {
+    int row[kUnroll], at[kUnroll], id[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int u = u0 + j * kThreads;
+      row[j] = u < units ? u / per_row : -1;
+      at[j] = (u - row[j] * per_row) * (VEC ? 8 : 1);
+      id[j] = row[j] >= 0 ? __ldg(a.ids + row0 + row[j]) : -1;
+      if (id[j] >= a.V) {
+        record_error(a.status, kStatusDeviceOob);
+        id[j] = -1;
+      }
+    }
+    if constexpr (VEC) {
+      Raw8<Tin> raw[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        raw[j].zero();
+        if (id[j] >= 0) raw[j].load(static_cast<const Tin*>(a.table) + id[j] * a.ld_table + at[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        if (row[j] < 0) continue;
+        float v[8];
+        raw[j].get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= a.scale;
+        store8(static_cast<Tout*>(a.out) + (row0 + row[j]) * a.ld_out + at[j], v);
+      }
+    } else {
+      float v[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        v[j] = id[j] >= 0 ? load1(static_cast<const Tin*>(a.table) + id[j] * a.ld_table + at[j])
+                          : 0.f;
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (row[j] >= 0)
+          store1(static_cast<Tout*>(a.out) + (row0 + row[j]) * a.ld_out + at[j], v[j] * a.scale);
+    }
+  }
+}
+
+template <typename Tin, typename Tout>
+void embed_typed(const EmbedArgs& a, cudaStream_t stream) {
+  const bool vec = a.D % 8 == 0 && rows_of_8(a.table, a.ld_table, a.table_dtype) &&
+                   rows_of_8(a.out, a.ld_out, a.out_dtype);
+  const int per_row = vec ? a.D / 8 : a.D;
+  // one round of units a block; few rows are spread over more blocks
+  const int rows = std::max(1, kThreads * kUnroll / per_row);
+  const int64_t blocks = (a.N + rows - 1) / rows;
+  if (vec)
+    embed_kernel<Tin, Tout, true><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a, rows);
+  else
+    embed_kernel<Tin, Tout, false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a, rows);
+}
+
+// grad[v] = scale * (sum of de over the rows whose token is v, in the order of the rows): a warp a
+// token looks through all ids.
+template <typename Tin, typename Tout>
+__global__ void __launch_bounds__(kThreads) embed_grad_kernel(EmbedGradArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t v = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
+  if (blockIdx.x == 0)
+    for (int64_t n = threadIdx.x; n < a.N; n += kThreads)
+      if (a.ids[n] >= a.V) record_error(a.status, kStatusDeviceOob);
+  if (v >= a.V) return;
+  Tout* const dst = static_cast<Tout*>(a.grad) + v * a.ld_grad;
+  for (int d0 = 0; d0 < a.D; d0 += 256) {
+    float s[8] = {};
+    bool any = false;
+    for (int64_t n0 = 0; n0 < a.N; n0 += 32) {
+      const bool hit = n0 + lane < a.N && a.ids[n0 + lane] == v;
+      unsigned m = __ballot_sync(0xFFFFFFFFu, hit);
+      any |= m != 0;
+      for (; m != 0; m &= m - 1) {
+        const Tin* const src = static_cast<const Tin*>(a.de) + (n0 + __ffs(m) - 1) * a.ld_de;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (d0 + i * 32 + lane < a.D) s[i] += load1(src + d0 + i * 32 + lane);
+      }
+    }
+    if (a.accumulate && !any) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int d = d0 + i * 32 + lane;
+      if (d < a.D) store1(dst + d, a.scale * s[i] + (a.accumulate ? load1(dst + d) : 0.f));
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_embed(const EmbedArgs& a, int* launches, cudaStream_t stream) {
+  if (a.N == 0) return cudaSuccess;
+  if (a.table_dtype == DSPARK_F32)
+    a.out_dtype == DSPARK_F32 ? embed_typed<float, float>(a, stream)
+                              : embed_typed<float, bf16>(a, stream);
+  else
+    a.out_dtype == DSPARK_F32 ? embed_typed<bf16, float>(a, stream)
+                              : embed_typed<bf16, bf16>(a, stream);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_embed_grad(const EmbedGradArgs& a, int* launches, cudaStream_t stream) {
+  if (a.N == 0 && a.accumulate) return cudaSuccess;
+  const unsigned blocks = (static_cast<unsigned>(a.V) * 32 + kThreads - 1) / kThreads;
+  if (a.de_dtype == DSPARK_F32)
+    a.grad_dtype == DSPARK_F32
+        ? embed_grad_kernel<float, float><<<blocks, kThreads, 0, stream>>>(a)
+        : embed_grad_kernel<float, bf16><<<blocks, kThreads, 0, stream>>>(a);
+  else
+    a.grad_dtype == DSPARK_F32
+        ? embed_grad_kernel<bf16, float><<<blocks, kThreads, 0, stream>>>(a)
+        : embed_grad_kernel<bf16, bf16><<<blocks, kThreads, 0, stream>>>(a);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+}  // namespace dspark
