@@ -114,7 +114,8 @@ int dspark_get_status(dspark_ctx* ctx, int* device_status);
 /* Testing knob: make CTA `cta` skip its grid-barrier arrival at step 0 in the
  * next draft launch (so every CTA's bounded wait runs out and the kernel exits
  * with DSPARK_ERR_TIMEOUT), or the sums of its first segments in the next
- * dspark_distill of long rows (so the waits for these rows run out), with
+ * dspark_distill of long rows (so the waits for these rows run out), or its
+ * loads in the products of the next dspark_linear or dspark_linear_grad, with
  * waits limited to timeout_ms.  Covers one call.  cta = -1 turns the knob off and
  * timeout_ms <= 0 restores the default limit (2000 ms). */
 int dspark_debug_set(dspark_ctx* ctx, int cta, int timeout_ms);
@@ -627,8 +628,8 @@ typedef enum dspark_act {
  *   y [M, N] of type y_dtype, rows ld_y apart
  *   pre [M, N] of type y_dtype, rows ld_pre apart: x W + bias, for the gradient (NULL: not
  *     written)
- * Any M >= 0 (< 2^31), K, N >= 1; pointers aligned to their element size.  Equal inputs at equal
- * addresses modulo 16 give equal bits.
+ * Any M >= 0 (< 2^31), 1 <= K, N <= 2^22; pointers aligned to their element size.  Equal inputs
+ * at equal addresses modulo 16 give equal bits.
  * workspace: device memory of the caller, 256-byte aligned, of *workspace_bytes bytes (it must
  * stay untouched until the call's work has run).  Where that is too little, *workspace_bytes is
  * set to what the same call needs, nothing is enqueued and DSPARK_ERR_CAPACITY is returned; 0

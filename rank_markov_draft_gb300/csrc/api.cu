@@ -15,6 +15,7 @@
 #include "internal.h"
 #include "philox.cuh"
 #include "step.h"
+#include "tensor_map.h"
 #include "training.h"
 
 using dspark::DraftArgs;
@@ -53,6 +54,7 @@ struct dspark_ctx {
   float* d_vp_sums = nullptr;
   int* d_vp_count = nullptr;             // [kVpMaxRequests]
   dspark::ScanSpan* d_spans = nullptr;   // [scan_span_count] segments of long recurrences
+  float* d_step = nullptr;               // [kStepScratchBytes] partial sums of the linear layers
   double* d_clip = nullptr;              // [clip_partials] sums of squares
   dspark::SmemOptIn opt_in;
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
@@ -68,44 +70,15 @@ struct dspark_ctx {
 
 namespace {
 
+using dspark::encode_2d;
+using dspark::encode_fn;
+using dspark::EncodeTiledFn;
+
 constexpr int kGateSplitsMax = 8;
 constexpr uint32_t kEpochMax = 16383;
 constexpr int64_t kMost = (1ll << 31) - 1;  // rows and row distances of the training step's tensors
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess) {
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-  });
-  return fn;
-}
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
-               uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t elem[2] = {1, 1};
-  return fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, elem,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // A [Bc][K][V] fp32 array (U, or the target's [Bc][K + 1][V]) as [Bc][K][V / 32][32]
 // (V % 32 == 0), boxes of 2 chunks x min(box_rows, 64) rows: each box reads 256 contiguous
@@ -152,6 +125,26 @@ dspark::ScanLaunch scan_launch(dspark_ctx* ctx) {
   c.launches = &ctx->last_launches;
   c.opt_in = &ctx->opt_in;
   return c;
+}
+
+dspark::LinearLaunch linear_launch(dspark_ctx* ctx) {
+  dspark::LinearLaunch c{};
+  c.scratch = ctx->d_step;
+  c.num_sms = ctx->num_sms;
+  c.status = ctx->d_status;
+  c.timeout_ns = ctx->timeout_ns;
+  c.debug_skip_cta = ctx->debug_skip_cta;
+  ctx->debug_skip_cta = -1;  // covers one call
+  c.opt_in = &ctx->opt_in;
+  c.launches = &ctx->last_launches;
+  return c;
+}
+
+// Whether the caller's workspace is enough; else *bytes is what the call needs.
+bool workspace_suffices(int64_t need, const void* workspace, int64_t* bytes) {
+  if (need == 0 || (workspace != nullptr && *bytes >= need)) return true;
+  *bytes = need;
+  return false;
 }
 
 // The arguments that both directions of the RNN head's recurrence share.
@@ -514,6 +507,7 @@ int dspark_ctx_create(dspark_ctx** out, int device, int B_max, int V_max, int K_
             cudaMalloc(&ctx->d_vp_count, sizeof(int) * dspark::kVpMaxRequests) == cudaSuccess &&
             cudaMalloc(&ctx->d_spans, sizeof(dspark::ScanSpan) * dspark::scan_span_count(ctx->num_sms)) ==
                 cudaSuccess &&
+            cudaMalloc(&ctx->d_step, dspark::kStepScratchBytes) == cudaSuccess &&
             cudaMalloc(&ctx->d_clip, sizeof(double) * dspark::clip_partials(ctx->num_sms)) ==
                 cudaSuccess;
   ok = ok && cudaMemset(ctx->d_status, 0, sizeof(int)) == cudaSuccess &&
@@ -559,6 +553,7 @@ int dspark_ctx_destroy(dspark_ctx* ctx) {
   cudaFree(ctx->d_vp_sums);
   cudaFree(ctx->d_vp_count);
   cudaFree(ctx->d_spans);
+  cudaFree(ctx->d_step);
   cudaFree(ctx->d_clip);
   delete ctx;
   return DSPARK_OK;
@@ -1301,6 +1296,7 @@ int dspark_linear(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16
     return DSPARK_ERR_INVALID_ARG;
   for (int64_t ld : {M, ld_x, ld_w, ld_y, ld_residual, ld_pre})
     if (ld > kMost) return DSPARK_ERR_UNSUPPORTED;
+  if (K > dspark::kLinearMaxWidth || N > dspark::kLinearMaxWidth) return DSPARK_ERR_UNSUPPORTED;
   int st;
   if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
   ctx->last_launches = 0;
@@ -1322,7 +1318,9 @@ int dspark_linear(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16
   a.y_dtype = y_dtype;
   a.y = y;
   a.pre = pre;
-  return cuda_status(dspark::launch_linear(a, &ctx->last_launches,
+  if (!workspace_suffices(dspark::linear_workspace(a), workspace, workspace_bytes))
+    return DSPARK_ERR_CAPACITY;
+  return cuda_status(dspark::launch_linear(a, linear_launch(ctx), workspace,
                                            reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1356,6 +1354,7 @@ int dspark_linear_grad(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const u
     return DSPARK_ERR_INVALID_ARG;
   for (int64_t ld : {M, ld_x, ld_w, ld_dy, ld_pre, ld_dx, ld_dw})
     if (ld > kMost) return DSPARK_ERR_UNSUPPORTED;
+  if (K > dspark::kLinearMaxWidth || N > dspark::kLinearMaxWidth) return DSPARK_ERR_UNSUPPORTED;
   int st;
   if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
   ctx->last_launches = 0;
@@ -1381,7 +1380,9 @@ int dspark_linear_grad(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const u
   a.dx = dx;
   a.dW = dW;
   a.dbias = dbias;
-  return cuda_status(dspark::launch_linear_grad(a, &ctx->last_launches,
+  if (!workspace_suffices(dspark::linear_grad_workspace(a), workspace, workspace_bytes))
+    return DSPARK_ERR_CAPACITY;
+  return cuda_status(dspark::launch_linear_grad(a, linear_launch(ctx), workspace,
                                                 reinterpret_cast<cudaStream_t>(stream)));
 }
 

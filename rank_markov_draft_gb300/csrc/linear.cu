@@ -1,165 +1,443 @@
 // linear.cu -- y = act(x W + bias) + residual, and the gradients of x, W and the bias.
 //
-// The heads' projections (h Wa, h Wg) and calibrated logits (U + s W2), forward and backward.
+// The heads' projections (h Wa, h Wg; equivalence page, "What the two methods do") and calibrated
+// logits (U + s W2), forward and backward.  The products are linear_gemm.cuh's; here are the choice of
+// tiles and splits, the joining of splits, and what the operands need first: rows on 16-byte
+// boundaries for TMA, and dz = dy act'(pre) as bf16 numbers.
 
 #include <algorithm>
 
-#include "dspark.h"
+#include "linear_gemm.cuh"
 #include "step.h"
-#include "typed.cuh"
+#include "tensor_map.h"
 
 namespace dspark {
 namespace {
 
 using bf16 = __nv_bfloat16;
 
-__device__ float act_value(int act, float z) {
-  switch (act) {
-    case DSPARK_ACT_SIGMOID: return 1.f / (1.f + expf(-z));
-    case DSPARK_ACT_TANH: return tanhf(z);
-    case DSPARK_ACT_RELU: return z < 0.f ? 0.f : z;
-    case DSPARK_ACT_SILU: return z / (1.f + expf(-z));
-    case DSPARK_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    default: return z;
+constexpr int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+__device__ __forceinline__ float load_as(const void* p, int f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const bf16*>(p)[i]);
+}
+
+// ------------------------------------------------------------------ joining of splits
+// The epilogue over sums of `splits` partials [splits][I][ld_part], in their order; four columns a
+// thread.
+struct JoinArgs {
+  const float* part;
+  int64_t I, ld_part, stride;
+  int J, splits;
+  const float* bias;
+  const void* residual;
+  int64_t ld_res, ld_out, ld_pre;
+  int res_f32, out_f32, act, vec;
+  void *out, *pre;
+};
+
+__global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
+  const int per_row = (a.J + 3) / 4;
+  const int64_t n = a.I * per_row;
+  for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < n; e += gridDim.x * 256ll) {
+    const int64_t r = e / per_row;
+    const int c = static_cast<int>(e - r * per_row) * 4;
+    const float* p = a.part + r * a.ld_part + c;
+    float z[4] = {};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+      const float4 f = __ldcs(reinterpret_cast<const float4*>(p + s * a.stride));
+      z[0] += f.x, z[1] += f.y, z[2] += f.z, z[3] += f.w;
+    }
+    const int m = min(4, a.J - c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < m && a.bias != nullptr) z[j] += a.bias[c + j];
+    auto put = [&](void* dst, int64_t ld) {
+      if (a.vec) {
+        epi_store<true>(dst, a.out_f32, r * ld + c, z);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float one[4] = {z[j]};
+          if (j < m) epi_store<false>(dst, a.out_f32, r * ld + c + j, one);
+        }
+      }
+    };
+    if (a.pre != nullptr) put(a.pre, a.ld_pre);
+    if (a.act != DSPARK_ACT_NONE) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = act_value(a.act, z[j]);
+    }
+    if (a.residual != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < m) z[j] += load_as(a.residual, a.res_f32, r * a.ld_res + c + j);
+    }
+    put(a.out, a.ld_out);
   }
 }
 
-__device__ float act_slope(int act, float z) {
-  switch (act) {
-    case DSPARK_ACT_SIGMOID: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f - s);
-    }
-    case DSPARK_ACT_TANH: {
-      const float t = tanhf(z);
-      return 1.f - t * t;
-    }
-    case DSPARK_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case DSPARK_ACT_SILU: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f + z * (1.f - s));
-    }
-    case DSPARK_ACT_GELU:
-      return 0.5f * (1.f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
-    default: return 1.f;
-  }
-}
+// ------------------------------------------------------------------ dz, and rows for TMA
+// hi (+ lo) = src act'(pre) as one or two bf16 numbers, rows ld_dst apart, and the column sums of a
+// block's rows.  Each of them may be left out.
+struct SplitArgs {
+  const void *src, *pre;
+  int64_t rows, ld_src, ld_pre, ld_dst;
+  int cols, src_f32, pre_f32, act, rows_per_block;
+  bf16 *hi, *lo;
+  float* sums;  // [row blocks][cols]
+};
 
-__device__ __forceinline__ float load_as(const void* p, int dtype, int64_t i) {
-  return dtype == DSPARK_F32 ? static_cast<const float*>(p)[i]
-                             : __bfloat162float(static_cast<const bf16*>(p)[i]);
-}
-__device__ __forceinline__ void store_as(void* p, int dtype, int64_t i, float v) {
-  if (dtype == DSPARK_F32)
-    static_cast<float*>(p)[i] = v;
-  else
-    static_cast<bf16*>(p)[i] = __float2bfloat16_rn(v);
-}
-
-__device__ __forceinline__ float slope_times(const LinearGradArgs& a, int64_t m, int64_t n) {
-  const float dy = load_as(a.dy, a.dy_dtype, m * a.ld_dy + n);
-  return a.act == DSPARK_ACT_NONE
-             ? dy
-             : dy * act_slope(a.act, load_as(a.pre, a.pre_dtype, m * a.ld_pre + n));
-}
-
-// A 64 x 64 tile of sum_k A(i, k) B(k, j), 16 elements a thread.
-constexpr int kTile = 64, kDeep = 16;
-template <typename FA, typename FB, typename FO>
-__device__ __forceinline__ void tile_product(int64_t I, int64_t J, int64_t Kc, FA A, FB B, FO out) {
-  __shared__ float sa[kDeep][kTile + 1], sb[kDeep][kTile + 1];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kTile, j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < Kc; k0 += kDeep) {
-    for (int e = threadIdx.x; e < kDeep * kTile; e += 256) {
-      const int k = e / kTile, r = e % kTile;
-      sa[k][r] = k0 + k < Kc && i0 + r < I ? A(i0 + r, k0 + k) : 0.f;
-      sb[k][r] = k0 + k < Kc && j0 + r < J ? B(k0 + k, j0 + r) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kDeep; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
+__global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
+  __shared__ float warps[8][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x * 128 + lane;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_block;
+  const int64_t r1 = min(a.rows, r0 + a.rows_per_block);
+  float sum[4] = {};
+#pragma unroll 2
+  for (int64_t r = r0 + warp; r < r1; r += 8) {
+    float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t r = i0 + ty * 4 + i, c = j0 + tx + 16 * j;
-      if (r < I && c < J) out(r, c, acc[i][j]);
+      const int c = c0 + 32 * j;
+      v[j] = c < a.cols ? load_as(a.src, a.src_f32, r * a.ld_src + c) : 0.f;
+      if (a.act != DSPARK_ACT_NONE && c < a.cols)
+        v[j] *= act_slope(a.act, load_as(a.pre, a.pre_f32, r * a.ld_pre + c));
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = c0 + 32 * j;
+      sum[j] += v[j];
+      if (c >= a.cols || a.hi == nullptr) continue;
+      const bf16 h = __float2bfloat16_rn(v[j]);
+      a.hi[r * a.ld_dst + c] = h;
+      if (a.lo != nullptr) {
+        // (of an infinity or NaN the second part is nothing, not NaN beside an infinity)
+        const float hf = __bfloat162float(h);
+        a.lo[r * a.ld_dst + c] = __float2bfloat16_rn(isfinite(hf) ? v[j] - hf : 0.f);
+      }
+    }
+  }
+  if (a.sums == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) warps[warp][lane + 32 * j] = sum[j];
+  __syncthreads();
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && c < a.cols) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += warps[w][threadIdx.x];
+    a.sums[static_cast<int64_t>(blockIdx.y) * a.cols + c] = s;
+  }
 }
 
-__global__ void __launch_bounds__(256) linear_kernel(LinearArgs a) {
-  const bf16 *x = reinterpret_cast<const bf16*>(a.x), *W = reinterpret_cast<const bf16*>(a.W);
-  tile_product(
-      a.M, a.N, a.K, [&](int64_t m, int64_t k) { return load1(x + m * a.ld_x + k); },
-      [&](int64_t k, int64_t n) { return load1(W + k * a.ld_w + n); },
-      [&](int64_t m, int64_t n, float z) {
-        if (a.bias != nullptr) z += a.bias[n];
-        if (a.pre != nullptr) store_as(a.pre, a.y_dtype, m * a.ld_pre + n, z);
-        z = act_value(a.act, z);
-        if (a.residual != nullptr) z += load_as(a.residual, a.res_dtype, m * a.ld_res + n);
-        store_as(a.y, a.y_dtype, m * a.ld_y + n, z);
-      });
-}
-
-__global__ void __launch_bounds__(256) linear_dx_kernel(LinearGradArgs a) {
-  const bf16* W = reinterpret_cast<const bf16*>(a.W);
-  tile_product(
-      a.M, a.K, a.N, [&](int64_t m, int64_t n) { return slope_times(a, m, n); },
-      [&](int64_t n, int64_t k) { return load1(W + k * a.ld_w + n); },
-      [&](int64_t m, int64_t k, float v) { store_as(a.dx, a.dx_dtype, m * a.ld_dx + k, v); });
-}
-
-__global__ void __launch_bounds__(256) linear_dw_kernel(LinearGradArgs a) {
-  const bf16* x = reinterpret_cast<const bf16*>(a.x);
-  tile_product(
-      a.K, a.N, a.M, [&](int64_t k, int64_t m) { return load1(x + m * a.ld_x + k); },
-      [&](int64_t m, int64_t n) { return slope_times(a, m, n); },
-      [&](int64_t k, int64_t n, float v) { store_as(a.dW, a.dw_dtype, k * a.ld_dw + n, v); });
-}
-
-__global__ void __launch_bounds__(256) linear_dbias_kernel(LinearGradArgs a) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= a.N) return;
+__global__ void __launch_bounds__(256) linear_sums_kernel(const float* part, int parts, int cols, float* out) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= cols) return;
   float s = 0.f;
-  for (int64_t m = 0; m < a.M; ++m) s += slope_times(a, m, n);
-  a.dbias[n] = s;
+#pragma unroll 8
+  for (int p = 0; p < parts; ++p) s += part[static_cast<int64_t>(p) * cols + c];
+  out[c] = s;
 }
 
-dim3 tiles(int64_t I, int64_t J) {
-  return dim3(static_cast<unsigned>((J + kTile - 1) / kTile), static_cast<unsigned>((I + kTile - 1) / kTile));
+// ------------------------------------------------------------------ host side
+// A bf16 matrix as TMA reads it.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, ld;
+};
+
+bool tma_rows(const void* p, int64_t ld) { return rows_of_8(p, ld, DSPARK_BF16); }
+
+class Workspace {
+ public:
+  explicit Workspace(void* base) : base_(static_cast<uint8_t*>(base)) {}
+  bf16* take(int64_t rows, int64_t cols) {
+    bf16* const p = reinterpret_cast<bf16*>(base_ + used_);
+    used_ += up(rows * up(cols, 8) * 2, 256);
+    return p;
+  }
+  int64_t used() const { return used_; }
+
+ private:
+  uint8_t* base_;
+  int64_t used_ = 0;
+};
+
+struct Launcher {
+  const LinearLaunch& c;
+  cudaStream_t stream;
+  cudaError_t error = cudaSuccess;
+
+  bool ok() const { return error == cudaSuccess; }
+  void launched() {
+    *c.launches += 1;
+    error = cudaGetLastError();
+  }
+
+  void split(SplitArgs a) {
+    if (!ok() || a.rows == 0) return;
+    const unsigned cols = static_cast<unsigned>((a.cols + 127) / 128);
+    // about four blocks an SM; of column sums, as many as the scratch takes
+    int64_t per = std::max<int64_t>(8, up((a.rows * cols + 4 * c.num_sms - 1) / (4 * c.num_sms), 8));
+    per = std::max(per, (a.rows + 65534) / 65535);
+    if (a.sums != nullptr) per = std::max(per, (a.rows * a.cols * 4 + kStepScratchBytes / 2 - 1) / (kStepScratchBytes / 2));
+    per = std::min(per, up(a.rows, 8));
+    a.rows_per_block = static_cast<int>(per);
+    const int64_t blocks = (a.rows + per - 1) / per;
+    linear_split_kernel<<<dim3(cols, static_cast<unsigned>(blocks)), 256, 0, stream>>>(a);
+    launched();
+    sum_blocks = static_cast<int>(blocks);
+  }
+  int sum_blocks = 0;  // of the last split()
+
+  // The matrix itself, or its copy with rows on 16-byte boundaries.
+  Matrix rows_for_tma(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld, Workspace& ws) {
+    if (tma_rows(p, ld)) return {p, rows, cols, ld};
+    bf16* const to = ws.take(rows, cols);
+    SplitArgs a{};
+    a.src = p;
+    a.rows = rows;
+    a.ld_src = ld;
+    a.ld_dst = up(cols, 8);
+    a.cols = static_cast<int>(cols);
+    a.hi = to;
+    split(a);
+    return {to, rows, cols, a.ld_dst};
+  }
+
+  template <int BN, bool A_MN, bool B_MN>
+  void gemm_sized(GemmArgs& g, bool vec) {
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(g.units, c.num_sms));
+    auto run = [&](auto kernel) {
+      error = (*c.opt_in)(kernel, GemmShape<BN>::kSmem);
+      if (!ok()) return;
+      kernel<<<grid, kGemmThreads, GemmShape<BN>::kSmem, stream>>>(g);
+      launched();
+    };
+    vec ? run(linear_gemm_kernel<BN, A_MN, B_MN, true>) : run(linear_gemm_kernel<BN, A_MN, B_MN, false>);
+  }
+
+  // out = act(A B + bias) + residual, A of parts a[0..na), B of b[0..nb); the epilogue's fields of g
+  // are set.
+  template <bool A_MN, bool B_MN>
+  void gemm(GemmArgs g, const Matrix* a, int na, const Matrix* b, int nb, int64_t I, int J, int64_t Kc) {
+    if (!ok()) return;
+    const bool vec_out = (reinterpret_cast<uintptr_t>(g.out) & (g.out_f32 ? 15 : 7)) == 0 && g.ld_out % 4 == 0 &&
+                         (g.pre == nullptr || ((reinterpret_cast<uintptr_t>(g.pre) & (g.out_f32 ? 15 : 7)) == 0 && g.ld_pre % 4 == 0)) &&
+                         J % 4 == 0;
+    const bool vec_res = g.residual == nullptr ||
+                         ((reinterpret_cast<uintptr_t>(g.residual) & (g.res_f32 ? 15 : 7)) == 0 && g.ld_res % 4 == 0);
+    g.blocks_k = (Kc + 63) / 64;
+    g.steps = g.blocks_k * std::max(na, nb);
+    const int64_t ld_part = up(J, 4);
+    // The tile and the number of splits that end soonest by this reckoning (us): a stage's four
+    // products take 0.27 whatever the tile's width, a tile's start and end 1.5 of which the next
+    // tile's products hide 1, the join of splits its launch and its bytes at 4 TB/s.
+    int BN = 256;
+    int64_t S = 1;
+    double best = 1e30;
+    for (int bn : {256, 128, 64}) {
+      const int64_t tiles = (I + 127) / 128 * ((J + bn - 1) / bn);
+      if (bn != 64 && J <= bn / 2) continue;
+      for (int64_t s = 1; s <= std::min<int64_t>(g.steps, 64); ++s) {
+        if (s > 1 && s * I * ld_part * 4 > kStepScratchBytes) break;
+        const int64_t per = (g.steps + s - 1) / s;
+        if ((g.steps + per - 1) / per != s) continue;
+        const int64_t waves = (tiles * s + c.num_sms - 1) / c.num_sms;
+        const double t = static_cast<double>(waves) * (0.27 * static_cast<double>(per) + 0.5) + 1.0 +
+                         (s > 1 ? 3.0 + static_cast<double>(2 * s * I * ld_part * 4) / 4e6 : 0.0);
+        if (t < best) best = t, BN = bn, S = s;
+      }
+    }
+    g.I = I;
+    g.J = J;
+    g.tiles_i = (I + 127) / 128;
+    g.tiles_j = (J + BN - 1) / BN;
+    g.splits = static_cast<int>(S);
+    g.per_split = (g.steps + S - 1) / S;
+    g.units = g.tiles_i * g.tiles_j * S;
+    g.a_parts = na;
+    g.b_parts = nb;
+    bool maps = true;
+    auto encode = [&](CUtensorMap* m, const Matrix& x, uint32_t height) {
+      maps = maps && encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x.p, x.cols, x.rows, x.ld * 2, 64, height);
+    };
+    for (int i = 0; i < na; ++i) encode(&g.a[i], a[i], A_MN ? 64 : 128);
+    for (int i = 0; i < nb; ++i) encode(&g.b[i], b[i], B_MN ? 64 : BN);
+    if (!maps) {
+      error = cudaErrorInvalidValue;
+      return;
+    }
+    g.status = c.status;
+    g.timeout_ns = c.timeout_ns;
+    g.skip_cta = c.debug_skip_cta;
+    JoinArgs j{};
+    if (S > 1) {  // sums of parts first, the epilogue where they are joined
+      j.part = c.scratch;
+      j.I = I;
+      j.ld_part = ld_part;
+      j.stride = I * ld_part;
+      j.J = J;
+      j.splits = static_cast<int>(S);
+      j.bias = g.bias;
+      j.residual = g.residual;
+      j.ld_res = g.ld_res;
+      j.ld_out = g.ld_out;
+      j.ld_pre = g.ld_pre;
+      j.res_f32 = g.res_f32;
+      j.out_f32 = g.out_f32;
+      j.act = g.act;
+      j.vec = vec_out;
+      j.out = g.out;
+      j.pre = g.pre;
+      g.bias = nullptr;
+      g.residual = nullptr;
+      g.pre = nullptr;
+      g.act = DSPARK_ACT_NONE;
+      g.out = c.scratch;
+      g.out_f32 = 1;
+      g.ld_out = ld_part;
+      g.split_stride = j.stride;
+    }
+    // (partials' rows are padded to vectors, but a vector may not pass the last column)
+    const bool vec = S > 1 ? J % 4 == 0 : vec_out && vec_res;
+    if (BN == 256)
+      gemm_sized<256, A_MN, B_MN>(g, vec);
+    else if (BN == 128)
+      gemm_sized<128, A_MN, B_MN>(g, vec);
+    else
+      gemm_sized<64, A_MN, B_MN>(g, vec);
+    if (S > 1) join(j);
+  }
+
+  void join(const JoinArgs& j) {
+    if (!ok()) return;
+    const int64_t n = j.I * ((j.J + 3) / 4);
+    const int64_t blocks = std::min<int64_t>((n + 255) / 256, 8 * c.num_sms);
+    linear_join_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(j);
+    launched();
+  }
+};
+
+// Whether dz is the given dy itself, bf16 with rows that TMA reads.
+bool dz_as_it_is(const LinearGradArgs& a) {
+  return a.act == DSPARK_ACT_NONE && a.dy_dtype == DSPARK_BF16 && tma_rows(a.dy, a.ld_dy);
 }
+bool two_parts(const LinearGradArgs& a) { return a.act != DSPARK_ACT_NONE || a.dy_dtype == DSPARK_F32; }
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs& a, int* launches, cudaStream_t stream) {
-  if (a.M == 0) return cudaSuccess;
-  linear_kernel<<<tiles(a.M, a.N), 256, 0, stream>>>(a);
-  *launches += 1;
-  return cudaGetLastError();
+int64_t linear_workspace(const LinearArgs& a) {
+  Workspace w(nullptr);
+  if (a.M == 0) return 0;
+  if (!tma_rows(a.x, a.ld_x)) w.take(a.M, a.K);
+  if (!tma_rows(a.W, a.ld_w)) w.take(a.K, a.N);
+  return w.used();
 }
 
-cudaError_t launch_linear_grad(const LinearGradArgs& a, int* launches, cudaStream_t stream) {
-  if (a.dx != nullptr && a.M > 0) {
-    linear_dx_kernel<<<tiles(a.M, a.K), 256, 0, stream>>>(a);
-    *launches += 1;
+int64_t linear_grad_workspace(const LinearGradArgs& a) {
+  Workspace w(nullptr);
+  if (a.M == 0) return 0;
+  if (a.dW != nullptr && !tma_rows(a.x, a.ld_x)) w.take(a.M, a.K);
+  if (a.dx != nullptr && !tma_rows(a.W, a.ld_w)) w.take(a.K, a.N);
+  if ((a.dx != nullptr || a.dW != nullptr) && !dz_as_it_is(a)) {
+    w.take(a.M, a.N);
+    if (two_parts(a)) w.take(a.M, a.N);
+  }
+  return w.used();
+}
+
+cudaError_t launch_linear(const LinearArgs& a, const LinearLaunch& c, void* workspace, cudaStream_t stream) {
+  if (a.M == 0) return cudaSuccess;
+  Launcher l{c, stream};
+  Workspace ws(workspace);
+  const Matrix x = l.rows_for_tma(a.x, a.M, a.K, a.ld_x, ws);
+  const Matrix W = l.rows_for_tma(a.W, a.K, a.N, a.ld_w, ws);
+  GemmArgs g{};
+  g.bias = a.bias;
+  g.residual = a.residual;
+  g.ld_res = a.ld_res;
+  g.res_f32 = a.res_dtype == DSPARK_F32;
+  g.act = a.act;
+  g.out = a.y;
+  g.ld_out = a.ld_y;
+  g.out_f32 = a.y_dtype == DSPARK_F32;
+  g.pre = a.pre;
+  g.ld_pre = a.ld_pre;
+  l.gemm<false, true>(g, &x, 1, &W, 1, a.M, a.N, a.K);
+  return l.error;
+}
+
+cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, void* workspace, cudaStream_t stream) {
+  Launcher l{c, stream};
+  if (a.M == 0) {  // sums of nothing
+    JoinArgs j{};
+    j.J = a.N;
+    j.I = a.K;
+    j.out = a.dW;
+    j.ld_out = a.ld_dw;
+    j.out_f32 = a.dw_dtype == DSPARK_F32;
+    if (a.dW != nullptr) l.join(j);
+    j.I = 1;
+    j.out = a.dbias;
+    j.ld_out = a.N;
+    j.out_f32 = 1;
+    if (a.dbias != nullptr) l.join(j);
+    return l.error;
+  }
+  Workspace ws(workspace);
+  Matrix x{}, W{};
+  if (a.dW != nullptr) x = l.rows_for_tma(a.x, a.M, a.K, a.ld_x, ws);
+  if (a.dx != nullptr) W = l.rows_for_tma(a.W, a.K, a.N, a.ld_w, ws);
+  Matrix dz[2] = {{a.dy, a.M, a.N, a.ld_dy}, {}};
+  int parts = 1;
+  const bool products = a.dx != nullptr || a.dW != nullptr;
+  if (a.dbias != nullptr || (products && !dz_as_it_is(a))) {
+    SplitArgs s{};
+    s.src = a.dy;
+    s.src_f32 = a.dy_dtype == DSPARK_F32;
+    s.ld_src = a.ld_dy;
+    s.pre = a.pre;
+    s.pre_f32 = a.pre_dtype == DSPARK_F32;
+    s.ld_pre = a.ld_pre;
+    s.act = a.act;
+    s.rows = a.M;
+    s.cols = a.N;
+    s.ld_dst = up(a.N, 8);
+    if (products && !dz_as_it_is(a)) {
+      s.hi = ws.take(a.M, a.N);
+      dz[0] = {s.hi, a.M, a.N, s.ld_dst};
+      if (two_parts(a)) {
+        s.lo = ws.take(a.M, a.N);
+        dz[1] = {s.lo, a.M, a.N, s.ld_dst};
+        parts = 2;
+      }
+    }
+    s.sums = a.dbias != nullptr ? c.scratch : nullptr;
+    l.split(s);
+    if (a.dbias != nullptr && l.ok()) {
+      linear_sums_kernel<<<(a.N + 255) / 256, 256, 0, stream>>>(c.scratch, l.sum_blocks, a.N, a.dbias);
+      l.launched();
+    }
+  }
+  if (a.dx != nullptr) {
+    GemmArgs g{};
+    g.out = a.dx;
+    g.ld_out = a.ld_dx;
+    g.out_f32 = a.dx_dtype == DSPARK_F32;
+    l.gemm<false, false>(g, dz, parts, &W, 1, a.M, a.K, a.N);
   }
   if (a.dW != nullptr) {
-    linear_dw_kernel<<<tiles(a.K, a.N), 256, 0, stream>>>(a);
-    *launches += 1;
+    GemmArgs g{};
+    g.out = a.dW;
+    g.ld_out = a.ld_dw;
+    g.out_f32 = a.dw_dtype == DSPARK_F32;
+    l.gemm<true, true>(g, &x, 1, dz, parts, a.K, a.N, a.M);
   }
-  if (a.dbias != nullptr) {
-    linear_dbias_kernel<<<(a.N + 255) / 256, 256, 0, stream>>>(a);
-    *launches += 1;
-  }
-  return cudaGetLastError();
+  return l.error;
 }
 
 }  // namespace dspark

@@ -52,6 +52,7 @@ constexpr int clip_partials(int num_sms) { return 4 * num_sms; }
 cudaError_t launch_clip(const ClipArgs& a, int* launches, cudaStream_t stream);
 
 // ---- products with an epilogue (linear.cu)
+constexpr int kLinearMaxWidth = 1 << 22;  // of K and N: a row of column sums fits half the scratch
 struct LinearArgs {
   const uint16_t *x, *W;    // [M, K], [K, N] bf16
   const float* bias;        // [N] or null
@@ -69,7 +70,22 @@ struct LinearGradArgs {
   void *dx, *dW;            // [M, K], [K, N]; each may be null
   float* dbias;             // [N] or null
 };
-cudaError_t launch_linear(const LinearArgs& a, int* launches, cudaStream_t stream);
-cudaError_t launch_linear_grad(const LinearGradArgs& a, int* launches, cudaStream_t stream);
+// What a context gives its launches.
+constexpr int64_t kStepScratchBytes = 32 << 20;
+struct LinearLaunch {
+  float* scratch;     // [kStepScratchBytes]
+  int num_sms;
+  int* status;
+  uint64_t timeout_ns;
+  int debug_skip_cta; // testing: the block of each product that loads nothing (-1: none)
+  SmemOptIn* opt_in;
+  int* launches;      // host: kernels launched (added to)
+};
+// Bytes that a call needs of its caller.
+int64_t linear_workspace(const LinearArgs& a);
+int64_t linear_grad_workspace(const LinearGradArgs& a);
+cudaError_t launch_linear(const LinearArgs& a, const LinearLaunch& c, void* workspace, cudaStream_t stream);
+cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, void* workspace,
+                               cudaStream_t stream);
 
 }  // namespace dspark

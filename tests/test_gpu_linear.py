@@ -250,3 +250,22 @@ def test_side_stream_and_graph(dsp, N):
         near(out["y"], y, ey)
         for name, (w, b) in step.linear_grad(x, W, dy, "gelu", out["pre"]).items():
             near(out_g[name], w, b, name)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_waits_that_run_out(backward):
+    """A block that loads nothing: its waits end, the status says so, and the context works again."""
+    x, W = make(1, 400, 128, 512)
+    with binding.Context(0, B_max=1, V_max=4096, K_max=1) as ctx:
+        ctx.debug_set(cta=1, timeout_ms=20)
+        if backward:
+            binding.linear_grad(ctx, x, W, normal(2, 400, 512).to(BF16))
+        else:
+            binding.linear(ctx, x, W)
+        torch.cuda.synchronize()
+        assert ctx.status() == binding.TIMEOUT
+        with pytest.raises(binding.DSparkError):
+            binding.linear(ctx, x, W)
+        ctx.reset()
+        check(ctx, x, W)
+        check_grad(ctx, x, W, normal(2, 400, 512).to(BF16))

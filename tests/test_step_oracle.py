@@ -118,7 +118,8 @@ def test_linear_argument_checks(lib):
                 dict(ws=P(0x1010), size=64), dict(size=-1), dict(sized=False), dict(res=P(0x2000), rt=1),
                 dict(res=P(0x2000), ldr=17)):
         assert f(**bad) == E.INVALID_ARG, bad
-    for bad in (dict(M=BIG), dict(ldx=BIG), dict(ldw=BIG), dict(ldy=BIG)):
+    for bad in (dict(M=BIG), dict(ldx=BIG), dict(ldw=BIG), dict(ldy=BIG), dict(K=(1 << 22) + 1, ldx=1 << 23),
+                dict(N=(1 << 22) + 1, ldw=1 << 23, ldy=1 << 23)):
         assert f(**bad) == E.UNSUPPORTED, bad
 
 
