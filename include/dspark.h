@@ -581,7 +581,8 @@ int dspark_embed(dspark_ctx* ctx, const void* table, int table_dtype, int64_t ld
  *   ids [N] as given to dspark_embed (negative: skipped; >= V: reported and skipped)
  *   de [N, D] of type de_dtype, rows ld_de elements apart
  *   grad [V, D] of type grad_dtype, rows ld_grad elements apart
- * 0 <= N <= 2^20 (more rows: several calls with accumulate); otherwise as dspark_embed. */
+ * 0 <= N <= 2^20 (more rows: several calls with accumulate), D <= 2^16; otherwise as
+ * dspark_embed. */
 int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int de_dtype,
                       int64_t ld_de, int64_t N, int V, int D, float scale, int accumulate,
                       void* grad, int grad_dtype, int64_t ld_grad, dspark_stream_t stream);

@@ -27,7 +27,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "draft.cu", "gate.cu", "selector.cu", "confidence.cu", "noalloc.cu", "verify.cu",
            "schedule.cu", "label.cu", "calibrate.cu", "verify_probs.cu", "distill.cu", "rnn_scan.cu",
-           "embed.cu", "clip.cu", "linear.cu"]
+           "embed.cu", "embed_grad.cu", "clip.cu", "linear.cu"]
 
 
 def nvcc() -> str:

@@ -54,7 +54,7 @@ struct dspark_ctx {
   float* d_vp_sums = nullptr;
   int* d_vp_count = nullptr;             // [kVpMaxRequests]
   dspark::ScanSpan* d_spans = nullptr;   // [scan_span_count] segments of long recurrences
-  float* d_step = nullptr;               // [kStepScratchBytes] partial sums of the linear layers
+  float* d_step = nullptr;               // [kStepScratchBytes] partial sums, sorted tokens
   double* d_clip = nullptr;              // [clip_partials] sums of squares
   dspark::SmemOptIn opt_in;
   uint32_t bar_counter = 0;              // host copy of the grid-barrier counter
@@ -1219,7 +1219,7 @@ int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int d
   if (ld_de < D || ld_grad < D) return DSPARK_ERR_INVALID_ARG;
   if (!aligned_to(ids, 4) || !aligned_to(de, ds) || !aligned_to(grad, gs))
     return DSPARK_ERR_INVALID_ARG;
-  if (V > (1 << 18) || N > dspark::kEmbedGradMaxRows || ld_de > kMost || ld_grad > kMost)
+  if (V > (1 << 18) || N > dspark::kEmbedGradMaxRows || D > dspark::kEmbedGradMaxWidth || ld_de > kMost || ld_grad > kMost)
     return DSPARK_ERR_UNSUPPORTED;
   int st;
   if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
@@ -1238,8 +1238,12 @@ int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int d
   a.accumulate = accumulate != 0;
   a.grad = grad;
   a.status = ctx->d_status;
-  return cuda_status(dspark::launch_embed_grad(a, &ctx->last_launches,
-                                               reinterpret_cast<cudaStream_t>(stream)));
+  dspark::EmbedGradLaunch c{};
+  c.scratch = reinterpret_cast<uint8_t*>(ctx->d_step);
+  c.num_sms = ctx->num_sms;
+  c.opt_in = &ctx->opt_in;
+  c.launches = &ctx->last_launches;
+  return cuda_status(dspark::launch_embed_grad(a, c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dspark_clip_grads(dspark_ctx* ctx, const void* const* grads, const int64_t* numel,

@@ -1,7 +1,7 @@
-// embed.cu -- rows of an embedding table by token, scaled and converted, and the table's gradient.
+// embed.cu -- rows of an embedding table by token, scaled and converted.
 //
 // The Markov head reads W1[x_{k-1}] (DSpark explainer, "The Markov head"); in training the same
-// rows are gathered for given predecessors and their gradients summed token by token.
+// rows are gathered for given predecessors.
 
 #include <algorithm>
 
@@ -83,40 +83,6 @@ void embed_typed(const EmbedArgs& a, cudaStream_t stream) {
     embed_kernel<Tin, Tout, false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a, rows);
 }
 
-// grad[v] = scale * (sum of de over the rows whose token is v, in the order of the rows): a warp a
-// token looks through all ids.
-template <typename Tin, typename Tout>
-__global__ void __launch_bounds__(kThreads) embed_grad_kernel(EmbedGradArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t v = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  if (blockIdx.x == 0)
-    for (int64_t n = threadIdx.x; n < a.N; n += kThreads)
-      if (a.ids[n] >= a.V) record_error(a.status, kStatusDeviceOob);
-  if (v >= a.V) return;
-  Tout* const dst = static_cast<Tout*>(a.grad) + v * a.ld_grad;
-  for (int d0 = 0; d0 < a.D; d0 += 256) {
-    float s[8] = {};
-    bool any = false;
-    for (int64_t n0 = 0; n0 < a.N; n0 += 32) {
-      const bool hit = n0 + lane < a.N && a.ids[n0 + lane] == v;
-      unsigned m = __ballot_sync(0xFFFFFFFFu, hit);
-      any |= m != 0;
-      for (; m != 0; m &= m - 1) {
-        const Tin* const src = static_cast<const Tin*>(a.de) + (n0 + __ffs(m) - 1) * a.ld_de;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (d0 + i * 32 + lane < a.D) s[i] += load1(src + d0 + i * 32 + lane);
-      }
-    }
-    if (a.accumulate && !any) continue;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = d0 + i * 32 + lane;
-      if (d < a.D) store1(dst + d, a.scale * s[i] + (a.accumulate ? load1(dst + d) : 0.f));
-    }
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_embed(const EmbedArgs& a, int* launches, cudaStream_t stream) {
@@ -127,21 +93,6 @@ cudaError_t launch_embed(const EmbedArgs& a, int* launches, cudaStream_t stream)
   else
     a.out_dtype == DSPARK_F32 ? embed_typed<bf16, float>(a, stream)
                               : embed_typed<bf16, bf16>(a, stream);
-  *launches += 1;
-  return cudaGetLastError();
-}
-
-cudaError_t launch_embed_grad(const EmbedGradArgs& a, int* launches, cudaStream_t stream) {
-  if (a.N == 0 && a.accumulate) return cudaSuccess;
-  const unsigned blocks = (static_cast<unsigned>(a.V) * 32 + kThreads - 1) / kThreads;
-  if (a.de_dtype == DSPARK_F32)
-    a.grad_dtype == DSPARK_F32
-        ? embed_grad_kernel<float, float><<<blocks, kThreads, 0, stream>>>(a)
-        : embed_grad_kernel<float, bf16><<<blocks, kThreads, 0, stream>>>(a);
-  else
-    a.grad_dtype == DSPARK_F32
-        ? embed_grad_kernel<bf16, float><<<blocks, kThreads, 0, stream>>>(a)
-        : embed_grad_kernel<bf16, bf16><<<blocks, kThreads, 0, stream>>>(a);
   *launches += 1;
   return cudaGetLastError();
 }

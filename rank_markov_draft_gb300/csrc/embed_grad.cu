@@ -1,0 +1,489 @@
+// embed_grad.cu -- the gradient of embedding rows by their table: per token, the sum of its rows.
+//
+// The rows are put in the order of their tokens (equal tokens in the order of the rows), and the
+// sorted list is cut into equal pieces, so that a token of a tenth of all rows costs no more than ten
+// thousand tokens of one row each; sums of tokens that lie in several pieces are joined in their order.
+// No atomics decide an order: equal inputs give equal bits.  Three launches:
+//   sort: one cluster sorts while the other clusters store the zeros of all table rows;
+//   sums: a group of lanes a piece, a row a group at a time, joined within the block;
+//   join: tokens that lie in several blocks.
+
+#include <algorithm>
+
+#include "dspark.h"
+#include "sm103.cuh"
+#include "step.h"
+#include "typed.cuh"
+
+namespace dspark {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+// ------------------------------------------------------------------ sort
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxCluster = 16, kSortMaxBins = 1024;
+
+struct SortArgs {
+  const int32_t* ids;
+  int64_t N;
+  int V;
+  int bits, passes;   // of a pass; 1 or 2 of them
+  int cluster;        // blocks that sort
+  uint32_t* totals;   // [passes][cluster][bins]
+  uint2* half;        // [N] after the first of two passes
+  uint2* sorted;      // [N] token (V: padding) and row
+  int* status;
+  // zeros beside it
+  void* grad;         // null: none
+  int64_t ld_grad;    // elements
+  int D, size;        // of a row, bytes of an element
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Rows [0, V) of the gradient set to zero by `blocks` blocks, from the last: the first rows, which
+// common tokens have, are stored last and still in L2 when their sums follow.
+__device__ __forceinline__ void store_zeros(const SortArgs& a, int block, int blocks) {
+  uint8_t* const base = static_cast<uint8_t*>(a.grad);
+  const int64_t row_bytes = static_cast<int64_t>(a.D) * a.size, ld = a.ld_grad * a.size;
+  const bool packed = a.ld_grad == a.D;
+  const int64_t rows = packed ? 1 : a.V, bytes = packed ? row_bytes * a.V : row_bytes;
+  const int64_t stride = static_cast<int64_t>(blocks) * kSortThreads, me = static_cast<int64_t>(block) * kSortThreads + threadIdx.x;
+  if ((reinterpret_cast<uintptr_t>(base) & 15) == 0 && (packed || (ld & 15) == 0)) {
+    const int64_t per_row = bytes / 16;
+    if (packed) {
+#pragma unroll 4
+      for (int64_t u = per_row - 1 - me; u >= 0; u -= stride)
+        reinterpret_cast<uint4*>(base)[u] = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int64_t u = me; u < rows * per_row; u += stride) {
+        const int64_t r = u / per_row;
+        reinterpret_cast<uint4*>(base + (rows - 1 - r) * ld)[u - r * per_row] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    const int tail = static_cast<int>(bytes - per_row * 16) / a.size;  // elements behind the vectors
+    for (int64_t u = me; u < rows * tail; u += stride) {
+      uint8_t* const p = base + (u / tail) * ld + per_row * 16 + (u % tail) * a.size;
+      if (a.size == 4)
+        *reinterpret_cast<uint32_t*>(p) = 0;
+      else
+        *reinterpret_cast<uint16_t*>(p) = 0;
+    }
+  } else {
+    const int64_t n = bytes / a.size;
+    for (int64_t u = me; u < rows * n; u += stride) {
+      uint8_t* const p = base + (u / n) * ld + (u % n) * a.size;
+      if (a.size == 4)
+        *reinterpret_cast<uint32_t*>(p) = 0;
+      else
+        *reinterpret_cast<uint16_t*>(p) = 0;
+    }
+  }
+}
+
+// Stable counting sort by `bits` bits of the token a pass, over one cluster: each warp counts the
+// digits of its stretch of the list, the counts of all blocks give each warp's first place of every
+// digit, and the warps place their elements 32 at a time.
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a) {
+  extern __shared__ uint32_t counts[];  // [warps][bins], then [bins]
+  __shared__ uint32_t warp_sum[kSortWarps];
+  griddep_launch_dependents();
+  const int c = blockIdx.x;
+  if (c >= a.cluster) {
+    store_zeros(a, c - a.cluster, gridDim.x - a.cluster);
+    return;
+  }
+  const int bins = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* const mine = counts + warp * bins;
+  uint32_t* const base = counts + kSortWarps * bins;
+  const int64_t stretch = (a.N + static_cast<int64_t>(a.cluster) * kSortThreads - 1) /
+                          (static_cast<int64_t>(a.cluster) * kSortThreads) * 32;  // a warp's
+  const int64_t lo = min(a.N, (static_cast<int64_t>(c) * kSortWarps + warp) * stretch);
+  const int64_t hi = min(a.N, lo + stretch);
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits;
+    uint2* const dst = pass + 1 < a.passes ? a.half : a.sorted;
+    auto element = [&](int64_t i) {
+      if (pass > 0) return __ldcg(a.half + i);
+      const int32_t id = a.ids[i];
+      return make_uint2(id < 0 || id >= a.V ? a.V : id, static_cast<uint32_t>(i));
+    };
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += 32) {
+      if (pass == 0 && a.ids[i] >= a.V) record_error(a.status, kStatusDeviceOob);
+      atomicAdd(mine + ((element(i).x >> shift) & (bins - 1)), 1u);
+    }
+    __syncthreads();
+    uint32_t* const totals = a.totals + static_cast<int64_t>(pass) * a.cluster * bins;
+    if (threadIdx.x < bins) {
+      uint32_t s = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t n = counts[w * bins + threadIdx.x];
+        counts[w * bins + threadIdx.x] = s;
+        s += n;
+      }
+      totals[c * bins + threadIdx.x] = s;
+    }
+    cluster_sync();
+    uint32_t below = 0, all = 0;
+    if (threadIdx.x < bins) {
+#pragma unroll 8
+      for (int k = 0; k < a.cluster; ++k) {
+        const uint32_t n = __ldcg(totals + k * bins + threadIdx.x);
+        below += k < c ? n : 0;
+        all += n;
+      }
+    }
+    uint32_t incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      incl += lane >= o ? n : 0;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    if (threadIdx.x < bins) base[threadIdx.x] = before + incl - all + below;
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+      const bool in = i0 + lane < hi;
+      const uint2 e = in ? element(i0 + lane) : make_uint2(0, 0);
+      const uint32_t digit = in ? (e.x >> shift) & (bins - 1) : 0xFFFFFFFFu;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
+      const uint32_t at = in ? mine[digit] : 0;
+      __syncwarp();
+      if (in) {
+        dst[base[digit] + at + __popc(same & ((1u << lane) - 1))] = e;
+        if (lane == __ffs(same) - 1) mine[digit] = at + __popc(same);
+      }
+      __syncwarp();
+    }
+    if (pass + 1 < a.passes) cluster_sync();
+  }
+}
+
+// ------------------------------------------------------------------ sums
+constexpr int kSumThreads = 256, kSumBlocks = 3;  // of an SM
+constexpr int kSumBatch = 4;  // rows under way a group
+
+struct SumArgs {
+  const uint2* sorted;
+  const void* de;
+  int64_t N, ld_de, ld_grad;
+  int V, D;
+  int lanes;        // of a group: 8 columns each
+  int piece;        // list entries of a group
+  float scale;
+  bool accumulate;
+  void* grad;
+  float *head, *tail;  // [slices][blocks][8 lanes]: sums of the tokens that reach in from the block
+                       // before, and out to the next
+};
+
+// The eight columns of a lane: neighbours (VEC) or `lanes` apart.
+template <typename T, bool VEC>
+struct Columns {
+  Raw8<T> raw;
+  float one[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const T* row, int col, int lanes, int D) {
+    if constexpr (VEC) {
+      raw.load(row + col);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) one[j] = col + j * lanes < D ? load1(row + col + j * lanes) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void add_to(float (&s)[8]) const {
+    if constexpr (VEC) {
+      float v[8];
+      raw.get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += one[j];
+    }
+  }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t token, int col, const float (&s)[8]) {
+  if (col >= a.D) return;
+  T* const row = static_cast<T*>(a.grad) + static_cast<int64_t>(token) * a.ld_grad;
+  float v[8] = {};
+  if (a.accumulate) {
+    Columns<T, VEC> old;
+    old.load(row, col, a.lanes, a.D);
+    old.add_to(v);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = fmaf(a.scale, s[j], v[j]);
+  if constexpr (VEC) {
+    store8(row + col, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j * a.lanes < a.D) store1(row + col + j * a.lanes, v[j]);
+  }
+}
+
+__device__ __forceinline__ int first_column(int slice, int lane, int lanes, bool vec) {
+  return slice * lanes * 8 + (vec ? lane * 8 : lane);
+}
+
+// A piece's runs of equal tokens that begin and end in it are done where they end.  `head` is the sum
+// of a run that reaches in from the piece before, `tail` of one that begins here and reaches out;
+// `through` says that the head reaches out too.
+template <typename Tin, typename Tout, bool VEC>
+__global__ void __launch_bounds__(kSumThreads, kSumBlocks) embed_sum_kernel(SumArgs a) {
+  __shared__ float heads[kSumThreads * 8], tails[kSumThreads * 8];
+  __shared__ uint32_t tokens[kSumThreads];
+  __shared__ uint8_t has_head[kSumThreads], has_tail[kSumThreads], through[kSumThreads];
+  const int group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes, groups = kSumThreads / a.lanes;
+  const int col = first_column(blockIdx.y, lane, a.lanes, VEC);
+  const int64_t begin = min(a.N, (static_cast<int64_t>(blockIdx.x) * groups + group) * a.piece);
+  const int64_t end = min(a.N, begin + a.piece);
+  const uint32_t none = static_cast<uint32_t>(a.V);
+  if (lane == 0) has_head[group] = has_tail[group] = through[group] = 0;
+  griddep_wait();
+  float s[8] = {};
+  auto deposit = [&](float* where) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) where[j * kSumThreads + threadIdx.x] = s[j];
+  };
+  if (begin < end) {
+    uint32_t token = a.sorted[begin].x;
+    bool reaches_in = begin > 0 && a.sorted[begin - 1].x == token;
+    uint2 e[kSumBatch];
+    auto entries = [&](int64_t i) {
+#pragma unroll
+      for (int j = 0; j < kSumBatch; ++j) e[j] = i + j < end ? a.sorted[i + j] : make_uint2(none, 0);
+    };
+    entries(begin);
+    for (int64_t i = begin; i < end && e[0].x != none; i += kSumBatch) {
+      Columns<Tin, VEC> rows[kSumBatch];
+      uint32_t t[kSumBatch];
+#pragma unroll
+      for (int j = 0; j < kSumBatch; ++j) {
+        t[j] = e[j].x;
+        if (t[j] != none && col < a.D)
+          rows[j].load(static_cast<const Tin*>(a.de) + e[j].y * a.ld_de, col, a.lanes, a.D);
+      }
+      entries(i + kSumBatch);
+#pragma unroll
+      for (int j = 0; j < kSumBatch; ++j) {
+        if (t[j] == none) continue;
+        if (t[j] != token) {
+          if (reaches_in) {
+            deposit(heads);
+            if (lane == 0) has_head[group] = 1;
+          } else {
+            write_row<Tout, VEC>(a, token, col, s);
+          }
+          reaches_in = false;
+          token = t[j];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s[k] = 0.f;
+        }
+        if (col < a.D) rows[j].add_to(s);
+      }
+    }
+    if (token != none) {
+      const bool reaches_out = end < a.N && a.sorted[end].x == token;
+      if (reaches_in) {
+        deposit(heads);
+        if (lane == 0) has_head[group] = 1, through[group] = reaches_out;
+      } else if (reaches_out) {
+        deposit(tails);
+        if (lane == 0) has_tail[group] = 1, tokens[group] = token;
+      } else {
+        write_row<Tout, VEC>(a, token, col, s);
+      }
+    }
+  }
+  __syncthreads();
+  auto add_head = [&](int g) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += heads[j * kSumThreads + g * a.lanes + lane];
+  };
+  auto keep = [&](float* where) {
+    float* const p = where + ((static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * a.lanes + lane) * 8;
+    store8(p, s);
+  };
+  if (group == 0 && has_head[0]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+    add_head(0);
+    int g = 0;
+    while (through[g] && g + 1 < groups) add_head(++g);
+    keep(a.head);
+  }
+  if (has_tail[group]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = tails[j * kSumThreads + threadIdx.x];
+    int g = group;
+    bool out = true;
+    while (out && g + 1 < groups) {
+      add_head(++g);
+      out = through[g];
+    }
+    if (out)
+      keep(a.tail);
+    else
+      write_row<Tout, VEC>(a, tokens[group], col, s);
+  }
+}
+
+// Runs over several blocks: a group for each block that one begins in.
+template <typename Tout, bool VEC>
+__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumArgs a, int blocks) {
+  griddep_wait();
+  const int group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes, groups = kSumThreads / a.lanes;
+  const int64_t per_block = static_cast<int64_t>(a.piece) * groups;
+  const int b = blockIdx.x * groups + group;
+  if (b + 1 >= blocks) return;
+  auto token_at = [&](int64_t i) { return a.sorted[i].x; };
+  const int64_t begin = b * per_block, end = begin + per_block;  // (a later block is not empty)
+  const uint32_t token = token_at(end - 1);
+  if (token == static_cast<uint32_t>(a.V) || token_at(end) != token) return;
+  if (begin > 0 && token_at(begin - 1) == token) return;  // begins in an earlier block
+  float s[8];
+  auto at = [&](const float* p, int block) {
+    return p + ((static_cast<int64_t>(blockIdx.y) * blocks + block) * a.lanes + lane) * 8;
+  };
+  Raw8<float> r;
+  r.load(at(a.tail, b));
+  r.get(s);
+  for (int k = b + 1; k < blocks; ++k) {
+    float v[8];
+    r.load(at(a.head, k));
+    r.get(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += v[j];
+    const int64_t next = (k + 1) * per_block;
+    if (next >= a.N || token_at(next) != token) break;
+  }
+  write_row<Tout, VEC>(a, token, first_column(blockIdx.y, lane, a.lanes, VEC), s);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename Tin, typename Tout, bool VEC>
+cudaError_t sums(const SumArgs& s, int blocks, int slices, int* launches, cudaStream_t stream) {
+  cudaError_t e = launch_dependent(embed_sum_kernel<Tin, Tout, VEC>, dim3(blocks, slices), stream, s);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (blocks == 1) return e;
+  const int groups = kSumThreads / s.lanes;
+  e = launch_dependent(embed_join_kernel<Tout, VEC>, dim3((blocks + groups - 1) / groups, slices), stream, s, blocks);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, cudaStream_t stream) {
+  if (a.N == 0 && a.accumulate) return cudaSuccess;
+  // the scratch: digit counts, the list after each pass, partial sums
+  uint8_t* p = c.scratch;
+  SortArgs t{};
+  t.totals = reinterpret_cast<uint32_t*>(p);
+  p += 2 * kSortMaxCluster * kSortMaxBins * 4;
+  t.half = reinterpret_cast<uint2*>(p);
+  p += kEmbedGradMaxRows * 8;
+  t.sorted = reinterpret_cast<uint2*>(p);
+  p += kEmbedGradMaxRows * 8;
+  t.ids = a.ids;
+  t.N = a.N;
+  t.V = a.V;
+  t.status = a.status;
+  int bits = 1;
+  while ((a.V >> bits) != 0) ++bits;  // tokens 0 .. V
+  t.passes = bits <= 9 ? 1 : 2;
+  t.bits = std::max(5, (bits + t.passes - 1) / t.passes);
+  // 4096 entries a block: below that another block costs more than its share saves
+  t.cluster = 1;
+  while (t.cluster < kSortMaxCluster && a.N > 4096 * static_cast<int64_t>(t.cluster)) t.cluster *= 2;
+  int grid = t.cluster;
+  if (!a.accumulate) {
+    t.grad = a.grad;
+    t.ld_grad = a.ld_grad;
+    t.D = a.D;
+    t.size = a.grad_dtype == DSPARK_F32 ? 4 : 2;
+    grid = c.num_sms / t.cluster * t.cluster;
+  }
+  const int smem = ((kSortWarps + 1) << t.bits) * 4;
+  cudaError_t e = (*c.opt_in)(embed_sort_kernel, ((kSortWarps + 1) * kSortMaxBins) * 4);
+  if (e != cudaSuccess) return e;
+  if (t.cluster > 8) {
+    e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = t.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, t);
+  if (e != cudaSuccess) return e;
+  *c.launches += 1;
+  if (a.N == 0) return e;
+
+  SumArgs s{};
+  s.sorted = t.sorted;
+  s.de = a.de;
+  s.N = a.N;
+  s.ld_de = a.ld_de;
+  s.ld_grad = a.ld_grad;
+  s.V = a.V;
+  s.D = a.D;
+  s.scale = a.scale;
+  s.accumulate = a.accumulate;
+  s.grad = a.grad;
+  const bool vec = a.D % 8 == 0 && rows_of_8(a.de, a.ld_de, a.de_dtype) && rows_of_8(a.grad, a.ld_grad, a.grad_dtype);
+  s.lanes = 32;
+  while (vec && s.lanes > 1 && s.lanes * 4 >= a.D) s.lanes /= 2;
+  const int slices = (a.D + s.lanes * 8 - 1) / (s.lanes * 8), groups = kSumThreads / s.lanes;
+  // one wave of blocks over list and columns
+  const int64_t most = kSumBlocks * c.num_sms * groups;
+  s.piece = static_cast<int>(std::max<int64_t>(4, (a.N * slices + most - 1) / most));
+  const int blocks = static_cast<int>((a.N + static_cast<int64_t>(s.piece) * groups - 1) / (static_cast<int64_t>(s.piece) * groups));
+  s.head = reinterpret_cast<float*>(p);
+  s.tail = s.head + static_cast<int64_t>(blocks) * slices * s.lanes * 8;
+  auto run = [&](auto in, auto out) {
+    using Tin = decltype(in);
+    using Tout = decltype(out);
+    return vec ? sums<Tin, Tout, true>(s, blocks, slices, c.launches, stream)
+               : sums<Tin, Tout, false>(s, blocks, slices, c.launches, stream);
+  };
+  if (a.de_dtype == DSPARK_F32)
+    return a.grad_dtype == DSPARK_F32 ? run(float(), float()) : run(float(), bf16());
+  return a.grad_dtype == DSPARK_F32 ? run(bf16(), float()) : run(bf16(), bf16());
+}
+
+}  // namespace dspark

@@ -10,6 +10,9 @@
 
 namespace dspark {
 
+// Scratch that the calls of a context share.
+constexpr int64_t kStepScratchBytes = 32 << 20;
+
 // ---- embedding rows and their gradient (embed.cu)
 struct EmbedArgs {
   const void* table;  // [V, D] of table_dtype, rows ld_table apart
@@ -33,7 +36,14 @@ struct EmbedGradArgs {
   void* grad;          // [V, D] of grad_dtype, rows ld_grad apart
   int* status;
 };
-cudaError_t launch_embed_grad(const EmbedGradArgs& a, int* launches, cudaStream_t stream);
+constexpr int kEmbedGradMaxWidth = 1 << 16;  // of D: 256 slices of columns
+struct EmbedGradLaunch {
+  uint8_t* scratch;  // [kStepScratchBytes]
+  int num_sms;
+  SmemOptIn* opt_in;
+  int* launches;     // host: kernels launched (added to)
+};
+cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, cudaStream_t stream);
 
 // ---- global norm and clipping (clip.cu)
 constexpr int kClipMaxTensors = 512;  // of one launch
@@ -71,7 +81,6 @@ struct LinearGradArgs {
   float* dbias;             // [N] or null
 };
 // What a context gives its launches.
-constexpr int64_t kStepScratchBytes = 32 << 20;
 struct LinearLaunch {
   float* scratch;     // [kStepScratchBytes]
   int num_sms;

@@ -87,7 +87,8 @@ def test_embed_grad_argument_checks(lib):
     for bad in (dict(ids=None), dict(de=None), dict(dt=2), dict(ld=7), dict(N=-1), dict(V=0), dict(D=0), dict(grad=None),
                 dict(gt=2), dict(ldg=7), dict(de=ODD), dict(grad=P(0x1002))):
         assert f(**bad) == E.INVALID_ARG, bad
-    for bad in (dict(N=(1 << 20) + 1), dict(V=(1 << 18) + 1), dict(ld=BIG), dict(ldg=BIG)):
+    for bad in (dict(N=(1 << 20) + 1), dict(V=(1 << 18) + 1), dict(D=(1 << 16) + 1, ld=1 << 17, ldg=1 << 17), dict(ld=BIG),
+                dict(ldg=BIG)):
         assert f(**bad) == E.UNSUPPORTED, bad
 
 
