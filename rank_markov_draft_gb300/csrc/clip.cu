@@ -26,7 +26,7 @@ struct ClipList {
   void* out[CAP];
   int64_t numel[CAP];
   int64_t first[CAP + 1];  // chunks before each tensor
-  uint8_t bf16_in[CAP], wide[CAP];  // its type; both addresses on 16-byte boundaries
+  uint8_t bf16_in[CAP], wide[CAP];  // its type; both addresses allow vectors of eight
   int count;
 };
 
@@ -169,7 +169,7 @@ void fill(ClipList<CAP>& l, const ClipArgs& a, int t0, int n) {
     l.numel[i] = a.numel[t0 + i];
     l.first[i + 1] = l.first[i] + (a.numel[t0 + i] + kChunk - 1) / kChunk;
     l.bf16_in[i] = a.dtypes[t0 + i] == DSPARK_BF16;
-    l.wide[i] = ((reinterpret_cast<uintptr_t>(l.in[i]) | reinterpret_cast<uintptr_t>(l.out[i])) & 15u) == 0;
+    l.wide[i] = rows_of_8(l.in[i], 0, a.dtypes[t0 + i]) && rows_of_8(l.out[i], 0, a.dtypes[t0 + i]);
   }
 }
 

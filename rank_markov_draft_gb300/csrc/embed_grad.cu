@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "async_copy.cuh"
 #include "dspark.h"
 #include "sm103.cuh"
 #include "step.h"
@@ -22,16 +23,16 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------ sort
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kSortMaxCluster = 16, kSortMaxBins = 1024;
+constexpr int kSortMaxCluster = 16, kSortMaxBits = 9, kSortMaxPasses = 3;
 
 struct SortArgs {
   const int32_t* ids;
   int64_t N;
   int V;
-  int bits, passes;   // of a pass; 1 or 2 of them
+  int bits, passes;   // of a pass; their number
   int cluster;        // blocks that sort
   uint32_t* totals;   // [passes][cluster][bins]
-  uint2* half;        // [N] after the first of two passes
+  uint2* half;        // [N] after every other pass
   uint2* sorted;      // [N] token (V: padding) and row
   int* status;
   // zeros beside it
@@ -86,7 +87,12 @@ __device__ __forceinline__ void store_zeros(const SortArgs& a, int block, int bl
 
 // Stable counting sort by `bits` bits of the token a pass, over one cluster: each warp counts the
 // digits of its stretch of the list, the counts of all blocks give each warp's first place of every
-// digit, and the warps place their elements 32 at a time.
+// digit, and the warps place their elements. Elements are taken 32 at a time; lanes of the same digit
+// find one another by a vote a bit, which takes as long for digits all alike (the high ones of text)
+// as for distinct ones (the match instruction took twice as long, atomics on a word a digit between). Where a warp's stretch fits its registers (131072 entries in 16
+// blocks) the places found while counting are kept.
+constexpr int kSortHeld = 8;  // elements of a lane in registers
+
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t counts[];  // [warps][bins], then [bins]
   __shared__ uint32_t warp_sum[kSortWarps];
@@ -103,26 +109,82 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
                           (static_cast<int64_t>(a.cluster) * kSortThreads) * 32;  // a warp's
   const int64_t lo = min(a.N, (static_cast<int64_t>(c) * kSortWarps + warp) * stretch);
   const int64_t hi = min(a.N, lo + stretch);
+  const bool held = stretch <= 32 * kSortHeld;
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.bits;
-    uint2* const dst = pass + 1 < a.passes ? a.half : a.sorted;
-    auto element = [&](int64_t i) {
-      if (pass > 0) return __ldcg(a.half + i);
-      const int32_t id = a.ids[i];
-      return make_uint2(id < 0 || id >= a.V ? a.V : id, static_cast<uint32_t>(i));
+    const bool last_is_odd = (a.passes - pass) & 1;
+    uint2* const dst = last_is_odd ? a.sorted : a.half;
+    const uint2* const src = last_is_odd ? a.half : a.sorted;
+    uint2 e[kSortHeld];
+    uint32_t place[kSortHeld];  // among the warp's elements of its digit
+    auto digit_of = [&](const uint2& x) { return (x.x >> shift) & (bins - 1); };
+    // elements [i0, i0 + 32 kSortHeld) of the stretch (beyond it: none)
+    auto fetch = [&](int64_t i0) {
+#pragma unroll
+      for (int j = 0; j < kSortHeld; ++j) {
+        const int64_t i = i0 + 32 * j + lane;
+        e[j] = make_uint2(0xFFFFFFFFu, static_cast<uint32_t>(i));
+        if (i < hi) {
+          if (pass > 0)
+            e[j] = __ldcg(src + i);
+          else
+            e[j].x = static_cast<uint32_t>(a.ids[i]);
+        }
+      }
+      if (pass > 0) return;
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < kSortHeld; ++j) {
+        const bool in = i0 + 32 * j + lane < hi;
+        const int32_t id = static_cast<int32_t>(e[j].x);
+        bad |= in && id >= a.V;
+        e[j].x = !in ? 0xFFFFFFFFu : static_cast<uint32_t>(id < 0 || id >= a.V ? a.V : id);
+      }
+      if (bad) record_error(a.status, kStatusDeviceOob);
     };
-    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0;
+    // counts them on
+    auto count = [&](int64_t i0) {
+#pragma unroll
+      for (int j = 0; j < kSortHeld; ++j) {
+        if (i0 + 32 * j >= hi) break;
+        const bool in = e[j].x != 0xFFFFFFFFu;
+        const uint32_t digit = digit_of(e[j]);
+        unsigned same = __ballot_sync(0xFFFFFFFFu, in);
+#pragma unroll
+        for (int bit = 0; bit < kSortMaxBits; ++bit) {
+          const bool one = digit & (1u << bit);
+          const unsigned set = __ballot_sync(0xFFFFFFFFu, one);
+          same &= one ? set : ~set;
+        }
+        const uint32_t at = in ? mine[digit] : 0;
+        place[j] = at + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (in && (same >> lane) == 1) mine[digit] = at + __popc(same);  // the last of them
+        __syncwarp();
+      }
+    };
+    auto put = [&](bool with_warp) {
+#pragma unroll
+      for (int j = 0; j < kSortHeld; ++j)
+        if (e[j].x != 0xFFFFFFFFu) {
+          const uint32_t d = digit_of(e[j]);
+          dst[base[d] + place[j] + (with_warp ? mine[d] : 0)] = e[j];
+        }
+    };
+    fetch(lo);
+    for (int i = threadIdx.x; i < kSortWarps * bins / 4; i += kSortThreads)
+      reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-#pragma unroll 4
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-      if (pass == 0 && a.ids[i] >= a.V) record_error(a.status, kStatusDeviceOob);
-      atomicAdd(mine + ((element(i).x >> shift) & (bins - 1)), 1u);
+    count(lo);
+    for (int64_t i0 = lo + 32 * kSortHeld; i0 < hi; i0 += 32 * kSortHeld) {
+      fetch(i0);
+      count(i0);
     }
     __syncthreads();
     uint32_t* const totals = a.totals + static_cast<int64_t>(pass) * a.cluster * bins;
     if (threadIdx.x < bins) {
       uint32_t s = 0;
-#pragma unroll 8
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t n = counts[w * bins + threadIdx.x];
         counts[w * bins + threadIdx.x] = s;
@@ -133,9 +195,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
     cluster_sync();
     uint32_t below = 0, all = 0;
     if (threadIdx.x < bins) {
-#pragma unroll 8
-      for (int k = 0; k < a.cluster; ++k) {
-        const uint32_t n = __ldcg(totals + k * bins + threadIdx.x);
+#pragma unroll
+      for (int k = 0; k < kSortMaxCluster; ++k) {
+        const uint32_t n = k < a.cluster ? __ldcg(totals + k * bins + threadIdx.x) : 0;
         below += k < c ? n : 0;
         all += n;
       }
@@ -148,37 +210,38 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    uint32_t before = lane < warp ? warp_sum[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     if (threadIdx.x < bins) base[threadIdx.x] = before + incl - all + below;
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const bool in = i0 + lane < hi;
-      const uint2 e = in ? element(i0 + lane) : make_uint2(0, 0);
-      const uint32_t digit = in ? (e.x >> shift) & (bins - 1) : 0xFFFFFFFFu;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
-      const uint32_t at = in ? mine[digit] : 0;
-      __syncwarp();
-      if (in) {
-        dst[base[digit] + at + __popc(same & ((1u << lane) - 1))] = e;
-        if (lane == __ffs(same) - 1) mine[digit] = at + __popc(same);
+    if (held) {
+      put(true);
+    } else {  // `mine` goes on as a running count
+      for (int64_t i0 = lo; i0 < hi; i0 += 32 * kSortHeld) {
+        fetch(i0);
+        count(i0);
+        put(false);
       }
-      __syncwarp();
     }
     if (pass + 1 < a.passes) cluster_sync();
   }
 }
 
 // ------------------------------------------------------------------ sums
-constexpr int kSumThreads = 256, kSumBlocks = 3;  // of an SM
-constexpr int kSumBatch = 4;  // rows under way a group
+constexpr int kSumThreads = 256, kSumBlocks = 4;  // of an SM
+// Rows under way a group, by asynchronous copies (VEC; 32 KB of shared memory a block): registers
+// would hold as many, but the few counters a warp waits on make it wait for later loads too.
+template <typename T>
+constexpr int kSumAhead = sizeof(T) == 2 ? 8 : 4;
+constexpr int kSumBatch = 2;  // otherwise, in registers
 
 struct SumArgs {
   const uint2* sorted;
   const void* de;
   int64_t N, ld_de, ld_grad;
   int V, D;
-  int lanes;        // of a group: 8 columns each
+  int lanes;        // of a group (8, 16 or 32): 8 columns each
   int piece;        // list entries of a group
   float scale;
   bool accumulate;
@@ -246,6 +309,9 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocks) embed_sum_kernel(SumA
   __shared__ float heads[kSumThreads * 8], tails[kSumThreads * 8];
   __shared__ uint32_t tokens[kSumThreads];
   __shared__ uint8_t has_head[kSumThreads], has_tail[kSumThreads], through[kSumThreads];
+  constexpr int kHalves = sizeof(Tin) / 2;  // 16-byte copies of a lane's columns
+  __shared__ uint4 ring[VEC ? kSumAhead<Tin> * kHalves * kSumThreads : 1];
+  auto slot = [&](int j, int h) { return ring + (j * kHalves + h) * kSumThreads + threadIdx.x; };
   const int group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes, groups = kSumThreads / a.lanes;
   const int col = first_column(blockIdx.y, lane, a.lanes, VEC);
   const int64_t begin = min(a.N, (static_cast<int64_t>(blockIdx.x) * groups + group) * a.piece);
@@ -258,41 +324,82 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocks) embed_sum_kernel(SumA
 #pragma unroll
     for (int j = 0; j < 8; ++j) where[j * kSumThreads + threadIdx.x] = s[j];
   };
-  if (begin < end) {
-    uint32_t token = a.sorted[begin].x;
-    bool reaches_in = begin > 0 && a.sorted[begin - 1].x == token;
-    uint2 e[kSumBatch];
-    auto entries = [&](int64_t i) {
-#pragma unroll
-      for (int j = 0; j < kSumBatch; ++j) e[j] = i + j < end ? a.sorted[i + j] : make_uint2(none, 0);
-    };
-    entries(begin);
-    for (int64_t i = begin; i < end && e[0].x != none; i += kSumBatch) {
-      Columns<Tin, VEC> rows[kSumBatch];
-      uint32_t t[kSumBatch];
-#pragma unroll
-      for (int j = 0; j < kSumBatch; ++j) {
-        t[j] = e[j].x;
-        if (t[j] != none && col < a.D)
-          rows[j].load(static_cast<const Tin*>(a.de) + e[j].y * a.ld_de, col, a.lanes, a.D);
+  // (entries of the warp's first group, the longest: its groups go on together)
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * groups + (threadIdx.x & ~31) / a.lanes) * a.piece;
+  const int64_t longest = min(static_cast<int64_t>(a.piece), a.N - first);
+  if (longest > 0) {
+    uint32_t token = begin < end ? a.sorted[begin].x : none;
+    bool reaches_in = begin > 0 && begin < end && a.sorted[begin - 1].x == token;
+    auto entry = [&](int64_t i) { return i < end ? a.sorted[i] : make_uint2(none, 0); };
+    // the next row's token: what has been summed for another is done
+    auto turn_to = [&](uint32_t next) {
+      if (next == token) return;
+      if (reaches_in) {
+        deposit(heads);
+        if (lane == 0) has_head[group] = 1;
+      } else {
+        write_row<Tout, VEC>(a, token, col, s);
       }
-      entries(i + kSumBatch);
+      reaches_in = false;
+      token = next;
 #pragma unroll
-      for (int j = 0; j < kSumBatch; ++j) {
-        if (t[j] == none) continue;
-        if (t[j] != token) {
-          if (reaches_in) {
-            deposit(heads);
-            if (lane == 0) has_head[group] = 1;
-          } else {
-            write_row<Tout, VEC>(a, token, col, s);
-          }
-          reaches_in = false;
-          token = t[j];
+      for (int k = 0; k < 8; ++k) s[k] = 0.f;
+    };
+    if constexpr (VEC) {
+      // entries arrive a window of a group's lanes at a time, an entry a lane
+      constexpr int kAhead = kSumAhead<Tin>;
+      uint2 now = entry(begin + lane), after = entry(begin + a.lanes + lane);
+      auto fetch = [&](int j, const uint2& w, int at) {  // the row of a window's entry
+        const uint32_t token_at = __shfl_sync(0xFFFFFFFFu, w.x, at, a.lanes);
+        const uint32_t n = __shfl_sync(0xFFFFFFFFu, w.y, at, a.lanes);
+        if (token_at != none && col < a.D) {
+          const Tin* const row = static_cast<const Tin*>(a.de) + n * a.ld_de + col;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s[k] = 0.f;
+          for (int h = 0; h < kHalves; ++h) cp_async_16(slot(j, h), row + h * 4);
         }
-        if (col < a.D) rows[j].add_to(s);
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) fetch(j, now, j);
+      for (int64_t i = 0; i < longest; i += a.lanes) {
+        for (int at = 0; at < a.lanes && i + at < longest; at += kAhead) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const uint32_t t = __shfl_sync(0xFFFFFFFFu, now.x, at + j, a.lanes);
+            cp_async_wait_group<kAhead - 1>();
+            if (t != none) {
+              turn_to(t);
+              if (col < a.D) {
+                Columns<Tin, VEC> row;
+                row.raw.load_halves(slot(j, 0), slot(j, kHalves - 1));
+                row.add_to(s);
+              }
+            }
+            if (at + kAhead < a.lanes)
+              fetch(j, now, at + kAhead + j);
+            else
+              fetch(j, after, j);
+          }
+        }
+        now = after;
+        after = entry(begin + i + 2 * a.lanes + lane);
+      }
+    } else {
+      for (int64_t i = begin; i < end; i += kSumBatch) {
+        Columns<Tin, VEC> rows[kSumBatch];
+        uint2 e[kSumBatch];
+#pragma unroll
+        for (int j = 0; j < kSumBatch; ++j) {
+          e[j] = entry(i + j);
+          if (e[j].x != none && col < a.D)
+            rows[j].load(static_cast<const Tin*>(a.de) + e[j].y * a.ld_de, col, a.lanes, a.D);
+        }
+#pragma unroll
+        for (int j = 0; j < kSumBatch; ++j) {
+          if (e[j].x == none) continue;
+          turn_to(e[j].x);
+          if (col < a.D) rows[j].add_to(s);
+        }
       }
     }
     if (token != none) {
@@ -358,17 +465,32 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumArgs a, int 
   auto at = [&](const float* p, int block) {
     return p + ((static_cast<int64_t>(blockIdx.y) * blocks + block) * a.lanes + lane) * 8;
   };
-  Raw8<float> r;
-  r.load(at(a.tail, b));
-  r.get(s);
-  for (int k = b + 1; k < blocks; ++k) {
-    float v[8];
-    r.load(at(a.head, k));
-    r.get(v);
+  Raw8<float> first;
+  first.load(at(a.tail, b));
+  first.get(s);
+  constexpr int kAhead = 4;
+  bool on = true;  // the run reaches into block k
+  for (int k0 = b + 1; k0 < blocks && on; k0 += kAhead) {
+    Raw8<float> r[kAhead];
+    bool out[kAhead];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] += v[j];
-    const int64_t next = (k + 1) * per_block;
-    if (next >= a.N || token_at(next) != token) break;
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j;
+      const int64_t next = (k + 1) * per_block;
+      out[j] = k < blocks && next < a.N && token_at(next) == token;
+      r[j].zero();
+      if (k < blocks) r[j].load(at(a.head, k));  // (of a block without a head: unused)
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (on) {
+        float v[8];
+        r[j].get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += v[i];
+      }
+      on = on && out[j];
+    }
   }
   write_row<Tout, VEC>(a, token, first_column(blockIdx.y, lane, a.lanes, VEC), s);
 }
@@ -407,7 +529,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
   uint8_t* p = c.scratch;
   SortArgs t{};
   t.totals = reinterpret_cast<uint32_t*>(p);
-  p += 2 * kSortMaxCluster * kSortMaxBins * 4;
+  p += (kSortMaxPasses * kSortMaxCluster * 4) << kSortMaxBits;
   t.half = reinterpret_cast<uint2*>(p);
   p += kEmbedGradMaxRows * 8;
   t.sorted = reinterpret_cast<uint2*>(p);
@@ -418,11 +540,11 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
   t.status = a.status;
   int bits = 1;
   while ((a.V >> bits) != 0) ++bits;  // tokens 0 .. V
-  t.passes = bits <= 9 ? 1 : 2;
+  t.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
   t.bits = std::max(5, (bits + t.passes - 1) / t.passes);
-  // 4096 entries a block: below that another block costs more than its share saves
+  // 2048 entries a block: below that another block costs more than its share saves
   t.cluster = 1;
-  while (t.cluster < kSortMaxCluster && a.N > 4096 * static_cast<int64_t>(t.cluster)) t.cluster *= 2;
+  while (t.cluster < kSortMaxCluster && a.N > 2048 * static_cast<int64_t>(t.cluster)) t.cluster *= 2;
   int grid = t.cluster;
   if (!a.accumulate) {
     t.grad = a.grad;
@@ -432,7 +554,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
     grid = c.num_sms / t.cluster * t.cluster;
   }
   const int smem = ((kSortWarps + 1) << t.bits) * 4;
-  cudaError_t e = (*c.opt_in)(embed_sort_kernel, ((kSortWarps + 1) * kSortMaxBins) * 4);
+  cudaError_t e = (*c.opt_in)(embed_sort_kernel, ((kSortWarps + 1) << kSortMaxBits) * 4);
   if (e != cudaSuccess) return e;
   if (t.cluster > 8) {
     e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -467,11 +589,12 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
   s.grad = a.grad;
   const bool vec = a.D % 8 == 0 && rows_of_8(a.de, a.ld_de, a.de_dtype) && rows_of_8(a.grad, a.ld_grad, a.grad_dtype);
   s.lanes = 32;
-  while (vec && s.lanes > 1 && s.lanes * 4 >= a.D) s.lanes /= 2;
+  while (vec && s.lanes > 8 && s.lanes * 4 >= a.D) s.lanes /= 2;
   const int slices = (a.D + s.lanes * 8 - 1) / (s.lanes * 8), groups = kSumThreads / s.lanes;
   // one wave of blocks over list and columns
   const int64_t most = kSumBlocks * c.num_sms * groups;
-  s.piece = static_cast<int>(std::max<int64_t>(4, (a.N * slices + most - 1) / most));
+  s.piece = static_cast<int>(std::max<int64_t>(8, (a.N * slices + most - 1) / most));
+  if (s.piece > s.lanes / 2) s.piece = (s.piece + s.lanes - 1) / s.lanes * s.lanes;  // whole windows
   const int blocks = static_cast<int>((a.N + static_cast<int64_t>(s.piece) * groups - 1) / (static_cast<int64_t>(s.piece) * groups));
   s.head = reinterpret_cast<float*>(p);
   s.tail = s.head + static_cast<int64_t>(blocks) * slices * s.lanes * 8;

@@ -1,5 +1,6 @@
-// typed.cuh -- elements of either type of the training step's tensors as floats: one, or eight at
-// 16-byte aligned addresses.
+// typed.cuh -- elements of either type of the training step's tensors as floats: one, or eight of a
+// lane in one 32-byte (fp32) or 16-byte (bf16) access at an address so aligned. (Two 16-byte accesses
+// of fp32 would each touch every 32-byte sector of a warp's piece.)
 #pragma once
 
 #include <cstdint>
@@ -28,8 +29,14 @@ template <>
 struct Raw8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                 : "l"(p)
+                 : "memory");
+  }
+  __device__ __forceinline__ void load_halves(const uint4* p, const uint4* q) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(q);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -43,6 +50,7 @@ struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     a = *reinterpret_cast<const uint4*>(p);
   }
+  __device__ __forceinline__ void load_halves(const uint4* p, const uint4*) { a = *p; }
   __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     widen2(a.x, v[0], v[1]);
@@ -52,18 +60,18 @@ struct Raw8<__nv_bfloat16> {
   }
 };
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(narrow2(v[0], v[1]), narrow2(v[2], v[3]),
                                             narrow2(v[4], v[5]), narrow2(v[6], v[7]));
 }
 
-// Rows that allow vectors of eight: the first on a 16-byte boundary, and all of them.
+// Rows that allow vectors of eight: the first on such a boundary, and all of them.
 inline bool rows_of_8(const void* p, int64_t ld, int dtype) {
-  const int64_t bytes = ld * (dtype == 0 ? 4 : 2);
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (bytes & 15) == 0;
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == 0 ? 31u : 15u)) == 0 && ld % 8 == 0;
 }
 
 }  // namespace dspark
