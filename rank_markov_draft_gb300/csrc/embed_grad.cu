@@ -3,8 +3,10 @@
 // The rows are put in the order of their tokens (equal tokens in the order of the rows), and the
 // sorted list is cut into equal pieces, so that a token of a tenth of all rows costs no more than ten
 // thousand tokens of one row each; sums of tokens that lie in several pieces are joined in their order.
-// No atomics decide an order: equal inputs give equal bits.  Three launches:
-//   sort: one cluster sorts while the other clusters store the zeros of all table rows;
+// No atomics decide an order: equal inputs give equal bits.  The launches:
+//   sort: one cluster sorts; beside it zeros are stored to all table rows, by the other clusters of its
+//     launch, or, beside a cluster of 16 (few of which find room at a time: the zeros of 156 MB then
+//     took 42 us instead of 25), by a launch that overlaps it;
 //   sums: a group of lanes a piece, a row a group at a time, joined within the block;
 //   join: tokens that lie in several blocks.
 
@@ -87,15 +89,18 @@ __device__ __forceinline__ void store_zeros(const SortArgs& a, int block, int bl
 
 // Stable counting sort by `bits` bits of the token a pass, over one cluster: each warp counts the
 // digits of its stretch of the list, the counts of all blocks give each warp's first place of every
-// digit, and the warps place their elements. Elements are taken 32 at a time; lanes of the same digit
-// find one another by a vote a bit, which takes as long for digits all alike (the high ones of text)
-// as for distinct ones (the match instruction took twice as long, atomics on a word a digit between). Where a warp's stretch fits its registers (131072 entries in 16
-// blocks) the places found while counting are kept.
+// digit, and the warps place their elements. Elements are taken 32 at a time, and each finds the lanes
+// of its digit: for the low digits by an OR of their bits into a word of shared memory (4400 clocks for
+// 8192 elements), for the high ones, which text has mostly alike, by a vote a bit (8700 clocks, where
+// the ORs would take 9400; the match instruction took as long for either).
+// Where a warp's stretch fits its registers (131072 entries in 16 blocks) the places found while
+// counting are kept, and the low digits' elements are put in order within the block first, so that
+// their stores go to runs of some 16 of them (4 clocks an element otherwise, a sector each).
 constexpr int kSortHeld = 8;  // elements of a lane in registers
 
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a) {
-  extern __shared__ uint32_t counts[];  // [warps][bins], then [bins]
-  __shared__ uint32_t warp_sum[kSortWarps];
+  extern __shared__ uint32_t counts[];  // [warps][bins], 3 [bins], lanes or elements
+  __shared__ uint32_t warp_sum[kSortWarps], warp_local[kSortWarps];
   griddep_launch_dependents();
   const int c = blockIdx.x;
   if (c >= a.cluster) {
@@ -105,6 +110,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
   const int bins = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* const mine = counts + warp * bins;
   uint32_t* const base = counts + kSortWarps * bins;
+  uint32_t* const local = base + bins;  // the block's elements of lower digits
+  uint32_t* const lanes = local + 2 * bins + warp * bins;
+  uint2* const staged = reinterpret_cast<uint2*>(local + 2 * bins);
   const int64_t stretch = (a.N + static_cast<int64_t>(a.cluster) * kSortThreads - 1) /
                           (static_cast<int64_t>(a.cluster) * kSortThreads) * 32;  // a warp's
   const int64_t lo = min(a.N, (static_cast<int64_t>(c) * kSortWarps + warp) * stretch);
@@ -112,6 +120,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
   const bool held = stretch <= 32 * kSortHeld;
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.bits;
+    const bool spread = pass + 1 < a.passes;
     const bool last_is_odd = (a.passes - pass) & 1;
     uint2* const dst = last_is_odd ? a.sorted : a.half;
     const uint2* const src = last_is_odd ? a.half : a.sorted;
@@ -149,17 +158,27 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
         if (i0 + 32 * j >= hi) break;
         const bool in = e[j].x != 0xFFFFFFFFu;
         const uint32_t digit = digit_of(e[j]);
-        unsigned same = __ballot_sync(0xFFFFFFFFu, in);
+        unsigned same = 0;
+        if (spread) {
+          if (in) atomicOr(lanes + digit, 1u << lane);
+          __syncwarp();
+          same = in ? lanes[digit] : 0;
+        } else {
+          same = __ballot_sync(0xFFFFFFFFu, in);
 #pragma unroll
-        for (int bit = 0; bit < kSortMaxBits; ++bit) {
-          const bool one = digit & (1u << bit);
-          const unsigned set = __ballot_sync(0xFFFFFFFFu, one);
-          same &= one ? set : ~set;
+          for (int bit = 0; bit < kSortMaxBits; ++bit) {
+            const bool one = digit & (1u << bit);
+            const unsigned set = __ballot_sync(0xFFFFFFFFu, one);
+            same &= one ? set : ~set;
+          }
         }
         const uint32_t at = in ? mine[digit] : 0;
         place[j] = at + __popc(same & ((1u << lane) - 1));
         __syncwarp();
-        if (in && (same >> lane) == 1) mine[digit] = at + __popc(same);  // the last of them
+        if (in && (same >> lane) == 1) {  // the last of them
+          mine[digit] = at + __popc(same);
+          if (spread) lanes[digit] = 0;
+        }
         __syncwarp();
       }
     };
@@ -172,8 +191,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
         }
     };
     fetch(lo);
-    for (int i = threadIdx.x; i < kSortWarps * bins / 4; i += kSortThreads)
+    for (int i = threadIdx.x; i < kSortWarps * bins / 4; i += kSortThreads) {
       reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
+      if (spread) reinterpret_cast<uint4*>(staged)[i] = make_uint4(0, 0, 0, 0);  // (the words of `lanes`)
+    }
     __syncthreads();
     count(lo);
     for (int64_t i0 = lo + 32 * kSortHeld; i0 < hi; i0 += 32 * kSortHeld) {
@@ -182,15 +203,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
     }
     __syncthreads();
     uint32_t* const totals = a.totals + static_cast<int64_t>(pass) * a.cluster * bins;
+    uint32_t here = 0;
     if (threadIdx.x < bins) {
-      uint32_t s = 0;
 #pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t n = counts[w * bins + threadIdx.x];
-        counts[w * bins + threadIdx.x] = s;
-        s += n;
+        counts[w * bins + threadIdx.x] = here;
+        here += n;
       }
-      totals[c * bins + threadIdx.x] = s;
+      totals[c * bins + threadIdx.x] = here;
     }
     cluster_sync();
     uint32_t below = 0, all = 0;
@@ -202,20 +223,42 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
         all += n;
       }
     }
-    uint32_t incl = all;
+    uint32_t incl = all, incl_here = here;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, incl, o), m = __shfl_up_sync(0xFFFFFFFFu, incl_here, o);
       incl += lane >= o ? n : 0;
+      incl_here += lane >= o ? m : 0;
     }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) warp_sum[warp] = incl, warp_local[warp] = incl_here;
     __syncthreads();
-    uint32_t before = lane < warp ? warp_sum[lane] : 0;
+    uint32_t before = lane < warp ? warp_sum[lane] : 0, before_here = lane < warp ? warp_local[lane] : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-    if (threadIdx.x < bins) base[threadIdx.x] = before + incl - all + below;
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+      before_here += __shfl_xor_sync(0xFFFFFFFFu, before_here, o);
+    }
+    if (threadIdx.x < bins) {
+      base[threadIdx.x] = before + incl - all + below;
+      local[threadIdx.x] = before_here + incl_here - here;
+    }
     __syncthreads();
-    if (held) {
+    if (held && spread) {
+#pragma unroll
+      for (int j = 0; j < kSortHeld; ++j)
+        if (e[j].x != 0xFFFFFFFFu) {
+          const uint32_t d = digit_of(e[j]);
+          staged[local[d] + mine[d] + place[j]] = e[j];
+        }
+      __syncthreads();
+      const int n = static_cast<int>(min(a.N, (c + 1) * kSortWarps * stretch) - min(a.N, c * kSortWarps * stretch));
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += kSortThreads) {
+        const uint2 x = staged[i];
+        const uint32_t d = digit_of(x);
+        dst[base[d] + i - local[d]] = x;
+      }
+    } else if (held) {
       put(true);
     } else {  // `mine` goes on as a running count
       for (int64_t i0 = lo; i0 < hi; i0 += 32 * kSortHeld) {
@@ -226,6 +269,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
     }
     if (pass + 1 < a.passes) cluster_sync();
   }
+}
+
+// The zeros as a launch of their own, which ends after the sort that it overlaps.
+__global__ void __launch_bounds__(kSortThreads) embed_zeros_kernel(SortArgs a) {
+  griddep_launch_dependents();
+  store_zeros(a, blockIdx.x, gridDim.x);
+  if (blockIdx.x + 1 == gridDim.x) griddep_wait();  // (all of them would hold their SMs meanwhile)
 }
 
 // ------------------------------------------------------------------ sums
@@ -468,7 +518,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumArgs a, int 
   Raw8<float> first;
   first.load(at(a.tail, b));
   first.get(s);
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   bool on = true;  // the run reaches into block k
   for (int k0 = b + 1; k0 < blocks && on; k0 += kAhead) {
     Raw8<float> r[kAhead];
@@ -496,10 +546,11 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumArgs a, int 
 }
 
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, cudaStream_t stream, Args... args) {
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream,
+                             Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kSumThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -511,12 +562,13 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, cudaStream_t 
 
 template <typename Tin, typename Tout, bool VEC>
 cudaError_t sums(const SumArgs& s, int blocks, int slices, int* launches, cudaStream_t stream) {
-  cudaError_t e = launch_dependent(embed_sum_kernel<Tin, Tout, VEC>, dim3(blocks, slices), stream, s);
+  cudaError_t e = launch_dependent(embed_sum_kernel<Tin, Tout, VEC>, dim3(blocks, slices), kSumThreads, stream, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (blocks == 1) return e;
   const int groups = kSumThreads / s.lanes;
-  e = launch_dependent(embed_join_kernel<Tout, VEC>, dim3((blocks + groups - 1) / groups, slices), stream, s, blocks);
+  e = launch_dependent(embed_join_kernel<Tout, VEC>, dim3((blocks + groups - 1) / groups, slices),
+                       kSumThreads, stream, s, blocks);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
@@ -551,10 +603,12 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
     t.ld_grad = a.ld_grad;
     t.D = a.D;
     t.size = a.grad_dtype == DSPARK_F32 ? 4 : 2;
-    grid = c.num_sms / t.cluster * t.cluster;
+    if (t.cluster <= 8) grid = c.num_sms / t.cluster * t.cluster;
   }
-  const int smem = ((kSortWarps + 1) << t.bits) * 4;
-  cudaError_t e = (*c.opt_in)(embed_sort_kernel, ((kSortWarps + 1) << kSortMaxBits) * 4);
+  // counts, three words a digit, and the larger of the lanes' words and the elements in order
+  auto sort_smem = [](int bits) { return ((kSortWarps + 3) << bits) * 4 + std::max((kSortWarps << bits) * 4, kSortThreads * kSortHeld * 8); };
+  const int smem = sort_smem(t.bits);
+  cudaError_t e = (*c.opt_in)(embed_sort_kernel, sort_smem(kSortMaxBits));
   if (e != cudaSuccess) return e;
   if (t.cluster > 8) {
     e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -574,6 +628,14 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
   e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, t);
   if (e != cudaSuccess) return e;
   *c.launches += 1;
+  if (!a.accumulate && t.cluster > 8) {
+    // (64 KB a block: the SMs that sort leave theirs to the others)
+    const int64_t chunks = static_cast<int64_t>(a.V) * a.D * t.size / 65536;
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(chunks, 1), 8192));
+    e = launch_dependent(embed_zeros_kernel, dim3(blocks), kSortThreads, stream, t);
+    if (e != cudaSuccess) return e;
+    *c.launches += 1;
+  }
   if (a.N == 0) return e;
 
   SumArgs s{};
