@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 from typing import Optional
 
@@ -528,23 +529,35 @@ def dspark_embed_grad(ctx: Context, ids, de, N, V, D, scale, accumulate, grad, s
     _check(code, "dspark_embed_grad")
 
 
+def _tensor_list(ts, name: str):
+    """Addresses, element counts and dtypes of a list of contiguous CUDA tensors, for C."""
+    for t in ts:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected torch.Tensors")
+    try:
+        dtypes = array("i", [_DTYPE[t.dtype] for t in ts])
+    except KeyError as e:
+        raise TypeError(f"{name}: dtype {e.args[0]} not in {tuple(_DTYPE)}") from None
+    if not all([t.is_contiguous() for t in ts]):
+        raise ValueError(f"{name}: must be contiguous")
+    if not all([t.is_cuda for t in ts]):
+        raise ValueError(f"{name}: must live in CUDA device memory")
+    return array("Q", [t.data_ptr() for t in ts]), array("q", [t.numel() for t in ts]), dtypes
+
+
 def dspark_clip_grads(ctx: Context, grads, max_norm, out, norm, stream=None):
     """grads and out: lists of contiguous tensors (out None: only the norm)."""
-    n = len(grads)
-    src = (ctypes.c_void_p * n)(*[_ptr(g, None, "grads") for g in grads])
-    numel = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    dtypes = (ctypes.c_int32 * n)(*[_dtype(g, "grads") for g in grads])
+    src, numel, dtypes = _tensor_list(grads, "grads")
     dst = None
     if out is grads:
         dst = src
     elif out is not None:
-        if len(out) != n:
-            raise ValueError(f"out: {len(out)} tensors for {n} gradients")
-        for o, g in zip(out, grads):
-            if o.dtype != g.dtype or o.shape != g.shape:
-                raise ValueError(f"out: {tuple(o.shape)} {o.dtype} is not {tuple(g.shape)} {g.dtype}")
-        dst = (ctypes.c_void_p * n)(*[_ptr(o, None, "out") for o in out])
-    code = ctx.lib.dspark_clip_grads(ctx.handle, src, numel, dtypes, n, float(max_norm), dst,
+        dst, n, dt = _tensor_list(out, "out")
+        if n != numel or dt != dtypes:
+            raise ValueError("out: other sizes or types than the gradients'")
+    address = lambda a: None if a is None else a.buffer_info()[0]  # noqa: E731
+    code = ctx.lib.dspark_clip_grads(ctx.handle, address(src), address(numel), address(dtypes),
+                                     len(src), float(max_norm), address(dst),
                                      _ptr(norm, (torch.float32,), "norm"),
                                      _stream(stream, ctx.device))
     _check(code, "dspark_clip_grads")

@@ -206,8 +206,8 @@ cudaError_t clip(const ClipArgs& a, int* launches, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_clip(const ClipArgs& a, int* launches, cudaStream_t stream) {
-  // a short list makes short launch arguments (1 KB instead of 17)
-  return a.count <= 32 ? clip<32>(a, launches, stream) : clip<kClipMaxTensors>(a, launches, stream);
+  // a short list makes short launch arguments (2 KB instead of 17)
+  return a.count <= 64 ? clip<64>(a, launches, stream) : clip<kClipMaxTensors>(a, launches, stream);
 }
 
 }  // namespace dspark

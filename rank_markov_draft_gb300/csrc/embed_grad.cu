@@ -5,8 +5,8 @@
 // thousand tokens of one row each; sums of tokens that lie in several pieces are joined in their order.
 // No atomics decide an order: equal inputs give equal bits.  The launches:
 //   sort: one cluster sorts; beside it zeros are stored to all table rows, by the other clusters of its
-//     launch, or, beside a cluster of 16 (few of which find room at a time: the zeros of 156 MB then
-//     took 42 us instead of 25), by a launch that overlaps it;
+//     launch, or, beside a cluster of 8 or 16 (few of which find room at a time: the zeros of 156 MB then
+//     took 42 us instead of 25, those of 65 MB 16 instead of 13), by a launch that overlaps it;
 //   sums: a group of lanes a piece, a row a group at a time, joined within the block;
 //   join: tokens that lie in several blocks.
 
@@ -603,7 +603,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
     t.ld_grad = a.ld_grad;
     t.D = a.D;
     t.size = a.grad_dtype == DSPARK_F32 ? 4 : 2;
-    if (t.cluster <= 8) grid = c.num_sms / t.cluster * t.cluster;
+    if (t.cluster <= 4) grid = c.num_sms / t.cluster * t.cluster;
   }
   // counts, three words a digit, and the larger of the lanes' words and the elements in order
   auto sort_smem = [](int bits) { return ((kSortWarps + 3) << bits) * 4 + std::max((kSortWarps << bits) * 4, kSortThreads * kSortHeld * 8); };
@@ -628,7 +628,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
   e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, t);
   if (e != cudaSuccess) return e;
   *c.launches += 1;
-  if (!a.accumulate && t.cluster > 8) {
+  if (!a.accumulate && t.cluster > 4) {
     // (64 KB a block: the SMs that sort leave theirs to the others)
     const int64_t chunks = static_cast<int64_t>(a.V) * a.D * t.size / 65536;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(chunks, 1), 8192));
