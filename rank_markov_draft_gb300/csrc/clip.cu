@@ -7,7 +7,9 @@
 
 #include <algorithm>
 
+#include "dependent.h"
 #include "dspark.h"
+#include "sm103.cuh"
 #include "step.h"
 #include "typed.cuh"
 
@@ -17,7 +19,9 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 512;
-constexpr int kChunk = 16384;  // elements of one tensor that a block takes at a time
+constexpr int kChunk = 8 * kThreads;  // elements of one tensor that a block takes at a time, eight a thread
+constexpr int kAhead = 2;             // chunks under way a block
+constexpr int kAdds = 32;             // squares that a thread adds up in 32 bits
 
 // The tensors of one launch.
 template <int CAP>
@@ -30,16 +34,86 @@ struct ClipList {
   int count;
 };
 
-// The tensor that chunk c lies in.
+// A block's chunks: an equal stretch of all of them, walked up or down.
 template <int CAP>
-__device__ __forceinline__ int tensor_of(const ClipList<CAP>& l, int64_t c) {
-  int lo = 0, hi = l.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    (l.first[mid] <= c ? lo : hi) = mid;
+struct Walk {
+  const ClipList<CAP>& l;
+  int64_t begin, end;
+  int t;  // tensor of the chunk asked for last
+
+  __device__ __forceinline__ explicit Walk(const ClipList<CAP>& list) : l(list) {
+    const int64_t chunks = l.first[l.count];
+    begin = chunks * blockIdx.x / gridDim.x;
+    end = chunks * (blockIdx.x + 1) / gridDim.x;
+    t = 0;
   }
-  return lo;
-}
+  // to the tensor of chunk c
+  __device__ __forceinline__ void find(int64_t c) {
+    int lo = 0, hi = l.count;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      (l.first[mid] <= c ? lo : hi) = mid;
+    }
+    t = lo;
+  }
+  __device__ __forceinline__ void follow(int64_t c) {  // the same for a neighbour of the last
+    while (l.first[t + 1] <= c) ++t;
+    while (l.first[t] > c) --t;
+  }
+};
+
+// This thread's part of a chunk.
+struct Piece {
+  Raw8<float> f;
+  Raw8<bf16> h;
+  int t, n;       // its tensor; elements (< 8: a tail or a tensor without vectors)
+  int64_t at;     // the first
+  float v[8];     // of those
+
+  template <int CAP>
+  __device__ __forceinline__ void load(Walk<CAP>& w, int64_t c) {
+    n = 0;
+    if (c < w.begin || c >= w.end) return;
+    w.follow(c);
+    t = w.t;
+    const int64_t rest = w.l.numel[t] - (c - w.l.first[t]) * kChunk;
+    at = (c - w.l.first[t]) * kChunk + 8 * threadIdx.x;
+    const int64_t mine = rest - 8 * static_cast<int>(threadIdx.x);
+    n = mine >= 8 ? 8 : (mine > 0 ? static_cast<int>(mine) : 0);
+    if (n == 8 && w.l.wide[t]) {
+      if (w.l.bf16_in[t])
+        h.load(static_cast<const bf16*>(w.l.in[t]) + at);
+      else
+        f.load(static_cast<const float*>(w.l.in[t]) + at);
+    }
+  }
+  template <int CAP>
+  __device__ __forceinline__ void get(const Walk<CAP>& w) {
+    const bool is_bf16 = w.l.bf16_in[t];
+    if (n == 8 && w.l.wide[t]) {
+      is_bf16 ? h.get(v) : f.get(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = 0.f;
+        if (j < n) v[j] = is_bf16 ? load1(static_cast<const bf16*>(w.l.in[t]) + at + j) : load1(static_cast<const float*>(w.l.in[t]) + at + j);
+      }
+    }
+  }
+  template <int CAP>
+  __device__ __forceinline__ void put(const Walk<CAP>& w, float c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= c;
+    const bool is_bf16 = w.l.bf16_in[t];
+    if (n == 8 && w.l.wide[t]) {
+      is_bf16 ? store8(static_cast<bf16*>(w.l.out[t]) + at, v) : store8(static_cast<float*>(w.l.out[t]) + at, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) is_bf16 ? store1(static_cast<bf16*>(w.l.out[t]) + at + j, v[j]) : store1(static_cast<float*>(w.l.out[t]) + at + j, v[j]);
+    }
+  }
+};
 
 // Sum over the block, on every thread.
 __device__ __forceinline__ double block_sum(double v) {
@@ -55,47 +129,37 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-template <typename T>
-__device__ __forceinline__ void add_squares(const T* p, int n, bool wide, float (&s)[8]) {
-  if (wide) {
-    const int n8 = n / 8;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n8; i += kThreads) {
-      Raw8<T> r;
-      float v[8];
-      r.load(p + 8 * i);
-      r.get(v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = fmaf(v[j], v[j], s[j]);
-    }
-    const int i = n8 * 8 + threadIdx.x;
-    if (i < n) s[0] = fmaf(load1(p + i), load1(p + i), s[0]);
-  } else {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float v = load1(p + i);
-      s[0] = fmaf(v, v, s[0]);
-    }
-  }
-}
-
-// The sums are of 32 bits within a thread (eight of them, a few dozen squares each and chunk) and of
-// 64 beyond.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     clip_squares_kernel(const __grid_constant__ ClipList<CAP> l, double* partial, bool add) {
+  griddep_launch_dependents();
+  Walk<CAP> w(l);
+  if (w.begin < w.end) w.find(w.begin);
   double total = 0.0;
-  for (int64_t c = blockIdx.x; c < l.first[l.count]; c += gridDim.x) {
-    const int t = tensor_of(l, c);
-    const int64_t at = (c - l.first[t]) * kChunk;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), l.numel[t] - at));
-    float s[8] = {};
-    if (l.bf16_in[t])
-      add_squares(static_cast<const bf16*>(l.in[t]) + at, n, l.wide[t], s);
-    else
-      add_squares(static_cast<const float*>(l.in[t]) + at, n, l.wide[t], s);
+  float s[8] = {};
+  int adds = 0;
+  auto fold = [&]() {
     total += static_cast<double>(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+    adds = 0;
+  };
+  Piece p[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) p[k].load(w, w.begin + k);
+  for (int64_t c = w.begin; c < w.end; c += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (p[k].n > 0) {
+        p[k].get(w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = fmaf(p[k].v[j], p[k].v[j], s[j]);
+      }
+      p[k].load(w, c + kAhead + k);
+    }
+    if ((adds += kAhead) == kAdds) fold();
   }
+  fold();
   total = block_sum(total);
   if (threadIdx.x == 0) partial[blockIdx.x] = total + (add ? partial[blockIdx.x] : 0.0);
 }
@@ -107,55 +171,36 @@ __device__ __forceinline__ double norm_of(const double* partial, int parts) {
 }
 
 __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const double* partial, int parts, float* norm) {
+  griddep_wait();
   const double v = norm_of(partial, parts);
   if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
-template <typename T>
-__device__ __forceinline__ void scale_chunk(const T* p, T* q, int n, bool wide, float c) {
-  if (wide) {
-    const int n8 = n / 8;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n8; i += kThreads) {
-      Raw8<T> r;
-      float v[8];
-      r.load(p + 8 * i);
-      r.get(v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= c;
-      store8(q + 8 * i, v);
-    }
-    const int i = n8 * 8 + threadIdx.x;
-    if (i < n) store1(q + i, load1(p + i) * c);
-  } else {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kThreads) store1(q + i, load1(p + i) * c);
-  }
-}
-
+// From the end of each block's stretch: what was read last is still in L2.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     clip_scale_kernel(const __grid_constant__ ClipList<CAP> l, const double* partial, int parts,
                       float max_norm, float* norm) {
+  Walk<CAP> w(l);
+  if (w.begin < w.end) w.find(w.end - 1);
+  griddep_wait();
+  Piece p[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) p[k].load(w, w.end - 1 - k);
   const double total = norm_of(partial, parts);
   double coef = static_cast<double>(max_norm) / (total + 1e-6);
   if (coef > 1.0) coef = 1.0;  // (a NaN stays one)
-  const float c = static_cast<float>(coef);
+  const float f = static_cast<float>(coef);
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
-  const int64_t chunks = l.first[l.count];
-  // from the end: what was read last is still in L2
-  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const int64_t at_chunk = chunks - 1 - k;
-    const int t = tensor_of(l, at_chunk);
-    if (c == 1.f && l.in[t] == l.out[t]) continue;
-    const int64_t at = (at_chunk - l.first[t]) * kChunk;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), l.numel[t] - at));
-    if (l.bf16_in[t])
-      scale_chunk(static_cast<const bf16*>(l.in[t]) + at, static_cast<bf16*>(l.out[t]) + at, n,
-                  l.wide[t], c);
-    else
-      scale_chunk(static_cast<const float*>(l.in[t]) + at, static_cast<float*>(l.out[t]) + at, n,
-                  l.wide[t], c);
+  for (int64_t c = w.end - 1; c >= w.begin; c -= kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (p[k].n > 0 && (f != 1.f || l.in[p[k].t] != l.out[p[k].t])) {
+        p[k].get(w);
+        p[k].put(w, f);
+      }
+      p[k].load(w, c - kAhead - k);
+    }
   }
 }
 
@@ -185,22 +230,24 @@ cudaError_t clip(const ClipArgs& a, int* launches, cudaStream_t stream) {
     *launches += 1;
     t0 += n;
   } while (t0 < a.count);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   if (a.out == nullptr) {
-    clip_norm_kernel<<<1, kThreads, 0, stream>>>(a.partial, parts, a.norm);
-    *launches += 1;
-    return cudaGetLastError();
+    e = launch_dependent(clip_norm_kernel, dim3(1), kThreads, stream, a.partial, parts, a.norm);
+    if (e == cudaSuccess) *launches += 1;
+    return e;
   }
   t0 = 0;
   do {
     const int n = std::min(CAP, a.count - t0);
     if (a.count > CAP) fill(l, a, t0, n);
-    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(parts, l.first[n]));
-    clip_scale_kernel<CAP><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
-        l, a.partial, parts, a.max_norm, t0 == 0 ? a.norm : nullptr);
+    e = launch_dependent(clip_scale_kernel<CAP>, dim3(parts), kThreads, stream, l, a.partial, parts,
+                         a.max_norm, t0 == 0 ? a.norm : nullptr);
+    if (e != cudaSuccess) return e;
     *launches += 1;
     t0 += n;
   } while (t0 < a.count);
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace

@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "async_copy.cuh"
+#include "dependent.h"
 #include "dspark.h"
 #include "sm103.cuh"
 #include "step.h"
@@ -543,21 +544,6 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumArgs a, int 
     }
   }
   write_row<Tout, VEC>(a, token, first_column(blockIdx.y, lane, a.lanes, VEC), s);
-}
-
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream,
-                             Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename Tin, typename Tout, bool VEC>
