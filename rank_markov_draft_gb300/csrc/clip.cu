@@ -6,6 +6,7 @@
 // tensors' addresses are launch arguments, so a captured graph holds them and nothing is copied.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dependent.h"
 #include "dspark.h"
@@ -18,10 +19,10 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kThreads = 512;
-constexpr int kChunk = 8 * kThreads;  // elements of one tensor that a block takes at a time, eight a thread
-constexpr int kAhead = 2;             // chunks under way a block
-constexpr int kAdds = 32;             // squares that a thread adds up in 32 bits
+constexpr int kThreads = 256, kBlocks = 4;  // of an SM
+constexpr int kChunk = 8 * kThreads;        // elements, eight a thread: the grain of the blocks' stretches
+constexpr int kAhead = 4;                   // vectors under way a thread
+constexpr int kAdds = 32;                   // squares that a thread adds up in 32 bits
 
 // The tensors of one launch.
 template <int CAP>
@@ -34,86 +35,28 @@ struct ClipList {
   int count;
 };
 
-// A block's chunks: an equal stretch of all of them, walked up or down.
-template <int CAP>
-struct Walk {
-  const ClipList<CAP>& l;
-  int64_t begin, end;
-  int t;  // tensor of the chunk asked for last
-
-  __device__ __forceinline__ explicit Walk(const ClipList<CAP>& list) : l(list) {
-    const int64_t chunks = l.first[l.count];
-    begin = chunks * blockIdx.x / gridDim.x;
-    end = chunks * (blockIdx.x + 1) / gridDim.x;
-    t = 0;
+// f(t, first, n) for each tensor in this block's equal stretch of all chunks: n elements from `first`.
+template <bool DOWN, int CAP, typename F>
+__device__ __forceinline__ void for_stretch(const ClipList<CAP>& l, F f) {
+  const int64_t chunks = l.first[l.count];
+  const int64_t begin = chunks * blockIdx.x / gridDim.x, end = chunks * (blockIdx.x + 1) / gridDim.x;
+  if (begin >= end) return;
+  const int64_t from = DOWN ? end - 1 : begin;
+  int lo = 0, hi = l.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    (l.first[mid] <= from ? lo : hi) = mid;
   }
-  // to the tensor of chunk c
-  __device__ __forceinline__ void find(int64_t c) {
-    int lo = 0, hi = l.count;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      (l.first[mid] <= c ? lo : hi) = mid;
+  for (int t = lo; t >= 0 && t < l.count; t += DOWN ? -1 : 1) {
+    const int64_t c0 = max(begin, l.first[t]), c1 = min(end, l.first[t + 1]);
+    if (c0 >= c1) {
+      if (DOWN ? l.first[t + 1] <= begin : l.first[t] >= end) break;
+      continue;  // (a tensor of no elements)
     }
-    t = lo;
+    const int64_t first = (c0 - l.first[t]) * kChunk;
+    f(t, first, min(l.numel[t], (c1 - l.first[t]) * kChunk) - first);
   }
-  __device__ __forceinline__ void follow(int64_t c) {  // the same for a neighbour of the last
-    while (l.first[t + 1] <= c) ++t;
-    while (l.first[t] > c) --t;
-  }
-};
-
-// This thread's part of a chunk.
-struct Piece {
-  Raw8<float> f;
-  Raw8<bf16> h;
-  int t, n;       // its tensor; elements (< 8: a tail or a tensor without vectors)
-  int64_t at;     // the first
-  float v[8];     // of those
-
-  template <int CAP>
-  __device__ __forceinline__ void load(Walk<CAP>& w, int64_t c) {
-    n = 0;
-    if (c < w.begin || c >= w.end) return;
-    w.follow(c);
-    t = w.t;
-    const int64_t rest = w.l.numel[t] - (c - w.l.first[t]) * kChunk;
-    at = (c - w.l.first[t]) * kChunk + 8 * threadIdx.x;
-    const int64_t mine = rest - 8 * static_cast<int>(threadIdx.x);
-    n = mine >= 8 ? 8 : (mine > 0 ? static_cast<int>(mine) : 0);
-    if (n == 8 && w.l.wide[t]) {
-      if (w.l.bf16_in[t])
-        h.load(static_cast<const bf16*>(w.l.in[t]) + at);
-      else
-        f.load(static_cast<const float*>(w.l.in[t]) + at);
-    }
-  }
-  template <int CAP>
-  __device__ __forceinline__ void get(const Walk<CAP>& w) {
-    const bool is_bf16 = w.l.bf16_in[t];
-    if (n == 8 && w.l.wide[t]) {
-      is_bf16 ? h.get(v) : f.get(v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = 0.f;
-        if (j < n) v[j] = is_bf16 ? load1(static_cast<const bf16*>(w.l.in[t]) + at + j) : load1(static_cast<const float*>(w.l.in[t]) + at + j);
-      }
-    }
-  }
-  template <int CAP>
-  __device__ __forceinline__ void put(const Walk<CAP>& w, float c) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= c;
-    const bool is_bf16 = w.l.bf16_in[t];
-    if (n == 8 && w.l.wide[t]) {
-      is_bf16 ? store8(static_cast<bf16*>(w.l.out[t]) + at, v) : store8(static_cast<float*>(w.l.out[t]) + at, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) is_bf16 ? store1(static_cast<bf16*>(w.l.out[t]) + at + j, v[j]) : store1(static_cast<float*>(w.l.out[t]) + at + j, v[j]);
-    }
-  }
-};
+}
 
 // Sum over the block, on every thread.
 __device__ __forceinline__ double block_sum(double v) {
@@ -129,38 +72,67 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads, 2)
-    clip_squares_kernel(const __grid_constant__ ClipList<CAP> l, double* partial, bool add) {
-  griddep_launch_dependents();
-  Walk<CAP> w(l);
-  if (w.begin < w.end) w.find(w.begin);
+// A thread's sum of squares: of 32 bits for kAdds of them in each of eight sums, of 64 beyond.
+struct Squares {
   double total = 0.0;
   float s[8] = {};
   int adds = 0;
-  auto fold = [&]() {
+
+  __device__ __forceinline__ void fold() {
     total += static_cast<double>(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = 0.f;
     adds = 0;
-  };
-  Piece p[kAhead];
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) p[k].load(w, w.begin + k);
-  for (int64_t c = w.begin; c < w.end; c += kAhead) {
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (p[k].n > 0) {
-        p[k].get(w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = fmaf(p[k].v[j], p[k].v[j], s[j]);
-      }
-      p[k].load(w, c + kAhead + k);
-    }
-    if ((adds += kAhead) == kAdds) fold();
   }
-  fold();
-  total = block_sum(total);
+  template <typename T>
+  __device__ __forceinline__ void add(const T* p, int64_t n, bool wide) {
+    int64_t i = 8 * static_cast<int>(threadIdx.x);
+    if (wide) {
+      for (; i + (kAhead - 1) * kChunk + 8 <= n; i += kAhead * kChunk) {
+        Raw8<T> r[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) r[k].load(p + i + k * kChunk);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          float v[8];
+          r[k].get(v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] = fmaf(v[j], v[j], s[j]);
+        }
+        if ((adds += kAhead) > kAdds - kAhead) fold();
+      }
+      for (; i + 8 <= n; i += kChunk) {
+        Raw8<T> r;
+        float v[8];
+        r.load(p + i);
+        r.get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = fmaf(v[j], v[j], s[j]);
+        if (++adds > kAdds - kAhead) fold();
+      }
+    }
+    for (; i < n; i += kChunk) {  // the last few, or rows that allow no vectors
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < n) s[j] = fmaf(load1(p + i + j), load1(p + i + j), s[j]);
+      if (++adds > kAdds - kAhead) fold();
+    }
+  }
+};
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    clip_squares_kernel(const __grid_constant__ ClipList<CAP> l, double* partial, bool add) {
+  griddep_launch_dependents();
+  Squares q;
+  for_stretch<false>(l, [&](int t, int64_t first, int64_t n) {
+    if (l.bf16_in[t])
+      q.add(static_cast<const bf16*>(l.in[t]) + first, n, l.wide[t]);
+    else
+      q.add(static_cast<const float*>(l.in[t]) + first, n, l.wide[t]);
+  });
+  q.fold();
+  const double total = block_sum(q.total);
   if (threadIdx.x == 0) partial[blockIdx.x] = total + (add ? partial[blockIdx.x] : 0.0);
 }
 
@@ -176,32 +148,60 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const double* parti
   if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
+// out = c in, from the end.
+template <typename T>
+__device__ __forceinline__ void scale_down(const T* in, T* out, int64_t n, bool wide, float c) {
+  int64_t i = (n - 1) / kChunk * kChunk + 8 * static_cast<int>(threadIdx.x);
+  auto slow = [&]() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) store1(out + i + j, load1(in + i + j) * c);
+  };
+  if (!wide) {
+    for (; i >= 0; i -= kChunk) slow();
+    return;
+  }
+  if (i + 8 > n) {
+    slow();
+    i -= kChunk;
+  }
+  auto vectors = [&](auto count) {
+    constexpr int kCount = decltype(count)::value;
+    Raw8<T> r[kCount];
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) r[k].load(in + i - k * kChunk);
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) {
+      float v[8];
+      r[k].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= c;
+      store8(out + i - k * kChunk, v);
+    }
+    i -= kCount * kChunk;
+  };
+  while (i >= (kAhead - 1) * kChunk) vectors(std::integral_constant<int, kAhead>());
+  while (i >= 0) vectors(std::integral_constant<int, 1>());
+}
+
 // From the end of each block's stretch: what was read last is still in L2.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBlocks)
     clip_scale_kernel(const __grid_constant__ ClipList<CAP> l, const double* partial, int parts,
                       float max_norm, float* norm) {
-  Walk<CAP> w(l);
-  if (w.begin < w.end) w.find(w.end - 1);
   griddep_wait();
-  Piece p[kAhead];
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) p[k].load(w, w.end - 1 - k);
   const double total = norm_of(partial, parts);
   double coef = static_cast<double>(max_norm) / (total + 1e-6);
   if (coef > 1.0) coef = 1.0;  // (a NaN stays one)
-  const float f = static_cast<float>(coef);
+  const float c = static_cast<float>(coef);
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
-  for (int64_t c = w.end - 1; c >= w.begin; c -= kAhead) {
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (p[k].n > 0 && (f != 1.f || l.in[p[k].t] != l.out[p[k].t])) {
-        p[k].get(w);
-        p[k].put(w, f);
-      }
-      p[k].load(w, c - kAhead - k);
-    }
-  }
+  for_stretch<true>(l, [&](int t, int64_t first, int64_t n) {
+    if (c == 1.f && l.in[t] == l.out[t]) return;
+    if (l.bf16_in[t])
+      scale_down(static_cast<const bf16*>(l.in[t]) + first, static_cast<bf16*>(l.out[t]) + first, n, l.wide[t], c);
+    else
+      scale_down(static_cast<const float*>(l.in[t]) + first, static_cast<float*>(l.out[t]) + first, n, l.wide[t], c);
+  });
 }
 
 template <int CAP>

@@ -58,7 +58,7 @@ struct ClipArgs {
   double* partial;        // context scratch: [clip_partials(num_sms)]
   int num_sms;
 };
-constexpr int clip_partials(int num_sms) { return 2 * num_sms; }
+constexpr int clip_partials(int num_sms) { return 4 * num_sms; }
 cudaError_t launch_clip(const ClipArgs& a, int* launches, cudaStream_t stream);
 
 // ---- products with an epilogue (linear.cu)
