@@ -18,10 +18,6 @@ using bf16 = __nv_bfloat16;
 
 constexpr int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-__device__ __forceinline__ float load_as(const void* p, int f32, int64_t i) {
-  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const bf16*>(p)[i]);
-}
-
 // ------------------------------------------------------------------ joining of splits
 // The epilogue over sums of `splits` partials [splits][I][ld_part], in their order; four columns a
 // thread.
@@ -54,14 +50,14 @@ __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
     for (int j = 0; j < 4; ++j)
       if (j < m && a.bias != nullptr) z[j] += a.bias[c + j];
     auto put = [&](void* dst, int64_t ld) {
-      if (a.vec) {
-        epi_store<true>(dst, a.out_f32, r * ld + c, z);
+      if (a.vec && a.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(dst) + r * ld + c) = make_float4(z[0], z[1], z[2], z[3]);
+      } else if (a.vec) {
+        *reinterpret_cast<uint2*>(static_cast<bf16*>(dst) + r * ld + c) = make_uint2(narrow2(z[0], z[1]), narrow2(z[2], z[3]));
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float one[4] = {z[j]};
-          if (j < m) epi_store<false>(dst, a.out_f32, r * ld + c + j, one);
-        }
+        for (int j = 0; j < 4; ++j)
+          if (j < m) store_as(dst, a.out_f32, r * ld + c + j, z[j]);
       }
     };
     if (a.pre != nullptr) put(a.pre, a.ld_pre);
@@ -209,15 +205,21 @@ struct Launcher {
   }
 
   template <int BN, bool A_MN, bool B_MN>
-  void gemm_sized(GemmArgs& g, bool vec) {
+  void gemm_sized(GemmArgs& g, GemmEpilogue epi) {
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(g.units, c.num_sms));
-    auto run = [&](auto kernel) {
-      error = (*c.opt_in)(kernel, GemmShape<BN>::kSmem);
+    auto run = [&](auto kernel, uint32_t smem) {
+      error = (*c.opt_in)(kernel, smem);
       if (!ok()) return;
-      kernel<<<grid, kGemmThreads, GemmShape<BN>::kSmem, stream>>>(g);
+      kernel<<<grid, kGemmThreads, smem, stream>>>(g);
       launched();
     };
-    vec ? run(linear_gemm_kernel<BN, A_MN, B_MN, true>) : run(linear_gemm_kernel<BN, A_MN, B_MN, false>);
+    if (epi == kEpiElements)
+      run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElements>, GemmShape<BN, kEpiElements>::kSmem);
+    else if (A_MN || !B_MN || epi == kEpiTma)  // (the gradients' products have no residual)
+      run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiTma>, GemmShape<BN, kEpiTma>::kSmem);
+    else
+      run(linear_gemm_kernel<BN, A_MN, B_MN, !A_MN && B_MN ? kEpiResidual : kEpiTma>,
+          GemmShape<BN, !A_MN && B_MN ? kEpiResidual : kEpiTma>::kSmem);
   }
 
   // out = act(A B + bias) + residual, A of parts a[0..na), B of b[0..nb); the epilogue's fields of g
@@ -225,11 +227,11 @@ struct Launcher {
   template <bool A_MN, bool B_MN>
   void gemm(GemmArgs g, const Matrix* a, int na, const Matrix* b, int nb, int64_t I, int J, int64_t Kc) {
     if (!ok()) return;
-    const bool vec_out = (reinterpret_cast<uintptr_t>(g.out) & (g.out_f32 ? 15 : 7)) == 0 && g.ld_out % 4 == 0 &&
-                         (g.pre == nullptr || ((reinterpret_cast<uintptr_t>(g.pre) & (g.out_f32 ? 15 : 7)) == 0 && g.ld_pre % 4 == 0)) &&
-                         J % 4 == 0;
-    const bool vec_res = g.residual == nullptr ||
-                         ((reinterpret_cast<uintptr_t>(g.residual) & (g.res_f32 ? 15 : 7)) == 0 && g.ld_res % 4 == 0);
+    auto tma = [](const void* p, int64_t ld, int f32) {  // rows that TMA takes
+      return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % (f32 ? 4 : 8) == 0;
+    };
+    bool by_tma = tma(g.out, g.ld_out, g.out_f32) && (g.residual == nullptr || tma(g.residual, g.ld_res, g.res_f32)) &&
+                  (g.pre == nullptr || (tma(g.pre, g.ld_pre, g.out_f32) && g.residual == nullptr));
     g.blocks_k = (Kc + 63) / 64;
     g.steps = g.blocks_k * std::max(na, nb);
     const int64_t ld_part = up(J, 4);
@@ -267,10 +269,6 @@ struct Launcher {
     };
     for (int i = 0; i < na; ++i) encode(&g.a[i], a[i], A_MN ? 64 : 128);
     for (int i = 0; i < nb; ++i) encode(&g.b[i], b[i], B_MN ? 64 : BN);
-    if (!maps) {
-      error = cudaErrorInvalidValue;
-      return;
-    }
     g.status = c.status;
     g.timeout_ns = c.timeout_ns;
     g.skip_cta = c.debug_skip_cta;
@@ -290,7 +288,7 @@ struct Launcher {
       j.res_f32 = g.res_f32;
       j.out_f32 = g.out_f32;
       j.act = g.act;
-      j.vec = vec_out;
+      j.vec = J % 4 == 0 && tma(g.out, g.ld_out, g.out_f32) && (g.pre == nullptr || tma(g.pre, g.ld_pre, g.out_f32));
       j.out = g.out;
       j.pre = g.pre;
       g.bias = nullptr;
@@ -302,14 +300,30 @@ struct Launcher {
       g.ld_out = ld_part;
       g.split_stride = j.stride;
     }
-    // (partials' rows are padded to vectors, but a vector may not pass the last column)
-    const bool vec = S > 1 ? J % 4 == 0 : vec_out && vec_res;
+    if (S > 1) by_tma = true;
+    if (by_tma) {
+      auto encode_out = [&](CUtensorMap* m, const void* p, int64_t ld, int f32, int64_t parts) {
+        const uint64_t size = f32 ? 4 : 2;
+        maps = maps && encode_3d(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, J, I, parts,
+                                 ld * size, I * ld * size, f32 ? 32 : 64, 32, 1);
+      };
+      encode_out(&g.out_map, g.out, g.ld_out, g.out_f32, S);
+      if (g.pre != nullptr) encode_out(&g.pre_map, g.pre, g.ld_pre, g.out_f32, 1);
+      if (g.residual != nullptr)
+        maps = maps && encode_2d(&g.res_map, g.res_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                 g.residual, J, I, g.ld_res * (g.res_f32 ? 4 : 2), g.res_f32 ? 32 : 64, 32);
+    }
+    if (!maps) {
+      error = cudaErrorInvalidValue;
+      return;
+    }
+    const GemmEpilogue epi = !by_tma ? kEpiElements : g.residual != nullptr ? kEpiResidual : kEpiTma;
     if (BN == 256)
-      gemm_sized<256, A_MN, B_MN>(g, vec);
+      gemm_sized<256, A_MN, B_MN>(g, epi);
     else if (BN == 128)
-      gemm_sized<128, A_MN, B_MN>(g, vec);
+      gemm_sized<128, A_MN, B_MN>(g, epi);
     else
-      gemm_sized<64, A_MN, B_MN>(g, vec);
+      gemm_sized<64, A_MN, B_MN>(g, epi);
     if (S > 1) join(j);
   }
 

@@ -5,7 +5,9 @@
 // contraction where the tiles alone would leave SMs idle).  One lane fills a ring of stages of 64
 // terms by TMA (128-byte swizzle), one issues tcgen05.mma (M = 128, N = BN, accumulator in TMEM), and
 // eight warps take finished accumulators through the epilogue while the next unit's products run into
-// the other half of TMEM.  Either operand may lie with the contraction contiguous (K-major) or with
+// the other half of TMEM. Outputs whose rows TMA can write leave by it, a warp's 32 rows x 64 columns at
+// a time through shared memory, and residuals arrive the same way, ahead of their products; others go
+// element by element.  Either operand may lie with the contraction contiguous (K-major) or with
 // its own index contiguous (MN-major), so x W, dz W^T and x^T dz read their matrices as they are.
 //
 // An operand may come in two parts, added up in the accumulator: A = A_0 + A_1 doubles the terms.
@@ -23,6 +25,7 @@ namespace dspark {
 
 struct GemmArgs {
   CUtensorMap a[2], b[2];
+  CUtensorMap out_map, pre_map, res_map;  // (outputs by TMA) boxes of 32 rows x 128 bytes
   int a_parts, b_parts;     // 1, or 2 of one of them
   int64_t I;                // rows and columns of the output
   int J;
@@ -43,83 +46,100 @@ struct GemmArgs {
 
 constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
-template <int BN>
+
+// The epilogue: element by element; by TMA; by TMA with a residual that arrives a chunk ahead (in two
+// slots of 8 KB a warp instead of 4 KB, for which the operands' ring gives up half its stages: as good
+// as none, since such outputs are bounded by their bytes).
+enum GemmEpilogue { kEpiElements, kEpiTma, kEpiResidual };
+
+template <int BN, int EPI>
 struct GemmShape {
+  static constexpr int kSlots = EPI == kEpiResidual ? 2 : 1;  // of a warp
+  static constexpr uint32_t kSlot = EPI == kEpiResidual ? 8192 : 4096;
   static constexpr uint32_t kA = 128 * 64 * 2, kB = BN * 64 * 2;
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;  // 192 KB
+  static constexpr uint32_t kEpi = kGemmEpiWarps * kSlots * kSlot;
+  static constexpr int kStages = (226 * 1024 - 1024 - 512 - kEpi) / (kA + kB) < 8
+                                     ? (226 * 1024 - 1024 - 512 - kEpi) / (kA + kB)
+                                     : 8;
   static constexpr uint32_t kOffB = kStages * kA;
   static constexpr uint32_t kOffEpi = kOffB + kStages * kB;
-  static constexpr uint32_t kOffBar = kOffEpi + kGemmEpiWarps * 4096;
-  static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
-  static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+  static constexpr uint32_t kOffBar = kOffEpi + kEpi;
+  static constexpr uint32_t kSmem = kOffBar + 512 + 1024;
+  static_assert(kStages >= 2 && kSmem <= 227 * 1024, "shared memory of a block");
+  static_assert((2 * kStages + 8 + kGemmEpiWarps * kSlots) * 8 <= 512, "barriers");
   static_assert(2 * BN <= 512, "tensor memory columns");
 };
 
-// A warp's 32 x 32 outputs as coalesced pieces: four neighbours of a row a lane (VEC: rows allow
-// 16-byte vectors of fp32 and 8-byte ones of bf16), or one.
-template <bool VEC>
-struct EpiMap {
-  static constexpr int kIters = VEC ? 8 : 32;
-  __device__ static __forceinline__ int row(int i, int lane) { return VEC ? 4 * i + lane / 8 : i; }
-  __device__ static __forceinline__ int col(int lane) { return VEC ? 4 * (lane % 8) : lane; }
-};
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// until this thread's stores have read their shared memory; until they are done
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// The word of element (r, c) in a warp's 32 x 32 buffer: 16-byte units XORed with the row, so that
-// both a lane writing its row and lanes reading along one meet no bank twice.
-__device__ __forceinline__ int epi_word(int r, int c) { return 32 * r + (((c >> 2) ^ (r & 7)) << 2) + (c & 3); }
+__device__ __forceinline__ void st_shared_v4(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_shared(uint32_t p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+  return v;
+}
 
-template <bool VEC>
-__device__ __forceinline__ void epi_store(void* p, int f32, int64_t at, const float (&v)[4]) {
-  if constexpr (VEC) {
-    if (f32)
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
-          make_uint2(narrow2(v[0], v[1]), narrow2(v[2], v[3]));
-  } else {
-    if (f32)
-      static_cast<float*>(p)[at] = v[0];
-    else
-      static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v[0]);
+__device__ __forceinline__ float load_as(const void* p, int f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_as(void* p, int f32, int64_t i, float v) {
+  if (f32)
+    static_cast<float*>(p)[i] = v;
+  else
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// 32 accumulators of this lane's row with the bias of their columns (lane j holds column j's) added,
+// and, in 128 bytes of shared memory of the lane's own at `line` (16-byte units in place u ^ (lane & 7)),
+// the activation: there one copy of the functions' code serves every column.
+__device__ __forceinline__ void epi_bias(float (&v)[32], float bias) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xFFFFFFFFu, bias, j);
+}
+__device__ __forceinline__ void epi_put32(const float (&v)[32], uint32_t line) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    st_shared_v4(line ^ (u << 4), __float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
+                 __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
+}
+__device__ __forceinline__ void epi_act(int act, uint32_t line) {
+#pragma unroll 1
+  for (int u = 0; u < 8; ++u) {
+    const uint4 w = ld_shared_v4(line ^ (u << 4));
+    st_shared_v4(line ^ (u << 4), __float_as_uint(act_value(act, __uint_as_float(w.x))),
+                 __float_as_uint(act_value(act, __uint_as_float(w.y))),
+                 __float_as_uint(act_value(act, __uint_as_float(w.z))),
+                 __float_as_uint(act_value(act, __uint_as_float(w.w))));
+  }
+}
+__device__ __forceinline__ void epi_get32(float (&v)[32], uint32_t line) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint4 w = ld_shared_v4(line ^ (u << 4));
+    v[4 * u] = __uint_as_float(w.x), v[4 * u + 1] = __uint_as_float(w.y);
+    v[4 * u + 2] = __uint_as_float(w.z), v[4 * u + 3] = __uint_as_float(w.w);
   }
 }
 
-// Residual elements as they lie in memory.
-template <bool VEC>
-struct EpiRaw {
-  uint4 v;
-  __device__ __forceinline__ void load(const void* p, int f32, int64_t at) {
-    if constexpr (VEC) {
-      if (f32) {
-        v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
-      } else {
-        const uint2 t = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at);
-        v.x = t.x, v.y = t.y;
-      }
-    } else {
-      v.x = f32 ? static_cast<const uint32_t*>(p)[at] : static_cast<const uint16_t*>(p)[at];
-    }
-  }
-  __device__ __forceinline__ void add(int f32, float (&z)[4]) const {
-    if constexpr (VEC) {
-      if (f32) {
-        z[0] += __uint_as_float(v.x), z[1] += __uint_as_float(v.y);
-        z[2] += __uint_as_float(v.z), z[3] += __uint_as_float(v.w);
-      } else {
-        float a, b, c, d;
-        widen2(v.x, a, b);
-        widen2(v.y, c, d);
-        z[0] += a, z[1] += b, z[2] += c, z[3] += d;
-      }
-    } else {
-      z[0] += f32 ? __uint_as_float(v.x) : __uint_as_float(v.x << 16);
-    }
-  }
-};
-
-template <int BN, bool A_MN, bool B_MN, bool VEC>
+template <int BN, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs g) {
-  using S = GemmShape<BN>;
+  using S = GemmShape<BN, EPI>;
   constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -132,6 +152,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
   uint64_t* drain = acc_full + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(acc_full + 6);
+  uint64_t* res_full = acc_full + 7;       // [warps][kSlots]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -144,6 +165,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
       mbar_init(&acc_empty[s], kGemmEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int s = 0; s < kGemmEpiWarps * S::kSlots; ++s) mbar_init(&res_full[s], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&g.a[0]);
@@ -253,99 +275,217 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
       }
     }
   } else {
-    using Map = EpiMap<VEC>;
-    constexpr int kChunks = BN / 64;
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    float* const buf32 = reinterpret_cast<float*>(smem + S::kOffEpi + (warp - 2) * 4096);
-    const int col_l = Map::col(lane);
-    uint32_t i = 0;
+    // warps of a TMEM quadrant take its rows; of two such warps each takes every other 64 columns
+    const int q = warp & 3, e = warp - 2, group = e >> 2;
+    constexpr int kChunks = BN / 64, kRound = kChunks < 2 ? 2 : kChunks;  // (of 64 columns the second group has none)
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t slots = smem_addr(smem + S::kOffEpi + e * S::kSlots * S::kSlot);
+    const uint32_t own = 128 * lane + ((lane & 7) << 4);  // this lane's line of a 4 KB box
+    const bool has_res = EPI == kEpiTma ? false : EPI == kEpiResidual || g.residual != nullptr;
+    auto place = [&](int64_t u, int64_t& row0, int& col0) {
+      const int64_t t = u % tiles;
+      row0 = (t % g.tiles_i) * 128 + q * 32;
+      col0 = static_cast<int>(t / g.tiles_i) * BN;
+    };
+    uint32_t phases = 0, pending = 0;  // bit a slot: of its barrier; a load is under way
+    // the residual of chunk c of unit u on its way into a slot (fp32: both boxes; bf16: the second)
+    auto load_residual = [&](int64_t u, int c, int slot) {
+      if (EPI != kEpiResidual || u >= g.units) return;
+      int64_t row0;
+      int col0;
+      place(u, row0, col0);
+      const int col = col0 + 64 * c;
+      if (row0 >= g.I || col >= g.J) return;
+      pending |= 1u << slot;
+      if (lane == 0) {
+        uint64_t* const bar = &res_full[e * S::kSlots + slot];
+        uint8_t* const to = smem + S::kOffEpi + (e * S::kSlots + slot) * S::kSlot;
+        const uint64_t pol = l2_policy_evict_first();
+        mbar_arrive_expect_tx(bar, g.res_f32 ? 8192 : 4096);
+        if (g.res_f32) {
+          tma_load_2d(to, &g.res_map, col, static_cast<int>(row0), bar, pol);
+          tma_load_2d(to + 4096, &g.res_map, col + 32, static_cast<int>(row0), bar, pol);
+        } else {
+          tma_load_2d(to + 4096, &g.res_map, col, static_cast<int>(row0), bar, pol);
+        }
+      }
+    };
+    // (position n + kSlots of the warp's chunks, from chunk c of unit u)
+    auto load_later = [&](int64_t u, int c, int slot) {
+      int k = c + 2 * S::kSlots;
+      for (; k >= kRound; k -= kRound) u += gridDim.x;
+      load_residual(u, k, slot);
+    };
+    bool ok = true;
+    uint32_t i = 0, n = 0;
+    if (group < kChunks) {
+      int64_t u = blockIdx.x;
+      int c = group;
+      for (int s = 0; s < S::kSlots; ++s) {
+        for (; c >= kRound; c -= kRound) u += gridDim.x;
+        load_residual(u, c, s);
+        c += 2;
+      }
+    }
     for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x, ++i) {
-      const int64_t t = u % tiles, sp = u / tiles;
-      const int64_t row0 = (t % g.tiles_i) * 128 + q * 32;
-      const int col0 = static_cast<int>(t / g.tiles_i) * BN + half * (BN / 2);
-      const int rows = static_cast<int>(min(static_cast<int64_t>(32), g.I - row0));  // (may be <= 0)
-      const int64_t out0 = sp * g.split_stride;
-      EpiRaw<VEC> res[Map::kIters];
-      auto load_residual = [&](int c) {
-        const int col = col0 + 32 * c + col_l;
-#pragma unroll
-        for (int k = 0; k < Map::kIters; ++k) {
-          const int r = Map::row(k, lane);
-          if (r < rows && col < g.J) res[k].load(g.residual, g.res_f32, (row0 + r) * g.ld_res + col);
-        }
-      };
-      if (g.residual != nullptr) load_residual(0);
+      int64_t row0;
+      int col0;
+      place(u, row0, col0);
+      const int sp = static_cast<int>(u / tiles);
       const uint32_t b = i & 1;
-      const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i >> 1) & 1, g.timeout_ns, abort_flag));
-      if (!ok) {
-        if (lane == 0) {
-          *abort_flag = 1;
-          record_error(g.status, kStatusTimeout);
-        }
-        break;
-      }
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i >> 1) & 1, g.timeout_ns, abort_flag));
+      if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        uint32_t v[32];
-        tmem_ld_x32(tmem + b * BN + half * (BN / 2) + 32 * c + (static_cast<uint32_t>(q * 32) << 16), v);
-        tmem_wait_ld();
-        if (c == kChunks - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[b]);
-        }
-        const int cc = col0 + 32 * c;
-        if (cc >= g.J || rows <= 0) continue;
-        if (g.bias != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (cc + j < g.J) v[j] = __float_as_uint(__uint_as_float(v[j]) + __ldg(g.bias + cc + j));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(buf32 + epi_word(lane, 4 * j)) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        __syncwarp();
-        const int col = cc + col_l;
-        auto piece = [&](int k, float (&z)[4]) {
-          const float* const p = buf32 + epi_word(Map::row(k, lane), col_l);
-          if constexpr (VEC) {
-            const float4 f = *reinterpret_cast<const float4*>(p);
-            z[0] = f.x, z[1] = f.y, z[2] = f.z, z[3] = f.w;
-          } else {
-            z[0] = *p;
-          }
-        };
-        if (g.pre != nullptr) {
-#pragma unroll 4
-          for (int k = 0; k < Map::kIters; ++k) {
-            const int r = Map::row(k, lane);
-            float z[4];
-            piece(k, z);
-            if (r < rows && col < g.J) epi_store<VEC>(g.pre, g.out_f32, (row0 + r) * g.ld_pre + col, z);
-          }
-        }
-        if (g.act != DSPARK_ACT_NONE) {
-          // in the buffer, each lane its row: one copy of the functions' code
-          __syncwarp();
 #pragma unroll 1
-          for (int j = 0; j < 32; ++j) {
-            float* const p = buf32 + 32 * lane + (j ^ lane);
-            *p = act_value(g.act, *p);
+      for (int c = group; c < kChunks; c += 2, ++n) {
+        const int col = col0 + 64 * c, slot = n % S::kSlots;
+        if (row0 >= g.I || col >= g.J) {
+          load_later(u, c, slot);
+          continue;
+        }
+        const uint32_t box = slots + slot * S::kSlot, line = box + own;
+        if constexpr (EPI != kEpiElements) {
+          if (pending >> slot & 1) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&res_full[e * S::kSlots + slot], phases >> slot & 1, g.timeout_ns, abort_flag));
+            if (!ok) break;
+            phases ^= 1u << slot;
+            pending &= ~(1u << slot);
+          } else {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
           }
-          __syncwarp();
-        }
+          // columns [col + shift, ...) of the slot's box at `from` on their way out
+          auto store = [&](const CUtensorMap* map, uint32_t from, int shift) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (col + shift < g.J) tma_store_3d(map, from, col + shift, static_cast<int>(row0), sp);
+              bulk_commit();
+            }
+          };
+          auto pass = [&](bool last, const CUtensorMap* map) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float v[32], r[32];
+              tmem_ld_x32(lane_base + b * BN + 64 * c + 32 * h, reinterpret_cast<uint32_t*>(v));
+              const int cc = col + 32 * h;
+              const float bias = g.bias != nullptr && cc + lane < g.J ? __ldg(g.bias + cc + lane) : 0.f;
+              // an fp32 half is a box: its own beside a residual, else the slot's one, again
+              const uint32_t half_box = EPI == kEpiResidual ? box + (h << 12) : box, half = half_box + own;
+              if constexpr (EPI == kEpiResidual) {
+                if (g.res_f32) {
+                  epi_get32(r, half);
+                } else {
 #pragma unroll
-        for (int k = 0; k < Map::kIters; ++k) {
-          const int r = Map::row(k, lane);
-          float z[4];
-          piece(k, z);
-          if (g.residual != nullptr) res[k].add(g.res_f32, z);
-          if (r < rows && col < g.J) epi_store<VEC>(g.out, g.out_f32, out0 + (row0 + r) * g.ld_out + col, z);
+                  for (int u8 = 0; u8 < 4; ++u8) {
+                    const uint4 w = ld_shared_v4((line + 4096) ^ ((4 * h + u8) << 4));
+                    widen2(w.x, r[8 * u8], r[8 * u8 + 1]);
+                    widen2(w.y, r[8 * u8 + 2], r[8 * u8 + 3]);
+                    widen2(w.z, r[8 * u8 + 4], r[8 * u8 + 5]);
+                    widen2(w.w, r[8 * u8 + 6], r[8 * u8 + 7]);
+                  }
+                }
+              }
+              tmem_wait_ld();
+              if (g.bias != nullptr) epi_bias(v, bias);
+              if (last && g.act != DSPARK_ACT_NONE) {
+                // (the slot's one box may hold the first half's bf16 outputs: they are kept meanwhile)
+                uint4 keep[EPI == kEpiResidual ? 1 : 4];
+                if constexpr (EPI != kEpiResidual) {
+#pragma unroll
+                  for (int u8 = 0; u8 < 4; ++u8) keep[u8] = ld_shared_v4(line ^ (u8 << 4));
+                }
+                epi_put32(v, half);
+                epi_act(g.act, half);
+                epi_get32(v, half);
+                if constexpr (EPI != kEpiResidual) {
+#pragma unroll
+                  for (int u8 = 0; u8 < 4; ++u8) st_shared_v4(line ^ (u8 << 4), keep[u8].x, keep[u8].y, keep[u8].z, keep[u8].w);
+                }
+              }
+              if constexpr (EPI == kEpiResidual) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += r[j];
+              }
+              if (g.out_f32) {
+                epi_put32(v, half);
+                store(map, half_box, 32 * h);
+                if (EPI != kEpiResidual && h == 0) {
+                  if (lane == 0) bulk_wait_read();
+                  __syncwarp();
+                }
+              } else {
+#pragma unroll
+                for (int u8 = 0; u8 < 4; ++u8)
+                  st_shared_v4(line ^ ((4 * h + u8) << 4), narrow2(v[8 * u8], v[8 * u8 + 1]),
+                               narrow2(v[8 * u8 + 2], v[8 * u8 + 3]), narrow2(v[8 * u8 + 4], v[8 * u8 + 5]),
+                               narrow2(v[8 * u8 + 6], v[8 * u8 + 7]));
+                if (h == 1) store(map, box, 0);
+              }
+            }
+          };
+          if (EPI == kEpiTma && g.pre != nullptr) {
+            pass(false, &g.pre_map);
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+          }
+          pass(true, &g.out_map);
+          if constexpr (EPI == kEpiResidual) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+            load_later(u, c, slot);
+          }
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int cc = col + 32 * h;
+            if (cc >= g.J) break;
+            float v[32];
+            tmem_ld_x32(lane_base + b * BN + 64 * c + 32 * h, reinterpret_cast<uint32_t*>(v));
+            const float bias = g.bias != nullptr && cc + lane < g.J ? __ldg(g.bias + cc + lane) : 0.f;
+            const int rows = static_cast<int>(min(static_cast<int64_t>(32), g.I - row0));
+            const bool in = cc + lane < g.J;
+            float r[32];  // of column `lane`, a row each
+            if (has_res) {
+              const int64_t at = row0 * g.ld_res + cc + lane;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) r[k] = in && k < rows ? load_as(g.residual, g.res_f32, at + k * g.ld_res) : 0.f;
+            }
+            tmem_wait_ld();
+            if (g.bias != nullptr) epi_bias(v, bias);
+            __syncwarp();
+            epi_put32(v, line);
+            // now by columns: element (k, lane)
+            auto put = [&](void* to, int64_t ld, bool add) {
+              __syncwarp();
+              const int64_t at = sp * g.split_stride + row0 * ld + cc + lane;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = ld_shared(box + 128 * k + ((((lane >> 2) ^ (k & 7)) << 4) | ((lane & 3) << 2)));
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (in && k < rows) store_as(to, g.out_f32, at + k * ld, add ? v[k] + r[k] : v[k]);
+              __syncwarp();
+            };
+            if (g.pre != nullptr) put(g.pre, g.ld_pre, false);
+            if (g.act != DSPARK_ACT_NONE) epi_act(g.act, line);
+            put(g.out, g.ld_out, has_res);
+          }
         }
-        if (c + 1 < kChunks && g.residual != nullptr) load_residual(c + 1);
       }
+      if (!ok) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      record_error(g.status, kStatusTimeout);
+    }
+    if constexpr (EPI != kEpiElements) {
+      // copies under way end before the block does
+      for (int s = 0; s < S::kSlots; ++s)
+        if (pending >> s & 1) mbar_wait(&res_full[e * S::kSlots + s], phases >> s & 1, g.timeout_ns, nullptr);
+      if (lane == 0) bulk_wait();
     }
   }
 
