@@ -630,7 +630,7 @@ typedef enum dspark_act {
  *   pre [M, N] of type y_dtype, rows ld_pre apart: x W + bias, for the gradient (NULL: not
  *     written)
  * Any M >= 0 (< 2^31), 1 <= K, N <= 2^22; pointers aligned to their element size.  Equal inputs
- * at equal addresses modulo 16 give equal bits.
+ * give equal bits.
  * workspace: device memory of the caller, 256-byte aligned, of *workspace_bytes bytes (it must
  * stay untouched until the call's work has run).  Where that is too little, *workspace_bytes is
  * set to what the same call needs, nothing is enqueued and DSPARK_ERR_CAPACITY is returned; 0

@@ -548,13 +548,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumArgs a, int 
 
 template <typename Tin, typename Tout, bool VEC>
 cudaError_t sums(const SumArgs& s, int blocks, int slices, int* launches, cudaStream_t stream) {
-  cudaError_t e = launch_dependent(embed_sum_kernel<Tin, Tout, VEC>, dim3(blocks, slices), kSumThreads, stream, s);
+  cudaError_t e = launch_dependent(embed_sum_kernel<Tin, Tout, VEC>, dim3(blocks, slices), kSumThreads, 0, stream, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (blocks == 1) return e;
   const int groups = kSumThreads / s.lanes;
   e = launch_dependent(embed_join_kernel<Tout, VEC>, dim3((blocks + groups - 1) / groups, slices),
-                       kSumThreads, stream, s, blocks);
+                       kSumThreads, 0, stream, s, blocks);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
@@ -618,7 +618,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
     // (64 KB a block: the SMs that sort leave theirs to the others)
     const int64_t chunks = static_cast<int64_t>(a.V) * a.D * t.size / 65536;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(chunks, 1), 8192));
-    e = launch_dependent(embed_zeros_kernel, dim3(blocks), kSortThreads, stream, t);
+    e = launch_dependent(embed_zeros_kernel, dim3(blocks), kSortThreads, 0, stream, t);
     if (e != cudaSuccess) return e;
     *c.launches += 1;
   }

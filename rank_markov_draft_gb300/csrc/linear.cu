@@ -7,6 +7,7 @@
 
 #include <algorithm>
 
+#include "dependent.h"
 #include "linear_gemm.cuh"
 #include "step.h"
 #include "tensor_map.h"
@@ -33,6 +34,8 @@ struct JoinArgs {
 };
 
 __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int per_row = (a.J + 3) / 4;
   const int64_t n = a.I * per_row;
   for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < n; e += gridDim.x * 256ll) {
@@ -86,6 +89,8 @@ struct SplitArgs {
 };
 
 __global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float warps[8][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x * 128 + lane;
@@ -130,6 +135,8 @@ __global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
 }
 
 __global__ void __launch_bounds__(256) linear_sums_kernel(const float* part, int parts, int cols, float* out) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= cols) return;
   float s = 0.f;
@@ -167,10 +174,23 @@ struct Launcher {
   cudaStream_t stream;
   cudaError_t error = cudaSuccess;
 
+  bool first = true;
+
   bool ok() const { return error == cudaSuccess; }
-  void launched() {
-    *c.launches += 1;
-    error = cudaGetLastError();
+
+  // The call's first kernel, or one that starts beside the end of the one before it (each waits for
+  // that one's end, and so for all before).
+  template <typename... Params, typename... Args>
+  void launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, const Args&... args) {
+    if (!ok()) return;
+    if (first) {
+      kernel<<<grid, threads, smem, stream>>>(args...);
+      error = cudaGetLastError();
+    } else {
+      error = launch_dependent(kernel, grid, threads, smem, stream, args...);
+    }
+    first = false;
+    if (ok()) *c.launches += 1;
   }
 
   void split(SplitArgs a) {
@@ -183,8 +203,7 @@ struct Launcher {
     per = std::min(per, up(a.rows, 8));
     a.rows_per_block = static_cast<int>(per);
     const int64_t blocks = (a.rows + per - 1) / per;
-    linear_split_kernel<<<dim3(cols, static_cast<unsigned>(blocks)), 256, 0, stream>>>(a);
-    launched();
+    launch(linear_split_kernel, dim3(cols, static_cast<unsigned>(blocks)), 256, 0, a);
     sum_blocks = static_cast<int>(blocks);
   }
   int sum_blocks = 0;  // of the last split()
@@ -209,9 +228,7 @@ struct Launcher {
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(g.units, c.num_sms));
     auto run = [&](auto kernel, uint32_t smem) {
       error = (*c.opt_in)(kernel, smem);
-      if (!ok()) return;
-      kernel<<<grid, kGemmThreads, smem, stream>>>(g);
-      launched();
+      launch(kernel, dim3(grid), kGemmThreads, smem, g);
     };
     if (epi == kEpiElements)
       run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElements>, GemmShape<BN, kEpiElements>::kSmem);
@@ -236,23 +253,31 @@ struct Launcher {
     g.steps = g.blocks_k * std::max(na, nb);
     const int64_t ld_part = up(J, 4);
     // The tile and the number of splits that end soonest by this reckoning (us): a stage's four
-    // products take 0.27 whatever the tile's width, a tile's start and end 1.5 of which the next
-    // tile's products hide 1, the join of splits its launch and its bytes at 4 TB/s.
+    // products take 0.3 at least and as long as its operands need from L2 (0.52 at a width of 256), a
+    // tile's start 0.5, the last one's outputs 3 by TMA and 10 by elements at a width of 256, the join
+    // of splits its launch and its bytes at 4 TB/s.
+    // The splits are chosen as if by TMA, so that equal inputs give equal bits wherever they lie.
     int BN = 256;
     int64_t S = 1;
     double best = 1e30;
-    for (int bn : {256, 128, 64}) {
-      const int64_t tiles = (I + 127) / 128 * ((J + bn - 1) / bn);
-      if (bn != 64 && J <= bn / 2) continue;
-      for (int64_t s = 1; s <= std::min<int64_t>(g.steps, 64); ++s) {
-        if (s > 1 && s * I * ld_part * 4 > kStepScratchBytes) break;
-        const int64_t per = (g.steps + s - 1) / s;
-        if ((g.steps + per - 1) / per != s) continue;
+    auto consider = [&](int64_t s, double outputs) {
+      const int64_t per = (g.steps + s - 1) / s;
+      if ((g.steps + per - 1) / per != s) return;
+      for (int bn : {256, 128, 64}) {
+        if (bn != 64 && J <= bn / 2) continue;
+        const int64_t tiles = (I + 127) / 128 * ((J + bn - 1) / bn);
         const int64_t waves = (tiles * s + c.num_sms - 1) / c.num_sms;
-        const double t = static_cast<double>(waves) * (0.27 * static_cast<double>(per) + 0.5) + 1.0 +
+        const double stage = std::max(0.3, 0.18 + 0.34 * bn / 256);
+        const double t = static_cast<double>(waves) * (stage * static_cast<double>(per) + 0.5) + outputs * bn / 256 +
                          (s > 1 ? 3.0 + static_cast<double>(2 * s * I * ld_part * 4) / 4e6 : 0.0);
         if (t < best) best = t, BN = bn, S = s;
       }
+    };
+    for (int64_t s = 1; s <= std::min<int64_t>(g.steps, 64) && (s == 1 || s * I * ld_part * 4 <= kStepScratchBytes); ++s)
+      consider(s, 3.0);
+    if (S == 1 && !by_tma) {
+      best = 1e30;
+      consider(1, 10.0);
     }
     g.I = I;
     g.J = J;
@@ -331,8 +356,7 @@ struct Launcher {
     if (!ok()) return;
     const int64_t n = j.I * ((j.J + 3) / 4);
     const int64_t blocks = std::min<int64_t>((n + 255) / 256, 8 * c.num_sms);
-    linear_join_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(j);
-    launched();
+    launch(linear_join_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, j);
   }
 };
 
@@ -432,10 +456,8 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, v
     }
     s.sums = a.dbias != nullptr ? c.scratch : nullptr;
     l.split(s);
-    if (a.dbias != nullptr && l.ok()) {
-      linear_sums_kernel<<<(a.N + 255) / 256, 256, 0, stream>>>(c.scratch, l.sum_blocks, a.N, a.dbias);
-      l.launched();
-    }
+    if (a.dbias != nullptr)
+      l.launch(linear_sums_kernel, dim3((a.N + 255) / 256), 256, 0, c.scratch, l.sum_blocks, a.N, a.dbias);
   }
   if (a.dx != nullptr) {
     GemmArgs g{};

@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
   uint64_t* res_full = acc_full + 7;       // [warps][kSlots]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // what the call's kernels before this one made; and the scratch is read to its end
 
   // unit u: tile (u % tiles_i, u / tiles_i % tiles_j), part u / (tiles_i tiles_j) of its stages, so
   // that blocks working at one time share their B tiles in L2
