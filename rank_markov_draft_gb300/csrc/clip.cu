@@ -233,7 +233,7 @@ cudaError_t clip(const ClipArgs& a, int* launches, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.out == nullptr) {
-    e = launch_dependent(clip_norm_kernel, dim3(1), kThreads, 0, stream, a.partial, parts, a.norm);
+    e = launch_kernel({dim3(1), kThreads}, stream, clip_norm_kernel, a.partial, parts, a.norm);
     if (e == cudaSuccess) *launches += 1;
     return e;
   }
@@ -241,8 +241,8 @@ cudaError_t clip(const ClipArgs& a, int* launches, cudaStream_t stream) {
   do {
     const int n = std::min(CAP, a.count - t0);
     if (a.count > CAP) fill(l, a, t0, n);
-    e = launch_dependent(clip_scale_kernel<CAP>, dim3(parts), kThreads, 0, stream, l, a.partial, parts,
-                         a.max_norm, t0 == 0 ? a.norm : nullptr);
+    e = launch_kernel({dim3(parts), kThreads}, stream, clip_scale_kernel<CAP>, l, a.partial, parts, a.max_norm,
+                      t0 == 0 ? a.norm : nullptr);
     if (e != cudaSuccess) return e;
     *launches += 1;
     t0 += n;

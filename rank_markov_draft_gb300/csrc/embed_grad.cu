@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "async_copy.cuh"
+#include "cta_pair.cuh"
 #include "dependent.h"
 #include "dspark.h"
 #include "sm103.cuh"
@@ -43,10 +44,6 @@ struct SortArgs {
   int64_t ld_grad;    // elements
   int D, size;        // of a row, bytes of an element
 };
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // Rows [0, V) of the gradient set to zero by `blocks` blocks, from the last: the first rows, which
 // common tokens have, are stored last and still in L2 when their sums follow.
@@ -548,13 +545,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumArgs a, int 
 
 template <typename Tin, typename Tout, bool VEC>
 cudaError_t sums(const SumArgs& s, int blocks, int slices, int* launches, cudaStream_t stream) {
-  cudaError_t e = launch_dependent(embed_sum_kernel<Tin, Tout, VEC>, dim3(blocks, slices), kSumThreads, 0, stream, s);
+  cudaError_t e = launch_kernel({dim3(blocks, slices), kSumThreads}, stream, embed_sum_kernel<Tin, Tout, VEC>, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (blocks == 1) return e;
   const int groups = kSumThreads / s.lanes;
-  e = launch_dependent(embed_join_kernel<Tout, VEC>, dim3((blocks + groups - 1) / groups, slices),
-                       kSumThreads, 0, stream, s, blocks);
+  e = launch_kernel({dim3((blocks + groups - 1) / groups, slices), kSumThreads}, stream,
+                    embed_join_kernel<Tout, VEC>, s, blocks);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
@@ -600,25 +597,14 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
     e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = t.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, t);
+  e = launch_kernel({dim3(grid), kSortThreads, static_cast<size_t>(smem), t.cluster, false}, stream, embed_sort_kernel, t);
   if (e != cudaSuccess) return e;
   *c.launches += 1;
   if (!a.accumulate && t.cluster > 4) {
     // (64 KB a block: the SMs that sort leave theirs to the others)
     const int64_t chunks = static_cast<int64_t>(a.V) * a.D * t.size / 65536;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(chunks, 1), 8192));
-    e = launch_dependent(embed_zeros_kernel, dim3(blocks), kSortThreads, 0, stream, t);
+    e = launch_kernel({dim3(blocks), kSortThreads}, stream, embed_zeros_kernel, t);
     if (e != cudaSuccess) return e;
     *c.launches += 1;
   }

@@ -181,15 +181,11 @@ struct Launcher {
   // The call's first kernel, or one that starts beside the end of the one before it (each waits for
   // that one's end, and so for all before).
   template <typename... Params, typename... Args>
-  void launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, const Args&... args) {
+  void launch(LaunchShape shape, void (*kernel)(Params...), const Args&... args) {
     if (!ok()) return;
-    if (first) {
-      kernel<<<grid, threads, smem, stream>>>(args...);
-      error = cudaGetLastError();
-    } else {
-      error = launch_dependent(kernel, grid, threads, smem, stream, args...);
-    }
+    shape.dependent = !first;
     first = false;
+    error = launch_kernel(shape, stream, kernel, args...);
     if (ok()) *c.launches += 1;
   }
 
@@ -203,7 +199,7 @@ struct Launcher {
     per = std::min(per, up(a.rows, 8));
     a.rows_per_block = static_cast<int>(per);
     const int64_t blocks = (a.rows + per - 1) / per;
-    launch(linear_split_kernel, dim3(cols, static_cast<unsigned>(blocks)), 256, 0, a);
+    launch({dim3(cols, static_cast<unsigned>(blocks)), 256}, linear_split_kernel, a);
     sum_blocks = static_cast<int>(blocks);
   }
   int sum_blocks = 0;  // of the last split()
@@ -224,12 +220,15 @@ struct Launcher {
   }
 
   template <int BN, bool A_MN, bool B_MN>
-  void gemm_sized(GemmArgs& g, GemmEpilogue epi) {
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(g.units, c.num_sms));
-    auto run = [&](auto kernel, uint32_t smem) {
+  void gemm_sized(GemmArgs& g, GemmEpilogue epi, bool pair) {
+    auto run = [&](auto kernel, uint32_t smem, int blocks = 1) {
+      const int64_t most = c.num_sms / blocks;
       error = (*c.opt_in)(kernel, smem);
-      launch(kernel, dim3(grid), kGemmThreads, smem, g);
+      launch({dim3(static_cast<unsigned>(std::min(g.units, most) * blocks)), kGemmThreads, smem, blocks}, kernel, g);
     };
+    if constexpr (BN == 256) {
+      if (pair) return run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiTma, true>, GemmShape<BN, kEpiTma, true>::kSmem, 2);
+    }
     if (epi == kEpiElements)
       run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElements>, GemmShape<BN, kEpiElements>::kSmem);
     else if (A_MN || !B_MN || epi == kEpiTma)  // (the gradients' products have no residual)
@@ -239,53 +238,76 @@ struct Launcher {
           GemmShape<BN, !A_MN && B_MN ? kEpiResidual : kEpiTma>::kSmem);
   }
 
+  // A product as it will be launched.
+  struct Plan {
+    GemmArgs g{};
+    JoinArgs j{};  // of splits
+    int BN = 256;
+    int64_t S = 1;
+    bool pair = false;
+    GemmEpilogue epi = kEpiTma;
+  };
+
+  static bool tma(const void* p, int64_t ld, int f32) {  // rows that TMA takes
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % (f32 ? 4 : 8) == 0;
+  }
+
   // out = act(A B + bias) + residual, A of parts a[0..na), B of b[0..nb); the epilogue's fields of g
-  // are set.
+  // are set. pair_splits: two blocks a tile, this many splits; 0: as pays.
   template <bool A_MN, bool B_MN>
-  void gemm(GemmArgs g, const Matrix* a, int na, const Matrix* b, int nb, int64_t I, int J, int64_t Kc) {
-    if (!ok()) return;
-    auto tma = [](const void* p, int64_t ld, int f32) {  // rows that TMA takes
-      return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % (f32 ? 4 : 8) == 0;
-    };
+  Plan plan(GemmArgs g, const Matrix* a, int na, const Matrix* b, int nb, int64_t I, int J, int64_t Kc,
+            int64_t pair_splits = 0) {
+    Plan p;
     bool by_tma = tma(g.out, g.ld_out, g.out_f32) && (g.residual == nullptr || tma(g.residual, g.ld_res, g.res_f32)) &&
                   (g.pre == nullptr || (tma(g.pre, g.ld_pre, g.out_f32) && g.residual == nullptr));
     g.blocks_k = (Kc + 63) / 64;
     g.steps = g.blocks_k * std::max(na, nb);
     const int64_t ld_part = up(J, 4);
     // The tile and the number of splits that end soonest by this reckoning (us): a stage's four
-    // products take 0.3 at least and as long as its operands need from L2 (0.52 at a width of 256), a
-    // tile's start 0.5, the last one's outputs 3 by TMA and 10 by elements at a width of 256, the join
-    // of splits its launch and its bytes at 4 TB/s.
+    // products take 0.3 at least and as long as its operands need from L2 (0.52 at a width of 256, 0.36
+    // where two blocks share a tile), a tile's start 0.5, the last one's outputs 3 by TMA and 10 by
+    // elements at a width of 256, the join of splits its launch and its bytes at 4 TB/s.
     // The splits are chosen as if by TMA, so that equal inputs give equal bits wherever they lie.
-    int BN = 256;
-    int64_t S = 1;
     double best = 1e30;
-    auto consider = [&](int64_t s, double outputs) {
+    auto consider = [&](int64_t s, double outputs, bool pairs_too) {
       const int64_t per = (g.steps + s - 1) / s;
       if ((g.steps + per - 1) / per != s) return;
+      const double join = s > 1 ? 3.0 + static_cast<double>(2 * s * I * ld_part * 4) / 4e6 : 0.0;
       for (int bn : {256, 128, 64}) {
         if (bn != 64 && J <= bn / 2) continue;
         const int64_t tiles = (I + 127) / 128 * ((J + bn - 1) / bn);
         const int64_t waves = (tiles * s + c.num_sms - 1) / c.num_sms;
         const double stage = std::max(0.3, 0.18 + 0.34 * bn / 256);
-        const double t = static_cast<double>(waves) * (stage * static_cast<double>(per) + 0.5) + outputs * bn / 256 +
-                         (s > 1 ? 3.0 + static_cast<double>(2 * s * I * ld_part * 4) / 4e6 : 0.0);
-        if (t < best) best = t, BN = bn, S = s;
+        const double t = static_cast<double>(waves) * (stage * static_cast<double>(per) + 0.5) + outputs * bn / 256 + join;
+        if (t < best) best = t, p.BN = bn, p.S = s, p.pair = false;
+      }
+      if (pairs_too && I > 128 && J > 128 && g.residual == nullptr) {
+        const int64_t tiles = (I + 255) / 256 * ((J + 255) / 256), pairs = c.num_sms / 2;
+        const double t = static_cast<double>((tiles * s + pairs - 1) / pairs) * (0.36 * static_cast<double>(per) + 0.5) +
+                         outputs + 1.0 + join;
+        if (t < best) best = t, p.BN = 256, p.S = s, p.pair = true;
       }
     };
-    for (int64_t s = 1; s <= std::min<int64_t>(g.steps, 64) && (s == 1 || s * I * ld_part * 4 <= kStepScratchBytes); ++s)
-      consider(s, 3.0);
-    if (S == 1 && !by_tma) {
-      best = 1e30;
-      consider(1, 10.0);
+    if (pair_splits > 0) {
+      const int64_t per = (g.steps + pair_splits - 1) / pair_splits;
+      p.S = (g.steps + per - 1) / per;
+      p.pair = true;
+    } else {
+      for (int64_t s = 1; s <= std::min<int64_t>(g.steps, 64) && (s == 1 || s * I * ld_part * 4 <= kStepScratchBytes); ++s)
+        consider(s, 3.0, true);
+      if (p.S == 1 && !by_tma) {
+        best = 1e30;
+        consider(1, 10.0, false);
+      }
     }
     g.I = I;
     g.J = J;
-    g.tiles_i = (I + 127) / 128;
-    g.tiles_j = (J + BN - 1) / BN;
-    g.splits = static_cast<int>(S);
-    g.per_split = (g.steps + S - 1) / S;
-    g.units = g.tiles_i * g.tiles_j * S;
+    g.tiles_i = p.pair ? (I + 255) / 256 : (I + 127) / 128;
+    g.tiles_j = (J + p.BN - 1) / p.BN;
+    g.splits = static_cast<int>(p.S);
+    g.streams = 1;
+    g.per_split = (g.steps + p.S - 1) / p.S;
+    g.units = g.tiles_i * g.tiles_j * p.S;
     g.a_parts = na;
     g.b_parts = nb;
     bool maps = true;
@@ -293,18 +315,18 @@ struct Launcher {
       maps = maps && encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x.p, x.cols, x.rows, x.ld * 2, 64, height);
     };
     for (int i = 0; i < na; ++i) encode(&g.a[i], a[i], A_MN ? 64 : 128);
-    for (int i = 0; i < nb; ++i) encode(&g.b[i], b[i], B_MN ? 64 : BN);
+    for (int i = 0; i < nb; ++i) encode(&g.b[i], b[i], B_MN ? 64 : p.pair ? p.BN / 2 : p.BN);
     g.status = c.status;
     g.timeout_ns = c.timeout_ns;
     g.skip_cta = c.debug_skip_cta;
-    JoinArgs j{};
-    if (S > 1) {  // sums of parts first, the epilogue where they are joined
+    if (p.S > 1) {  // sums of parts first, the epilogue where they are joined
+      JoinArgs& j = p.j;
       j.part = c.scratch;
       j.I = I;
       j.ld_part = ld_part;
       j.stride = I * ld_part;
       j.J = J;
-      j.splits = static_cast<int>(S);
+      j.splits = static_cast<int>(p.S);
       j.bias = g.bias;
       j.residual = g.residual;
       j.ld_res = g.ld_res;
@@ -324,39 +346,73 @@ struct Launcher {
       g.out_f32 = 1;
       g.ld_out = ld_part;
       g.split_stride = j.stride;
+      by_tma = true;
     }
-    if (S > 1) by_tma = true;
     if (by_tma) {
-      auto encode_out = [&](CUtensorMap* m, const void* p, int64_t ld, int f32, int64_t parts) {
+      auto encode_out = [&](CUtensorMap* m, const void* to, int64_t ld, int f32, int64_t parts) {
         const uint64_t size = f32 ? 4 : 2;
-        maps = maps && encode_3d(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, J, I, parts,
+        maps = maps && encode_3d(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, to, J, I, parts,
                                  ld * size, I * ld * size, f32 ? 32 : 64, 32, 1);
       };
-      encode_out(&g.out_map, g.out, g.ld_out, g.out_f32, S);
+      encode_out(&g.out_map, g.out, g.ld_out, g.out_f32, p.S);
       if (g.pre != nullptr) encode_out(&g.pre_map, g.pre, g.ld_pre, g.out_f32, 1);
       if (g.residual != nullptr)
         maps = maps && encode_2d(&g.res_map, g.res_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                                  g.residual, J, I, g.ld_res * (g.res_f32 ? 4 : 2), g.res_f32 ? 32 : 64, 32);
     }
-    if (!maps) {
-      error = cudaErrorInvalidValue;
-      return;
-    }
-    const GemmEpilogue epi = !by_tma ? kEpiElements : g.residual != nullptr ? kEpiResidual : kEpiTma;
-    if (BN == 256)
-      gemm_sized<256, A_MN, B_MN>(g, epi);
-    else if (BN == 128)
-      gemm_sized<128, A_MN, B_MN>(g, epi);
+    if (!maps && ok()) error = cudaErrorInvalidValue;
+    p.epi = !by_tma ? kEpiElements : g.residual != nullptr ? kEpiResidual : kEpiTma;
+    p.g = g;
+    return p;
+  }
+
+  template <bool A_MN, bool B_MN>
+  void run(Plan p) {
+    if (!ok()) return;
+    if (p.BN == 256)
+      gemm_sized<256, A_MN, B_MN>(p.g, p.epi, p.pair);
+    else if (p.BN == 128)
+      gemm_sized<128, A_MN, B_MN>(p.g, p.epi, false);
     else
-      gemm_sized<64, A_MN, B_MN>(g, epi);
-    if (S > 1) join(j);
+      gemm_sized<64, A_MN, B_MN>(p.g, p.epi, false);
+    if (p.S > 1) join(p.j);
+  }
+
+  // Both products of a gradient in one launch, where dz passes what L2 keeps between two launches
+  // (64 MB of its 129, the other streams taking their share) and dz W^T is of so few tiles that splits
+  // of it keep half the blocks busy. Returns whether it did.
+  bool both(const GemmArgs& gx, const GemmArgs& gw, const Matrix* dz, int parts, const Matrix& W, const Matrix& x) {
+    const int64_t M = x.rows, K = x.cols, N = dz[0].cols, pairs = c.num_sms / 2;
+    const int64_t tiles_x = (M + 255) / 256 * ((K + 255) / 256), units_w = (K + 255) / 256 * ((N + 255) / 256);
+    if (M * N * 2 * parts < (64ll << 20) || tiles_x > pairs / 2 || !tma(gw.out, gw.ld_out, gw.out_f32)) return false;
+    const int64_t steps_x = (N + 63) / 64 * parts, steps_w = (M + 63) / 64 * parts;
+    int64_t S = 0, best = INT64_MAX;  // stages until the later of the two is done
+    for (int64_t s = 2; s * tiles_x < pairs && s <= steps_x && s * M * up(K, 4) * 4 <= kStepScratchBytes; ++s) {
+      const int64_t left = pairs - s * tiles_x;
+      const int64_t t = std::max((steps_x + s - 1) / s, (units_w + left - 1) / left * steps_w);
+      if (t < best) best = t, S = s;
+    }
+    if (S == 0) return false;
+    Plan px = plan<false, false>(gx, dz, parts, &W, 1, M, static_cast<int>(K), N, S);
+    Plan pw = plan<true, true>(gw, &x, 1, dz, parts, K, static_cast<int>(N), M, 1);
+    if (!ok()) return true;
+    GemmBoth both;
+    both.dx = px.g;
+    both.dw = pw.g;
+    both.dw.streams = static_cast<int>(std::min<int64_t>(px.S, pw.g.tiles_j));
+    both.dx_pairs = static_cast<int>(px.g.units);
+    constexpr uint32_t smem = GemmShape<256, kEpiTma, true>::kSmem;
+    error = (*c.opt_in)(linear_both_kernel, smem);
+    launch({dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2}, linear_both_kernel, both);
+    if (px.S > 1) join(px.j);
+    return true;
   }
 
   void join(const JoinArgs& j) {
     if (!ok()) return;
     const int64_t n = j.I * ((j.J + 3) / 4);
     const int64_t blocks = std::min<int64_t>((n + 255) / 256, 8 * c.num_sms);
-    launch(linear_join_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, j);
+    launch({dim3(static_cast<unsigned>(blocks)), 256}, linear_join_kernel, j);
   }
 };
 
@@ -405,7 +461,7 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearLaunch& c, void* work
   g.out_f32 = a.y_dtype == DSPARK_F32;
   g.pre = a.pre;
   g.ld_pre = a.ld_pre;
-  l.gemm<false, true>(g, &x, 1, &W, 1, a.M, a.N, a.K);
+  l.run<false, true>(l.plan<false, true>(g, &x, 1, &W, 1, a.M, a.N, a.K));
   return l.error;
 }
 
@@ -457,22 +513,18 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, v
     s.sums = a.dbias != nullptr ? c.scratch : nullptr;
     l.split(s);
     if (a.dbias != nullptr)
-      l.launch(linear_sums_kernel, dim3((a.N + 255) / 256), 256, 0, c.scratch, l.sum_blocks, a.N, a.dbias);
+      l.launch({dim3((a.N + 255) / 256), 256}, linear_sums_kernel, c.scratch, l.sum_blocks, a.N, a.dbias);
   }
-  if (a.dx != nullptr) {
-    GemmArgs g{};
-    g.out = a.dx;
-    g.ld_out = a.ld_dx;
-    g.out_f32 = a.dx_dtype == DSPARK_F32;
-    l.gemm<false, false>(g, dz, parts, &W, 1, a.M, a.K, a.N);
-  }
-  if (a.dW != nullptr) {
-    GemmArgs g{};
-    g.out = a.dW;
-    g.ld_out = a.ld_dw;
-    g.out_f32 = a.dw_dtype == DSPARK_F32;
-    l.gemm<true, true>(g, &x, 1, dz, parts, a.K, a.N, a.M);
-  }
+  GemmArgs gx{}, gw{};
+  gx.out = a.dx;
+  gx.ld_out = a.ld_dx;
+  gx.out_f32 = a.dx_dtype == DSPARK_F32;
+  gw.out = a.dW;
+  gw.ld_out = a.ld_dw;
+  gw.out_f32 = a.dw_dtype == DSPARK_F32;
+  if (a.dx != nullptr && a.dW != nullptr && l.both(gx, gw, dz, parts, W, x)) return l.error;
+  if (a.dx != nullptr) l.run<false, false>(l.plan<false, false>(gx, dz, parts, &W, 1, a.M, a.K, a.N));
+  if (a.dW != nullptr) l.run<true, true>(l.plan<true, true>(gw, &x, 1, dz, parts, a.K, a.N, a.M));
   return l.error;
 }
 

@@ -10,6 +10,10 @@
 // element by element.  Either operand may lie with the contraction contiguous (K-major) or with
 // its own index contiguous (MN-major), so x W, dz W^T and x^T dz read their matrices as they are.
 //
+// Where the products bound it, two blocks share tiles of 256 x 256 (PAIR): each loads half of A's rows and
+// half of B's columns, so that an output costs two thirds of the reads from L2, which is what a block by
+// itself waits for (0.52 us a stage of 48 KB; its products take 0.27).
+//
 // An operand may come in two parts, added up in the accumulator: A = A_0 + A_1 doubles the terms.
 #pragma once
 
@@ -18,6 +22,7 @@
 
 #include "activation.cuh"
 #include "async_copy.cuh"
+#include "cta_pair.cuh"
 #include "sm103.cuh"
 #include "typed.cuh"
 
@@ -33,6 +38,7 @@ struct GemmArgs {
   int tiles_j, splits;
   int64_t steps, per_split; // stages of a tile (all parts), of a unit
   int64_t blocks_k;         // stages of a part
+  int streams;              // columns of tiles are taken in turn from this many stretches of them
   // the epilogue
   const float* bias;
   const void* residual;
@@ -52,11 +58,11 @@ constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
 // as none, since such outputs are bounded by their bytes).
 enum GemmEpilogue { kEpiElements, kEpiTma, kEpiResidual };
 
-template <int BN, int EPI>
+template <int BN, int EPI, bool PAIR = false>
 struct GemmShape {
   static constexpr int kSlots = EPI == kEpiResidual ? 2 : 1;  // of a warp
   static constexpr uint32_t kSlot = EPI == kEpiResidual ? 8192 : 4096;
-  static constexpr uint32_t kA = 128 * 64 * 2, kB = BN * 64 * 2;
+  static constexpr uint32_t kA = 128 * 64 * 2, kB = (PAIR ? BN / 2 : BN) * 64 * 2;
   static constexpr uint32_t kEpi = kGemmEpiWarps * kSlots * kSlot;
   static constexpr int kStages = (226 * 1024 - 1024 - 512 - kEpi) / (kA + kB) < 8
                                      ? (226 * 1024 - 1024 - 512 - kEpi) / (kA + kB)
@@ -137,9 +143,10 @@ __device__ __forceinline__ void epi_get32(float (&v)[32], uint32_t line) {
   }
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs g) {
-  using S = GemmShape<BN, EPI>;
+// Units first, first + stride, ... of a product.
+template <int BN, bool A_MN, bool B_MN, int EPI, bool PAIR>
+__device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t first, const int64_t stride) {
+  using S = GemmShape<BN, EPI, PAIR>;
   constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -155,6 +162,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
   uint64_t* res_full = acc_full + 7;       // [warps][kSlots]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the pair's first block issues its products, on its own `full` and `acc_empty`
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  constexpr int kRows = PAIR ? 256 : 128;  // of a tile
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], kGemmEpiWarps);
+      mbar_init(&acc_empty[s], (PAIR ? 2 : 1) * kGemmEpiWarps);
     }
     mbar_init(drain, 1);
     for (int s = 0; s < kGemmEpiWarps * S::kSlots; ++s) mbar_init(&res_full[s], 1);
@@ -173,11 +183,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
     tma_prefetch_desc(&g.b[0]);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 2 * BN);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, 2 * BN);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 2 * BN);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) {  // both blocks' barriers are ready
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();  // what the call's kernels before this one made; and the scratch is read to its end
@@ -185,15 +204,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
   // unit u: tile (u % tiles_i, u / tiles_i % tiles_j), part u / (tiles_i tiles_j) of its stages, so
   // that blocks working at one time share their B tiles in L2
   const int64_t tiles = g.tiles_i * g.tiles_j;
+  auto column = [&](int64_t t) {  // of tile t
+    const int n = static_cast<int>(t / g.tiles_i);
+    if (g.streams == 1) return n * BN;
+    const int each = g.tiles_j / g.streams, more = g.tiles_j % g.streams;
+    const int r = n < each * g.streams ? n % g.streams : n - each * g.streams;
+    return (r * each + min(r, more) + n / g.streams) * BN;
+  };
 
   if (warp == 0) {
     if (lane == 0 && static_cast<int>(blockIdx.x) != g.skip_cta) {
       const uint64_t pol = l2_policy_evict_normal();
       bool ok = true;
       uint32_t n = 0;  // stages filled
-      for (int64_t u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
+      for (int64_t u = first; u < g.units && ok; u += stride) {
         const int64_t t = u % tiles, sp = u / tiles;
-        const int i0 = static_cast<int>(t % g.tiles_i) * 128, j0 = static_cast<int>(t / g.tiles_i) * BN;
+        const int i0 = static_cast<int>((t % g.tiles_i) * kRows + rank * 128);
+        const int j0 = column(t) + static_cast<int>(rank) * (BN / 2);
         const int64_t end = min(g.steps, (sp + 1) * g.per_split);
         for (int64_t k = sp * g.per_split; k < end; ++k, ++n) {
           const uint32_t s = n % kStages;
@@ -207,41 +234,56 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
           const CUtensorMap* const mb = &g.b[g.b_parts == 2 ? part : 0];
           uint8_t* const sa = smem + s * S::kA;
           uint8_t* const sb = smem + S::kOffB + s * S::kB;
-          mbar_arrive_expect_tx(&full[s], S::kA + S::kB);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (S::kA + S::kB));
+          const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
+          auto load = [&](uint8_t* to, const CUtensorMap* map, int x, int y) {
+            if constexpr (PAIR)
+              tma_load_2d_pair(to, map, x, y, bar, pol);
+            else
+              tma_load_2d(to, map, x, y, &full[s], pol);
+          };
           if constexpr (A_MN) {
-            tma_load_2d(sa, ma, i0, k0, &full[s], pol);
-            tma_load_2d(sa + 8192, ma, i0 + 64, k0, &full[s], pol);
+            load(sa, ma, i0, k0);
+            load(sa + 8192, ma, i0 + 64, k0);
           } else {
-            tma_load_2d(sa, ma, k0, i0, &full[s], pol);
+            load(sa, ma, k0, i0);
           }
           if constexpr (B_MN) {
 #pragma unroll
-            for (int c = 0; c < BN / 64; ++c)
-              tma_load_2d(sb + c * 8192, mb, j0 + c * 64, k0, &full[s], pol);
+            for (int c = 0; c < (PAIR ? BN / 128 : BN / 64); ++c) load(sb + c * 8192, mb, j0 + c * 64, k0);
           } else {
-            tma_load_2d(sb, mb, k0, j0, &full[s], pol);
+            load(sb, mb, k0, j0);
           }
         }
       }
       if (!ok) {
         *abort_flag = 1;
         record_error(g.status, kStatusTimeout);
-        for (uint32_t j = 0; j < kStages && j < n; ++j) {  // copies under way end first
+        // copies under way end first (a pair's second block's are over when the first one's wait for
+        // both is, or has run out; it meets the first at the end)
+        for (uint32_t j = 0; rank == 0 && j < kStages && j < n; ++j) {
           const uint32_t m = n - 1 - j;
-          mbar_wait(&full[m % kStages], (m / kStages) & 1, g.timeout_ns, nullptr);
+          if (!mbar_wait(&full[m % kStages], (m / kStages) & 1, g.timeout_ns, nullptr)) break;
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, BN, A_MN, B_MN);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kRows, BN, A_MN, B_MN);
+      auto commit = [](uint64_t* bar) {
+        if constexpr (PAIR)
+          umma_commit_pair(bar);
+        else
+          umma_commit(bar);
+      };
       bool ok = true, issued = false;
       uint32_t n = 0, i = 0;
-      for (int64_t u = blockIdx.x; u < g.units && ok; u += gridDim.x, ++i) {
+      for (int64_t u = first; u < g.units && ok; u += stride, ++i) {
         const int64_t sp = u / tiles;
         const int64_t k_begin = sp * g.per_split, end = min(g.steps, (sp + 1) * g.per_split);
         const uint32_t buf = i & 1;
-        if (!mbar_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag)) {
+        if (!(PAIR ? mbar_wait_cluster(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag)
+                   : mbar_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag))) {
           ok = false;
           break;
         }
@@ -260,18 +302,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
             // 16 terms: 32 bytes along K-major rows, two groups of eight rows of MN-major boxes
             const uint64_t da = A_MN ? smem_desc(a0 + kk * 2048, 8192, 1024) : smem_desc(a0 + kk * 32, 16, 1024);
             const uint64_t db = B_MN ? smem_desc(b0 + kk * 2048, 8192, 1024) : smem_desc(b0 + kk * 32, 16, 1024);
-            umma_bf16(d, da, db, idesc, k > k_begin || kk > 0 ? 1u : 0u);
+            const uint32_t add = k > k_begin || kk > 0 ? 1u : 0u;
+            if constexpr (PAIR)
+              umma_bf16_pair(d, da, db, idesc, add);
+            else
+              umma_bf16(d, da, db, idesc, add);
           }
           issued = true;
-          umma_commit(&empty[s]);
+          commit(&empty[s]);
         }
-        if (ok) umma_commit(&acc_full[buf]);
+        if (ok) commit(&acc_full[buf]);
       }
       if (!ok) {
         *abort_flag = 1;
         record_error(g.status, kStatusTimeout);
         if (issued) {  // products under way end before TMEM is freed
-          umma_commit(drain);
+          commit(drain);
           mbar_wait(drain, 0, g.timeout_ns, nullptr);
         }
       }
@@ -286,8 +332,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
     const bool has_res = EPI == kEpiTma ? false : EPI == kEpiResidual || g.residual != nullptr;
     auto place = [&](int64_t u, int64_t& row0, int& col0) {
       const int64_t t = u % tiles;
-      row0 = (t % g.tiles_i) * 128 + q * 32;
-      col0 = static_cast<int>(t / g.tiles_i) * BN;
+      row0 = (t % g.tiles_i) * kRows + rank * 128 + q * 32;
+      col0 = column(t);
     };
     uint32_t phases = 0, pending = 0;  // bit a slot: of its barrier; a load is under way
     // the residual of chunk c of unit u on its way into a slot (fp32: both boxes; bf16: the second)
@@ -315,21 +361,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
     // (position n + kSlots of the warp's chunks, from chunk c of unit u)
     auto load_later = [&](int64_t u, int c, int slot) {
       int k = c + 2 * S::kSlots;
-      for (; k >= kRound; k -= kRound) u += gridDim.x;
+      for (; k >= kRound; k -= kRound) u += stride;
       load_residual(u, k, slot);
     };
     bool ok = true;
     uint32_t i = 0, n = 0;
     if (group < kChunks) {
-      int64_t u = blockIdx.x;
+      int64_t u = first;
       int c = group;
       for (int s = 0; s < S::kSlots; ++s) {
-        for (; c >= kRound; c -= kRound) u += gridDim.x;
+        for (; c >= kRound; c -= kRound) u += stride;
         load_residual(u, c, s);
         c += 2;
       }
     }
-    for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x, ++i) {
+    for (int64_t u = first; u < g.units; u += stride, ++i) {
       int64_t row0;
       int col0;
       place(u, row0, col0);
@@ -477,7 +523,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
       if (!ok) break;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
+        else
+          mbar_arrive(&acc_empty[b]);
+      }
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -493,11 +544,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __gr
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) {  // neither block's shared memory is in use any more
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, 2 * BN);
+    else
+      tmem_dealloc(tmem, 2 * BN);
   }
+}
+
+template <int BN, bool A_MN, bool B_MN, int EPI, bool PAIR = false>
+__global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs g) {
+  if constexpr (PAIR)
+    gemm_units<BN, A_MN, B_MN, EPI, true>(g, blockIdx.x / 2, gridDim.x / 2);
+  else
+    gemm_units<BN, A_MN, B_MN, EPI, false>(g, blockIdx.x, gridDim.x);
+}
+
+// Both products of a gradient at once: pairs [0, dx_pairs) work on dz W^T, the others on x^T dz, and walk
+// through the columns of dz side by side, so that what one has read of it the other finds in L2.
+struct GemmBoth {
+  GemmArgs dx, dw;
+  int dx_pairs;
+};
+__global__ void __launch_bounds__(kGemmThreads, 1) linear_both_kernel(const __grid_constant__ GemmBoth b) {
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  if (pair < b.dx_pairs)
+    gemm_units<256, false, false, kEpiTma, true>(b.dx, pair, b.dx_pairs);
+  else
+    gemm_units<256, true, true, kEpiTma, true>(b.dw, pair - b.dx_pairs, pairs - b.dx_pairs);
 }
 
 }  // namespace dspark
