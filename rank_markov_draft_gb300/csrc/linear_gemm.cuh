@@ -28,6 +28,12 @@
 
 namespace dspark {
 
+enum GemmL2 { kL2Normal, kL2First, kL2Last };  // when L2 gives a line up
+
+__device__ __forceinline__ uint64_t gemm_policy(int l2) {
+  return l2 == kL2First ? l2_policy_evict_first() : l2 == kL2Last ? l2_policy_evict_last() : l2_policy_evict_normal();
+}
+
 struct GemmArgs {
   CUtensorMap a[2], b[2];
   CUtensorMap out_map, pre_map, res_map;  // (outputs by TMA) boxes of 32 rows x 128 bytes
@@ -47,6 +53,7 @@ struct GemmArgs {
   void *out, *pre;
   int* status;
   uint64_t timeout_ns;
+  int l2_a, l2_b, l2_out;   // GemmL2 of the operands and the output
   int skip_cta;             // testing: the block that loads nothing (-1: none)
 };
 
@@ -76,11 +83,13 @@ struct GemmShape {
   static_assert(2 * BN <= 512, "tensor memory columns");
 };
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(src)
-               : "memory");
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src), "l"(policy)
+      : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // until this thread's stores have read their shared memory; until they are done
@@ -214,7 +223,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
 
   if (warp == 0) {
     if (lane == 0 && static_cast<int>(blockIdx.x) != g.skip_cta) {
-      const uint64_t pol = l2_policy_evict_normal();
+      const uint64_t pol_a = gemm_policy(g.l2_a), pol_b = gemm_policy(g.l2_b);
       bool ok = true;
       uint32_t n = 0;  // stages filled
       for (int64_t u = first; u < g.units && ok; u += stride) {
@@ -236,23 +245,23 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
           uint8_t* const sb = smem + S::kOffB + s * S::kB;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (S::kA + S::kB));
           const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
-          auto load = [&](uint8_t* to, const CUtensorMap* map, int x, int y) {
+          auto load = [&](uint8_t* to, const CUtensorMap* map, int x, int y, uint64_t pol) {
             if constexpr (PAIR)
               tma_load_2d_pair(to, map, x, y, bar, pol);
             else
               tma_load_2d(to, map, x, y, &full[s], pol);
           };
           if constexpr (A_MN) {
-            load(sa, ma, i0, k0);
-            load(sa + 8192, ma, i0 + 64, k0);
+            load(sa, ma, i0, k0, pol_a);
+            load(sa + 8192, ma, i0 + 64, k0, pol_a);
           } else {
-            load(sa, ma, k0, i0);
+            load(sa, ma, k0, i0, pol_a);
           }
           if constexpr (B_MN) {
 #pragma unroll
-            for (int c = 0; c < (PAIR ? BN / 128 : BN / 64); ++c) load(sb + c * 8192, mb, j0 + c * 64, k0);
+            for (int c = 0; c < (PAIR ? BN / 128 : BN / 64); ++c) load(sb + c * 8192, mb, j0 + c * 64, k0, pol_b);
           } else {
-            load(sb, mb, k0, j0);
+            load(sb, mb, k0, j0, pol_b);
           }
         }
       }
@@ -327,6 +336,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
     const int q = warp & 3, e = warp - 2, group = e >> 2;
     constexpr int kChunks = BN / 64, kRound = kChunks < 2 ? 2 : kChunks;  // (of 64 columns the second group has none)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint64_t pol_out = gemm_policy(g.l2_out);
     const uint32_t slots = smem_addr(smem + S::kOffEpi + e * S::kSlots * S::kSlot);
     const uint32_t own = 128 * lane + ((lane & 7) << 4);  // this lane's line of a 4 KB box
     const bool has_res = EPI == kEpiTma ? false : EPI == kEpiResidual || g.residual != nullptr;
@@ -407,7 +417,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              if (col + shift < g.J) tma_store_3d(map, from, col + shift, static_cast<int>(row0), sp);
+              if (col + shift < g.J) tma_store_3d(map, from, col + shift, static_cast<int>(row0), sp, pol_out);
               bulk_commit();
             }
           };
