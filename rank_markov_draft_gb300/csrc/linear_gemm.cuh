@@ -358,7 +358,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       if (lane == 0) {
         uint64_t* const bar = &res_full[e * S::kSlots + slot];
         uint8_t* const to = smem + S::kOffEpi + (e * S::kSlots + slot) * S::kSlot;
-        const uint64_t pol = l2_policy_evict_first();
+        const uint64_t pol = l2_policy_evict_normal();
         mbar_arrive_expect_tx(bar, g.res_f32 ? 8192 : 4096);
         if (g.res_f32) {
           tma_load_2d(to, &g.res_map, col, static_cast<int>(row0), bar, pol);
