@@ -31,12 +31,30 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// mbar_wait for arrivals from other CTAs of the cluster.
+// mbar_wait for arrivals from other CTAs of the cluster (a fence of the cluster after mbar_wait took 40 of
+// 270 us where a product's lane waits every few us).
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
                                                   volatile int* abort_flag) {
-  if (!mbar_wait(bar, parity, timeout_ns, abort_flag)) return false;
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return true;
+  uint64_t deadline = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok != 0) return true;
+    if ((it & 7u) == 7u) {
+      if (abort_flag != nullptr && *abort_flag) return false;
+      const uint64_t now = globaltimer_ns();
+      if (deadline == 0)
+        deadline = now + timeout_ns;
+      else if (now > deadline)
+        return false;
+    }
+  }
 }
 
 // A TMA load into this CTA's shared memory that completes on a barrier of the pair's other CTA (or its

@@ -78,13 +78,13 @@ __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
 }
 
 // ------------------------------------------------------------------ dz, and rows for TMA
-// hi (+ lo) = src act'(pre) as one or two bf16 numbers, rows ld_dst apart, and the column sums of a
-// block's rows.  Each of them may be left out.
+// src act'(pre) as the sum of up to three bf16 numbers (8 bits of it each), rows ld_dst apart, and the
+// column sums of a block's rows.  Each of them may be left out.
 struct SplitArgs {
   const void *src, *pre;
   int64_t rows, ld_src, ld_pre, ld_dst;
   int cols, src_f32, pre_f32, act, rows_per_block;
-  bf16 *hi, *lo;
+  bf16* part[3];
   float* sums;  // [row blocks][cols]
 };
 
@@ -111,13 +111,16 @@ __global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
     for (int j = 0; j < 4; ++j) {
       const int c = c0 + 32 * j;
       sum[j] += v[j];
-      if (c >= a.cols || a.hi == nullptr) continue;
-      const bf16 h = __float2bfloat16_rn(v[j]);
-      a.hi[r * a.ld_dst + c] = h;
-      if (a.lo != nullptr) {
-        // (of an infinity or NaN the second part is nothing, not NaN beside an infinity)
-        const float hf = __bfloat162float(h);
-        a.lo[r * a.ld_dst + c] = __float2bfloat16_rn(isfinite(hf) ? v[j] - hf : 0.f);
+      if (c >= a.cols) continue;
+      float rest = v[j];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        if (a.part[p] == nullptr) break;
+        const bf16 h = __float2bfloat16_rn(rest);
+        a.part[p][r * a.ld_dst + c] = h;
+        // (of an infinity or NaN nothing is left, not a NaN beside an infinity)
+        const float f = __bfloat162float(h);
+        rest = isfinite(f) ? rest - f : 0.f;
       }
     }
   }
@@ -214,7 +217,7 @@ struct Launcher {
     a.ld_src = ld;
     a.ld_dst = up(cols, 8);
     a.cols = static_cast<int>(cols);
-    a.hi = to;
+    a.part[0] = to;
     split(a);
     return {to, rows, cols, a.ld_dst};
   }
@@ -306,6 +309,7 @@ struct Launcher {
     g.tiles_j = (J + p.BN - 1) / p.BN;
     g.splits = static_cast<int>(p.S);
     g.streams = 1;
+    g.restart = g.out_f32 ? kGemmRestart : g.steps;
     g.per_split = (g.steps + p.S - 1) / p.S;
     g.units = g.tiles_i * g.tiles_j * p.S;
     g.a_parts = na;
@@ -381,11 +385,12 @@ struct Launcher {
   // Both products of a gradient in one launch, where dz passes what L2 keeps between two launches
   // (64 MB of its 129, the other streams taking their share) and dz W^T is of so few tiles that splits
   // of it keep half the blocks busy. Returns whether it did.
-  bool both(const GemmArgs& gx, const GemmArgs& gw, const Matrix* dz, int parts, const Matrix& W, const Matrix& x) {
+  bool both(const GemmArgs& gx, const GemmArgs& gw, const Matrix* dz, int parts_x, int parts_w, const Matrix& W,
+            const Matrix& x) {
     const int64_t M = x.rows, K = x.cols, N = dz[0].cols, pairs = c.num_sms / 2;
     const int64_t tiles_x = (M + 255) / 256 * ((K + 255) / 256), units_w = (K + 255) / 256 * ((N + 255) / 256);
-    if (M * N * 2 * parts < (64ll << 20) || tiles_x > pairs / 2 || !tma(gw.out, gw.ld_out, gw.out_f32)) return false;
-    const int64_t steps_x = (N + 63) / 64 * parts, steps_w = (M + 63) / 64 * parts;
+    if (M * N * 2 * std::max(parts_x, parts_w) < (64ll << 20) || tiles_x > pairs / 2 || !tma(gw.out, gw.ld_out, gw.out_f32)) return false;
+    const int64_t steps_x = (N + 63) / 64 * parts_x, steps_w = (M + 63) / 64 * parts_w;
     // Time until the later of the two is done: a stage of dz W^T takes 0.36 us, one of x^T dz (both of its
     // operands MN-major) 0.45.
     int64_t S = 0, best = INT64_MAX;
@@ -395,18 +400,16 @@ struct Launcher {
       if (t < best) best = t, S = s;
     }
     if (S == 0) return false;
-    Plan px = plan<false, false>(gx, dz, parts, &W, 1, M, static_cast<int>(K), N, S);
-    Plan pw = plan<true, true>(gw, &x, 1, dz, parts, K, static_cast<int>(N), M, 1);
+    Plan px = plan<false, false>(gx, dz, parts_x, &W, 1, M, static_cast<int>(K), N, S);
+    Plan pw = plan<true, true>(gw, &x, 1, dz, parts_w, K, static_cast<int>(N), M, 1);
     if (!ok()) return true;
     GemmBoth both;
     both.dx = px.g;
     both.dw = pw.g;
     both.dw.streams = static_cast<int>(std::min<int64_t>(px.S, pw.g.tiles_j));
     both.dx_pairs = static_cast<int>(px.g.units);
-    // dz stays in L2 from its reading for dW, which is ahead, to the one for dx; dW passes through (207 us
-    // for 2048 x 151936 of 256, 215 without these hints, 253 in two launches)
-    both.dw.l2_b = kL2Last;
-    both.dx.l2_a = kL2First;
+    // dW passes through L2, which has dz to keep for its second reading (213 us for 2048 x 151936 of 256, 216
+    // without, 253 in two launches)
     both.dw.l2_out = kL2First;
     constexpr uint32_t smem = GemmShape<256, kEpiTma, true>::kSmem;
     error = (*c.opt_in)(linear_both_kernel, smem);
@@ -427,7 +430,14 @@ struct Launcher {
 bool dz_as_it_is(const LinearGradArgs& a) {
   return a.act == DSPARK_ACT_NONE && a.dy_dtype == DSPARK_BF16 && tma_rows(a.dy, a.ld_dy);
 }
-bool two_parts(const LinearGradArgs& a) { return a.act != DSPARK_ACT_NONE || a.dy_dtype == DSPARK_F32; }
+// The bf16 numbers that stand for an element of dz in a product of this type: two (2^-17 of it lost) are
+// much finer than a bf16 output, three (2^-25) as fine as an fp32 one.
+int parts_of(const LinearGradArgs& a, int out_dtype) {
+  return a.act == DSPARK_ACT_NONE && a.dy_dtype == DSPARK_BF16 ? 1 : out_dtype == DSPARK_F32 ? 3 : 2;
+}
+int parts_of(const LinearGradArgs& a) {
+  return std::max(a.dx != nullptr ? parts_of(a, a.dx_dtype) : 0, a.dW != nullptr ? parts_of(a, a.dw_dtype) : 0);
+}
 
 }  // namespace
 
@@ -445,8 +455,7 @@ int64_t linear_grad_workspace(const LinearGradArgs& a) {
   if (a.dW != nullptr && !tma_rows(a.x, a.ld_x)) w.take(a.M, a.K);
   if (a.dx != nullptr && !tma_rows(a.W, a.ld_w)) w.take(a.K, a.N);
   if ((a.dx != nullptr || a.dW != nullptr) && !dz_as_it_is(a)) {
-    w.take(a.M, a.N);
-    if (two_parts(a)) w.take(a.M, a.N);
+    for (int p = 0; p < parts_of(a); ++p) w.take(a.M, a.N);
   }
   return w.used();
 }
@@ -493,8 +502,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, v
   Matrix x{}, W{};
   if (a.dW != nullptr) x = l.rows_for_tma(a.x, a.M, a.K, a.ld_x, ws);
   if (a.dx != nullptr) W = l.rows_for_tma(a.W, a.K, a.N, a.ld_w, ws);
-  Matrix dz[2] = {{a.dy, a.M, a.N, a.ld_dy}, {}};
-  int parts = 1;
+  Matrix dz[3] = {{a.dy, a.M, a.N, a.ld_dy}};
   const bool products = a.dx != nullptr || a.dW != nullptr;
   if (a.dbias != nullptr || (products && !dz_as_it_is(a))) {
     SplitArgs s{};
@@ -509,12 +517,9 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, v
     s.cols = a.N;
     s.ld_dst = up(a.N, 8);
     if (products && !dz_as_it_is(a)) {
-      s.hi = ws.take(a.M, a.N);
-      dz[0] = {s.hi, a.M, a.N, s.ld_dst};
-      if (two_parts(a)) {
-        s.lo = ws.take(a.M, a.N);
-        dz[1] = {s.lo, a.M, a.N, s.ld_dst};
-        parts = 2;
+      for (int p = 0; p < parts_of(a); ++p) {
+        s.part[p] = ws.take(a.M, a.N);
+        dz[p] = {s.part[p], a.M, a.N, s.ld_dst};
       }
     }
     s.sums = a.dbias != nullptr ? c.scratch : nullptr;
@@ -529,9 +534,10 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, v
   gw.out = a.dW;
   gw.ld_out = a.ld_dw;
   gw.out_f32 = a.dw_dtype == DSPARK_F32;
-  if (a.dx != nullptr && a.dW != nullptr && l.both(gx, gw, dz, parts, W, x)) return l.error;
-  if (a.dx != nullptr) l.run<false, false>(l.plan<false, false>(gx, dz, parts, &W, 1, a.M, a.K, a.N));
-  if (a.dW != nullptr) l.run<true, true>(l.plan<true, true>(gw, &x, 1, dz, parts, a.K, a.N, a.M));
+  const int parts_x = parts_of(a, a.dx_dtype), parts_w = parts_of(a, a.dw_dtype);
+  if (a.dx != nullptr && a.dW != nullptr && l.both(gx, gw, dz, parts_x, parts_w, W, x)) return l.error;
+  if (a.dx != nullptr) l.run<false, false>(l.plan<false, false>(gx, dz, parts_x, &W, 1, a.M, a.K, a.N));
+  if (a.dW != nullptr) l.run<true, true>(l.plan<true, true>(gw, &x, 1, dz, parts_w, a.K, a.N, a.M));
   return l.error;
 }
 

@@ -14,7 +14,12 @@
 // half of B's columns, so that an output costs two thirds of the reads from L2, which is what a block by
 // itself waits for (0.52 us a stage of 48 KB; its products take 0.27).
 //
-// An operand may come in two parts, added up in the accumulator: A = A_0 + A_1 doubles the terms.
+// An operand may come in up to three parts, added up like further terms: A = A_0 + A_1 + A_2.
+//
+// The accumulator cuts what a sum of fp32 would round, so that a long sum of terms drifts (2e-6 of itself
+// over 2048 terms, 2e-5 over 50000). For fp32 outputs it starts again every 512 terms, and the epilogue's
+// threads add up what it held, rounded, in registers: 5e-7 at any length, a sum of fp32 in order gives
+// 4e-7 to 8e-7. (Every 256 terms gave 2.4e-7, but the logits' gradients then took 287 us instead of 213.)
 #pragma once
 
 #include <cstdint>
@@ -35,15 +40,16 @@ __device__ __forceinline__ uint64_t gemm_policy(int l2) {
 }
 
 struct GemmArgs {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[3], b[3];
   CUtensorMap out_map, pre_map, res_map;  // (outputs by TMA) boxes of 32 rows x 128 bytes
-  int a_parts, b_parts;     // 1, or 2 of one of them
+  int a_parts, b_parts;     // 1, or 2 or 3 of one of them
   int64_t I;                // rows and columns of the output
   int J;
   int64_t tiles_i, units;
   int tiles_j, splits;
   int64_t steps, per_split; // stages of a tile (all parts), of a unit
   int64_t blocks_k;         // stages of a part
+  int64_t restart;          // stages after which the accumulator starts again
   int streams;              // columns of tiles are taken in turn from this many stretches of them
   // the epilogue
   const float* bias;
@@ -57,6 +63,7 @@ struct GemmArgs {
   int skip_cta;             // testing: the block that loads nothing (-1: none)
 };
 
+constexpr int kGemmRestart = 8;  // stages of 64 terms
 constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
 
@@ -82,6 +89,16 @@ struct GemmShape {
   static_assert((2 * kStages + 8 + kGemmEpiWarps * kSlots) * 8 <= 512, "barriers");
   static_assert(2 * BN <= 512, "tensor memory columns");
 };
+
+// 16 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+      : "memory");
+}
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z,
                                              uint64_t policy) {
@@ -237,10 +254,10 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
             ok = false;
             break;
           }
-          const int part = k >= g.blocks_k ? 1 : 0;
-          const int k0 = static_cast<int>(k - (part ? g.blocks_k : 0)) * 64;
-          const CUtensorMap* const ma = &g.a[g.a_parts == 2 ? part : 0];
-          const CUtensorMap* const mb = &g.b[g.b_parts == 2 ? part : 0];
+          const int part = k < g.blocks_k ? 0 : k < 2 * g.blocks_k ? 1 : 2;
+          const int k0 = static_cast<int>(k - part * g.blocks_k) * 64;
+          const CUtensorMap* const ma = &g.a[g.a_parts > 1 ? part : 0];
+          const CUtensorMap* const mb = &g.b[g.b_parts > 1 ? part : 0];
           uint8_t* const sa = smem + s * S::kA;
           uint8_t* const sb = smem + S::kOffB + s * S::kB;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (S::kA + S::kB));
@@ -287,40 +304,42 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       };
       bool ok = true, issued = false;
       uint32_t n = 0, i = 0;
-      for (int64_t u = first; u < g.units && ok; u += stride, ++i) {
+      for (int64_t u = first; u < g.units && ok; u += stride) {
         const int64_t sp = u / tiles;
-        const int64_t k_begin = sp * g.per_split, end = min(g.steps, (sp + 1) * g.per_split);
-        const uint32_t buf = i & 1;
-        if (!(PAIR ? mbar_wait_cluster(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag)
-                   : mbar_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + buf * BN;
-        for (int64_t k = k_begin; k < end; ++k, ++n) {
-          const uint32_t s = n % kStages;
-          if (!mbar_wait(&full[s], (n / kStages) & 1, g.timeout_ns, abort_flag, 20u)) {
+        const int64_t end = min(g.steps, (sp + 1) * g.per_split);
+        for (int64_t k0 = sp * g.per_split; k0 < end && ok; k0 += g.restart, ++i) {
+          const uint32_t buf = i & 1;
+          if (!(PAIR ? mbar_wait_cluster(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag)
+                     : mbar_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_addr(smem + s * S::kA), b0 = smem_addr(smem + S::kOffB + s * S::kB);
+          const uint32_t d = tmem + buf * BN;
+          for (int64_t k = k0; k < min(end, k0 + g.restart); ++k, ++n) {
+            const uint32_t s = n % kStages;
+            if (!mbar_wait(&full[s], (n / kStages) & 1, g.timeout_ns, abort_flag, 20u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_addr(smem + s * S::kA), b0 = smem_addr(smem + S::kOffB + s * S::kB);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            // 16 terms: 32 bytes along K-major rows, two groups of eight rows of MN-major boxes
-            const uint64_t da = A_MN ? smem_desc(a0 + kk * 2048, 8192, 1024) : smem_desc(a0 + kk * 32, 16, 1024);
-            const uint64_t db = B_MN ? smem_desc(b0 + kk * 2048, 8192, 1024) : smem_desc(b0 + kk * 32, 16, 1024);
-            const uint32_t add = k > k_begin || kk > 0 ? 1u : 0u;
-            if constexpr (PAIR)
-              umma_bf16_pair(d, da, db, idesc, add);
-            else
-              umma_bf16(d, da, db, idesc, add);
+            for (int kk = 0; kk < 4; ++kk) {
+              // 16 terms: 32 bytes along K-major rows, two groups of eight rows of MN-major boxes
+              const uint64_t da = A_MN ? smem_desc(a0 + kk * 2048, 8192, 1024) : smem_desc(a0 + kk * 32, 16, 1024);
+              const uint64_t db = B_MN ? smem_desc(b0 + kk * 2048, 8192, 1024) : smem_desc(b0 + kk * 32, 16, 1024);
+              const uint32_t add = k > k0 || kk > 0 ? 1u : 0u;
+              if constexpr (PAIR)
+                umma_bf16_pair(d, da, db, idesc, add);
+              else
+                umma_bf16(d, da, db, idesc, add);
+            }
+            issued = true;
+            commit(&empty[s]);
           }
-          issued = true;
-          commit(&empty[s]);
+          if (ok) commit(&acc_full[buf]);
         }
-        if (ok) commit(&acc_full[buf]);
       }
       if (!ok) {
         *abort_flag = 1;
@@ -385,15 +404,64 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
         c += 2;
       }
     }
+    auto accumulator_free = [&](uint32_t b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
+        else
+          mbar_arrive(&acc_empty[b]);
+      }
+    };
     for (int64_t u = first; u < g.units; u += stride, ++i) {
       int64_t row0;
       int col0;
       place(u, row0, col0);
       const int sp = static_cast<int>(u / tiles);
+      // all accumulators of the unit but the last are added up in registers, and their sum joins that one
+      const int64_t end = min(g.steps, (sp + 1) * g.per_split), stages = end - sp * g.per_split;
+      constexpr int kMine = BN >= 128 ? BN / 32 : 4;  // 16-column pieces of a warp
+      if (stages > g.restart) {
+        float sum[kMine][16];
+#pragma unroll
+        for (int p = 0; p < kMine; ++p)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[p][j] = 0.f;
+        auto piece = [&](uint32_t b, int p) { return lane_base + b * BN + 64 * (group + 2 * (p / 4)) + 16 * (p % 4); };
+        for (int64_t left = stages;; left -= g.restart) {
+          const uint32_t b = i & 1;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i >> 1) & 1, g.timeout_ns, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (group < kChunks) {
+#pragma unroll
+            for (int p = 0; p < kMine; ++p) {
+              uint32_t v[16];
+              tmem_ld_x16(piece(b, p), v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[p][j] += __uint_as_float(v[j]);
+            }
+          }
+          if (left <= g.restart) {
+            if (group < kChunks) {
+#pragma unroll
+              for (int p = 0; p < kMine; ++p) tmem_st_x16(piece(b, p), sum[p]);
+            }
+            break;
+          }
+          accumulator_free(b);
+          ++i;
+        }
+        if (!ok) break;
+        tmem_wait_st();
+      } else {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[i & 1], (i >> 1) & 1, g.timeout_ns, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+      }
       const uint32_t b = i & 1;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i >> 1) & 1, g.timeout_ns, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
 #pragma unroll 1
       for (int c = group; c < kChunks; c += 2, ++n) {
         const int col = col0 + 64 * c, slot = n % S::kSlots;
@@ -531,14 +599,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
         }
       }
       if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR)
-          mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
-        else
-          mbar_arrive(&acc_empty[b]);
-      }
+      accumulator_free(b);
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
