@@ -1,39 +1,56 @@
 // activation.cuh -- the linear layers' activations and their slopes, in fp32 by CUDA's functions.
 #pragma once
 
+#include <type_traits>
+
 #include "dspark.h"
 
 namespace dspark {
 
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case DSPARK_ACT_SIGMOID: return 1.f / (1.f + expf(-z));
-    case DSPARK_ACT_TANH: return tanhf(z);
-    case DSPARK_ACT_RELU: return z < 0.f ? 0.f : z;  // (a NaN stays one)
-    case DSPARK_ACT_SILU: return z / (1.f + expf(-z));
-    case DSPARK_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678f);
-    default: return z;
-  }
+// 1 / (1 + e^-z); the quick division is right to two roundings, and gives 0 where the quotient is
+// below 2^-126.
+__device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == DSPARK_ACT_SIGMOID) return sigmoid_of(z);
+  if constexpr (ACT == DSPARK_ACT_TANH) return tanhf(z);
+  if constexpr (ACT == DSPARK_ACT_RELU) return z < 0.f ? 0.f : z;  // (a NaN stays one)
+  if constexpr (ACT == DSPARK_ACT_SILU) return __fdividef(z, 1.f + expf(-z));
+  if constexpr (ACT == DSPARK_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678f);
+  return z;
 }
 
-__device__ __forceinline__ float act_slope(int act, float z) {
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == DSPARK_ACT_SIGMOID) {
+    const float s = sigmoid_of(z);
+    return s * (1.f - s);
+  }
+  if constexpr (ACT == DSPARK_ACT_TANH) {
+    const float t = tanhf(z);
+    return 1.f - t * t;
+  }
+  if constexpr (ACT == DSPARK_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == DSPARK_ACT_SILU) {
+    const float s = sigmoid_of(z);
+    return s * (1.f + z * (1.f - s));
+  }
+  if constexpr (ACT == DSPARK_ACT_GELU)
+    return 0.5f * erfcf(z * -0.70710678f) + z * expf(-0.5f * z * z) * 0.39894228f;
+  return 1.f;
+}
+
+// f with the activation as a constant: one branch for many elements.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
-    case DSPARK_ACT_SIGMOID: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f - s);
-    }
-    case DSPARK_ACT_TANH: {
-      const float t = tanhf(z);
-      return 1.f - t * t;
-    }
-    case DSPARK_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case DSPARK_ACT_SILU: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f + z * (1.f - s));
-    }
-    case DSPARK_ACT_GELU:
-      return 0.5f * erfcf(z * -0.70710678f) + z * expf(-0.5f * z * z) * 0.39894228f;
-    default: return 1.f;
+    case DSPARK_ACT_SIGMOID: f(std::integral_constant<int, DSPARK_ACT_SIGMOID>()); break;
+    case DSPARK_ACT_TANH: f(std::integral_constant<int, DSPARK_ACT_TANH>()); break;
+    case DSPARK_ACT_RELU: f(std::integral_constant<int, DSPARK_ACT_RELU>()); break;
+    case DSPARK_ACT_SILU: f(std::integral_constant<int, DSPARK_ACT_SILU>()); break;
+    case DSPARK_ACT_GELU: f(std::integral_constant<int, DSPARK_ACT_GELU>()); break;
+    default: break;
   }
 }
 

@@ -6,6 +6,7 @@
 // boundaries for TMA, and dz = dy act'(pre) as bf16 numbers.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dependent.h"
 #include "linear_gemm.cuh"
@@ -39,9 +40,9 @@ __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
   const int per_row = (a.J + 3) / 4;
   const int64_t n = a.I * per_row;
   for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < n; e += gridDim.x * 256ll) {
-    const int64_t r = e / per_row;
-    const int c = static_cast<int>(e - r * per_row) * 4;
-    const float* p = a.part + r * a.ld_part + c;
+    const int64_t row = e / per_row;
+    const int c = static_cast<int>(e - row * per_row) * 4;
+    const float* p = a.part + row * a.ld_part + c;
     float z[4] = {};
 #pragma unroll 4
     for (int s = 0; s < a.splits; ++s) {
@@ -49,30 +50,41 @@ __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
       z[0] += f.x, z[1] += f.y, z[2] += f.z, z[3] += f.w;
     }
     const int m = min(4, a.J - c);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < m && a.bias != nullptr) z[j] += a.bias[c + j];
-    auto put = [&](void* dst, int64_t ld) {
-      if (a.vec && a.out_f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(dst) + r * ld + c) = make_float4(z[0], z[1], z[2], z[3]);
-      } else if (a.vec) {
-        *reinterpret_cast<uint2*>(static_cast<bf16*>(dst) + r * ld + c) = make_uint2(narrow2(z[0], z[1]), narrow2(z[2], z[3]));
-      } else {
+    float r[4] = {};
+    if (a.residual != nullptr)
+      with_type(a.residual, a.res_f32, [&](auto q) {
+        q += row * a.ld_res + c;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j < m) store_as(dst, a.out_f32, r * ld + c + j, z[j]);
-      }
-    };
-    if (a.pre != nullptr) put(a.pre, a.ld_pre);
-    if (a.act != DSPARK_ACT_NONE) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = act_value(a.act, z[j]);
-    }
-    if (a.residual != nullptr) {
+          if (j < m) r[j] = load1(q + j);
+      });
+    if (a.bias != nullptr) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (j < m) z[j] += load_as(a.residual, a.res_f32, r * a.ld_res + c + j);
+        if (j < m) z[j] += a.bias[c + j];
     }
+    auto put = [&](void* dst, int64_t ld) {
+      with_type(dst, a.out_f32, [&](auto q) {
+        q += row * ld + c;
+        if (a.vec) {
+          if constexpr (sizeof(*q) == 4)
+            *reinterpret_cast<float4*>(q) = make_float4(z[0], z[1], z[2], z[3]);
+          else
+            *reinterpret_cast<uint2*>(q) = make_uint2(narrow2(z[0], z[1]), narrow2(z[2], z[3]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < m) store1(q + j, z[j]);
+        }
+      });
+    };
+    if (a.pre != nullptr) put(a.pre, a.ld_pre);
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = act_value<decltype(act)::value>(z[j]);
+    });
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] += r[j];
     put(a.out, a.ld_out);
   }
 }
@@ -88,48 +100,83 @@ struct SplitArgs {
   float* sums;  // [row blocks][cols]
 };
 
+constexpr int kSplitRows = 2;  // rows under way a thread
+
+// A warp takes 256 columns of a row: eight neighbours a lane where rows allow vectors (VEC), else every
+// 32nd.
+template <bool VEC>
 __global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ float warps[8][128];
+  __shared__ float warps[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x * 128 + lane;
+  const int c0 = blockIdx.x * 256 + (VEC ? 8 * lane : lane);
+  constexpr int kStep = VEC ? 1 : 32;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_block;
   const int64_t r1 = min(a.rows, r0 + a.rows_per_block);
-  float sum[4] = {};
-#pragma unroll 2
-  for (int64_t r = r0 + warp; r < r1; r += 8) {
-    float v[4];
+  float sum[8] = {};
+  auto fetch = [&](const void* p, int f32, int64_t ld, int64_t r, float (&v)[kSplitRows][8]) {
+    with_type(p, f32, [&](auto q) {
+      using T = std::remove_const_t<std::remove_pointer_t<decltype(q)>>;
+      if constexpr (VEC) {
+        Raw8<T> raw[kSplitRows];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + 32 * j;
-      v[j] = c < a.cols ? load_as(a.src, a.src_f32, r * a.ld_src + c) : 0.f;
-      if (a.act != DSPARK_ACT_NONE && c < a.cols)
-        v[j] *= act_slope(a.act, load_as(a.pre, a.pre_f32, r * a.ld_pre + c));
+        for (int k = 0; k < kSplitRows; ++k) {
+          raw[k].zero();
+          if (c0 < a.cols && r + 8 * k < r1) raw[k].load(q + (r + 8 * k) * ld + c0);
+        }
+#pragma unroll
+        for (int k = 0; k < kSplitRows; ++k) raw[k].get(v[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kSplitRows; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[k][j] = c0 + kStep * j < a.cols && r + 8 * k < r1 ? load1(q + (r + 8 * k) * ld + c0 + kStep * j) : 0.f;
+      }
+    });
+  };
+  for (int64_t r = r0 + warp; r < r1; r += 8 * kSplitRows) {
+    float v[kSplitRows][8], z[kSplitRows][8];
+    fetch(a.src, a.src_f32, a.ld_src, r, v);
+    if (a.act != DSPARK_ACT_NONE) {
+      fetch(a.pre, a.pre_f32, a.ld_pre, r, z);
+      with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int k = 0; k < kSplitRows; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[k][j] *= act_slope<decltype(act)::value>(z[k][j]);
+      });
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + 32 * j;
-      sum[j] += v[j];
-      if (c >= a.cols) continue;
-      float rest = v[j];
+    for (int k = 0; k < kSplitRows; ++k) {
+      if (r + 8 * k >= r1 || c0 >= a.cols) continue;
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        if (a.part[p] == nullptr) break;
-        const bf16 h = __float2bfloat16_rn(rest);
-        a.part[p][r * a.ld_dst + c] = h;
+      for (int j = 0; j < 8; ++j) sum[j] += v[k][j];
+      for (int p = 0; p < 3 && a.part[p] != nullptr; ++p) {
+        bf16* const dst = a.part[p] + (r + 8 * k) * a.ld_dst + c0;
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = __bfloat162float(__float2bfloat16_rn(v[k][j]));
+        if constexpr (VEC) {
+          store8(dst, h);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c0 + kStep * j < a.cols) store1(dst + kStep * j, h[j]);
+        }
         // (of an infinity or NaN nothing is left, not a NaN beside an infinity)
-        const float f = __bfloat162float(h);
-        rest = isfinite(f) ? rest - f : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = isfinite(h[j]) ? v[k][j] - h[j] : 0.f;
       }
     }
   }
   if (a.sums == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) warps[warp][lane + 32 * j] = sum[j];
+  for (int j = 0; j < 8; ++j) warps[warp][VEC ? 8 * lane + j : lane + 32 * j] = sum[j];
   __syncthreads();
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (threadIdx.x < 128 && c < a.cols) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c < a.cols) {
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) s += warps[w][threadIdx.x];
@@ -194,15 +241,17 @@ struct Launcher {
 
   void split(SplitArgs a) {
     if (!ok() || a.rows == 0) return;
-    const unsigned cols = static_cast<unsigned>((a.cols + 127) / 128);
-    // about four blocks an SM; of column sums, as many as the scratch takes
-    int64_t per = std::max<int64_t>(8, up((a.rows * cols + 4 * c.num_sms - 1) / (4 * c.num_sms), 8));
+    const unsigned cols = static_cast<unsigned>((a.cols + 255) / 256);
+    // about six blocks an SM; of column sums, as many as the scratch takes
+    int64_t per = std::max<int64_t>(8, up((a.rows * cols + 6 * c.num_sms - 1) / (6 * c.num_sms), 8));
     per = std::max(per, (a.rows + 65534) / 65535);
     if (a.sums != nullptr) per = std::max(per, (a.rows * a.cols * 4 + kStepScratchBytes / 2 - 1) / (kStepScratchBytes / 2));
     per = std::min(per, up(a.rows, 8));
     a.rows_per_block = static_cast<int>(per);
     const int64_t blocks = (a.rows + per - 1) / per;
-    launch({dim3(cols, static_cast<unsigned>(blocks)), 256}, linear_split_kernel, a);
+    const bool vec = a.cols % 8 == 0 && rows_of_8(a.src, a.ld_src, a.src_f32 ? DSPARK_F32 : DSPARK_BF16) &&
+                     (a.act == DSPARK_ACT_NONE || rows_of_8(a.pre, a.ld_pre, a.pre_f32 ? DSPARK_F32 : DSPARK_BF16));
+    launch({dim3(cols, static_cast<unsigned>(blocks)), 256}, vec ? linear_split_kernel<true> : linear_split_kernel<false>, a);
     sum_blocks = static_cast<int>(blocks);
   }
   int sum_blocks = 0;  // of the last split()

@@ -127,14 +127,20 @@ __device__ __forceinline__ float ld_shared(uint32_t p) {
   return v;
 }
 
-__device__ __forceinline__ float load_as(const void* p, int f32, int64_t i) {
-  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-__device__ __forceinline__ void store_as(void* p, int f32, int64_t i, float v) {
+// f with a pointer of the elements' type: one branch for many loads, which else would wait for one another.
+template <typename F>
+__device__ __forceinline__ void with_type(const void* p, int f32, F f) {
   if (f32)
-    static_cast<float*>(p)[i] = v;
+    f(static_cast<const float*>(p));
   else
-    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    f(static_cast<const __nv_bfloat16*>(p));
+}
+template <typename F>
+__device__ __forceinline__ void with_type(void* p, int f32, F f) {
+  if (f32)
+    f(static_cast<float*>(p));
+  else
+    f(static_cast<__nv_bfloat16*>(p));
 }
 
 // 32 accumulators of this lane's row with the bias of their columns (lane j holds column j's) added,
@@ -151,14 +157,17 @@ __device__ __forceinline__ void epi_put32(const float (&v)[32], uint32_t line) {
                  __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
 }
 __device__ __forceinline__ void epi_act(int act, uint32_t line) {
-#pragma unroll 1
-  for (int u = 0; u < 8; ++u) {
-    const uint4 w = ld_shared_v4(line ^ (u << 4));
-    st_shared_v4(line ^ (u << 4), __float_as_uint(act_value(act, __uint_as_float(w.x))),
-                 __float_as_uint(act_value(act, __uint_as_float(w.y))),
-                 __float_as_uint(act_value(act, __uint_as_float(w.z))),
-                 __float_as_uint(act_value(act, __uint_as_float(w.w))));
-  }
+  with_act(act, [&](auto a) {
+    constexpr int kAct = decltype(a)::value;
+#pragma unroll 2
+    for (int u = 0; u < 8; ++u) {
+      const uint4 w = ld_shared_v4(line ^ (u << 4));
+      st_shared_v4(line ^ (u << 4), __float_as_uint(act_value<kAct>(__uint_as_float(w.x))),
+                   __float_as_uint(act_value<kAct>(__uint_as_float(w.y))),
+                   __float_as_uint(act_value<kAct>(__uint_as_float(w.z))),
+                   __float_as_uint(act_value<kAct>(__uint_as_float(w.w))));
+    }
+  });
 }
 __device__ __forceinline__ void epi_get32(float (&v)[32], uint32_t line) {
 #pragma unroll
@@ -573,9 +582,14 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
             const bool in = cc + lane < g.J;
             float r[32];  // of column `lane`, a row each
             if (has_res) {
-              const int64_t at = row0 * g.ld_res + cc + lane;
+              with_type(g.residual, g.res_f32, [&](auto p) {
+                p += row0 * g.ld_res + cc + lane;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) r[k] = in && k < rows ? load_as(g.residual, g.res_f32, at + k * g.ld_res) : 0.f;
+                for (int k = 0; k < 32; ++k) {
+                  r[k] = in && k < rows ? load1(p) : 0.f;
+                  p += g.ld_res;
+                }
+              });
             }
             tmem_wait_ld();
             if (g.bias != nullptr) epi_bias(v, bias);
@@ -584,12 +598,16 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
             // now by columns: element (k, lane)
             auto put = [&](void* to, int64_t ld, bool add) {
               __syncwarp();
-              const int64_t at = sp * g.split_stride + row0 * ld + cc + lane;
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] = ld_shared(box + 128 * k + ((((lane >> 2) ^ (k & 7)) << 4) | ((lane & 3) << 2)));
+              with_type(to, g.out_f32, [&](auto p) {
+                p += sp * g.split_stride + row0 * ld + cc + lane;
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (in && k < rows) store_as(to, g.out_f32, at + k * ld, add ? v[k] + r[k] : v[k]);
+                for (int k = 0; k < 32; ++k) {
+                  if (in && k < rows) store1(p, add ? v[k] + r[k] : v[k]);
+                  p += ld;
+                }
+              });
               __syncwarp();
             };
             if (g.pre != nullptr) put(g.pre, g.ld_pre, false);
