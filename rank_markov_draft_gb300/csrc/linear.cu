@@ -100,18 +100,66 @@ struct SplitArgs {
   float* sums;  // [row blocks][cols]
 };
 
-constexpr int kSplitRows = 2;  // rows under way a thread
 
-// A warp takes 256 columns of a row: eight neighbours a lane where rows allow vectors (VEC), else every
-// 32nd.
+// Eight neighbours from an address that allows no vectors, of a matrix that ends before `last`: the
+// 16-byte pieces around them, of which the last is the next lane's first, moved into place. (Lanes that
+// have no such pieces inside the matrix read element by element; all lanes of a warp call this.)
+template <typename T>
+__device__ __forceinline__ void load8_shifted(const T* p, const T* start, const T* last, bool use, float (&v)[8]) {
+  constexpr int kOwn = sizeof(T) / 2;  // pieces of 16 bytes in eight elements
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p), piece = at & ~static_cast<uintptr_t>(15);
+  const uint32_t off = static_cast<uint32_t>(at - piece) / sizeof(T);
+  const bool whole = use && piece >= reinterpret_cast<uintptr_t>(start) &&
+                     piece + 16 * (kOwn + 1) <= reinterpret_cast<uintptr_t>(last);
+  uint32_t w[4 * kOwn + 4];
+#pragma unroll
+  for (int k = 0; k < kOwn + 1; ++k) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    // (a lane's first piece serves its neighbour too, so it is read whenever it lies inside)
+    const bool inside = piece >= reinterpret_cast<uintptr_t>(start) && piece + 16 * (k + 1) <= reinterpret_cast<uintptr_t>(last);
+    if (k < kOwn ? inside && (use || k == 0) : whole && (threadIdx.x & 31) == 31)
+      x = reinterpret_cast<const uint4*>(piece)[k];
+    w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[j], 1);
+    if ((threadIdx.x & 31) != 31) w[4 * kOwn + j] = next;
+  }
+  constexpr int kWords = 4 * kOwn + 4;
+  const uint32_t words = sizeof(T) == 4 ? off : off / 2;
+#pragma unroll
+  for (int s = 2; s > 0; s /= 2)
+    if (words & s) {
+#pragma unroll
+      for (int j = 0; j + s < kWords; ++j) w[j] = w[j + s];
+    }
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+  } else {
+    if (off & 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) widen2(w[j], v[2 * j], v[2 * j + 1]);
+  }
+  if (!whole) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = use && p + j < last ? load1(p + j) : 0.f;
+  }
+}
+
+// A warp takes 256 columns of a row, eight neighbours a lane; VEC: rows allow vectors of eight.
 template <bool VEC>
-__global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
+__global__ void __launch_bounds__(256, VEC ? 2 : 3) linear_split_kernel(SplitArgs a) {
+  constexpr int kSplitRows = VEC ? 2 : 1;  // under way a thread
   griddep_launch_dependents();
   griddep_wait();
   __shared__ float warps[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x * 256 + (VEC ? 8 * lane : lane);
-  constexpr int kStep = VEC ? 1 : 32;
+  const int c0 = blockIdx.x * 256 + 8 * lane;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_block;
   const int64_t r1 = min(a.rows, r0 + a.rows_per_block);
   float sum[8] = {};
@@ -128,11 +176,10 @@ __global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
 #pragma unroll
         for (int k = 0; k < kSplitRows; ++k) raw[k].get(v[k]);
       } else {
+        const T* const last = q + (a.rows - 1) * ld + a.cols;
 #pragma unroll
         for (int k = 0; k < kSplitRows; ++k)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[k][j] = c0 + kStep * j < a.cols && r + 8 * k < r1 ? load1(q + (r + 8 * k) * ld + c0 + kStep * j) : 0.f;
+          load8_shifted(q + (r + 8 * k) * ld + c0, q, last, c0 < a.cols && r + 8 * k < r1, v[k]);
       }
     });
   };
@@ -154,17 +201,11 @@ __global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[k][j];
       for (int p = 0; p < 3 && a.part[p] != nullptr; ++p) {
-        bf16* const dst = a.part[p] + (r + 8 * k) * a.ld_dst + c0;
         float h[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = __bfloat162float(__float2bfloat16_rn(v[k][j]));
-        if constexpr (VEC) {
-          store8(dst, h);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (c0 + kStep * j < a.cols) store1(dst + kStep * j, h[j]);
-        }
+        // (rows are padded to vectors: what lies beyond the last column is not read)
+        store8(a.part[p] + (r + 8 * k) * a.ld_dst + c0, h);
         // (of an infinity or NaN nothing is left, not a NaN beside an infinity)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = isfinite(h[j]) ? v[k][j] - h[j] : 0.f;
@@ -173,7 +214,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(SplitArgs a) {
   }
   if (a.sums == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) warps[warp][VEC ? 8 * lane + j : lane + 32 * j] = sum[j];
+  for (int j = 0; j < 8; ++j) warps[warp][8 * lane + j] = sum[j];
   __syncthreads();
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c < a.cols) {
@@ -283,11 +324,14 @@ struct Launcher {
     }
     if (epi == kEpiElements)
       run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElements>, GemmShape<BN, kEpiElements>::kSmem);
-    else if (A_MN || !B_MN || epi == kEpiTma)  // (the gradients' products have no residual)
+    else if (epi == kEpiTma)
       run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiTma>, GemmShape<BN, kEpiTma>::kSmem);
-    else
-      run(linear_gemm_kernel<BN, A_MN, B_MN, !A_MN && B_MN ? kEpiResidual : kEpiTma>,
-          GemmShape<BN, !A_MN && B_MN ? kEpiResidual : kEpiTma>::kSmem);
+    if constexpr (!A_MN && B_MN) {  // (the gradients' products have no residual)
+      if (epi == kEpiResidual)
+        run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiResidual>, GemmShape<BN, kEpiResidual>::kSmem);
+      else if (epi == kEpiElementsResidual)
+        run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElementsResidual>, GemmShape<BN, kEpiElementsResidual>::kSmem);
+    }
   }
 
   // A product as it will be launched.
@@ -414,7 +458,8 @@ struct Launcher {
                                  g.residual, J, I, g.ld_res * (g.res_f32 ? 4 : 2), g.res_f32 ? 32 : 64, 32);
     }
     if (!maps && ok()) error = cudaErrorInvalidValue;
-    p.epi = !by_tma ? kEpiElements : g.residual != nullptr ? kEpiResidual : kEpiTma;
+    const bool res = g.residual != nullptr;
+    p.epi = by_tma ? (res ? kEpiResidual : kEpiTma) : res && g.res_f32 ? kEpiElementsResidual : kEpiElements;
     p.g = g;
     return p;
   }

@@ -67,15 +67,15 @@ constexpr int kGemmRestart = 8;  // stages of 64 terms
 constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
 
-// The epilogue: element by element; by TMA; by TMA with a residual that arrives a chunk ahead (in two
+// The epilogue: element by element; so with an fp32 residual, by asynchronous copies; by TMA; by TMA with a residual that arrives a chunk ahead (in two
 // slots of 8 KB a warp instead of 4 KB, for which the operands' ring gives up half its stages: as good
 // as none, since such outputs are bounded by their bytes).
-enum GemmEpilogue { kEpiElements, kEpiTma, kEpiResidual };
+enum GemmEpilogue { kEpiElements, kEpiElementsResidual, kEpiTma, kEpiResidual };
 
 template <int BN, int EPI, bool PAIR = false>
 struct GemmShape {
   static constexpr int kSlots = EPI == kEpiResidual ? 2 : 1;  // of a warp
-  static constexpr uint32_t kSlot = EPI == kEpiResidual ? 8192 : 4096;
+  static constexpr uint32_t kSlot = EPI == kEpiResidual ? 8192 : EPI == kEpiElementsResidual ? 12288 : 4096;
   static constexpr uint32_t kA = 128 * 64 * 2, kB = (PAIR ? BN / 2 : BN) * 64 * 2;
   static constexpr uint32_t kEpi = kGemmEpiWarps * kSlots * kSlot;
   static constexpr int kStages = (226 * 1024 - 1024 - 512 - kEpi) / (kA + kB) < 8
@@ -367,7 +367,8 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
     const uint64_t pol_out = gemm_policy(g.l2_out);
     const uint32_t slots = smem_addr(smem + S::kOffEpi + e * S::kSlots * S::kSlot);
     const uint32_t own = 128 * lane + ((lane & 7) << 4);  // this lane's line of a 4 KB box
-    const bool has_res = EPI == kEpiTma ? false : EPI == kEpiResidual || g.residual != nullptr;
+    constexpr bool kElements = EPI == kEpiElements || EPI == kEpiElementsResidual;
+    const bool has_res = EPI == kEpiTma ? false : EPI != kEpiElements || g.residual != nullptr;
     auto place = [&](int64_t u, int64_t& row0, int& col0) {
       const int64_t t = u % tiles;
       row0 = (t % g.tiles_i) * kRows + rank * 128 + q * 32;
@@ -402,9 +403,32 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       for (; k >= kRound; k -= kRound) u += stride;
       load_residual(u, k, slot);
     };
+    // an fp32 residual whose rows TMA cannot take: the 32 x 32 elements of half h of chunk c, each copied
+    // asynchronously by the lane that will add it
+    auto copy_residual = [&](int64_t u, int c, int h, int slot) {
+      if constexpr (EPI == kEpiElementsResidual) {
+        if (u < g.units && group < kChunks) {
+          int64_t row0;
+          int col0;
+          place(u, row0, col0);
+          const int col = col0 + 64 * c + 32 * h + lane;
+          const int rows = col < g.J ? static_cast<int>(min(static_cast<int64_t>(32), g.I - row0)) : 0;
+          const float* p = static_cast<const float*>(g.residual) + row0 * g.ld_res + col;
+          uint8_t* const to = smem + S::kOffEpi + e * S::kSlot + 4096 * (1 + slot) + 4 * lane;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (k < rows) cp_async_4(to + 128 * k, p);
+            p += g.ld_res;
+          }
+        }
+        cp_async_commit();
+      }
+    };
+    copy_residual(first, group, 0, 0);
+    copy_residual(first, group, 1, 1);
     bool ok = true;
     uint32_t i = 0, n = 0;
-    if (group < kChunks) {
+    if (EPI == kEpiResidual && group < kChunks) {
       int64_t u = first;
       int c = group;
       for (int s = 0; s < S::kSlots; ++s) {
@@ -474,12 +498,12 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
 #pragma unroll 1
       for (int c = group; c < kChunks; c += 2, ++n) {
         const int col = col0 + 64 * c, slot = n % S::kSlots;
-        if (row0 >= g.I || col >= g.J) {
+        if (!kElements && (row0 >= g.I || col >= g.J)) {
           load_later(u, c, slot);
           continue;
         }
         const uint32_t box = slots + slot * S::kSlot, line = box + own;
-        if constexpr (EPI != kEpiElements) {
+        if constexpr (!kElements) {
           if (pending >> slot & 1) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(&res_full[e * S::kSlots + slot], phases >> slot & 1, g.timeout_ns, abort_flag));
             if (!ok) break;
@@ -574,14 +598,19 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int cc = col + 32 * h;
-            if (cc >= g.J) break;
+            const int rows = static_cast<int>(min(static_cast<int64_t>(32), g.I - row0));
+            // then on to the copies of the next chunk's same half
+            auto done = [&]() { c + 2 < kRound ? copy_residual(u, c + 2, h, h) : copy_residual(u + stride, group, h, h); };
+            if (cc >= g.J || rows <= 0) {
+              done();
+              continue;
+            }
             float v[32];
             tmem_ld_x32(lane_base + b * BN + 64 * c + 32 * h, reinterpret_cast<uint32_t*>(v));
             const float bias = g.bias != nullptr && cc + lane < g.J ? __ldg(g.bias + cc + lane) : 0.f;
-            const int rows = static_cast<int>(min(static_cast<int64_t>(32), g.I - row0));
             const bool in = cc + lane < g.J;
-            float r[32];  // of column `lane`, a row each
-            if (has_res) {
+            float r[32];  // the residual of column `lane`, a row each
+            if (EPI == kEpiElements && has_res) {
               with_type(g.residual, g.res_f32, [&](auto p) {
                 p += row0 * g.ld_res + cc + lane;
 #pragma unroll
@@ -600,11 +629,21 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
               __syncwarp();
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] = ld_shared(box + 128 * k + ((((lane >> 2) ^ (k & 7)) << 4) | ((lane & 3) << 2)));
+              if (add) {
+                if constexpr (EPI == kEpiElementsResidual) {
+                  cp_async_wait_group<1>();
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) v[k] += ld_shared(box + 4096 * (1 + h) + 128 * k + 4 * lane);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) v[k] += r[k];
+                }
+              }
               with_type(to, g.out_f32, [&](auto p) {
                 p += sp * g.split_stride + row0 * ld + cc + lane;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                  if (in && k < rows) store1(p, add ? v[k] + r[k] : v[k]);
+                  if (in && k < rows) store1(p, v[k]);
                   p += ld;
                 }
               });
@@ -613,6 +652,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
             if (g.pre != nullptr) put(g.pre, g.ld_pre, false);
             if (g.act != DSPARK_ACT_NONE) epi_act(g.act, line);
             put(g.out, g.ld_out, has_res);
+            done();
           }
         }
       }
@@ -623,7 +663,8 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       *abort_flag = 1;
       record_error(g.status, kStatusTimeout);
     }
-    if constexpr (EPI != kEpiElements) {
+    if constexpr (EPI == kEpiElementsResidual) cp_async_wait_all();
+    if constexpr (!kElements) {
       // copies under way end before the block does
       for (int s = 0; s < S::kSlots; ++s)
         if (pending >> s & 1) mbar_wait(&res_full[e * S::kSlots + s], phases >> s & 1, g.timeout_ns, nullptr);
