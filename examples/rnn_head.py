@@ -5,7 +5,8 @@
 A target (an RNN head of fixed random weights over the same base logits) writes blocks; a student
 head starts from noise and is fitted to the target's top logits:
 
-    rnn_scan -> logits -> distill (loss and gradient) -> rnn_scan_grad -> Adam
+    embed, linear (gates) -> rnn_scan -> linear (logits) -> distill (loss and gradient) ->
+    linear_grad -> rnn_scan_grad -> linear_grad, embed_grad -> clip_grads -> Adam
 
 Then the student drafts new blocks (rnn_draft) and the target verifies them (verify_probs), as it
 did before the training: the accepted length is what the training is for.  Synthetic data."""
@@ -76,17 +77,19 @@ def train_step(ctx, head, target, gen, seed):
     weight = torch.exp(-torch.arange(K, device="cuda") / 4.0).expand(B, K) / (B * K)
 
     w = head.bf16()
-    e, za, zg = w["W1"][prev.long()], h @ w["Wa"], h @ w["Wg"]
+    e = binding.embed(ctx, head.w["W1"], prev, dtype=torch.bfloat16)
+    za, zg = binding.linear(ctx, h, w["Wa"])["y"], binding.linear(ctx, h, w["Wg"])["y"]
     s = binding.rnn_scan(ctx, za, zg, e)["s"]
-    logits = U + s.float() @ w["W2"].float()
+    logits = binding.linear(ctx, s, w["W2"], residual=U, dtype=torch.float32)["y"]
     out = binding.distill(ctx, logits, top.indices.int(), top.values, teacher_rest=rest,
                           row_weight=weight.contiguous(), grad=logits)  # in place of the logits
-    ds = (logits @ w["W2"].float().T).bfloat16()
-    g = binding.rnn_scan_grad(ctx, za, zg, e, s, ds)
-    rows = h.reshape(-1, D).float()
-    head.adam(dict(W1=torch.zeros_like(head.w["W1"]).index_add_(0, prev.flatten().long(), g["de"].reshape(-1, R).float()),
-                   W2=s.reshape(-1, R).float().T @ logits.view(-1, V),
-                   Wa=rows.T @ g["dza"].reshape(-1, R).float(), Wg=rows.T @ g["dzg"].reshape(-1, R).float()))
+    back = binding.linear_grad(ctx, s, w["W2"], logits)
+    g = binding.rnn_scan_grad(ctx, za, zg, e, s, back["dx"])
+    grads = dict(W1=binding.embed_grad(ctx, prev, g["de"], V), W2=back["dW"],
+                 Wa=binding.linear_grad(ctx, h, w["Wa"], g["dza"], dx=False)["dW"],
+                 Wg=binding.linear_grad(ctx, h, w["Wg"], g["dzg"], dx=False)["dW"])
+    binding.clip_grads(ctx, list(grads.values()), 1.0)
+    head.adam(grads)
     return float(out["loss"].sum())
 
 
