@@ -568,7 +568,7 @@ int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const 
  *   ids [N] int32: negative ids are padding (a row of zeros); ids >= V are reported as
  *     DSPARK_ERR_DEVICE_OOB and give zeros
  *   out [N, D] of type out_dtype, rows ld_out elements apart
- * The product is formed in fp32 and rounded once.  Any N >= 0 (< 2^31), D >= 1; V <= 2^18;
+ * The product is formed in fp32 and rounded once; out must not overlap table.  Any N >= 0 (< 2^31), D >= 1; V <= 2^18;
  * pointers aligned to their element size. */
 int dspark_embed(dspark_ctx* ctx, const void* table, int table_dtype, int64_t ld_table,
                  const int32_t* ids, int64_t N, int V, int D, float scale, void* out,
@@ -629,6 +629,7 @@ typedef enum dspark_act {
  *   y [M, N] of type y_dtype, rows ld_y apart
  *   pre [M, N] of type y_dtype, rows ld_pre apart: x W + bias, for the gradient (NULL: not
  *     written)
+ * Outputs must not overlap inputs or one another, but for y and the residual.
  * Any M >= 0 (< 2^31), 1 <= K, N <= 2^22; pointers aligned to their element size.  Equal inputs
  * give equal bits.
  * workspace: device memory of the caller, 256-byte aligned, of *workspace_bytes bytes (it must
@@ -649,8 +650,10 @@ int dspark_linear(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16
  *     apart, as dspark_linear wrote it (read only with an activation; else it may be NULL)
  *   dx [M, K] of dx_dtype, dW [K, N] of dw_dtype, dbias [N] fp32: each may be NULL (W is read
  *     only for dx, x only for dW)
- * Sizes, workspace and determinism as dspark_linear; *workspace_bytes of 0 suffices where x, W
- * and dy have 16-byte aligned rows and dy is bf16 without an activation. */
+ * Equal inputs give equal bits where the same outputs are asked for (dx and dW of a large dz share
+ * their blocks out between them).  Sizes, overlap and workspace as dspark_linear;
+ * *workspace_bytes of 0 suffices where x, W and dy have 16-byte aligned rows and dy is bf16
+ * without an activation. */
 int dspark_linear_grad(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16_t* W,
                        int64_t ld_w, const void* dy, int dy_dtype, int64_t ld_dy, int act,
                        const void* pre, int pre_dtype, int64_t ld_pre, int64_t M, int K, int N,

@@ -563,18 +563,31 @@ def dspark_clip_grads(ctx: Context, grads, max_norm, out, norm, stream=None):
     _check(code, "dspark_clip_grads")
 
 
-def _with_workspace(call, workspace, device, stream, where: str):
-    """call(address, bytes) -> status; a call that asks for more workspace gets it from torch's
-    allocator (given back when the stream's work so far is done)."""
+def _with_workspace(call, workspace, likely: int, device, stream, where: str):
+    """call(address, bytes) -> status.  Without a workspace of the caller's, `likely` bytes of one (0:
+    none) or what the call then asks for come from torch's allocator, which has them back when the
+    stream's work so far is done."""
+    def allocate(n):
+        w = torch.empty(n, dtype=torch.uint8, device=device)
+        if stream is not None:
+            w.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                            torch.cuda.ExternalStream(int(stream), device=device))
+        return w
+
+    given = workspace is not None
+    if not given and likely > 0:
+        workspace = allocate(likely)
     size = ctypes.c_int64(0 if workspace is None else workspace.numel() * workspace.element_size())
     code = call(_ptr(workspace, None, "workspace"), ctypes.byref(size))
-    if code == CAPACITY and workspace is None:
-        workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                    torch.cuda.ExternalStream(int(stream), device=device))
+    if code == CAPACITY and not given:
+        workspace = allocate(size.value)
         code = call(workspace.data_ptr(), ctypes.byref(size))
     _check(code, where)
+
+
+def _copy_bytes(rows: int, cols: int) -> int:
+    """Of a bf16 matrix with rows on 16-byte boundaries, as the linear layers copy one."""
+    return (rows * ((cols + 7) & ~7) * 2 + 255) & ~255
 
 
 def dspark_linear(ctx: Context, x, W, bias, act, residual, M, K, N, y, pre, workspace=None,
@@ -590,10 +603,15 @@ def dspark_linear(ctx: Context, x, W, bias, act, residual, M, K, N, y, pre, work
         rdt = _dtype(residual, "residual")
         pr, ld_r = _rows(residual, residual.dtype, "residual")
     pb, a, s = _ptr(bias, (torch.float32,), "bias"), _act(act), _stream(stream, ctx.device)
+    likely = 0
+    if (px or 0) & 15 or ld_x & 7:
+        likely += _copy_bytes(M, K)
+    if (pw or 0) & 15 or ld_w & 7:
+        likely += _copy_bytes(K, N)
     _with_workspace(
         lambda p, size: ctx.lib.dspark_linear(ctx.handle, px, ld_x, pw, ld_w, pb, a, pr, rdt, ld_r,
                                               M, K, N, py, dtype, ld_y, pp, ld_pre, p, size, s),
-        workspace, x.device, stream, "dspark_linear")
+        workspace, likely, x.device, stream, "dspark_linear")
 
 
 def dspark_linear_grad(ctx: Context, x, W, dy, act, pre, M, K, N, dx, dW, dbias, workspace=None,
@@ -612,11 +630,19 @@ def dspark_linear_grad(ctx: Context, x, W, dy, act, pre, M, K, N, dx, dW, dbias,
             rows.append((*_rows(t, t.dtype, name), dt))
     (pp, ld_p, pdt), (pdx, ld_dx, xdt), (pdw, ld_dw, wdt) = rows
     pb, a, s = _ptr(dbias, (torch.float32,), "dbias"), _act(act), _stream(stream, ctx.device)
+    likely = 0
+    if dW is not None and ((px or 0) & 15 or ld_x & 7):
+        likely += _copy_bytes(M, K)
+    if dx is not None and ((pw or 0) & 15 or ld_w & 7):
+        likely += _copy_bytes(K, N)
+    if (dx is not None or dW is not None) and (a or ydt == 0 or (py or 0) & 15 or ld_dy & 7):
+        fp32 = (dx is not None and xdt == 0) or (dW is not None and wdt == 0)
+        likely += (1 if not a and ydt else 3 if fp32 else 2) * _copy_bytes(M, N)
     _with_workspace(
         lambda p, size: ctx.lib.dspark_linear_grad(
             ctx.handle, px, ld_x, pw, ld_w, py, ydt, ld_dy, a, pp, pdt, ld_p, M, K, N, pdx, xdt,
             ld_dx, pdw, wdt, ld_dw, pb, p, size, s),
-        workspace, dy.device, stream, "dspark_linear_grad")
+        workspace, likely, dy.device, stream, "dspark_linear_grad")
 
 
 def dspark_markov_draft_noalloc(U, W1, W2, anchors, B, K, V, r, temperature, seed, tokens,
@@ -919,7 +945,7 @@ def embed_grad(ctx: Context, ids, de, V=None, *, scale=1.0, dtype=torch.float32,
 def grad_norm(ctx: Context, grads, stream=None) -> torch.Tensor:
     """The norm of all tensors of a list together (fp32 scalar on the device)."""
     norm = torch.empty((), dtype=torch.float32, device=torch.device("cuda", ctx.device))
-    dspark_clip_grads(ctx, grads, 0.0, None, norm, stream)
+    dspark_clip_grads(ctx, list(grads), 0.0, None, norm, stream)
     return norm
 
 
@@ -927,7 +953,8 @@ def clip_grads(ctx: Context, grads, max_norm, *, out=None, stream=None) -> torch
     """Scale a list of gradients (fp32, bf16) to a common norm of at most max_norm, in place or
     into the tensors of out; returns their norm before (fp32 scalar on the device)."""
     norm = torch.empty((), dtype=torch.float32, device=torch.device("cuda", ctx.device))
-    dspark_clip_grads(ctx, grads, max_norm, grads if out is None else out, norm, stream)
+    grads = list(grads)
+    dspark_clip_grads(ctx, grads, max_norm, grads if out is None else list(out), norm, stream)
     return norm
 
 

@@ -3,9 +3,11 @@
 // the hot path runs in this library's kernels; the host code only checks,
 // describes and enqueues.
 
+#include <algorithm>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <cuda.h>
@@ -125,6 +127,11 @@ dspark::LinearLaunch linear_launch(dspark_ctx* ctx) {
   c.opt_in = &ctx->opt_in;
   c.launches = &ctx->last_launches;
   return c;
+}
+
+// Whether an output (if any) is one of these inputs.
+bool one_of(const void* out, std::initializer_list<const void*> inputs) {
+  return out != nullptr && std::find(inputs.begin(), inputs.end(), out) != inputs.end();
 }
 
 // Whether the caller's workspace is enough; else *bytes is what the call needs.
@@ -1172,7 +1179,7 @@ int dspark_embed(dspark_ctx* ctx, const void* table, int table_dtype, int64_t ld
     return DSPARK_ERR_INVALID_ARG;
   if (N > 0 && (ids == nullptr || out == nullptr)) return DSPARK_ERR_INVALID_ARG;
   if (ld_table < D || ld_out < D) return DSPARK_ERR_INVALID_ARG;
-  if (!aligned_to(table, ts) || !aligned_to(ids, 4) || !aligned_to(out, os))
+  if (!aligned_to(table, ts) || !aligned_to(ids, 4) || !aligned_to(out, os) || out == table)
     return DSPARK_ERR_INVALID_ARG;
   if (V > (1 << 18) || N > kMost || ld_table > kMost || ld_out > kMost)
     return DSPARK_ERR_UNSUPPORTED;
@@ -1204,7 +1211,7 @@ int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int d
     return DSPARK_ERR_INVALID_ARG;
   if (N > 0 && (ids == nullptr || de == nullptr)) return DSPARK_ERR_INVALID_ARG;
   if (ld_de < D || ld_grad < D) return DSPARK_ERR_INVALID_ARG;
-  if (!aligned_to(ids, 4) || !aligned_to(de, ds) || !aligned_to(grad, gs))
+  if (!aligned_to(ids, 4) || !aligned_to(de, ds) || !aligned_to(grad, gs) || grad == de)
     return DSPARK_ERR_INVALID_ARG;
   if (V > (1 << 18) || N > dspark::kEmbedGradMaxRows || D > dspark::kEmbedGradMaxWidth || ld_de > kMost || ld_grad > kMost)
     return DSPARK_ERR_UNSUPPORTED;
@@ -1280,7 +1287,8 @@ int dspark_linear(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16
     return DSPARK_ERR_INVALID_ARG;
   if (residual != nullptr && (rs == 0 || ld_residual < N || !aligned_to(residual, rs)))
     return DSPARK_ERR_INVALID_ARG;
-  if (M > 0 && (pre == y || (residual == y && (residual_dtype != y_dtype || ld_residual != ld_y))))
+  if (M > 0 && (pre == y || (residual == y && (residual_dtype != y_dtype || ld_residual != ld_y)) ||
+                one_of(y, {x, W}) || one_of(pre, {x, W, residual})))
     return DSPARK_ERR_INVALID_ARG;
   if (!aligned_to(x, 2) || !aligned_to(W, 2) || !aligned_to(bias, 4) || !aligned_to(y, ys) ||
       !aligned_to(pre, ys) || !aligned_to(workspace, 256) || *workspace_bytes < 0)
@@ -1343,6 +1351,7 @@ int dspark_linear_grad(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const u
       (pre != nullptr && !aligned_to(pre, dtype_size(pre_dtype))) || !aligned_to(dbias, 4) ||
       !aligned_to(workspace, 256) || *workspace_bytes < 0)
     return DSPARK_ERR_INVALID_ARG;
+  if (one_of(dx, {x, W, dy, pre}) || one_of(dW, {x, W, dy, pre, dx})) return DSPARK_ERR_INVALID_ARG;
   for (int64_t ld : {M, ld_x, ld_w, ld_dy, ld_pre, ld_dx, ld_dw})
     if (ld > kMost) return DSPARK_ERR_UNSUPPORTED;
   if (K > dspark::kLinearMaxWidth || N > dspark::kLinearMaxWidth) return DSPARK_ERR_UNSUPPORTED;

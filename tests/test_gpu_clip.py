@@ -80,6 +80,15 @@ def test_shapes_and_views(dsp):
     check(dsp, grads, 0.01, binding.clip_grads(dsp, grads, 0.01, out=out), out)
 
 
+def test_any_iterable(dsp):
+    grads = make(1, [50, 60], (F32,))
+    want = float(binding.grad_norm(dsp, grads))
+    assert float(binding.grad_norm(dsp, (g for g in grads))) == want
+    mine = [g.clone() for g in grads]
+    assert float(binding.clip_grads(dsp, (g for g in mine), 0.01)) == want
+    check(dsp, grads, 0.01, binding.clip_grads(dsp, tuple(grads), 0.01, out=tuple(torch.empty_like(g) for g in grads)), mine)
+
+
 def test_no_tensors(dsp):
     assert float(binding.grad_norm(dsp, [])) == 0.0 and float(binding.clip_grads(dsp, [], 1.0)) == 0.0
     grads = [torch.zeros(100, device="cuda")]

@@ -252,14 +252,56 @@ def test_side_stream_and_graph(dsp, N):
             near(out_g[name], w, b, name)
 
 
-@pytest.mark.parametrize("backward", [False, True])
-def test_waits_that_run_out(backward):
+BOTH = [(700, 256, 50000, None, BF16), (3000, 136, 12000, None, BF16), (300, 200, 40008, "silu", BF16), (257, 64, 50008, None, F32),
+        (140, 520, 100000, "sigmoid", F32)]
+
+
+@pytest.mark.parametrize("dw_dtype", [F32, BF16])
+@pytest.mark.parametrize("M,K,N,act,dtype", BOTH)
+def test_both_products_of_a_large_gradient(dsp, M, K, N, act, dtype, dw_dtype):
+    """dz beyond what L2 keeps: both products in one launch, of one to three parts."""
+    x, W = make(M, M, K, N)
+    dy, pre = (normal(1, M, N) / M).to(dtype), normal(2, M, N).to(BF16) if act else None
+    dW = torch.full_like(W, 9.0, dtype=dw_dtype)
+    out = binding.linear_grad(dsp, x, W, dy, act=act, pre=pre, dW=dW)
+    done(dsp)
+    want = step.linear_grad(x, W, dy, act, pre)
+    near(out["dx"], *want["dx"], "dx")
+    near(dW, *want["dW"], "dW")
+    again = binding.linear_grad(dsp, x, W, dy, act=act, pre=pre, dW=torch.empty_like(dW))
+    assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dW"], dW)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,K,N", [(1000, 2000, 1000), (3000, 1500, 1400), (2000, 1024, 4096), (257, 9000, 264)])
+def test_products_that_bound_the_time(dsp, M, K, N, dtype):
+    """Many stages a tile: pairs of blocks, splits, accumulators that start again."""
+    x, W = make(M + K, M, K, N)
+    check(dsp, x, W, dtype=dtype, bias=normal(5, N), act="sigmoid")
+    check_grad(dsp, x, W, normal(9, M, N).to(BF16), dx_dtype=dtype)
+
+
+def test_rows_wherever_they_lie_give_equal_bits(dsp):
+    for M, K, N in ((1000, 2000, 1000), (520, 256, 3000)):
+        x, W = make(1, M, K, N)
+        want = binding.linear(dsp, x, W, dtype=F32)["y"]
+        out = wide(torch.zeros(M, N, device="cuda"), 1)[1]
+        binding.linear(dsp, wide(x, 3, 1)[1], wide(W, 5, 2)[1], out=out)
+        done(dsp)
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("cta", [0, 1, 100])
+@pytest.mark.parametrize("backward,N", [(False, 512), (True, 512), (True, 50000)])
+def test_waits_that_run_out(backward, N, cta):
     """A block that loads nothing: its waits end, the status says so, and the context works again."""
-    x, W = make(1, 400, 128, 512)
+    if N == 512 and cta == 100:
+        pytest.skip("fewer blocks")
+    x, W = make(1, 700, 128, N)
     with binding.Context(0, B_max=1, V_max=4096, K_max=1) as ctx:
-        ctx.debug_set(cta=1, timeout_ms=20)
+        ctx.debug_set(cta=cta, timeout_ms=20)
         if backward:
-            binding.linear_grad(ctx, x, W, normal(2, 400, 512).to(BF16))
+            binding.linear_grad(ctx, x, W, normal(2, 700, N).to(BF16))
         else:
             binding.linear(ctx, x, W)
         torch.cuda.synchronize()
@@ -268,4 +310,8 @@ def test_waits_that_run_out(backward):
             binding.linear(ctx, x, W)
         ctx.reset()
         check(ctx, x, W)
-        check_grad(ctx, x, W, normal(2, 400, 512).to(BF16))
+        dy = normal(2, 700, N).to(BF16)
+        out, want = binding.linear_grad(ctx, x, W, dy), step.linear_grad(x, W, dy)
+        done(ctx)
+        near(out["dx"], *want["dx"])
+        near(out["dW"], *want["dW"])

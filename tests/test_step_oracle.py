@@ -67,12 +67,12 @@ def lib():
 
 
 def test_embed_argument_checks(lib):
-    def f(table=GOOD, tt=0, ldt=8, ids=GOOD, N=4, V=100, D=8, out=GOOD, ot=1, ldo=8):
+    def f(table=GOOD, tt=0, ldt=8, ids=GOOD, N=4, V=100, D=8, out=P(0x2000), ot=1, ldo=8):
         return lib.dspark_embed(None, table, tt, ldt, ids, N, V, D, 1.0, out, ot, ldo, None)
 
     assert f() == E.INVALID_ARG  # valid arguments, no context
     for bad in (dict(table=None), dict(tt=2), dict(ot=-1), dict(ids=None), dict(out=None), dict(N=-1), dict(V=0), dict(D=0),
-                dict(ldt=7), dict(ldo=7), dict(table=ODD), dict(ids=P(0x1002)), dict(out=ODD)):
+                dict(ldt=7), dict(ldo=7), dict(table=ODD), dict(ids=P(0x1002)), dict(out=ODD), dict(out=P(0x1000))):
         assert f(**bad) == E.INVALID_ARG, bad
     for bad in (dict(V=(1 << 18) + 1), dict(N=BIG), dict(ldt=BIG), dict(ldo=BIG)):
         assert f(**bad) == E.UNSUPPORTED, bad
@@ -80,12 +80,12 @@ def test_embed_argument_checks(lib):
 
 
 def test_embed_grad_argument_checks(lib):
-    def f(ids=GOOD, de=GOOD, dt=1, ld=8, N=4, V=100, D=8, grad=GOOD, gt=0, ldg=8):
+    def f(ids=GOOD, de=GOOD, dt=1, ld=8, N=4, V=100, D=8, grad=P(0x2000), gt=0, ldg=8):
         return lib.dspark_embed_grad(None, ids, de, dt, ld, N, V, D, 1.0, 0, grad, gt, ldg, None)
 
     assert f() == E.INVALID_ARG
     for bad in (dict(ids=None), dict(de=None), dict(dt=2), dict(ld=7), dict(N=-1), dict(V=0), dict(D=0), dict(grad=None),
-                dict(gt=2), dict(ldg=7), dict(de=ODD), dict(grad=P(0x1002))):
+                dict(gt=2), dict(ldg=7), dict(de=ODD), dict(grad=P(0x1002)), dict(grad=P(0x1000))):
         assert f(**bad) == E.INVALID_ARG, bad
     for bad in (dict(N=(1 << 20) + 1), dict(V=(1 << 18) + 1), dict(D=(1 << 16) + 1, ld=1 << 17, ldg=1 << 17), dict(ld=BIG),
                 dict(ldg=BIG)):
@@ -106,7 +106,7 @@ def test_clip_argument_checks(lib):
 
 
 def test_linear_argument_checks(lib):
-    def f(x=GOOD, ldx=8, W=GOOD, ldw=16, bias=None, act=0, res=None, rt=0, ldr=16, M=4, K=8, N=16, y=P(0x2000), yt=0, ldy=16,
+    def f(x=GOOD, ldx=8, W=P(0x5000), ldw=16, bias=None, act=0, res=None, rt=0, ldr=16, M=4, K=8, N=16, y=P(0x2000), yt=0, ldy=16,
           pre=None, ldp=16, ws=None, size=0, sized=True):
         n = ctypes.c_int64(size)
         return lib.dspark_linear(None, x, ldx, W, ldw, bias, act, res, rt, ldr, M, K, N, y, yt, ldy, pre, ldp, ws,
@@ -115,7 +115,8 @@ def test_linear_argument_checks(lib):
     assert f() == E.INVALID_ARG
     for bad in (dict(x=None), dict(W=None), dict(y=None), dict(ldx=7), dict(ldw=15), dict(ldy=15), dict(act=6), dict(act=-1),
                 dict(res=GOOD, rt=2), dict(res=GOOD, ldr=15), dict(res=P(0x1002)), dict(M=-1), dict(K=0), dict(N=0), dict(yt=2),
-                dict(pre=GOOD, ldp=15), dict(pre=P(0x2000)), dict(x=ODD), dict(W=ODD), dict(bias=P(0x1002)), dict(y=P(0x1002)),
+                dict(pre=P(0x3000), ldp=15), dict(pre=P(0x2000)), dict(pre=GOOD), dict(pre=P(0x4000), res=P(0x4000)), dict(y=GOOD),
+                dict(y=P(0x5000)), dict(x=ODD), dict(W=ODD), dict(bias=P(0x1002)), dict(y=P(0x1002)),
                 dict(ws=P(0x1010), size=64), dict(size=-1), dict(sized=False), dict(res=P(0x2000), rt=1),
                 dict(res=P(0x2000), ldr=17)):
         assert f(**bad) == E.INVALID_ARG, bad
@@ -125,8 +126,8 @@ def test_linear_argument_checks(lib):
 
 
 def test_linear_grad_argument_checks(lib):
-    def f(x=GOOD, ldx=8, W=GOOD, ldw=16, dy=GOOD, dt=1, ldy=16, act=0, pre=None, pt=1, ldp=16, M=4, K=8, N=16, dx=GOOD, xt=1,
-          lddx=8, dW=GOOD, wt=0, lddw=16, db=GOOD, size=0):
+    def f(x=GOOD, ldx=8, W=P(0x2000), ldw=16, dy=P(0x3000), dt=1, ldy=16, act=0, pre=None, pt=1, ldp=16, M=4, K=8, N=16,
+          dx=P(0x4000), xt=1, lddx=8, dW=P(0x5000), wt=0, lddw=16, db=P(0x6000), size=0):
         n = ctypes.c_int64(size)
         return lib.dspark_linear_grad(None, x, ldx, W, ldw, dy, dt, ldy, act, pre, pt, ldp, M, K, N, dx, xt, lddx, dW, wt, lddw,
                                       db, None, ctypes.byref(n), None)
@@ -135,7 +136,7 @@ def test_linear_grad_argument_checks(lib):
     for bad in (dict(x=None), dict(W=None), dict(dy=None), dict(dt=2), dict(ldy=15), dict(act=6), dict(act=1), dict(act=1, pre=ODD),
                 dict(act=1, pre=GOOD, ldp=15), dict(act=1, pre=GOOD, pt=2), dict(M=-1), dict(K=0), dict(N=0), dict(xt=2),
                 dict(lddx=7), dict(wt=2), dict(lddw=15), dict(ldx=7), dict(ldw=15), dict(db=P(0x1002)), dict(dx=ODD), dict(size=-1),
-                dict(dx=None, dW=None, db=None)):
+                dict(dx=None, dW=None, db=None), dict(dx=P(0x3000)), dict(dx=GOOD), dict(dW=P(0x2000)), dict(dW=P(0x4000))):
         assert f(**bad) == E.INVALID_ARG, bad
     for bad in (dict(M=BIG), dict(ldy=BIG), dict(lddx=BIG)):
         assert f(**bad) == E.UNSUPPORTED, bad
