@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_zeros_kernel(SortArgs a) {
 }
 
 // ------------------------------------------------------------------ sums
-constexpr int kSumThreads = 256, kSumBlocks = 4;  // of an SM
-// Rows under way a group, by asynchronous copies (VEC; 32 KB of shared memory a block): registers
+constexpr int kSumThreads = 512, kSumBlocks = 2;  // of an SM
+// Rows under way a group, by asynchronous copies (VEC; 64 KB of shared memory a block): registers
 // would hold as many, but the few counters a warp waits on make it wait for later loads too.
 template <typename T>
 constexpr int kSumAhead = sizeof(T) == 2 ? 8 : 4;
