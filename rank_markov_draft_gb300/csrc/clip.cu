@@ -2,8 +2,13 @@
 //   norm = sqrt(sum g^2), out = g min(1, max_norm / (norm + 1e-6)).
 //
 // Two launches: the blocks' sums of squares, then the scaling, each of whose blocks adds those sums
-// again in their order (no atomics, so equal inputs give equal bits; a few KB from L2).  The
-// tensors' addresses are launch arguments, so a captured graph holds them and nothing is copied.
+// again in their order (no atomics, so equal inputs give equal bits; a few KB from L2). The tensors'
+// addresses are launch arguments, so a captured graph holds them and nothing is copied.
+//
+// DRAM bounds it: 320 MB are read twice and written once in 157 us (6.1 TB/s), 36 MB that L2 holds in
+// 26. Each block takes an equal stretch of all tensors, in straight loops of four vectors a thread, and
+// goes back over it from its end (chunks two ahead with a search for each one's tensor took 167 us,
+// L2 hints for what is read last 188).
 
 #include <algorithm>
 #include <type_traits>

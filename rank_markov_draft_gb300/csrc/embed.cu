@@ -1,7 +1,8 @@
 // embed.cu -- rows of an embedding table by token, scaled and converted.
 //
 // The Markov head reads W1[x_{k-1}] (DSpark explainer, "The Markov head"); in training the same
-// rows are gathered for given predecessors.
+// rows are gathered for given predecessors. Bytes bound it: 131072 rows of 256 from fp32 to bf16 take 27 us
+// (202 MB at 7.4 TB/s, common rows coming from L2), with four vectors under way a thread.
 
 #include <algorithm>
 

@@ -9,6 +9,8 @@
 //     took 42 us instead of 25, those of 65 MB 16 instead of 13), by a launch that overlaps it;
 //   sums: a group of lanes a piece, a row a group at a time, joined within the block;
 //   join: tokens that lie in several blocks.
+// 131072 rows of 256 bf16 into 151936 x 256 of fp32: 28 us for the sort, under which the zeros hide, 26 for
+// the sums (rows, sums, and the zeros on their way from L2 to DRAM: 5 to 6 TB/s), 4.5 for the join.
 
 #include <algorithm>
 
