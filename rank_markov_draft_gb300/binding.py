@@ -13,6 +13,7 @@ import ctypes
 import os
 from array import array
 from dataclasses import dataclass
+from operator import attrgetter
 from typing import Optional
 
 import torch
@@ -531,18 +532,19 @@ def dspark_embed_grad(ctx: Context, ids, de, N, V, D, scale, accumulate, grad, s
 
 def _tensor_list(ts, name: str):
     """Addresses, element counts and dtypes of a list of contiguous CUDA tensors, for C."""
-    for t in ts:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected torch.Tensors")
     try:
-        dtypes = array("i", [_DTYPE[t.dtype] for t in ts])
-    except KeyError as e:
-        raise TypeError(f"{name}: dtype {e.args[0]} not in {tuple(_DTYPE)}") from None
-    if not all([t.is_contiguous() for t in ts]):
+        dtypes = list(map(_DTYPE.get, map(attrgetter("dtype"), ts)))
+        contiguous = all(map(torch.Tensor.is_contiguous, ts))
+        pointers, numel = list(map(torch.Tensor.data_ptr, ts)), list(map(torch.Tensor.numel, ts))
+    except (AttributeError, TypeError):
+        raise TypeError(f"{name}: expected torch.Tensors") from None
+    if None in dtypes:
+        raise TypeError(f"{name}: dtype {ts[dtypes.index(None)].dtype} not in {tuple(_DTYPE)}")
+    if not contiguous:
         raise ValueError(f"{name}: must be contiguous")
-    if not all([t.is_cuda for t in ts]):
+    if not all(map(attrgetter("is_cuda"), ts)):
         raise ValueError(f"{name}: must live in CUDA device memory")
-    return array("Q", [t.data_ptr() for t in ts]), array("q", [t.numel() for t in ts]), dtypes
+    return array("Q", pointers), array("q", numel), array("i", dtypes)
 
 
 def dspark_clip_grads(ctx: Context, grads, max_norm, out, norm, stream=None):

@@ -134,6 +134,11 @@ def test_refusals(dsp):
         binding.grad_norm(dsp, [g[0].double()])
     with pytest.raises(ValueError):
         binding.grad_norm(dsp, [g[0][::2]])
+    with pytest.raises(ValueError):
+        binding.grad_norm(dsp, [g[0].cpu()])
+    for other in (None, 1.0, "g"):
+        with pytest.raises(TypeError):
+            binding.grad_norm(dsp, [g[0], other])
 
 
 def test_side_stream_graph_and_equal_bits(dsp):
