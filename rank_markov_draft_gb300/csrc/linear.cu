@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
 struct SplitArgs {
   const void *src, *pre;
   int64_t rows, ld_src, ld_pre, ld_dst;
-  int cols, src_f32, pre_f32, act, rows_per_block;
+  int cols, src_f32, pre_f32, act, rows_per_block, vec;
   bf16* part[3];
   float* sums;  // [row blocks][cols]
 };
@@ -153,11 +153,8 @@ __device__ __forceinline__ void load8_shifted(const T* p, const T* start, const 
 
 // A warp takes 256 columns of a row, eight neighbours a lane; VEC: rows allow vectors of eight.
 template <bool VEC>
-__global__ void __launch_bounds__(256, VEC ? 2 : 3) linear_split_kernel(SplitArgs a) {
+__device__ __forceinline__ void split_rows(const SplitArgs& a, float (&warps)[8][256]) {
   constexpr int kSplitRows = VEC ? 2 : 1;  // under way a thread
-  griddep_launch_dependents();
-  griddep_wait();
-  __shared__ float warps[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x * 256 + 8 * lane;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_block;
@@ -225,6 +222,19 @@ __global__ void __launch_bounds__(256, VEC ? 2 : 3) linear_split_kernel(SplitArg
   }
 }
 
+// What a call's operands need, in one launch: x, W and dz.
+struct SplitJobs {
+  SplitArgs job[3];
+};
+__global__ void __launch_bounds__(256, 2) linear_split_kernel(const __grid_constant__ SplitJobs jobs) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float warps[8][256];
+  const SplitArgs& a = jobs.job[blockIdx.z];
+  if (blockIdx.x * 256 >= a.cols || static_cast<int64_t>(blockIdx.y) * a.rows_per_block >= a.rows) return;
+  a.vec ? split_rows<true>(a, warps) : split_rows<false>(a, warps);
+}
+
 __global__ void __launch_bounds__(256) linear_sums_kernel(const float* part, int parts, int cols, float* out) {
   griddep_launch_dependents();
   griddep_wait();
@@ -280,8 +290,8 @@ struct Launcher {
     if (ok()) *c.launches += 1;
   }
 
+  // Put down for the next prepare().
   void split(SplitArgs a) {
-    if (!ok() || a.rows == 0) return;
     const unsigned cols = static_cast<unsigned>((a.cols + 255) / 256);
     // about six blocks an SM; of column sums, as many as the scratch takes
     int64_t per = std::max<int64_t>(8, up((a.rows * cols + 6 * c.num_sms - 1) / (6 * c.num_sms), 8));
@@ -289,13 +299,23 @@ struct Launcher {
     if (a.sums != nullptr) per = std::max(per, (a.rows * a.cols * 4 + kStepScratchBytes / 2 - 1) / (kStepScratchBytes / 2));
     per = std::min(per, up(a.rows, 8));
     a.rows_per_block = static_cast<int>(per);
-    const int64_t blocks = (a.rows + per - 1) / per;
-    const bool vec = a.cols % 8 == 0 && rows_of_8(a.src, a.ld_src, a.src_f32 ? DSPARK_F32 : DSPARK_BF16) &&
-                     (a.act == DSPARK_ACT_NONE || rows_of_8(a.pre, a.ld_pre, a.pre_f32 ? DSPARK_F32 : DSPARK_BF16));
-    launch({dim3(cols, static_cast<unsigned>(blocks)), 256}, vec ? linear_split_kernel<true> : linear_split_kernel<false>, a);
-    sum_blocks = static_cast<int>(blocks);
+    a.vec = a.cols % 8 == 0 && rows_of_8(a.src, a.ld_src, a.src_f32 ? DSPARK_F32 : DSPARK_BF16) &&
+            (a.act == DSPARK_ACT_NONE || rows_of_8(a.pre, a.ld_pre, a.pre_f32 ? DSPARK_F32 : DSPARK_BF16));
+    sum_blocks = static_cast<int>((a.rows + per - 1) / per);
+    split_grid.x = std::max(split_grid.x, cols);
+    split_grid.y = std::max(split_grid.y, static_cast<unsigned>(sum_blocks));
+    jobs.job[num_jobs++] = a;
   }
+  SplitJobs jobs{};
+  int num_jobs = 0;
+  dim3 split_grid{1, 1, 1};
   int sum_blocks = 0;  // of the last split()
+
+  void prepare() {
+    if (num_jobs == 0) return;
+    split_grid.z = num_jobs;
+    launch({split_grid, 256}, linear_split_kernel, jobs);
+  }
 
   // The matrix itself, or its copy with rows on 16-byte boundaries.
   Matrix rows_for_tma(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld, Workspace& ws) {
@@ -560,6 +580,7 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearLaunch& c, void* work
   Workspace ws(workspace);
   const Matrix x = l.rows_for_tma(a.x, a.M, a.K, a.ld_x, ws);
   const Matrix W = l.rows_for_tma(a.W, a.K, a.N, a.ld_w, ws);
+  l.prepare();
   GemmArgs g{};
   g.bias = a.bias;
   g.residual = a.residual;
@@ -618,9 +639,10 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, v
     }
     s.sums = a.dbias != nullptr ? c.scratch : nullptr;
     l.split(s);
-    if (a.dbias != nullptr)
-      l.launch({dim3((a.N + 255) / 256), 256}, linear_sums_kernel, c.scratch, l.sum_blocks, a.N, a.dbias);
   }
+  l.prepare();
+  if (a.dbias != nullptr)
+    l.launch({dim3((a.N + 255) / 256), 256}, linear_sums_kernel, c.scratch, l.sum_blocks, a.N, a.dbias);
   GemmArgs gx{}, gw{};
   gx.out = a.dx;
   gx.ld_out = a.ld_dx;
