@@ -67,9 +67,10 @@ constexpr int kGemmRestart = 8;  // stages of 64 terms
 constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
 
-// The epilogue: element by element; so with an fp32 residual, by asynchronous copies; by TMA; by TMA with a residual that arrives a chunk ahead (in two
-// slots of 8 KB a warp instead of 4 KB, for which the operands' ring gives up half its stages: as good
-// as none, since such outputs are bounded by their bytes).
+// The epilogue: element by element; so with an fp32 residual, by asynchronous copies; by TMA; by TMA with
+// a residual that arrives a chunk ahead (in two slots of 8 KB a warp instead of 4 KB, for which the
+// operands' ring gives up half its stages: as good as none, since such outputs are bounded by their
+// bytes).
 enum GemmEpilogue { kEpiElements, kEpiElementsResidual, kEpiTma, kEpiResidual };
 
 template <int BN, int EPI, bool PAIR = false>
