@@ -556,7 +556,10 @@ struct Launcher {
       const int64_t t = std::max(4 * ((steps_x + s - 1) / s), 5 * ((units_w + left - 1) / left * steps_w));
       if (t < best) best = t, S = s;
     }
-    if (S == 0) return false;
+    // Two launches, each split by itself, where more than 2 / 7 of the pairs' time would be waiting: 1024 x 23960
+    // of 2048 rows with sigmoid (0.76 of it) took 1219 us in one and 538 in two, 256 x 41112 of 2048 (0.06) 94
+    // and 118; they meet near 0.3.
+    if (S == 0 || 5 * best * pairs > 7 * (4 * tiles_x * steps_x + 5 * units_w * steps_w)) return false;
     Plan px = plan<false, false>(gx, dz, parts_x, &W, 1, M, static_cast<int>(K), N, S);
     Plan pw = plan<true, true>(gw, &x, 1, dz, parts_w, K, static_cast<int>(N), M, 1);
     if (!ok()) return true;
