@@ -410,6 +410,10 @@ struct Launcher {
   static bool tma(const void* p, int64_t ld, int f32) {  // rows that TMA takes
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % (f32 ? 4 : 8) == 0;
   }
+  // Rows that TMA stores: it writes whole 16 bytes, zeros into the last ones where a row ends within them.
+  static bool tma_out(const void* p, int64_t ld, int f32, int64_t width) {
+    return tma(p, ld, f32) && width % (f32 ? 4 : 8) == 0;
+  }
 
   // out = act(A B + bias) + residual, A of parts a[0..na), B of b[0..nb); the epilogue's fields of g
   // are set. pair_splits: two blocks a tile, this many splits; 0: as pays.
@@ -417,7 +421,7 @@ struct Launcher {
   Plan plan(GemmArgs g, const Matrix* a, int na, const Matrix* b, int nb, int64_t I, int J, int64_t Kc,
             int64_t pair_splits = 0) {
     Plan p;
-    bool by_tma = tma(g.out, g.ld_out, g.out_f32) && (g.residual == nullptr || tma(g.residual, g.ld_res, g.res_f32)) &&
+    bool by_tma = tma_out(g.out, g.ld_out, g.out_f32, J) && (g.residual == nullptr || tma(g.residual, g.ld_res, g.res_f32)) &&
                   (g.pre == nullptr || (tma(g.pre, g.ld_pre, g.out_f32) && g.residual == nullptr));
     g.blocks_k = (Kc + 63) / 64;
     g.steps = g.blocks_k * std::max(na, nb);
@@ -546,7 +550,7 @@ struct Launcher {
             const Matrix& x) {
     const int64_t M = x.rows, K = x.cols, N = dz[0].cols, pairs = c.num_sms / 2;
     const int64_t tiles_x = (M + 255) / 256 * ((K + 255) / 256), units_w = (K + 255) / 256 * ((N + 255) / 256);
-    if (M * N * 2 * std::max(parts_x, parts_w) < (64ll << 20) || tiles_x > pairs / 2 || !tma(gw.out, gw.ld_out, gw.out_f32)) return false;
+    if (M * N * 2 * std::max(parts_x, parts_w) < (64ll << 20) || tiles_x > pairs / 2 || !tma_out(gw.out, gw.ld_out, gw.out_f32, N)) return false;
     const int64_t steps_x = (N + 63) / 64 * parts_x, steps_w = (M + 63) / 64 * parts_w;
     // Time until the later of the two is done: a stage of dz W^T takes 0.36 us, one of x^T dz (both of its
     // operands MN-major) 0.45.

@@ -177,6 +177,47 @@ def test_residuals_of_many_tiles(dsp, M, K, N, residual, dtype):
         assert torch.equal(res, y)
 
 
+def gap(M, N, ld, dtype):
+    """A matrix with elements beside its rows and after them, and all of them."""
+    store = torch.full((M * ld + 5,), 777.0, dtype=dtype, device="cuda")
+    return store[:M * ld].view(M, ld)[:, :N], store
+
+
+def beside(store, M, N, ld):
+    kept = store.clone()
+    kept[:M * ld].view(M, ld)[:, :N] = 777
+    return bool((kept == 777).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K,N,ld", [(65, 67, 67, 72), (65, 40, 65, 68), (40, 72, 1, 8), (300, 97, 300, 304), (300, 66, 1001, 1008),
+                                      (2048, 256, 20001, 20008)])
+def test_nothing_beside_an_output(dsp, M, K, N, ld, residual, dtype):
+    """Rows on boundaries for vectors and TMA that end within one."""
+    x, W = make(1, M, K, N)
+    y, all_y = gap(M, N, ld, dtype)
+    pre, all_pre = gap(M, N, ld, dtype)
+    res = normal(3, M, N).to(dtype) if residual else None
+    want = binding.linear(dsp, x, W, residual=res, dtype=dtype, act="silu", pre=True)
+    binding.linear(dsp, x, W, residual=res, out=y, act="silu", pre=pre)
+    done(dsp)
+    assert torch.equal(y, want["y"]) and torch.equal(pre, want["pre"])
+    assert beside(all_y, M, N, ld) and beside(all_pre, M, N, ld)
+    if residual:
+        return
+    dy, ldk = normal(4, M, N).to(BF16), (K + 8) // 8 * 8
+    dx, all_dx = gap(M, K, ldk, dtype)
+    dW, all_dW = gap(K, N, ld, dtype)
+    for act, z in ((None, None), ("silu", want["pre"])):
+        binding.linear_grad(dsp, x, W, dy, act=act, pre=z, dx=dx, dW=dW)
+        done(dsp)
+        bounds = step.linear_grad(x, W, dy, act, z)
+        near(dx, *bounds["dx"], "dx")
+        near(dW, *bounds["dW"], "dW")
+        assert beside(all_dx, M, K, ldk) and beside(all_dW, K, N, ld)
+
+
 def test_logits_of_a_large_vocabulary(dsp):
     """A ragged vocabulary, more tiles than blocks; the gradients' long contraction."""
     M, K, V = 384, 256, 50003
