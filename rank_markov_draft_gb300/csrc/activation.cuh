@@ -7,16 +7,17 @@
 
 namespace dspark {
 
-// 1 / (1 + e^-z); the quick division is right to two roundings, and gives 0 where the quotient is
-// below 2^-126.
-__device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
+// 1 / (1 + e^-z) by the quick exponential, right to 2 + 1.2 |z| units in the last place of e^-z (which
+// counts where z < 0; elsewhere 1 is the larger summand), and the quick division, right to two, and 0
+// below 2^-126.  (1825 x 256 x 35840 with sigmoid takes 70 us; with expf 82.)
+__device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == DSPARK_ACT_SIGMOID) return sigmoid_of(z);
   if constexpr (ACT == DSPARK_ACT_TANH) return tanhf(z);
   if constexpr (ACT == DSPARK_ACT_RELU) return z < 0.f ? 0.f : z;  // (a NaN stays one)
-  if constexpr (ACT == DSPARK_ACT_SILU) return __fdividef(z, 1.f + expf(-z));
+  if constexpr (ACT == DSPARK_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
   if constexpr (ACT == DSPARK_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678f);
   return z;
 }

@@ -392,8 +392,10 @@ struct Launcher {
     if constexpr (!A_MN && B_MN) {  // (the gradients' products have no residual)
       if (epi == kEpiResidual)
         run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiResidual>, GemmShape<BN, kEpiResidual>::kSmem);
-      else if (epi == kEpiElementsResidual)
-        run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElementsResidual>, GemmShape<BN, kEpiElementsResidual>::kSmem);
+      else if (epi == kEpiElementsF32)
+        run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElementsF32>, GemmShape<BN, kEpiElementsF32>::kSmem);
+      else if (epi == kEpiElementsBf16)
+        run(linear_gemm_kernel<BN, A_MN, B_MN, kEpiElementsBf16>, GemmShape<BN, kEpiElementsBf16>::kSmem);
     }
   }
 
@@ -526,7 +528,7 @@ struct Launcher {
     }
     if (!maps && ok()) error = cudaErrorInvalidValue;
     const bool res = g.residual != nullptr;
-    p.epi = by_tma ? (res ? kEpiResidual : kEpiTma) : res && g.res_f32 ? kEpiElementsResidual : kEpiElements;
+    p.epi = by_tma ? (res ? kEpiResidual : kEpiTma) : res ? (g.res_f32 ? kEpiElementsF32 : kEpiElementsBf16) : kEpiElements;
     p.g = g;
     return p;
   }

@@ -67,16 +67,17 @@ constexpr int kGemmRestart = 8;  // stages of 64 terms
 constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
 
-// The epilogue: element by element; so with an fp32 residual, by asynchronous copies; by TMA; by TMA with
+// The epilogue: element by element; so with a residual, by asynchronous copies; by TMA; by TMA with
 // a residual that arrives a chunk ahead (in two slots of 8 KB a warp instead of 4 KB, for which the
 // operands' ring gives up half its stages: as good as none, since such outputs are bounded by their
 // bytes).
-enum GemmEpilogue { kEpiElements, kEpiElementsResidual, kEpiTma, kEpiResidual };
+enum GemmEpilogue { kEpiElements, kEpiElementsF32, kEpiElementsBf16, kEpiTma, kEpiResidual };
 
 template <int BN, int EPI, bool PAIR = false>
 struct GemmShape {
   static constexpr int kSlots = EPI == kEpiResidual ? 2 : 1;  // of a warp
-  static constexpr uint32_t kSlot = EPI == kEpiResidual ? 8192 : EPI == kEpiElementsResidual ? 12288 : 4096;
+  static constexpr uint32_t kResidual = 4096;  // 32 x 32 elements, bf16 rows in five pieces of 16 bytes
+  static constexpr uint32_t kSlot = EPI == kEpiResidual ? 8192 : EPI == kEpiElementsF32 || EPI == kEpiElementsBf16 ? 4096 + 2 * kResidual : 4096;
   static constexpr uint32_t kA = 128 * 64 * 2, kB = (PAIR ? BN / 2 : BN) * 64 * 2;
   static constexpr uint32_t kEpi = kGemmEpiWarps * kSlots * kSlot;
   static constexpr int kStages = (226 * 1024 - 1024 - 512 - kEpi) / (kA + kB) < 8
@@ -128,6 +129,12 @@ __device__ __forceinline__ float ld_shared(uint32_t p) {
   return v;
 }
 
+__device__ __forceinline__ float ld_shared_bf16(uint32_t p) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
 // f with a pointer of the elements' type: one branch for many loads, which else would wait for one another.
 template <typename F>
 __device__ __forceinline__ void with_type(const void* p, int f32, F f) {
@@ -169,6 +176,23 @@ __device__ __forceinline__ void epi_act(int act, uint32_t line) {
                    __float_as_uint(act_value<kAct>(__uint_as_float(w.w))));
     }
   });
+}
+// The same of values in registers, for functions of a few instructions; returns whether it was one.
+__device__ __forceinline__ bool epi_act_short(int act, float (&v)[32]) {
+  auto all = [&](auto a) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+  };
+  if (act == DSPARK_ACT_SIGMOID) {
+    all(std::integral_constant<int, DSPARK_ACT_SIGMOID>());
+  } else if (act == DSPARK_ACT_SILU) {
+    all(std::integral_constant<int, DSPARK_ACT_SILU>());
+  } else if (act == DSPARK_ACT_RELU) {
+    all(std::integral_constant<int, DSPARK_ACT_RELU>());
+  } else {
+    return act == DSPARK_ACT_NONE;
+  }
+  return true;
 }
 __device__ __forceinline__ void epi_get32(float (&v)[32], uint32_t line) {
 #pragma unroll
@@ -368,8 +392,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
     const uint64_t pol_out = gemm_policy(g.l2_out);
     const uint32_t slots = smem_addr(smem + S::kOffEpi + e * S::kSlots * S::kSlot);
     const uint32_t own = 128 * lane + ((lane & 7) << 4);  // this lane's line of a 4 KB box
-    constexpr bool kElements = EPI == kEpiElements || EPI == kEpiElementsResidual;
-    const bool has_res = EPI == kEpiTma ? false : EPI != kEpiElements || g.residual != nullptr;
+    constexpr bool kCopied = EPI == kEpiElementsF32 || EPI == kEpiElementsBf16, kElements = EPI == kEpiElements || kCopied;
     auto place = [&](int64_t u, int64_t& row0, int& col0) {
       const int64_t t = u % tiles;
       row0 = (t % g.tiles_i) * kRows + rank * 128 + q * 32;
@@ -404,29 +427,49 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       for (; k >= kRound; k -= kRound) u += stride;
       load_residual(u, k, slot);
     };
-    // an fp32 residual whose rows TMA cannot take: the 32 x 32 elements of half h of chunk c, each copied
-    // asynchronously by the lane that will add it
+    // a residual whose rows TMA cannot take: the 32 x 32 elements of half h of chunk c, each row the pieces of
+    // 16 bytes that hold it, copied asynchronously
     auto copy_residual = [&](int64_t u, int c, int h, int slot) {
-      if constexpr (EPI == kEpiElementsResidual) {
+      if constexpr (kCopied) {
         if (u < g.units && group < kChunks) {
           int64_t row0;
           int col0;
           place(u, row0, col0);
-          const int col = col0 + 64 * c + 32 * h + lane;
-          const int rows = col < g.J ? static_cast<int>(min(static_cast<int64_t>(32), g.I - row0)) : 0;
-          const float* p = static_cast<const float*>(g.residual) + row0 * g.ld_res + col;
-          uint8_t* const to = smem + S::kOffEpi + e * S::kSlot + 4096 * (1 + slot) + 4 * lane;
+          const int cc = col0 + 64 * c + 32 * h, cols = min(32, g.J - cc);
+          const int rows = cols > 0 ? static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), g.I - row0))) : 0;
+          uint8_t* const to = smem + S::kOffEpi + e * S::kSlot + 4096 + S::kResidual * slot;
+          if constexpr (EPI == kEpiElementsF32) {
+            const float* p = static_cast<const float*>(g.residual) + row0 * g.ld_res + cc + lane;
+            const int mine = lane < cols ? rows : 0;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (k < rows) cp_async_4(to + 128 * k, p);
-            p += g.ld_res;
+            for (int k = 0; k < 32; ++k) {
+              if (k < mine) cp_async_4(to + 128 * k + 4 * lane, p);
+              p += g.ld_res;
+            }
+          } else {
+            const auto start = reinterpret_cast<uintptr_t>(g.residual);
+            const uintptr_t corner = start + 2 * (row0 * g.ld_res + cc);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+              const int k = (32 * i + lane) / 5, piece = (32 * i + lane) % 5;
+              const uintptr_t row = corner + 2 * k * g.ld_res, end = row + 2 * cols;
+              const uintptr_t from = (row & ~static_cast<uintptr_t>(15)) + 16 * piece;
+              if (k >= rows || from >= end) continue;
+              uint8_t* const at = to + 16 * (5 * k + piece);
+              if (from >= start) {
+                cp_async_16_zfill(at, reinterpret_cast<const void*>(from), static_cast<int>(min(end - from, static_cast<uintptr_t>(16))));
+              } else {  // (nothing before the first element is touched)
+                for (uintptr_t f = start; f < min(end, from + 16); f += 2)
+                  *reinterpret_cast<__nv_bfloat16*>(at + (f - from)) = *reinterpret_cast<const __nv_bfloat16*>(f);
+              }
+            }
           }
         }
         cp_async_commit();
       }
     };
-    copy_residual(first, group, 0, 0);
-    copy_residual(first, group, 1, 1);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) copy_residual(first, group, h, h);
     bool ok = true;
     uint32_t i = 0, n = 0;
     if (EPI == kEpiResidual && group < kChunks) {
@@ -548,7 +591,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
               }
               tmem_wait_ld();
               if (g.bias != nullptr) epi_bias(v, bias);
-              if (last && g.act != DSPARK_ACT_NONE) {
+              if (last && !epi_act_short(g.act, v)) {
                 // (the slot's one box may hold the first half's bf16 outputs: they are kept meanwhile)
                 uint4 keep[EPI == kEpiResidual ? 1 : 4];
                 if constexpr (EPI != kEpiResidual) {
@@ -600,60 +643,54 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
           for (int h = 0; h < 2; ++h) {
             const int cc = col + 32 * h;
             const int rows = static_cast<int>(min(static_cast<int64_t>(32), g.I - row0));
+            if (cc < g.J && rows > 0) {
+              float v[32];
+              tmem_ld_x32(lane_base + b * BN + 64 * c + 32 * h, reinterpret_cast<uint32_t*>(v));
+              const float bias = g.bias != nullptr && cc + lane < g.J ? __ldg(g.bias + cc + lane) : 0.f;
+              const bool in = cc + lane < g.J;
+              tmem_wait_ld();
+              if (g.bias != nullptr) epi_bias(v, bias);
+              __syncwarp();
+              epi_put32(v, line);
+              // now by columns: element (k, lane)
+              auto put = [&](void* to, int64_t ld, bool last) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = ld_shared(box + 128 * k + ((((lane >> 2) ^ (k & 7)) << 4) | ((lane & 3) << 2)));
+                if (last) epi_act_short(g.act, v);
+                if constexpr (kCopied) {
+                  if (last) {
+                    cp_async_wait_group<1>();
+                    __syncwarp();
+                    const uint32_t from = box + 4096 + S::kResidual * h;
+                    if constexpr (EPI == kEpiElementsF32) {
+#pragma unroll
+                      for (int k = 0; k < 32; ++k) v[k] += ld_shared(from + 128 * k + 4 * lane);
+                    } else {
+                      const auto row = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(g.residual) + 2 * (row0 * g.ld_res + cc));
+                      const uint32_t pitch = 2 * static_cast<uint32_t>(g.ld_res);
+#pragma unroll
+                      for (int k = 0; k < 32; ++k) v[k] += ld_shared_bf16(from + 80 * k + (row + k * pitch & 15) + 2 * lane);
+                    }
+                  }
+                }
+                with_type(to, g.out_f32, [&](auto p) {
+                  p += sp * g.split_stride + row0 * ld + cc + lane;
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) {
+                    if (in && k < rows) store1(p, v[k]);
+                    p += ld;
+                  }
+                });
+                __syncwarp();
+              };
+              if (g.pre != nullptr) put(g.pre, g.ld_pre, false);
+              if (g.act == DSPARK_ACT_TANH || g.act == DSPARK_ACT_GELU) epi_act(g.act, line);
+              put(g.out, g.ld_out, true);
+            }
             // then on to the copies of the next chunk's same half
-            auto done = [&]() { c + 2 < kRound ? copy_residual(u, c + 2, h, h) : copy_residual(u + stride, group, h, h); };
-            if (cc >= g.J || rows <= 0) {
-              done();
-              continue;
-            }
-            float v[32];
-            tmem_ld_x32(lane_base + b * BN + 64 * c + 32 * h, reinterpret_cast<uint32_t*>(v));
-            const float bias = g.bias != nullptr && cc + lane < g.J ? __ldg(g.bias + cc + lane) : 0.f;
-            const bool in = cc + lane < g.J;
-            float r[32];  // the residual of column `lane`, a row each
-            if (EPI == kEpiElements && has_res) {
-              with_type(g.residual, g.res_f32, [&](auto p) {
-                p += row0 * g.ld_res + cc + lane;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  r[k] = in && k < rows ? load1(p) : 0.f;
-                  p += g.ld_res;
-                }
-              });
-            }
-            tmem_wait_ld();
-            if (g.bias != nullptr) epi_bias(v, bias);
-            __syncwarp();
-            epi_put32(v, line);
-            // now by columns: element (k, lane)
-            auto put = [&](void* to, int64_t ld, bool add) {
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = ld_shared(box + 128 * k + ((((lane >> 2) ^ (k & 7)) << 4) | ((lane & 3) << 2)));
-              if (add) {
-                if constexpr (EPI == kEpiElementsResidual) {
-                  cp_async_wait_group<1>();
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) v[k] += ld_shared(box + 4096 * (1 + h) + 128 * k + 4 * lane);
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) v[k] += r[k];
-                }
-              }
-              with_type(to, g.out_f32, [&](auto p) {
-                p += sp * g.split_stride + row0 * ld + cc + lane;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  if (in && k < rows) store1(p, v[k]);
-                  p += ld;
-                }
-              });
-              __syncwarp();
-            };
-            if (g.pre != nullptr) put(g.pre, g.ld_pre, false);
-            if (g.act != DSPARK_ACT_NONE) epi_act(g.act, line);
-            put(g.out, g.ld_out, has_res);
-            done();
+            const bool here = c + 2 < kRound;
+            copy_residual(here ? u : u + stride, here ? c + 2 : group, h, h);
           }
         }
       }
@@ -664,7 +701,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       *abort_flag = 1;
       record_error(g.status, kStatusTimeout);
     }
-    if constexpr (EPI == kEpiElementsResidual) cp_async_wait_all();
+    if constexpr (kCopied) cp_async_wait_all();
     if constexpr (!kElements) {
       // copies under way end before the block does
       for (int s = 0; s < S::kSlots; ++s)

@@ -218,6 +218,26 @@ def test_nothing_beside_an_output(dsp, M, K, N, ld, residual, dtype):
         assert beside(all_dx, M, K, ldk) and beside(all_dW, K, N, ld)
 
 
+@pytest.mark.parametrize("act", [None, "sigmoid", "gelu"])
+@pytest.mark.parametrize("residual", [F32, BF16])
+@pytest.mark.parametrize("first", [0, 1, 2, 3, 7])
+@pytest.mark.parametrize("M,N,ld", [(1, 1, 1), (2, 1, 3), (33, 31, 31), (130, 33, 34), (65, 67, 68), (129, 97, 101), (3, 1000, 1001), (300, 64, 65)])
+def test_residuals_at_any_address(dsp, M, N, ld, first, residual, act):
+    """Rows that begin within a word, with values beside them that must not count (the largest there are)."""
+    x, W = make(M + N, M, 40, N)
+    store = torch.full((first + M * ld + 5,), torch.finfo(residual).max, dtype=residual, device="cuda")
+    res = store[first:first + M * ld].view(M, ld)[:, :N]
+    res.copy_(3 * normal(3, M, N))
+    check(dsp, x, W, residual=res, act=act)
+    kept = store.clone()
+    y = binding.linear(dsp, x, W, residual=res, dtype=residual, act=act)["y"]
+    assert binding.linear(dsp, x, W, residual=res, out=res, act=act)["y"] is res
+    done(dsp)
+    assert torch.equal(res, y)
+    res.copy_(kept[first:first + M * ld].view(M, ld)[:, :N])
+    assert torch.equal(store, kept)
+
+
 def test_logits_of_a_large_vocabulary(dsp):
     """A ragged vocabulary, more tiles than blocks; the gradients' long contraction."""
     M, K, V = 384, 256, 50003
