@@ -151,9 +151,9 @@ __device__ __forceinline__ void with_type(void* p, int f32, F f) {
     f(static_cast<__nv_bfloat16*>(p));
 }
 
-// 32 accumulators of this lane's row with the bias of their columns (lane j holds column j's) added,
-// and, in 128 bytes of shared memory of the lane's own at `line` (16-byte units in place u ^ (lane & 7)),
-// the activation: there one copy of the functions' code serves every column.
+// 32 accumulators of this lane's row: the bias of their columns (lane j holds column j's) added, to and
+// from 128 bytes of shared memory of the lane's own at `line` (16-byte units in place u ^ (lane & 7)), and
+// the activation.
 __device__ __forceinline__ void epi_bias(float (&v)[32], float bias) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xFFFFFFFFu, bias, j);
@@ -164,35 +164,33 @@ __device__ __forceinline__ void epi_put32(const float (&v)[32], uint32_t line) {
     st_shared_v4(line ^ (u << 4), __float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
                  __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
 }
-__device__ __forceinline__ void epi_act(int act, uint32_t line) {
-  with_act(act, [&](auto a) {
-    constexpr int kAct = decltype(a)::value;
-#pragma unroll 2
-    for (int u = 0; u < 8; ++u) {
-      const uint4 w = ld_shared_v4(line ^ (u << 4));
-      st_shared_v4(line ^ (u << 4), __float_as_uint(act_value<kAct>(__uint_as_float(w.x))),
-                   __float_as_uint(act_value<kAct>(__uint_as_float(w.y))),
-                   __float_as_uint(act_value<kAct>(__uint_as_float(w.z))),
-                   __float_as_uint(act_value<kAct>(__uint_as_float(w.w))));
-    }
-  });
-}
-// The same of values in registers, for functions of a few instructions; returns whether it was one.
-__device__ __forceinline__ bool epi_act_short(int act, float (&v)[32]) {
+// The activation in registers: 1825 x 256 x 35840 takes 70 to 76 us with sigmoid and 85 with tanh against 56
+// without (by a loop over the line 97 and 107).  GELU, of many more instructions, is such a loop, for one
+// copy of its code: 32 of them cost every kernel registers and gained nothing (182 to 188 us).
+__device__ __forceinline__ void epi_act(int act, float (&v)[32]) {
   auto all = [&](auto a) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
   };
   if (act == DSPARK_ACT_SIGMOID) {
     all(std::integral_constant<int, DSPARK_ACT_SIGMOID>());
-  } else if (act == DSPARK_ACT_SILU) {
-    all(std::integral_constant<int, DSPARK_ACT_SILU>());
+  } else if (act == DSPARK_ACT_TANH) {
+    all(std::integral_constant<int, DSPARK_ACT_TANH>());
   } else if (act == DSPARK_ACT_RELU) {
     all(std::integral_constant<int, DSPARK_ACT_RELU>());
-  } else {
-    return act == DSPARK_ACT_NONE;
+  } else if (act == DSPARK_ACT_SILU) {
+    all(std::integral_constant<int, DSPARK_ACT_SILU>());
   }
-  return true;
+}
+__device__ __forceinline__ void epi_gelu(uint32_t line) {
+#pragma unroll 2
+  for (int u = 0; u < 8; ++u) {
+    const uint4 w = ld_shared_v4(line ^ (u << 4));
+    st_shared_v4(line ^ (u << 4), __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.x))),
+                 __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.y))),
+                 __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.z))),
+                 __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.w))));
+  }
 }
 __device__ __forceinline__ void epi_get32(float (&v)[32], uint32_t line) {
 #pragma unroll
@@ -591,7 +589,8 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
               }
               tmem_wait_ld();
               if (g.bias != nullptr) epi_bias(v, bias);
-              if (last && !epi_act_short(g.act, v)) {
+              if (last) epi_act(g.act, v);
+              if (last && g.act == DSPARK_ACT_GELU) {
                 // (the slot's one box may hold the first half's bf16 outputs: they are kept meanwhile)
                 uint4 keep[EPI == kEpiResidual ? 1 : 4];
                 if constexpr (EPI != kEpiResidual) {
@@ -599,7 +598,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
                   for (int u8 = 0; u8 < 4; ++u8) keep[u8] = ld_shared_v4(line ^ (u8 << 4));
                 }
                 epi_put32(v, half);
-                epi_act(g.act, half);
+                epi_gelu(half);
                 epi_get32(v, half);
                 if constexpr (EPI != kEpiResidual) {
 #pragma unroll
@@ -657,7 +656,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = ld_shared(box + 128 * k + ((((lane >> 2) ^ (k & 7)) << 4) | ((lane & 3) << 2)));
-                if (last) epi_act_short(g.act, v);
+                if (last) epi_act(g.act, v);
                 if constexpr (kCopied) {
                   if (last) {
                     cp_async_wait_group<1>();
@@ -685,7 +684,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
                 __syncwarp();
               };
               if (g.pre != nullptr) put(g.pre, g.ld_pre, false);
-              if (g.act == DSPARK_ACT_TANH || g.act == DSPARK_ACT_GELU) epi_act(g.act, line);
+              if (g.act == DSPARK_ACT_GELU) epi_gelu(line);
               put(g.out, g.ld_out, true);
             }
             // then on to the copies of the next chunk's same half
