@@ -351,6 +351,20 @@ def test_both_products_of_a_large_gradient(dsp, M, K, N, act, dtype, dw_dtype):
     assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dW"], dW)
 
 
+@pytest.mark.parametrize("M,K,N,act", [(1100, 64, 31080, None), (1100, 130, 31240, None), (700, 65, 48008, None), (2048, 60, 17000, None),
+                                       (2048, 1024, 8360, "sigmoid"), (3000, 256, 5001, "tanh"), (5000, 64, 120, "relu")])
+def test_gradients_of_tiles_that_reach_beyond(dsp, M, K, N, act):
+    """Tiles of which whole boxes lie outside, in one launch or two, and the column sums of many parts."""
+    x, W = make(M, M, K, N)
+    dy, pre = (normal(1, M, N) / M).to(BF16), normal(2, M, N).to(BF16) if act else None
+    out = binding.linear_grad(dsp, x, W, dy, act=act, pre=pre, dbias=True)
+    done(dsp)
+    for name, (want, bound) in step.linear_grad(x, W, dy, act, pre).items():
+        near(out[name], want, bound, name)
+    again = binding.linear_grad(dsp, x, W, dy, act=act, pre=pre, dbias=True)
+    assert all(torch.equal(again[name], out[name]) for name in out)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("M,K,N", [(1000, 2000, 1000), (3000, 1500, 1400), (2000, 1024, 4096), (257, 9000, 264)])
 def test_products_that_bound_the_time(dsp, M, K, N, dtype):
