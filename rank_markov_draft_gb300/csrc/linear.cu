@@ -479,7 +479,6 @@ struct Launcher {
     g.tiles_j = (J + p.BN - 1) / p.BN;
     g.splits = static_cast<int>(p.S);
     g.streams = 1;
-    g.restart = g.out_f32 ? kGemmRestart : g.steps;
     g.per_split = (g.steps + p.S - 1) / p.S;
     g.units = g.tiles_i * g.tiles_j * p.S;
     g.a_parts = na;

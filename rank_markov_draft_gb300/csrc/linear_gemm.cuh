@@ -17,9 +17,13 @@
 // An operand may come in up to three parts, added up like further terms: A = A_0 + A_1 + A_2.
 //
 // The accumulator cuts what a sum of fp32 would round, so that a long sum of terms drifts (2e-6 of itself
-// over 2048 terms, 2e-5 over 50000). For fp32 outputs it starts again every 512 terms, and the epilogue's
-// threads add up what it held, rounded, in registers: 5e-7 at any length, a sum of fp32 in order gives
-// 4e-7 to 8e-7. (Every 256 terms gave 2.4e-7, but the logits' gradients then took 287 us instead of 213.)
+// over 2048 terms, 2e-5 over 50000). So it starts again every 512 terms, and the epilogue's threads add up
+// what it held, rounded, in registers: 5e-7 at any length, a sum of fp32 in order gives 4e-7 to 8e-7.
+// (Every 256 terms gave 2.4e-7, but the logits' gradients then took 287 us instead of 221.)  bf16 outputs
+// need it too: of the logits' dx, 17000 terms a block, 1.8% of the elements lay a step beside the nearest
+// bf16 number without, 0.04% with it (0.11% where fp32 sums are taken in order).  It costs them 216 -> 221 us
+// there, and 166 -> 184 where a tile's start waits for the one before (4096 x 8192 x 4096); every 1024 terms
+// 175, and twice as many elements beside.
 #pragma once
 
 #include <cstdint>
@@ -49,7 +53,6 @@ struct GemmArgs {
   int tiles_j, splits;
   int64_t steps, per_split; // stages of a tile (all parts), of a unit
   int64_t blocks_k;         // stages of a part
-  int64_t restart;          // stages after which the accumulator starts again
   int streams;              // columns of tiles are taken in turn from this many stretches of them
   // the epilogue
   const float* bias;
@@ -63,7 +66,7 @@ struct GemmArgs {
   int skip_cta;             // testing: the block that loads nothing (-1: none)
 };
 
-constexpr int kGemmRestart = 8;  // stages of 64 terms
+constexpr int kGemmRestart = 8;  // stages of 64 terms after which the accumulator starts again
 constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
 
@@ -352,7 +355,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       for (int64_t u = first; u < g.units && ok; u += stride) {
         const int64_t sp = u / tiles;
         const int64_t end = min(g.steps, (sp + 1) * g.per_split);
-        for (int64_t k0 = sp * g.per_split; k0 < end && ok; k0 += g.restart, ++i) {
+        for (int64_t k0 = sp * g.per_split; k0 < end && ok; k0 += kGemmRestart, ++i) {
           const uint32_t buf = i & 1;
           if (!(PAIR ? mbar_wait_cluster(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag)
                      : mbar_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, g.timeout_ns, abort_flag))) {
@@ -361,7 +364,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
           }
           tc_fence_after();
           const uint32_t d = tmem + buf * BN;
-          for (int64_t k = k0; k < min(end, k0 + g.restart); ++k, ++n) {
+          for (int64_t k = k0; k < min(end, k0 + kGemmRestart); ++k, ++n) {
             const uint32_t s = n % kStages;
             if (!mbar_wait(&full[s], (n / kStages) & 1, g.timeout_ns, abort_flag, 20u)) {
               ok = false;
@@ -510,14 +513,14 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
       // all accumulators of the unit but the last are added up in registers, and their sum joins that one
       const int64_t end = min(g.steps, (sp + 1) * g.per_split), stages = end - sp * g.per_split;
       constexpr int kMine = BN >= 128 ? BN / 32 : 4;  // 16-column pieces of a warp
-      if (stages > g.restart) {
+      if (stages > kGemmRestart) {
         float sum[kMine][16];
 #pragma unroll
         for (int p = 0; p < kMine; ++p)
 #pragma unroll
           for (int j = 0; j < 16; ++j) sum[p][j] = 0.f;
         auto piece = [&](uint32_t b, int p) { return lane_base + b * BN + 64 * (group + 2 * (p / 4)) + 16 * (p % 4); };
-        for (int64_t left = stages;; left -= g.restart) {
+        for (int64_t left = stages;; left -= kGemmRestart) {
           const uint32_t b = i & 1;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i >> 1) & 1, g.timeout_ns, abort_flag));
           if (!ok) break;
@@ -532,7 +535,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
               for (int j = 0; j < 16; ++j) sum[p][j] += __uint_as_float(v[j]);
             }
           }
-          if (left <= g.restart) {
+          if (left <= kGemmRestart) {
             if (group < kChunks) {
 #pragma unroll
               for (int p = 0; p < kMine; ++p) tmem_st_x16(piece(b, p), sum[p]);
