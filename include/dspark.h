@@ -644,8 +644,7 @@ int dspark_linear(dspark_ctx* ctx, const uint16_t* x, int64_t ld_x, const uint16
 
 /* Gradients of dspark_linear: dz = dy act'(pre), dx = dz W^T, dW = x^T dz, dbias = sum_m dz
  * (the residual's is dy).  dz is formed in fp32 and enters the products as bf16, or, where it is
- * no bf16 number (dy of fp32, or an activation), as the sum of two for a bf16 output (2^-17 of
- * itself lost) and of three for an fp32 one (2^-25).
+ * no bf16 number (dy of fp32, or an activation), as the sum of three (2^-25 of itself lost).
  *   dy [M, N] of type dy_dtype, rows ld_dy apart; pre [M, N] of type pre_dtype, rows ld_pre
  *     apart, as dspark_linear wrote it (read only with an activation; else it may be NULL)
  *   dx [M, K] of dx_dtype, dW [K, N] of dw_dtype, dbias [N] fp32: each may be NULL (W is read

@@ -85,7 +85,7 @@ def linear(x, W, bias=None, name=None, residual=None):
 
 def linear_grad(x, W, dy, name=None, pre=None):
     """dx, dW, dbias and their bounds.  dz is right to the activation's roundings; where it is no
-    bf16 number it enters the products as two, 2^-17 of itself at most away."""
+    bf16 number it enters the products as three, 2^-25 of itself at most away."""
     d = dy.double()
     err = torch.zeros_like(d)
     if name is not None:
@@ -95,7 +95,7 @@ def linear_grad(x, W, dy, name=None, pre=None):
         d = d * k
     rest = err.clone()
     if name is not None or dy.dtype != torch.bfloat16:
-        rest = rest + d.abs() * 2.0 ** -17
+        rest = rest + d.abs() * 2.0 ** -25
     Wd, xd = W.double(), x.double()
     dx, ex = product(d, Wd.T)
     dW, ew = product(xd.T, d)

@@ -638,8 +638,7 @@ def dspark_linear_grad(ctx: Context, x, W, dy, act, pre, M, K, N, dx, dW, dbias,
     if dx is not None and ((pw or 0) & 15 or ld_w & 7):
         likely += _copy_bytes(K, N)
     if (dx is not None or dW is not None) and (a or ydt == 0 or (py or 0) & 15 or ld_dy & 7):
-        fp32 = (dx is not None and xdt == 0) or (dW is not None and wdt == 0)
-        likely += (1 if not a and ydt else 3 if fp32 else 2) * _copy_bytes(M, N)
+        likely += (1 if not a and ydt else 3) * _copy_bytes(M, N)
     _with_workspace(
         lambda p, size: ctx.lib.dspark_linear_grad(
             ctx.handle, px, ld_x, pw, ld_w, py, ydt, ld_dy, a, pp, pdt, ld_p, M, K, N, pdx, xdt,

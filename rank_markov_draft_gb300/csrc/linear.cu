@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
 }
 
 // ------------------------------------------------------------------ dz, and rows for TMA
-// src act'(pre) as the sum of up to three bf16 numbers (8 bits of it each), rows ld_dst apart, and the
+// src act'(pre) as the sum of one bf16 number or three (8 bits of it each), rows ld_dst apart, and the
 // column sums of a block's rows.  Each of them may be left out.
 struct SplitArgs {
   const void *src, *pre;
@@ -555,12 +555,11 @@ struct Launcher {
   // Both products of a gradient in one launch, where dz passes what L2 keeps between two launches
   // (64 MB of its 129, the other streams taking their share) and dz W^T is of so few tiles that splits
   // of it keep half the blocks busy. Returns whether it did.
-  bool both(const GemmArgs& gx, const GemmArgs& gw, const Matrix* dz, int parts_x, int parts_w, const Matrix& W,
-            const Matrix& x) {
+  bool both(const GemmArgs& gx, const GemmArgs& gw, const Matrix* dz, int parts, const Matrix& W, const Matrix& x) {
     const int64_t M = x.rows, K = x.cols, N = dz[0].cols, pairs = c.num_sms / 2;
     const int64_t tiles_x = (M + 255) / 256 * ((K + 255) / 256), units_w = (K + 255) / 256 * ((N + 255) / 256);
-    if (M * N * 2 * std::max(parts_x, parts_w) < (64ll << 20) || tiles_x > pairs / 2 || !tma_out(gw.out, gw.ld_out, gw.out_f32, N)) return false;
-    const int64_t steps_x = (N + 63) / 64 * parts_x, steps_w = (M + 63) / 64 * parts_w;
+    if (M * N * 2 * parts < (64ll << 20) || tiles_x > pairs / 2 || !tma_out(gw.out, gw.ld_out, gw.out_f32, N)) return false;
+    const int64_t steps_x = (N + 63) / 64 * parts, steps_w = (M + 63) / 64 * parts;
     // Time until the later of the two is done: a stage of dz W^T takes 0.36 us, one of x^T dz (both of its
     // operands MN-major) 0.45.
     int64_t S = 0, best = INT64_MAX;
@@ -573,8 +572,8 @@ struct Launcher {
     // of 2048 rows with sigmoid (0.76 of it) took 1219 us in one and 538 in two, 256 x 41112 of 2048 (0.06) 94
     // and 118; they meet near 0.3.
     if (S == 0 || 5 * best * pairs > 7 * (4 * tiles_x * steps_x + 5 * units_w * steps_w)) return false;
-    Plan px = plan<false, false>(gx, dz, parts_x, &W, 1, M, static_cast<int>(K), N, S);
-    Plan pw = plan<true, true>(gw, &x, 1, dz, parts_w, K, static_cast<int>(N), M, 1);
+    Plan px = plan<false, false>(gx, dz, parts, &W, 1, M, static_cast<int>(K), N, S);
+    Plan pw = plan<true, true>(gw, &x, 1, dz, parts, K, static_cast<int>(N), M, 1);
     if (!ok()) return true;
     GemmBoth both;
     both.dx = px.g;
@@ -603,14 +602,11 @@ struct Launcher {
 bool dz_as_it_is(const LinearGradArgs& a) {
   return a.act == DSPARK_ACT_NONE && a.dy_dtype == DSPARK_BF16 && tma_rows(a.dy, a.ld_dy);
 }
-// The bf16 numbers that stand for an element of dz in a product of this type: two (2^-17 of it lost) are
-// much finer than a bf16 output, three (2^-25) as fine as an fp32 one.
-int parts_of(const LinearGradArgs& a, int out_dtype) {
-  return a.act == DSPARK_ACT_NONE && a.dy_dtype == DSPARK_BF16 ? 1 : out_dtype == DSPARK_F32 ? 3 : 2;
-}
-int parts_of(const LinearGradArgs& a) {
-  return std::max(a.dx != nullptr ? parts_of(a, a.dx_dtype) : 0, a.dW != nullptr ? parts_of(a, a.dw_dtype) : 0);
-}
+// The bf16 numbers that stand for an element of dz: itself, or three (2^-25 of it lost, less than a rounding to
+// fp32).  Two lose 2^-17: far less than a bf16 output's own rounding, but of the odd gate's dx 0.20% of the elements
+// then lay a step beside the nearest bf16 number, with three 0.03% (fp32 throughout: 0.02%).  The third costs a bf16
+// dx its share of the time: 3885 x 256 x 12880 with sigmoid 216 -> 236 us, 2048 x 1024 x 23960 530 -> 627.
+int parts_of(const LinearGradArgs& a) { return a.act == DSPARK_ACT_NONE && a.dy_dtype == DSPARK_BF16 ? 1 : 3; }
 
 }  // namespace
 
@@ -711,10 +707,10 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const LinearLaunch& c, v
   gw.out = a.dW;
   gw.ld_out = a.ld_dw;
   gw.out_f32 = a.dw_dtype == DSPARK_F32;
-  const int parts_x = parts_of(a, a.dx_dtype), parts_w = parts_of(a, a.dw_dtype);
-  if (a.dx != nullptr && a.dW != nullptr && l.both(gx, gw, dz, parts_x, parts_w, W, x)) return l.error;
-  if (a.dx != nullptr) l.run<false, false>(l.plan<false, false>(gx, dz, parts_x, &W, 1, a.M, a.K, a.N));
-  if (a.dW != nullptr) l.run<true, true>(l.plan<true, true>(gw, &x, 1, dz, parts_w, a.K, a.N, a.M));
+  const int parts = parts_of(a);
+  if (a.dx != nullptr && a.dW != nullptr && l.both(gx, gw, dz, parts, W, x)) return l.error;
+  if (a.dx != nullptr) l.run<false, false>(l.plan<false, false>(gx, dz, parts, &W, 1, a.M, a.K, a.N));
+  if (a.dW != nullptr) l.run<true, true>(l.plan<true, true>(gw, &x, 1, dz, parts, a.K, a.N, a.M));
   return l.error;
 }
 

@@ -14,7 +14,7 @@
 // half of B's columns, so that an output costs two thirds of the reads from L2, which is what a block by
 // itself waits for (0.52 us a stage of 48 KB; its products take 0.27).
 //
-// An operand may come in up to three parts, added up like further terms: A = A_0 + A_1 + A_2.
+// An operand may come in three parts, added up like further terms: A = A_0 + A_1 + A_2.
 //
 // The accumulator cuts what a sum of fp32 would round, so that a long sum of terms drifts (2e-6 of itself
 // over 2048 terms, 2e-5 over 50000). So it starts again every 512 terms, and the epilogue's threads add up
@@ -46,7 +46,7 @@ __device__ __forceinline__ uint64_t gemm_policy(int l2) {
 struct GemmArgs {
   CUtensorMap a[3], b[3];
   CUtensorMap out_map, pre_map, res_map;  // (outputs by TMA) boxes of 32 rows x 128 bytes
-  int a_parts, b_parts;     // 1, or 2 or 3 of one of them
+  int a_parts, b_parts;     // 1, or 3 of one of them
   int64_t I;                // rows and columns of the output
   int J;
   int64_t tiles_i, units;

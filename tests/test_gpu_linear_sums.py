@@ -92,3 +92,24 @@ def test_sums_of_both_gradients_at_once(dsp, dw_dtype):
     done(dsp)
     check(g["dx"], dy.double() @ W.double().T, N)
     check(g["dW"], x.double().T @ dy.double(), M)
+
+
+# dz in 32 bits: sums of one term, three numbers of bf16 that together leave 2^-25 of it, and three cuts.
+ONE = (2 * 3 + 1) * step.EPS32
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_dy_of_32_bits_enters_the_products_whole(dsp, dtype):
+    dy = 1 + torch.rand(3000, 1, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    W = positive(2, 40, 1)
+    dx = binding.linear_grad(dsp, torch.empty(3000, 40, dtype=BF16, device="cuda"), W, dy, dW=False,
+                             dx=torch.empty(3000, 40, dtype=dtype, device="cuda"))["dx"]
+    row = dy.T.contiguous()
+    x = positive(3, 1, 40)
+    dW = binding.linear_grad(dsp, x, torch.empty(40, 3000, dtype=BF16, device="cuda"), row, dx=False,
+                             dW=torch.empty(40, 3000, dtype=dtype, device="cuda"))["dW"]
+    done(dsp)
+    for got, want in ((dx, dy.double() @ W.double().T), (dW, x.double().T @ row.double())):
+        err = (got.double() - want).abs()
+        bad = err > ONE * want + (0 if dtype == F32 else half_step(want, dtype))
+        assert not bad.any(), (int(bad.sum()), float((err / want).max()))
