@@ -214,6 +214,22 @@ def _stream(stream, device):
     return int(stream)
 
 
+def _empty(stream, shape, dtype, device, returned=True):
+    """A tensor for a call's work on `stream` (None: the current one), of memory that was last used
+    there: what torch's allocator hands out for another stream may still be in use by work queued on
+    that one, which the call's does not wait for.  The caller's current stream, which may read what is
+    `returned`, is recorded, so that the memory goes back when its work so far is done too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _check(code: int, where: str):
     if code != OK:
         raise DSparkError(code, where)
@@ -296,14 +312,14 @@ class Confidence:
     verify_len: Optional[torch.Tensor] = None  # out [B] int32
     tau: Optional[torch.Tensor] = None         # [K] fp32 STS temperatures (None: all 1)
 
-    def allocate(self, B: int, K: int):
+    def allocate(self, B: int, K: int, stream=None):
         dev = self.h.device
         if self.conf is None:
-            self.conf = torch.empty(B, K, dtype=torch.float32, device=dev)
+            self.conf = _empty(stream, (B, K), torch.float32, dev)
         if self.cumprod is None:
-            self.cumprod = torch.empty(B, K, dtype=torch.float32, device=dev)
+            self.cumprod = _empty(stream, (B, K), torch.float32, dev)
         if self.verify_len is None:
-            self.verify_len = torch.empty(B, dtype=torch.int32, device=dev)
+            self.verify_len = _empty(stream, (B,), torch.int32, dev)
         return self
 
     def struct(self) -> ConfArgs:
@@ -567,22 +583,14 @@ def dspark_clip_grads(ctx: Context, grads, max_norm, out, norm, stream=None):
 
 def _with_workspace(call, workspace, likely: int, device, stream, where: str):
     """call(address, bytes) -> status.  Without a workspace of the caller's, `likely` bytes of one (0:
-    none) or what the call then asks for come from torch's allocator, which has them back when the
-    stream's work so far is done."""
-    def allocate(n):
-        w = torch.empty(n, dtype=torch.uint8, device=device)
-        if stream is not None:
-            w.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                            torch.cuda.ExternalStream(int(stream), device=device))
-        return w
-
+    none) or what the call then asks for come from torch's allocator, for the call's stream alone."""
     given = workspace is not None
     if not given and likely > 0:
-        workspace = allocate(likely)
+        workspace = _empty(stream, (likely,), torch.uint8, device, returned=False)
     size = ctypes.c_int64(0 if workspace is None else workspace.numel() * workspace.element_size())
     code = call(_ptr(workspace, None, "workspace"), ctypes.byref(size))
     if code == CAPACITY and not given:
-        workspace = allocate(size.value)
+        workspace = _empty(stream, (size.value,), torch.uint8, device, returned=False)
         code = call(workspace.data_ptr(), ctypes.byref(size))
     _check(code, where)
 
@@ -667,6 +675,9 @@ def dspark_markov_draft_noalloc(U, W1, W2, anchors, B, K, V, r, temperature, see
 
 
 # ------------------------------------------------------ allocating wrappers
+# With `stream`, the outputs that a wrapper makes (and its workspace) are that stream's memory; they may
+# be read on it, or on the caller's current stream once that waits for it.  Inputs must be ready on it,
+# and stay in use until its work is done, as with any torch call on another stream.
 def _rank(W1) -> int:
     return 0 if W1 is None else int(W1.shape[1])
 
@@ -676,10 +687,10 @@ def markov_draft(ctx: Context, U, W1, W2, anchors, *, temperature=1.0, seed=0, h
     """Vanilla (h, Wg None) or gated draft; returns tokens and logprobs [B, K]."""
     B, K, V = U.shape
     r = _rank(W1)
-    tokens = torch.empty(B, K, dtype=torch.int32, device=U.device)
-    logprobs = torch.empty(B, K, dtype=torch.float32, device=U.device)
+    tokens = _empty(stream, (B, K), torch.int32, U.device)
+    logprobs = _empty(stream, (B, K), torch.float32, U.device)
     if conf is not None:
-        conf.allocate(B, K)
+        conf.allocate(B, K, stream)
     if h is None and Wg is None:
         dspark_markov_draft(ctx, U, W1, W2, anchors, B, K, V, r, temperature, seed, tokens,
                             logprobs, conf, stream)
@@ -695,7 +706,7 @@ def markov_draft(ctx: Context, U, W1, W2, anchors, *, temperature=1.0, seed=0, h
 def gate(ctx: Context, h, Wg, stream=None) -> torch.Tensor:
     d, r = Wg.shape
     M = h.numel() // d
-    H = torch.empty(*h.shape[:-1], r, dtype=torch.float32, device=h.device)
+    H = _empty(stream, (*h.shape[:-1], r), torch.float32, h.device)
     dspark_gate(ctx, h, Wg, M, d, r, H, stream)
     return H
 
@@ -704,9 +715,9 @@ def selector_scores(ctx: Context, U, A, Bt, anchors, *, topk=16, h=None, Wg=None
                     stream=None) -> dict:
     B, K, V = U.shape
     r = int(A.shape[1])
-    cand = torch.empty(B, K, topk, dtype=torch.int32, device=U.device)
-    cand_U = torch.empty(B, K, topk, dtype=torch.float32, device=U.device)
-    scores = torch.empty(B, K, topk, topk, dtype=torch.float32, device=U.device)
+    cand = _empty(stream, (B, K, topk), torch.int32, U.device)
+    cand_U = _empty(stream, (B, K, topk), torch.float32, U.device)
+    scores = _empty(stream, (B, K, topk, topk), torch.float32, U.device)
     d = 0 if h is None else int(h.shape[-1])
     dspark_selector_scores(ctx, U, A, Bt, anchors, h, Wg, d, B, K, V, r, topk, cand, cand_U,
                            scores, stream)
@@ -717,10 +728,10 @@ def selector_walk(ctx: Context, cand, scores, anchors, *, V, A=None, temperature
                   conf: Optional[Confidence] = None, stream=None) -> dict:
     B, K, topk = cand.shape
     r = 0 if A is None else int(A.shape[1])
-    tokens = torch.empty(B, K, dtype=torch.int32, device=cand.device)
-    logprobs = torch.empty(B, K, dtype=torch.float32, device=cand.device)
+    tokens = _empty(stream, (B, K), torch.int32, cand.device)
+    logprobs = _empty(stream, (B, K), torch.float32, cand.device)
     if conf is not None:
-        conf.allocate(B, K)
+        conf.allocate(B, K, stream)
     dspark_selector_walk(ctx, cand, scores, anchors, A, B, K, V, r, topk, temperature, seed,
                          tokens, logprobs, conf, stream)
     out = dict(tokens=tokens, logprobs=logprobs)
@@ -733,9 +744,9 @@ def confidence(ctx: Context, h, W1, anchors, tokens, w, *, V, bias=0.0, with_mar
                threshold=0.3, tau=None, stream=None) -> dict:
     B, K, d = h.shape
     r = _rank(W1) if with_markov else 0
-    conf = torch.empty(B, K, dtype=torch.float32, device=h.device)
-    cum = torch.empty(B, K, dtype=torch.float32, device=h.device)
-    vl = torch.empty(B, dtype=torch.int32, device=h.device)
+    conf = _empty(stream, (B, K), torch.float32, h.device)
+    cum = _empty(stream, (B, K), torch.float32, h.device)
+    vl = _empty(stream, (B,), torch.int32, h.device)
     dspark_confidence(ctx, h, W1 if with_markov else None, anchors, tokens, w, bias, with_markov,
                       B, K, d, r, V, threshold, tau, conf, cum, vl, stream)
     return dict(conf=conf, cumprod=cum, verify_len=vl)
@@ -746,9 +757,9 @@ def verify(ctx: Context, P, U, W1, W2, anchors, tokens, draft_logprobs, *, draft
     """Speculative verification of drafted tokens [B, K] against target logits P [B, K+1, V]."""
     B, K, V = U.shape
     r = _rank(W1)
-    n_acc = torch.empty(B, dtype=torch.int32, device=U.device)
-    next_token = torch.empty(B, dtype=torch.int32, device=U.device)
-    accept_prob = torch.empty(B, K, dtype=torch.float32, device=U.device)
+    n_acc = _empty(stream, (B,), torch.int32, U.device)
+    next_token = _empty(stream, (B,), torch.int32, U.device)
+    accept_prob = _empty(stream, (B, K), torch.float32, U.device)
     d = 0 if h is None else int(h.shape[-1])
     dspark_verify(ctx, P, U, W1, W2, anchors, h, Wg, d, tokens, draft_logprobs, ell, B, K, V, r,
                   draft_temperature, target_temperature, seed, n_acc, next_token, accept_prob,
@@ -761,7 +772,7 @@ def accept_label(ctx: Context, P, U, W1, W2, anchors, tokens, draft_logprobs=Non
     """Acceptance label 1 - TV(draft, target) [B, K] of drafted tokens [B, K]."""
     B, K, V = U.shape
     r = _rank(W1)
-    label = torch.empty(B, K, dtype=torch.float32, device=U.device)
+    label = _empty(stream, (B, K), torch.float32, U.device)
     d = 0 if h is None else int(h.shape[-1])
     dspark_accept_label(ctx, P, U, W1, W2, anchors, h, Wg, d, tokens, draft_logprobs, B, K, V, r,
                         draft_temperature, target_temperature, label, stream)
@@ -771,8 +782,8 @@ def accept_label(ctx: Context, P, U, W1, W2, anchors, tokens, draft_logprobs=Non
 def sts_fit(ctx: Context, conf, label, *, tau_lo=1.0 / 64, tau_hi=64.0, stream=None) -> dict:
     """Sequential temperature scaling: temperatures [K] from raw confidences and labels [N, K]."""
     N, K = conf.shape
-    tau = torch.empty(K, dtype=torch.float32, device=conf.device)
-    loss = torch.empty(K, dtype=torch.float32, device=conf.device)
+    tau = _empty(stream, (K,), torch.float32, conf.device)
+    loss = _empty(stream, (K,), torch.float32, conf.device)
     dspark_sts_fit(ctx, conf, label, N, K, tau_lo, tau_hi, tau, loss, stream)
     return dict(tau=tau, loss=loss)
 
@@ -780,8 +791,8 @@ def sts_fit(ctx: Context, conf, label, *, tau_lo=1.0 / 64, tau_hi=64.0, stream=N
 def schedule(ctx: Context, a, sps, stream=None) -> dict:
     """Greedy load-aware verify lengths: survival a [R, K], SPS(B) table [>= R (K+1) + 1]."""
     R, K = a.shape
-    ell = torch.empty(R, dtype=torch.int32, device=a.device)
-    theta = torch.empty(1, dtype=torch.float32, device=a.device)
+    ell = _empty(stream, (R,), torch.int32, a.device)
+    theta = _empty(stream, (1,), torch.float32, a.device)
     dspark_schedule(ctx, a, R, K, sps, ell, theta, stream)
     return dict(ell=ell, theta=theta)
 
@@ -792,10 +803,10 @@ def rnn_draft(ctx: Context, U, W1, W2, anchors, h, Wa, *, Wg=None, temperature=1
     logprobs [B, K] (and the confidence head's outputs when conf is given)."""
     B, K, V = U.shape
     r = _rank(W1)
-    tokens = torch.empty(B, K, dtype=torch.int32, device=U.device)
-    logprobs = torch.empty(B, K, dtype=torch.float32, device=U.device)
+    tokens = _empty(stream, (B, K), torch.int32, U.device)
+    logprobs = _empty(stream, (B, K), torch.float32, U.device)
     if conf is not None:
-        conf.allocate(B, K)
+        conf.allocate(B, K, stream)
     dspark_rnn_draft(ctx, U, W1, W2, anchors, h, Wa, Wg, int(h.shape[-1]), B, K, V, r,
                      temperature, seed, tokens, logprobs, conf, stream)
     out = dict(tokens=tokens, logprobs=logprobs)
@@ -809,8 +820,8 @@ def rnn_logits(ctx: Context, U, W1, W2, prev_tokens, h, Wa, *, Wg=None, temperat
     """The RNN head's teacher-forced logits [B, K, V] and LSE [B, K]."""
     B, K, V = U.shape
     r = _rank(W1)
-    logits = torch.empty(B, K, V, dtype=torch.float32, device=U.device)
-    lse = torch.empty(B, K, dtype=torch.float32, device=U.device)
+    logits = _empty(stream, (B, K, V), torch.float32, U.device)
+    lse = _empty(stream, (B, K), torch.float32, U.device)
     dspark_rnn_logits(ctx, U, W1, W2, prev_tokens, h, Wa, Wg, int(h.shape[-1]), B, K, V, r,
                       temperature, logits, lse, stream)
     return dict(logits=logits, lse=lse)
@@ -820,8 +831,8 @@ def markov_logits(ctx: Context, U, W1, W2, prev_tokens, *, temperature=1.0, h=No
                   stream=None) -> dict:
     B, K, V = U.shape
     r = _rank(W1)
-    logits = torch.empty(B, K, V, dtype=torch.float32, device=U.device)
-    lse = torch.empty(B, K, dtype=torch.float32, device=U.device)
+    logits = _empty(stream, (B, K, V), torch.float32, U.device)
+    lse = _empty(stream, (B, K), torch.float32, U.device)
     d = 0 if h is None else int(h.shape[-1])
     dspark_markov_logits(ctx, U, W1, W2, prev_tokens, h, Wg, d, B, K, V, r, temperature, logits,
                          lse, stream)
@@ -843,9 +854,9 @@ def verify_probs(ctx: Context, P, tokens, u_accept, u_draw, *, Q=None, cand=None
     _shape(u_accept, (B, K), "u_accept")
     _shape(u_draw, (B,), "u_draw")
     _shape(ell, (B,), "ell")
-    n_acc = torch.empty(B, dtype=torch.int32, device=P.device)
-    next_token = torch.empty(B, dtype=torch.int32, device=P.device)
-    accept_prob = torch.empty(B, K, dtype=torch.float32, device=P.device)
+    n_acc = _empty(stream, (B,), torch.int32, P.device)
+    next_token = _empty(stream, (B,), torch.int32, P.device)
+    accept_prob = _empty(stream, (B, K), torch.float32, P.device)
     dspark_verify_probs(ctx, P, Q, cand, cand_q, m, tokens, u_accept, u_draw, ell, B, K, V, n_acc,
                         next_token, accept_prob, stream)
     return dict(n_acc=n_acc, next_token=next_token, accept_prob=accept_prob)
@@ -864,10 +875,10 @@ def distill(ctx: Context, logits, teacher_ids, teacher_logits, *, teacher_rest=N
     _shape(teacher_rest, lead, "teacher_rest")
     _shape(row_weight, lead, "row_weight")
     N = lead.numel()
-    loss = torch.empty(lead, dtype=torch.float32, device=logits.device)
-    tv = torch.empty(lead, dtype=torch.float32, device=logits.device)
+    loss = _empty(stream, lead, torch.float32, logits.device)
+    tv = _empty(stream, lead, torch.float32, logits.device)
     if grad is True:
-        grad = torch.empty(*lead, V, dtype=logits.dtype, device=logits.device)
+        grad = _empty(stream, (*lead, V), logits.dtype, logits.device)
     elif grad is False:
         grad = None
     _shape(grad, (*lead, V), "grad")
@@ -887,8 +898,8 @@ def rnn_scan(ctx: Context, za, zg, e, *, s0=None, reset=None, stream=None) -> di
     _shape(zg, e.shape, "zg")
     _shape(s0, (N, D), "s0")
     _shape(reset, (N, L), "reset")
-    s = torch.empty(N, L, D, dtype=e.dtype, device=e.device)
-    s_last = torch.empty(N, D, dtype=torch.float32, device=e.device)
+    s = _empty(stream, (N, L, D), e.dtype, e.device)
+    s_last = _empty(stream, (N, D), torch.float32, e.device)
     dspark_rnn_scan(ctx, za, zg, e, s0, reset, N, L, D, s, s_last, stream)
     return dict(s=s, s_last=s_last)
 
@@ -905,10 +916,10 @@ def rnn_scan_grad(ctx: Context, za, zg, e, s, ds, *, s0=None, ds_last=None, rese
     _shape(s0, (N, D), "s0")
     _shape(ds_last, (N, D), "ds_last")
     _shape(reset, (N, L), "reset")
-    dz = torch.empty(N, L, D if zg is None else 2 * D, dtype=e.dtype, device=e.device)
+    dz = _empty(stream, (N, L, D if zg is None else 2 * D), e.dtype, e.device)
     dza, dzg = dz[..., :D], None if zg is None else dz[..., D:]
-    de = torch.empty(N, L, D, dtype=e.dtype, device=e.device)
-    ds0 = torch.empty(N, D, dtype=torch.float32, device=e.device)
+    de = _empty(stream, (N, L, D), e.dtype, e.device)
+    ds0 = _empty(stream, (N, D), torch.float32, e.device)
     dspark_rnn_scan_grad(ctx, za, zg, e, s, ds, s0, reset, ds_last, N, L, D, dza, dzg, de, ds0,
                          stream)
     out = dict(dza=dza, de=de, ds0=ds0)
@@ -922,7 +933,7 @@ def embed(ctx: Context, table, ids, *, scale=1.0, dtype=None, out=None, stream=N
     (fp32, bf16); out receives it."""
     V, D = table.shape
     if out is None:
-        out = torch.empty(*ids.shape, D, dtype=dtype or table.dtype, device=table.device)
+        out = _empty(stream, (*ids.shape, D), dtype or table.dtype, table.device)
     _shape(out, (*ids.shape, D), "out")
     dspark_embed(ctx, table, ids, ids.numel(), V, D, scale, out, stream)
     return out
@@ -937,7 +948,7 @@ def embed_grad(ctx: Context, ids, de, V=None, *, scale=1.0, dtype=torch.float32,
     if grad is None:
         if accumulate or V is None:
             raise ValueError("embed_grad: accumulate needs grad, and a new gradient V")
-        grad = torch.empty(V, D, dtype=dtype, device=de.device)
+        grad = _empty(stream, (V, D), dtype, de.device)
     _shape(grad, (grad.shape[0] if V is None else V, D), "grad")
     dspark_embed_grad(ctx, ids, de, ids.numel(), grad.shape[0], D, scale, accumulate, grad, stream)
     return grad
@@ -945,7 +956,7 @@ def embed_grad(ctx: Context, ids, de, V=None, *, scale=1.0, dtype=torch.float32,
 
 def grad_norm(ctx: Context, grads, stream=None) -> torch.Tensor:
     """The norm of all tensors of a list together (fp32 scalar on the device)."""
-    norm = torch.empty((), dtype=torch.float32, device=torch.device("cuda", ctx.device))
+    norm = _empty(stream, (), torch.float32, torch.device("cuda", ctx.device))
     dspark_clip_grads(ctx, list(grads), 0.0, None, norm, stream)
     return norm
 
@@ -953,7 +964,7 @@ def grad_norm(ctx: Context, grads, stream=None) -> torch.Tensor:
 def clip_grads(ctx: Context, grads, max_norm, *, out=None, stream=None) -> torch.Tensor:
     """Scale a list of gradients (fp32, bf16) to a common norm of at most max_norm, in place or
     into the tensors of out; returns their norm before (fp32 scalar on the device)."""
-    norm = torch.empty((), dtype=torch.float32, device=torch.device("cuda", ctx.device))
+    norm = _empty(stream, (), torch.float32, torch.device("cuda", ctx.device))
     grads = list(grads)
     dspark_clip_grads(ctx, grads, max_norm, grads if out is None else list(out), norm, stream)
     return norm
@@ -969,10 +980,10 @@ def linear(ctx: Context, x, W, *, bias=None, act=None, residual=None, dtype=None
     _shape(x, (*lead, K), "x")
     _shape(bias, (N,), "bias")
     _shape(residual, (*lead, N), "residual")
-    y = torch.empty(*lead, N, dtype=dtype or x.dtype, device=x.device) if out is None else out
+    y = _empty(stream, (*lead, N), dtype or x.dtype, x.device) if out is None else out
     _shape(y, (*lead, N), "out")
     if pre is True:
-        pre = torch.empty(*lead, N, dtype=y.dtype, device=x.device)
+        pre = _empty(stream, (*lead, N), y.dtype, x.device)
     elif pre is False:
         pre = None
     _shape(pre, (*lead, N), "pre")
@@ -997,7 +1008,7 @@ def linear_grad(ctx: Context, x, W, dy, *, act=None, pre=None, dx=True, dW=True,
     out = {}
     for name, (want, shape, dtype) in given.items():
         if want is True:
-            out[name] = torch.empty(shape, dtype=dtype, device=dy.device)
+            out[name] = _empty(stream, shape, dtype, dy.device)
         elif want is not False:
             _shape(want, shape, name)
             out[name] = want
