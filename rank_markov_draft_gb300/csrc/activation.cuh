@@ -7,17 +7,23 @@
 
 namespace dspark {
 
-// 1 / (1 + e^-z) by the quick exponential, right to 2 + 1.2 |z| units in the last place of e^-z (which
-// counts where z < 0; elsewhere 1 is the larger summand), and the quick division, right to two, and 0
-// below 2^-126.  (1825 x 256 x 35840 with sigmoid takes 70 us; with expf 82.)
-__device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + e^-z) without cancellation or overflow, right to four units in the last place (the
+// exponential to one, the quick division of numbers up to 2 by ones of 1 to 2 to two).
+__device__ __forceinline__ float sigmoid_of(float z) {
+  const float e = expf(-fabsf(z));
+  return __fdividef(z < 0.f ? e : 1.f, 1.f + e);
+}
+// The same by the quick exponential, right to 2 + 1.2 |z| units in the last place of e^-z (which counts where
+// z < 0; elsewhere 1 is the larger summand), and 0 below 2^-126: for outputs of bf16, 2^-8 of whose own
+// rounding it stays below. (1825 x 256 x 35840 with sigmoid to bf16 takes 80 us; with expf 99.)
+__device__ __forceinline__ float quick_sigmoid_of(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-template <int ACT>
+template <int ACT, bool QUICK>
 __device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == DSPARK_ACT_SIGMOID) return sigmoid_of(z);
+  if constexpr (ACT == DSPARK_ACT_SIGMOID) return QUICK ? quick_sigmoid_of(z) : sigmoid_of(z);
   if constexpr (ACT == DSPARK_ACT_TANH) return tanhf(z);
   if constexpr (ACT == DSPARK_ACT_RELU) return z < 0.f ? 0.f : z;  // (a NaN stays one)
-  if constexpr (ACT == DSPARK_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+  if constexpr (ACT == DSPARK_ACT_SILU) return QUICK ? __fdividef(z, 1.f + __expf(-z)) : z * sigmoid_of(z);
   if constexpr (ACT == DSPARK_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678f);
   return z;
 }
@@ -25,7 +31,7 @@ __device__ __forceinline__ float act_value(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == DSPARK_ACT_SIGMOID) {
-    const float s = sigmoid_of(z);
+    const float s = quick_sigmoid_of(z);
     return s * (1.f - s);
   }
   if constexpr (ACT == DSPARK_ACT_TANH) {
@@ -34,7 +40,7 @@ __device__ __forceinline__ float act_slope(float z) {
   }
   if constexpr (ACT == DSPARK_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if constexpr (ACT == DSPARK_ACT_SILU) {
-    const float s = sigmoid_of(z);
+    const float s = quick_sigmoid_of(z);
     return s * (1.f + z * (1.f - s));
   }
   if constexpr (ACT == DSPARK_ACT_GELU)

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(256) linear_join_kernel(JoinArgs a) {
     if (a.pre != nullptr) put(a.pre, a.ld_pre);
     with_act(a.act, [&](auto act) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = act_value<decltype(act)::value>(z[j]);
+      for (int j = 0; j < 4; ++j)
+        z[j] = a.out_f32 ? act_value<decltype(act)::value, false>(z[j]) : act_value<decltype(act)::value, true>(z[j]);
     });
 #pragma unroll
     for (int j = 0; j < 4; ++j) z[j] += r[j];

@@ -167,32 +167,39 @@ __device__ __forceinline__ void epi_put32(const float (&v)[32], uint32_t line) {
     st_shared_v4(line ^ (u << 4), __float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
                  __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
 }
-// The activation in registers: 1825 x 256 x 35840 takes 70 to 76 us with sigmoid and 85 with tanh against 56
-// without (by a loop over the line 97 and 107).  GELU, of many more instructions, is such a loop, for one
-// copy of its code: 32 of them cost every kernel registers and gained nothing (182 to 188 us).
-__device__ __forceinline__ void epi_act(int act, float (&v)[32]) {
-  auto all = [&](auto a) {
+// The activation in registers: 1825 x 256 x 35840 to bf16 takes 80 us with sigmoid and 90 with tanh against 59
+// without (by a loop over the line some 25 more); to fp32, whose exponentials are exact, 105 against 71.  GELU, of
+// many more instructions, is such a loop, for one copy of its code: 32 of them cost every kernel registers and
+// gained nothing (182 to 192 us).
+__device__ __forceinline__ void epi_act(int act, int out_f32, float (&v)[32]) {
+  auto all = [&](auto a, auto quick) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+    for (int j = 0; j < 32; ++j) v[j] = act_value<decltype(a)::value, decltype(quick)::value>(v[j]);
+  };
+  auto by_type = [&](auto a) {
+    if (out_f32)
+      all(a, std::false_type());
+    else
+      all(a, std::true_type());
   };
   if (act == DSPARK_ACT_SIGMOID) {
-    all(std::integral_constant<int, DSPARK_ACT_SIGMOID>());
+    by_type(std::integral_constant<int, DSPARK_ACT_SIGMOID>());
   } else if (act == DSPARK_ACT_TANH) {
-    all(std::integral_constant<int, DSPARK_ACT_TANH>());
+    all(std::integral_constant<int, DSPARK_ACT_TANH>(), std::false_type());
   } else if (act == DSPARK_ACT_RELU) {
-    all(std::integral_constant<int, DSPARK_ACT_RELU>());
+    all(std::integral_constant<int, DSPARK_ACT_RELU>(), std::false_type());
   } else if (act == DSPARK_ACT_SILU) {
-    all(std::integral_constant<int, DSPARK_ACT_SILU>());
+    by_type(std::integral_constant<int, DSPARK_ACT_SILU>());
   }
 }
 __device__ __forceinline__ void epi_gelu(uint32_t line) {
 #pragma unroll 2
   for (int u = 0; u < 8; ++u) {
     const uint4 w = ld_shared_v4(line ^ (u << 4));
-    st_shared_v4(line ^ (u << 4), __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.x))),
-                 __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.y))),
-                 __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.z))),
-                 __float_as_uint(act_value<DSPARK_ACT_GELU>(__uint_as_float(w.w))));
+    st_shared_v4(line ^ (u << 4), __float_as_uint(act_value<DSPARK_ACT_GELU, false>(__uint_as_float(w.x))),
+                 __float_as_uint(act_value<DSPARK_ACT_GELU, false>(__uint_as_float(w.y))),
+                 __float_as_uint(act_value<DSPARK_ACT_GELU, false>(__uint_as_float(w.z))),
+                 __float_as_uint(act_value<DSPARK_ACT_GELU, false>(__uint_as_float(w.w))));
   }
 }
 __device__ __forceinline__ void epi_get32(float (&v)[32], uint32_t line) {
@@ -605,7 +612,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
               }
               tmem_wait_ld();
               if (g.bias != nullptr) epi_bias(v, bias);
-              if (last) epi_act(g.act, v);
+              if (last) epi_act(g.act, g.out_f32, v);
               if (last && g.act == DSPARK_ACT_GELU) {
                 // (the slot's one box may hold the first half's bf16 outputs: they are kept meanwhile)
                 uint4 keep[EPI == kEpiResidual ? 1 : 4];
@@ -672,7 +679,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = ld_shared(box + 128 * k + ((((lane >> 2) ^ (k & 7)) << 4) | ((lane & 3) << 2)));
-                if (last) epi_act(g.act, v);
+                if (last) epi_act(g.act, g.out_f32, v);
                 if constexpr (kCopied) {
                   if (last) {
                     cp_async_wait_group<1>();
