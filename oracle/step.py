@@ -52,12 +52,13 @@ def act(name, z):
 
 
 def slope(name, z):
-    """d act / d z (0 at relu's kink)."""
+    """d act / d z (0 at relu's kink), without a difference from 1 that a far argument leaves nothing of."""
     if name is None:
         return torch.ones_like(z)
-    s = 1 / (1 + torch.exp(-z))
-    return {"sigmoid": lambda: s * (1 - s), "tanh": lambda: 1 - torch.tanh(z) ** 2, "relu": lambda: (z > 0).double(),
-            "silu": lambda: s + z * s * (1 - s),
+    e = torch.exp(-z.abs())
+    s = torch.where(z < 0, e, 1.0) / (1 + e)
+    return {"sigmoid": lambda: e / (1 + e) ** 2, "tanh": lambda: 4 * e ** 2 / (1 + e ** 2) ** 2, "relu": lambda: (z > 0).double(),
+            "silu": lambda: s * (1 + z * torch.where(z < 0, 1.0, e) / (1 + e)),
             "gelu": lambda: 0.5 * torch.erfc(-z / math.sqrt(2)) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)}[name]()
 
 
@@ -90,8 +91,9 @@ def linear_grad(x, W, dy, name=None, pre=None):
     err = torch.zeros_like(d)
     if name is not None:
         k = slope(name, pre.double())
-        # (a slope is a sum of two terms of up to 1.13 that may cancel)
-        err = d.abs() * 24 * EPS32
+        # the functions' own roundings and a few products'; SiLU's and GELU's slopes are sums of two terms
+        # of up to 1.13 that may cancel
+        err = d.abs() * (24 if name in ("silu", "gelu") else 12 * k) * EPS32
         d = d * k
     rest = err.clone()
     if name is not None or dy.dtype != torch.bfloat16:

@@ -63,3 +63,30 @@ def test_values_of_32_bits(dsp, name, rows, K):
     bad = err > roundings(name, z.double()) * step.EPS32 * want.abs() + TINY
     assert not bad.any(), (z[bad][:3], y[-1][bad][:3], want[bad][:3])
     assert torch.equal(y, y[:1].expand_as(y))
+
+
+@pytest.mark.parametrize("name", ["sigmoid", "tanh", "silu", "gelu"])
+def test_slopes_of_32_bits(dsp, name):
+    """dW of one row is x times dz, and dbias is dz; three bf16 numbers of dz leave 2^-25 of it, their sum cuts three
+    times.  (SiLU's and GELU's slopes are sums of two terms of either sign: relative to those.)"""
+    z = arguments()
+    dy = torch.full((1, z.numel()), 1.5, dtype=BF16, device="cuda")
+    g = binding.linear_grad(dsp, torch.ones(1, 1, dtype=BF16, device="cuda"), torch.ones(1, z.numel(), dtype=BF16, device="cuda"),
+                            dy, act=name, pre=z[None], dx=False, dbias=True)
+    done(dsp)
+    d = z.double()
+    want = slope(name, d)
+    if name == "sigmoid":
+        allowed = (2 + 2 + 4 + 1) * want
+    elif name == "tanh":
+        allowed = (2 + 2 + 4 + 2) * want
+    elif name == "silu":
+        s = value("sigmoid", d)
+        allowed = 9 * s + (9 + 9 + 2) * s * d.abs() * value("sigmoid", -d) + want.abs()
+    else:
+        # the exponential's argument z^2 / 2 is rounded twice
+        allowed = roundings("gelu", d) * 0.5 * torch.erfc(-d / math.sqrt(2)) + (2 + d * d + 4) * d.abs() * torch.exp(-d * d / 2) / math.sqrt(2 * math.pi) + want.abs()
+    for got, more in ((g["dW"][0], 7), (g["dbias"], 1)):
+        err = (got.double() - 1.5 * want).abs()
+        bad = err > 1.5 * (allowed + more * want.abs()) * step.EPS32 + TINY
+        assert not bad.any(), (z[bad][:3], got[bad][:3], 1.5 * want[bad][:3])
