@@ -62,11 +62,13 @@ def slope(name, z):
             "gelu": lambda: 0.5 * torch.erfc(-z / math.sqrt(2)) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)}[name]()
 
 
-def product(a, b):
-    """a b and its bound: the terms are exact, their sum is taken 16 at a time, each step rounded (or
-    cut: a whole step of float32) relative to what has been added up so far."""
-    K = a.shape[-1]
-    return a @ b, (K / 16 + 16) * 2 * EPS32 * (a.abs() @ b.abs())
+def product(a, b, parts=1):
+    """a b and its bound: the terms (of `parts` exact numbers an element) are exact, their sum is taken 16 at a
+    time, each step rounded (or cut: a whole step of float32) relative to what has been added up so far,
+    for 512 terms at most; up to 64 sums of these, and these, are added up in float32."""
+    K = parts * a.shape[-1]
+    cuts, adds = min(K / 16, 32) + 16, min(K / 64, 64) + K / 512
+    return a @ b, (2 * cuts + adds) * EPS32 * (a.abs() @ b.abs())
 
 
 def linear(x, W, bias=None, name=None, residual=None):
@@ -95,11 +97,11 @@ def linear_grad(x, W, dy, name=None, pre=None):
         # of up to 1.13 that may cancel
         err = d.abs() * (24 if name in ("silu", "gelu") else 12 * k) * EPS32
         d = d * k
-    rest = err.clone()
+    rest, parts = err.clone(), 1
     if name is not None or dy.dtype != torch.bfloat16:
-        rest = rest + d.abs() * 2.0 ** -25
+        rest, parts = rest + d.abs() * 2.0 ** -25, 3
     Wd, xd = W.double(), x.double()
-    dx, ex = product(d, Wd.T)
-    dW, ew = product(xd.T, d)
+    dx, ex = product(d, Wd.T, parts)
+    dW, ew = product(xd.T, d, parts)
     db, eb = d.sum(0), d.abs().sum(0) * d.shape[0] * EPS32 + err.sum(0)
     return dict(dx=(dx, ex + rest @ Wd.abs().T), dW=(dW, ew + xd.abs().T @ rest), dbias=(db, eb))
