@@ -425,10 +425,10 @@ struct Launcher {
   }
 
   // out = act(A B + bias) + residual, A of parts a[0..na), B of b[0..nb); the epilogue's fields of g
-  // are set. pair_splits: two blocks a tile, this many splits; 0: as pays.
+  // are set. splits: this many of them, and two blocks a tile where TMA stores its outputs; 0: as pays.
   template <bool A_MN, bool B_MN>
   Plan plan(GemmArgs g, const Matrix* a, int na, const Matrix* b, int nb, int64_t I, int J, int64_t Kc,
-            int64_t pair_splits = 0) {
+            int64_t splits = 0) {
     Plan p;
     bool by_tma = tma_out(g.out, g.ld_out, g.out_f32, J) && (g.residual == nullptr || tma(g.residual, g.ld_res, g.res_f32)) &&
                   (g.pre == nullptr || (tma(g.pre, g.ld_pre, g.out_f32) && g.residual == nullptr));
@@ -460,17 +460,17 @@ struct Launcher {
         if (t < best) best = t, p.BN = 256, p.S = s, p.pair = true;
       }
     };
-    if (pair_splits > 0) {
-      const int64_t per = (g.steps + pair_splits - 1) / pair_splits;
+    if (splits > 0) {
+      const int64_t per = (g.steps + splits - 1) / splits;
       p.S = (g.steps + per - 1) / per;
       p.pair = true;
     } else {
       for (int64_t s = 1; s <= std::min<int64_t>(g.steps, 64) && (s == 1 || s * I * ld_part * 4 <= kStepScratchBytes); ++s)
         consider(s, 3.0, true);
-      if (p.S == 1 && !by_tma) {
-        best = 1e30;
-        consider(1, 10.0, false);
-      }
+    }
+    if (p.S == 1 && !by_tma) {
+      best = 1e30;
+      consider(1, 10.0, false);
     }
     g.I = I;
     g.J = J;
@@ -553,11 +553,13 @@ struct Launcher {
 
   // Both products of a gradient in one launch, where dz passes what L2 keeps between two launches
   // (64 MB of its 129, the other streams taking their share) and dz W^T is of so few tiles that splits
-  // of it keep half the blocks busy. Returns whether it did.
+  // of it keep half the blocks busy. Returns whether it did. Sizes and types alone decide, so that equal
+  // inputs give equal bits wherever they lie: a dW that TMA does not store gets a launch of its own
+  // beside the same splits of dx.
   bool both(const GemmArgs& gx, const GemmArgs& gw, const Matrix* dz, int parts, const Matrix& W, const Matrix& x) {
     const int64_t M = x.rows, K = x.cols, N = dz[0].cols, pairs = c.num_sms / 2;
     const int64_t tiles_x = (M + 255) / 256 * ((K + 255) / 256), units_w = (K + 255) / 256 * ((N + 255) / 256);
-    if (M * N * 2 * parts < (64ll << 20) || tiles_x > pairs / 2 || !tma_out(gw.out, gw.ld_out, gw.out_f32, N)) return false;
+    if (M * N * 2 * parts < (64ll << 20) || tiles_x > pairs / 2 || N % (gw.out_f32 ? 4 : 8) != 0) return false;
     const int64_t steps_x = (N + 63) / 64 * parts, steps_w = (M + 63) / 64 * parts;
     // Time until the later of the two is done: a stage of dz W^T takes 0.36 us, one of x^T dz (both of its
     // operands MN-major) 0.45.
@@ -573,7 +575,11 @@ struct Launcher {
     if (S == 0 || 5 * best * pairs > 7 * (4 * tiles_x * steps_x + 5 * units_w * steps_w)) return false;
     Plan px = plan<false, false>(gx, dz, parts, &W, 1, M, static_cast<int>(K), N, S);
     Plan pw = plan<true, true>(gw, &x, 1, dz, parts, K, static_cast<int>(N), M, 1);
-    if (!ok()) return true;
+    if (!pw.pair) {
+      run<false, false>(px);
+      run<true, true>(pw);
+    }
+    if (!ok() || !pw.pair) return true;
     GemmBoth both;
     both.dx = px.g;
     both.dw = pw.g;

@@ -14,7 +14,7 @@ import torch
 
 from oracle import step
 from rank_markov_draft_gb300 import binding
-from tests.test_gpu_embed import done
+from tests.test_gpu_embed import done, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,18 @@ def test_dy_of_32_bits_enters_the_products_whole(dsp, dtype):
         err = (got.double() - want).abs()
         bad = err > ONE * want + (0 if dtype == F32 else half_step(want, dtype))
         assert not bad.any(), (int(bad.sum()), float((err / want).max()))
+
+
+@pytest.mark.parametrize("M,K,N,act,dtype", [(700, 256, 50000, None, BF16), (2048, 100, 20000, None, F32), (1500, 136, 24000, "silu", BF16)])
+def test_large_gradients_wherever_they_lie_give_equal_bits(dsp, M, K, N, act, dtype):
+    """Both products of a large dz share the blocks out by sizes, not by where dW lies."""
+    x, W, dy = positive(1, M, K), positive(2, K, N), positive(3, M, N).to(dtype)
+    pre = positive(4, M, N) if act else None
+    for dw_dtype in (F32, BF16):
+        want = binding.linear_grad(dsp, x, W, dy, act=act, pre=pre, dW=torch.empty(K, N, dtype=dw_dtype, device="cuda"))
+        for extra, at in ((3, 1), (8, 0), (16, 4)):
+            dW = wide(torch.zeros(K, N, dtype=dw_dtype, device="cuda"), extra, at)[1]
+            dx = wide(torch.zeros(M, K, dtype=BF16, device="cuda"), extra, at)[1]
+            binding.linear_grad(dsp, x, W, dy, act=act, pre=pre, dx=dx, dW=dW)
+            done(dsp)
+            assert torch.equal(dx, want["dx"]) and torch.equal(dW, want["dW"]), (extra, at)
