@@ -568,8 +568,8 @@ int dspark_rnn_scan_grad(dspark_ctx* ctx, const void* za, const void* zg, const 
  *   ids [N] int32: negative ids are padding (a row of zeros); ids >= V are reported as
  *     DSPARK_ERR_DEVICE_OOB and give zeros
  *   out [N, D] of type out_dtype, rows ld_out elements apart
- * The product is formed in fp32 and rounded once; out must not overlap table.  Any N >= 0 (< 2^31), D >= 1; V <= 2^18;
- * pointers aligned to their element size. */
+ * The product is formed in fp32 and rounded once; out must not overlap table.  Any N >= 0 (< 2^31), D >= 1 with
+ * N ceil(D / 1024) < 2^31; V <= 2^18; pointers aligned to their element size. */
 int dspark_embed(dspark_ctx* ctx, const void* table, int table_dtype, int64_t ld_table,
                  const int32_t* ids, int64_t N, int V, int D, float scale, void* out,
                  int out_dtype, int64_t ld_out, dspark_stream_t stream);

@@ -1183,6 +1183,7 @@ int dspark_embed(dspark_ctx* ctx, const void* table, int table_dtype, int64_t ld
     return DSPARK_ERR_INVALID_ARG;
   if (V > (1 << 18) || N > kMost || ld_table > kMost || ld_out > kMost)
     return DSPARK_ERR_UNSUPPORTED;
+  if (N * ((static_cast<int64_t>(D) + 1023) / 1024) > kMost) return DSPARK_ERR_UNSUPPORTED;  // (blocks)
   int st;
   if ((st = check_ctx(ctx)) != DSPARK_OK) return st;
   ctx->last_launches = 0;
