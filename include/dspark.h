@@ -597,7 +597,7 @@ int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int d
  *     dspark_dtypes (contiguous tensors; a count of 0 elements may have a NULL address)
  *   out: HOST array of `count` addresses that receive the scaled tensors, in their types:
  *     a tensor's own address scales it in place (where the factor is 1 it is not touched);
- *     otherwise tensors must not overlap.  NULL: only the norm is computed, max_norm unread
+ *     otherwise tensors must not overlap (nor be listed twice).  NULL: only the norm is computed, max_norm unread
  *   norm: device fp32 scalar
  * The host arrays are read during the call.  Squares are of fp32 (a gradient beyond 1e19 makes
  * the norm infinite), their sums of 64 bits beyond a thread's own.  An infinite norm gives the

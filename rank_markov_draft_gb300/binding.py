@@ -563,6 +563,14 @@ def _tensor_list(ts, name: str):
     return array("Q", pointers), array("q", numel), array("i", dtypes)
 
 
+def _each_once(pointers, numel, name: str):
+    """No tensor (that has elements) is listed twice: both of its places would scale it at one time."""
+    if len(set(pointers)) != len(pointers):
+        used = [p for p, n in zip(pointers, numel) if n > 0]
+        if len(set(used)) != len(used):
+            raise ValueError(f"{name}: the same tensor twice")
+
+
 def dspark_clip_grads(ctx: Context, grads, max_norm, out, norm, stream=None):
     """grads and out: lists of contiguous tensors (out None: only the norm)."""
     src, numel, dtypes = _tensor_list(grads, "grads")
@@ -573,6 +581,8 @@ def dspark_clip_grads(ctx: Context, grads, max_norm, out, norm, stream=None):
         dst, n, dt = _tensor_list(out, "out")
         if n != numel or dt != dtypes:
             raise ValueError("out: other sizes or types than the gradients'")
+    if dst is not None:
+        _each_once(dst, numel, "grads" if out is grads else "out")
     address = lambda a: None if a is None else a.buffer_info()[0]  # noqa: E731
     code = ctx.lib.dspark_clip_grads(ctx.handle, address(src), address(numel), address(dtypes),
                                      len(src), float(max_norm), address(dst),
@@ -963,7 +973,8 @@ def grad_norm(ctx: Context, grads, stream=None) -> torch.Tensor:
 
 def clip_grads(ctx: Context, grads, max_norm, *, out=None, stream=None) -> torch.Tensor:
     """Scale a list of gradients (fp32, bf16) to a common norm of at most max_norm, in place or
-    into the tensors of out; returns their norm before (fp32 scalar on the device)."""
+    into the tensors of out; returns their norm before (fp32 scalar on the device).  A tensor that
+    several parameters share is listed once."""
     norm = _empty(stream, (), torch.float32, torch.device("cuda", ctx.device))
     grads = list(grads)
     dspark_clip_grads(ctx, grads, max_norm, grads if out is None else list(out), norm, stream)
