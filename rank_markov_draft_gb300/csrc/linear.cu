@@ -587,7 +587,7 @@ struct Launcher {
     both.dx_pairs = static_cast<int>(px.g.units);
     // dW passes through L2, which has dz to keep for its second reading (213 us for 2048 x 151936 of 256, 216
     // without, 253 in two launches)
-    both.dw.l2_out = kL2First;
+    both.dw.out_first = 1;
     constexpr uint32_t smem = GemmShape<256, kEpiTma, true>::kSmem;
     error = (*c.opt_in)(linear_both_kernel, smem);
     launch({dim3(static_cast<unsigned>(2 * pairs)), kGemmThreads, smem, 2}, linear_both_kernel, both);

@@ -37,12 +37,6 @@
 
 namespace dspark {
 
-enum GemmL2 { kL2Normal, kL2First, kL2Last };  // when L2 gives a line up
-
-__device__ __forceinline__ uint64_t gemm_policy(int l2) {
-  return l2 == kL2First ? l2_policy_evict_first() : l2 == kL2Last ? l2_policy_evict_last() : l2_policy_evict_normal();
-}
-
 struct GemmArgs {
   CUtensorMap a[3], b[3];
   CUtensorMap out_map, pre_map, res_map;  // (outputs by TMA) boxes of 32 rows x 128 bytes
@@ -62,7 +56,7 @@ struct GemmArgs {
   void *out, *pre;
   int* status;
   uint64_t timeout_ns;
-  int l2_a, l2_b, l2_out;   // GemmL2 of the operands and the output
+  int out_first;            // L2 gives up the output's lines before others
   int skip_cta;             // testing: the block that loads nothing (-1: none)
 };
 
@@ -282,7 +276,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
 
   if (warp == 0) {
     if (lane == 0 && static_cast<int>(blockIdx.x) != g.skip_cta) {
-      const uint64_t pol_a = gemm_policy(g.l2_a), pol_b = gemm_policy(g.l2_b);
+      const uint64_t pol = l2_policy_evict_normal();
       bool ok = true;
       uint32_t n = 0;  // stages filled
       for (int64_t u = first; u < g.units && ok; u += stride) {
@@ -315,7 +309,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
           uint8_t* const sb = smem + S::kOffB + s * S::kB;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
-          auto load = [&](uint8_t* to, const CUtensorMap* map, int x, int y, uint64_t pol) {
+          auto load = [&](uint8_t* to, const CUtensorMap* map, int x, int y) {
             if constexpr (PAIR)
               tma_load_2d_pair(to, map, x, y, bar, pol);
             else
@@ -324,16 +318,16 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
           if constexpr (A_MN) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              if (c < boxes_a) load(sa + c * 8192, ma, i0 + c * 64, k0, pol_a);
+              if (c < boxes_a) load(sa + c * 8192, ma, i0 + c * 64, k0);
           } else {
-            load(sa, ma, k0, i0, pol_a);
+            load(sa, ma, k0, i0);
           }
           if constexpr (B_MN) {
 #pragma unroll
             for (int c = 0; c < kBoxesB; ++c)
-              if (c < boxes_b) load(sb + c * 8192, mb, j0 + c * 64, k0, pol_b);
+              if (c < boxes_b) load(sb + c * 8192, mb, j0 + c * 64, k0);
           } else {
-            load(sb, mb, k0, j0, pol_b);
+            load(sb, mb, k0, j0);
           }
         }
       }
@@ -410,7 +404,7 @@ __device__ __forceinline__ void gemm_units(const GemmArgs& g, const int64_t firs
     const int q = warp & 3, e = warp - 2, group = e >> 2;
     constexpr int kChunks = BN / 64, kRound = kChunks < 2 ? 2 : kChunks;  // (of 64 columns the second group has none)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const uint64_t pol_out = gemm_policy(g.l2_out);
+    const uint64_t pol_out = g.out_first ? l2_policy_evict_first() : l2_policy_evict_normal();
     const uint32_t slots = smem_addr(smem + S::kOffEpi + e * S::kSlots * S::kSlot);
     const uint32_t own = 128 * lane + ((lane & 7) << 4);  // this lane's line of a 4 KB box
     constexpr bool kCopied = EPI == kEpiElementsF32 || EPI == kEpiElementsBf16, kElements = EPI == kEpiElements || kCopied;
