@@ -99,7 +99,7 @@ __device__ __forceinline__ void store_zeros(const SortArgs& a, int block, int bl
 constexpr int kSortHeld = 8;  // elements of a lane in registers
 
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a) {
-  extern __shared__ uint32_t counts[];  // [warps][bins], 3 [bins], lanes or elements
+  extern __shared__ uint32_t counts[];  // [warps][bins], 2 [bins], lanes or elements
   __shared__ uint32_t warp_sum[kSortWarps], warp_local[kSortWarps];
   griddep_launch_dependents();
   const int c = blockIdx.x;
@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(SortArgs a)
   uint32_t* const mine = counts + warp * bins;
   uint32_t* const base = counts + kSortWarps * bins;
   uint32_t* const local = base + bins;  // the block's elements of lower digits
-  uint32_t* const lanes = local + 2 * bins + warp * bins;
-  uint2* const staged = reinterpret_cast<uint2*>(local + 2 * bins);
+  uint32_t* const lanes = local + bins + warp * bins;
+  uint2* const staged = reinterpret_cast<uint2*>(local + bins);
   const int64_t stretch = (a.N + static_cast<int64_t>(a.cluster) * kSortThreads - 1) /
                           (static_cast<int64_t>(a.cluster) * kSortThreads) * 32;  // a warp's
   const int64_t lo = min(a.N, (static_cast<int64_t>(c) * kSortWarps + warp) * stretch);
@@ -590,8 +590,8 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& c, 
     t.size = a.grad_dtype == DSPARK_F32 ? 4 : 2;
     if (t.cluster <= 4) grid = c.num_sms / t.cluster * t.cluster;
   }
-  // counts, three words a digit, and the larger of the lanes' words and the elements in order
-  auto sort_smem = [](int bits) { return ((kSortWarps + 3) << bits) * 4 + std::max((kSortWarps << bits) * 4, kSortThreads * kSortHeld * 8); };
+  // counts, two words a digit, and the larger of the lanes' words and the elements in order
+  auto sort_smem = [](int bits) { return ((kSortWarps + 2) << bits) * 4 + std::max((kSortWarps << bits) * 4, kSortThreads * kSortHeld * 8); };
   const int smem = sort_smem(t.bits);
   cudaError_t e = (*c.opt_in)(embed_sort_kernel, sort_smem(kSortMaxBits));
   if (e != cudaSuccess) return e;
