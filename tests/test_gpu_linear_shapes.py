@@ -25,3 +25,21 @@ def test_tall_beside_wide(dsp, M, K, N, act, dtype):
     near(out["pre"], z, ez, "pre")
     for name, (want, bound) in step.linear_grad(x, W, dy, act, out["pre"]).items():
         near(g[name], want, bound, name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("residual", [F32, BF16])
+@pytest.mark.parametrize("N", [640, 641])
+def test_residuals_beside_long_sums(dsp, N, residual, dtype):
+    """Accumulators that start again while residuals arrive, over more tiles than blocks."""
+    M, K = 20050, 1100
+    x, W = normal(1, M, K).to(BF16), (normal(2, K, N) / K ** 0.5).to(BF16)
+    res, bias = (3 * normal(3, M, N)).to(residual), normal(4, N)
+    out = binding.linear(dsp, x, W, bias=bias, act="silu", residual=res, dtype=dtype)["y"]
+    done(dsp)
+    want, _, bound, _ = step.linear(x, W, bias, "silu", res)
+    near(out, want, bound)
+    if residual == dtype:
+        binding.linear(dsp, x, W, bias=bias, act="silu", residual=res, out=res)
+        done(dsp)
+        assert torch.equal(res, out)
