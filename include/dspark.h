@@ -94,7 +94,8 @@ typedef struct dspark_conf_args {
 
 /* Create a context on `device` with scratch for up to B_max requests, K_max
  * block positions (<= 64) and V_max vocabulary entries.  Allocates device
- * memory (the only allocation the library makes).  *ctx receives the handle;
+ * memory (the only allocation the library makes; 32 MiB of it whatever the
+ * limits, the scratch of dspark_embed_grad and the linear layers).  *ctx receives the handle;
  * release it with dspark_ctx_destroy. */
 int dspark_ctx_create(dspark_ctx** ctx, int device, int B_max, int V_max, int K_max);
 

@@ -14,8 +14,8 @@ __device__ __forceinline__ float sigmoid_of(float z) {
   return __fdividef(z < 0.f ? e : 1.f, 1.f + e);
 }
 // The same by the quick exponential, right to 2 + 1.2 |z| units in the last place of e^-z (which counts where
-// z < 0; elsewhere 1 is the larger summand), and 0 below 2^-126: for outputs of bf16, 2^-8 of whose own
-// rounding it stays below. (1825 x 256 x 35840 with sigmoid to bf16 takes 80 us; with expf 99.)
+// z < 0; elsewhere 1 is the larger summand), and 0 below 2^-126: for outputs of bf16, of whose steps that is
+// less than a three-hundredth. (1825 x 256 x 35840 with sigmoid to bf16 takes 80 us; with expf 99.)
 __device__ __forceinline__ float quick_sigmoid_of(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 template <int ACT, bool QUICK>

@@ -154,9 +154,9 @@ __device__ __forceinline__ void load8_shifted(const T* p, const T* start, const 
 }
 
 // A warp takes 256 columns of a row, eight neighbours a lane; VEC: rows allow vectors of eight.  Bounded
-// by the bytes of dy, the pre-activation and the parts: 3328 x 10000 with tanh or sigmoid in two parts
-// takes 61 us (4.3 TB/s), fp32 dy in three without activation 50 (6.6 TB/s); one row a thread 68, rows
-// that no vector can read 98.
+// by the bytes of dy, the pre-activation and the parts: 3328 x 10000 with tanh or sigmoid in three parts
+// takes 62 us (5.3 TB/s), fp32 dy without activation 48 (6.9 TB/s); with one row a thread the former took
+// 68, rows that no vector can read 98.
 template <bool VEC>
 __device__ __forceinline__ void split_rows(const SplitArgs& a, const SplitBlocks::Place& here, float (&warps)[8][256]) {
   constexpr int kSplitRows = VEC ? 2 : 1;  // under way a thread, of dy and the pre-activation both
@@ -570,8 +570,8 @@ struct Launcher {
       if (t < best) best = t, S = s;
     }
     // Two launches, each split by itself, where more than 2 / 7 of the pairs' time would be waiting: 1024 x 23960
-    // of 2048 rows with sigmoid (0.76 of it) took 1219 us in one and 538 in two, 256 x 41112 of 2048 (0.06) 94
-    // and 118; they meet near 0.3.
+    // of 2048 rows with sigmoid (0.76 of it) took 1249 us in one and 638 in two, 256 x 41112 of 2048 (0.06) 95
+    // and 117; they meet near 0.3.
     if (S == 0 || 5 * best * pairs > 7 * (4 * tiles_x * steps_x + 5 * units_w * steps_w)) return false;
     Plan px = plan<false, false>(gx, dz, parts, &W, 1, M, static_cast<int>(K), N, S);
     Plan pw = plan<true, true>(gw, &x, 1, dz, parts, K, static_cast<int>(N), M, 1);
@@ -585,8 +585,8 @@ struct Launcher {
     both.dw = pw.g;
     both.dw.streams = static_cast<int>(std::min<int64_t>(px.S, pw.g.tiles_j));
     both.dx_pairs = static_cast<int>(px.g.units);
-    // dW passes through L2, which has dz to keep for its second reading (213 us for 2048 x 151936 of 256, 216
-    // without, 253 in two launches)
+    // dW passes through L2, which has dz to keep for its second reading (221 us for 2048 x 151936 of 256, 222
+    // without, 271 in two launches)
     both.dw.out_first = 1;
     constexpr uint32_t smem = GemmShape<256, kEpiTma, true>::kSmem;
     error = (*c.opt_in)(linear_both_kernel, smem);
