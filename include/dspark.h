@@ -598,11 +598,13 @@ int dspark_embed_grad(dspark_ctx* ctx, const int32_t* ids, const void* de, int d
  *     dspark_dtypes (contiguous tensors; a count of 0 elements may have a NULL address)
  *   out: HOST array of `count` addresses that receive the scaled tensors, in their types:
  *     a tensor's own address scales it in place (where the factor is 1 it is not touched);
- *     otherwise tensors must not overlap (nor be listed twice).  NULL: only the norm is computed, max_norm unread
+ *     otherwise tensors must not overlap (nor be listed twice).  NULL: only the norm is computed,
+ *     max_norm unread
  *   norm: device fp32 scalar
  * The host arrays are read during the call.  Squares are of fp32 (a gradient beyond 1e19 makes
  * the norm infinite, one below 1e-19 counts with fewer digits, one below 1e-23 as 0), their sums
- * of 64 bits beyond a thread's own.  An infinite norm gives the factor 0 and a NaN one NaN, as the formula does.  max_norm >= 0; equal inputs give equal bits. */
+ * of 64 bits beyond a thread's own.  An infinite norm gives the factor 0 and a NaN one NaN, as
+ * the formula does.  max_norm >= 0; equal inputs give equal bits. */
 int dspark_clip_grads(dspark_ctx* ctx, const void* const* grads, const int64_t* numel,
                       const int32_t* dtypes, int count, float max_norm, void* const* out,
                       float* norm, dspark_stream_t stream);
